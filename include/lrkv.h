@@ -75,6 +75,7 @@ enum {
 #define LRKV_STATUS_BAD_SEQLEN 2u   /* sequence length < 1 or > max_pages*page_size */
 #define LRKV_STATUS_BAD_ROW 4u      /* append: position/sequence id out of range */
 #define LRKV_STATUS_TIMEOUT 8u      /* an on-chip wait gave up (never expected) */
+#define LRKV_STATUS_NO_PAGES 16u    /* page plan: too few free pages or rows; a request did not grow */
 
 /*
  * Paged factored cache (section 3, after Algorithm 1: shared and private
@@ -385,6 +386,100 @@ LRKV_API int lrkv_key_norms(const int32_t *positions, const int32_t *seq_ids, in
                             const void *B_K, const lrkv_cache_t *cache, const int32_t *page_table,
                             int32_t B, int32_t max_pages, int32_t *dev_status,
                             lrkv_stream_t stream);
+
+/*
+ * Sliding window with sinks -- attention whose history is bounded (library
+ * operators; the paper attends the whole history).  A query at position t
+ * sees row j of its request when
+ *     j <= t  and  (j > t - window  or  j < sinks),
+ * that is the last `window` rows, itself included, and the first `sinks`
+ * rows; everything else is lrkv_decode and lrkv_prefill (one softmax over the
+ * visible rows, scale 1/sqrt(d_h), equations 6 and 7, key norms, groups, every
+ * cache dtype; no rotary variant).  window >= 1 and sinks >= 0, else
+ * LRKV_E_SHAPE; a window that covers the history attends all of it.
+ *
+ * A row that no query of the call sees is never attended, whatever its memory
+ * holds, and a page that holds only such rows needs no page: its table entry
+ * may be anything (-1, a page given to another request) and is not flagged.
+ * So a request needs ceil(sinks / page_size) pages for its sinks and
+ * about window / page_size + 1 for its window, however long it gets
+ * (lrkv_page_plan keeps exactly those).
+ *
+ * lrkv_decode_window takes the arguments of lrkv_decode.  Its workspace is
+ * lrkv_decode_window_workspace_bytes(...) bytes, 256-byte aligned, scratch
+ * that needs no initialisation; no block waits for another outside its own
+ * thread-block cluster, so calls on several streams run side by side (each
+ * with a workspace of its own).
+ *
+ * lrkv_prefill_window takes the arguments of lrkv_prefill and its workspace
+ * (lrkv_prefill_workspace_bytes); rows 0 .. start_pos[b]-1 that a new row can
+ * see must be in the cache.
+ */
+LRKV_API size_t lrkv_decode_window_workspace_bytes(int32_t B, int32_t H, int32_t d_h, int32_t r,
+                                                   int32_t max_seq_len, int32_t window,
+                                                   int32_t sinks, int32_t dtype);
+LRKV_API int lrkv_decode_window(const void *q, const lrkv_cache_t *cache, const void *B_K,
+                                const void *B_V, const int32_t *seq_lens, const int32_t *page_table,
+                                int32_t B, int32_t max_pages, int32_t max_seq_len, int32_t window,
+                                int32_t sinks, void *out, void *workspace, size_t workspace_bytes,
+                                int32_t *dev_status, lrkv_stream_t stream);
+LRKV_API int lrkv_prefill_window(const void *X, const void *Q, const int32_t *cu_rows,
+                                 const int32_t *start_pos, int32_t B, int32_t n, int32_t max_ctx,
+                                 int32_t d, const void *W_S_K, const void *W_S_V, const void *U_K,
+                                 const void *U_V, const void *B_K, const void *B_V,
+                                 const lrkv_cache_t *cache, const int32_t *page_table,
+                                 int32_t max_pages, int32_t window, int32_t sinks, void *out,
+                                 void *workspace, size_t workspace_bytes, int32_t *dev_status,
+                                 lrkv_stream_t stream);
+
+/*
+ * lrkv_page_plan - the pages and slots of one serving step, built on the GPU
+ * from the requests' lengths.  (Library plumbing: the paper only asks that
+ * shared and private pages share their ids and lifetime, section 3 after
+ * Algorithm 1.)
+ *
+ * Request b holds seq_lens[b] rows and gets new_rows[b] more, 0 for none, or
+ * ends (-1).  The call
+ *  - takes the pages that the new rows need, ceil((L + n) / page_size) -
+ *    ceil(L / page_size) of them, off the end of the free list, in (request,
+ *    page) order, and enters them in page_table;
+ *  - releases the pages that left the window (window > 0): with D(L) =
+ *    max(0, floor((L - window + 1) / page_size)) and sp = ceil(sinks /
+ *    page_size), pages max(D(L), sp) .. max(D(L + n), sp) - 1, and, of a
+ *    request that ends, all it holds.  Their ids go behind what is left of the
+ *    free list, in (request, page) order, so they are handed out by a later
+ *    call at the earliest: attention of this step, enqueued after this call,
+ *    may still read them.  Their table entries stay as they are.
+ *  - writes, for every new row in (request, position) order, its position,
+ *    request and pool row: positions[i], seq_ids[i] and slots[i] =
+ *    page * page_size + position % page_size are what lrkv_append takes and
+ *    where it stores the row; cu_rows and seq_lens (as start_pos) are what
+ *    lrkv_prefill takes.  Entries cu_rows[B] .. max_rows-1 become -1.
+ *
+ *   seq_lens, new_rows [B] int32; page_table [B, max_pages] int32, updated in
+ *     place; free_pages, free_out [num_pages] int32; n_free, n_free_out one
+ *     int32: free_pages[0 .. n_free) are the pages nobody holds; after the call
+ *     free_out[0 .. n_free_out) are, and the rest of free_out is untouched.
+ *   seq_lens_out [B]: L + n, or 0 for a request that ended.  cu_rows [B + 1].
+ *   positions, seq_ids, slots [max_rows], 16-byte aligned.
+ * All on the device; no output may overlap an input (keep two free lists and
+ * two length arrays and swap them).
+ *
+ * A request does not grow, keeps its length and flags LRKV_STATUS_NO_PAGES
+ * when the rows asked for by the requests up to and including it exceed
+ * max_rows, or when it needs pages and the pages asked for up to and
+ * including it exceed n_free.  A length outside [0, max_pages*page_size], n <
+ * -1 or a grown length past the table leaves the request as it is and flags
+ * LRKV_STATUS_BAD_SEQLEN.  An id outside [0, num_pages) is passed on as -1
+ * (slot -1) and flags LRKV_STATUS_BAD_PAGE.
+ */
+LRKV_API int lrkv_page_plan(const int32_t *seq_lens, const int32_t *new_rows, int32_t B,
+                            int32_t max_pages, int32_t page_size, int32_t num_pages,
+                            int32_t window, int32_t sinks, int32_t max_rows, int32_t *page_table,
+                            const int32_t *free_pages, const int32_t *n_free,
+                            int32_t *seq_lens_out, int32_t *cu_rows, int32_t *positions,
+                            int32_t *seq_ids, int32_t *slots, int32_t *free_out,
+                            int32_t *n_free_out, int32_t *dev_status, lrkv_stream_t stream);
 
 /*
  * Exact rotary position embedding over the factored cache (reading note,

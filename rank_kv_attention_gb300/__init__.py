@@ -9,7 +9,7 @@ does, and raises if the library has not been built (see ``build.build``).
 from ._abi import (LRKV_BF16, LRKV_F32, LRKV_OK, LRKV_E_INVALID_ARG, LRKV_E_SHAPE,
                    LRKV_E_DTYPE, LRKV_E_BOUNDS, LRKV_E_WORKSPACE, LRKV_E_CUDA,
                    LRKV_STATUS_BAD_PAGE, LRKV_STATUS_BAD_SEQLEN, LRKV_STATUS_BAD_ROW,
-                   LRKV_STATUS_TIMEOUT, LRKV_PREFILL_PER_ROW, LRKV_PREFILL_TILED, CacheDesc,
+                   LRKV_STATUS_TIMEOUT, LRKV_STATUS_NO_PAGES, LRKV_PREFILL_PER_ROW, LRKV_PREFILL_TILED, CacheDesc,
                    LrkvError, lib)
 
 __all__ = [
@@ -18,7 +18,8 @@ __all__ = [
     "prefill_kernel_kind", "decode_step", "decode_step_workspace_bytes", "rope_table",
     "decode_rope", "prefill_rope", "key_norms", "RopeTable", "rope_table_bytes",
     "decode_rope_workspace_bytes", "decode_step_host", "decode_step_host_workspace_bytes",
-    "StepGraph",
+    "StepGraph", "decode_window", "decode_window_workspace_bytes", "prefill_window", "page_plan",
+    "PagePlan",
 ]
 
 
@@ -30,7 +31,8 @@ def __getattr__(name):
                 "decode_step", "decode_step_workspace_bytes", "rope_table", "decode_rope",
                 "prefill_rope", "key_norms", "RopeTable", "rope_table_bytes",
                 "decode_rope_workspace_bytes", "decode_step_host",
-                "decode_step_host_workspace_bytes", "StepGraph"):
+                "decode_step_host_workspace_bytes", "StepGraph", "decode_window",
+                "decode_window_workspace_bytes", "prefill_window", "page_plan", "PagePlan"):
         from . import api
         return getattr(api, name)
     raise AttributeError(name)

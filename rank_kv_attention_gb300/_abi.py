@@ -36,6 +36,7 @@ LRKV_STATUS_BAD_PAGE = 1
 LRKV_STATUS_BAD_SEQLEN = 2
 LRKV_STATUS_BAD_ROW = 4
 LRKV_STATUS_TIMEOUT = 8
+LRKV_STATUS_NO_PAGES = 16
 
 
 class CacheDesc(ctypes.Structure):
@@ -70,6 +71,13 @@ SZ = ctypes.c_size_t
 CACHE_P = ctypes.POINTER(CacheDesc)
 
 SIGNATURES = {
+    "lrkv_decode_window_workspace_bytes": (SZ, [I32] * 8),
+    "lrkv_decode_window": (ctypes.c_int, [P, CACHE_P, P, P, P, P, I32, I32, I32, I32, I32, P, P, SZ, P,
+                                          P]),
+    "lrkv_prefill_window": (ctypes.c_int, [P, P, P, P, I32, I32, I32, I32, P, P, P, P, P, P, CACHE_P, P,
+                                           I32, I32, I32, P, P, SZ, P, P]),
+    "lrkv_page_plan": (ctypes.c_int, [P, P, I32, I32, I32, I32, I32, I32, I32, P, P, P, P, P, P, P, P, P,
+                                      P, P, P]),
     "lrkv_append": (ctypes.c_int, [P, P, P, I32, I32, P, P, P, P, CACHE_P, P, I32, I32, P, P]),
     "lrkv_decode_workspace_bytes": (SZ, [I32, I32, I32, I32, I32, I32]),
     "lrkv_decode": (ctypes.c_int, [P, CACHE_P, P, P, P, P, I32, I32, I32, P, P, SZ, P, P]),

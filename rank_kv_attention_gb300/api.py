@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 from dataclasses import dataclass
+from typing import NamedTuple
 
 import torch
 
@@ -336,6 +337,151 @@ def prefill(X, Q, cu_rows, start_pos, max_ctx, W_S_K, W_S_V, U_K, U_V, B_K, B_V,
                                    _ptr(status), _stream(stream))
     _abi.check("lrkv_prefill", code)
     return out
+
+
+# ----------------------------------------------------------------------------
+# Sliding window with sinks, and the page plan of such a cache (see
+# include/lrkv.h).  These check every shape, and that all tensors lie on the
+# current device, before the library is called.
+# ----------------------------------------------------------------------------
+def _arg(t, name, dtype, shape):
+    """Address of a tensor of exactly this dtype and shape, contiguous, on the current device."""
+    if (not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != shape or not t.is_cuda
+            or not t.is_contiguous() or t.get_device() != torch.cuda.current_device()):
+        _need(t, name, dtype)
+        if t.shape != shape:
+            raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, not on the current device "
+                         f"cuda:{torch.cuda.current_device()}")
+    return t.data_ptr()
+
+
+def _table_arg(page_table, B):
+    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
+        raise ValueError("page_table must be a [B, max_pages] tensor")
+    return _arg(page_table, "page_table", torch.int32, (B, page_table.shape[1])), page_table.shape[1]
+
+
+def _own_buffer(shape, dtype, device, stream):
+    """A buffer made for a call on `stream`: not reused before the stream has passed it."""
+    t = torch.empty(shape, dtype=dtype, device=device)
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
+def _status_ptr(status):
+    return None if status is None else _arg(status, "status", torch.int32, (1,))
+
+
+def decode_window_workspace_bytes(B, H, d_h, r, max_seq_len, window, sinks=0, dtype=torch.bfloat16) -> int:
+    return _abi.lib().lrkv_decode_window_workspace_bytes(B, H, d_h, r, max_seq_len, window, sinks, _DT[dtype])
+
+
+def decode_window(q, cache: PagedCache, B_K, B_V, seq_lens, page_table, max_seq_len, window, sinks=0,
+                  out=None, ws=None, status=None, stream=None):
+    """lrkv_decode_window: one decode step in which request b sees its last
+    ``window`` rows and its first ``sinks`` rows; returns out [B, H, d_h]."""
+    if q.dim() != 3:
+        raise ValueError("q must be a [B, H, d_h] tensor")
+    dt = cache.act_dtype
+    desc = cache.desc()
+    B, H, d_h, r = q.shape[0], desc.H, desc.d_h, desc.r
+    pq = _arg(q, "q", dt, (B, H, d_h))
+    bases = _arg(B_K, "B_K", dt, (H, d_h, r)), _arg(B_V, "B_V", dt, (H, d_h, r))
+    lens = _arg(seq_lens, "seq_lens", torch.int32, (B,))
+    table, max_pages = _table_arg(page_table, B)
+    if out is None:
+        out = _own_buffer(q.shape, dt, q.device, stream)
+    L = _abi.lib()
+    if ws is None:
+        ws = _own_buffer(max(1, L.lrkv_decode_window_workspace_bytes(B, H, d_h, r, max_seq_len, window,
+                                                                     sinks, desc.dtype)),
+                         torch.uint8, q.device, stream)
+    code = L.lrkv_decode_window(pq, ctypes.byref(desc), *bases, lens, table, B, max_pages, max_seq_len,
+                                window, sinks, _arg(out, "out", dt, (B, H, d_h)),
+                                _arg(ws, "ws", torch.uint8, (ws.numel(),)), ws.numel(),
+                                _status_ptr(status), _stream(stream))
+    _abi.check("lrkv_decode_window", code)
+    return out
+
+
+def prefill_window(X, Q, cu_rows, start_pos, max_ctx, W_S_K, W_S_V, U_K, U_V, B_K, B_V,
+                   cache: PagedCache, page_table, window, sinks=0, out=None, ws=None, status=None,
+                   stream=None):
+    """lrkv_prefill_window: append the chunk X, then attention of each row's Q
+    over the last ``window`` rows up to its own and the first ``sinks`` rows."""
+    if X.dim() != 2:
+        raise ValueError("X must be a [n, d] tensor")
+    dt = cache.act_dtype
+    desc = cache.desc()
+    n, d = X.shape
+    H, d_h, r, G = desc.H, desc.d_h, desc.r, max(1, desc.G)
+    B = start_pos.shape[0]
+    if out is None:
+        out = _own_buffer(Q.shape, dt, X.device, stream)
+    L = _abi.lib()
+    if ws is None:
+        ws = _own_buffer(max(1, L.lrkv_prefill_workspace_bytes(B, n, H, d_h, r, max_ctx, desc.dtype)),
+                         torch.uint8, X.device, stream)
+    table, max_pages = _table_arg(page_table, B)
+    code = L.lrkv_prefill_window(
+        _arg(X, "X", dt, (n, d)), _arg(Q, "Q", dt, (n, H, d_h)),
+        _arg(cu_rows, "cu_rows", torch.int32, (B + 1,)), _arg(start_pos, "start_pos", torch.int32, (B,)),
+        B, n, max_ctx, d, _arg(W_S_K, "W_S_K", dt, (G * d_h, d)), _arg(W_S_V, "W_S_V", dt, (G * d_h, d)),
+        _arg(U_K, "U_K", dt, (H, r, d)), _arg(U_V, "U_V", dt, (H, r, d)),
+        _arg(B_K, "B_K", dt, (H, d_h, r)), _arg(B_V, "B_V", dt, (H, d_h, r)), ctypes.byref(desc), table,
+        max_pages, window, sinks, _arg(out, "out", dt, (n, H, d_h)),
+        _arg(ws, "ws", torch.uint8, (ws.numel(),)), ws.numel(), _status_ptr(status), _stream(stream))
+    _abi.check("lrkv_prefill_window", code)
+    return out
+
+
+class PagePlan(NamedTuple):
+    """What lrkv_page_plan writes beside the page table: the lengths after the
+    step, each request's rows as cu_rows offsets, the rows' positions, requests
+    and pool rows (slots), and the free list after the step with its count."""
+    seq_lens: torch.Tensor
+    cu_rows: torch.Tensor
+    positions: torch.Tensor
+    seq_ids: torch.Tensor
+    slots: torch.Tensor
+    free_pages: torch.Tensor
+    n_free: torch.Tensor
+
+
+def page_plan(seq_lens, new_rows, page_table, free_pages, n_free, page_size, max_rows, free_out=None,
+              window=0, sinks=0, status=None, stream=None) -> PagePlan:
+    """lrkv_page_plan: pages and slots of one step, in which request b gains
+    new_rows[b] rows (-1: it ends).  page_table is updated in place; free_out
+    ([num_pages]) takes the free list after the step."""
+    if seq_lens.dim() != 1 or free_pages.dim() != 1:
+        raise ValueError("seq_lens and free_pages must be one-dimensional")
+    B, num_pages = seq_lens.shape[0], free_pages.shape[0]
+    dev = seq_lens.device
+    lens, new = _arg(seq_lens, "seq_lens", torch.int32, (B,)), _arg(new_rows, "new_rows", torch.int32, (B,))
+    table, max_pages = _table_arg(page_table, B)
+    free, nf = (_arg(free_pages, "free_pages", torch.int32, (num_pages,)),
+                _arg(n_free, "n_free", torch.int32, (1,)))
+    if free_out is None:
+        free_out = _own_buffer((num_pages,), torch.int32, dev, stream)
+    if max_rows < 0:
+        raise ValueError("max_rows must not be negative")
+    # one buffer for the small outputs: each part starts on a 16-byte boundary
+    sizes = (max_rows, max_rows, max_rows, B, B + 1, 1)
+    starts, at = [], 0
+    for s in sizes:
+        starts.append(at)
+        at += (s + 3) // 4 * 4
+    buf = _own_buffer((at,), torch.int32, dev, stream)
+    pos, ids, slots, after, cu, left = (buf[a:a + s] for a, s in zip(starts, sizes))
+    code = _abi.lib().lrkv_page_plan(
+        lens, new, B, max_pages, page_size, num_pages, window, sinks, max_rows, table, free, nf,
+        after.data_ptr(), cu.data_ptr(), pos.data_ptr(), ids.data_ptr(), slots.data_ptr(),
+        _arg(free_out, "free_out", torch.int32, (num_pages,)), left.data_ptr(), _status_ptr(status),
+        _stream(stream))
+    _abi.check("lrkv_page_plan", code)
+    return PagePlan(after, cu, pos, ids, slots, free_out, left)
 
 
 # ----------------------------------------------------------------------------

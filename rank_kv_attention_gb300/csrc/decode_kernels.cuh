@@ -37,6 +37,10 @@ struct DecodeArgs {
     // back the copies of tiles that hold a new row until its own wait (which
     // the prologue's completion, and so the append's, releases).
     bool early = false;
+    // Sliding window with sinks (lrkv_decode_window, lrkv_prefill_window):
+    // 0 attends the whole history.
+    int window = 0;
+    int sinks = 0;
 };
 
 // Longest sequence length a decode attends: what the page table can hold;
@@ -56,10 +60,28 @@ inline int decode_max_len(const DecodeArgs &a) {
 constexpr int kRopeMaxRank = 64;
 cudaError_t launch_rope_table(double base, int d_h, int max_pos, void *table, cudaStream_t s);
 
+// Visible rows of a query that ends a history of L rows: [0, sinks) and
+// [first, L).  Sinks that reach the window are part of it (sinks <= first
+// always holds), and without a window (0) everything is: first = 0.
+struct VisibleRows {
+    int32_t sinks, first;
+    __host__ __device__ __forceinline__ VisibleRows(int32_t L, int window, int max_sinks) {
+        first = window > 0 && L > window ? L - window : 0;
+        sinks = max_sinks < first ? max_sinks : first;
+    }
+    // the v-th visible row
+    __host__ __device__ __forceinline__ int32_t row(int32_t v) const {
+        return v < sinks ? v : v - sinks + first;
+    }
+};
+
 // Rows the split kernels stream for a request of length L: none for an
-// invalid length, else L.
-__host__ __device__ __forceinline__ int32_t streamed_len(int32_t L, int max_len) {
-    return (L < 1 || L > max_len) ? 0 : L;
+// invalid length, else the visible ones (all L without a window).
+__host__ __device__ __forceinline__ int32_t streamed_len(int32_t L, int max_len, int window = 0,
+                                                         int sinks = 0) {
+    if (L < 1 || L > max_len) return 0;
+    const VisibleRows v(L, window, sinks);
+    return L - v.first + v.sinks;
 }
 
 // beside_split: the tensor-core split kernel follows (smaller prologue blocks).

@@ -9,6 +9,7 @@
 
 #include "append_kernels.cuh"
 #include "decode_kernels.cuh"
+#include "page_kernels.cuh"
 
 namespace lrkv {
 
@@ -129,14 +130,19 @@ static size_t decode_ws_bytes(int B, int H, int d_h, int r, int max_seq_len) {
     return decode_ws_layout(nullptr, B, H, d_h, r, g.G_ws).bytes;
 }
 
+// Most rows that a query sees through a window with sinks.
+static int window_bound(int max_seq_len, int window, int sinks) {
+    return (int)std::min<int64_t>(max_seq_len, (int64_t)window + sinks);
+}
+
 static int run_decode(const DecodeArgs &a, void *workspace, size_t ws_bytes) {
     const auto &c = a.cache;
-    DecodeGeom geo = decode_geom(a.B, a.max_seq_len);
+    DecodeGeom geo = decode_geom(a.B, a.window ? window_bound(a.max_seq_len, a.window, a.sinks) : a.max_seq_len);
     DecodeWs ws = decode_ws_layout(workspace, a.B, c.H, c.d_h, c.r, geo.G_ws);
     if (ws_bytes < ws.bytes) return LRKV_E_WORKSPACE;
     const bool rope_fast = a.rope_ws.wt != nullptr;
-    const bool fast = rope_fast || (!a.rope && fast_decode_supported(c.H, c.d_h, c.r, c.page_size, c.dtype,
-                                                                      cache_groups(c)));
+    const bool fast = rope_fast || (!a.rope && !a.window && fast_decode_supported(c.H, c.d_h, c.r, c.page_size, c.dtype,
+                                                                                  cache_groups(c)));
     const int G = fast ? geo.G_fast : geo.G_gen;
     cudaError_t e;
     if (c.dtype != LRKV_F32) {  // bf16 activations (bf16 or 8-bit cache)
@@ -699,7 +705,7 @@ static int prefill_impl(const void *X, const void *Q, const int32_t *cu_rows,
                         const void *B_K, const void *B_V, const lrkv_cache_t *cache,
                         const int32_t *page_table, int32_t max_pages, const float *rope,
                         int32_t rope_max_pos, void *out, void *workspace, size_t workspace_bytes,
-                        int32_t *dev_status, lrkv_stream_t stream) {
+                        int32_t *dev_status, lrkv_stream_t stream, int window = 0, int sinks = 0) {
     int st = check_append(X, cu_rows, start_pos, n, d, W_S_K, W_S_V, U_K, U_V, cache, page_table,
                           B, max_pages);
     if (st) return st;
@@ -724,7 +730,7 @@ static int prefill_impl(const void *X, const void *Q, const int32_t *cu_rows,
         e = launch_key_norms(w.pos, w.sid, n, B_K, *cache, page_table, B, max_pages, dev_status, s);
         if (e != cudaSuccess) return cuda_fail(e);
     }
-    if (!rope && !cache->N_K) {
+    if (!rope && !cache->N_K && !window) {
         // Causal attention on tensor cores (query tiles of 128 rows per head).
         PrefillTcArgs p;
         p.Q = Q;
@@ -765,6 +771,8 @@ static int prefill_impl(const void *X, const void *Q, const int32_t *cu_rows,
     a.stream = s;
     a.rope = rope;
     a.rope_max_pos = rope_max_pos;
+    a.window = window;
+    a.sinks = sinks;
     return run_decode(a, w.dec, w.dec_bytes);
 }
 
@@ -777,6 +785,113 @@ int lrkv_prefill(const void *X, const void *Q, const int32_t *cu_rows, const int
     return prefill_impl(X, Q, cu_rows, start_pos, B, n, max_ctx, d, W_S_K, W_S_V, U_K, U_V, B_K,
                         B_V, cache, page_table, max_pages, nullptr, 0, out, workspace,
                         workspace_bytes, dev_status, stream);
+}
+
+// ---------------------------------------------------------------------------
+// Sliding window with sinks, and the page plan of such a cache
+// ---------------------------------------------------------------------------
+size_t lrkv_decode_window_workspace_bytes(int32_t B, int32_t H, int32_t d_h, int32_t r,
+                                          int32_t max_seq_len, int32_t window, int32_t sinks,
+                                          int32_t dtype) {
+    if (check_dims(H, d_h, r, dtype) || B < 1 || max_seq_len < 1 || window < 1 || sinks < 0) return 0;
+    return decode_ws_bytes(B, H, d_h, r, window_bound(max_seq_len, window, sinks));
+}
+
+int lrkv_decode_window(const void *q, const lrkv_cache_t *cache, const void *B_K, const void *B_V,
+                       const int32_t *seq_lens, const int32_t *page_table, int32_t B,
+                       int32_t max_pages, int32_t max_seq_len, int32_t window, int32_t sinks,
+                       void *out, void *workspace, size_t workspace_bytes, int32_t *dev_status,
+                       lrkv_stream_t stream) {
+    int st = check_cache(cache);
+    if (st) return st;
+    if (B < 1 || max_pages < 1 || max_seq_len < 1 || window < 1 || sinks < 0) return LRKV_E_SHAPE;
+    if ((int64_t)max_pages * cache->page_size > INT32_MAX / 2) return LRKV_E_SHAPE;
+    if ((int64_t)max_seq_len > (int64_t)max_pages * cache->page_size) return LRKV_E_BOUNDS;
+    // a length may exceed max_seq_len (not the page table): the streamed rows
+    // are counted in 32 bits whatever the lengths hold
+    if ((int64_t)B * window_bound(max_pages * cache->page_size, window, sinks) > INT32_MAX / 2)
+        return LRKV_E_SHAPE;
+    if (!q || !B_K || !B_V || !seq_lens || !page_table || !out) return LRKV_E_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(B_K) || !aligned16(B_V) || !aligned16(out))
+        return LRKV_E_INVALID_ARG;
+    if (!workspace || !aligned256(workspace)) return LRKV_E_WORKSPACE;
+    DecodeArgs a;
+    a.q = q;
+    a.cache = *cache;
+    a.B_K = B_K;
+    a.B_V = B_V;
+    a.seq_lens = seq_lens;
+    a.page_table = page_table;
+    a.req_row = nullptr;
+    a.B = B;
+    a.max_pages = max_pages;
+    a.max_seq_len = max_seq_len;
+    a.window = window;
+    a.sinks = sinks;
+    a.out = out;
+    a.status = dev_status;
+    a.stream = (cudaStream_t)stream;
+    return run_decode(a, workspace, workspace_bytes);
+}
+
+int lrkv_prefill_window(const void *X, const void *Q, const int32_t *cu_rows,
+                        const int32_t *start_pos, int32_t B, int32_t n, int32_t max_ctx, int32_t d,
+                        const void *W_S_K, const void *W_S_V, const void *U_K, const void *U_V,
+                        const void *B_K, const void *B_V, const lrkv_cache_t *cache,
+                        const int32_t *page_table, int32_t max_pages, int32_t window, int32_t sinks,
+                        void *out, void *workspace, size_t workspace_bytes, int32_t *dev_status,
+                        lrkv_stream_t stream) {
+    if (window < 1 || sinks < 0) return LRKV_E_SHAPE;
+    return prefill_impl(X, Q, cu_rows, start_pos, B, n, max_ctx, d, W_S_K, W_S_V, U_K, U_V, B_K,
+                        B_V, cache, page_table, max_pages, nullptr, 0, out, workspace,
+                        workspace_bytes, dev_status, stream, window, sinks);
+}
+
+int lrkv_page_plan(const int32_t *seq_lens, const int32_t *new_rows, int32_t B, int32_t max_pages,
+                   int32_t page_size, int32_t num_pages, int32_t window, int32_t sinks,
+                   int32_t max_rows, int32_t *page_table, const int32_t *free_pages,
+                   const int32_t *n_free, int32_t *seq_lens_out, int32_t *cu_rows,
+                   int32_t *positions, int32_t *seq_ids, int32_t *slots, int32_t *free_out,
+                   int32_t *n_free_out, int32_t *dev_status, lrkv_stream_t stream) {
+    if (B < 1 || max_pages < 1 || num_pages < 1 || max_rows < 0 || window < 0 || sinks < 0)
+        return LRKV_E_SHAPE;
+    if (page_size < 16 || page_size > 1024 || page_size % 16) return LRKV_E_SHAPE;
+    if ((int64_t)max_pages * page_size > INT32_MAX / 2 || (int64_t)num_pages * page_size > INT32_MAX / 2 ||
+        max_rows > INT32_MAX / 2)
+        return LRKV_E_SHAPE;
+    if (!seq_lens || !new_rows || !page_table || !free_pages || !n_free || !seq_lens_out || !cu_rows ||
+        !free_out || !n_free_out || (max_rows > 0 && (!positions || !seq_ids || !slots)))
+        return LRKV_E_INVALID_ARG;
+    const void *ins[] = {seq_lens, new_rows, free_pages, n_free};
+    const void *outs[] = {seq_lens_out, cu_rows, free_out, n_free_out};
+    for (const void *i : ins)
+        for (const void *o : outs)
+            if (i == o) return LRKV_E_INVALID_ARG;  // read by every block while outputs are written
+    if (max_rows > 0 && (!aligned16(positions) || !aligned16(seq_ids) || !aligned16(slots)))
+        return LRKV_E_INVALID_ARG;
+    PagePlanArgs a;
+    a.seq_lens = seq_lens;
+    a.new_rows = new_rows;
+    a.B = B;
+    a.max_pages = max_pages;
+    a.page_size = page_size;
+    a.num_pages = num_pages;
+    a.window = window;
+    a.sinks = sinks;
+    a.max_rows = max_rows;
+    a.page_table = page_table;
+    a.free_pages = free_pages;
+    a.n_free = n_free;
+    a.seq_lens_out = seq_lens_out;
+    a.cu_rows = cu_rows;
+    a.positions = positions;
+    a.seq_ids = seq_ids;
+    a.slots = slots;
+    a.free_out = free_out;
+    a.n_free_out = n_free_out;
+    a.status = dev_status;
+    cudaError_t e = launch_page_plan(a, (cudaStream_t)stream);
+    return e == cudaSuccess ? LRKV_OK : cuda_fail(e);
 }
 
 // ---------------------------------------------------------------------------
