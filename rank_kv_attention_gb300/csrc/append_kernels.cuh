@@ -97,6 +97,7 @@ struct PrefillTcArgs {
     void *out;
     int32_t *status;
     cudaStream_t stream;
+    int window = 0, sinks = 0;  // lrkv_prefill_window; window 0: the whole history
 };
 int launch_prefill_tc(const PrefillTcArgs &p);
 // Whether lrkv_prefill runs the tensor-core attention kernel for this cache.

@@ -730,7 +730,7 @@ static int prefill_impl(const void *X, const void *Q, const int32_t *cu_rows,
         e = launch_key_norms(w.pos, w.sid, n, B_K, *cache, page_table, B, max_pages, dev_status, s);
         if (e != cudaSuccess) return cuda_fail(e);
     }
-    if (!rope && !cache->N_K && !window) {
+    if (!rope && !cache->N_K) {
         // Causal attention on tensor cores (query tiles of 128 rows per head).
         PrefillTcArgs p;
         p.Q = Q;
@@ -747,6 +747,8 @@ static int prefill_impl(const void *X, const void *Q, const int32_t *cu_rows,
         p.out = out;
         p.status = dev_status;
         p.stream = s;
+        p.window = window;
+        p.sinks = sinks;
         prof_before(LRKV_PROFILE_ATTENTION, s);
         const int rc = launch_prefill_tc(p);
         if (rc == 0) prof_after(LRKV_PROFILE_ATTENTION, s);

@@ -39,6 +39,12 @@
 // tensor memory only when the maximum grows by more than 2^8).  Keys past
 // every row of the CTA have their value rows cleared in shared memory, so
 // whatever the cache holds there cannot reach the output.
+//
+// WIN: row i sees j <= t_i with j > t_i - window or j < sinks.  The CTA's key
+// tiles are then those of the sinks and those from the window of its first
+// row on (`KeyTiles`); the tiles between are not visited, the scores of a
+// visited tile are masked per row where a window starts or the sinks end, and
+// value rows that no row of the CTA sees are cleared like those past the end.
 #include <algorithm>
 
 #include "append_kernels.cuh"
@@ -91,6 +97,29 @@ struct PfArgs {
     int32_t *status;
     int n, B, H, r, page_size, max_pages, num_pages, max_len, n_qtiles;
     float scale_log2;  // log2(e) / sqrt(d_h)
+    int window, sinks;  // WIN only; both at most max_len
+};
+
+// Key tiles that the rows of one CTA visit, in order: tiles 0 .. ns-1 hold the
+// sinks, tiles kt0 .. the rows from `lo` (the first row of the window of the
+// CTA's first query) on.  ns <= kt0; without a window everything from tile 0.
+template <bool WIN>
+struct KeyTiles {
+    int lo, ns, kt0, count;
+    __device__ __forceinline__ KeyTiles(const PfArgs &a, int min_p, int max_p) {
+        lo = WIN ? max(0, min_p - a.window + 1) : 0;
+        kt0 = lo / PF_BN;
+        ns = WIN ? min((a.sinks + PF_BN - 1) / PF_BN, kt0) : 0;
+        count = ns + max_p / PF_BN - kt0 + 1;
+    }
+    // position of the first key of the kt-th visited tile
+    __device__ __forceinline__ int base(int kt) const {
+        return (!WIN ? kt : kt < ns ? kt : kt - ns + kt0) * PF_BN;
+    }
+    // whether no row of the CTA sees any of keys key0 .. key0 + 63 (lower end)
+    __device__ __forceinline__ bool dead(const PfArgs &a, int key0) const {
+        return WIN && key0 + PF_HALF <= lo && key0 >= a.sinks;
+    }
 };
 
 // 2^x on the special-function unit (PTX ex2.approx.ftz: ~2 ulp; -inf -> +0).
@@ -131,7 +160,7 @@ __device__ __forceinline__ void split_pack(float x0, float x1, uint32_t &hi, uin
     lo = pack_bf16(x0 - bf16lo(hi), x1 - bf16hi(hi));
 }
 
-template <int R16>
+template <int R16, bool WIN>
 __global__ void __launch_bounds__(PF_THREADS, 1)
     prefill_tc_kernel(const __grid_constant__ PfMaps maps, const PfArgs a) {
     constexpr int NPV = 128 + 16 * R16;  // value columns [S_V | R_V[h] (padded)]
@@ -191,7 +220,8 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
         return;
     }
     const int max_p = p0 + t_hi - 1;  // last key position any row sees
-    const int nkt = max_p / PF_BN + 1;
+    const KeyTiles<WIN> keys(a, p0 + t_lo, max_p);
+    const int nkt = keys.count;
 
     if (warp == 8) {
         if (lane == 0) {
@@ -221,8 +251,8 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
             // pool row of a 64-key slice of key tile kt (a fully out-of-range row,
             // which reads as zeros, for slices past the table or on an invalid page)
             auto slice_row = [&](int kt, int hh) -> int {
-                const int key0 = kt * PF_BN + hh * PF_HALF;
-                if (key0 / a.page_size >= a.max_pages) return -PF_HALF;
+                const int key0 = keys.base(kt) + hh * PF_HALF;
+                if (key0 / a.page_size >= a.max_pages || keys.dead(a, key0)) return -PF_HALF;
                 const int32_t page = pt_row[key0 / a.page_size];
                 if (page < 0 || page >= a.num_pages) {
                     if (kprod && key0 <= max_p) status_or(a.status, LRKV_STATUS_BAD_PAGE);
@@ -408,11 +438,12 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
             tc_fence_before();
             mbar_arrive(&bar.qa_ready);
         }
-        int32_t page_next = pt_row[min(hf * PF_HALF / a.page_size, a.max_pages - 1)];
+        int32_t page_next = pt_row[min((keys.base(0) + hf * PF_HALF) / a.page_size, a.max_pages - 1)];
         for (int kt = 0; kt < nkt && ok; ++kt) {
-            const int st = kt & 1, key0 = kt * PF_BN + hf * PF_HALF;
+            const int st = kt & 1, key0 = keys.base(kt) + hf * PF_HALF;
             const int32_t page = page_next;  // read one tile ahead, off the critical path
-            if (kt + 1 < nkt) page_next = pt_row[min((key0 + PF_BN) / a.page_size, a.max_pages - 1)];
+            if (kt + 1 < nkt)
+                page_next = pt_row[min((keys.base(kt + 1) + hf * PF_HALF) / a.page_size, a.max_pages - 1)];
             if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bar.s_full[st], (kt >> 1) & 1)))) break;
             tc_fence_after();
             float s[64];
@@ -429,6 +460,13 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
             if (klim < PF_HALF - 1) {
 #pragma unroll
                 for (int j = 0; j < 64; ++j) s[j] = (j <= klim) ? s[j] : -INFINITY;
+            }
+            if (WIN) {  // keys before the row's window that are not sinks
+                const int wlim = lim - a.window + 1 - key0, slim = a.sinks - key0;
+                if (wlim > 0 && slim < PF_HALF) {
+#pragma unroll
+                    for (int j = 0; j < 64; ++j) s[j] = (j >= wlim || j < slim) ? s[j] : -INFINITY;
+                }
             }
             // row maximum of the raw scores (the scale is positive), combined
             // with the other half of the row through shared memory
@@ -491,19 +529,28 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
                 }
             }
             tmem_st32(lane_base + PF_COL_S + 128 * st + 32 * hf, pk);  // probabilities over the scores
-            if (kt == nkt - 1 && max_p + 1 - kt * PF_BN < PF_BN) {
-                // keys past every row of the CTA: clear their value rows
+            // keys of the tile that no row of the CTA sees, z0 <= key < z1: past
+            // every row, or (WIN, another tile or the same) between the sinks and
+            // the first row's window
+            const int kb = key0 - hf * PF_HALF;
+            const int z_end = max_p + 1 - kb;
+            const int w0 = WIN ? max(a.sinks - kb, 0) : 0, w1 = WIN ? min(keys.lo - kb, PF_BN) : 0;
+            if ((kt == nkt - 1 && z_end < PF_BN) || (WIN && w0 < w1)) {
+                // clear their value rows
                 if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bar.v_full[st], (kt >> 1) & 1)))) break;
-                const int z0 = max_p + 1 - kt * PF_BN;  // 1..127
                 uint8_t *vb = smem + PF_OFF_V + st * PF_STAGE;
-                // 3 blocks x (128 - z0) rows x 8 16-byte units; key j of a block
-                // sits in 64-row box j / 64, row j % 64
-                const int units = (PF_BN - z0) * 8;
-                for (int u = tid; u < 3 * units; u += 2 * PF_BM) {
-                    const int blk = u / units, w = u - blk * units, key = z0 + (w >> 3);
-                    *reinterpret_cast<uint4 *>(vb + blk * PF_BLK + (key >> 6) * PF_BOX + (key & 63) * 128 +
-                                               (w & 7) * 16) = make_uint4(0, 0, 0, 0);
-                }
+                auto clear = [&](int z0, int z1) {
+                    // 3 blocks x (z1 - z0) rows x 8 16-byte units; key j of a block
+                    // sits in 64-row box j / 64, row j % 64
+                    const int units = (z1 - z0) * 8;
+                    for (int u = tid; u < 3 * units; u += 2 * PF_BM) {
+                        const int blk = u / units, w = u - blk * units, key = z0 + (w >> 3);
+                        *reinterpret_cast<uint4 *>(vb + blk * PF_BLK + (key >> 6) * PF_BOX +
+                                                   (key & 63) * 128 + (w & 7) * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                };
+                if (kt == nkt - 1 && z_end < PF_BN) clear(z_end, PF_BN);
+                if (WIN && w0 < w1) clear(w0, w1);
                 fence_proxy_async_smem();
             }
             tc_fence_before();
@@ -600,11 +647,15 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
     }
 }
 
+template <int R16, bool WIN>
+cudaError_t launch_win(const PfMaps &maps, const PfArgs &a, dim3 grid, cudaStream_t s) {
+    cudaError_t e = smem_limit_once(prefill_tc_kernel<R16, WIN>, PF_SMEM);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(prefill_tc_kernel<R16, WIN>, grid, dim3(PF_THREADS), PF_SMEM, s, maps, a);
+}
 template <int R16>
 cudaError_t launch_r16(const PfMaps &maps, const PfArgs &a, dim3 grid, cudaStream_t s) {
-    cudaError_t e = smem_limit_once(prefill_tc_kernel<R16>, PF_SMEM);
-    if (e != cudaSuccess) return e;
-    return launch_pdl(prefill_tc_kernel<R16>, grid, dim3(PF_THREADS), PF_SMEM, s, maps, a);
+    return a.window ? launch_win<R16, true>(maps, a, grid, s) : launch_win<R16, false>(maps, a, grid, s);
 }
 
 }  // namespace
@@ -673,6 +724,8 @@ int launch_prefill_tc(const PrefillTcArgs &p) {
     a.max_len = p.max_pages * c.page_size;
     a.n_qtiles = n_qtiles;
     a.scale_log2 = 1.4426950408889634f / sqrtf(128.f);
+    a.window = std::min(p.window, a.max_len);
+    a.sinks = std::min(p.sinks, a.max_len);
     // heaviest query tiles (most keys) first: blockIdx.z counts tiles from the end
     const dim3 grid(c.H, p.B, n_qtiles);
     cudaError_t e;
