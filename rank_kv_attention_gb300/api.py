@@ -342,36 +342,76 @@ def prefill(X, Q, cu_rows, start_pos, max_ctx, W_S_K, W_S_V, U_K, U_V, B_K, B_V,
 # ----------------------------------------------------------------------------
 # Sliding window with sinks, and the page plan of such a cache (see
 # include/lrkv.h).  These check every shape, and that all tensors lie on the
-# current device, before the library is called.
+# current device, before the library is called; one comparison per property on
+# the way through, the message only where one fails.
 # ----------------------------------------------------------------------------
-def _arg(t, name, dtype, shape):
-    """Address of a tensor of exactly this dtype and shape, contiguous, on the current device."""
-    if (not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != shape or not t.is_cuda
-            or not t.is_contiguous() or t.get_device() != torch.cuda.current_device()):
-        _need(t, name, dtype)
-        if t.shape != shape:
-            raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-        raise ValueError(f"{name} is on cuda:{t.get_device()}, not on the current device "
-                         f"cuda:{torch.cuda.current_device()}")
-    return t.data_ptr()
+_F4 = ctypes.c_float * 4
+_i32, _Tensor = torch.int32, torch.Tensor
 
 
-def _table_arg(page_table, B):
-    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
+def _refuse(t, name, dtype, shape, dev):
+    """Say what is wrong with an argument that _arg does not take."""
+    _need(t, name, dtype)
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    raise ValueError(f"{name} is on cuda:{t.get_device()}, not on the current device cuda:{dev}")
+
+
+def _arg(t, name, dtype, shape, dev):
+    """Address of a tensor of exactly this dtype and shape, contiguous, on the current device `dev`."""
+    if (isinstance(t, _Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == dev
+            and t.is_contiguous()):
+        return t.data_ptr()
+    _refuse(t, name, dtype, shape, dev)
+
+
+def _table_arg(page_table, B, dev):
+    if not isinstance(page_table, _Tensor) or page_table.dim() != 2:
         raise ValueError("page_table must be a [B, max_pages] tensor")
-    return _arg(page_table, "page_table", torch.int32, (B, page_table.shape[1])), page_table.shape[1]
+    max_pages = page_table.shape[1]
+    return _arg(page_table, "page_table", _i32, (B, max_pages), dev), max_pages
 
 
-def _own_buffer(shape, dtype, device, stream):
+def _cache_arg(cache, dev):
+    """PagedCache.desc() with all pools' shapes and devices checked."""
+    S_K, R_K = cache.S_K, cache.R_K
+    if not (isinstance(S_K, _Tensor) and isinstance(R_K, _Tensor)) or S_K.dim() not in (3, 4) or R_K.dim() != 4:
+        raise ValueError("S_K must be [num_pages, page_size, (G,) d_h] and R_K [num_pages, page_size, H, r]")
+    dt, ss = S_K.dtype, S_K.shape
+    n, ps, H, r = rs = R_K.shape
+    if dt not in _DT:
+        raise TypeError(f"cache dtype {dt} is not supported")
+    if ss[0] != n or ss[1] != ps:
+        raise ValueError(f"S_K {list(ss)} and R_K {list(rs)} must have the same pages")
+    act = torch.bfloat16 if dt is torch.float8_e4m3fn else dt
+    N_K = cache.N_K
+    desc = _abi.CacheDesc(_arg(S_K, "S_K", dt, ss, dev), _arg(cache.S_V, "S_V", dt, ss, dev),
+                          _arg(R_K, "R_K", dt, rs, dev), _arg(cache.R_V, "R_V", dt, rs, dev), n, ps, H, ss[-1], r,
+                          _DT[dt], _F4(*cache.scale),
+                          None if N_K is None else _arg(N_K, "N_K", act, (n, ps, H), dev), cache.norm_eps,
+                          ss[2] if len(ss) == 4 else 1)
+    return desc, act, H, ss[-1], r
+
+
+def _own_buffer(shape, dtype, dev, stream):
     """A buffer made for a call on `stream`: not reused before the stream has passed it."""
-    t = torch.empty(shape, dtype=dtype, device=device)
+    t = torch.empty(shape, dtype=dtype, device=dev)
     if stream is not None:
         t.record_stream(stream)
     return t
 
 
-def _status_ptr(status):
-    return None if status is None else _arg(status, "status", torch.int32, (1,))
+def _raw_stream(stream, dev):
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _device_of(t, name):
+    """The current device, where the first argument has to be."""
+    if not isinstance(t, _Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return torch.cuda.current_device()
 
 
 def decode_window_workspace_bytes(B, H, d_h, r, max_seq_len, window, sinks=0, dtype=torch.bfloat16) -> int:
@@ -382,27 +422,27 @@ def decode_window(q, cache: PagedCache, B_K, B_V, seq_lens, page_table, max_seq_
                   out=None, ws=None, status=None, stream=None):
     """lrkv_decode_window: one decode step in which request b sees its last
     ``window`` rows and its first ``sinks`` rows; returns out [B, H, d_h]."""
+    dev = _device_of(q, "q")
+    desc, dt, H, d_h, r = _cache_arg(cache, dev)
     if q.dim() != 3:
         raise ValueError("q must be a [B, H, d_h] tensor")
-    dt = cache.act_dtype
-    desc = cache.desc()
-    B, H, d_h, r = q.shape[0], desc.H, desc.d_h, desc.r
-    pq = _arg(q, "q", dt, (B, H, d_h))
-    bases = _arg(B_K, "B_K", dt, (H, d_h, r)), _arg(B_V, "B_V", dt, (H, d_h, r))
-    lens = _arg(seq_lens, "seq_lens", torch.int32, (B,))
-    table, max_pages = _table_arg(page_table, B)
-    if out is None:
-        out = _own_buffer(q.shape, dt, q.device, stream)
+    B = q.shape[0]
+    shape, base = (B, H, d_h), (H, d_h, r)
+    table, max_pages = _table_arg(page_table, B, dev)
     L = _abi.lib()
+    if out is None:
+        out = _own_buffer(shape, dt, q.device, stream)
     if ws is None:
-        ws = _own_buffer(max(1, L.lrkv_decode_window_workspace_bytes(B, H, d_h, r, max_seq_len, window,
-                                                                     sinks, desc.dtype)),
-                         torch.uint8, q.device, stream)
-    code = L.lrkv_decode_window(pq, ctypes.byref(desc), *bases, lens, table, B, max_pages, max_seq_len,
-                                window, sinks, _arg(out, "out", dt, (B, H, d_h)),
-                                _arg(ws, "ws", torch.uint8, (ws.numel(),)), ws.numel(),
-                                _status_ptr(status), _stream(stream))
-    _abi.check("lrkv_decode_window", code)
+        ws = _own_buffer(max(1, L.lrkv_decode_window_workspace_bytes(B, H, d_h, r, max_seq_len, window, sinks,
+                                                                     desc.dtype)), torch.uint8, q.device, stream)
+    n = ws.numel()
+    code = L.lrkv_decode_window(
+        _arg(q, "q", dt, shape, dev), desc, _arg(B_K, "B_K", dt, base, dev), _arg(B_V, "B_V", dt, base, dev),
+        _arg(seq_lens, "seq_lens", _i32, (B,), dev), table, B, max_pages, max_seq_len, window, sinks,
+        _arg(out, "out", dt, shape, dev), _arg(ws, "ws", torch.uint8, (n,), dev), n,
+        None if status is None else _arg(status, "status", _i32, (1,), dev), _raw_stream(stream, dev))
+    if code:
+        _abi.check("lrkv_decode_window", code)
     return out
 
 
@@ -411,29 +451,30 @@ def prefill_window(X, Q, cu_rows, start_pos, max_ctx, W_S_K, W_S_V, U_K, U_V, B_
                    stream=None):
     """lrkv_prefill_window: append the chunk X, then attention of each row's Q
     over the last ``window`` rows up to its own and the first ``sinks`` rows."""
+    dev = _device_of(X, "X")
+    desc, dt, H, d_h, r = _cache_arg(cache, dev)
     if X.dim() != 2:
         raise ValueError("X must be a [n, d] tensor")
-    dt = cache.act_dtype
-    desc = cache.desc()
     n, d = X.shape
-    H, d_h, r, G = desc.H, desc.d_h, desc.r, max(1, desc.G)
     B = start_pos.shape[0]
-    if out is None:
-        out = _own_buffer(Q.shape, dt, X.device, stream)
+    shape, base, shared, private = (n, H, d_h), (H, d_h, r), (max(1, desc.G) * d_h, d), (H, r, d)
+    table, max_pages = _table_arg(page_table, B, dev)
     L = _abi.lib()
+    if out is None:
+        out = _own_buffer(shape, dt, X.device, stream)
     if ws is None:
         ws = _own_buffer(max(1, L.lrkv_prefill_workspace_bytes(B, n, H, d_h, r, max_ctx, desc.dtype)),
                          torch.uint8, X.device, stream)
-    table, max_pages = _table_arg(page_table, B)
+    m = ws.numel()
     code = L.lrkv_prefill_window(
-        _arg(X, "X", dt, (n, d)), _arg(Q, "Q", dt, (n, H, d_h)),
-        _arg(cu_rows, "cu_rows", torch.int32, (B + 1,)), _arg(start_pos, "start_pos", torch.int32, (B,)),
-        B, n, max_ctx, d, _arg(W_S_K, "W_S_K", dt, (G * d_h, d)), _arg(W_S_V, "W_S_V", dt, (G * d_h, d)),
-        _arg(U_K, "U_K", dt, (H, r, d)), _arg(U_V, "U_V", dt, (H, r, d)),
-        _arg(B_K, "B_K", dt, (H, d_h, r)), _arg(B_V, "B_V", dt, (H, d_h, r)), ctypes.byref(desc), table,
-        max_pages, window, sinks, _arg(out, "out", dt, (n, H, d_h)),
-        _arg(ws, "ws", torch.uint8, (ws.numel(),)), ws.numel(), _status_ptr(status), _stream(stream))
-    _abi.check("lrkv_prefill_window", code)
+        _arg(X, "X", dt, (n, d), dev), _arg(Q, "Q", dt, shape, dev), _arg(cu_rows, "cu_rows", _i32, (B + 1,), dev),
+        _arg(start_pos, "start_pos", _i32, (B,), dev), B, n, max_ctx, d, _arg(W_S_K, "W_S_K", dt, shared, dev),
+        _arg(W_S_V, "W_S_V", dt, shared, dev), _arg(U_K, "U_K", dt, private, dev), _arg(U_V, "U_V", dt, private, dev),
+        _arg(B_K, "B_K", dt, base, dev), _arg(B_V, "B_V", dt, base, dev), desc, table, max_pages, window, sinks,
+        _arg(out, "out", dt, shape, dev), _arg(ws, "ws", torch.uint8, (m,), dev), m,
+        None if status is None else _arg(status, "status", _i32, (1,), dev), _raw_stream(stream, dev))
+    if code:
+        _abi.check("lrkv_prefill_window", code)
     return out
 
 
@@ -455,33 +496,32 @@ def page_plan(seq_lens, new_rows, page_table, free_pages, n_free, page_size, max
     """lrkv_page_plan: pages and slots of one step, in which request b gains
     new_rows[b] rows (-1: it ends).  page_table is updated in place; free_out
     ([num_pages]) takes the free list after the step."""
+    dev = _device_of(seq_lens, "seq_lens")
     if seq_lens.dim() != 1 or free_pages.dim() != 1:
         raise ValueError("seq_lens and free_pages must be one-dimensional")
-    B, num_pages = seq_lens.shape[0], free_pages.shape[0]
-    dev = seq_lens.device
-    lens, new = _arg(seq_lens, "seq_lens", torch.int32, (B,)), _arg(new_rows, "new_rows", torch.int32, (B,))
-    table, max_pages = _table_arg(page_table, B)
-    free, nf = (_arg(free_pages, "free_pages", torch.int32, (num_pages,)),
-                _arg(n_free, "n_free", torch.int32, (1,)))
-    if free_out is None:
-        free_out = _own_buffer((num_pages,), torch.int32, dev, stream)
     if max_rows < 0:
         raise ValueError("max_rows must not be negative")
-    # one buffer for the small outputs: each part starts on a 16-byte boundary
-    sizes = (max_rows, max_rows, max_rows, B, B + 1, 1)
-    starts, at = [], 0
-    for s in sizes:
-        starts.append(at)
-        at += (s + 3) // 4 * 4
-    buf = _own_buffer((at,), torch.int32, dev, stream)
-    pos, ids, slots, after, cu, left = (buf[a:a + s] for a, s in zip(starts, sizes))
+    B, num_pages = seq_lens.shape[0], free_pages.shape[0]
+    table, max_pages = _table_arg(page_table, B, dev)
+    if free_out is None:
+        free_out = _own_buffer((num_pages,), _i32, seq_lens.device, stream)
+    # one buffer for the small outputs, each part on a 16-byte boundary
+    r4, b4, c4 = (max_rows + 3) // 4 * 4, (B + 3) // 4 * 4, (B + 4) // 4 * 4
+    parts = _own_buffer((3 * r4 + b4 + c4 + 4,), _i32, seq_lens.device, stream)
+    p = parts.data_ptr()
+    after = p + 12 * r4
+    cu = after + 4 * b4
     code = _abi.lib().lrkv_page_plan(
-        lens, new, B, max_pages, page_size, num_pages, window, sinks, max_rows, table, free, nf,
-        after.data_ptr(), cu.data_ptr(), pos.data_ptr(), ids.data_ptr(), slots.data_ptr(),
-        _arg(free_out, "free_out", torch.int32, (num_pages,)), left.data_ptr(), _status_ptr(status),
-        _stream(stream))
-    _abi.check("lrkv_page_plan", code)
-    return PagePlan(after, cu, pos, ids, slots, free_out, left)
+        _arg(seq_lens, "seq_lens", _i32, (B,), dev), _arg(new_rows, "new_rows", _i32, (B,), dev), B, max_pages,
+        page_size, num_pages, window, sinks, max_rows, table,
+        _arg(free_pages, "free_pages", _i32, (num_pages,), dev), _arg(n_free, "n_free", _i32, (1,), dev),
+        after, cu, p, p + 4 * r4, p + 8 * r4, _arg(free_out, "free_out", _i32, (num_pages,), dev), cu + 4 * c4,
+        None if status is None else _arg(status, "status", _i32, (1,), dev), _raw_stream(stream, dev))
+    if code:
+        _abi.check("lrkv_page_plan", code)
+    pos, _, ids, _, slots, _, lens, _, cu_rows, _, left, _ = parts.split(
+        (max_rows, r4 - max_rows, max_rows, r4 - max_rows, max_rows, r4 - max_rows, B, b4 - B, B + 1, c4 - B - 1, 1, 3))
+    return PagePlan(lens, cu_rows, pos, ids, slots, free_out, left)
 
 
 # ----------------------------------------------------------------------------

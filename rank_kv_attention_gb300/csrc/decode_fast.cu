@@ -35,8 +35,7 @@
 // results, so only launch latency overlaps.
 #include <algorithm>
 
-#include "decode_kernels.cuh"
-#include "tc_common.cuh"
+#include "decode_tile.cuh"
 
 namespace lrkv {
 
@@ -247,25 +246,10 @@ __device__ bool issue_next(IssueCursor *cur, const FastParams &P, const FastMaps
     return true;
 }
 
-__device__ __forceinline__ uint32_t ld_u32(const __nv_bfloat16 *p) {
-    return *reinterpret_cast<const uint32_t *>(p);
-}
-
-// The running maximum (log2 units) only moves when a tile exceeds it by this
-// much; weights stay below 2^kLazyMax, far inside fp32 range.
-constexpr float kLazyMax = 8.f;
-
 // Byte offset, inside a stage region made of 64-column swizzled boxes, of the
 // 16-byte chunk `cc` (counted along the row) of tile row `j`.
 __device__ __forceinline__ uint32_t box_chunk(int j, int cc) {
     return (uint32_t)((cc >> 3) * (16 * 128)) + swz128(j, cc & 7);
-}
-
-// Byte offset, inside a region of 64-column swizzled boxes of TS rows, of the
-// 16-byte chunk `cc` (counted along the row) of row `j`.
-template <int TS>
-__device__ __forceinline__ uint32_t box_chunk_rows(int j, int cc) {
-    return (uint32_t)((cc >> 3) * (TS * 128)) + swz128(j, cc & 7);
 }
 
 // ---------------------------------------------------------------------------
@@ -347,17 +331,6 @@ __device__ __forceinline__ void q8_segment_setup(const FastParams &P, int b, int
     fR[1] = __shfl_sync(0xffffffffu, fp, 8 * tq + 4);
 }
 
-__device__ __forceinline__ uint32_t lds_u32(const uint8_t *p) {
-    return *reinterpret_cast<const uint32_t *>(p);
-}
-__device__ __forceinline__ uint32_t lds_u16(const uint8_t *p) {
-    return *reinterpret_cast<const uint16_t *>(p);
-}
-__device__ __forceinline__ uint32_t f16x2_lo(uint32_t w) { return f16x2_from_e4m3x2((uint16_t)w); }
-__device__ __forceinline__ uint32_t f16x2_hi(uint32_t w) {
-    return f16x2_from_e4m3x2((uint16_t)(w >> 16));
-}
-
 // Scores of a tile: c[row x head] = fS . (S_K . Q^T) + fR . (R_K . blockdiag(p)^T).
 // rb: first stage row of the 16-row half being scored.
 template <class C>
@@ -386,22 +359,6 @@ __device__ __forceinline__ void q8_scores(const uint8_t *st, int rb, int warp, i
     }
 #pragma unroll
     for (int e = 0; e < 4; ++e) c[e] = fS[e & 1] * (c[e] + c1[e]) + fR[e & 1] * (c2[e] + c3[e]);
-}
-
-// A fragments of two value m-tiles from the 32-bit words of rows 2tq, 2tq+1,
-// 2tq+8, 2tq+9 (see the layout note above); MASK: zero invalid rows.
-template <bool MASK>
-__device__ __forceinline__ void q8_pair_frags(uint32_t w0, uint32_t w1, uint32_t w8, uint32_t w9,
-                                              uint32_t m01, uint32_t m89, uint32_t (&a)[4],
-                                              uint32_t (&b)[4]) {
-    const uint32_t x01 = prmt<0x5140>(w0, w1), y01 = prmt<0x7362>(w0, w1);
-    const uint32_t x89 = prmt<0x5140>(w8, w9), y89 = prmt<0x7362>(w8, w9);
-    a[0] = f16x2_lo(x01); a[1] = f16x2_hi(x01); a[2] = f16x2_lo(x89); a[3] = f16x2_hi(x89);
-    b[0] = f16x2_lo(y01); b[1] = f16x2_hi(y01); b[2] = f16x2_lo(y89); b[3] = f16x2_hi(y89);
-    if (MASK) {
-        a[0] &= m01; a[1] &= m01; a[2] &= m89; a[3] &= m89;
-        b[0] &= m01; b[1] &= m01; b[2] &= m89; b[3] &= m89;
-    }
 }
 
 // Values of a tile: accS += S_V^T . P^T, accR += R_V^T(warp columns) . P^T.
@@ -437,14 +394,6 @@ __device__ __forceinline__ void q8_values(const uint8_t *st, int rb, int warp, i
         if (MASK) { a[0] &= m01; a[1] &= m01; a[2] &= m89; a[3] &= m89; }
         mma_f16_16816(accR[mt], a, b0, b1);
     }
-}
-
-// Value column (relative to the tile's or the warp's first column) of
-// accumulator m-tile mt, element e, under the permutation of q8_values.
-template <int KSP>
-__device__ __forceinline__ int q8_value_col(int mt, int e, int gq) {
-    return (mt < (KSP & ~1)) ? 32 * (mt >> 1) + 4 * gq + 2 * (mt & 1) + (e >> 1)
-                             : 16 * mt + 2 * gq + (e >> 1);
 }
 
 template <class C>
@@ -1723,14 +1672,8 @@ static bool encode_cached(CUtensorMap *map, const MapKey &key, Encode &&encode) 
     return true;
 }
 
-// Map over a pool viewed as [rows, cols] elements of eb bytes (bf16, f16 or
-// 8-bit codes), as three dimensions (128 / eb columns, rows, cols * eb / 128
-// blocks of 128 bytes) with strides (eb, cols * eb, 128 bytes).  A box of
-// (128 / eb) x 16 x box_blocks (default: all blocks) with 128-byte swizzle
-// lands a 16-row tile as consecutive 16-row x 128-byte boxes (matches
-// box_chunk).
-static bool make_map(CUtensorMap *map, const void *pool, int64_t rows, int cols, int eb,
-                     int box_blocks = 0, bool f16 = false, int box_rows = 16) {
+bool make_map(CUtensorMap *map, const void *pool, int64_t rows, int cols, int eb, int box_blocks, bool f16,
+              int box_rows) {
     EncodeTiledFn enc = get_encode_tiled();
     if (!enc) return false;
     const int per = 128 / eb, blocks = cols * eb / 128;
@@ -1768,11 +1711,7 @@ static bool make_block_map(CUtensorMap *map, const void *pool, int64_t rows, int
     });
 }
 
-// Map over a row-major [rows, H] array of elements of eb bytes (bf16 joint
-// key norms, fp32 given scores) as (H, rows, 1): a box of H x 16 x 1 lands a
-// tile's 16 rows, unswizzled.
-static bool make_row_map(CUtensorMap *map, const void *base, int64_t rows, int H, int eb,
-                         int box_rows = 16) {
+bool make_row_map(CUtensorMap *map, const void *base, int64_t rows, int H, int eb, int box_rows) {
     EncodeTiledFn enc = get_encode_tiled();
     if (!enc) return false;
     return encode_cached(map, MapKey{base, rows, H, eb, box_rows, 2}, [&](CUtensorMap *m) {
@@ -1855,11 +1794,6 @@ static cudaError_t launch_fast_cfg(const DecodeArgs &a, const DecodeWs &ws, int 
     if (GS) P.norm = 0;
     return launch_pdl(kern, dim3(G), dim3(C::NT), C::SMEM, a.stream, maps, P);
 }
-
-#define LRKV_FAST_SHAPES(X) X(16, 16) X(16, 32) X(16, 48) X(16, 56) X(16, 64) X(32, 16) X(32, 32)
-
-// Shapes the tensor-core decode serves with two shared groups (bf16).
-#define LRKV_FAST_SHAPES_G2(X) X(16, 32) X(16, 48)
 
 bool fast_decode_supported(int H, int d_h, int r, int page_size, int dtype, int groups) {
     if (groups == 2) {

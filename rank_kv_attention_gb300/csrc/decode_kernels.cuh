@@ -99,6 +99,11 @@ cudaError_t launch_combine(const DecodeArgs &a, const DecodeWs &ws, int G);
 bool fast_decode_supported(int H, int d_h, int r, int page_size, int dtype, int groups = 1);
 
 int fast_decode_grid(int H, int r);
+
+// Windowed decode of the shapes fast_decode_supported covers (a.window > 0), with
+// ws_bytes of scratch for the states of split requests.
+cudaError_t launch_window_fast(const DecodeArgs &a, void *ws, size_t ws_bytes);
+size_t window_state_bytes(int B, int H, int r, int max_seq_len, int window, int sinks, int dtype);
 cudaError_t launch_split_fast(const DecodeArgs &a, const DecodeWs &ws, int G);
 
 // Exact RoPE on the tensor cores (bf16 cache, a tensor-core decode shape with

@@ -145,6 +145,12 @@ static int run_decode(const DecodeArgs &a, void *workspace, size_t ws_bytes) {
                                                                                   cache_groups(c)));
     const int G = fast ? geo.G_fast : geo.G_gen;
     cudaError_t e;
+    if (a.window && fast_decode_supported(c.H, c.d_h, c.r, c.page_size, c.dtype, cache_groups(c))) {
+        prof_before(LRKV_PROFILE_ATTENTION, a.stream);
+        e = launch_window_fast(a, workspace, ws_bytes);
+        prof_after(LRKV_PROFILE_ATTENTION, a.stream);
+        return e == cudaSuccess ? LRKV_OK : cuda_fail(e);
+    }
     if (c.dtype != LRKV_F32) {  // bf16 activations (bf16 or 8-bit cache)
         e = launch_prologue<__nv_bfloat16>(a, ws, G, kPlanTileAlign, fast);
         if (e == cudaSuccess && rope_fast) {
@@ -792,11 +798,19 @@ int lrkv_prefill(const void *X, const void *Q, const int32_t *cu_rows, const int
 // ---------------------------------------------------------------------------
 // Sliding window with sinks, and the page plan of such a cache
 // ---------------------------------------------------------------------------
+// The generic kernels' workspace, or the states of requests that the tensor-core
+// kernel splits over clusters.
+static size_t decode_window_ws_bytes(int B, int H, int d_h, int r, int max_seq_len, int window, int sinks,
+                                     int dtype) {
+    const size_t states = d_h == 128 ? window_state_bytes(B, H, r, max_seq_len, window, sinks, dtype) : 0;
+    return std::max(decode_ws_bytes(B, H, d_h, r, window_bound(max_seq_len, window, sinks)), align256(states));
+}
+
 size_t lrkv_decode_window_workspace_bytes(int32_t B, int32_t H, int32_t d_h, int32_t r,
                                           int32_t max_seq_len, int32_t window, int32_t sinks,
                                           int32_t dtype) {
     if (check_dims(H, d_h, r, dtype) || B < 1 || max_seq_len < 1 || window < 1 || sinks < 0) return 0;
-    return decode_ws_bytes(B, H, d_h, r, window_bound(max_seq_len, window, sinks));
+    return decode_window_ws_bytes(B, H, d_h, r, max_seq_len, window, sinks, dtype);
 }
 
 int lrkv_decode_window(const void *q, const lrkv_cache_t *cache, const void *B_K, const void *B_V,
@@ -833,6 +847,9 @@ int lrkv_decode_window(const void *q, const lrkv_cache_t *cache, const void *B_K
     a.out = out;
     a.status = dev_status;
     a.stream = (cudaStream_t)stream;
+    if (workspace_bytes < decode_window_ws_bytes(B, cache->H, cache->d_h, cache->r, max_seq_len, window, sinks,
+                                                 cache->dtype))
+        return LRKV_E_WORKSPACE;
     return run_decode(a, workspace, workspace_bytes);
 }
 

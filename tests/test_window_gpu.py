@@ -195,6 +195,17 @@ def test_decode_streams_at_once_and_graph_replay():
     assert torch.equal(out, run_decode(d, 1024, 4))
 
 
+@pytest.mark.parametrize("H,r,dtype", [(16, 48, "bf16"), (32, 32, "bf16"), (16, 56, "bf16"), (16, 64, "fp8")])
+@pytest.mark.parametrize("B", [1, 2, 5])
+def test_decode_split_requests(H, r, dtype, B):
+    """Few requests with windows long enough that each is split over clusters, one of them short and one empty."""
+    lens = [6000, 40, 0, 4097, 5999][:B]
+    case = decode_case(lens, H, 128, r, dtype, seed=B)
+    blank_unseen(case, 4000, 30)
+    got = host(run_decode(DevDecode(case), 4000, 30), case.act_dtype)
+    check(got, *decode_reference(case, 4000, 30), f"B={B}")
+
+
 # ---------------------------------------------------------------------------
 # Prefill
 # ---------------------------------------------------------------------------
@@ -316,6 +327,19 @@ def test_prefill_groups_and_norms():
     cache.norm_eps = 1e-6
     out = run_prefill(w, pt, cache, X, Q, rows, starts, 30, 3, "bf16")
     check_prefill(out, cache, w, pt, X, Q, rows, starts, 30, 3, "bf16", False, N_K=host(cache.N_K, "bf16"))
+
+
+def test_prefill_one_row_over_a_long_window():
+    """A single row per request through the per-row path, on an 8-bit cache and on one with key norms."""
+    for dtype in ("fp8", "bf16"):
+        w, pt, cache, X, Q = prefill_inputs([1], [5000], 64, 16, 128, 48, dtype, 4500, 3, seed=11)
+        N = None
+        if dtype == "bf16":
+            cache.N_K = torch.rand(*cache.R_K.shape[:3], device="cuda").add_(0.5).to(torch.bfloat16)
+            cache.norm_eps = 1e-6
+        out = run_prefill(w, pt, cache, X, Q, [1], [5000], 4500, 3, "bf16")
+        N = host(cache.N_K, "bf16") if dtype == "bf16" else None
+        check_prefill(out, cache, w, pt, X, Q, [1], [5000], 4500, 3, dtype, False, N_K=N)
 
 
 def test_prefill_empty_requests_and_no_rows():
