@@ -407,9 +407,11 @@ LRKV_API int lrkv_key_norms(const int32_t *positions, const int32_t *seq_ids, in
  *
  * lrkv_decode_window takes the arguments of lrkv_decode.  Its workspace is
  * lrkv_decode_window_workspace_bytes(...) bytes, 256-byte aligned, scratch
- * that needs no initialisation; no block waits for another outside its own
- * thread-block cluster, so calls on several streams run side by side (each
- * with a workspace of its own).
+ * that needs no initialisation.  Most calls are one launch and need none: that
+ * function returns 0 and workspace may be NULL.  (Few requests with long windows
+ * are split over the GPU and leave partial states.)  No block waits for another
+ * outside its own thread-block cluster, so calls on several streams run side by
+ * side (each with a workspace of its own).
  *
  * lrkv_prefill_window takes the arguments of lrkv_prefill and its workspace
  * (lrkv_prefill_workspace_bytes); rows 0 .. start_pos[b]-1 that a new row can
@@ -461,7 +463,7 @@ LRKV_API int lrkv_prefill_window(const void *X, const void *Q, const int32_t *cu
  *     int32: free_pages[0 .. n_free) are the pages nobody holds; after the call
  *     free_out[0 .. n_free_out) are, and the rest of free_out is untouched.
  *   seq_lens_out [B]: L + n, or 0 for a request that ended.  cu_rows [B + 1].
- *   positions, seq_ids, slots [max_rows], 16-byte aligned.
+ *   positions, seq_ids, slots [max_rows].
  * All on the device; no output may overlap an input (keep two free lists and
  * two length arrays and swap them).
  *

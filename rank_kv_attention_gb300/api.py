@@ -342,55 +342,55 @@ def prefill(X, Q, cu_rows, start_pos, max_ctx, W_S_K, W_S_V, U_K, U_V, B_K, B_V,
 # ----------------------------------------------------------------------------
 # Sliding window with sinks, and the page plan of such a cache (see
 # include/lrkv.h).  These check every shape, and that all tensors lie on the
-# current device, before the library is called; one comparison per property on
-# the way through, the message only where one fails.
+# current device, before the library is called.  A decode step takes less time
+# than a careful look at its arguments, so each function compares everything in
+# one expression and looks for the fault only when something differs.
 # ----------------------------------------------------------------------------
 _F4 = ctypes.c_float * 4
-_i32, _Tensor = torch.int32, torch.Tensor
+_i32, _u8, _Tensor = torch.int32, torch.uint8, torch.Tensor
+_current_device = torch.cuda.current_device
 
 
-def _refuse(t, name, dtype, shape, dev):
-    """Say what is wrong with an argument that _arg does not take."""
-    _need(t, name, dtype)
-    if t.shape != shape:
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    raise ValueError(f"{name} is on cuda:{t.get_device()}, not on the current device cuda:{dev}")
+def _refuse(args, dev):
+    """Raise for the first of (tensor, name, dtype, shape) that is not such a contiguous tensor on device `dev`."""
+    for t, name, dtype, shape in args:
+        _need(t, name, dtype)
+        if t.shape != shape:
+            raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+        if t.get_device() != dev:
+            raise ValueError(f"{name} is on cuda:{t.get_device()}, not on the current device cuda:{dev}")
 
 
-def _arg(t, name, dtype, shape, dev):
-    """Address of a tensor of exactly this dtype and shape, contiguous, on the current device `dev`."""
-    if (isinstance(t, _Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == dev
-            and t.is_contiguous()):
-        return t.data_ptr()
-    _refuse(t, name, dtype, shape, dev)
-
-
-def _table_arg(page_table, B, dev):
-    if not isinstance(page_table, _Tensor) or page_table.dim() != 2:
-        raise ValueError("page_table must be a [B, max_pages] tensor")
-    max_pages = page_table.shape[1]
-    return _arg(page_table, "page_table", _i32, (B, max_pages), dev), max_pages
+def _fits(args, dev):
+    for t, name, dtype, shape in args:
+        if not (isinstance(t, _Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == dev
+                and t.is_contiguous()):
+            _refuse(args, dev)
 
 
 def _cache_arg(cache, dev):
     """PagedCache.desc() with all pools' shapes and devices checked."""
-    S_K, R_K = cache.S_K, cache.R_K
+    S_K, S_V, R_K, R_V, N_K = cache.S_K, cache.S_V, cache.R_K, cache.R_V, cache.N_K
     if not (isinstance(S_K, _Tensor) and isinstance(R_K, _Tensor)) or S_K.dim() not in (3, 4) or R_K.dim() != 4:
         raise ValueError("S_K must be [num_pages, page_size, (G,) d_h] and R_K [num_pages, page_size, H, r]")
-    dt, ss = S_K.dtype, S_K.shape
-    n, ps, H, r = rs = R_K.shape
+    dt, ss, rs = S_K.dtype, S_K.shape, R_K.shape
+    n, ps, H, r = rs
     if dt not in _DT:
         raise TypeError(f"cache dtype {dt} is not supported")
     if ss[0] != n or ss[1] != ps:
         raise ValueError(f"S_K {list(ss)} and R_K {list(rs)} must have the same pages")
     act = torch.bfloat16 if dt is torch.float8_e4m3fn else dt
-    N_K = cache.N_K
-    desc = _abi.CacheDesc(_arg(S_K, "S_K", dt, ss, dev), _arg(cache.S_V, "S_V", dt, ss, dev),
-                          _arg(R_K, "R_K", dt, rs, dev), _arg(cache.R_V, "R_V", dt, rs, dev), n, ps, H, ss[-1], r,
-                          _DT[dt], _F4(*cache.scale),
-                          None if N_K is None else _arg(N_K, "N_K", act, (n, ps, H), dev), cache.norm_eps,
-                          ss[2] if len(ss) == 4 else 1)
-    return desc, act, H, ss[-1], r
+    if not (isinstance(S_V, _Tensor) and isinstance(R_V, _Tensor) and S_V.dtype is dt and R_K.dtype is dt
+            and R_V.dtype is dt and S_V.shape == ss and R_V.shape == rs and S_K.get_device() == dev
+            and S_V.get_device() == dev and R_K.get_device() == dev and R_V.get_device() == dev
+            and S_K.is_contiguous() and S_V.is_contiguous() and R_K.is_contiguous() and R_V.is_contiguous()):
+        _refuse(((S_K, "S_K", dt, ss), (S_V, "S_V", dt, ss), (R_K, "R_K", dt, rs), (R_V, "R_V", dt, rs)), dev)
+    nk = None
+    if N_K is not None:
+        _fits(((N_K, "N_K", act, (n, ps, H)),), dev)
+        nk = N_K.data_ptr()
+    return _abi.CacheDesc(S_K.data_ptr(), S_V.data_ptr(), R_K.data_ptr(), R_V.data_ptr(), n, ps, H, ss[-1], r,
+                          _DT[dt], _F4(*cache.scale), nk, cache.norm_eps, ss[2] if len(ss) == 4 else 1), act, H, ss[-1], r
 
 
 def _own_buffer(shape, dtype, dev, stream):
@@ -411,7 +411,29 @@ def _device_of(t, name):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    return torch.cuda.current_device()
+    return _current_device()
+
+
+def _dim(t, name, n):
+    if not isinstance(t, _Tensor) or t.dim() != n:
+        raise ValueError(f"{name} must be a tensor of {n} dimension(s)")
+    return t.shape
+
+
+def _workspace(ws, dev):
+    """(address, bytes) of a caller's workspace."""
+    if ws is None:
+        return None, 0
+    n = ws.numel()
+    _fits(((ws, "ws", _u8, (n,)),), dev)
+    return ws.data_ptr(), n
+
+
+def _status(status, dev):
+    if status is None:
+        return None
+    _fits(((status, "status", _i32, (1,)),), dev)
+    return status.data_ptr()
 
 
 def decode_window_workspace_bytes(B, H, d_h, r, max_seq_len, window, sinks=0, dtype=torch.bfloat16) -> int:
@@ -424,23 +446,32 @@ def decode_window(q, cache: PagedCache, B_K, B_V, seq_lens, page_table, max_seq_
     ``window`` rows and its first ``sinks`` rows; returns out [B, H, d_h]."""
     dev = _device_of(q, "q")
     desc, dt, H, d_h, r = _cache_arg(cache, dev)
-    if q.dim() != 3:
-        raise ValueError("q must be a [B, H, d_h] tensor")
-    B = q.shape[0]
-    shape, base = (B, H, d_h), (H, d_h, r)
-    table, max_pages = _table_arg(page_table, B, dev)
-    L = _abi.lib()
+    B = _dim(q, "q", 3)[0]
+    max_pages = _dim(page_table, "page_table", 2)[1]
     if out is None:
-        out = _own_buffer(shape, dt, q.device, stream)
-    if ws is None:
-        ws = _own_buffer(max(1, L.lrkv_decode_window_workspace_bytes(B, H, d_h, r, max_seq_len, window, sinks,
-                                                                     desc.dtype)), torch.uint8, q.device, stream)
-    n = ws.numel()
-    code = L.lrkv_decode_window(
-        _arg(q, "q", dt, shape, dev), desc, _arg(B_K, "B_K", dt, base, dev), _arg(B_V, "B_V", dt, base, dev),
-        _arg(seq_lens, "seq_lens", _i32, (B,), dev), table, B, max_pages, max_seq_len, window, sinks,
-        _arg(out, "out", dt, shape, dev), _arg(ws, "ws", torch.uint8, (n,), dev), n,
-        None if status is None else _arg(status, "status", _i32, (1,), dev), _raw_stream(stream, dev))
+        out = torch.empty_like(q)
+        if stream is not None:
+            out.record_stream(stream)
+    shape, base = (B, H, d_h), (H, d_h, r)
+    if not (isinstance(B_K, _Tensor) and isinstance(B_V, _Tensor) and isinstance(seq_lens, _Tensor)
+            and isinstance(out, _Tensor) and q.dtype is dt and B_K.dtype is dt and B_V.dtype is dt and out.dtype is dt
+            and seq_lens.dtype is _i32 and page_table.dtype is _i32 and q.shape == shape and out.shape == shape
+            and B_K.shape == base and B_V.shape == base and seq_lens.shape == (B,) and page_table.shape[0] == B
+            and q.get_device() == dev and B_K.get_device() == dev and B_V.get_device() == dev
+            and seq_lens.get_device() == dev and page_table.get_device() == dev and out.get_device() == dev
+            and q.is_contiguous() and B_K.is_contiguous() and B_V.is_contiguous() and seq_lens.is_contiguous()
+            and page_table.is_contiguous() and out.is_contiguous()):
+        _refuse(((q, "q", dt, shape), (B_K, "B_K", dt, base), (B_V, "B_V", dt, base), (seq_lens, "seq_lens", _i32, (B,)),
+                 (page_table, "page_table", _i32, (B, max_pages)), (out, "out", dt, shape)), dev)
+    L = _abi.lib()
+    args = (q.data_ptr(), desc, B_K.data_ptr(), B_V.data_ptr(), seq_lens.data_ptr(), page_table.data_ptr(), B,
+            max_pages, max_seq_len, window, sinks, out.data_ptr())
+    tail = _status(status, dev), _raw_stream(stream, dev)
+    code = L.lrkv_decode_window(*args, *_workspace(ws, dev), *tail)
+    if code == _abi.LRKV_E_WORKSPACE and ws is None:  # (most calls need none)
+        n = L.lrkv_decode_window_workspace_bytes(B, H, d_h, r, max_seq_len, window, sinks, desc.dtype)
+        ws = _own_buffer((n,), _u8, q.device, stream)
+        code = L.lrkv_decode_window(*args, ws.data_ptr(), n, *tail)
     if code:
         _abi.check("lrkv_decode_window", code)
     return out
@@ -453,26 +484,24 @@ def prefill_window(X, Q, cu_rows, start_pos, max_ctx, W_S_K, W_S_V, U_K, U_V, B_
     over the last ``window`` rows up to its own and the first ``sinks`` rows."""
     dev = _device_of(X, "X")
     desc, dt, H, d_h, r = _cache_arg(cache, dev)
-    if X.dim() != 2:
-        raise ValueError("X must be a [n, d] tensor")
-    n, d = X.shape
-    B = start_pos.shape[0]
+    n, d = _dim(X, "X", 2)
+    (B,) = _dim(start_pos, "start_pos", 1)
+    max_pages = _dim(page_table, "page_table", 2)[1]
     shape, base, shared, private = (n, H, d_h), (H, d_h, r), (max(1, desc.G) * d_h, d), (H, r, d)
-    table, max_pages = _table_arg(page_table, B, dev)
-    L = _abi.lib()
     if out is None:
         out = _own_buffer(shape, dt, X.device, stream)
+    _fits(((X, "X", dt, (n, d)), (Q, "Q", dt, shape), (cu_rows, "cu_rows", _i32, (B + 1,)),
+           (start_pos, "start_pos", _i32, (B,)), (W_S_K, "W_S_K", dt, shared), (W_S_V, "W_S_V", dt, shared),
+           (U_K, "U_K", dt, private), (U_V, "U_V", dt, private), (B_K, "B_K", dt, base), (B_V, "B_V", dt, base),
+           (page_table, "page_table", _i32, (B, max_pages)), (out, "out", dt, shape)), dev)
+    L = _abi.lib()
     if ws is None:
-        ws = _own_buffer(max(1, L.lrkv_prefill_workspace_bytes(B, n, H, d_h, r, max_ctx, desc.dtype)),
-                         torch.uint8, X.device, stream)
-    m = ws.numel()
+        ws = _own_buffer((max(1, L.lrkv_prefill_workspace_bytes(B, n, H, d_h, r, max_ctx, desc.dtype)),), _u8, X.device,
+                         stream)
     code = L.lrkv_prefill_window(
-        _arg(X, "X", dt, (n, d), dev), _arg(Q, "Q", dt, shape, dev), _arg(cu_rows, "cu_rows", _i32, (B + 1,), dev),
-        _arg(start_pos, "start_pos", _i32, (B,), dev), B, n, max_ctx, d, _arg(W_S_K, "W_S_K", dt, shared, dev),
-        _arg(W_S_V, "W_S_V", dt, shared, dev), _arg(U_K, "U_K", dt, private, dev), _arg(U_V, "U_V", dt, private, dev),
-        _arg(B_K, "B_K", dt, base, dev), _arg(B_V, "B_V", dt, base, dev), desc, table, max_pages, window, sinks,
-        _arg(out, "out", dt, shape, dev), _arg(ws, "ws", torch.uint8, (m,), dev), m,
-        None if status is None else _arg(status, "status", _i32, (1,), dev), _raw_stream(stream, dev))
+        X.data_ptr(), Q.data_ptr(), cu_rows.data_ptr(), start_pos.data_ptr(), B, n, max_ctx, d, W_S_K.data_ptr(),
+        W_S_V.data_ptr(), U_K.data_ptr(), U_V.data_ptr(), B_K.data_ptr(), B_V.data_ptr(), desc, page_table.data_ptr(),
+        max_pages, window, sinks, out.data_ptr(), *_workspace(ws, dev), _status(status, dev), _raw_stream(stream, dev))
     if code:
         _abi.check("lrkv_prefill_window", code)
     return out
@@ -497,30 +526,28 @@ def page_plan(seq_lens, new_rows, page_table, free_pages, n_free, page_size, max
     new_rows[b] rows (-1: it ends).  page_table is updated in place; free_out
     ([num_pages]) takes the free list after the step."""
     dev = _device_of(seq_lens, "seq_lens")
-    if seq_lens.dim() != 1 or free_pages.dim() != 1:
-        raise ValueError("seq_lens and free_pages must be one-dimensional")
+    (B,), (num_pages,) = _dim(seq_lens, "seq_lens", 1), _dim(free_pages, "free_pages", 1)
+    max_pages = _dim(page_table, "page_table", 2)[1]
     if max_rows < 0:
         raise ValueError("max_rows must not be negative")
-    B, num_pages = seq_lens.shape[0], free_pages.shape[0]
-    table, max_pages = _table_arg(page_table, B, dev)
     if free_out is None:
         free_out = _own_buffer((num_pages,), _i32, seq_lens.device, stream)
-    # one buffer for the small outputs, each part on a 16-byte boundary
-    r4, b4, c4 = (max_rows + 3) // 4 * 4, (B + 3) // 4 * 4, (B + 4) // 4 * 4
-    parts = _own_buffer((3 * r4 + b4 + c4 + 4,), _i32, seq_lens.device, stream)
-    p = parts.data_ptr()
-    after = p + 12 * r4
-    cu = after + 4 * b4
+    _fits(((seq_lens, "seq_lens", _i32, (B,)), (new_rows, "new_rows", _i32, (B,)),
+           (page_table, "page_table", _i32, (B, max_pages)), (free_pages, "free_pages", _i32, (num_pages,)),
+           (n_free, "n_free", _i32, (1,)), (free_out, "free_out", _i32, (num_pages,))), dev)
+    # one buffer for the small outputs
+    sizes = (max_rows, max_rows, max_rows, B, B + 1, 1)
+    parts = _own_buffer((3 * max_rows + 2 * B + 2,), _i32, seq_lens.device, stream)
+    p, row = parts.data_ptr(), 4 * max_rows
+    after = p + 3 * row
+    cu = after + 4 * B
     code = _abi.lib().lrkv_page_plan(
-        _arg(seq_lens, "seq_lens", _i32, (B,), dev), _arg(new_rows, "new_rows", _i32, (B,), dev), B, max_pages,
-        page_size, num_pages, window, sinks, max_rows, table,
-        _arg(free_pages, "free_pages", _i32, (num_pages,), dev), _arg(n_free, "n_free", _i32, (1,), dev),
-        after, cu, p, p + 4 * r4, p + 8 * r4, _arg(free_out, "free_out", _i32, (num_pages,), dev), cu + 4 * c4,
-        None if status is None else _arg(status, "status", _i32, (1,), dev), _raw_stream(stream, dev))
+        seq_lens.data_ptr(), new_rows.data_ptr(), B, max_pages, page_size, num_pages, window, sinks, max_rows,
+        page_table.data_ptr(), free_pages.data_ptr(), n_free.data_ptr(), after, cu, p, p + row, p + 2 * row,
+        free_out.data_ptr(), cu + 4 * (B + 1), _status(status, dev), _raw_stream(stream, dev))
     if code:
         _abi.check("lrkv_page_plan", code)
-    pos, _, ids, _, slots, _, lens, _, cu_rows, _, left, _ = parts.split(
-        (max_rows, r4 - max_rows, max_rows, r4 - max_rows, max_rows, r4 - max_rows, B, b4 - B, B + 1, c4 - B - 1, 1, 3))
+    pos, ids, slots, lens, cu_rows, left = parts.split_with_sizes(sizes)
     return PagePlan(lens, cu_rows, pos, ids, slots, free_out, left)
 
 

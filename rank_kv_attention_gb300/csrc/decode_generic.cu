@@ -110,8 +110,7 @@ __global__ void __launch_bounds__(NTHR, NTHR == 128 ? 10 : 1) decode_prologue_ke
     const T *__restrict__ q, const T *__restrict__ B_K, const int32_t *__restrict__ seq_lens,
     T *__restrict__ out,
     int B, int H, int d_h, int r, int max_len, int G, int tile_align, bool staged,
-    DecodeWs ws, int32_t *status, const float2 *__restrict__ rope_tab, RopeFastWs rf, bool early,
-    int window, int sinks) {
+    DecodeWs ws, int32_t *status, const float2 *__restrict__ rope_tab, RopeFastWs rf, bool early) {
     constexpr int nrows = (ROPE || NTHR == 128) ? 1 : kProRows;
     const int tid = threadIdx.x;
     // early mode: the split kernel may launch at once (its own early work
@@ -165,7 +164,7 @@ __global__ void __launch_bounds__(NTHR, NTHR == 128 ? 10 : 1) decode_prologue_ke
         const int per = (B + blockDim.x - 1) / blockDim.x;
         const int lo = tid * per, hi = min(B, lo + per);
         int32_t s = 0;
-        for (int b = lo; b < hi; ++b) s += streamed_len(seq_lens[b], max_len, window, sinks);
+        for (int b = lo; b < hi; ++b) s += streamed_len(seq_lens[b], max_len);
         part[tid] = s;
         __syncthreads();
         constexpr int NPL = NTHR / 32;  // partial sums per lane
@@ -198,7 +197,7 @@ __global__ void __launch_bounds__(NTHR, NTHR == 128 ? 10 : 1) decode_prologue_ke
             const int32_t L = seq_lens[b];
             bad |= (L < 1 || L > max_len);
             ws.off[b] = run;
-            run += streamed_len(L, max_len, window, sinks);
+            run += streamed_len(L, max_len);
         }
         if (bad) status_or(status, LRKV_STATUS_BAD_SEQLEN);
         return;
@@ -432,8 +431,7 @@ __global__ void __launch_bounds__(kGenTile) decode_split_generic_kernel(
     const TC *__restrict__ R_K, const TC *__restrict__ R_V, const int32_t *__restrict__ page_table,
     const int32_t *__restrict__ req_row, int max_pages, int num_pages, int page_size, int B, int H, int d_h, int r,
     float scale_log2, float4 sc, DecodeWs ws, int32_t *status, const T *__restrict__ B_K, RopeArgs rope,
-    const T *__restrict__ N_K, int s_stride, int hpg, const int32_t *__restrict__ seq_lens, int window,
-    int sinks) {
+    const T *__restrict__ N_K, int s_stride, int hpg) {
     // s_stride: elements of a token's shared row (G d_h); hpg: heads per shared group
     extern __shared__ float sm[];
     float *qs = sm;                 // d_h
@@ -468,9 +466,7 @@ __global__ void __launch_bounds__(kGenTile) decode_split_generic_kernel(
         const int32_t base = ws.off[b];
         const int32_t seg_end = min(end, ws.off[b + 1]);
         const int t_a = start - base, t_b = seg_end - base;
-        const int32_t q_pos = ws.off[b + 1] - base - 1;  // rotary (no window): the query's position
-        // the request's streamed rows are its visible ones, in order
-        const VisibleRows vis(seq_lens[b], window, sinks);
+        const int32_t q_pos = ws.off[b + 1] - base - 1;  // rotary: the query's position
         // rotary: a query past the end of the cos/sin table is not attended
         // (zero output, flagged) rather than read out of bounds
         const bool rope_ok = RP == 0 || q_pos < rope.max_pos;
@@ -530,13 +526,12 @@ __global__ void __launch_bounds__(kGenTile) decode_split_generic_kernel(
             float s = -INFINITY;
             int32_t prow = -1;
             if (valid) {
-                const int32_t jr = vis.row(j);
-                int32_t page = pt[jr / page_size];
+                int32_t page = pt[j / page_size];
                 if (page < 0 || page >= num_pages) {
                     status_or(status, LRKV_STATUS_BAD_PAGE);
                     valid = false;
                 } else {
-                    prow = page * page_size + jr % page_size;
+                    prow = page * page_size + j % page_size;
                     const TC *sk = S_K + (size_t)prow * s_stride;
                     const TC *rk = R_K + ((size_t)prow * H + h) * r;
                     float acc = 0.f;
@@ -827,7 +822,7 @@ cudaError_t launch_prologue(const DecodeArgs &a, const DecodeWs &ws, int G, int 
                       static_cast<const T *>(a.q), static_cast<const T *>(a.B_K), a.seq_lens,
                       static_cast<T *>(a.out), a.B, a.cache.H, a.cache.d_h, a.cache.r,
                       max_len, G, tile_align, staged, ws, a.status,
-                      reinterpret_cast<const float2 *>(a.rope), a.rope_ws, a.early, a.window, a.sinks);
+                      reinterpret_cast<const float2 *>(a.rope), a.rope_ws, a.early);
 }
 
 template <typename T, typename TC, int RP>
@@ -851,8 +846,7 @@ static cudaError_t launch_split_generic_t(const DecodeArgs &a, const DecodeWs &w
                       static_cast<const TC *>(c.R_K), static_cast<const TC *>(c.R_V), a.page_table,
                       a.req_row, a.max_pages, c.num_pages, c.page_size, a.B, c.H, c.d_h, c.r,
                       scale_log2, sc, ws, a.status, static_cast<const T *>(a.B_K), rope,
-                      static_cast<const T *>(c.N_K), cache_groups(c) * c.d_h, c.H / cache_groups(c),
-                      a.seq_lens, a.window, a.sinks);
+                      static_cast<const T *>(c.N_K), cache_groups(c) * c.d_h, c.H / cache_groups(c));
 }
 
 template <typename T, typename TC>

@@ -76,12 +76,9 @@ struct VisibleRows {
 };
 
 // Rows the split kernels stream for a request of length L: none for an
-// invalid length, else the visible ones (all L without a window).
-__host__ __device__ __forceinline__ int32_t streamed_len(int32_t L, int max_len, int window = 0,
-                                                         int sinks = 0) {
-    if (L < 1 || L > max_len) return 0;
-    const VisibleRows v(L, window, sinks);
-    return L - v.first + v.sinks;
+// invalid length, else L.
+__host__ __device__ __forceinline__ int32_t streamed_len(int32_t L, int max_len) {
+    return (L < 1 || L > max_len) ? 0 : L;
 }
 
 // beside_split: the tensor-core split kernel follows (smaller prologue blocks).
@@ -103,6 +100,8 @@ int fast_decode_grid(int H, int r);
 // Windowed decode of the shapes fast_decode_supported covers (a.window > 0), with
 // ws_bytes of scratch for the states of split requests.
 cudaError_t launch_window_fast(const DecodeArgs &a, void *ws, size_t ws_bytes);
+// The same for every other shape.
+cudaError_t launch_window_any(const DecodeArgs &a);
 size_t window_state_bytes(int B, int H, int r, int max_seq_len, int window, int sinks, int dtype);
 cudaError_t launch_split_fast(const DecodeArgs &a, const DecodeWs &ws, int G);
 

@@ -1092,7 +1092,7 @@ struct WinPlan {
 // 12 ns per KB of bf16 rows, 34 ns per KB of 8-bit codes (0.67 us and 1.0 us for
 // 16 heads, r = 48); a segment costs a cluster fixed[] us besides (private
 // queries, start of the ring, the states' way to their owners; measured for
-// segments of a few tiles), a combine 5 us, and nothing is faster than the copy
+// segments of a few tiles), a combine 8 us with its launch, and nothing is faster than the copy
 // bandwidth.  Measured at 16 heads, r = 48, against this rule's choice:
 //   16 requests, window 1024:  CL 1, 2, 4, 8 in 58.5, 33.9, 22.1, 31.0 us (eight
 //     CTAs a cluster: 15 clusters fit the GPU at once, so one request waits)
@@ -1116,7 +1116,7 @@ static WinPlan window_plan(int B, int64_t rows, double tile_bytes, bool q8, int 
             const int64_t per_cta = ((tiles + S - 1) / S + CL - 1) / CL;
             const double work = rounds * (per_cta * tile_us + fixed[i]);
             // (where the memory's rate decides, the layout with the fewest segments)
-            const double t = std::max(work, hbm_us) + 0.3 * rounds * fixed[i] + (S > 1 ? 5. : 0.);
+            const double t = std::max(work, hbm_us) + 0.3 * rounds * fixed[i] + (S > 1 ? 8. : 0.);
             if (t < least) {
                 least = t;
                 best = {CL, (int)used, (int)S};

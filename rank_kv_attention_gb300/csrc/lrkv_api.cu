@@ -137,20 +137,22 @@ static int window_bound(int max_seq_len, int window, int sinks) {
 
 static int run_decode(const DecodeArgs &a, void *workspace, size_t ws_bytes) {
     const auto &c = a.cache;
-    DecodeGeom geo = decode_geom(a.B, a.window ? window_bound(a.max_seq_len, a.window, a.sinks) : a.max_seq_len);
-    DecodeWs ws = decode_ws_layout(workspace, a.B, c.H, c.d_h, c.r, geo.G_ws);
-    if (ws_bytes < ws.bytes) return LRKV_E_WORKSPACE;
-    const bool rope_fast = a.rope_ws.wt != nullptr;
-    const bool fast = rope_fast || (!a.rope && !a.window && fast_decode_supported(c.H, c.d_h, c.r, c.page_size, c.dtype,
-                                                                                  cache_groups(c)));
-    const int G = fast ? geo.G_fast : geo.G_gen;
-    cudaError_t e;
-    if (a.window && fast_decode_supported(c.H, c.d_h, c.r, c.page_size, c.dtype, cache_groups(c))) {
+    if (a.window) {
         prof_before(LRKV_PROFILE_ATTENTION, a.stream);
-        e = launch_window_fast(a, workspace, ws_bytes);
+        const cudaError_t e = fast_decode_supported(c.H, c.d_h, c.r, c.page_size, c.dtype, cache_groups(c))
+                                  ? launch_window_fast(a, workspace, ws_bytes)
+                                  : launch_window_any(a);
         prof_after(LRKV_PROFILE_ATTENTION, a.stream);
         return e == cudaSuccess ? LRKV_OK : cuda_fail(e);
     }
+    DecodeGeom geo = decode_geom(a.B, a.max_seq_len);
+    DecodeWs ws = decode_ws_layout(workspace, a.B, c.H, c.d_h, c.r, geo.G_ws);
+    if (ws_bytes < ws.bytes) return LRKV_E_WORKSPACE;
+    const bool rope_fast = a.rope_ws.wt != nullptr;
+    const bool fast = rope_fast || (!a.rope && fast_decode_supported(c.H, c.d_h, c.r, c.page_size, c.dtype,
+                                                                      cache_groups(c)));
+    const int G = fast ? geo.G_fast : geo.G_gen;
+    cudaError_t e;
     if (c.dtype != LRKV_F32) {  // bf16 activations (bf16 or 8-bit cache)
         e = launch_prologue<__nv_bfloat16>(a, ws, G, kPlanTileAlign, fast);
         if (e == cudaSuccess && rope_fast) {
@@ -798,19 +800,12 @@ int lrkv_prefill(const void *X, const void *Q, const int32_t *cu_rows, const int
 // ---------------------------------------------------------------------------
 // Sliding window with sinks, and the page plan of such a cache
 // ---------------------------------------------------------------------------
-// The generic kernels' workspace, or the states of requests that the tensor-core
-// kernel splits over clusters.
-static size_t decode_window_ws_bytes(int B, int H, int d_h, int r, int max_seq_len, int window, int sinks,
-                                     int dtype) {
-    const size_t states = d_h == 128 ? window_state_bytes(B, H, r, max_seq_len, window, sinks, dtype) : 0;
-    return std::max(decode_ws_bytes(B, H, d_h, r, window_bound(max_seq_len, window, sinks)), align256(states));
-}
-
 size_t lrkv_decode_window_workspace_bytes(int32_t B, int32_t H, int32_t d_h, int32_t r,
                                           int32_t max_seq_len, int32_t window, int32_t sinks,
                                           int32_t dtype) {
     if (check_dims(H, d_h, r, dtype) || B < 1 || max_seq_len < 1 || window < 1 || sinks < 0) return 0;
-    return decode_window_ws_bytes(B, H, d_h, r, max_seq_len, window, sinks, dtype);
+    // only the states of requests that the tensor-core kernel splits over clusters
+    return d_h == 128 ? align256(window_state_bytes(B, H, r, max_seq_len, window, sinks, dtype)) : 0;
 }
 
 int lrkv_decode_window(const void *q, const lrkv_cache_t *cache, const void *B_K, const void *B_V,
@@ -830,7 +825,7 @@ int lrkv_decode_window(const void *q, const lrkv_cache_t *cache, const void *B_K
     if (!q || !B_K || !B_V || !seq_lens || !page_table || !out) return LRKV_E_INVALID_ARG;
     if (!aligned16(q) || !aligned16(B_K) || !aligned16(B_V) || !aligned16(out))
         return LRKV_E_INVALID_ARG;
-    if (!workspace || !aligned256(workspace)) return LRKV_E_WORKSPACE;
+    if (!aligned256(workspace)) return LRKV_E_WORKSPACE;
     DecodeArgs a;
     a.q = q;
     a.cache = *cache;
@@ -847,9 +842,11 @@ int lrkv_decode_window(const void *q, const lrkv_cache_t *cache, const void *B_K
     a.out = out;
     a.status = dev_status;
     a.stream = (cudaStream_t)stream;
-    if (workspace_bytes < decode_window_ws_bytes(B, cache->H, cache->d_h, cache->r, max_seq_len, window, sinks,
-                                                 cache->dtype))
-        return LRKV_E_WORKSPACE;
+    const size_t need = fast_decode_supported(cache->H, cache->d_h, cache->r, cache->page_size, cache->dtype,
+                                              cache_groups(*cache))
+                            ? window_state_bytes(B, cache->H, cache->r, max_seq_len, window, sinks, cache->dtype)
+                            : 0;
+    if (need && (!workspace || workspace_bytes < need)) return LRKV_E_WORKSPACE;
     return run_decode(a, workspace, workspace_bytes);
 }
 
@@ -886,8 +883,6 @@ int lrkv_page_plan(const int32_t *seq_lens, const int32_t *new_rows, int32_t B, 
     for (const void *i : ins)
         for (const void *o : outs)
             if (i == o) return LRKV_E_INVALID_ARG;  // read by every block while outputs are written
-    if (max_rows > 0 && (!aligned16(positions) || !aligned16(seq_ids) || !aligned16(slots)))
-        return LRKV_E_INVALID_ARG;
     PagePlanArgs a;
     a.seq_lens = seq_lens;
     a.new_rows = new_rows;

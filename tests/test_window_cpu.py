@@ -85,18 +85,14 @@ def test_decode_window_refusals(lib):
     assert call(_cache(S_K=None)) == _abi.LRKV_E_INVALID_ARG
     assert lib.lrkv_decode_window(16, None, 16, 16, 16, 16, 2, 4, 100, 64, 4, 16, WS, 1 << 30, None, None) \
         == _abi.LRKV_E_INVALID_ARG
-    assert call(ws=None) == _abi.LRKV_E_WORKSPACE
-    assert call(ws=ctypes.c_void_p(16)) == _abi.LRKV_E_WORKSPACE
-    small = _cache(H=4)  # a shape of the generic kernels: always some workspace
-    assert call(small, wsb=16) == _abi.LRKV_E_WORKSPACE
+    # a workspace is checked for its alignment even where none is needed
+    assert call(_cache(H=4), ws=ctypes.c_void_p(16)) == _abi.LRKV_E_WORKSPACE
 
 
 def test_decode_window_workspace(lib):
     f = lib.lrkv_decode_window_workspace_bytes
-    assert f(4, 6, 32, 8, 4096, 1024, 4, 0) > 0
-    # bounded by the window, not by the history
-    assert f(4, 6, 32, 8, 1 << 20, 1024, 4, 0) == f(4, 6, 32, 8, 1 << 22, 1024, 4, 0)
-    assert f(4, 6, 32, 8, 1 << 20, 2 ** 31 - 1, 2 ** 31 - 1, 0) > 0
+    assert f(4, 6, 32, 8, 4096, 1024, 4, 0) == 0          # one launch, no scratch
+    assert f(4, 6, 32, 8, 1 << 20, 2 ** 31 - 1, 2 ** 31 - 1, 0) == 0
     for bad in ((0, 6, 32, 8, 64, 64, 0, 0), (4, 6, 32, 8, 0, 64, 0, 0), (4, 6, 32, 8, 64, 0, 0, 0),
                 (4, 6, 32, 8, 64, 64, -1, 0), (4, 6, 33, 8, 64, 64, 0, 0), (4, 6, 32, 8, 64, 64, 0, 9)):
         assert f(*bad) == 0, bad
@@ -135,8 +131,6 @@ def test_page_plan_refusals(lib):
                                   a["no"], None, None)
     for name in names + ("pos", "ids", "slots"):
         assert call(**{name: None}) == _abi.LRKV_E_INVALID_ARG, name
-    for name in ("pos", "ids", "slots"):
-        assert call(**{name: 8}) == _abi.LRKV_E_INVALID_ARG, name
     for over in (dict(B=0), dict(mp=0), dict(num=0), dict(rows=-1), dict(win=-1), dict(snk=-1), dict(ps=0), dict(ps=24),
                  dict(ps=2048), dict(mp=1 << 28), dict(num=1 << 28), dict(rows=2 ** 31 - 1)):
         assert call(**over) == _abi.LRKV_E_SHAPE, over

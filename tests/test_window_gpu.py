@@ -150,7 +150,7 @@ def test_decode_stale_workspace_repeats_bit_for_bit():
         H, d_h, r, dtype = shape
         case = decode_case(lens, H, d_h, r, dtype, seed=8)
         d = DevDecode(case)
-        ws = L.workspace(L.decode_window_workspace_bytes(len(lens), H, d_h, r, d.max_seq_len, window, 4, d.cache.dtype))
+        ws = L.workspace(L.decode_window_workspace_bytes(len(lens), H, d_h, r, d.max_seq_len, window, 4, d.cache.dtype) + 256)
         outs = []
         for fill in (0xFF, 0x7F, 0x00):
             ws.fill_(fill)
