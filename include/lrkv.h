@@ -415,7 +415,9 @@ LRKV_API int lrkv_key_norms(const int32_t *positions, const int32_t *seq_ids, in
  *
  * lrkv_prefill_window takes the arguments of lrkv_prefill and its workspace
  * (lrkv_prefill_workspace_bytes); rows 0 .. start_pos[b]-1 that a new row can
- * see must be in the cache.
+ * see must be in the cache.  Rows that some new row of a request sees must hold
+ * finite values: the tiled kernel gives a row of a tile that another row of it
+ * does not see the weight 0, and 0 times an infinity or NaN is NaN.
  */
 LRKV_API size_t lrkv_decode_window_workspace_bytes(int32_t B, int32_t H, int32_t d_h, int32_t r,
                                                    int32_t max_seq_len, int32_t window,

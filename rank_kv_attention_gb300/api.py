@@ -532,9 +532,17 @@ def page_plan(seq_lens, new_rows, page_table, free_pages, n_free, page_size, max
         raise ValueError("max_rows must not be negative")
     if free_out is None:
         free_out = _own_buffer((num_pages,), _i32, seq_lens.device, stream)
-    _fits(((seq_lens, "seq_lens", _i32, (B,)), (new_rows, "new_rows", _i32, (B,)),
-           (page_table, "page_table", _i32, (B, max_pages)), (free_pages, "free_pages", _i32, (num_pages,)),
-           (n_free, "n_free", _i32, (1,)), (free_out, "free_out", _i32, (num_pages,))), dev)
+    if not (isinstance(new_rows, _Tensor) and isinstance(n_free, _Tensor) and isinstance(free_out, _Tensor)
+            and seq_lens.dtype is _i32 and new_rows.dtype is _i32 and page_table.dtype is _i32
+            and free_pages.dtype is _i32 and n_free.dtype is _i32 and free_out.dtype is _i32
+            and new_rows.shape == (B,) and page_table.shape[0] == B and n_free.shape == (1,)
+            and free_out.shape == (num_pages,) and seq_lens.get_device() == dev and new_rows.get_device() == dev
+            and page_table.get_device() == dev and free_pages.get_device() == dev and n_free.get_device() == dev
+            and free_out.get_device() == dev and seq_lens.is_contiguous() and new_rows.is_contiguous()
+            and page_table.is_contiguous() and free_pages.is_contiguous() and free_out.is_contiguous()):
+        _refuse(((seq_lens, "seq_lens", _i32, (B,)), (new_rows, "new_rows", _i32, (B,)),
+                 (page_table, "page_table", _i32, (B, max_pages)), (free_pages, "free_pages", _i32, (num_pages,)),
+                 (n_free, "n_free", _i32, (1,)), (free_out, "free_out", _i32, (num_pages,))), dev)
     # one buffer for the small outputs
     sizes = (max_rows, max_rows, max_rows, B, B + 1, 1)
     parts = _own_buffer((3 * max_rows + 2 * B + 2,), _i32, seq_lens.device, stream)

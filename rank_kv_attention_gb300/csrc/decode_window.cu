@@ -32,7 +32,6 @@
 // clusters whose states a combine kernel merges.
 #include <algorithm>
 #include <mutex>
-#include <vector>
 
 #include "decode_tile.cuh"
 #include "tc_pair.cuh"
@@ -1061,12 +1060,13 @@ static int active_clusters(const void *kern, int smem, int nthreads, int CL, cud
         int dev, CL, n;
     };
     static std::mutex mu;
-    static std::vector<Key> known;
+    static Key known[512];  // (past these the query is simply made each time)
+    static int count = 0;
     int dev = 0;
     if ((*err = cudaGetDevice(&dev)) != cudaSuccess) return 0;
     std::lock_guard<std::mutex> lock(mu);
-    for (const Key &k : known)
-        if (k.kern == kern && k.dev == dev && k.CL == CL) return k.n;
+    for (int i = 0; i < count; ++i)
+        if (known[i].kern == kern && known[i].dev == dev && known[i].CL == CL) return known[i].n;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(CL);
     cfg.blockDim = dim3(nthreads);
@@ -1079,7 +1079,7 @@ static int active_clusters(const void *kern, int smem, int nthreads, int CL, cud
     cfg.numAttrs = 1;
     int n = 0;
     if ((*err = cudaOccupancyMaxActiveClusters(&n, kern, &cfg)) != cudaSuccess) return 0;
-    known.push_back({kern, dev, CL, n});
+    if (count < 512) known[count++] = {kern, dev, CL, n};
     return n;
 }
 

@@ -67,7 +67,10 @@ cudaError_t smem_limit_once(const void *kern, int bytes) {
     for (const Key &k : done)
         if (k.kern == kern && k.dev == dev && k.bytes == bytes) return cudaSuccess;
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e == cudaSuccess) done.push_back({kern, dev, bytes});
+    if (e == cudaSuccess) try {
+            done.push_back({kern, dev, bytes});
+        } catch (...) {  // (no memory to remember it: the attribute is set again next time)
+        }
     return e;
 }
 

@@ -15,7 +15,7 @@
 // the step's own attention, which still sees some of them, runs before any
 // later step can hand them out.
 //
-// One launch.  Each block scans all requests itself (two block scans over
+// One launch.  Each block scans all requests itself (two passes of block scans over
 // tiles of kTile requests: the lengths are a few kilobytes in L2) and writes
 // its share of every tile's rows, table entries and released ids, so nothing
 // waits on another block and nothing is kept between launches.  What bounds it:
@@ -32,6 +32,7 @@ namespace {
 constexpr int kNT = 512;            // threads per block
 constexpr int kPer = 4;             // requests per thread and tile
 constexpr int kTile = kNT * kPer;
+constexpr int kRun = 4;             // rows per lane and search
 
 // What the step does to one request.
 struct Step {
@@ -51,36 +52,49 @@ struct Geometry {
     }
 };
 
-// Exclusive block scan of four values per thread; total in *sum.
-template <typename V>
-__device__ __forceinline__ void block_scan(V (&v)[kPer], V *part, V &sum) {
+// Exclusive block scans of N sequences of kPer values per thread; totals in sum.
+template <typename V, int N>
+__device__ __forceinline__ void block_scan(V (&v)[N][kPer], V (&part)[N][kNT / 32], V (&sum)[N]) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    V run = 0;
+    V incl[N], run[N];
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) {
-        const V x = v[k];
-        v[k] = run;
-        run += x;
-    }
-    V incl = run;
+    for (int n = 0; n < N; ++n) {
+        run[n] = 0;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const V y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
+        for (int k = 0; k < kPer; ++k) {
+            const V x = v[n][k];
+            v[n][k] = run[n];
+            run[n] += x;
+        }
+        incl[n] = run[n];
     }
-    if (lane == 31) part[warp] = incl;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            const V y = __shfl_up_sync(0xffffffffu, incl[n], o);
+            if (lane >= o) incl[n] += y;
+        }
+    if (lane == 31)
+#pragma unroll
+        for (int n = 0; n < N; ++n) part[n][warp] = incl[n];
     __syncthreads();
-    V base = incl - run, all = 0;
 #pragma unroll
-    for (int w = 0; w < kNT / 32; ++w) {
-        const V x = part[w];
-        if (w < warp) base += x;
-        all += x;
+    for (int n = 0; n < N; ++n) {
+        // every warp scans the warps' totals itself
+        V t = lane < kNT / 32 ? part[n][lane] : 0;
+#pragma unroll
+        for (int o = 1; o < kNT / 32; o <<= 1) {
+            const V y = __shfl_up_sync(0xffffffffu, t, o);
+            if (lane >= o) t += y;
+        }
+        sum[n] = __shfl_sync(0xffffffffu, t, kNT / 32 - 1);
+        const V before = __shfl_sync(0xffffffffu, t, warp ? warp - 1 : 0);
+        const V base = incl[n] - run[n] + (warp ? before : 0);
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) v[n][k] += base;
     }
     __syncthreads();  // part is reused by the next scan
-#pragma unroll
-    for (int k = 0; k < kPer; ++k) v[k] += base;
-    sum = all;
 }
 
 // First entry of the nondecreasing off[0 .. n] (off[0] <= x < off[n]) whose
@@ -96,8 +110,8 @@ __device__ __forceinline__ int find(const int32_t *off, int n, int32_t x) {
 }
 
 struct Shared {
-    int64_t part64[kNT / 32];
-    int32_t part32[kNT / 32];
+    int64_t part64[2][kNT / 32];
+    int32_t part32[3][kNT / 32];
     // of the current tile, exclusive, with the tile's total at the end
     int32_t rows[kTile + 1], need[kTile + 1], rel[kTile + 1];
     int32_t len[kTile], lo[kTile], front[kTile];
@@ -134,7 +148,7 @@ __global__ void __launch_bounds__(kNT) page_plan_kernel(const PagePlanArgs a) {
         for (int t0 = 0; t0 < a.B; t0 += kTile) {
             const int nb = min(kTile, a.B - t0);
             Step st[kPer];
-            int64_t want[kPer], need[kPer];
+            int64_t asked[2][kPer], asked_all[2];  // rows, pages
 #pragma unroll
             for (int k = 0; k < kPer; ++k) {
                 const int i = tid * kPer + k;
@@ -149,18 +163,16 @@ __global__ void __launch_bounds__(kNT) page_plan_kernel(const PagePlanArgs a) {
                     s.rows = s.bad || n < 0 ? 0 : n;
                     s.need = s.rows ? geo.pages(s.L + s.rows) - geo.pages(s.L) : 0;
                 }
-                want[k] = s.rows;
-                need[k] = s.need;
+                asked[0][k] = s.rows;
+                asked[1][k] = s.need;
             }
-            int64_t want_all, need_all;
-            block_scan(want, sm.part64, want_all);
-            block_scan(need, sm.part64, need_all);
-            int32_t rows[kPer], alloc[kPer], rel[kPer];
+            block_scan(asked, sm.part64, asked_all);
+            int32_t got[3][kPer], got_all[3];  // rows, pages, released
 #pragma unroll
             for (int k = 0; k < kPer; ++k) {
                 Step &s = st[k];
-                const bool fits = want0 + want[k] + s.rows <= a.max_rows &&
-                                  (s.need == 0 || need0 + need[k] + s.need <= n_free);
+                const bool fits = want0 + asked[0][k] + s.rows <= a.max_rows &&
+                                  (s.need == 0 || need0 + asked[1][k] + s.need <= n_free);
                 s.refused = !fits && s.rows > 0;
                 if (s.refused) s.rows = s.need = 0;
                 s.front = 0;
@@ -174,36 +186,34 @@ __global__ void __launch_bounds__(kNT) page_plan_kernel(const PagePlanArgs a) {
                     s.lo = geo.dead(s.L);
                     s.hi = geo.dead(s.L + s.rows);
                 }
-                rows[k] = s.rows;
-                alloc[k] = s.need;
-                rel[k] = s.released();
+                got[0][k] = s.rows;
+                got[1][k] = s.need;
+                got[2][k] = s.released();
             }
-            int32_t rows_all, alloc_all, rel_all;
-            block_scan(alloc, sm.part32, alloc_all);
+            block_scan(got, sm.part32, got_all);
+            const int32_t rows_all = got_all[0], alloc_all = got_all[1], rel_all = got_all[2];
+            want0 += asked_all[0];
+            need0 += asked_all[1];
             if (pass == 0) {
                 taken += alloc_all;
-                want0 += want_all;
-                need0 += need_all;
                 continue;
             }
             if (ntile == 1) taken = alloc_all;
-            block_scan(rows, sm.part32, rows_all);
-            block_scan(rel, sm.part32, rel_all);
             const int32_t left = n_free - taken;
 #pragma unroll
             for (int k = 0; k < kPer; ++k) {
                 const int i = tid * kPer + k;
                 if (i < nb) {
                     const Step &s = st[k];
-                    sm.rows[i] = rows[k];
-                    sm.need[i] = alloc[k];
-                    sm.rel[i] = rel[k];
+                    sm.rows[i] = got[0][k];
+                    sm.need[i] = got[1][k];
+                    sm.rel[i] = got[2][k];
                     sm.len[i] = s.L;
                     sm.lo[i] = s.lo;
                     sm.front[i] = s.front;
                     if (g == 0) {
                         a.seq_lens_out[t0 + i] = s.ends ? 0 : s.L + s.rows;
-                        a.cu_rows[t0 + i] = rows0 + rows[k];
+                        a.cu_rows[t0 + i] = rows0 + got[0][k];
                         if (s.bad) flags |= LRKV_STATUS_BAD_SEQLEN;
                         if (s.refused) flags |= LRKV_STATUS_NO_PAGES;
                     }
@@ -238,18 +248,30 @@ __global__ void __launch_bounds__(kNT) page_plan_kernel(const PagePlanArgs a) {
                 if (id < 0 || at >= a.num_pages) flags |= LRKV_STATUS_BAD_PAGE;
                 if (at < a.num_pages) a.free_out[at] = id;
             }
-            for (int x = g * kNT + tid; x < rows_all; x += G * kNT) {
-                const int i = find(sm.rows, nb, x);
-                const int32_t pos = sm.len[i] + x - sm.rows[i];
-                const int32_t p = pos / geo.ps;
-                const int32_t id = page_of(i, p);
-                if (id < 0) flags |= LRKV_STATUS_BAD_PAGE;
-                a.positions[rows0 + x] = pos;
-                a.seq_ids[rows0 + x] = t0 + i;
-                a.slots[rows0 + x] = id < 0 ? -1 : id * geo.ps + (pos - p * geo.ps);
+            // rows: a warp takes kRun x 32 consecutive ones, a search for the first
+            // of each lane and steps from there, all page ids in flight at once
+            for (int x0 = (g * (kNT / 32) + (tid >> 5)) * 32 * kRun; x0 < rows_all; x0 += G * kNT * kRun) {
+                int i = find(sm.rows, nb, min(x0 + (tid & 31), rows_all - 1));
+                int req[kRun], pos[kRun], id[kRun];
+#pragma unroll
+                for (int k = 0; k < kRun; ++k) {
+                    const int x = min(x0 + 32 * k + (tid & 31), rows_all - 1);
+                    while (sm.rows[i + 1] <= x) ++i;
+                    req[k] = i;
+                    pos[k] = sm.len[i] + x - sm.rows[i];
+                    id[k] = page_of(i, pos[k] / geo.ps);
+                }
+#pragma unroll
+                for (int k = 0; k < kRun; ++k) {
+                    const int x = x0 + 32 * k + (tid & 31);
+                    if (x < rows_all) {
+                        if (id[k] < 0) flags |= LRKV_STATUS_BAD_PAGE;
+                        a.positions[rows0 + x] = pos[k];
+                        a.seq_ids[rows0 + x] = t0 + req[k];
+                        a.slots[rows0 + x] = id[k] < 0 ? -1 : id[k] * geo.ps + pos[k] % geo.ps;
+                    }
+                }
             }
-            want0 += want_all;
-            need0 += need_all;
             rows0 += rows_all;
             alloc0 += alloc_all;
             rel0 += rel_all;

@@ -515,3 +515,53 @@ def test_serving_run_with_a_bounded_pool():
         spare = free[0].tolist()[:int(n_free.item())]
         assert sorted(live + spare) == list(range(num)), f"step {k}: a page is lost or held twice"
     assert max(len(x) for x in kept) > 70
+
+
+def test_serving_step_in_a_graph():
+    """Plan, append and decode of single tokens captured once and replayed, against the same calls made one by one."""
+    import rank_kv_attention_gb300 as L
+    from rank_kv_attention_gb300.api import PagedCache
+    H, d_h, r, d, ps, window, sinks, B = 16, 128, 48, 64, 16, 48, 4, 5
+    num, gen = B * 8 + 6, torch.Generator(device="cuda").manual_seed(3)
+    w = I.make_weights(d, H, d_h, r, "bf16", seed=2)
+    W4 = [dev(a, "bf16") for a in (w.W_S_K, w.W_S_V, w.U_K, w.U_V)]
+    bases = [dev(w.B_K, "bf16"), dev(w.B_V, "bf16")]
+    steps, ends = 70, {20: 1, 41: 3, 42: 0}
+
+    def start():
+        return dict(lens=torch.zeros(B, dtype=torch.int32, device="cuda"), new=torch.ones(B, dtype=torch.int32, device="cuda"),
+                    table=torch.full((B, 64), -1, dtype=torch.int32, device="cuda"), free=torch.arange(num, dtype=torch.int32, device="cuda"),
+                    out_free=torch.empty(num, dtype=torch.int32, device="cuda"), n=torch.tensor([num], dtype=torch.int32, device="cuda"),
+                    X=torch.empty(B, d, dtype=torch.bfloat16, device="cuda"), q=torch.empty(B, H, d_h, dtype=torch.bfloat16, device="cuda"),
+                    cache=PagedCache(*[dev(p, "bf16") for p in I.empty_pools(num, ps, H, d_h, r, "bf16")]))
+
+    def step(s):
+        p = L.page_plan(s["lens"], s["new"], s["table"], s["free"], s["n"], ps, B, free_out=s["out_free"], window=window, sinks=sinks)
+        L.append(s["X"], p.positions, p.seq_ids, *W4, s["cache"], s["table"])
+        out = L.decode_window(s["q"], s["cache"], *bases, p.seq_lens, s["table"], 1024, window, sinks)
+        s["lens"].copy_(p.seq_lens)
+        s["n"].copy_(p.n_free)
+        s["free"].copy_(s["out_free"])
+        return out
+
+    a, b = start(), start()
+    step(a)                                             # (a step before the capture; undone)
+    a = start()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        captured = step(a)
+    a.update({k: a[k] for k in a})
+    for k in ("lens", "new", "table", "free", "n"):
+        a[k].copy_(start()[k])
+    for k in range(steps):
+        x, q = (torch.randn(t.shape, device="cuda", generator=gen).to(torch.bfloat16) for t in (a["X"], a["q"]))
+        for s in (a, b):
+            s["X"].copy_(x), s["q"].copy_(q), s["new"].fill_(1)
+            if k in ends:
+                s["new"][ends[k]] = -1
+        g.replay()
+        want = step(b)
+        live = b["new"] > 0
+        assert torch.equal(captured[live], want[live]), k
+        assert torch.equal(a["lens"], b["lens"]) and torch.equal(a["table"], b["table"]) and torch.equal(a["n"], b["n"]), k
+    assert int(b["lens"].max()) == steps
