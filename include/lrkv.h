@@ -468,6 +468,8 @@ LRKV_API int lrkv_prefill_window(const void *X, const void *Q, const int32_t *cu
  *   positions, seq_ids, slots [max_rows].
  * All on the device; no output may overlap an input (keep two free lists and
  * two length arrays and swap them).
+ * B * max_pages, max_pages * page_size, num_pages * page_size and max_rows are
+ * below 2^30 (LRKV_E_SHAPE beyond).
  *
  * A request does not grow, keeps its length and flags LRKV_STATUS_NO_PAGES
  * when the rows asked for by the requests up to and including it exceed

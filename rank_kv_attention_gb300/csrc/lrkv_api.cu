@@ -876,13 +876,13 @@ int lrkv_page_plan(const int32_t *seq_lens, const int32_t *new_rows, int32_t B, 
         return LRKV_E_SHAPE;
     if (page_size < 16 || page_size > 1024 || page_size % 16) return LRKV_E_SHAPE;
     if ((int64_t)max_pages * page_size > INT32_MAX / 2 || (int64_t)num_pages * page_size > INT32_MAX / 2 ||
-        max_rows > INT32_MAX / 2)
-        return LRKV_E_SHAPE;
+        (int64_t)B * max_pages > INT32_MAX / 2 || max_rows > INT32_MAX / 2)
+        return LRKV_E_SHAPE;  // (all counts of pages and rows stay within 32 bits, whatever the lengths hold)
     if (!seq_lens || !new_rows || !page_table || !free_pages || !n_free || !seq_lens_out || !cu_rows ||
         !free_out || !n_free_out || (max_rows > 0 && (!positions || !seq_ids || !slots)))
         return LRKV_E_INVALID_ARG;
     const void *ins[] = {seq_lens, new_rows, free_pages, n_free};
-    const void *outs[] = {seq_lens_out, cu_rows, free_out, n_free_out};
+    const void *outs[] = {seq_lens_out, cu_rows, free_out, n_free_out, page_table, positions, seq_ids, slots};
     for (const void *i : ins)
         for (const void *o : outs)
             if (i == o) return LRKV_E_INVALID_ARG;  // read by every block while outputs are written

@@ -139,6 +139,19 @@ def test_page_plan_refusals(lib):
             assert call(**{o: good[i]}) == _abi.LRKV_E_INVALID_ARG, (i, o)
 
 
+def test_page_plan_refuses_tables_past_32_bit_counts(lib):
+    """B * max_pages bounds the pages that a step can release; every array on its own lies in range."""
+    p = [1024 * (i + 1) for i in range(12)]
+
+    def call(B, max_pages, out=p[5]):
+        return lib.lrkv_page_plan(p[0], p[1], B, max_pages, 16, 10, 100, 4, 8, p[2], p[3], p[4], p[6], p[7], out, p[8],
+                                  p[9], p[10], p[11], None, None)
+    assert call(1 << 12, 1 << 18) == _abi.LRKV_E_SHAPE
+    assert call(2 ** 31 - 1, 1) == _abi.LRKV_E_SHAPE
+    for i in range(2):
+        assert call(2, 4, out=p[i]) == _abi.LRKV_E_INVALID_ARG  # positions on top of an input
+
+
 def test_binding_refuses_host_tensors_and_wrong_shapes():
     import torch
 

@@ -143,6 +143,19 @@ def test_decode_huge_scores_and_infinities_in_unseen_rows():
     check(got, *decode_reference(case, 64, 3))
 
 
+@pytest.mark.parametrize("H,d_h,r,dtype", [(16, 128, 48, "bf16"), (16, 128, 48, "fp8"), (4, 16, 4, "f32"), (8, 64, 24, "bf16")])
+@pytest.mark.parametrize("row", [0, 3, 201, 230, 299])
+def test_decode_nan_in_a_visible_row_is_not_hidden(H, d_h, r, dtype, row):
+    """A NaN key of a row that a query sees makes that request's outputs NaN, and no other's."""
+    canary = {"bf16": I.BF16_NAN_BITS, "fp8": I.FP8_NAN_CODE}.get(dtype, I.F32_NAN_CANARY)
+    case = decode_case([300, 300, 8], H, d_h, r, dtype, seed=31)
+    clean = host(run_decode(DevDecode(case), 99, 4), case.act_dtype)
+    case.S_K[case.page_table[1, row // 64], row % 64] = canary
+    got = host(run_decode(DevDecode(case), 99, 4), case.act_dtype)
+    assert np.isnan(got[1]).all()
+    np.testing.assert_array_equal(got[[0, 2]], clean[[0, 2]])
+
+
 def test_decode_stale_workspace_repeats_bit_for_bit():
     import rank_kv_attention_gb300 as L
     for lens, window, shape in (([700, 5, 2500], 600, (16, 128, 48, "bf16")), ([9000], 8000, (16, 128, 48, "bf16")),
