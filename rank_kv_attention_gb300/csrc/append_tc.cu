@@ -52,10 +52,11 @@ struct TcMaps {
 };
 
 // The output's 128-column blocks: block k lies in segment seg[k] from its
-// column col[k]; tile j pairs blocks 2j and 2j + 1 (the last may be alone).
+// column col[k]; tile j takes blocks 2j and 2j + 1 (the last may be alone), or
+// block j alone (per = 1).
 constexpr int TC_MAX_BLOCKS = 32;
 struct TcBlocks {
-    int nblocks, ncoltiles, nrowtiles, npairs;  // npairs: (row-tile pair, column tile) items
+    int nblocks, per, ncoltiles, nrowtiles, npairs;  // npairs: (row-tile pair, column tile) items
     int seg[TC_MAX_BLOCKS];
     int col[TC_MAX_BLOCKS];
     int width[4];
@@ -67,8 +68,8 @@ struct TcBlocks {
 __device__ __forceinline__ void tc_tile_of(const TcBlocks &t, int pt, int rank, int &m0, int &b0, int &nb) {
     const int rp = pt / t.ncoltiles, ct = pt % t.ncoltiles;
     m0 = (2 * rp + rank) * TC_BM;
-    b0 = 2 * ct;
-    nb = min(2, t.nblocks - b0);
+    b0 = t.per * ct;
+    nb = min(t.per, t.nblocks - b0);
 }
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TC_THREADS, 1)
@@ -313,9 +314,14 @@ static bool tc_blocks(const AppendArgsT<__nv_bfloat16> &a, TcBlocks &t) {
             ++t.nblocks;
         }
     }
-    t.ncoltiles = (t.nblocks + 1) / 2;
     t.nrowtiles = (a.n + TC_BM - 1) / TC_BM;
-    t.npairs = t.ncoltiles * ((t.nrowtiles + 1) / 2);
+    const int rowpairs = (t.nrowtiles + 1) / 2;
+    // One block a tile while all of them run at once: each of twice as many SMs
+    // then does half the products and half the stores.  Otherwise two, which
+    // need half the copies per product.
+    t.per = 2 * t.nblocks * rowpairs <= device_sm_count() ? 1 : 2;
+    t.ncoltiles = (t.nblocks + t.per - 1) / t.per;
+    t.npairs = t.ncoltiles * rowpairs;
     return true;
 }
 
