@@ -415,7 +415,9 @@ LRKV_API int lrkv_key_norms(const int32_t *positions, const int32_t *seq_ids, in
  *
  * lrkv_prefill_window takes the arguments of lrkv_prefill and its workspace
  * (lrkv_prefill_workspace_bytes); rows 0 .. start_pos[b]-1 that a new row can
- * see must be in the cache.  Rows that some new row of a request sees must hold
+ * see must be in the cache before the call (a history that another request of
+ * the call appends does not count: its tiles may be read beside the append).
+ * Rows that some new row of a request sees must hold
  * finite values: the tiled kernel gives a row of a tile that another row of it
  * does not see the weight 0, and 0 times an infinity or NaN is NaN.
  */

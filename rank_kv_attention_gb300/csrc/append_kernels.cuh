@@ -15,6 +15,11 @@ struct AppendArgsT {
     // [1, step_max_len] skips the row and flags it)
     const int32_t *step_lens = nullptr;
     int step_max_len = 0;
+    // prefill: the predecessor in the stream is the same call's
+    // prefill_rows_kernel, which writes positions and seq_ids only and let this
+    // kernel launch after passing its own wait; the tensor-core kernel reads X
+    // and the weights without waiting for it
+    bool after_rows = false;
     int n, d;
     const T *W_S_K, *W_S_V, *U_K, *U_V;
     T *S_K, *S_V, *R_K, *R_V;
@@ -67,6 +72,8 @@ cudaError_t launch_append_rows_mma(const AppendArgsT<__nv_bfloat16> &a);
 
 // Tensor-core append (bf16): covered shapes and launcher.
 bool tc_append_supported(int n, int d, int d_h, int H, int r);
+// Whether its CTAs, one per SM, leave SMs of the device idle.
+bool tc_append_leaves_sms(int n, int d_h, int H, int r);
 cudaError_t launch_append_tc(const AppendArgsT<__nv_bfloat16> &a);
 int device_sm_count();  // SMs of the current device (lrkv_api.cu)
 
@@ -98,6 +105,10 @@ struct PrefillTcArgs {
     int32_t *status;
     cudaStream_t stream;
     int window = 0, sinks = 0;  // lrkv_prefill_window; window 0: the whole history
+    // The predecessor in the stream is the same call's append, which let this
+    // kernel launch after passing its own wait and finishes within a few
+    // milliseconds: only the copies of tiles that hold new rows wait for it.
+    bool early = false;
 };
 int launch_prefill_tc(const PrefillTcArgs &p);
 // Whether lrkv_prefill runs the tensor-core attention kernel for this cache.

@@ -84,8 +84,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TC_THREADS, 1)
     uint64_t *acc_empty = acc_full + 2;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + TC_OFF_TMEM);
 
-    pdl_wait();
-    pdl_launch_dependents();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int nk = a.d / TC_BK;
     const int rank = (int)cluster_ctarank();
@@ -111,6 +109,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TC_THREADS, 1)
     cluster_sync_all();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    // (after_rows: the epilogue's warps wait, before they look up their rows)
+    if (!a.after_rows || warp >= 2) pdl_wait();
+    pdl_launch_dependents();
     bool ok = true;
     int issued = 0;  // producer: k-steps whose copies were requested
 
@@ -301,9 +302,8 @@ static bool tc_map(CUtensorMap *m, const void *base, int64_t rows, int d) {
 }
 
 // The 128-column blocks of the output: per segment ceil(width / 128).
-static bool tc_blocks(const AppendArgsT<__nv_bfloat16> &a, TcBlocks &t) {
-    const int Hr = a.H * a.r;
-    const int widths[4] = {a.d_h, a.d_h, Hr, Hr};
+static bool tc_blocks(int n, int d_h, int Hr, TcBlocks &t) {
+    const int widths[4] = {d_h, d_h, Hr, Hr};
     t.nblocks = 0;
     for (int k = 0; k < 4; ++k) {
         t.width[k] = widths[k];
@@ -314,7 +314,7 @@ static bool tc_blocks(const AppendArgsT<__nv_bfloat16> &a, TcBlocks &t) {
             ++t.nblocks;
         }
     }
-    t.nrowtiles = (a.n + TC_BM - 1) / TC_BM;
+    t.nrowtiles = (n + TC_BM - 1) / TC_BM;
     const int rowpairs = (t.nrowtiles + 1) / 2;
     // One block a tile while all of them run at once: each of twice as many SMs
     // then does half the products and half the stores.  Otherwise two, which
@@ -332,6 +332,11 @@ bool tc_append_supported(int n, int d, int d_h, int H, int r) {
            tc_encode() != nullptr;
 }
 
+bool tc_append_leaves_sms(int n, int d_h, int H, int r) {
+    TcBlocks t;
+    return tc_blocks(n, d_h, H * r, t) && 2 * t.npairs < device_sm_count();
+}
+
 cudaError_t launch_append_tc(const AppendArgsT<__nv_bfloat16> &a) {
     TcMaps maps;
     const int Hr = a.H * a.r;
@@ -340,7 +345,7 @@ cudaError_t launch_append_tc(const AppendArgsT<__nv_bfloat16> &a) {
         !tc_map(&maps.w[3], a.U_V, Hr, a.d))
         return cudaErrorInvalidValue;
     TcBlocks t;
-    if (!tc_blocks(a, t)) return cudaErrorInvalidValue;
+    if (!tc_blocks(a.n, a.d_h, Hr, t)) return cudaErrorInvalidValue;
     cudaError_t e = smem_limit_once(append_tc_kernel, TC_SMEM);
     if (e != cudaSuccess) return e;
     const int grid = 2 * std::min(t.npairs, device_sm_count() / 2);

@@ -247,9 +247,12 @@ static int run_append(const void *X, const int32_t *positions, const int32_t *se
                       int d, const void *W_S_K, const void *W_S_V, const void *U_K,
                       const void *U_V, const lrkv_cache_t *c, const int32_t *page_table, int B,
                       int max_pages, int32_t *status, cudaStream_t s,
-                      const int32_t *step_lens = nullptr) {
+                      const int32_t *step_lens = nullptr, bool *light = nullptr) {
     // step_lens: row i is request i's row at position step_lens[i] - 1
-    // (positions and seq_ids unused)
+    // (positions and seq_ids unused).  light: the predecessor is the prefill's
+    // row kernel; set to whether the append takes a few rows only, or a part of
+    // the SMs for one wave
+    if (light) *light = false;
     if (n == 0) return LRKV_OK;
     cudaError_t e;
     prof_before(LRKV_PROFILE_PROJECTION, s);
@@ -258,9 +261,13 @@ static int run_append(const void *X, const int32_t *positions, const int32_t *se
                                                  U_V, c, page_table, B, max_pages, status, s);
         a.step_lens = step_lens;
         a.step_max_len = max_pages * c->page_size;
-        if (rows_mma_append_fits(a)) e = launch_append_rows_mma(a);
-        else if (rows_append_fits(a)) e = launch_append_rows(a);
-        else if (tc_append_supported(n, d, c->d_h, c->H, c->r)) e = launch_append_tc(a);
+        a.after_rows = light != nullptr;
+        const bool mma = rows_mma_append_fits(a), few = mma || rows_append_fits(a);
+        const bool tc = !few && tc_append_supported(n, d, c->d_h, c->H, c->r);
+        if (light) *light = few || (tc && tc_append_leaves_sms(n, c->d_h, c->H, c->r));
+        if (mma) e = launch_append_rows_mma(a);
+        else if (few) e = launch_append_rows(a);
+        else if (tc) e = launch_append_tc(a);
         else e = launch_append_generic(a);
     } else {
         auto a = make_append_args<float>(X, positions, seq_ids, n, d, W_S_K, W_S_V, U_K, U_V, c,
@@ -734,8 +741,9 @@ static int prefill_impl(const void *X, const void *Q, const int32_t *cu_rows,
     cudaError_t e = launch_prefill_rows(cu_rows, start_pos, B, n, max_pages * cache->page_size,
                                         w.pos, w.sid, w.vlen, w.req_row, dev_status, s);
     if (e != cudaSuccess) return cuda_fail(e);
+    bool light = false;
     st = run_append(X, w.pos, w.sid, n, d, W_S_K, W_S_V, U_K, U_V, cache, page_table, B, max_pages,
-                    dev_status, s);
+                    dev_status, s, nullptr, &light);
     if (st) return st;
     if (cache->N_K) {
         e = launch_key_norms(w.pos, w.sid, n, B_K, *cache, page_table, B, max_pages, dev_status, s);
@@ -760,6 +768,7 @@ static int prefill_impl(const void *X, const void *Q, const int32_t *cu_rows,
         p.stream = s;
         p.window = window;
         p.sinks = sinks;
+        p.early = light && window;
         prof_before(LRKV_PROFILE_ATTENTION, s);
         const int rc = launch_prefill_tc(p);
         if (rc == 0) prof_after(LRKV_PROFILE_ATTENTION, s);
