@@ -28,23 +28,25 @@
 //   [256, 384), [384, 512)  two fp32 score buffers; the softmax overwrites the
 //               first 64 columns of a buffer with the bf16 probabilities that
 //               the value MMA reads as its A operand
-// p = q B_K[h] is computed into the first score buffer before the loop and
-// the B_V[h] expansion into it after the loop.
+// p = q B_K[h] is computed into the second score buffer before the loop and
+// the B_V[h] expansion into the first after the loop.
 //
 // Issue order: scores of key tile k+1, then values of tile k (after its
 // softmax), so the tensor core computes the next scores while the softmax of
 // the current tile runs.  tcgen05.mma runs in issue order, so the scores of
 // tile k+2 (issued after the values of tile k) never overwrite probabilities
 // still being read.  Softmax keeps a lazy running maximum (O is rescaled in
-// tensor memory only when the maximum grows by more than 2^8).  Keys past
-// every row of the CTA have their value rows cleared in shared memory, so
-// whatever the cache holds there cannot reach the output.
+// tensor memory only when the maximum grows by more than 2^8).  Groups of 16
+// keys past every row of the CTA are left out of the value products, and of a
+// group that straddles that end the value rows past it are cleared in shared
+// memory, so whatever the cache holds there cannot reach the output.
 //
 // WIN: row i sees j <= t_i with j > t_i - window or j < sinks.  The CTA's key
 // tiles are then those of the sinks and those from the window of its first
 // row on (`KeyTiles`); the tiles between are not visited, the scores of a
 // visited tile are masked per row where a window starts or the sinks end, and
-// value rows that no row of the CTA sees are cleared like those past the end.
+// keys that no row of the CTA sees are treated like those past the end (clearing
+// the rows of whole groups too took 4000 of a CTA's 37,000 cycles).
 //
 // `early` (WIN, when the append before it leaves SMs idle): a CTA starts beside
 // the call's append and works through the tiles that lie in the history; the
@@ -128,6 +130,18 @@ struct KeyTiles {
         return WIN && key0 + PF_HALF <= lo && key0 >= a.sinks;
     }
 };
+// Keys of the tile at position kb that no row of the CTA sees: [w0, w1), between
+// the sinks and the first row's window, and those from z on, past every row.
+template <bool WIN>
+struct UnseenKeys {
+    int w0, w1, z;
+    __device__ __forceinline__ UnseenKeys(const PfArgs &a, const KeyTiles<WIN> &keys, int kb, int max_p)
+        : w0(WIN ? max(a.sinks - kb, 0) : 0), w1(WIN ? min(keys.lo - kb, PF_BN) : 0), z(min(max_p + 1 - kb, PF_BN)) {}
+    // none of the 16 keys from j on is seen: their products are left out
+    __device__ __forceinline__ bool all16(int j) const { return j >= z || (j >= w0 && j + 16 <= w1); }
+    // unseen keys among 16 that are not left out: their value rows are cleared
+    __device__ __forceinline__ bool any() const { return (z & 15) || (w0 < w1 && ((w0 | w1) & 15)); }
+};
 
 // 2^x on the special-function unit (PTX ex2.approx.ftz: ~2 ulp; -inf -> +0).
 __device__ __forceinline__ float ex2_approx(float x) {
@@ -159,6 +173,13 @@ __device__ __forceinline__ float max3f(float a, float b, float c) {
     float r;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
+}
+
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(p));
+    return p != 0;
 }
 
 // x -> (hi, lo) with hi = bf16(x), lo = bf16(x - hi), packed in pairs.
@@ -333,7 +354,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
             if (bv_issued) mbar_wait(&bar.bv_full, 0);
         }
     } else if (warp == 9) {
-        if (lane == 0) {
+        if (elect_one()) {
             // ================= MMA issuer =================
             constexpr uint32_t id_s = tc_idesc_bf16(PF_BM, PF_BN);
             constexpr uint32_t id_pv = tc_idesc_bf16_bmn(PF_BM, NPV);
@@ -343,16 +364,20 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
             const uint32_t q0 = sw128_desc_lo(base + PF_OFF_Q, 16);
             const uint32_t q1 = sw128_desc_lo(base + PF_OFF_Q + PF_BM * 128, 16);
             const uint32_t pq = tmem + PF_COL_PQ;
-            // scores of key tile kt into buffer kt & 1
-            auto scores = [&](int kt) {
+            // scores of key tile kt into buffer kt & 1: the shared branch, then the
+            // private one
+            auto shared_scores = [&](int kt) {
                 const uint32_t kb = base + PF_OFF_K + (kt & 1) * PF_STAGE;
                 const uint32_t k0 = sw128_desc_lo(kb, 16), k1 = sw128_desc_lo(kb + PF_BLK, 16);
-                const uint32_t kr = sw128_desc_lo(kb + 2 * PF_BLK, 16);
                 const uint32_t d = tmem + PF_COL_S + 128 * (kt & 1);
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk) tc_mma_lo(d, q0 + 2 * kk, k0 + 2 * kk, id_s, kk != 0);
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk) tc_mma_lo(d, q1 + 2 * kk, k1 + 2 * kk, id_s, 1);
+            };
+            auto private_scores = [&](int kt) {
+                const uint32_t kr = sw128_desc_lo(base + PF_OFF_K + (kt & 1) * PF_STAGE + 2 * PF_BLK, 16);
+                const uint32_t d = tmem + PF_COL_S + 128 * (kt & 1);
 #pragma unroll
                 for (int kk = 0; kk < R16; ++kk) {  // p_hi . R_K[h] + p_lo . R_K[h]
                     tc_mma_ts_lo(d, pq + 8 * kk, kr + 2 * kk, id_s, 1);
@@ -366,14 +391,20 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
                 const uint32_t bk = sw128_desc_lo(base + PF_OFF_V + PF_STAGE, PF_BLK);
 #pragma unroll
                 for (int kk = 0; kk < 8; ++kk)
-                    tc_mma_lo(tmem + PF_COL_S, (kk < 4 ? q0 : q1) + 2 * (kk & 3), bk + 128 * kk, id_pre,
+                    tc_mma_lo(tmem + PF_COL_S + 128, (kk < 4 ? q0 : q1) + 2 * (kk & 3), bk + 128 * kk, id_pre,
                               kk != 0);
                 tc_commit(&bar.pre_done);
-                ok = mbar_wait(&bar.qa_ready, 0) && mbar_wait(&bar.k_full[0], 0);
+                ok = mbar_wait(&bar.k_full[0], 0);
+            }
+            if (ok) {
+                // (while p is brought into its halves)
+                tc_fence_after();
+                shared_scores(0);
+                ok = mbar_wait(&bar.qa_ready, 0);
             }
             if (ok) {
                 tc_fence_after();
-                scores(0);
+                private_scores(0);
                 tc_commit(&bar.s_full[0]);
             }
             for (int kt = 0; kt < nkt && ok; ++kt) {
@@ -385,7 +416,8 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
                         break;
                     }
                     tc_fence_after();
-                    scores(kt + 1);
+                    shared_scores(kt + 1);
+                    private_scores(kt + 1);
                     tc_commit(&bar.s_full[s1]);
                 }
                 if (!mbar_wait(&bar.p_full[st], (kt >> 1) & 1) ||
@@ -396,9 +428,20 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
                 tc_fence_after();
                 const uint32_t vb = sw128_desc_lo(base + PF_OFF_V + st * PF_STAGE, PF_BLK);
                 const uint32_t pa = tmem + PF_COL_S + 128 * st;
+                const UnseenKeys<WIN> un(a, keys, keys.base(kt), max_p);
+                // 16 keys (8 packed columns) per instruction
+                if (un.z == PF_BN && un.w0 >= un.w1) {
 #pragma unroll
-                for (int kk = 0; kk < 8; ++kk)  // 16 keys (8 packed columns) per instruction
-                    tc_mma_ts_lo(tmem, pa + 8 * kk, vb + 128 * kk, id_pv, (kt | kk) != 0);
+                    for (int kk = 0; kk < 8; ++kk) tc_mma_ts_lo(tmem, pa + 8 * kk, vb + 128 * kk, id_pv, (kt | kk) != 0);
+                } else {
+                    bool begun = kt > 0;
+#pragma unroll 1
+                    for (int kk = 0; kk < 8; ++kk)
+                        if (!un.all16(16 * kk)) {
+                            tc_mma_ts_lo(tmem, pa + 8 * kk, vb + 128 * kk, id_pv, begun);
+                            begun = true;
+                        }
+                }
                 tc_commit(&bar.pv_done[st]);
             }
             // E = (O_R / l)_hi B_V[h]^T + (O_R / l)_lo B_V[h]^T into score buffer 0
@@ -441,14 +484,14 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
             // p -> bf16 halves in tensor memory: warp half 0 writes p_hi, half 1 p_lo
             tc_fence_after();
             uint32_t v[32], pk[32];
-            tmem_ld32(lane_base + PF_COL_S, v);
+            tmem_ld32(lane_base + PF_COL_S + 128, v);
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
                 uint32_t hi, lo;
                 split_pack(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]), hi, lo);
                 pk[j] = hf ? lo : hi;
             }
-            tmem_ld32(lane_base + PF_COL_S + 32, v);
+            tmem_ld32(lane_base + PF_COL_S + 128 + 32, v);
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
                 uint32_t hi, lo;
@@ -550,28 +593,27 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
                 }
             }
             tmem_st32(lane_base + PF_COL_S + 128 * st + 32 * hf, pk);  // probabilities over the scores
-            // keys of the tile that no row of the CTA sees, z0 <= key < z1: past
-            // every row, or (WIN, another tile or the same) between the sinks and
-            // the first row's window
-            const int kb = key0 - hf * PF_HALF;
-            const int z_end = max_p + 1 - kb;
-            const int w0 = WIN ? max(a.sinks - kb, 0) : 0, w1 = WIN ? min(keys.lo - kb, PF_BN) : 0;
-            if ((kt == nkt - 1 && z_end < PF_BN) || (WIN && w0 < w1)) {
-                // clear their value rows
+            const UnseenKeys<WIN> un(a, keys, key0 - hf * PF_HALF, max_p);
+            if (un.any()) {
+                // the value rows that no row of the CTA sees, of the 16-key groups
+                // that also hold seen ones
                 if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bar.v_full[st], (kt >> 1) & 1)))) break;
                 uint8_t *vb = smem + PF_OFF_V + st * PF_STAGE;
                 auto clear = [&](int z0, int z1) {
-                    // 3 blocks x (z1 - z0) rows x 8 16-byte units; key j of a block
+                    // (z1 - z0) rows x 3 blocks x 8 16-byte units; key j of a block
                     // sits in 64-row box j / 64, row j % 64
-                    const int units = (z1 - z0) * 8;
-                    for (int u = tid; u < 3 * units; u += 2 * PF_BM) {
-                        const int blk = u / units, w = u - blk * units, key = z0 + (w >> 3);
-                        *reinterpret_cast<uint4 *>(vb + blk * PF_BLK + (key >> 6) * PF_BOX +
+                    for (int u = tid; u < (z1 - z0) * 24; u += 2 * PF_BM) {
+                        const int key = z0 + u / 24, w = u % 24;
+                        *reinterpret_cast<uint4 *>(vb + (w >> 3) * PF_BLK + (key >> 6) * PF_BOX +
                                                    (key & 63) * 128 + (w & 7) * 16) = make_uint4(0, 0, 0, 0);
                     }
                 };
-                if (kt == nkt - 1 && z_end < PF_BN) clear(z_end, PF_BN);
-                if (WIN && w0 < w1) clear(w0, w1);
+                clear(un.z, (un.z + 15) & ~15);
+                if (WIN && un.w0 < un.w1) {
+                    const int e = min(un.w1, (un.w0 + 15) & ~15);
+                    clear(un.w0, e);
+                    clear(max(e, un.w1 & ~15), un.w1);
+                }
                 fence_proxy_async_smem();
             }
             tc_fence_before();
