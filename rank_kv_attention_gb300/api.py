@@ -490,10 +490,26 @@ def prefill_window(X, Q, cu_rows, start_pos, max_ctx, W_S_K, W_S_V, U_K, U_V, B_
     shape, base, shared, private = (n, H, d_h), (H, d_h, r), (max(1, desc.G) * d_h, d), (H, r, d)
     if out is None:
         out = _own_buffer(shape, dt, X.device, stream)
-    _fits(((X, "X", dt, (n, d)), (Q, "Q", dt, shape), (cu_rows, "cu_rows", _i32, (B + 1,)),
-           (start_pos, "start_pos", _i32, (B,)), (W_S_K, "W_S_K", dt, shared), (W_S_V, "W_S_V", dt, shared),
-           (U_K, "U_K", dt, private), (U_V, "U_V", dt, private), (B_K, "B_K", dt, base), (B_V, "B_V", dt, base),
-           (page_table, "page_table", _i32, (B, max_pages)), (out, "out", dt, shape)), dev)
+    T = _Tensor
+    if not (isinstance(Q, T) and isinstance(cu_rows, T) and isinstance(W_S_K, T) and isinstance(W_S_V, T)
+            and isinstance(U_K, T) and isinstance(U_V, T) and isinstance(B_K, T) and isinstance(B_V, T)
+            and isinstance(out, T) and X.dtype is dt and Q.dtype is dt and cu_rows.dtype is _i32
+            and start_pos.dtype is _i32 and W_S_K.dtype is dt and W_S_V.dtype is dt and U_K.dtype is dt
+            and U_V.dtype is dt and B_K.dtype is dt and B_V.dtype is dt and page_table.dtype is _i32 and out.dtype is dt
+            and Q.shape == shape and cu_rows.shape == (B + 1,) and W_S_K.shape == shared and W_S_V.shape == shared
+            and U_K.shape == private and U_V.shape == private and B_K.shape == base and B_V.shape == base
+            and page_table.shape[0] == B and out.shape == shape
+            and X.get_device() == dev and Q.get_device() == dev and cu_rows.get_device() == dev
+            and start_pos.get_device() == dev and W_S_K.get_device() == dev and W_S_V.get_device() == dev
+            and U_K.get_device() == dev and U_V.get_device() == dev and B_K.get_device() == dev
+            and B_V.get_device() == dev and page_table.get_device() == dev and out.get_device() == dev
+            and X.is_contiguous() and Q.is_contiguous() and cu_rows.is_contiguous() and start_pos.is_contiguous()
+            and W_S_K.is_contiguous() and W_S_V.is_contiguous() and U_K.is_contiguous() and U_V.is_contiguous()
+            and B_K.is_contiguous() and B_V.is_contiguous() and page_table.is_contiguous() and out.is_contiguous()):
+        _refuse(((X, "X", dt, (n, d)), (Q, "Q", dt, shape), (cu_rows, "cu_rows", _i32, (B + 1,)),
+                 (start_pos, "start_pos", _i32, (B,)), (W_S_K, "W_S_K", dt, shared), (W_S_V, "W_S_V", dt, shared),
+                 (U_K, "U_K", dt, private), (U_V, "U_V", dt, private), (B_K, "B_K", dt, base), (B_V, "B_V", dt, base),
+                 (page_table, "page_table", _i32, (B, max_pages)), (out, "out", dt, shape)), dev)
     L = _abi.lib()
     if ws is None:
         ws = _own_buffer((max(1, L.lrkv_prefill_workspace_bytes(B, n, H, d_h, r, max_ctx, desc.dtype)),), _u8, X.device,
@@ -555,7 +571,7 @@ def page_plan(seq_lens, new_rows, page_table, free_pages, n_free, page_size, max
         free_out.data_ptr(), cu + 4 * (B + 1), _status(status, dev), _raw_stream(stream, dev))
     if code:
         _abi.check("lrkv_page_plan", code)
-    pos, ids, slots, lens, cu_rows, left = parts.split_with_sizes(sizes)
+    pos, ids, slots, lens, cu_rows, left = parts.unsafe_split_with_sizes(sizes)  # (nothing here is differentiated)
     return PagePlan(lens, cu_rows, pos, ids, slots, free_out, left)
 
 

@@ -360,13 +360,7 @@ __global__ void prefill_rows_kernel(const int32_t *__restrict__ cu_rows,
     const int i = blockIdx.x * blockDim.x + threadIdx.x;
     if (i >= n) return;
     // request b with cu_rows[b] <= i < cu_rows[b+1]
-    int lo = 0, hi = B;  // search in [0, B)
-    while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (cu_rows[mid + 1] > i) hi = mid;
-        else lo = mid + 1;
-    }
-    const int b = lo;
+    const int b = request_of_row(cu_rows, B, i);
     bool ok = b < B && cu_rows[b] <= i && i < cu_rows[b + 1];
     int32_t p = ok ? start_pos[b] + (i - cu_rows[b]) : -1;
     if (ok && (p < 0 || p >= max_len)) ok = false;

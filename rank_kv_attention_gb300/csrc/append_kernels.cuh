@@ -15,11 +15,10 @@ struct AppendArgsT {
     // [1, step_max_len] skips the row and flags it)
     const int32_t *step_lens = nullptr;
     int step_max_len = 0;
-    // prefill: the predecessor in the stream is the same call's
-    // prefill_rows_kernel, which writes positions and seq_ids only and let this
-    // kernel launch after passing its own wait; the tensor-core kernel reads X
-    // and the weights without waiting for it
-    bool after_rows = false;
+    // prefill on tensor cores: when set, request b's rows are cu_rows[b] ..
+    // cu_rows[b + 1] - 1 and lie from position start_pos[b] on (positions and
+    // seq_ids unused; a row of no request is skipped and flagged)
+    const int32_t *cu_rows = nullptr, *start_pos = nullptr;
     int n, d;
     const T *W_S_K, *W_S_V, *U_K, *U_V;
     T *S_K, *S_V, *R_K, *R_V;
@@ -32,6 +31,17 @@ struct AppendArgsT {
     uint8_t *q8[4] = {nullptr, nullptr, nullptr, nullptr};  // S_K, S_V, R_K, R_V codes
     float inv_scale[4] = {1.f, 1.f, 1.f, 1.f};
 };
+
+// The first request b with cu_rows[b + 1] > row (B when there is none).
+__device__ __forceinline__ int request_of_row(const int32_t *cu_rows, int B, int row) {
+    int lo = 0, hi = B;
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (cu_rows[mid + 1] > row) hi = mid;
+        else lo = mid + 1;
+    }
+    return lo;
+}
 
 // Store value v of packed output column c (0 .. 2 d_h + 2 H r) for pool row
 // `row`: the four pools in order S_K, S_V, R_K, R_V.

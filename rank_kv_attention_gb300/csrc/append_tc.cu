@@ -109,8 +109,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TC_THREADS, 1)
     cluster_sync_all();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    // (after_rows: the epilogue's warps wait, before they look up their rows)
-    if (!a.after_rows || warp >= 2) pdl_wait();
+    pdl_wait();
     pdl_launch_dependents();
     bool ok = true;
     int issued = 0;  // producer: k-steps whose copies were requested
@@ -191,6 +190,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TC_THREADS, 1)
                         const int32_t L = a.step_lens[r];
                         b = r;
                         pos = (L < 1 || L > a.step_max_len) ? -1 : L - 1;
+                    } else if (a.cu_rows) {
+                        b = request_of_row(a.cu_rows, a.B, r);
+                        const int32_t c0 = b < a.B ? a.cu_rows[b] : r + 1;
+                        if (b == a.B || c0 > r) b = -1;
+                        pos = b < 0 ? -1 : a.start_pos[b] + (r - c0);
                     } else {
                         b = a.seq_ids[r];
                         pos = a.positions[r];

@@ -243,31 +243,50 @@ static int check_append(const void *X, const int32_t *positions, const int32_t *
     return LRKV_OK;
 }
 
+// A prefill's append: request b has rows cu_rows[b] .. cu_rows[b + 1] - 1, from
+// position start_pos[b] on.
+struct PrefillRows {
+    const int32_t *cu_rows, *start_pos;
+    int max_len;
+    int32_t *pos, *sid, *vlen, *req_row;  // of every row, from prefill_rows_kernel
+    // in: nothing but the append needs those arrays; out: nothing does, the
+    // append looked its rows up itself, and the arrays were not filled
+    bool in_append;
+    bool light;  // out: the append takes a few rows only, or a part of the SMs for one wave
+};
+
+static cudaError_t launch_rows(const PrefillRows &p, int B, int n, int32_t *status, cudaStream_t s) {
+    return launch_prefill_rows(p.cu_rows, p.start_pos, B, n, p.max_len, p.pos, p.sid, p.vlen, p.req_row, status, s);
+}
+
 static int run_append(const void *X, const int32_t *positions, const int32_t *seq_ids, int n,
                       int d, const void *W_S_K, const void *W_S_V, const void *U_K,
                       const void *U_V, const lrkv_cache_t *c, const int32_t *page_table, int B,
                       int max_pages, int32_t *status, cudaStream_t s,
-                      const int32_t *step_lens = nullptr, bool *light = nullptr) {
+                      const int32_t *step_lens = nullptr, PrefillRows *rows = nullptr) {
     // step_lens: row i is request i's row at position step_lens[i] - 1
-    // (positions and seq_ids unused).  light: the predecessor is the prefill's
-    // row kernel; set to whether the append takes a few rows only, or a part of
-    // the SMs for one wave
-    if (light) *light = false;
+    // (positions and seq_ids unused).  rows: a prefill's
     if (n == 0) return LRKV_OK;
     cudaError_t e;
+    if (rows) {
+        const bool tc = n > 64 && c->dtype != LRKV_F32 && tc_append_supported(n, d, c->d_h, c->H, c->r);
+        rows->in_append = rows->in_append && tc;
+        rows->light = n <= 64 || (tc && tc_append_leaves_sms(n, c->d_h, c->H, c->r));
+        if (!rows->in_append && (e = launch_rows(*rows, B, n, status, s)) != cudaSuccess) return cuda_fail(e);
+    }
     prof_before(LRKV_PROFILE_PROJECTION, s);
     if (c->dtype != LRKV_F32) {  // bf16 rows and weights (bf16 or 8-bit cache)
         auto a = make_append_args<__nv_bfloat16>(X, positions, seq_ids, n, d, W_S_K, W_S_V, U_K,
                                                  U_V, c, page_table, B, max_pages, status, s);
         a.step_lens = step_lens;
         a.step_max_len = max_pages * c->page_size;
-        a.after_rows = light != nullptr;
-        const bool mma = rows_mma_append_fits(a), few = mma || rows_append_fits(a);
-        const bool tc = !few && tc_append_supported(n, d, c->d_h, c->H, c->r);
-        if (light) *light = few || (tc && tc_append_leaves_sms(n, c->d_h, c->H, c->r));
-        if (mma) e = launch_append_rows_mma(a);
-        else if (few) e = launch_append_rows(a);
-        else if (tc) e = launch_append_tc(a);
+        if (rows && rows->in_append) {
+            a.cu_rows = rows->cu_rows;
+            a.start_pos = rows->start_pos;
+        }
+        if (rows_mma_append_fits(a)) e = launch_append_rows_mma(a);
+        else if (rows_append_fits(a)) e = launch_append_rows(a);
+        else if (tc_append_supported(n, d, c->d_h, c->H, c->r)) e = launch_append_tc(a);
         else e = launch_append_generic(a);
     } else {
         auto a = make_append_args<float>(X, positions, seq_ids, n, d, W_S_K, W_S_V, U_K, U_V, c,
@@ -738,15 +757,13 @@ static int prefill_impl(const void *X, const void *Q, const int32_t *cu_rows,
     PrefillWs w = prefill_ws_layout(workspace, n, cache->H, cache->d_h, cache->r, max_ctx);
     if (workspace_bytes < w.bytes) return LRKV_E_WORKSPACE;
     cudaStream_t s = (cudaStream_t)stream;
-    cudaError_t e = launch_prefill_rows(cu_rows, start_pos, B, n, max_pages * cache->page_size,
-                                        w.pos, w.sid, w.vlen, w.req_row, dev_status, s);
-    if (e != cudaSuccess) return cuda_fail(e);
-    bool light = false;
+    PrefillRows rows = {cu_rows, start_pos, max_pages * cache->page_size, w.pos, w.sid, w.vlen, w.req_row,
+                        window && !cache->N_K, false};
     st = run_append(X, w.pos, w.sid, n, d, W_S_K, W_S_V, U_K, U_V, cache, page_table, B, max_pages,
-                    dev_status, s, nullptr, &light);
+                    dev_status, s, nullptr, &rows);
     if (st) return st;
     if (cache->N_K) {
-        e = launch_key_norms(w.pos, w.sid, n, B_K, *cache, page_table, B, max_pages, dev_status, s);
+        cudaError_t e = launch_key_norms(w.pos, w.sid, n, B_K, *cache, page_table, B, max_pages, dev_status, s);
         if (e != cudaSuccess) return cuda_fail(e);
     }
     if (!rope && !cache->N_K) {
@@ -768,12 +785,16 @@ static int prefill_impl(const void *X, const void *Q, const int32_t *cu_rows,
         p.stream = s;
         p.window = window;
         p.sinks = sinks;
-        p.early = light && window;
+        p.early = rows.light && window;
         prof_before(LRKV_PROFILE_ATTENTION, s);
         const int rc = launch_prefill_tc(p);
         if (rc == 0) prof_after(LRKV_PROFILE_ATTENTION, s);
         if (rc < 0) return cuda_fail((cudaError_t)(-rc));
         if (rc == 0) return LRKV_OK;
+    }
+    if (rows.in_append) {
+        const cudaError_t e = launch_rows(rows, B, n, dev_status, s);
+        if (e != cudaSuccess) return cuda_fail(e);
     }
     // Other shapes: row i is a one-query decode over its request's rows
     // 0..pos_i, reading the page-table row of its request.
