@@ -1016,6 +1016,19 @@ __global__ void __launch_bounds__(128) window_combine_kernel(const __nv_bfloat16
     pdl_wait();
     pdl_launch_dependents();
     const size_t s0 = ((size_t)b * S) * H + h;  // state of split k: s0 + k H
+    // this thread's shared column and, of the first r, a private one, eight splits
+    // at a time; the first eight are on the way while the weights are formed
+    constexpr int N = 8;
+    float av[N], ap[N];
+    auto fetch = [&](int k0) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const float *a = acc + (s0 + (size_t)(k0 + i) * H) * W;
+            av[i] = k0 + i < S ? a[tid] : 0.f;
+            ap[i] = k0 + i < S && tid < r ? a[128 + tid] : 0.f;
+        }
+    };
+    fetch(0);
     if (tid < 32) {
         const float2 s = tid < S ? *reinterpret_cast<const float2 *>(ml + (s0 + (size_t)tid * H) * 2)
                                  : make_float2(-INFINITY, 0.f);
@@ -1028,14 +1041,15 @@ __global__ void __launch_bounds__(128) window_combine_kernel(const __nv_bfloat16
         for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
         wts[tid] = L > 0.f ? x / L : 0.f;
     }
-    // this thread's shared column and, of the first r, a private one
     float v = 0.f, p = 0.f;
     __syncthreads();
-#pragma unroll 4
-    for (int k = 0; k < S; ++k) {
-        const float *a = acc + (s0 + (size_t)k * H) * W;
-        v = fmaf(wts[k], a[tid], v);
-        if (tid < r) p = fmaf(wts[k], a[128 + tid], p);
+    for (int k0 = 0; k0 < S; k0 += N) {  // (weights past S are 0: kMaxSplits is a multiple of N)
+        if (k0) fetch(k0);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            v = fmaf(wts[k0 + i], av[i], v);
+            p = fmaf(wts[k0 + i], ap[i], p);
+        }
     }
     if (tid < 64) priv[tid] = tid < r ? p : 0.f;
     __syncthreads();

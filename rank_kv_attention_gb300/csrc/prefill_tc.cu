@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
     }
 
     // ---- tile geometry (identical in every thread)
-    const int r0 = a.cu_rows[b], r1 = min(a.cu_rows[b + 1], a.n);
+    const int r0 = a.cu_rows[b], r1 = min(a.cu_rows[b + 1], a.n), start = a.start_pos[b];
     const int i0 = r0 + tq * PF_BM;
     if (r0 < 0 || i0 >= r1) {
         if (WIN && a.early) pdl_wait();
@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
         if (tid == 0) status_or(a.status, LRKV_STATUS_BAD_SEQLEN);
     }
     const int nrows = min(PF_BM, r1 - i0);
-    const int p0 = a.start_pos[b] + (i0 - r0);                       // position of tile row 0
+    const int p0 = start + (i0 - r0);                       // position of tile row 0
     const int t_lo = max(0, -p0), t_hi = min(nrows, a.max_len - p0);  // rows with a valid position
     if (t_lo >= t_hi) {  // no row of this tile has a valid position: zero its outputs
         if (WIN && a.early) pdl_wait();
