@@ -368,6 +368,63 @@ def test_prefill_empty_requests_and_no_rows():
     assert o.shape == (0, 2, 128)
 
 
+@pytest.mark.parametrize("n", [20, 130, 300])
+def test_prefill_chunks_back_to_back(n):
+    """Chunks of two prompts enqueued without a pause (each one's history is what the one before appends), eagerly and
+    from a graph, give what the same chunks give one at a time."""
+    from rank_kv_attention_gb300.api import PagedCache
+    window, sinks, chunks, d = 150, 10, 5, 2048
+    rows, ends = [n, n - 7], [chunks * n, chunks * (n - 7)]
+    w, pt, cache, X, Q = prefill_inputs(ends, [0, 0], d, 16, 128, 48, "bf16", 10 ** 6, 0, seed=n)
+    ws = [dev(a, "bf16") for a in (w.W_S_K, w.W_S_V, w.U_K, w.U_V, w.B_K, w.B_V)]
+    Xd, Qd, table = dev(X, "bf16"), dev(Q, "bf16"), dev(pt, "i32")
+    cu = dev(np.cumsum([0] + rows), "i32")
+    take = [torch.cat([torch.arange(b * ends[0] + k * m, b * ends[0] + (k + 1) * m) for b, m in enumerate(rows)]).cuda()
+            for k in range(chunks)]
+    parts = [(Xd[i].contiguous(), Qd[i].contiguous(), dev(np.array([k * m for m in rows]), "i32")) for k, i in enumerate(take)]
+
+    def run(c, pause):
+        import rank_kv_attention_gb300 as L
+        outs = []
+        for x, q, start in parts:
+            outs.append(L.prefill_window(x, q, cu, start, max(ends), *ws, c, table, window, sinks))
+            if pause:
+                torch.cuda.synchronize()
+        return torch.cat(outs)
+
+    fresh = lambda: PagedCache(*[p.clone() for p in (cache.S_K, cache.S_V, cache.R_K, cache.R_V)])
+    want = run(fresh(), True)
+    assert torch.isfinite(want.float()).all()
+    for _ in range(5):
+        assert torch.equal(run(fresh(), False), want)
+    c, g = fresh(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = run(c, False)
+    for _ in range(3):
+        for p, q in zip((c.S_K, c.S_V, c.R_K, c.R_V), (cache.S_K, cache.S_V, cache.R_K, cache.R_V)):
+            p.copy_(q)
+        g.replay()
+        assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("n", [40, 100, 700])
+def test_prefill_rows_of_no_request_are_flagged(n):
+    """Rows past cu_rows[B] and rows past the page table are skipped and flagged, whichever append runs."""
+    import rank_kv_attention_gb300 as L
+    rows, starts = [n, n], [0, 64]
+    w, pt, cache, X, Q = prefill_inputs(rows, starts, 64, 2, 128, 16, "bf16", 50, 2, seed=n)
+    want = run_prefill(w, pt, cache, X, Q, rows, starts, 50, 2, "bf16")
+    call = lambda cu, start, status: L.prefill_window(
+        dev(X, "bf16"), dev(Q, "bf16"), dev(np.array(cu), "i32"), dev(np.array(start), "i32"), n + 64, dev(w.W_S_K, "bf16"),
+        dev(w.W_S_V, "bf16"), dev(w.U_K, "bf16"), dev(w.U_V, "bf16"), dev(w.B_K, "bf16"), dev(w.B_V, "bf16"), cache,
+        dev(pt, "i32"), 50, 2, status=status)
+    for cu, start in (((0, n, n + n // 2), (0, 64)), ((0, n, 2 * n), (0, pt.shape[1] * 64 - 5))):
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        got = call(cu, start, status)
+        assert int(status.item()) & L._abi.LRKV_STATUS_BAD_ROW
+        assert torch.equal(got[:n], want[:n])
+
+
 def test_prefill_bad_page_is_flagged():
     """A page that rows of the window lie on is missing: flagged, the rows that do not need it still match."""
     import rank_kv_attention_gb300 as L
