@@ -414,7 +414,9 @@ LRKV_API int lrkv_key_norms(const int32_t *positions, const int32_t *seq_ids, in
  * side (each with a workspace of its own).
  *
  * lrkv_prefill_window takes the arguments of lrkv_prefill and its workspace
- * (lrkv_prefill_workspace_bytes); rows 0 .. start_pos[b]-1 that a new row can
+ * (lrkv_prefill_workspace_bytes; a call of more than 64 rows that
+ * LRKV_PREFILL_TILED covers needs none in most shapes: with workspace NULL a call
+ * that does returns LRKV_E_WORKSPACE and has enqueued nothing); rows 0 .. start_pos[b]-1 that a new row can
  * see must be in the cache before the call (a history that another request of
  * the call appends does not count: its tiles may be read beside the append).
  * Rows that some new row of a request sees must hold

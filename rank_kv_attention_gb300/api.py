@@ -511,13 +511,15 @@ def prefill_window(X, Q, cu_rows, start_pos, max_ctx, W_S_K, W_S_V, U_K, U_V, B_
                  (U_K, "U_K", dt, private), (U_V, "U_V", dt, private), (B_K, "B_K", dt, base), (B_V, "B_V", dt, base),
                  (page_table, "page_table", _i32, (B, max_pages)), (out, "out", dt, shape)), dev)
     L = _abi.lib()
-    if ws is None:
-        ws = _own_buffer((max(1, L.lrkv_prefill_workspace_bytes(B, n, H, d_h, r, max_ctx, desc.dtype)),), _u8, X.device,
-                         stream)
-    code = L.lrkv_prefill_window(
-        X.data_ptr(), Q.data_ptr(), cu_rows.data_ptr(), start_pos.data_ptr(), B, n, max_ctx, d, W_S_K.data_ptr(),
-        W_S_V.data_ptr(), U_K.data_ptr(), U_V.data_ptr(), B_K.data_ptr(), B_V.data_ptr(), desc, page_table.data_ptr(),
-        max_pages, window, sinks, out.data_ptr(), *_workspace(ws, dev), _status(status, dev), _raw_stream(stream, dev))
+    args = (X.data_ptr(), Q.data_ptr(), cu_rows.data_ptr(), start_pos.data_ptr(), B, n, max_ctx, d, W_S_K.data_ptr(),
+            W_S_V.data_ptr(), U_K.data_ptr(), U_V.data_ptr(), B_K.data_ptr(), B_V.data_ptr(), desc,
+            page_table.data_ptr(), max_pages, window, sinks, out.data_ptr())
+    tail = _status(status, dev), _raw_stream(stream, dev)
+    code = L.lrkv_prefill_window(*args, *_workspace(ws, dev), *tail)
+    if code == _abi.LRKV_E_WORKSPACE and ws is None:  # (few rows, or the per-row path)
+        m = L.lrkv_prefill_workspace_bytes(B, n, H, d_h, r, max_ctx, desc.dtype)
+        ws = _own_buffer((m,), _u8, X.device, stream)
+        code = L.lrkv_prefill_window(*args, ws.data_ptr(), m, *tail)
     if code:
         _abi.check("lrkv_prefill_window", code)
     return out

@@ -121,6 +121,8 @@ struct PrefillTcArgs {
     bool early = false;
 };
 int launch_prefill_tc(const PrefillTcArgs &p);
+// Whether it covers this call.
+bool prefill_tc_fits(const PrefillTcArgs &p);
 // Whether lrkv_prefill runs the tensor-core attention kernel for this cache.
 bool prefill_tc_covers(const lrkv_cache_t &cache);
 

@@ -249,8 +249,8 @@ struct PrefillRows {
     const int32_t *cu_rows, *start_pos;
     int max_len;
     int32_t *pos, *sid, *vlen, *req_row;  // of every row, from prefill_rows_kernel
-    // in: nothing but the append needs those arrays; out: nothing does, the
-    // append looked its rows up itself, and the arrays were not filled
+    // the tensor-core append runs and looks its rows up itself: nothing needs
+    // those arrays, they are not filled
     bool in_append;
     bool light;  // out: the append takes a few rows only, or a part of the SMs for one wave
 };
@@ -270,7 +270,6 @@ static int run_append(const void *X, const int32_t *positions, const int32_t *se
     cudaError_t e;
     if (rows) {
         const bool tc = n > 64 && c->dtype != LRKV_F32 && tc_append_supported(n, d, c->d_h, c->H, c->r);
-        rows->in_append = rows->in_append && tc;
         rows->light = n <= 64 || (tc && tc_append_leaves_sms(n, c->d_h, c->H, c->r));
         if (!rows->in_append && (e = launch_rows(*rows, B, n, status, s)) != cudaSuccess) return cuda_fail(e);
     }
@@ -753,12 +752,33 @@ static int prefill_impl(const void *X, const void *Q, const int32_t *cu_rows,
     if (!Q || !B_K || !B_V || !out || !aligned16(Q) || !aligned16(B_K) || !aligned16(B_V) ||
         !aligned16(out))
         return LRKV_E_INVALID_ARG;
-    if (!workspace || !aligned256(workspace)) return LRKV_E_WORKSPACE;
-    PrefillWs w = prefill_ws_layout(workspace, n, cache->H, cache->d_h, cache->r, max_ctx);
-    if (workspace_bytes < w.bytes) return LRKV_E_WORKSPACE;
     cudaStream_t s = (cudaStream_t)stream;
+    // Causal attention on tensor cores (query tiles of 128 rows per head).
+    PrefillTcArgs p;
+    p.Q = Q;
+    p.cu_rows = cu_rows;
+    p.start_pos = start_pos;
+    p.B = B;
+    p.n = n;
+    p.max_ctx = max_ctx;
+    p.B_K = B_K;
+    p.B_V = B_V;
+    p.cache = *cache;
+    p.page_table = page_table;
+    p.max_pages = max_pages;
+    p.out = out;
+    p.status = dev_status;
+    p.stream = s;
+    p.window = window;
+    p.sinks = sinks;
+    // a windowed call that runs it after the tensor-core append needs no workspace
+    const bool bare = window && n > 64 && cache->dtype != LRKV_F32 &&
+                      tc_append_supported(n, d, cache->d_h, cache->H, cache->r) && prefill_tc_fits(p);
+    if (!aligned256(workspace) || (!workspace && !bare)) return LRKV_E_WORKSPACE;
+    PrefillWs w = prefill_ws_layout(workspace, n, cache->H, cache->d_h, cache->r, max_ctx);
+    if (!bare && workspace_bytes < w.bytes) return LRKV_E_WORKSPACE;
     PrefillRows rows = {cu_rows, start_pos, max_pages * cache->page_size, w.pos, w.sid, w.vlen, w.req_row,
-                        window && !cache->N_K, false};
+                        bare, false};
     st = run_append(X, w.pos, w.sid, n, d, W_S_K, W_S_V, U_K, U_V, cache, page_table, B, max_pages,
                     dev_status, s, nullptr, &rows);
     if (st) return st;
@@ -767,24 +787,6 @@ static int prefill_impl(const void *X, const void *Q, const int32_t *cu_rows,
         if (e != cudaSuccess) return cuda_fail(e);
     }
     if (!rope && !cache->N_K) {
-        // Causal attention on tensor cores (query tiles of 128 rows per head).
-        PrefillTcArgs p;
-        p.Q = Q;
-        p.cu_rows = cu_rows;
-        p.start_pos = start_pos;
-        p.B = B;
-        p.n = n;
-        p.max_ctx = max_ctx;
-        p.B_K = B_K;
-        p.B_V = B_V;
-        p.cache = *cache;
-        p.page_table = page_table;
-        p.max_pages = max_pages;
-        p.out = out;
-        p.status = dev_status;
-        p.stream = s;
-        p.window = window;
-        p.sinks = sinks;
         p.early = rows.light && window;
         prof_before(LRKV_PROFILE_ATTENTION, s);
         const int rc = launch_prefill_tc(p);
@@ -792,10 +794,7 @@ static int prefill_impl(const void *X, const void *Q, const int32_t *cu_rows,
         if (rc < 0) return cuda_fail((cudaError_t)(-rc));
         if (rc == 0) return LRKV_OK;
     }
-    if (rows.in_append) {
-        const cudaError_t e = launch_rows(rows, B, n, dev_status, s);
-        if (e != cudaSuccess) return cuda_fail(e);
-    }
+    if (bare) return cuda_fail(cudaErrorInvalidValue);  // (not reached: the attention fits)
     // Other shapes: row i is a one-query decode over its request's rows
     // 0..pos_i, reading the page-table row of its request.
     DecodeArgs a;

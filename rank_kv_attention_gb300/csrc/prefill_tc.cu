@@ -767,6 +767,12 @@ bool prefill_tc_covers(const lrkv_cache_t &cache) {
     return prefill_tc_plan(p, maps, nq);
 }
 
+bool prefill_tc_fits(const PrefillTcArgs &p) {
+    PfMaps maps;
+    int nq = 0;
+    return prefill_tc_plan(p, maps, nq);
+}
+
 int launch_prefill_tc(const PrefillTcArgs &p) {
     const lrkv_cache_t &c = p.cache;
     PfMaps maps;
