@@ -322,7 +322,8 @@ static bool tc_blocks(int n, int d_h, int Hr, TcBlocks &t) {
     const int rowpairs = (t.nrowtiles + 1) / 2;
     // One block a tile while all of them run at once: each of twice as many SMs
     // then does half the products and half the stores.  Otherwise two, which
-    // need half the copies per product.
+    // need half the copies of X per product.  A prefill call of 512 rows of
+    // d = 2048, its attention behind it: 39.2 us with one, 42.2 with two.
     t.per = 2 * t.nblocks * rowpairs <= device_sm_count() ? 1 : 2;
     t.ncoltiles = (t.nblocks + t.per - 1) / t.per;
     t.npairs = t.ncoltiles * rowpairs;

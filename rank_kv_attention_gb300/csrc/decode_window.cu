@@ -30,6 +30,14 @@
 // kernel is the whole decode, in one launch.  Only for few requests with long
 // windows, which whole requests would put on few SMs, a request is split over S
 // clusters whose states a combine kernel merges.
+//
+// In a graph, 16 heads, r = 48, bf16 unless noted: 1 request, window 512, 11.1 us
+// and 16 requests, window 1024, 22 us (59 MB): latency, of which 8 to 9 us are a
+// launch's and a segment's fixed cost and 0.67 us a tile (57 KB) per CTA; 64 ragged
+// requests, window 4000, r = 56: 132 us, 6.2 TB/s, 92% of the measured copy bandwidth,
+// DRAM reads 1.004 of the visible rows; 32 requests, window 2048, 8-bit: 46 us, where
+// the conversions of codes bound a tile (1.0 us for 28 KB); 4 requests of 32 heads,
+// r = 32, window 8192, split: 34 us, 4.5 TB/s.
 #include <algorithm>
 #include <mutex>
 
