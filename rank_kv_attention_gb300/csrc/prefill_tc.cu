@@ -317,11 +317,6 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
                     pdl_launch_dependents();
                     waited = true;
                 }
-                // page ids of the next tile: loads in flight while this one waits
-                if (kt + 1 < nkt) {
-                    ya = slice_row(kt + 1, 0);
-                    yb = slice_row(kt + 1, 1);
-                }
                 // value stage 1 holds B_K[h] until p = q B_K[h] has been computed
                 if ((kt >= 2 && !mbar_wait(&empty[st], ((kt >> 1) - 1) & 1)) ||
                     (!kprod && kt == 1 && !mbar_wait(&bar.pre_done, 0))) {
@@ -337,6 +332,11 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
                 tma_load_2d(sb + 2 * PF_BLK, m_r, hr, y0, &full[st]);
                 tma_load_2d(sb + 2 * PF_BLK + PF_BOX, m_r, hr, y1, &full[st]);
                 ++n_iss;
+                // page ids of the next tile, while this one is on its way
+                if (kt + 1 < nkt) {
+                    ya = slice_row(kt + 1, 0);
+                    yb = slice_row(kt + 1, 1);
+                }
             }
             // B_V[h] (K-major for the expansion) into the key stage tile nkt would use
             bool bv_issued = false;
