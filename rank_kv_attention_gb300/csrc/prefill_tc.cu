@@ -264,6 +264,34 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
     const KeyTiles<WIN> keys(a, p0 + t_lo, max_p);
     const int nkt = keys.count;
 
+    const int32_t *pt_row = a.page_table + (size_t)b * a.max_pages;
+    // pool row of a 64-key slice of key tile kt (a fully out-of-range row, which
+    // reads as zeros, for slices past the table or on an invalid page)
+    auto slice_row = [&](int kt, int hh) -> int {
+        const int key0 = keys.base(kt) + hh * PF_HALF;
+        if (key0 / a.page_size >= a.max_pages || keys.dead(a, key0)) return -PF_HALF;
+        const int32_t page = pt_row[key0 / a.page_size];
+        if (page < 0 || page >= a.num_pages) {
+            if (warp == 8 && key0 <= max_p) status_or(a.status, LRKV_STATUS_BAD_PAGE);
+            return -PF_HALF;
+        }
+        return page * a.page_size + key0 % a.page_size;
+    };
+    // the key or value tile whose slices start at pool rows y0 and y1
+    auto copy_tile = [&](uint8_t *sb, const CUtensorMap *m_s, const CUtensorMap *m_r, int y0, int y1, uint64_t *full) {
+        mbar_arrive_expect_tx(full, PF_STAGE);
+        tma_load_2d(sb, m_s, 0, y0, full);
+        tma_load_2d(sb + PF_BOX, m_s, 0, y1, full);
+        tma_load_2d(sb + PF_BLK, m_s, 64, y0, full);
+        tma_load_2d(sb + PF_BLK + PF_BOX, m_s, 64, y1, full);
+        tma_load_2d(sb + 2 * PF_BLK, m_r, h * a.r, y0, full);
+        tma_load_2d(sb + 2 * PF_BLK + PF_BOX, m_r, h * a.r, y1, full);
+    };
+    const int first_new = p0 - tq * PF_BM;  // position of the request's first new row
+    // whether the append has to be waited for before tile kt is copied
+    auto needs_append = [&](int kt) { return WIN && a.early && keys.base(kt) + PF_BN > first_new; };
+    int n_iss = 0;  // copy threads: tiles issued
+
     if (warp == 8) {
         if (lane == 0) {
             // q tile and B_K[h] (staged in value stage 1 until p = q B_K[h] is
@@ -273,6 +301,10 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
             tma_load_3d(smem + PF_OFF_Q + PF_BM * 128, &maps.q, 64, h, i0, &bar.q_full);
             tma_load_2d(smem + PF_OFF_V + PF_STAGE, &maps.bk, 0, h * 128, &bar.q_full);
             tma_load_2d(smem + PF_OFF_V + PF_STAGE + PF_BOX, &maps.bk, 0, h * 128 + 64, &bar.q_full);
+            if (!needs_append(0)) {
+                copy_tile(smem + PF_OFF_K, &maps.sk, &maps.rk, slice_row(0, 0), slice_row(0, 1), &bar.k_full[0]);
+                n_iss = 1;
+            }
         }
         __syncwarp();
         tmem_alloc(&bar.tmem, PF_TMEM_COLS);
@@ -281,38 +313,26 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = bar.tmem;
-    const int32_t *pt_row = a.page_table + (size_t)b * a.max_pages;
 
     if (warp == 8 || warp == 10) {
         if (lane == 0) {
             // ================= TMA producers: warp 8 keys, warp 10 values =================
             const bool kprod = warp == 8;
             bool ok = true;
-            const int hr = h * a.r;
-            // pool row of a 64-key slice of key tile kt (a fully out-of-range row,
-            // which reads as zeros, for slices past the table or on an invalid page)
-            auto slice_row = [&](int kt, int hh) -> int {
-                const int key0 = keys.base(kt) + hh * PF_HALF;
-                if (key0 / a.page_size >= a.max_pages || keys.dead(a, key0)) return -PF_HALF;
-                const int32_t page = pt_row[key0 / a.page_size];
-                if (page < 0 || page >= a.num_pages) {
-                    if (kprod && key0 <= max_p) status_or(a.status, LRKV_STATUS_BAD_PAGE);
-                    return -PF_HALF;
-                }
-                return page * a.page_size + key0 % a.page_size;
-            };
             const CUtensorMap *m_s = kprod ? &maps.sk : &maps.sv;
             const CUtensorMap *m_r = kprod ? &maps.rk : &maps.rv;
             uint64_t *full = kprod ? bar.k_full : bar.v_full;
             uint64_t *empty = kprod ? bar.s_full : bar.pv_done;
             uint8_t *ring = smem + (kprod ? PF_OFF_K : PF_OFF_V);
-            int n_iss = 0;
-            int ya = slice_row(0, 0), yb = slice_row(0, 1);
-            const int first_new = p0 - tq * PF_BM;  // position of the request's first new row
-            bool waited = !(WIN && a.early);
-            for (int kt = 0; kt < nkt; ++kt) {
+            int ya = 0, yb = 0;
+            if (n_iss < nkt) {
+                ya = slice_row(n_iss, 0);
+                yb = slice_row(n_iss, 1);
+            }
+            bool waited = false;
+            for (int kt = n_iss; kt < nkt; ++kt) {
                 const int st = kt & 1, y0 = ya, y1 = yb;
-                if (!waited && keys.base(kt) + PF_BN > first_new) {  // (positions grow from tile to tile)
+                if (!waited && needs_append(kt)) {  // (positions grow from tile to tile)
                     pdl_wait();
                     pdl_launch_dependents();
                     waited = true;
@@ -323,14 +343,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
                     ok = false;
                     break;
                 }
-                uint8_t *sb = ring + st * PF_STAGE;
-                mbar_arrive_expect_tx(&full[st], PF_STAGE);
-                tma_load_2d(sb, m_s, 0, y0, &full[st]);
-                tma_load_2d(sb + PF_BOX, m_s, 0, y1, &full[st]);
-                tma_load_2d(sb + PF_BLK, m_s, 64, y0, &full[st]);
-                tma_load_2d(sb + PF_BLK + PF_BOX, m_s, 64, y1, &full[st]);
-                tma_load_2d(sb + 2 * PF_BLK, m_r, hr, y0, &full[st]);
-                tma_load_2d(sb + 2 * PF_BLK + PF_BOX, m_r, hr, y1, &full[st]);
+                copy_tile(ring + st * PF_STAGE, m_s, m_r, y0, y1, &full[st]);
                 ++n_iss;
                 // page ids of the next tile, while this one is on its way
                 if (kt + 1 < nkt) {
