@@ -638,14 +638,14 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
             tc_fence_before();
             mbar_arrive(&bar.p_full[st]);
         }
-        if (ok)
-            ok = __all_sync(0xffffffffu, mbar_wait(&bar.pv_done[(nkt - 1) & 1], ((nkt - 1) >> 1) & 1));
         if (WIN && a.early) pdl_wait();  // (long past: the last tiles hold new rows)
         // row sum of both halves, exchanged through the q tile (no longer read:
         // the last scores completed before this softmax began)
         float *lsum = reinterpret_cast<float *>(smem + PF_OFF_Q);
         lsum[hf * PF_BM + t] = l;
         if (ok) ok = pair_exchange();
+        if (ok)
+            ok = __all_sync(0xffffffffu, mbar_wait(&bar.pv_done[(nkt - 1) & 1], ((nkt - 1) >> 1) & 1));
         const float lt = l + lsum[(hf ^ 1) * PF_BM + t];
         const float inv_l = lt > 0.f ? 1.f / lt : 0.f;
         if (ok) {
