@@ -7,6 +7,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "liblrkv.so")
@@ -52,6 +53,13 @@ class CacheDesc(ctypes.Structure):
     ]
 
 
+# The same as bytes, made in one step; functions that take a bare pointer for the
+# descriptor accept them.
+_PACK_CACHE = struct.Struct("@4P6i4fPfi")
+assert _PACK_CACHE.size == ctypes.sizeof(CacheDesc)
+pack_cache = _PACK_CACHE.pack
+
+
 class LrkvError(RuntimeError):
     def __init__(self, fn, code, lib=None):
         msg = f"{fn} failed: {code}"
@@ -72,9 +80,9 @@ CACHE_P = ctypes.POINTER(CacheDesc)
 
 SIGNATURES = {
     "lrkv_decode_window_workspace_bytes": (SZ, [I32] * 8),
-    "lrkv_decode_window": (ctypes.c_int, [P, CACHE_P, P, P, P, P, I32, I32, I32, I32, I32, P, P, SZ, P,
+    "lrkv_decode_window": (ctypes.c_int, [P, P, P, P, P, P, I32, I32, I32, I32, I32, P, P, SZ, P,
                                           P]),
-    "lrkv_prefill_window": (ctypes.c_int, [P, P, P, P, I32, I32, I32, I32, P, P, P, P, P, P, CACHE_P, P,
+    "lrkv_prefill_window": (ctypes.c_int, [P, P, P, P, I32, I32, I32, I32, P, P, P, P, P, P, P, P,
                                            I32, I32, I32, P, P, SZ, P, P]),
     "lrkv_page_plan": (ctypes.c_int, [P, P, I32, I32, I32, I32, I32, I32, I32, P, P, P, P, P, P, P, P, P,
                                       P, P, P]),

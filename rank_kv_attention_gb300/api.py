@@ -346,7 +346,6 @@ def prefill(X, Q, cu_rows, start_pos, max_ctx, W_S_K, W_S_V, U_K, U_V, B_K, B_V,
 # than a careful look at its arguments, so each function compares everything in
 # one expression and looks for the fault only when something differs.
 # ----------------------------------------------------------------------------
-_F4 = ctypes.c_float * 4
 _i32, _u8, _Tensor = torch.int32, torch.uint8, torch.Tensor
 _current_device = torch.cuda.current_device
 
@@ -369,7 +368,8 @@ def _fits(args, dev):
 
 
 def _cache_arg(cache, dev):
-    """PagedCache.desc() with all pools' shapes and devices checked."""
+    """(PagedCache.desc() as bytes, activation dtype, H, d_h, r, groups, LRKV_* dtype) with all pools' shapes and
+    devices checked."""
     S_K, S_V, R_K, R_V, N_K = cache.S_K, cache.S_V, cache.R_K, cache.R_V, cache.N_K
     if not (isinstance(S_K, _Tensor) and isinstance(R_K, _Tensor)) or S_K.dim() not in (3, 4) or R_K.dim() != 4:
         raise ValueError("S_K must be [num_pages, page_size, (G,) d_h] and R_K [num_pages, page_size, H, r]")
@@ -385,12 +385,14 @@ def _cache_arg(cache, dev):
             and S_V.get_device() == dev and R_K.get_device() == dev and R_V.get_device() == dev
             and S_K.is_contiguous() and S_V.is_contiguous() and R_K.is_contiguous() and R_V.is_contiguous()):
         _refuse(((S_K, "S_K", dt, ss), (S_V, "S_V", dt, ss), (R_K, "R_K", dt, rs), (R_V, "R_V", dt, rs)), dev)
-    nk = None
+    nk = 0
     if N_K is not None:
         _fits(((N_K, "N_K", act, (n, ps, H)),), dev)
         nk = N_K.data_ptr()
-    return _abi.CacheDesc(S_K.data_ptr(), S_V.data_ptr(), R_K.data_ptr(), R_V.data_ptr(), n, ps, H, ss[-1], r,
-                          _DT[dt], _F4(*cache.scale), nk, cache.norm_eps, ss[2] if len(ss) == 4 else 1), act, H, ss[-1], r
+    d_h, G, code = ss[-1], ss[2] if len(ss) == 4 else 1, _DT[dt]
+    s0, s1, s2, s3 = cache.scale
+    return _abi.pack_cache(S_K.data_ptr(), S_V.data_ptr(), R_K.data_ptr(), R_V.data_ptr(), n, ps, H, d_h, r, code,
+                           s0, s1, s2, s3, nk, cache.norm_eps, G), act, H, d_h, r, G, code
 
 
 def _own_buffer(shape, dtype, dev, stream):
@@ -399,6 +401,10 @@ def _own_buffer(shape, dtype, dev, stream):
     if stream is not None:
         t.record_stream(stream)
     return t
+
+
+def _too_large(**sizes):
+    raise ValueError(", ".join(f"{k} = {v}" for k, v in sizes.items()) + ": sizes are 32-bit")
 
 
 def _raw_stream(stream, dev):
@@ -445,7 +451,7 @@ def decode_window(q, cache: PagedCache, B_K, B_V, seq_lens, page_table, max_seq_
     """lrkv_decode_window: one decode step in which request b sees its last
     ``window`` rows and its first ``sinks`` rows; returns out [B, H, d_h]."""
     dev = _device_of(q, "q")
-    desc, dt, H, d_h, r = _cache_arg(cache, dev)
+    desc, dt, H, d_h, r, G, code = _cache_arg(cache, dev)
     B = _dim(q, "q", 3)[0]
     max_pages = _dim(page_table, "page_table", 2)[1]
     if out is None:
@@ -464,16 +470,18 @@ def decode_window(q, cache: PagedCache, B_K, B_V, seq_lens, page_table, max_seq_
         _refuse(((q, "q", dt, shape), (B_K, "B_K", dt, base), (B_V, "B_V", dt, base), (seq_lens, "seq_lens", _i32, (B,)),
                  (page_table, "page_table", _i32, (B, max_pages)), (out, "out", dt, shape)), dev)
     L = _abi.lib()
+    if (max_seq_len | window | sinks) > 0x7fffffff:
+        _too_large(max_seq_len=max_seq_len, window=window, sinks=sinks)
     args = (q.data_ptr(), desc, B_K.data_ptr(), B_V.data_ptr(), seq_lens.data_ptr(), page_table.data_ptr(), B,
             max_pages, max_seq_len, window, sinks, out.data_ptr())
     tail = _status(status, dev), _raw_stream(stream, dev)
-    code = L.lrkv_decode_window(*args, *_workspace(ws, dev), *tail)
-    if code == _abi.LRKV_E_WORKSPACE and ws is None:  # (most calls need none)
-        n = L.lrkv_decode_window_workspace_bytes(B, H, d_h, r, max_seq_len, window, sinks, desc.dtype)
+    err = L.lrkv_decode_window(*args, *_workspace(ws, dev), *tail)
+    if err == _abi.LRKV_E_WORKSPACE and ws is None:  # (most calls need none)
+        n = L.lrkv_decode_window_workspace_bytes(B, H, d_h, r, max_seq_len, window, sinks, code)
         ws = _own_buffer((n,), _u8, q.device, stream)
-        code = L.lrkv_decode_window(*args, ws.data_ptr(), n, *tail)
-    if code:
-        _abi.check("lrkv_decode_window", code)
+        err = L.lrkv_decode_window(*args, ws.data_ptr(), n, *tail)
+    if err:
+        _abi.check("lrkv_decode_window", err)
     return out
 
 
@@ -483,11 +491,11 @@ def prefill_window(X, Q, cu_rows, start_pos, max_ctx, W_S_K, W_S_V, U_K, U_V, B_
     """lrkv_prefill_window: append the chunk X, then attention of each row's Q
     over the last ``window`` rows up to its own and the first ``sinks`` rows."""
     dev = _device_of(X, "X")
-    desc, dt, H, d_h, r = _cache_arg(cache, dev)
+    desc, dt, H, d_h, r, G, code = _cache_arg(cache, dev)
     n, d = _dim(X, "X", 2)
     (B,) = _dim(start_pos, "start_pos", 1)
     max_pages = _dim(page_table, "page_table", 2)[1]
-    shape, base, shared, private = (n, H, d_h), (H, d_h, r), (max(1, desc.G) * d_h, d), (H, r, d)
+    shape, base, shared, private = (n, H, d_h), (H, d_h, r), (G * d_h, d), (H, r, d)
     if out is None:
         out = _own_buffer(shape, dt, X.device, stream)
     T = _Tensor
@@ -515,13 +523,15 @@ def prefill_window(X, Q, cu_rows, start_pos, max_ctx, W_S_K, W_S_V, U_K, U_V, B_
             W_S_V.data_ptr(), U_K.data_ptr(), U_V.data_ptr(), B_K.data_ptr(), B_V.data_ptr(), desc,
             page_table.data_ptr(), max_pages, window, sinks, out.data_ptr())
     tail = _status(status, dev), _raw_stream(stream, dev)
-    code = L.lrkv_prefill_window(*args, *_workspace(ws, dev), *tail)
-    if code == _abi.LRKV_E_WORKSPACE and ws is None:  # (few rows, or the per-row path)
-        m = L.lrkv_prefill_workspace_bytes(B, n, H, d_h, r, max_ctx, desc.dtype)
+    if (max_ctx | window | sinks) > 0x7fffffff:
+        _too_large(max_ctx=max_ctx, window=window, sinks=sinks)
+    err = L.lrkv_prefill_window(*args, *_workspace(ws, dev), *tail)
+    if err == _abi.LRKV_E_WORKSPACE and ws is None:  # (few rows, or the per-row path)
+        m = L.lrkv_prefill_workspace_bytes(B, n, H, d_h, r, max_ctx, code)
         ws = _own_buffer((m,), _u8, X.device, stream)
-        code = L.lrkv_prefill_window(*args, ws.data_ptr(), m, *tail)
-    if code:
-        _abi.check("lrkv_prefill_window", code)
+        err = L.lrkv_prefill_window(*args, ws.data_ptr(), m, *tail)
+    if err:
+        _abi.check("lrkv_prefill_window", err)
     return out
 
 
@@ -548,6 +558,8 @@ def page_plan(seq_lens, new_rows, page_table, free_pages, n_free, page_size, max
     max_pages = _dim(page_table, "page_table", 2)[1]
     if max_rows < 0:
         raise ValueError("max_rows must not be negative")
+    if (max_rows | page_size | window | sinks) > 0x7fffffff:
+        _too_large(max_rows=max_rows, page_size=page_size, window=window, sinks=sinks)
     if free_out is None:
         free_out = _own_buffer((num_pages,), _i32, seq_lens.device, stream)
     if not (isinstance(new_rows, _Tensor) and isinstance(n_free, _Tensor) and isinstance(free_out, _Tensor)

@@ -530,6 +530,23 @@ def test_plan_bad_ids_become_minus_one():
 # ---------------------------------------------------------------------------
 # All of them as a server would run them
 # ---------------------------------------------------------------------------
+def test_binding_refuses_sizes_past_32_bits():
+    """A size that would wrap into a valid one is refused."""
+    import rank_kv_attention_gb300 as L
+    d = DevDecode(decode_case([5, 9], 16, 128, 48))
+    for window, sinks, longest in ((2 ** 32 + 5, 0, 9), (5, 2 ** 32, 9), (5, 0, 2 ** 32 + 9)):
+        with pytest.raises(ValueError):
+            L.decode_window(d.q, d.cache, d.B_K, d.B_V, d.seq_lens, d.page_table, longest, window, sinks)
+    w, pt, cache, X, Q = prefill_inputs([70], [0], 64, 16, 128, 48, "bf16", 50, 2, seed=1)
+    for window, sinks in ((2 ** 32 + 5, 0), (5, 2 ** 32 + 1)):
+        with pytest.raises(ValueError):
+            run_prefill(w, pt, cache, X, Q, [70], [0], window, sinks, "bf16")
+    with pytest.raises(ValueError):
+        plan_on_device([3], [1], [[0, 1]], [2], 3, 64, 4, window=2 ** 32 + 64, sinks=0)
+    with pytest.raises(ValueError):
+        plan_on_device([3], [1], [[0, 1]], [2], 3, 2 ** 32 + 64, 4, window=64, sinks=0)
+
+
 def test_serving_run_with_a_bounded_pool():
     """Prompts in chunks, then single tokens, requests that end and new ones in their place: plan, prefill and
     decode on a pool that holds only the windows' pages, one graph-captured decode step among them.  Each output
