@@ -347,7 +347,6 @@ def prefill(X, Q, cu_rows, start_pos, max_ctx, W_S_K, W_S_V, U_K, U_V, B_K, B_V,
 # one expression and looks for the fault only when something differs.
 # ----------------------------------------------------------------------------
 _i32, _u8, _Tensor = torch.int32, torch.uint8, torch.Tensor
-_current_device = torch.cuda.current_device
 
 
 def _refuse(args, dev):
@@ -417,7 +416,7 @@ def _device_of(t, name):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    return _current_device()
+    return torch._C._cuda_getDevice()  # (CUDA is initialised: t is on it)
 
 
 def _dim(t, name, n):
@@ -452,8 +451,7 @@ def decode_window(q, cache: PagedCache, B_K, B_V, seq_lens, page_table, max_seq_
     ``window`` rows and its first ``sinks`` rows; returns out [B, H, d_h]."""
     dev = _device_of(q, "q")
     desc, dt, H, d_h, r, G, code = _cache_arg(cache, dev)
-    B = _dim(q, "q", 3)[0]
-    max_pages = _dim(page_table, "page_table", 2)[1]
+    B, max_pages = _dim(q, "q", 3)[0], _dim(page_table, "page_table", 2)[1]
     if out is None:
         out = torch.empty_like(q)
         if stream is not None:
@@ -474,8 +472,10 @@ def decode_window(q, cache: PagedCache, B_K, B_V, seq_lens, page_table, max_seq_
         _too_large(max_seq_len=max_seq_len, window=window, sinks=sinks)
     args = (q.data_ptr(), desc, B_K.data_ptr(), B_V.data_ptr(), seq_lens.data_ptr(), page_table.data_ptr(), B,
             max_pages, max_seq_len, window, sinks, out.data_ptr())
-    tail = _status(status, dev), _raw_stream(stream, dev)
-    err = L.lrkv_decode_window(*args, *_workspace(ws, dev), *tail)
+    tail = (None if status is None else _status(status, dev),
+            torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
+    err = (L.lrkv_decode_window(*args, None, 0, *tail) if ws is None
+           else L.lrkv_decode_window(*args, *_workspace(ws, dev), *tail))
     if err == _abi.LRKV_E_WORKSPACE and ws is None:  # (most calls need none)
         n = L.lrkv_decode_window_workspace_bytes(B, H, d_h, r, max_seq_len, window, sinks, code)
         ws = _own_buffer((n,), _u8, q.device, stream)
