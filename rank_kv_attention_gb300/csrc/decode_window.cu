@@ -1129,21 +1129,25 @@ static WinPlan window_plan(int B, int64_t rows, double tile_bytes, bool q8, int 
     const double hbm_us = (double)B * tiles * tile_bytes / 6.5e6;
     WinPlan best{1, 1, 1};
     double least = 1e300;
-    for (int i = 0; i < 4; ++i) {
-        const int CL = 1 << i, nc = active[i];
-        if (nc < 1) continue;
-        const int64_t smax = std::max<int64_t>(1, std::min<int64_t>(most_splits, nc / B));
-        for (int64_t S = 1; S <= smax; ++S) {
-            const int64_t used = std::min<int64_t>((int64_t)B * S, nc), rounds = ((int64_t)B * S + used - 1) / used;
-            const int64_t per_cta = ((tiles + S - 1) / S + CL - 1) / CL;
-            const double work = rounds * (per_cta * tile_us + fixed[i]);
-            // (where the memory's rate decides, the layout with the fewest segments)
-            const double t = std::max(work, hbm_us) + 0.3 * rounds * fixed[i] + (S > 1 ? 8. : 0.);
-            if (t < least) {
-                least = t;
-                best = {CL, (int)used, (int)S};
-            }
+    auto consider = [&](int i, int64_t S) {
+        const int64_t CL = 1 << i, used = std::min<int64_t>((int64_t)B * S, active[i]);
+        const int64_t rounds = ((int64_t)B * S + used - 1) / used, per_cta = ((tiles + S - 1) / S + CL - 1) / CL;
+        const double work = rounds * (per_cta * tile_us + fixed[i]);
+        // (where the memory's rate decides, the layout with the fewest segments)
+        const double t = std::max(work, hbm_us) + 0.3 * rounds * fixed[i] + (S > 1 ? 8. : 0.);
+        if (t < least) {
+            least = t;
+            best = {(int)CL, (int)used, (int)S};
         }
+        return per_cta;
+    };
+    for (int i = 0; i < 4; ++i)
+        if (active[i] > 0) consider(i, 1);
+    for (int i = 0; i < 4; ++i) {
+        if (active[i] < 1 || 1.3 * fixed[i] + tile_us + 8. >= least) continue;  // (the least that splits could take)
+        const int64_t smax = std::min<int64_t>(most_splits, active[i] / B);
+        for (int64_t S = 2; S <= smax; ++S)
+            if (consider(i, S) == 1) break;  // (more splits take no less)
     }
     return best;
 }
@@ -1177,6 +1181,7 @@ static cudaError_t launch_cfg(const DecodeArgs &a, void *ws, size_t ws_bytes) {
     cudaError_t e = plan_cfg<C>(a.B, a.max_seq_len, a.window, a.sinks, &plan);
     if (e != cudaSuccess) return e;
     size_t states = (size_t)a.B * plan.S * H;
+    if (plan.S > 1 && !ws) return cudaErrorNotSupported;
     if (plan.S > 1 && ws_bytes < states * (2 + C::W) * sizeof(float)) {  // (a prefill's workspace)
         e = plan_cfg<C>(a.B, a.max_seq_len, a.window, a.sinks, &plan, 1);
         if (e != cudaSuccess) return e;

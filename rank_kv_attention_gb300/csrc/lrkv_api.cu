@@ -146,6 +146,7 @@ static int run_decode(const DecodeArgs &a, void *workspace, size_t ws_bytes) {
                                   ? launch_window_fast(a, workspace, ws_bytes)
                                   : launch_window_any(a);
         prof_after(LRKV_PROFILE_ATTENTION, a.stream);
+        if (e == cudaErrorNotSupported && !workspace) return LRKV_E_WORKSPACE;  // requests to split, nothing enqueued
         return e == cudaSuccess ? LRKV_OK : cuda_fail(e);
     }
     DecodeGeom geo = decode_geom(a.B, a.max_seq_len);
@@ -874,11 +875,12 @@ int lrkv_decode_window(const void *q, const lrkv_cache_t *cache, const void *B_K
     a.out = out;
     a.status = dev_status;
     a.stream = (cudaStream_t)stream;
-    const size_t need = fast_decode_supported(cache->H, cache->d_h, cache->r, cache->page_size, cache->dtype,
-                                              cache_groups(*cache))
-                            ? window_state_bytes(B, cache->H, cache->r, max_seq_len, window, sinks, cache->dtype)
-                            : 0;
-    if (need && (!workspace || workspace_bytes < need)) return LRKV_E_WORKSPACE;
+    // (without a workspace the launcher says whether one is needed: the same plan
+    // is not made twice)
+    if (workspace &&
+        fast_decode_supported(cache->H, cache->d_h, cache->r, cache->page_size, cache->dtype, cache_groups(*cache)) &&
+        workspace_bytes < window_state_bytes(B, cache->H, cache->r, max_seq_len, window, sinks, cache->dtype))
+        return LRKV_E_WORKSPACE;
     return run_decode(a, workspace, workspace_bytes);
 }
 
