@@ -103,13 +103,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TC_THREADS, 1)
         prefetch_tensormap(&maps.x);
         for (int k = 0; k < 4; ++k) prefetch_tensormap(&maps.w[k]);
     }
+    // (tensor memory is taken after the wait: a predecessor on this SM may still
+    // have to take its own)
+    pdl_wait();
     if (warp == 1) tmem_alloc_pair(tmem_slot, TC_TMEM_COLS);
     // both CTAs' barriers are initialised before either copies into the other
     tc_fence_before();
     cluster_sync_all();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    pdl_wait();
     pdl_launch_dependents();
     bool ok = true;
     int issued = 0;  // producer: k-steps whose copies were requested
