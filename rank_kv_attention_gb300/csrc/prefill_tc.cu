@@ -47,9 +47,10 @@
 // visited tile are masked per row where a window starts or the sinks end, and
 // keys that no row of the CTA sees are treated like those past the end (clearing
 // the rows of whole groups too took 4000 of a CTA's 37,000 cycles).
-// 8 prompts of 2048 rows, window 1024, 4 sinks, 16 heads, r = 48: a CTA takes ten
-// tiles of 2050 cycles, 12,500 cycles before and after them and 1600 until the
-// next one starts.  A tile's period is the chain softmax -> value products ->
+// 8 prompts of 2048 rows, window 1024, 4 sinks, 16 heads, r = 48 (272 us with the
+// append): a CTA takes ten tiles of 2050 cycles (3300 and 2700 the first two), 4800
+// cycles before them (two dependent lookups, a copy's latency, p) and 5000 after
+// them, and the SM's next one starts 1600 later.  A tile's period is the chain softmax -> value products ->
 // scores of the tile after next, with two score buffers: fewer products (no low
 // half of p, narrower values), no exponentials, an exchange of maxima hidden
 // behind the weights or 16 softmax warps changed the call by -3 to +4%.
