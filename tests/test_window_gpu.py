@@ -530,6 +530,36 @@ def test_plan_bad_ids_become_minus_one():
 # ---------------------------------------------------------------------------
 # All of them as a server would run them
 # ---------------------------------------------------------------------------
+def far(cache, extra):
+    """The same cache at the end of pools that are `extra` pages longer."""
+    from rank_kv_attention_gb300.api import PagedCache
+
+    def grow(p):
+        q = torch.empty((extra + p.shape[0], *p.shape[1:]), dtype=p.dtype, device="cuda")
+        q[extra:].view(torch.uint8).copy_(p.view(torch.uint8))
+        return q
+    return PagedCache(*[grow(p) for p in (cache.S_K, cache.S_V, cache.R_K, cache.R_V)], cache.scale)
+
+
+@pytest.mark.parametrize("H,d_h,r,dtype", [(16, 128, 48, "bf16"), (16, 128, 48, "fp8"), (8, 64, 16, "f32")])
+def test_offsets_past_32_bits(H, d_h, r, dtype):
+    """Pages whose private rows start past 2^31 elements: decode, append and prefill as in a small pool, bit for bit."""
+    extra = 2 ** 31 // (64 * H * r) + 1
+    d = DevDecode(decode_case([1, 300, 65, 700], H, d_h, r, dtype, seed=H))
+    want = run_decode(d, 200, 5)
+    d.cache, d.page_table = far(d.cache, extra), d.page_table + extra
+    assert torch.equal(run_decode(d, 200, 5), want)
+    del d
+    rows, starts, adt = [90, 33], [130, 0], I.act_dtype(dtype)
+    w, pt, cache, X, Q = prefill_inputs(rows, starts, 64, H, d_h, r, dtype, 120, 3, seed=2)
+    big = far(cache, extra)
+    want = run_prefill(w, pt, cache, X, Q, rows, starts, 120, 3, adt)
+    got = run_prefill(w, np.where(pt >= 0, pt + extra, pt), big, X, Q, rows, starts, 120, 3, adt)
+    assert torch.equal(got, want)
+    for p, q in zip((cache.S_K, cache.S_V, cache.R_K, cache.R_V), (big.S_K, big.S_V, big.R_K, big.R_V)):
+        assert torch.equal(q[extra:].view(torch.uint8), p.view(torch.uint8))
+
+
 def test_binding_refuses_sizes_past_32_bits():
     """A size that would wrap into a valid one is refused."""
     import rank_kv_attention_gb300 as L
