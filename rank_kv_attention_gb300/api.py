@@ -448,7 +448,9 @@ def decode_window_workspace_bytes(B, H, d_h, r, max_seq_len, window, sinks=0, dt
 def decode_window(q, cache: PagedCache, B_K, B_V, seq_lens, page_table, max_seq_len, window, sinks=0,
                   out=None, ws=None, status=None, stream=None):
     """lrkv_decode_window: one decode step in which request b sees its last
-    ``window`` rows and its first ``sinks`` rows; returns out [B, H, d_h]."""
+    ``window`` rows and its first ``sinks`` rows; returns out [B, H, d_h].  With
+    ``ws`` (decode_window_workspace_bytes uint8) few requests may be laid out
+    faster; without it one is made where a long call needs it."""
     dev = _device_of(q, "q")
     desc, dt, H, d_h, r, G, code = _cache_arg(cache, dev)
     B, max_pages = _dim(q, "q", 3)[0], _dim(page_table, "page_table", 2)[1]

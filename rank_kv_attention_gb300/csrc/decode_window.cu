@@ -1114,16 +1114,22 @@ struct WinPlan {
 // 12 ns per KB of bf16 rows, 34 ns per KB of 8-bit codes (0.67 us and 1.0 us for
 // 16 heads, r = 48); a segment costs a cluster fixed[] us besides (private
 // queries, start of the ring, the states' way to their owners; measured for
-// segments of a few tiles), a combine 8 us with its launch, and nothing is faster than the copy
-// bandwidth.  Measured at 16 heads, r = 48, against this rule's choice:
+// segments of a few tiles), a combine 4 us, and nothing is faster than the copy
+// bandwidth.  A split without a workspace at hand (unsplit_below: 25 us) costs the
+// caller another call and an allocation: it is chosen only where both layouts
+// take longer than that.  Measured at 16 heads, r = 48, against this rule's choice:
 //   16 requests, window 1024:  CL 1, 2, 4, 8 in 58.5, 33.9, 22.1, 31.0 us (eight
 //     CTAs a cluster: 15 clusters fit the GPU at once, so one request waits)
 //   64 requests, window 1024:  61.5, 45.5, 51.5, 76.9 us
 //   1 request, window 8000:    CL 8 unsplit 51.1 us, split over 15 clusters 18.4 us
+//   1 request, window 1024:    unsplit 13.4 us, split 10.8; 4 requests, window
+//     2048: 20.0, 16.3; 16 requests, window 1024: 21.8, 21.0; 40, window 2048:
+//     60.8, 57.1 (a combine taken as 2 us: 12 requests, window 2048: 25.1 for 23.3)
 // `rows`: visible rows of the longest request; active[i]: clusters of 1 << i CTAs
 // that the GPU holds at once.
-static WinPlan window_plan(int B, int64_t rows, double tile_bytes, bool q8, int most_splits, const int (&active)[4]) {
-    static const double fixed[4] = {17., 12., 9., 8.};
+static WinPlan window_plan(int B, int64_t rows, double tile_bytes, bool q8, int most_splits, double unsplit_below,
+                           const int (&active)[4]) {
+    static const double fixed[4] = {17., 12., 9., 8.}, combine = 4.;
     const int64_t tiles = (rows + kTS - 1) / kTS;
     const double tile_us = tile_bytes / 1024. * (q8 ? 0.034 : 0.012);
     const double hbm_us = (double)B * tiles * tile_bytes / 6.5e6;
@@ -1134,7 +1140,8 @@ static WinPlan window_plan(int B, int64_t rows, double tile_bytes, bool q8, int 
         const int64_t rounds = ((int64_t)B * S + used - 1) / used, per_cta = ((tiles + S - 1) / S + CL - 1) / CL;
         const double work = rounds * (per_cta * tile_us + fixed[i]);
         // (where the memory's rate decides, the layout with the fewest segments)
-        const double t = std::max(work, hbm_us) + 0.3 * rounds * fixed[i] + (S > 1 ? 8. : 0.);
+        double t = std::max(work, hbm_us) + 0.3 * rounds * fixed[i];
+        if (S > 1) t = std::max(t + combine, unsplit_below);
         if (t < least) {
             least = t;
             best = {(int)CL, (int)used, (int)S};
@@ -1144,7 +1151,8 @@ static WinPlan window_plan(int B, int64_t rows, double tile_bytes, bool q8, int 
     for (int i = 0; i < 4; ++i)
         if (active[i] > 0) consider(i, 1);
     for (int i = 0; i < 4; ++i) {
-        if (active[i] < 1 || 1.3 * fixed[i] + tile_us + 8. >= least) continue;  // (the least that splits could take)
+        // (the least that splits could take)
+        if (active[i] < 1 || std::max(1.3 * fixed[i] + tile_us + combine, unsplit_below) >= least) continue;
         const int64_t smax = std::min<int64_t>(most_splits, active[i] / B);
         for (int64_t S = 2; S <= smax; ++S)
             if (consider(i, S) == 1) break;  // (more splits take no less)
@@ -1153,7 +1161,8 @@ static WinPlan window_plan(int B, int64_t rows, double tile_bytes, bool q8, int 
 }
 
 template <class C>
-static cudaError_t plan_cfg(int B, int max_seq_len, int window, int sinks, WinPlan *plan, int most_splits = kMaxSplits) {
+static cudaError_t plan_cfg(int B, int max_seq_len, int window, int sinks, WinPlan *plan, int most_splits = kMaxSplits,
+                            double unsplit_below = 0.) {
     auto kern = decode_window_kernel<C>;
     cudaError_t e = smem_limit_once(kern, C::SMEM);
     int active[4];
@@ -1161,7 +1170,7 @@ static cudaError_t plan_cfg(int B, int max_seq_len, int window, int sinks, WinPl
         active[i] = active_clusters(reinterpret_cast<const void *>(kern), C::SMEM, C::THREADS, 1 << i, &e);
     if (e == cudaSuccess)
         *plan = window_plan(B, std::min<int64_t>(max_seq_len, (int64_t)window + sinks) + kTS, 2.0 * C::SLOT, C::Q8,
-                            most_splits, active);
+                            most_splits, unsplit_below, active);
     return e;
 }
 
@@ -1178,7 +1187,7 @@ static cudaError_t launch_cfg(const DecodeArgs &a, void *ws, size_t ws_bytes) {
         (c.N_K && !make_row_map(&maps.nk, c.N_K, pool_rows, H, 2, kTS)))
         return cudaErrorInvalidValue;
     WinPlan plan;
-    cudaError_t e = plan_cfg<C>(a.B, a.max_seq_len, a.window, a.sinks, &plan);
+    cudaError_t e = plan_cfg<C>(a.B, a.max_seq_len, a.window, a.sinks, &plan, kMaxSplits, ws ? 0. : 25.);
     if (e != cudaSuccess) return e;
     size_t states = (size_t)a.B * plan.S * H;
     if (plan.S > 1 && !ws) return cudaErrorNotSupported;

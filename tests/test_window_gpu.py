@@ -219,6 +219,27 @@ def test_decode_split_requests(H, r, dtype, B):
     check(got, *decode_reference(case, 4000, 30), f"B={B}")
 
 
+@pytest.mark.parametrize("H,r,dtype", [(16, 48, "bf16"), (32, 32, "bf16"), (16, 56, "bf16"), (16, 64, "fp8")])
+@pytest.mark.parametrize("lens,window,sinks", [([3000], 1000, 4), ([6000, 40], 4000, 30), ([1500, 0, 1400, 1501, 17], 1024, 0),
+                                               ([2100] * 7 + [5], 2048, 4), ([1100] * 16, 1024, 4)])
+def test_decode_split_with_a_workspace(H, r, dtype, lens, window, sinks):
+    """The layout that a caller's workspace allows, beside the one without: both within the bound; one byte less is refused."""
+    import rank_kv_attention_gb300 as L
+    case = decode_case(lens, H, 128, r, dtype, seed=len(lens))
+    blank_unseen(case, window, sinks)
+    d, (ref, bound) = DevDecode(case), decode_reference(case, window, sinks)
+    need = L.decode_window_workspace_bytes(len(lens), H, 128, r, d.max_seq_len, window, sinks, d.cache.dtype)
+    assert need > 0 or len(lens) > 5
+    check(host(run_decode(d, window, sinks), case.act_dtype), ref, bound, "without")
+    if need:
+        ws = L.workspace(need).fill_(0xFF)
+        got = run_decode(d, window, sinks, ws=ws)
+        check(host(got, case.act_dtype), ref, bound, "with")
+        assert torch.equal(got, run_decode(d, window, sinks, ws=ws))
+        with pytest.raises(L.LrkvError):
+            run_decode(d, window, sinks, ws=L.workspace(need - 256)[:need - 256])
+
+
 # ---------------------------------------------------------------------------
 # Prefill
 # ---------------------------------------------------------------------------
