@@ -405,14 +405,17 @@ LRKV_API int lrkv_key_norms(const int32_t *positions, const int32_t *seq_ids, in
  * about window / page_size + 1 for its window, however long it gets
  * (lrkv_page_plan keeps exactly those).
  *
- * lrkv_decode_window takes the arguments of lrkv_decode.  Its workspace is
- * lrkv_decode_window_workspace_bytes(...) bytes, 256-byte aligned, scratch
- * that needs no initialisation.  Most calls are one launch and need none: that
- * function returns 0.  Few requests with long windows are split over the GPU
- * and leave partial states there.  With workspace NULL a call is split only
- * where that saves a good part of a long call, and then returns
- * LRKV_E_WORKSPACE with nothing enqueued; a caller that keeps a workspace gets
- * the faster layout (1 request, window 1024: 10.8 us instead of 13.4).  No block waits for another
+ * lrkv_decode_window takes the arguments of lrkv_decode.  Most calls are one
+ * launch; few requests with long windows are split over the GPU and leave
+ * partial states in the workspace: scratch, 256-byte aligned, that needs no
+ * initialisation, at least lrkv_decode_window_workspace_bytes(...) bytes of the
+ * call (less is LRKV_E_WORKSPACE).  That function never falls as B, max_seq_len,
+ * window or sinks grow, so a workspace sized for a server's largest call serves
+ * every smaller one; it is about 3 MB at most, and 0 for head shapes that are never
+ * split.  With workspace NULL a call is split only where that saves a good part
+ * of a long call, and then returns LRKV_E_WORKSPACE with nothing enqueued; a
+ * caller that keeps a workspace gets the faster layout (1 request, window 1024:
+ * 10.8 us instead of 13.4).  No block waits for another
  * outside its own thread-block cluster, so calls on several streams run side by
  * side (each with a workspace of its own).
  *

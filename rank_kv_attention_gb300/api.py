@@ -442,6 +442,7 @@ def _status(status, dev):
 
 
 def decode_window_workspace_bytes(B, H, d_h, r, max_seq_len, window, sinks=0, dtype=torch.bfloat16) -> int:
+    """lrkv_decode_window_workspace_bytes: enough for this call and for every smaller one."""
     return _abi.lib().lrkv_decode_window_workspace_bytes(B, H, d_h, r, max_seq_len, window, sinks, _DT[dtype])
 
 

@@ -1160,17 +1160,29 @@ static WinPlan window_plan(int B, int64_t rows, double tile_bytes, bool q8, int 
     return best;
 }
 
+// Visible rows of the longest request that a call lays out, tile edges included.
+static int64_t planned_rows(int max_seq_len, int window, int sinks) {
+    return std::min<int64_t>(max_seq_len, (int64_t)window + sinks) + kTS;
+}
+
+// active[i]: clusters of 1 << i CTAs that the GPU holds at once.
+template <class C>
+static cudaError_t active_cfg(int (&active)[4]) {
+    auto kern = decode_window_kernel<C>;
+    cudaError_t e = smem_limit_once(kern, C::SMEM);
+    for (int i = 0; i < 4 && e == cudaSuccess; ++i)
+        active[i] = active_clusters(reinterpret_cast<const void *>(kern), C::SMEM, C::THREADS, 1 << i, &e);
+    return e;
+}
+
 template <class C>
 static cudaError_t plan_cfg(int B, int max_seq_len, int window, int sinks, WinPlan *plan, int most_splits = kMaxSplits,
                             double unsplit_below = 0.) {
-    auto kern = decode_window_kernel<C>;
-    cudaError_t e = smem_limit_once(kern, C::SMEM);
     int active[4];
-    for (int i = 0; i < 4 && e == cudaSuccess; ++i)
-        active[i] = active_clusters(reinterpret_cast<const void *>(kern), C::SMEM, C::THREADS, 1 << i, &e);
+    const cudaError_t e = active_cfg<C>(active);
     if (e == cudaSuccess)
-        *plan = window_plan(B, std::min<int64_t>(max_seq_len, (int64_t)window + sinks) + kTS, 2.0 * C::SLOT, C::Q8,
-                            most_splits, unsplit_below, active);
+        *plan = window_plan(B, planned_rows(max_seq_len, window, sinks), 2.0 * C::SLOT, C::Q8, most_splits,
+                            unsplit_below, active);
     return e;
 }
 
@@ -1257,27 +1269,34 @@ cudaError_t launch_window_fast(const DecodeArgs &a, void *ws, size_t ws_bytes) {
     return cudaErrorInvalidValue;
 }
 
-// Bytes of the states of split requests (0 for shapes that this kernel does not
-// cover or does not split).  Of the two group counts of a shape it takes the
-// larger need.
+// Bytes that the states of split requests need at most, in this call and in every
+// call with fewer requests or shorter lengths or windows (0 for shapes that this
+// kernel does not cover).  The number of splits that window_plan chooses rises and
+// falls with each size (16 heads, r = 48, window 2048: 364 KB for 16 requests, none
+// for 24), so this counts what bounds it: the clusters that the GPU holds at once,
+// kMaxSplits for a request, and its tiles.  About 3 MB at most.  Of the two group counts
+// of a shape it takes the larger need.
 size_t window_state_bytes(int B, int H, int r, int max_seq_len, int window, int sinks, int dtype) {
-    WinPlan p{1, 1, 1};
-    int S = 1;
-    auto add = [&](cudaError_t e) {
-        if (e != cudaSuccess) cudaGetLastError();  // (no device: sizing queries only)
-        else S = std::max(S, p.S);
+    int most = 0;  // clusters at once
+    auto add = [&](auto cfg) {
+        int active[4];
+        if (active_cfg<decltype(cfg)>(active) != cudaSuccess) cudaGetLastError();  // (no device: sizing queries only)
+        else most = std::max({most, active[0], active[1], active[2], active[3]});
     };
-#define X(h, rr)                                                                                              \
-    if (H == h && r == rr)                                                                                    \
-        add(dtype == LRKV_FP8_E4M3 ? plan_cfg<WinCfg<h, rr, true, 1>>(B, max_seq_len, window, sinks, &p)      \
-                                   : plan_cfg<WinCfg<h, rr, false, 1>>(B, max_seq_len, window, sinks, &p));
+#define X(h, rr)                                              \
+    if (H == h && r == rr) {                                  \
+        if (dtype == LRKV_FP8_E4M3) add(WinCfg<h, rr, true, 1>{}); \
+        else add(WinCfg<h, rr, false, 1>{});                  \
+    }
     if (dtype != LRKV_F32) { LRKV_FAST_SHAPES(X) }
 #undef X
 #define X(h, rr) \
-    if (H == h && r == rr) add(plan_cfg<WinCfg<h, rr, false, 2>>(B, max_seq_len, window, sinks, &p));
+    if (H == h && r == rr) add(WinCfg<h, rr, false, 2>{});
     if (dtype == LRKV_BF16) { LRKV_FAST_SHAPES_G2(X) }
 #undef X
-    return S > 1 ? (size_t)B * S * H * (128 + r + 2) * sizeof(float) : 0;
+    const int64_t tiles = (planned_rows(max_seq_len, window, sinks) + kTS - 1) / kTS;
+    const int64_t states = std::min<int64_t>(most, B * std::min<int64_t>(kMaxSplits, tiles));
+    return (size_t)states * H * (128 + r + 2) * sizeof(float);
 }
 
 }  // namespace lrkv

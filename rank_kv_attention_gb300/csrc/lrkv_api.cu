@@ -837,7 +837,7 @@ size_t lrkv_decode_window_workspace_bytes(int32_t B, int32_t H, int32_t d_h, int
                                           int32_t max_seq_len, int32_t window, int32_t sinks,
                                           int32_t dtype) {
     if (check_dims(H, d_h, r, dtype) || B < 1 || max_seq_len < 1 || window < 1 || sinks < 0) return 0;
-    // only the states of requests that the tensor-core kernel splits over clusters
+    // only the states of requests that the tensor-core kernel splits over clusters; never less for a larger call
     return d_h == 128 ? align256(window_state_bytes(B, H, r, max_seq_len, window, sinks, dtype)) : 0;
 }
 
@@ -875,8 +875,7 @@ int lrkv_decode_window(const void *q, const lrkv_cache_t *cache, const void *B_K
     a.out = out;
     a.status = dev_status;
     a.stream = (cudaStream_t)stream;
-    // (without a workspace the launcher says whether one is needed: the same plan
-    // is not made twice)
+    // (without a workspace the launcher says whether one is needed)
     if (workspace &&
         fast_decode_supported(cache->H, cache->d_h, cache->r, cache->page_size, cache->dtype, cache_groups(*cache)) &&
         workspace_bytes < window_state_bytes(B, cache->H, cache->r, max_seq_len, window, sinks, cache->dtype))
