@@ -345,6 +345,10 @@ def prefill(X, Q, cu_rows, start_pos, max_ctx, W_S_K, W_S_V, U_K, U_V, B_K, B_V,
 # current device, before the library is called.  A decode step takes less time
 # than a careful look at its arguments, so each function compares everything in
 # one expression and looks for the fault only when something differs.
+#
+# stream: the stream of the call (default: the current one).  Its inputs have to
+# be ready there, and a reader on another stream waits for it, as with any work
+# of two streams; what a call allocates for itself is in order on it.
 # ----------------------------------------------------------------------------
 _i32, _u8, _Tensor = torch.int32, torch.uint8, torch.Tensor
 
@@ -394,11 +398,18 @@ def _cache_arg(cache, dev):
                            s0, s1, s2, s3, nk, cache.norm_eps, G), act, H, d_h, r, G, code
 
 
-def _own_buffer(shape, dtype, dev, stream):
-    """A buffer made for a call on `stream`: not reused before the stream has passed it."""
-    t = torch.empty(shape, dtype=dtype, device=dev)
-    if stream is not None:
-        t.record_stream(stream)
+def _own_buffer(shape, dtype, dev, stream, scratch=False):
+    """A buffer made for a call on `stream`, from that stream's memory: work still
+    queued on the current stream cannot hold it.  Unless it is scratch, it is
+    not reused before the current stream, where the result is read, has passed
+    the point at which it is freed."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    here = torch.cuda.current_stream(dev)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=dev)
+    if not scratch:
+        t.record_stream(here)
     return t
 
 
@@ -456,9 +467,7 @@ def decode_window(q, cache: PagedCache, B_K, B_V, seq_lens, page_table, max_seq_
     desc, dt, H, d_h, r, G, code = _cache_arg(cache, dev)
     B, max_pages = _dim(q, "q", 3)[0], _dim(page_table, "page_table", 2)[1]
     if out is None:
-        out = torch.empty_like(q)
-        if stream is not None:
-            out.record_stream(stream)
+        out = torch.empty_like(q) if stream is None else _own_buffer(q.shape, q.dtype, q.device, stream)
     shape, base = (B, H, d_h), (H, d_h, r)
     if not (isinstance(B_K, _Tensor) and isinstance(B_V, _Tensor) and isinstance(seq_lens, _Tensor)
             and isinstance(out, _Tensor) and q.dtype is dt and B_K.dtype is dt and B_V.dtype is dt and out.dtype is dt
@@ -481,7 +490,7 @@ def decode_window(q, cache: PagedCache, B_K, B_V, seq_lens, page_table, max_seq_
            else L.lrkv_decode_window(*args, *_workspace(ws, dev), *tail))
     if err == _abi.LRKV_E_WORKSPACE and ws is None:  # (most calls need none)
         n = L.lrkv_decode_window_workspace_bytes(B, H, d_h, r, max_seq_len, window, sinks, code)
-        ws = _own_buffer((n,), _u8, q.device, stream)
+        ws = _own_buffer((n,), _u8, q.device, stream, scratch=True)
         err = L.lrkv_decode_window(*args, ws.data_ptr(), n, *tail)
     if err:
         _abi.check("lrkv_decode_window", err)
@@ -531,7 +540,7 @@ def prefill_window(X, Q, cu_rows, start_pos, max_ctx, W_S_K, W_S_V, U_K, U_V, B_
     err = L.lrkv_prefill_window(*args, *_workspace(ws, dev), *tail)
     if err == _abi.LRKV_E_WORKSPACE and ws is None:  # (few rows, or the per-row path)
         m = L.lrkv_prefill_workspace_bytes(B, n, H, d_h, r, max_ctx, code)
-        ws = _own_buffer((m,), _u8, X.device, stream)
+        ws = _own_buffer((m,), _u8, X.device, stream, scratch=True)
         err = L.lrkv_prefill_window(*args, ws.data_ptr(), m, *tail)
     if err:
         _abi.check("lrkv_prefill_window", err)

@@ -1,0 +1,96 @@
+"""What the binding of the windowed operators does around a library call, on
+host tensors and a library that only records what it is asked.  No call here
+touches a GPU."""
+import pytest
+import torch
+
+from rank_kv_attention_gb300 import _abi, api
+
+H, D_H, R, PAGE, B, MAX_PAGES, N, D = 4, 128, 16, 64, 2, 3, 7, 64
+
+
+class Stream:
+    cuda_stream = 77
+
+    def __init__(self, name):
+        self.name = name
+
+
+class Library:
+    """Entry points that record their arguments; a sizing query answers 512, a call without a workspace asks for one."""
+
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, name):
+        def entry(*args):
+            if name.endswith("_bytes"):
+                return 512
+            self.calls.append((name, args))
+            # (address and size of the workspace: fourth and third argument from the end)
+            return _abi.LRKV_E_WORKSPACE if name != "lrkv_page_plan" and args[-4] is None else _abi.LRKV_OK
+        return entry
+
+
+@pytest.fixture
+def lib(monkeypatch):
+    fake = Library()
+    monkeypatch.setattr(_abi, "lib", lambda: fake)
+    monkeypatch.setattr(api, "_device_of", lambda t, name: -1)  # (what host tensors answer)
+    return fake
+
+
+def bf(*shape):
+    return torch.zeros(shape, dtype=torch.bfloat16)
+
+
+def i32(*shape):
+    return torch.zeros(shape, dtype=torch.int32)
+
+
+def cache():
+    return api.PagedCache(bf(5, PAGE, D_H), bf(5, PAGE, D_H), bf(5, PAGE, H, R), bf(5, PAGE, H, R))
+
+
+def decode(longest=100, window=40, sinks=2, **kw):
+    return api.decode_window(bf(B, H, D_H), cache(), bf(H, D_H, R), bf(H, D_H, R), i32(B), i32(B, MAX_PAGES), longest, window,
+                             sinks, **kw)
+
+
+def prefill(longest=100, window=40, sinks=2, **kw):
+    return api.prefill_window(bf(N, D), bf(N, H, D_H), i32(B + 1), i32(B), longest, bf(D_H, D), bf(D_H, D), bf(H, R, D),
+                              bf(H, R, D), bf(H, D_H, R), bf(H, D_H, R), cache(), i32(B, MAX_PAGES), window, sinks, **kw)
+
+
+def plan(page=PAGE, rows=9, window=40, sinks=2, **kw):
+    return api.page_plan(i32(B), i32(B), i32(B, MAX_PAGES), i32(5), i32(1), page, rows, window=window, sinks=sinks, **kw)
+
+
+@pytest.mark.parametrize("call,made,outputs", [(decode, 2, 1), (prefill, 2, 1), (plan, 2, 2)])
+def test_buffers_of_a_call_come_from_its_stream(lib, monkeypatch, call, made, outputs):
+    """Whatever a call on another stream allocates (outputs and scratch) comes from that stream's memory, and outputs
+    wait for the current stream before they are reused."""
+    at, current, marked, empty = [], ["here"], [], torch.empty
+
+    class On:
+        def __init__(self, stream):
+            self.stream = stream
+
+        def __enter__(self):
+            current.append(self.stream.name)
+
+        def __exit__(self, *exc):
+            current.pop()
+
+    def recorded(*args, **kw):
+        at.append(current[-1])
+        return empty(*args, **kw)
+    monkeypatch.setattr(torch.cuda, "stream", On)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda dev=None: Stream(current[-1]))
+    monkeypatch.setattr(torch, "empty", recorded)
+    monkeypatch.setattr(torch, "empty_like", lambda t, **kw: recorded(t.shape, dtype=t.dtype))
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: marked.append(s.name))
+    call(stream=Stream("side"))
+    assert at == ["side"] * made
+    assert marked == ["here"] * outputs
+    assert all(args[-1] == Stream.cuda_stream for _, args in lib.calls)

@@ -1,10 +1,11 @@
 """The windowed operators in the calls that a server makes around the ordinary
 ones.  References and bounds are those of window_util."""
+import numpy as np
 import pytest
 import torch
 
-from gpu_util import DevDecode, host
-from test_window_gpu import decode_case
+from gpu_util import DevDecode, dev, host
+from test_window_gpu import decode_case, prefill_inputs, run_decode
 from window_util import check, decode_reference
 
 pytestmark = pytest.mark.gpu
@@ -41,3 +42,76 @@ def test_a_workspace_for_the_largest_batch_serves_the_smaller_ones(H, r, dtype):
             longest = max(lens[:B])
             got = L.decode_window(d.q[:B], d.cache, d.B_K, d.B_V, d.seq_lens[:B], d.page_table[:B], longest, window, sinks, ws=ws)
             check(host(got, case.act_dtype), ref[:B], bound[:B], f"B={B} window={window}")
+
+
+# ---------------------------------------------------------------------------
+# Streams of the caller's
+# ---------------------------------------------------------------------------
+def stream_calls(kind):
+    """A call on fixed inputs that gives the same outputs each time: call(stream=...) -> tensors."""
+    import rank_kv_attention_gb300 as L
+    if kind.startswith("decode"):
+        lens, window = ([9000], 8000) if kind == "decode split" else ([300, 5, 2000, 1100], 1024)
+        d = DevDecode(decode_case(lens, 16, 128, 48, seed=1))
+        return lambda **kw: [run_decode(d, window, 4, **kw)]
+    if kind.startswith("prefill"):
+        dtype, rows, starts = ("fp8" if kind == "prefill per row" else "bf16"), [100, 30], [70, 200]
+        w, pt, cache, X, Q = prefill_inputs(rows, starts, 64, 16, 128, 48, dtype, 90, 3, seed=6)
+        args = [dev(a, "bf16") for a in (X, Q)], [dev(np.array(a), "i32") for a in ([0, 100, 130], starts)]
+        weights = [dev(a, "bf16") for a in (w.W_S_K, w.W_S_V, w.U_K, w.U_V, w.B_K, w.B_V)]
+        table = dev(pt, "i32")
+        return lambda **kw: [L.prefill_window(*args[0], *args[1], 230, *weights, cache, table, 90, 3, **kw)]
+    lens, new = [dev(np.array(a), "i32") for a in ([500, 64, 7], [300, -1, 1])]
+    table = dev(np.arange(3 * 16).reshape(3, 16), "i32")
+    free, n_free = torch.arange(48, 100, dtype=torch.int32, device="cuda"), dev(np.array([52]), "i32")
+    pages = torch.cat([free, torch.full((48,), -1, dtype=torch.int32, device="cuda")])
+
+    def call(**kw):
+        p = L.page_plan(lens, new, table, pages, n_free, 64, 400, window=200, sinks=4, **kw)
+        return [p.seq_lens, p.cu_rows, p.positions, p.seq_ids, p.slots, p.n_free, p.free_pages[:48]]
+    return call
+
+
+@pytest.mark.parametrize("kind", ["decode", "decode split", "prefill", "prefill per row", "plan"])
+def test_outputs_on_another_stream(kind):
+    """A call on a stream of its own while memory just freed on the current stream has work queued on it, and outputs read
+    on the current stream and freed before that read has run: neither disturbs a result."""
+    call, side, here = stream_calls(kind), torch.cuda.Stream(), torch.cuda.current_stream()
+    want = [t.clone() for t in call()]
+    same = lambda got: all(torch.equal(a, b) for a, b in zip(got, want))
+    torch.cuda.synchronize()
+    for _ in range(3):
+        freed = [torch.empty_like(t) for t in want] + [torch.empty(1 << k, dtype=torch.uint8, device="cuda") for k in range(9, 24)]
+        torch.cuda._sleep(50_000_000)
+        for t in freed:
+            t.view(torch.uint8).fill_(0xEE)
+        del freed, t
+        got = call(stream=side)
+        torch.cuda.synchronize()
+        assert same(got)
+        got = call(stream=side)
+        here.wait_stream(side)
+        torch.cuda._sleep(50_000_000)
+        kept = [t.clone() for t in got]
+        shapes = [(t.shape, t.dtype) for t in got]
+        del got
+        with torch.cuda.stream(side):
+            over = [torch.empty(s, dtype=d, device="cuda").view(torch.uint8).fill_(0xEE) for s, d in shapes for _ in range(3)]
+        torch.cuda.synchronize()
+        assert same(kept)
+        del kept, over
+
+
+@pytest.mark.parametrize("kind", ["prefill", "prefill per row", "plan", "decode split"])
+def test_calls_at_once_on_several_streams(kind):
+    calls = [stream_calls(kind) for _ in range(4)]
+    want = [t.clone() for t in calls[0]()]
+    torch.cuda.synchronize()
+    sides = [torch.cuda.Stream() for _ in calls]
+    for _ in range(5):
+        got = []
+        for call, s in zip(calls, sides):
+            with torch.cuda.stream(s):
+                got.append(call())
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for g in got for a, b in zip(g, want))
