@@ -413,7 +413,10 @@ def _own_buffer(shape, dtype, dev, stream, scratch=False):
     return t
 
 
-def _too_large(**sizes):
+_LEAST, _MOST = -2 ** 31, 2 ** 31 - 1  # (a size past these would wrap on its way into the library)
+
+
+def _past_32_bits(**sizes):
     raise ValueError(", ".join(f"{k} = {v}" for k, v in sizes.items()) + ": sizes are 32-bit")
 
 
@@ -454,6 +457,8 @@ def _status(status, dev):
 
 def decode_window_workspace_bytes(B, H, d_h, r, max_seq_len, window, sinks=0, dtype=torch.bfloat16) -> int:
     """lrkv_decode_window_workspace_bytes: enough for this call and for every smaller one."""
+    if not (_LEAST <= max_seq_len <= _MOST and _LEAST <= window <= _MOST and _LEAST <= sinks <= _MOST):
+        _past_32_bits(max_seq_len=max_seq_len, window=window, sinks=sinks)
     return _abi.lib().lrkv_decode_window_workspace_bytes(B, H, d_h, r, max_seq_len, window, sinks, _DT[dtype])
 
 
@@ -480,8 +485,8 @@ def decode_window(q, cache: PagedCache, B_K, B_V, seq_lens, page_table, max_seq_
         _refuse(((q, "q", dt, shape), (B_K, "B_K", dt, base), (B_V, "B_V", dt, base), (seq_lens, "seq_lens", _i32, (B,)),
                  (page_table, "page_table", _i32, (B, max_pages)), (out, "out", dt, shape)), dev)
     L = _abi.lib()
-    if (max_seq_len | window | sinks) > 0x7fffffff:
-        _too_large(max_seq_len=max_seq_len, window=window, sinks=sinks)
+    if not (_LEAST <= max_seq_len <= _MOST and _LEAST <= window <= _MOST and _LEAST <= sinks <= _MOST):
+        _past_32_bits(max_seq_len=max_seq_len, window=window, sinks=sinks)
     args = (q.data_ptr(), desc, B_K.data_ptr(), B_V.data_ptr(), seq_lens.data_ptr(), page_table.data_ptr(), B,
             max_pages, max_seq_len, window, sinks, out.data_ptr())
     tail = (None if status is None else _status(status, dev),
@@ -530,13 +535,13 @@ def prefill_window(X, Q, cu_rows, start_pos, max_ctx, W_S_K, W_S_V, U_K, U_V, B_
                  (start_pos, "start_pos", _i32, (B,)), (W_S_K, "W_S_K", dt, shared), (W_S_V, "W_S_V", dt, shared),
                  (U_K, "U_K", dt, private), (U_V, "U_V", dt, private), (B_K, "B_K", dt, base), (B_V, "B_V", dt, base),
                  (page_table, "page_table", _i32, (B, max_pages)), (out, "out", dt, shape)), dev)
+    if not (_LEAST <= max_ctx <= _MOST and _LEAST <= window <= _MOST and _LEAST <= sinks <= _MOST):
+        _past_32_bits(max_ctx=max_ctx, window=window, sinks=sinks)
     L = _abi.lib()
     args = (X.data_ptr(), Q.data_ptr(), cu_rows.data_ptr(), start_pos.data_ptr(), B, n, max_ctx, d, W_S_K.data_ptr(),
             W_S_V.data_ptr(), U_K.data_ptr(), U_V.data_ptr(), B_K.data_ptr(), B_V.data_ptr(), desc,
             page_table.data_ptr(), max_pages, window, sinks, out.data_ptr())
     tail = _status(status, dev), _raw_stream(stream, dev)
-    if (max_ctx | window | sinks) > 0x7fffffff:
-        _too_large(max_ctx=max_ctx, window=window, sinks=sinks)
     err = L.lrkv_prefill_window(*args, *_workspace(ws, dev), *tail)
     if err == _abi.LRKV_E_WORKSPACE and ws is None:  # (few rows, or the per-row path)
         m = L.lrkv_prefill_workspace_bytes(B, n, H, d_h, r, max_ctx, code)
@@ -570,8 +575,9 @@ def page_plan(seq_lens, new_rows, page_table, free_pages, n_free, page_size, max
     max_pages = _dim(page_table, "page_table", 2)[1]
     if max_rows < 0:
         raise ValueError("max_rows must not be negative")
-    if (max_rows | page_size | window | sinks) > 0x7fffffff:
-        _too_large(max_rows=max_rows, page_size=page_size, window=window, sinks=sinks)
+    if not (max_rows <= _MOST and _LEAST <= page_size <= _MOST and _LEAST <= window <= _MOST
+            and _LEAST <= sinks <= _MOST):
+        _past_32_bits(max_rows=max_rows, page_size=page_size, window=window, sinks=sinks)
     if free_out is None:
         free_out = _own_buffer((num_pages,), _i32, seq_lens.device, stream)
     if not (isinstance(new_rows, _Tensor) and isinstance(n_free, _Tensor) and isinstance(free_out, _Tensor)

@@ -94,3 +94,34 @@ def test_buffers_of_a_call_come_from_its_stream(lib, monkeypatch, call, made, ou
     assert at == ["side"] * made
     assert marked == ["here"] * outputs
     assert all(args[-1] == Stream.cuda_stream for _, args in lib.calls)
+
+
+WRAPS = [2 ** 31, 2 ** 32 + 40, -(2 ** 31) - 1, -(2 ** 32) + 40, -(2 ** 33)]
+
+
+@pytest.mark.parametrize("size", WRAPS)
+@pytest.mark.parametrize("call,names", [(decode, ("longest", "window", "sinks")), (prefill, ("longest", "window", "sinks")),
+                                        (plan, ("page", "rows", "window", "sinks"))])
+def test_sizes_past_32_bits_are_refused(lib, call, names, size):
+    """A size that would wrap is refused, also a negative one (2^32 below a valid one) and also beside a negative one."""
+    for name in names:
+        with pytest.raises(ValueError):
+            call(**{name: size})
+        for other in set(names) - {name, "rows"}:
+            with pytest.raises(ValueError):
+                call(**{name: size, other: -1})
+        if call is decode:
+            sizes = dict(dict(longest=100, window=40, sinks=2), **{name: size})
+            with pytest.raises(ValueError):
+                api.decode_window_workspace_bytes(B, H, D_H, R, sizes["longest"], sizes["window"], sizes["sinks"])
+    assert not lib.calls
+
+
+def test_sizes_within_32_bits_reach_the_library(lib, monkeypatch):
+    """Refusing them is the library's part."""
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: 5, raising=False)
+    for size in (2 ** 31 - 1, -1, -(2 ** 31)):
+        decode(window=size, sinks=size, longest=size, ws=torch.empty(512, dtype=torch.uint8))
+        prefill(window=size, sinks=size, longest=size, ws=torch.empty(512, dtype=torch.uint8))
+        plan(window=size, sinks=size, page=size)
+    assert [len(lib.calls), {args[-1] for _, args in lib.calls}] == [9, {5}]
