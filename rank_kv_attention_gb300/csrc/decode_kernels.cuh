@@ -97,9 +97,15 @@ bool fast_decode_supported(int H, int d_h, int r, int page_size, int dtype, int 
 
 int fast_decode_grid(int H, int r);
 
-// Windowed decode of the shapes fast_decode_supported covers (a.window > 0), with
-// ws_bytes of scratch for the states of split requests.
-cudaError_t launch_window_fast(const DecodeArgs &a, void *ws, size_t ws_bytes);
+// Windowed decode of the shapes fast_decode_supported covers (a.window > 0): NC
+// clusters of CL CTAs, S of them per request, whose states go to scratch.  The
+// layout is chosen before anything is enqueued, within ws_bytes of scratch;
+// cudaErrorNotSupported: the call is worth a workspace and has none.
+struct WindowLayout {
+    int CL, NC, S;
+};
+cudaError_t window_layout(const DecodeArgs &a, const void *ws, size_t ws_bytes, WindowLayout *layout);
+cudaError_t launch_window_fast(const DecodeArgs &a, void *ws, const WindowLayout &layout);
 // The same for every other shape.
 cudaError_t launch_window_any(const DecodeArgs &a);
 size_t window_state_bytes(int B, int H, int r, int max_seq_len, int window, int sinks, int dtype);

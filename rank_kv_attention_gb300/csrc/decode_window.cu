@@ -1105,11 +1105,6 @@ static int active_clusters(const void *kern, int smem, int nthreads, int CL, cud
     return n;
 }
 
-// How a call is laid out: NC clusters of CL CTAs, S of them per request.
-struct WinPlan {
-    int CL, NC, S;
-};
-
 // The layout with the least estimated time.  A CTA takes a tile (tile_bytes) in
 // 12 ns per KB of bf16 rows, 34 ns per KB of 8-bit codes (0.67 us and 1.0 us for
 // 16 heads, r = 48); a segment costs a cluster fixed[] us besides (private
@@ -1127,13 +1122,13 @@ struct WinPlan {
 //     60.8, 57.1 (a combine taken as 2 us: 12 requests, window 2048: 25.1 for 23.3)
 // `rows`: visible rows of the longest request; active[i]: clusters of 1 << i CTAs
 // that the GPU holds at once.
-static WinPlan window_plan(int B, int64_t rows, double tile_bytes, bool q8, int most_splits, double unsplit_below,
-                           const int (&active)[4]) {
+static WindowLayout window_plan(int B, int64_t rows, double tile_bytes, bool q8, int most_splits, double unsplit_below,
+                                const int (&active)[4]) {
     static const double fixed[4] = {17., 12., 9., 8.}, combine = 4.;
     const int64_t tiles = (rows + kTS - 1) / kTS;
     const double tile_us = tile_bytes / 1024. * (q8 ? 0.034 : 0.012);
     const double hbm_us = (double)B * tiles * tile_bytes / 6.5e6;
-    WinPlan best{1, 1, 1};
+    WindowLayout best{1, 1, 1};
     double least = 1e300;
     auto consider = [&](int i, int64_t S) {
         const int64_t CL = 1 << i, used = std::min<int64_t>((int64_t)B * S, active[i]);
@@ -1176,7 +1171,7 @@ static cudaError_t active_cfg(int (&active)[4]) {
 }
 
 template <class C>
-static cudaError_t plan_cfg(int B, int max_seq_len, int window, int sinks, WinPlan *plan, int most_splits = kMaxSplits,
+static cudaError_t plan_cfg(int B, int max_seq_len, int window, int sinks, WindowLayout *plan, int most_splits = kMaxSplits,
                             double unsplit_below = 0.) {
     int active[4];
     const cudaError_t e = active_cfg<C>(active);
@@ -1186,9 +1181,21 @@ static cudaError_t plan_cfg(int B, int max_seq_len, int window, int sinks, WinPl
     return e;
 }
 
-template <int H, int R, bool Q8, int NGRP>
-static cudaError_t launch_cfg(const DecodeArgs &a, void *ws, size_t ws_bytes) {
-    using C = WinCfg<H, R, Q8, NGRP>;
+// The layout of a call within its scratch.
+template <class C>
+static cudaError_t layout_cfg(const DecodeArgs &a, const void *ws, size_t ws_bytes, WindowLayout *plan) {
+    cudaError_t e = plan_cfg<C>(a.B, a.max_seq_len, a.window, a.sinks, plan, kMaxSplits, ws ? 0. : 25.);
+    if (e != cudaSuccess) return e;
+    if (plan->S > 1 && !ws) return cudaErrorNotSupported;
+    if (plan->S > 1 && ws_bytes < (size_t)a.B * plan->S * C::H * (2 + C::W) * sizeof(float))  // (a prefill's workspace)
+        e = plan_cfg<C>(a.B, a.max_seq_len, a.window, a.sinks, plan, 1);
+    return e;
+}
+
+template <class C>
+static cudaError_t launch_cfg(const DecodeArgs &a, void *ws, const WindowLayout &plan) {
+    constexpr int H = C::H, R = C::R, NGRP = C::NGRP;
+    constexpr bool Q8 = C::Q8;
     const auto &c = a.cache;
     const int64_t pool_rows = (int64_t)c.num_pages * c.page_size;
     WinMaps maps;
@@ -1198,16 +1205,7 @@ static cudaError_t launch_cfg(const DecodeArgs &a, void *ws, size_t ws_bytes) {
         !make_map(&maps.rv, c.R_V, pool_rows, H * R, C::EB, 0, false, kTS) ||
         (c.N_K && !make_row_map(&maps.nk, c.N_K, pool_rows, H, 2, kTS)))
         return cudaErrorInvalidValue;
-    WinPlan plan;
-    cudaError_t e = plan_cfg<C>(a.B, a.max_seq_len, a.window, a.sinks, &plan, kMaxSplits, ws ? 0. : 25.);
-    if (e != cudaSuccess) return e;
-    size_t states = (size_t)a.B * plan.S * H;
-    if (plan.S > 1 && !ws) return cudaErrorNotSupported;
-    if (plan.S > 1 && ws_bytes < states * (2 + C::W) * sizeof(float)) {  // (a prefill's workspace)
-        e = plan_cfg<C>(a.B, a.max_seq_len, a.window, a.sinks, &plan, 1);
-        if (e != cudaSuccess) return e;
-        states = (size_t)a.B * H;
-    }
+    const size_t states = (size_t)a.B * plan.S * H;
     WinParams P;
     P.q = static_cast<const __nv_bfloat16 *>(a.q);
     P.B_K = static_cast<const __nv_bfloat16 *>(a.B_K);
@@ -1243,30 +1241,38 @@ static cudaError_t launch_cfg(const DecodeArgs &a, void *ws, size_t ws_bytes) {
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    e = cudaLaunchKernelEx(&cfg, decode_window_kernel<C>, maps, P);
+    // (the kernel's shared-memory limit was set for the layout)
+    cudaError_t e = cudaLaunchKernelEx(&cfg, decode_window_kernel<C>, maps, P);
     if (e == cudaSuccess && plan.S > 1)
         e = launch_pdl(window_combine_kernel, dim3(H, a.B), dim3(128), 0, a.stream, P.B_V, (const float *)P.ml,
                        (const float *)P.acc, H, R, plan.S, P.out);
     return e;
 }
 
-cudaError_t launch_window_fast(const DecodeArgs &a, void *ws, size_t ws_bytes) {
-    const int H = a.cache.H, r = a.cache.r;
-    const bool q8 = a.cache.dtype == LRKV_FP8_E4M3;
-    if (cache_groups(a.cache) == 2) {
+// f(configuration) of a cache's shape.
+template <typename F>
+static cudaError_t with_cfg(const lrkv_cache_t &c, F &&f) {
+    if (cache_groups(c) == 2) {
 #define X(h, rr) \
-        if (H == h && r == rr) return launch_cfg<h, rr, false, 2>(a, ws, ws_bytes);
+        if (c.H == h && c.r == rr) return f(WinCfg<h, rr, false, 2>{});
         LRKV_FAST_SHAPES_G2(X)
 #undef X
         return cudaErrorInvalidValue;
     }
-#define X(h, rr)                                                                      \
-    if (H == h && r == rr)                                                            \
-        return q8 ? launch_cfg<h, rr, true, 1>(a, ws, ws_bytes)            \
-                  : launch_cfg<h, rr, false, 1>(a, ws, ws_bytes);
+    const bool q8 = c.dtype == LRKV_FP8_E4M3;
+#define X(h, rr)                                                                                            \
+    if (c.H == h && c.r == rr) return q8 ? f(WinCfg<h, rr, true, 1>{}) : f(WinCfg<h, rr, false, 1>{});
     LRKV_FAST_SHAPES(X)
 #undef X
     return cudaErrorInvalidValue;
+}
+
+cudaError_t window_layout(const DecodeArgs &a, const void *ws, size_t ws_bytes, WindowLayout *layout) {
+    return with_cfg(a.cache, [&](auto cfg) { return layout_cfg<decltype(cfg)>(a, ws, ws_bytes, layout); });
+}
+
+cudaError_t launch_window_fast(const DecodeArgs &a, void *ws, const WindowLayout &layout) {
+    return with_cfg(a.cache, [&](auto cfg) { return launch_cfg<decltype(cfg)>(a, ws, layout); });
 }
 
 // Bytes that the states of split requests need at most, in this call and in every

@@ -141,13 +141,18 @@ static int window_bound(int max_seq_len, int window, int sinks) {
 static int run_decode(const DecodeArgs &a, void *workspace, size_t ws_bytes) {
     const auto &c = a.cache;
     if (a.window) {
+        const bool fast = fast_decode_supported(c.H, c.d_h, c.r, c.page_size, c.dtype, cache_groups(c));
+        WindowLayout layout;
+        if (fast) {
+            const cudaError_t e = window_layout(a, workspace, ws_bytes, &layout);
+            if (e == cudaErrorNotSupported) return LRKV_E_WORKSPACE;  // requests to split, nothing enqueued
+            if (e != cudaSuccess) return cuda_fail(e);
+        }
         prof_before(LRKV_PROFILE_ATTENTION, a.stream);
-        const cudaError_t e = fast_decode_supported(c.H, c.d_h, c.r, c.page_size, c.dtype, cache_groups(c))
-                                  ? launch_window_fast(a, workspace, ws_bytes)
-                                  : launch_window_any(a);
+        const cudaError_t e = fast ? launch_window_fast(a, workspace, layout) : launch_window_any(a);
+        if (e != cudaSuccess) return cuda_fail(e);
         prof_after(LRKV_PROFILE_ATTENTION, a.stream);
-        if (e == cudaErrorNotSupported && !workspace) return LRKV_E_WORKSPACE;  // requests to split, nothing enqueued
-        return e == cudaSuccess ? LRKV_OK : cuda_fail(e);
+        return LRKV_OK;
     }
     DecodeGeom geo = decode_geom(a.B, a.max_seq_len);
     DecodeWs ws = decode_ws_layout(workspace, a.B, c.H, c.d_h, c.r, geo.G_ws);
@@ -875,7 +880,7 @@ int lrkv_decode_window(const void *q, const lrkv_cache_t *cache, const void *B_K
     a.out = out;
     a.status = dev_status;
     a.stream = (cudaStream_t)stream;
-    // (without a workspace the launcher says whether one is needed)
+    // (without a workspace the layout says whether one is needed)
     if (workspace &&
         fast_decode_supported(cache->H, cache->d_h, cache->r, cache->page_size, cache->dtype, cache_groups(*cache)) &&
         workspace_bytes < window_state_bytes(B, cache->H, cache->r, max_seq_len, window, sinks, cache->dtype))

@@ -1,5 +1,7 @@
 """The windowed operators in the calls that a server makes around the ordinary
 ones.  References and bounds are those of window_util."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -115,3 +117,33 @@ def test_calls_at_once_on_several_streams(kind):
                 got.append(call())
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for g in got for a, b in zip(g, want))
+
+
+# ---------------------------------------------------------------------------
+# The benchmark's profile
+# ---------------------------------------------------------------------------
+def test_profile_counts_a_split_call_once():
+    """A call that first asks for a workspace is one launch of the attention kernel, not two."""
+    import rank_kv_attention_gb300 as L
+    lib = L.lib()
+
+    def launches():
+        ms, n = ctypes.c_double(), ctypes.c_int32()
+        assert lib.lrkv_profile_read(0, ctypes.byref(ms), ctypes.byref(n)) == L.LRKV_OK
+        return n.value, ms.value
+
+    d = DevDecode(decode_case([9000], 16, 128, 48))
+    desc = d.cache.desc()
+    out = torch.empty_like(d.q)
+    bare = lambda: lib.lrkv_decode_window(
+        d.q.data_ptr(), ctypes.byref(desc), d.B_K.data_ptr(), d.B_V.data_ptr(), d.seq_lens.data_ptr(), d.page_table.data_ptr(),
+        1, d.page_table.shape[1], 9000, 8000, 4, out.data_ptr(), None, 0, None, torch.cuda.current_stream().cuda_stream)
+    assert bare() == L.LRKV_E_WORKSPACE
+    assert lib.lrkv_profile_enable(1) == L.LRKV_OK
+    try:
+        assert bare() == L.LRKV_E_WORKSPACE and launches() == (0, 0.0)
+        run_decode(d, 8000, 4)
+        n, ms = launches()
+        assert n == 1 and ms > 0
+    finally:
+        lib.lrkv_profile_enable(0)
