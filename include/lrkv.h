@@ -347,7 +347,8 @@ LRKV_API size_t lrkv_prefill_workspace_bytes(int32_t B, int32_t n, int32_t H, in
  *   X   [n, d]    Q, out [n, H, d_h]
  *   cu_rows [B+1] int32, device (cu_rows[0] = 0, nondecreasing, cu_rows[B] = n)
  *   start_pos [B] int32, device
- *   max_ctx   host upper bound of start_pos[b] + rows of b (<= max_pages*page_size)
+ *   max_ctx   host upper bound of start_pos[b] + rows of b (<= max_pages*page_size);
+ *             n * max_ctx is below 2^30 (LRKV_E_SHAPE beyond)
  *   weights as lrkv_append; B_K, B_V as lrkv_decode.
  *   workspace >= lrkv_prefill_workspace_bytes(...) bytes, 256-byte aligned.
  */
@@ -422,7 +423,10 @@ LRKV_API int lrkv_key_norms(const int32_t *positions, const int32_t *seq_ids, in
  * lrkv_prefill_window takes the arguments of lrkv_prefill and its workspace
  * (lrkv_prefill_workspace_bytes; a call of more than 64 rows that
  * LRKV_PREFILL_TILED covers needs none in most shapes: with workspace NULL a call
- * that does returns LRKV_E_WORKSPACE and has enqueued nothing); rows 0 .. start_pos[b]-1 that a new row can
+ * that does returns LRKV_E_WORKSPACE and has enqueued nothing).  Its limits are
+ * its own: n is below 2^30 (fp32 caches and shapes without a tensor-core append,
+ * which also wants d and H r in whole tiles: at most 65535 * 32), and n * max_ctx
+ * is not bounded.  Rows 0 .. start_pos[b]-1 that a new row can
  * see must be in the cache before the call (a history that another request of
  * the call appends does not count: its tiles may be read beside the append).
  * Rows that some new row of a request sees must hold

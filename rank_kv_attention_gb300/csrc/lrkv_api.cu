@@ -754,7 +754,13 @@ static int prefill_impl(const void *X, const void *Q, const int32_t *cu_rows,
     if (max_ctx < 1) return LRKV_E_SHAPE;
     if ((int64_t)max_ctx > (int64_t)max_pages * cache->page_size) return LRKV_E_BOUNDS;
     if (n == 0) return LRKV_OK;
-    if ((int64_t)n * max_ctx > INT32_MAX / 2) return LRKV_E_SHAPE;
+    // The full history's per-row path counts the rows of all queries in 32 bits.
+    // Through a window no kernel counts visible rows of more than one query.
+    if (!window && (int64_t)n * max_ctx > INT32_MAX / 2) return LRKV_E_SHAPE;
+    if (n > INT32_MAX / 2) return LRKV_E_SHAPE;
+    // (a launch of the any-shape append holds that many rows)
+    if (window && n > 65535 * 32 && (cache->dtype == LRKV_F32 || !tc_append_supported(n, d, cache->d_h, cache->H, cache->r)))
+        return LRKV_E_SHAPE;
     if (!Q || !B_K || !B_V || !out || !aligned16(Q) || !aligned16(B_K) || !aligned16(B_V) ||
         !aligned16(out))
         return LRKV_E_INVALID_ARG;

@@ -1,6 +1,8 @@
 """What the binding of the windowed operators does around a library call, on
 host tensors and a library that only records what it is asked.  No call here
 touches a GPU."""
+import ctypes
+
 import pytest
 import torch
 
@@ -125,3 +127,22 @@ def test_sizes_within_32_bits_reach_the_library(lib, monkeypatch):
         prefill(window=size, sinks=size, longest=size, ws=torch.empty(512, dtype=torch.uint8))
         plan(window=size, sinks=size, page=size)
     assert [len(lib.calls), {args[-1] for _, args in lib.calls}] == [9, {5}]
+
+
+def test_prefill_is_bounded_by_its_window():
+    """Rows times context may pass 2^30 where each row sees a window of it; the full prefill counts those rows in 32 bits."""
+    from rank_kv_attention_gb300 import build
+    build.build()
+    real, desc = _abi.lib(), ctypes.byref(_abi.CacheDesc(16, 16, 16, 16, 40, 64, 4, 32, 8, _abi.LRKV_F32))
+
+    def call(n, ctx, window):
+        head = (16, 16, 16, 16, 2, n, ctx, 64, 16, 16, 16, 16, 16, 16, desc, 16, 1 << 20)
+        if window:
+            return real.lrkv_prefill_window(*head, window, 4, 16, None, 0, None, None)
+        return real.lrkv_prefill(*head, 16, None, 0, None, None)
+    # (an fp32 call always needs a workspace: a call that passes its checks asks for it, and nothing is launched)
+    for n, ctx in ((8200, 139272), (65535 * 32, 1 << 26), (1, 1 << 26)):
+        assert call(n, ctx, 1024) == _abi.LRKV_E_WORKSPACE, (n, ctx)
+    for n, ctx in ((65535 * 32 + 1, 64), (2 ** 30, 64), (2 ** 31 - 1, 1)):
+        assert call(n, ctx, 1024) == _abi.LRKV_E_SHAPE, (n, ctx)
+    assert call(8200, 139272, 0) == _abi.LRKV_E_SHAPE and call(8200, 64, 0) == _abi.LRKV_E_WORKSPACE

@@ -6,8 +6,9 @@ import numpy as np
 import pytest
 import torch
 
+import lrkv_inputs as I
 from gpu_util import DevDecode, dev, host
-from test_window_gpu import decode_case, prefill_inputs, run_decode
+from test_window_gpu import check_prefill, decode_case, prefill_inputs, run_decode, run_prefill
 from window_util import check, decode_reference
 
 pytestmark = pytest.mark.gpu
@@ -147,3 +148,21 @@ def test_profile_counts_a_split_call_once():
         assert n == 1 and ms > 0
     finally:
         lib.lrkv_profile_enable(0)
+
+
+# ---------------------------------------------------------------------------
+# Contexts far longer than the window
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("H,d_h,r,dtype,n", [(2, 128, 16, "bf16", 8300), (2, 64, 8, "fp8", 8300), (2, 32, 4, "f32", 8300),
+                                             (2, 128, 16, "bf16", 61)])
+def test_prefill_on_a_long_context(H, d_h, r, dtype, n):
+    """New rows at positions about 2^17: rows times context pass 2^30 where n is 8300, rows times visible rows stay small.
+    All but the last pages of the table are -1."""
+    start, window, sinks = 131000, 90, 3
+    w, pt, cache, X, Q = prefill_inputs([n], [start], 64, H, d_h, r, dtype, window, sinks, seed=n)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = run_prefill(w, pt, cache, X, Q, [n], [start], window, sinks, I.act_dtype(dtype), status=status)
+    tiled = dtype == "bf16" and d_h == 128
+    check_prefill(out, cache, w, pt, X, Q, [n], [start], window, sinks, dtype, tiled,
+                  sample=[0, 1, 60, 63, 64, 88, 89, 90, 127, 128, 4000, 8191, 8192, 8299])
+    assert int(status.item()) == 0
