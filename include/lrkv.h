@@ -427,8 +427,8 @@ LRKV_API int lrkv_key_norms(const int32_t *positions, const int32_t *seq_ids, in
  * its own: n is below 2^30 (fp32 caches and shapes without a tensor-core append,
  * which also wants d and H r in whole tiles: at most 65535 * 32), and n * max_ctx
  * is not bounded.  Rows 0 .. start_pos[b]-1 that a new row can
- * see must be in the cache before the call (a history that another request of
- * the call appends does not count: its tiles may be read beside the append).
+ * see must be in the cache before the call, or be new rows of another request of
+ * the call (a shared prefix), as for lrkv_prefill.
  * Rows that some new row of a request sees must hold
  * finite values: the tiled kernel gives a row of a tile that another row of it
  * does not see the weight 0, and 0 times an infinity or NaN is NaN.

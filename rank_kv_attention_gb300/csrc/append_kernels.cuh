@@ -117,7 +117,7 @@ struct PrefillTcArgs {
     int window = 0, sinks = 0;  // lrkv_prefill_window; window 0: the whole history
     // The predecessor in the stream is the same call's append, which let this
     // kernel launch after passing its own wait and finishes within a few
-    // milliseconds: only the copies of tiles that hold new rows wait for it.
+    // milliseconds: only the copies of tiles that may hold new rows wait for it.
     bool early = false;
 };
 int launch_prefill_tc(const PrefillTcArgs &p);

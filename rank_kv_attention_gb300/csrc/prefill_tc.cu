@@ -56,10 +56,13 @@
 // behind the weights or 16 softmax warps changed the call by -3 to +4%.
 //
 // `early` (WIN, when the append before it leaves SMs idle): a CTA starts beside
-// the call's append and works through the tiles that lie in the history; the
-// copy of the first tile with a new row waits for the append.  512 rows on a
-// history of 3001, window 1024, 16 heads, r = 48: the whole call took 39.2 us with
-// every CTA waiting at its start, 28.3 like this.
+// the call's append, and the copy of the first tile that may hold a new row waits
+// for the append.  With one request those are its own rows, and the tiles before
+// them are worked through meanwhile: 512 rows on a history of 3001, window 1024, 16
+// heads, r = 48, take 39.2 us with every CTA waiting at its start, 26.9 like this.
+// Of several requests one may see a history that another's new rows make (a prefix
+// that they share), so every copy of keys and values waits; what goes before (the
+// queries, p) still overlaps.
 #include <algorithm>
 
 #include "append_kernels.cuh"
@@ -288,7 +291,9 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
         tma_load_2d(sb + 2 * PF_BLK, m_r, h * a.r, y0, full);
         tma_load_2d(sb + 2 * PF_BLK + PF_BOX, m_r, h * a.r, y1, full);
     };
-    const int first_new = p0 - tq * PF_BM;  // position of the request's first new row
+    // first position that may hold a new row: the request's own, or, of several
+    // requests, any (a history may be another's new rows)
+    const int first_new = a.B > 1 ? 0 : p0 - tq * PF_BM;
     // whether the append has to be waited for before tile kt is copied
     auto needs_append = [&](int kt) { return WIN && a.early && keys.base(kt) + PF_BN > first_new; };
     int n_iss = 0;  // copy threads: tiles issued

@@ -166,3 +166,24 @@ def test_prefill_on_a_long_context(H, d_h, r, dtype, n):
     check_prefill(out, cache, w, pt, X, Q, [n], [start], window, sinks, dtype, tiled,
                   sample=[0, 1, 60, 63, 64, 88, 89, 90, 127, 128, 4000, 8191, 8192, 8299])
     assert int(status.item()) == 0
+
+
+# ---------------------------------------------------------------------------
+# A prefix that requests of one call share
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("rows,starts,d", [([128, 40, 30], [0, 128, 64], 2048), ([64, 100, 400], [256, 320, 320], 2048),
+                                           ([30, 20, 1], [34, 64, 64], 2048)])
+def test_prefill_shares_a_prefix_within_the_call(rows, starts, d):
+    """The histories of two requests are whole pages of another's new rows, in calls so small that the append leaves SMs
+    idle.  The cache holds NaN until the append has written it."""
+    window, sinks, ps = 200, 5, 64
+    w, pt, cache, X, Q = prefill_inputs(rows, starts, d, 16, 128, 48, "bf16", 10 ** 6, 0, seed=len(rows) + rows[0])
+    for b in (1, 2):
+        pt[b, :starts[b] // ps] = pt[0, :starts[b] // ps]
+    pools = (cache.S_K, cache.S_V, cache.R_K, cache.R_V)
+    before = [p.clone() for p in pools]
+    for _ in range(5):
+        for p, x in zip(pools, before):
+            p.copy_(x)
+        out = run_prefill(w, pt, cache, X, Q, rows, starts, window, sinks, "bf16")
+        check_prefill(out, cache, w, pt, X, Q, rows, starts, window, sinks, "bf16", True, sample=[0, 1, 19, 29, 39, 63, 99, 399])
