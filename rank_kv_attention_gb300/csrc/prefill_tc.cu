@@ -510,6 +510,9 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
             tc_fence_after();
             uint32_t v[32], pk[32];
             tmem_ld32(lane_base + PF_COL_S + 128, v);
+            // a query with a NaN makes all of p and of its scores NaN, which the maxima
+            // pass over: its sum starts as one
+            if (WIN && __uint_as_float(v[0]) != __uint_as_float(v[0])) l = __uint_as_float(v[0]);
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
                 uint32_t hi, lo;
@@ -653,7 +656,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
         if (ok)
             ok = __all_sync(0xffffffffu, mbar_wait(&bar.pv_done[(nkt - 1) & 1], ((nkt - 1) >> 1) & 1));
         const float lt = l + lsum[(hf ^ 1) * PF_BM + t];
-        const float inv_l = lt > 0.f ? 1.f / lt : 0.f;
+        const float inv_l = lt > 0.f || (WIN && lt != 0.f) ? 1.f / lt : 0.f;  // (NaN stays NaN)
         if (ok) {
             // (O_R / l) in bf16 halves over p's columns: half 0 the high part, half 1 the low part
             tc_fence_after();

@@ -187,3 +187,29 @@ def test_prefill_shares_a_prefix_within_the_call(rows, starts, d):
             p.copy_(x)
         out = run_prefill(w, pt, cache, X, Q, rows, starts, window, sinks, "bf16")
         check_prefill(out, cache, w, pt, X, Q, rows, starts, window, sinks, "bf16", True, sample=[0, 1, 19, 29, 39, 63, 99, 399])
+
+
+# ---------------------------------------------------------------------------
+# NaN queries
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("n", [1, 40, 130, 300])
+def test_prefill_nan_queries_reach_the_output(n):
+    """A query with a NaN has no answer: its row is NaN in the heads it touches, as in the single-token form; other rows
+    and heads are unchanged."""
+    import rank_kv_attention_gb300 as L
+    rows, starts, window, sinks, H = [n, 3], [200, 0], 90, 4, 2
+    w, pt, cache, X, Q = prefill_inputs(rows, starts, 64, H, 128, 16, "bf16", window, sinks, seed=n)
+    clean = run_prefill(w, pt, cache, X, Q, rows, starts, window, sinks, "bf16")
+    hit = sorted({0, n // 2, n - 1, n + 1})
+    for i in hit:
+        Q[i, 1, 7] = I.BF16_NAN_BITS
+    got = run_prefill(w, pt, cache, X, Q, rows, starts, window, sinks, "bf16")
+    want = clean.clone()
+    want[hit, 1] = float("nan")
+    assert torch.equal(torch.isnan(got), torch.isnan(want))
+    assert torch.equal(torch.nan_to_num(got), torch.nan_to_num(want))
+    # the same query as a single token
+    last = torch.tensor([starts[0] + n], dtype=torch.int32, device="cuda")
+    one = L.decode_window(dev(Q[n - 1:n], "bf16"), cache, dev(w.B_K, "bf16"), dev(w.B_V, "bf16"), last, dev(pt[:1], "i32"),
+                          int(last), window, sinks)
+    assert torch.equal(torch.isnan(one[0]), torch.isnan(got[n - 1]))
