@@ -213,3 +213,36 @@ def test_prefill_nan_queries_reach_the_output(n):
     one = L.decode_window(dev(Q[n - 1:n], "bf16"), cache, dev(w.B_K, "bf16"), dev(w.B_V, "bf16"), last, dev(pt[:1], "i32"),
                           int(last), window, sinks)
     assert torch.equal(torch.isnan(one[0]), torch.isnan(got[n - 1]))
+
+
+# ---------------------------------------------------------------------------
+# Many requests
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("H,d_h,r,dtype", [(16, 128, 32, "bf16"), (16, 128, 32, "fp8"), (3, 32, 8, "f32")])
+def test_decode_of_many_requests(H, d_h, r, dtype):
+    """Far more requests than the GPU holds clusters, some empty, some of one row."""
+    rng = np.random.default_rng(1)
+    lens = rng.integers(0, 150, size=1100)
+    lens[::7] = 1
+    window, sinks = 70, 3
+    case = decode_case(lens, H, d_h, r, dtype, seed=2)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = host(run_decode(DevDecode(case), window, sinks, status=status), case.act_dtype)
+    check(got, *decode_reference(case, window, sinks))
+    import rank_kv_attention_gb300 as L
+    assert int(status.item()) == L.LRKV_STATUS_BAD_SEQLEN  # (the empty ones)
+
+
+@pytest.mark.parametrize("dtype,most", [("bf16", 300), ("bf16", 1300), ("fp8", 90)])
+def test_prefill_of_a_mixed_step(dtype, most):
+    """One prompt's chunk beside single tokens, each request on a history of its own."""
+    rng = np.random.default_rng(most)
+    rows, starts = [1] * 60, [int(x) for x in rng.integers(0, 500, size=60)]
+    rows[23], rows[41] = most, 5
+    window, sinks = 130, 4
+    w, pt, cache, X, Q = prefill_inputs(rows, starts, 64, 4, 128, 16, dtype, window, sinks, seed=most)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = run_prefill(w, pt, cache, X, Q, rows, starts, window, sinks, "bf16", status=status)
+    check_prefill(out, cache, w, pt, X, Q, rows, starts, window, sinks, dtype, dtype == "bf16",
+                  sample=[0, 1, 4, 63, 64, 127, 128, 129, 255, 299, 1023, 1299])
+    assert int(status.item()) == 0
