@@ -36,7 +36,7 @@ __device__ __forceinline__ uint32_t f16x2_hi(uint32_t w) {
 }
 
 // A fragments of two value m-tiles from the 32-bit words of rows 2tq, 2tq+1,
-// 2tq+8, 2tq+9 (see the layout note above); MASK: zero invalid rows.
+// 2tq+8, 2tq+9 (the layout of 8-bit tiles is described in decode_fast.cu); MASK: zero invalid rows.
 template <bool MASK>
 __device__ __forceinline__ void q8_pair_frags(uint32_t w0, uint32_t w1, uint32_t w8, uint32_t w9,
                                               uint32_t m01, uint32_t m89, uint32_t (&a)[4],

@@ -16,6 +16,11 @@
 // flight.  Every head reads the shared rows again (out of L2).  6 fp32 requests of
 // 8 heads, window 500 (2.9 MB): 10.5 us in a graph, where the generic split kernel and
 // its combine took 54 us a call and this takes 20, most of it the call's.
+// 16 requests, window 1024, d_h = 128, r = 48: 47 us with 8 heads in bf16 (5.0 at the
+// copy bandwidth), 184 with 40 heads (19.9), 106 with 16 heads in fp32 (17.4).  Far
+// from the floor: every head's cluster reads the shared rows, and at d_h = 128 a lane
+// runs the form for 256 columns with half of its slots empty, at 236 to 255 registers
+// (fp32 with d_h and r above 64 spills 696 bytes).
 #include <algorithm>
 
 #include "decode_kernels.cuh"

@@ -808,7 +808,9 @@ static int prefill_impl(const void *X, const void *Q, const int32_t *cu_rows,
     }
     if (bare) return cuda_fail(cudaErrorInvalidValue);  // (not reached: the attention fits)
     // Other shapes: row i is a one-query decode over its request's rows
-    // 0..pos_i, reading the page-table row of its request.
+    // 0..pos_i, reading the page-table row of its request.  8 prompts of 2048 rows
+    // through a window of 1024 (0.27 ms tiled): 8-bit cache 6.9 ms, key norms 5.8,
+    // pages of 32 rows 5.3; each row streams its own window.
     DecodeArgs a;
     a.q = Q;
     a.cache = *cache;
