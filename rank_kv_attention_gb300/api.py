@@ -1,8 +1,10 @@
 """PyTorch-facing binding of the LRKV C ABI.
 
 Every function here only checks tensor properties, builds the C arguments
-and calls the library on the current CUDA stream; all arithmetic runs in the
-library's CUDA kernels.  Tensors must be contiguous CUDA tensors of the
+and calls the library on the current CUDA stream, or on `stream`: inputs have
+to be ready there, a reader on another stream waits for it as with any work of
+two streams, and what a call allocates for itself is in order on it.  All
+arithmetic runs in the library's CUDA kernels.  Tensors must be contiguous CUDA tensors of the
 cache's dtype (torch.bfloat16 or torch.float32); integer metadata is int32.
 """
 from __future__ import annotations
@@ -125,6 +127,26 @@ def workspace(nbytes, device="cuda") -> torch.Tensor:
     return torch.empty(max(int(nbytes), 1), dtype=torch.uint8, device=device)
 
 
+def _own_buffer(shape, dtype, dev, stream, scratch=False):
+    """A buffer made for a call on `stream`, from that stream's memory: work still
+    queued on the current stream cannot hold it.  Unless it is scratch, it is
+    not reused before the current stream, where the result is read, has passed
+    the point at which it is freed."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    here = torch.cuda.current_stream(dev)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=dev)
+    if not scratch:
+        t.record_stream(here)
+    return t
+
+
+def _scratch(nbytes, dev, stream):
+    """A workspace made for a call on `stream`."""
+    return _own_buffer((max(int(nbytes), 1),), torch.uint8, dev, stream, scratch=True)
+
+
 def append(X, positions, seq_ids, W_S_K, W_S_V, U_K, U_V, cache: PagedCache, page_table,
            status=None, stream=None):
     """lrkv_append: project rows X and store them at (seq_ids, positions)."""
@@ -155,11 +177,11 @@ def decode(q, cache: PagedCache, B_K, B_V, seq_lens, page_table, max_seq_len, ou
     B, H, d_h = q.shape
     r = cache.R_K.shape[3]
     if out is None:
-        out = torch.empty_like(q)
+        out = _own_buffer(q.shape, dt, q.device, stream)
     _need(out, "out", dt)
     need = decode_workspace_bytes(B, H, d_h, r, max_seq_len, dt)
     if ws is None:
-        ws = workspace(need, q.device)
+        ws = _scratch(need, q.device, stream)
     _need(ws, "ws", torch.uint8)
     desc = cache.desc()
     code = _abi.lib().lrkv_decode(_ptr(q), ctypes.byref(desc), _ptr(B_K), _ptr(B_V),
@@ -187,11 +209,11 @@ def decode_step(X, W_S_K, W_S_V, U_K, U_V, q, cache: PagedCache, B_K, B_V, seq_l
     B, H, d_h = q.shape
     r = cache.R_K.shape[3]
     if out is None:
-        out = torch.empty_like(q)
+        out = _own_buffer(q.shape, dt, q.device, stream)
     _need(out, "out", dt)
     need = decode_step_workspace_bytes(B, H, d_h, r, max_seq_len, dt)
     if ws is None:
-        ws = workspace(need, q.device)
+        ws = _scratch(need, q.device, stream)
     _need(ws, "ws", torch.uint8)
     desc = cache.desc()
     code = _abi.lib().lrkv_decode_step(_ptr(X), X.shape[1], _ptr(W_S_K), _ptr(W_S_V), _ptr(U_K),
@@ -234,7 +256,7 @@ def decode_step_host(X, W_S_K, W_S_V, U_K, U_V, q, cache: PagedCache, B_K, B_V, 
         raise ValueError("out must be a host tensor")
     need = decode_step_host_workspace_bytes(B, H, d_h, r, d, max_seq_len, dt)
     if ws is None:
-        ws = workspace(need, page_table.device)
+        ws = _scratch(need, page_table.device, stream)
     _need(ws, "ws", torch.uint8)
     desc = cache.desc()
     code = _abi.lib().lrkv_decode_step_host(_ptr(X), d, _ptr(W_S_K), _ptr(W_S_V), _ptr(U_K),
@@ -325,10 +347,10 @@ def prefill(X, Q, cu_rows, start_pos, max_ctx, W_S_K, W_S_V, U_K, U_V, B_K, B_V,
     r = cache.R_K.shape[3]
     B = start_pos.shape[0]
     if out is None:
-        out = torch.empty_like(Q)
+        out = _own_buffer(Q.shape, dt, Q.device, stream)
     need = prefill_workspace_bytes(B, n, H, d_h, r, max_ctx, dt)
     if ws is None:
-        ws = workspace(need, X.device)
+        ws = _scratch(need, X.device, stream)
     desc = cache.desc()
     code = _abi.lib().lrkv_prefill(_ptr(X), _ptr(Q), _ptr(cu_rows), _ptr(start_pos), B, n,
                                    max_ctx, d, _ptr(W_S_K), _ptr(W_S_V), _ptr(U_K), _ptr(U_V),
@@ -345,10 +367,6 @@ def prefill(X, Q, cu_rows, start_pos, max_ctx, W_S_K, W_S_V, U_K, U_V, B_K, B_V,
 # current device, before the library is called.  A decode step takes less time
 # than a careful look at its arguments, so each function compares everything in
 # one expression and looks for the fault only when something differs.
-#
-# stream: the stream of the call (default: the current one).  Its inputs have to
-# be ready there, and a reader on another stream waits for it, as with any work
-# of two streams; what a call allocates for itself is in order on it.
 # ----------------------------------------------------------------------------
 _i32, _u8, _Tensor = torch.int32, torch.uint8, torch.Tensor
 
@@ -396,21 +414,6 @@ def _cache_arg(cache, dev):
     s0, s1, s2, s3 = cache.scale
     return _abi.pack_cache(S_K.data_ptr(), S_V.data_ptr(), R_K.data_ptr(), R_V.data_ptr(), n, ps, H, d_h, r, code,
                            s0, s1, s2, s3, nk, cache.norm_eps, G), act, H, d_h, r, G, code
-
-
-def _own_buffer(shape, dtype, dev, stream, scratch=False):
-    """A buffer made for a call on `stream`, from that stream's memory: work still
-    queued on the current stream cannot hold it.  Unless it is scratch, it is
-    not reused before the current stream, where the result is read, has passed
-    the point at which it is freed."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
-    here = torch.cuda.current_stream(dev)
-    with torch.cuda.stream(stream):
-        t = torch.empty(shape, dtype=dtype, device=dev)
-    if not scratch:
-        t.record_stream(here)
-    return t
 
 
 _LEAST, _MOST = -2 ** 31, 2 ** 31 - 1  # (a size past these would wrap on its way into the library)
@@ -495,7 +498,7 @@ def decode_window(q, cache: PagedCache, B_K, B_V, seq_lens, page_table, max_seq_
            else L.lrkv_decode_window(*args, *_workspace(ws, dev), *tail))
     if err == _abi.LRKV_E_WORKSPACE and ws is None:  # (most calls need none)
         n = L.lrkv_decode_window_workspace_bytes(B, H, d_h, r, max_seq_len, window, sinks, code)
-        ws = _own_buffer((n,), _u8, q.device, stream, scratch=True)
+        ws = _scratch(n, q.device, stream)
         err = L.lrkv_decode_window(*args, ws.data_ptr(), n, *tail)
     if err:
         _abi.check("lrkv_decode_window", err)
@@ -545,7 +548,7 @@ def prefill_window(X, Q, cu_rows, start_pos, max_ctx, W_S_K, W_S_V, U_K, U_V, B_
     err = L.lrkv_prefill_window(*args, *_workspace(ws, dev), *tail)
     if err == _abi.LRKV_E_WORKSPACE and ws is None:  # (few rows, or the per-row path)
         m = L.lrkv_prefill_workspace_bytes(B, n, H, d_h, r, max_ctx, code)
-        ws = _own_buffer((m,), _u8, X.device, stream, scratch=True)
+        ws = _scratch(m, X.device, stream)
         err = L.lrkv_prefill_window(*args, ws.data_ptr(), m, *tail)
     if err:
         _abi.check("lrkv_prefill_window", err)
@@ -642,7 +645,7 @@ def rope_table(d_h, max_pos, base=10000.0, device="cuda", stream=None) -> RopeTa
     nbytes = rope_table_bytes(d_h, max_pos)
     if nbytes == 0:
         raise ValueError(f"invalid rotary table size d_h={d_h} max_pos={max_pos}")
-    buf = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    buf = _own_buffer((nbytes,), torch.uint8, device, stream)
     _abi.check("lrkv_rope_table", _abi.lib().lrkv_rope_table(float(base), d_h, max_pos, _ptr(buf),
                                                              _stream(stream)))
     return RopeTable(buf, d_h, max_pos)
@@ -673,10 +676,10 @@ def decode_rope(q, cache: PagedCache, B_K, B_V, seq_lens, page_table, max_seq_le
     _need_table(table, d_h)
     r = cache.R_K.shape[3]
     if out is None:
-        out = torch.empty_like(q)
+        out = _own_buffer(q.shape, dt, q.device, stream)
     _need(out, "out", dt)
     if ws is None:
-        ws = workspace(decode_rope_workspace_bytes(B, H, d_h, r, max_seq_len, dt), q.device)
+        ws = _scratch(decode_rope_workspace_bytes(B, H, d_h, r, max_seq_len, dt), q.device, stream)
     _need(ws, "ws", torch.uint8)
     desc = cache.desc()
     code = _abi.lib().lrkv_decode_rope(_ptr(q), ctypes.byref(desc), _ptr(B_K), _ptr(B_V),
@@ -704,9 +707,9 @@ def prefill_rope(X, Q, cu_rows, start_pos, max_ctx, W_S_K, W_S_V, U_K, U_V, B_K,
     r = cache.R_K.shape[3]
     B = start_pos.shape[0]
     if out is None:
-        out = torch.empty_like(Q)
+        out = _own_buffer(Q.shape, dt, Q.device, stream)
     if ws is None:
-        ws = workspace(prefill_workspace_bytes(B, n, H, d_h, r, max_ctx, dt), X.device)
+        ws = _scratch(prefill_workspace_bytes(B, n, H, d_h, r, max_ctx, dt), X.device, stream)
     desc = cache.desc()
     code = _abi.lib().lrkv_prefill_rope(_ptr(X), _ptr(Q), _ptr(cu_rows), _ptr(start_pos), B, n,
                                         max_ctx, d, _ptr(W_S_K), _ptr(W_S_V), _ptr(U_K),

@@ -1,5 +1,5 @@
-"""What the binding of the windowed operators does around a library call, on
-host tensors and a library that only records what it is asked.  No call here
+"""What the binding does around a library call (most of it for the windowed
+operators), on host tensors and a library that only records what it is asked.  No call here
 touches a GPU."""
 import ctypes
 
@@ -30,7 +30,7 @@ class Library:
                 return 512
             self.calls.append((name, args))
             # (address and size of the workspace: fourth and third argument from the end)
-            return _abi.LRKV_E_WORKSPACE if name != "lrkv_page_plan" and args[-4] is None else _abi.LRKV_OK
+            return _abi.LRKV_E_WORKSPACE if name.endswith("_window") and args[-4] is None else _abi.LRKV_OK
         return entry
 
 
@@ -68,11 +68,44 @@ def plan(page=PAGE, rows=9, window=40, sinks=2, **kw):
     return api.page_plan(i32(B), i32(B), i32(B, MAX_PAGES), i32(5), i32(1), page, rows, window=window, sinks=sinks, **kw)
 
 
-@pytest.mark.parametrize("call,made,outputs", [(decode, 2, 1), (prefill, 2, 1), (plan, 2, 2)])
+def full_decode(**kw):
+    return api.decode(bf(B, H, D_H), cache(), bf(H, D_H, R), bf(H, D_H, R), i32(B), i32(B, MAX_PAGES), 100, **kw)
+
+
+def full_step(**kw):
+    return api.decode_step(bf(B, D), bf(D_H, D), bf(D_H, D), bf(H, R, D), bf(H, R, D), bf(B, H, D_H), cache(),
+                           bf(H, D_H, R), bf(H, D_H, R), i32(B), i32(B, MAX_PAGES), 100, **kw)
+
+
+def full_prefill(**kw):
+    return api.prefill(bf(N, D), bf(N, H, D_H), i32(B + 1), i32(B), 100, bf(D_H, D), bf(D_H, D), bf(H, R, D), bf(H, R, D),
+                       bf(H, D_H, R), bf(H, D_H, R), cache(), i32(B, MAX_PAGES), **kw)
+
+
+def table():
+    return api.RopeTable(torch.zeros(4, dtype=torch.uint8), D_H, 100)
+
+
+def rope_decode(**kw):
+    return api.decode_rope(bf(B, H, D_H), cache(), bf(H, D_H, R), bf(H, D_H, R), i32(B), i32(B, MAX_PAGES), 100, table(), **kw)
+
+
+def rope_prefill(**kw):
+    return api.prefill_rope(bf(N, D), bf(N, H, D_H), i32(B + 1), i32(B), 100, bf(D_H, D), bf(D_H, D), bf(H, R, D),
+                            bf(H, R, D), bf(H, D_H, R), bf(H, D_H, R), cache(), i32(B, MAX_PAGES), table(), **kw)
+
+
+def rope_table(stream):
+    return api.rope_table(D_H, 100, device="cpu", stream=stream)
+
+
+@pytest.mark.parametrize("call,made,outputs", [(decode, 2, 1), (prefill, 2, 1), (plan, 2, 2), (full_decode, 2, 1),
+                                               (full_step, 2, 1), (full_prefill, 2, 1), (rope_decode, 2, 1),
+                                               (rope_prefill, 2, 1), (rope_table, 1, 1)])
 def test_buffers_of_a_call_come_from_its_stream(lib, monkeypatch, call, made, outputs):
     """Whatever a call on another stream allocates (outputs and scratch) comes from that stream's memory, and outputs
     wait for the current stream before they are reused."""
-    at, current, marked, empty = [], ["here"], [], torch.empty
+    at, current, marked, empty, need = [], ["here"], [], torch.empty, api._need
 
     class On:
         def __init__(self, stream):
@@ -92,10 +125,11 @@ def test_buffers_of_a_call_come_from_its_stream(lib, monkeypatch, call, made, ou
     monkeypatch.setattr(torch, "empty", recorded)
     monkeypatch.setattr(torch, "empty_like", lambda t, **kw: recorded(t.shape, dtype=t.dtype))
     monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: marked.append(s.name))
+    monkeypatch.setattr(api, "_need", lambda t, name, dtype=None, device=True: need(t, name, dtype, False))
     call(stream=Stream("side"))
     assert at == ["side"] * made
     assert marked == ["here"] * outputs
-    assert all(args[-1] == Stream.cuda_stream for _, args in lib.calls)
+    assert all(getattr(args[-1], "value", args[-1]) == Stream.cuda_stream for _, args in lib.calls)
 
 
 WRAPS = [2 ** 31, 2 ** 32 + 40, -(2 ** 31) - 1, -(2 ** 32) + 40, -(2 ** 33)]
