@@ -451,6 +451,129 @@ LRKV_API int lrkv_prefill_window(const void *X, const void *Q, const int32_t *cu
                                  lrkv_stream_t stream);
 
 /*
+ * Block-scaled cache -- an 8-bit cache that finds its scales itself (library
+ * operators; the paper counts elements, not bits).  LRKV_FP8_E4M3 gives a whole
+ * pool one scale, which has to be known before the first row is written; here
+ * every head of every block of `block` consecutive tokens has its own (the
+ * shared rows: every group), taken from the rows themselves:
+ *     value = code * 2^e,  e in [LRKV_SCALED_MIN_EXP, LRKV_SCALED_MAX_EXP],
+ * codes E4M3, e stored as the byte e + 127 (a byte outside that range reads as
+ * the nearest one in it).  A power of two makes every value that a cache can
+ * hold a bf16 (and an fp32) value, exactly.
+ *     S_K, S_V : [num_pages, page_size, G, d_h]  codes    R_K, R_V : [num_pages, page_size, H, r]
+ *     E_S_K, E_S_V : [num_pages, page_size/block, G]      E_R_K, E_R_V : [num_pages, page_size/block, H]
+ * Pages, positions and page tables are lrkv_cache_t's.  Sizes as its
+ * LRKV_FP8_E4M3 form (d_h a multiple of 16, r of 8, H*r of 16); block divides
+ * page_size and is a multiple of 16.  G: 0 or 1 is one shared basis.  All
+ * pointers 16-byte aligned.  Nothing needs initialising.
+ *
+ * Rows are addressed as by lrkv_prefill: request b owns rows cu_rows[b] ..
+ * cu_rows[b+1]-1 of a call, at positions start_pos[b], start_pos[b]+1, ...
+ * (one new row a request in a decode step: cu_rows = 0, 1, .. B and start_pos =
+ * lengths before the step).  Rows of no request are left alone.  A row past the
+ * page table or at a negative position is skipped (LRKV_STATUS_BAD_ROW), so are
+ * rows on a page outside the pool (LRKV_STATUS_BAD_PAGE).  Two requests of a
+ * writing call must not write to the same block.
+ *
+ * lrkv_write_scaled quantises rows into the cache.  For a block that the call
+ * writes to, with a the largest finite magnitude of a head's new values there,
+ * need = the least e with a <= 448 * 2^e (the smallest e where a = 0):
+ *  - a row in the block's first slot begins the block: e = need, whatever the
+ *    block held before;
+ *  - else the rows before the first new one stay: e = max(old e, need), and
+ *    where that is more than the old e their codes become code * 2^(old - e),
+ *    rounded to the nearest code (exact but for the smallest 2^-6 of a block's
+ *    range).  Slots past the new rows are left as they are.
+ * New codes are x / 2^e rounded to nearest, ties to even, saturating (magnitudes
+ * beyond 448 * 2^119 only); infinities and NaN become the NaN code.
+ *   S_K, S_V [n, G*d_h], R_K, R_V [n, H*r] of `dtype` (LRKV_F32 or LRKV_BF16)
+ *   with row strides ld_* in elements (at least a row; a row begins at a
+ *   multiple of 16 bytes), so the slices of one projection's output do.
+ *
+ * lrkv_read_scaled is its inverse: row i of the outputs (same strides) gets the
+ * values of its cache row, exact in either dtype (NaN codes as NaN).  Skipped
+ * rows and rows of no request stay as they are.
+ *
+ * lrkv_append_scaled projects X as lrkv_append does (fp32 sums) and writes the
+ * fp32 rows as lrkv_write_scaled does; they are rounded once.  Workspace:
+ * lrkv_append_scaled_workspace_bytes bytes.
+ *
+ * lrkv_decode_scaled is lrkv_decode on such a cache, with q, B_K, B_V and out in
+ * bf16.  On tensor cores (d_h = 128, G = 1, H a multiple of 4 up to 32, r up to 64,
+ * and what of it fits in tensor memory) the codes are multiplied as
+ * they are: q, q B_K[h] and the weights enter as sums of two or three E4M3 terms
+ * (at least bf16's precision), and the scales are applied to the sums.  Rows
+ * that a query sees must hold no NaN code there: a NaN reaches other heads of
+ * the request.  What pages hold past a request's length never matters.
+ * Workspace: lrkv_decode_scaled_workspace_bytes bytes; that never falls as B or
+ * max_seq_len grows.  A length may exceed max_seq_len up to the page table's end.
+ *
+ * lrkv_prefill_scaled is lrkv_append_scaled, then causal attention of every new
+ * row over its request's cache rows (what the cache holds, the new rows
+ * quantised), as lrkv_prefill.  max_ctx: host upper bound of start_pos[b] + rows of b.
+ * Where lrkv_prefill runs its tiled kernel on a bf16 cache of these sizes, the
+ * values are laid out in bf16 in the workspace and that kernel runs; other
+ * sizes run one decode a row.
+ *
+ * Workspaces are 256-byte aligned device memory, scratch, without
+ * initialisation; one per call in flight.
+ */
+#define LRKV_SCALED_MIN_EXP (-117)
+#define LRKV_SCALED_MAX_EXP 119
+typedef struct {
+    void *S_K;
+    void *S_V;
+    void *R_K;
+    void *R_V;
+    uint8_t *E_S_K;
+    uint8_t *E_S_V;
+    uint8_t *E_R_K;
+    uint8_t *E_R_V;
+    int32_t num_pages;
+    int32_t page_size;
+    int32_t H;
+    int32_t d_h;
+    int32_t r;
+    int32_t G;
+    int32_t block;
+    int32_t reserved; /* 0 */
+} lrkv_scaled_t;
+
+LRKV_API int lrkv_write_scaled(const void *S_K, int64_t ld_sk, const void *S_V, int64_t ld_sv,
+                               const void *R_K, int64_t ld_rk, const void *R_V, int64_t ld_rv,
+                               int32_t dtype, const int32_t *cu_rows, const int32_t *start_pos,
+                               int32_t B, int32_t n, const lrkv_scaled_t *cache,
+                               const int32_t *page_table, int32_t max_pages, int32_t *dev_status,
+                               lrkv_stream_t stream);
+LRKV_API int lrkv_read_scaled(const lrkv_scaled_t *cache, const int32_t *cu_rows,
+                              const int32_t *start_pos, int32_t B, int32_t n,
+                              const int32_t *page_table, int32_t max_pages, int32_t dtype, void *S_K,
+                              int64_t ld_sk, void *S_V, int64_t ld_sv, void *R_K, int64_t ld_rk,
+                              void *R_V, int64_t ld_rv, int32_t *dev_status, lrkv_stream_t stream);
+LRKV_API size_t lrkv_append_scaled_workspace_bytes(const lrkv_scaled_t *cache, int32_t n);
+LRKV_API int lrkv_append_scaled(const void *X, const int32_t *cu_rows, const int32_t *start_pos,
+                                int32_t B, int32_t n, int32_t d, const void *W_S_K, const void *W_S_V,
+                                const void *U_K, const void *U_V, const lrkv_scaled_t *cache,
+                                const int32_t *page_table, int32_t max_pages, void *workspace,
+                                size_t workspace_bytes, int32_t *dev_status, lrkv_stream_t stream);
+LRKV_API size_t lrkv_decode_scaled_workspace_bytes(const lrkv_scaled_t *cache, int32_t B,
+                                                   int32_t max_seq_len);
+LRKV_API int lrkv_decode_scaled(const void *q, const lrkv_scaled_t *cache, const void *B_K,
+                                const void *B_V, const int32_t *seq_lens, const int32_t *page_table,
+                                int32_t B, int32_t max_pages, int32_t max_seq_len, void *out,
+                                void *workspace, size_t workspace_bytes, int32_t *dev_status,
+                                lrkv_stream_t stream);
+LRKV_API size_t lrkv_prefill_scaled_workspace_bytes(const lrkv_scaled_t *cache, int32_t B, int32_t n,
+                                                    int32_t max_ctx);
+LRKV_API int lrkv_prefill_scaled(const void *X, const void *Q, const int32_t *cu_rows,
+                                 const int32_t *start_pos, int32_t B, int32_t n, int32_t max_ctx,
+                                 int32_t d, const void *W_S_K, const void *W_S_V, const void *U_K,
+                                 const void *U_V, const void *B_K, const void *B_V,
+                                 const lrkv_scaled_t *cache, const int32_t *page_table,
+                                 int32_t max_pages, void *out, void *workspace, size_t workspace_bytes,
+                                 int32_t *dev_status, lrkv_stream_t stream);
+
+/*
  * lrkv_page_plan - the pages and slots of one serving step, built on the GPU
  * from the requests' lengths.  (Library plumbing: the paper only asks that
  * shared and private pages share their ids and lifetime, section 3 after

@@ -19,7 +19,9 @@ __all__ = [
     "decode_rope", "prefill_rope", "key_norms", "RopeTable", "rope_table_bytes",
     "decode_rope_workspace_bytes", "decode_step_host", "decode_step_host_workspace_bytes",
     "StepGraph", "decode_window", "decode_window_workspace_bytes", "prefill_window", "page_plan",
-    "PagePlan",
+    "PagePlan", "ScaledCache", "ScaledRows", "write_scaled", "read_scaled", "append_scaled",
+    "append_scaled_workspace_bytes", "decode_scaled", "decode_scaled_workspace_bytes", "prefill_scaled",
+    "prefill_scaled_workspace_bytes",
 ]
 
 
@@ -32,7 +34,10 @@ def __getattr__(name):
                 "prefill_rope", "key_norms", "RopeTable", "rope_table_bytes",
                 "decode_rope_workspace_bytes", "decode_step_host",
                 "decode_step_host_workspace_bytes", "StepGraph", "decode_window",
-                "decode_window_workspace_bytes", "prefill_window", "page_plan", "PagePlan"):
+                "decode_window_workspace_bytes", "prefill_window", "page_plan", "PagePlan", "ScaledCache",
+                "ScaledRows", "write_scaled", "read_scaled", "append_scaled", "append_scaled_workspace_bytes",
+                "decode_scaled", "decode_scaled_workspace_bytes", "prefill_scaled",
+                "prefill_scaled_workspace_bytes"):
         from . import api
         return getattr(api, name)
     raise AttributeError(name)

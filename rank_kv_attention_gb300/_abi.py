@@ -53,11 +53,20 @@ class CacheDesc(ctypes.Structure):
     ]
 
 
+class ScaledDesc(ctypes.Structure):
+    """Mirror of lrkv_scaled_t."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("S_K", "S_V", "R_K", "R_V", "E_S_K", "E_S_V", "E_R_K", "E_R_V")] + \
+               [(n, ctypes.c_int32) for n in ("num_pages", "page_size", "H", "d_h", "r", "G", "block", "reserved")]
+
+
 # The same as bytes, made in one step; functions that take a bare pointer for the
 # descriptor accept them.
 _PACK_CACHE = struct.Struct("@4P6i4fPfi")
 assert _PACK_CACHE.size == ctypes.sizeof(CacheDesc)
 pack_cache = _PACK_CACHE.pack
+_PACK_SCALED = struct.Struct("@8P8i")
+assert _PACK_SCALED.size == ctypes.sizeof(ScaledDesc)
+pack_scaled = _PACK_SCALED.pack
 
 
 class LrkvError(RuntimeError):
@@ -75,6 +84,7 @@ _lib = None
 
 P = ctypes.c_void_p
 I32 = ctypes.c_int32
+I64 = ctypes.c_int64
 SZ = ctypes.c_size_t
 CACHE_P = ctypes.POINTER(CacheDesc)
 
@@ -86,6 +96,15 @@ SIGNATURES = {
                                            I32, I32, I32, P, P, SZ, P, P]),
     "lrkv_page_plan": (ctypes.c_int, [P, P, I32, I32, I32, I32, I32, I32, I32, P, P, P, P, P, P, P, P, P,
                                       P, P, P]),
+    "lrkv_write_scaled": (ctypes.c_int, [P, I64, P, I64, P, I64, P, I64, I32, P, P, I32, I32, P, P, I32, P, P]),
+    "lrkv_read_scaled": (ctypes.c_int, [P, P, P, I32, I32, P, I32, I32, P, I64, P, I64, P, I64, P, I64, P, P]),
+    "lrkv_append_scaled_workspace_bytes": (SZ, [P, I32]),
+    "lrkv_append_scaled": (ctypes.c_int, [P, P, P, I32, I32, I32, P, P, P, P, P, P, I32, P, SZ, P, P]),
+    "lrkv_decode_scaled_workspace_bytes": (SZ, [P, I32, I32]),
+    "lrkv_decode_scaled": (ctypes.c_int, [P, P, P, P, P, P, I32, I32, I32, P, P, SZ, P, P]),
+    "lrkv_prefill_scaled_workspace_bytes": (SZ, [P, I32, I32, I32]),
+    "lrkv_prefill_scaled": (ctypes.c_int, [P, P, P, P, I32, I32, I32, I32, P, P, P, P, P, P, P, P, I32, P, P, SZ, P,
+                                           P]),
     "lrkv_append": (ctypes.c_int, [P, P, P, I32, I32, P, P, P, P, CACHE_P, P, I32, I32, P, P]),
     "lrkv_decode_workspace_bytes": (SZ, [I32, I32, I32, I32, I32, I32]),
     "lrkv_decode": (ctypes.c_int, [P, CACHE_P, P, P, P, P, I32, I32, I32, P, P, SZ, P, P]),

@@ -611,6 +611,295 @@ def page_plan(seq_lens, new_rows, page_table, free_pages, n_free, page_size, max
 
 
 # ----------------------------------------------------------------------------
+# Block-scaled cache (see include/lrkv.h): 8-bit codes with a power-of-two scale
+# for each block of tokens and head.  Checked like the windowed functions.
+# ----------------------------------------------------------------------------
+_POOLS = ("S_K", "S_V", "R_K", "R_V")
+
+
+@dataclass
+class ScaledCache:
+    """Caller-owned paged cache in 8 bits that finds its scales itself.
+
+    S_K, S_V: codes [num_pages, page_size, d_h] (or [.., G, d_h] for G shared
+    groups); R_K, R_V: [num_pages, page_size, H, r], all torch.float8_e4m3fn.
+    E_S_K, E_S_V: [num_pages, page_size // block, G] and E_R_K, E_R_V: [..., H],
+    torch.uint8: a code's value is code * 2^(byte - 127) with the byte of its
+    block of ``block`` tokens and its head (group).  Nothing needs initialising:
+    the functions that write rows set the scales of the blocks they begin.
+    """
+    S_K: torch.Tensor
+    S_V: torch.Tensor
+    R_K: torch.Tensor
+    R_V: torch.Tensor
+    E_S_K: torch.Tensor
+    E_S_V: torch.Tensor
+    E_R_K: torch.Tensor
+    E_R_V: torch.Tensor
+
+    @classmethod
+    def empty(cls, num_pages, page_size, H, d_h, r, block=64, device="cuda", groups=1):
+        if block < 1 or page_size % block:
+            raise ValueError(f"block = {block} must divide page_size = {page_size}")
+        code = lambda *s: torch.empty(s, dtype=torch.float8_e4m3fn, device=device)
+        exp = lambda n: torch.empty((num_pages, page_size // block, n), dtype=torch.uint8, device=device)
+        sh = (num_pages, page_size, d_h) if groups == 1 else (num_pages, page_size, groups, d_h)
+        return cls(code(*sh), code(*sh), code(num_pages, page_size, H, r), code(num_pages, page_size, H, r),
+                   exp(groups), exp(groups), exp(H), exp(H))
+
+    @property
+    def block(self):
+        """Tokens that share a scale."""
+        return self.R_K.shape[1] // self.E_R_K.shape[1]
+
+    @property
+    def groups(self):
+        """Shared key/value groups (1: one shared basis)."""
+        return self.S_K.shape[2] if self.S_K.dim() == 4 else 1
+
+
+class ScaledRows(NamedTuple):
+    """Rows read back: S_K, S_V [n, d_h] (or [n, G, d_h]), R_K, R_V [n, H, r]."""
+    S_K: torch.Tensor
+    S_V: torch.Tensor
+    R_K: torch.Tensor
+    R_V: torch.Tensor
+
+
+_f8, _bf16, _f32 = torch.float8_e4m3fn, torch.bfloat16, torch.float32
+
+
+def _scaled_arg(cache, dev):
+    """(lrkv_scaled_t as bytes, H, d_h, r, groups) with all tensors' shapes and devices checked."""
+    S_K, S_V, R_K, R_V = cache.S_K, cache.S_V, cache.R_K, cache.R_V
+    E_S_K, E_S_V, E_R_K, E_R_V = cache.E_S_K, cache.E_S_V, cache.E_R_K, cache.E_R_V
+    if not (isinstance(S_K, _Tensor) and isinstance(R_K, _Tensor) and isinstance(E_R_K, _Tensor)) \
+            or S_K.dim() not in (3, 4) or R_K.dim() != 4 or E_R_K.dim() != 3:
+        raise ValueError("S_K must be [num_pages, page_size, (G,) d_h], R_K [num_pages, page_size, H, r] and E_R_K "
+                         "[num_pages, page_size / block, H]")
+    ss, rs = S_K.shape, R_K.shape
+    n, ps, H, r = rs
+    d_h, G, nb = ss[-1], ss[2] if len(ss) == 4 else 1, E_R_K.shape[1]
+    es, er = (n, nb, G), (n, nb, H)
+    if ss[0] != n or ss[1] != ps:
+        raise ValueError(f"S_K {list(ss)} and R_K {list(rs)} must have the same pages")
+    if nb < 1 or ps % nb:
+        raise ValueError(f"E_R_K {list(E_R_K.shape)} does not divide pages of {ps} tokens into blocks")
+    if not (isinstance(S_V, _Tensor) and isinstance(R_V, _Tensor) and isinstance(E_S_K, _Tensor)
+            and isinstance(E_S_V, _Tensor) and isinstance(E_R_V, _Tensor) and S_K.dtype is _f8 and S_V.dtype is _f8
+            and R_K.dtype is _f8 and R_V.dtype is _f8 and E_S_K.dtype is _u8 and E_S_V.dtype is _u8
+            and E_R_K.dtype is _u8 and E_R_V.dtype is _u8 and S_V.shape == ss and R_V.shape == rs
+            and E_S_K.shape == es and E_S_V.shape == es and E_R_K.shape == er and E_R_V.shape == er
+            and S_K.get_device() == dev and S_V.get_device() == dev and R_K.get_device() == dev
+            and R_V.get_device() == dev and E_S_K.get_device() == dev and E_S_V.get_device() == dev
+            and E_R_K.get_device() == dev and E_R_V.get_device() == dev and S_K.is_contiguous()
+            and S_V.is_contiguous() and R_K.is_contiguous() and R_V.is_contiguous() and E_S_K.is_contiguous()
+            and E_S_V.is_contiguous() and E_R_K.is_contiguous() and E_R_V.is_contiguous()):
+        _refuse(((S_K, "S_K", _f8, ss), (S_V, "S_V", _f8, ss), (R_K, "R_K", _f8, rs), (R_V, "R_V", _f8, rs),
+                 (E_S_K, "E_S_K", _u8, es), (E_S_V, "E_S_V", _u8, es), (E_R_K, "E_R_K", _u8, er),
+                 (E_R_V, "E_R_V", _u8, er)), dev)
+    return _abi.pack_scaled(S_K.data_ptr(), S_V.data_ptr(), R_K.data_ptr(), R_V.data_ptr(), E_S_K.data_ptr(),
+                            E_S_V.data_ptr(), E_R_K.data_ptr(), E_R_V.data_ptr(), n, ps, H, d_h, r, G, ps // nb,
+                            0), H, d_h, r, G
+
+
+def _row_args(cu_rows, start_pos, page_table, dev):
+    """(B, max_pages) of the requests' rows of a call."""
+    (B,), max_pages = _dim(start_pos, "start_pos", 1), _dim(page_table, "page_table", 2)[1]
+    if not (isinstance(cu_rows, _Tensor) and cu_rows.dtype is _i32 and start_pos.dtype is _i32
+            and page_table.dtype is _i32 and cu_rows.shape == (B + 1,) and page_table.shape[0] == B
+            and cu_rows.get_device() == dev and start_pos.get_device() == dev and page_table.get_device() == dev
+            and cu_rows.is_contiguous() and start_pos.is_contiguous() and page_table.is_contiguous()):
+        _refuse(((cu_rows, "cu_rows", _i32, (B + 1,)), (start_pos, "start_pos", _i32, (B,)),
+                 (page_table, "page_table", _i32, (B, max_pages))), dev)
+    return B, max_pages
+
+
+def _strided_rows(rows, n, H, d_h, r, G, dev):
+    """[address, row stride] of the four pools' rows one after the other, and their dtype.  A row is dense; rows may
+    lie apart (slices of one projection's output)."""
+    out, dt = [], None
+    for name, t in zip(_POOLS, rows):
+        if not isinstance(t, _Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        shape, ld = t.shape, t.stride()
+        flat, deep = ((n, G * d_h), (n, G, d_h)) if name[0] == "S" else ((n, H * r), (n, H, r))
+        if dt is None:
+            dt = t.dtype
+            if dt is not _bf16 and dt is not _f32:
+                raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {dt}")
+        if t.dtype is not dt:
+            raise TypeError(f"{name} must be {dt}, got {t.dtype}")
+        if shape != flat and shape != deep:
+            raise ValueError(f"{name} must be {list(deep)} or {list(flat)}, got {list(shape)}")
+        if t.get_device() != dev:
+            raise ValueError(f"{name} is on {t.device}, not on the current device cuda:{dev}")
+        if n and not (ld[-1] == 1 and (len(shape) == 2 or ld[1] == shape[2] or shape[1] == 1)):
+            raise ValueError(f"{name}: the values of a row must be contiguous")
+        # (one row has no distance to a next one)
+        out += [t.data_ptr(), max(ld[0], flat[1]) if n <= 1 else ld[0]]
+    return out, dt
+
+
+def write_scaled(S_K, S_V, R_K, R_V, cu_rows, start_pos, cache: ScaledCache, page_table, status=None, stream=None):
+    """lrkv_write_scaled: quantise rows (S_K, S_V [n, d_h] or [n, G, d_h]; R_K, R_V [n, H, r] or [n, H * r], bf16 or
+    fp32, rows may have a stride) of requests b = rows cu_rows[b] .. cu_rows[b + 1] - 1 into the cache at positions
+    start_pos[b], start_pos[b] + 1, ..."""
+    dev = _device_of(S_K, "S_K")
+    desc, H, d_h, r, G = _scaled_arg(cache, dev)
+    B, max_pages = _row_args(cu_rows, start_pos, page_table, dev)
+    n = S_K.shape[0] if S_K.dim() else 0
+    rows, dt = _strided_rows((S_K, S_V, R_K, R_V), n, H, d_h, r, G, dev)
+    code = _abi.lib().lrkv_write_scaled(*rows, _DT[dt], cu_rows.data_ptr(), start_pos.data_ptr(), B, n, desc,
+                                        page_table.data_ptr(), max_pages, _status(status, dev),
+                                        _raw_stream(stream, dev))
+    if code:
+        _abi.check("lrkv_write_scaled", code)
+
+
+def read_scaled(cu_rows, start_pos, n, cache: ScaledCache, page_table, dtype=torch.bfloat16, out=None, status=None,
+                stream=None) -> ScaledRows:
+    """lrkv_read_scaled: the values of n rows, addressed as by write_scaled, in bf16 or fp32 (exact in both).  Rows of
+    ``out`` (a ScaledRows) that no request owns, or that lie on no page, stay as they are."""
+    dev = _device_of(cu_rows, "cu_rows")
+    desc, H, d_h, r, G = _scaled_arg(cache, dev)
+    B, max_pages = _row_args(cu_rows, start_pos, page_table, dev)
+    if n < 0:
+        raise ValueError("n must not be negative")
+    if n > _MOST:
+        _past_32_bits(n=n)
+    if out is None:
+        shared = (n, d_h) if cache.S_K.dim() == 3 else (n, G, d_h)
+        if dtype is not _bf16 and dtype is not _f32:
+            raise TypeError(f"dtype must be torch.bfloat16 or torch.float32, got {dtype}")
+        out = ScaledRows(*[_own_buffer(s, dtype, cu_rows.device, stream) for s in (shared, shared, (n, H, r), (n, H, r))])
+    rows, dt = _strided_rows(out, n, H, d_h, r, G, dev)
+    code = _abi.lib().lrkv_read_scaled(desc, cu_rows.data_ptr(), start_pos.data_ptr(), B, n, page_table.data_ptr(),
+                                       max_pages, _DT[dt], *rows, _status(status, dev), _raw_stream(stream, dev))
+    if code:
+        _abi.check("lrkv_read_scaled", code)
+    return ScaledRows(*out)
+
+
+def _projection_args(X, W_S_K, W_S_V, U_K, U_V, H, d_h, r, G, dev):
+    """(n, d) with the projection's tensors checked."""
+    n, d = _dim(X, "X", 2)
+    shared, private = (G * d_h, d), (H, r, d)
+    if not (isinstance(W_S_K, _Tensor) and isinstance(W_S_V, _Tensor) and isinstance(U_K, _Tensor)
+            and isinstance(U_V, _Tensor) and X.dtype is _bf16 and W_S_K.dtype is _bf16 and W_S_V.dtype is _bf16
+            and U_K.dtype is _bf16 and U_V.dtype is _bf16 and W_S_K.shape == shared and W_S_V.shape == shared
+            and U_K.shape == private and U_V.shape == private and X.get_device() == dev
+            and W_S_K.get_device() == dev and W_S_V.get_device() == dev and U_K.get_device() == dev
+            and U_V.get_device() == dev and X.is_contiguous() and W_S_K.is_contiguous() and W_S_V.is_contiguous()
+            and U_K.is_contiguous() and U_V.is_contiguous()):
+        _refuse(((X, "X", _bf16, (n, d)), (W_S_K, "W_S_K", _bf16, shared), (W_S_V, "W_S_V", _bf16, shared),
+                 (U_K, "U_K", _bf16, private), (U_V, "U_V", _bf16, private)), dev)
+    return n, d
+
+
+def _own_workspace(ws, need, dev, device, stream):
+    """(address, bytes) of the caller's workspace, or of one made for the call; the tensor, to keep it until then."""
+    if ws is None:
+        ws = torch.empty(max(need, 1), dtype=_u8, device=device) if stream is None else _scratch(need, device, stream)
+        return ws.data_ptr(), need, ws
+    return *_workspace(ws, dev), ws
+
+
+def append_scaled_workspace_bytes(cache: ScaledCache, n) -> int:
+    """lrkv_append_scaled_workspace_bytes: for up to n rows."""
+    return _abi.lib().lrkv_append_scaled_workspace_bytes(_scaled_arg(cache, cache.S_K.get_device())[0], n)
+
+
+def append_scaled(X, cu_rows, start_pos, W_S_K, W_S_V, U_K, U_V, cache: ScaledCache, page_table, ws=None, status=None,
+                  stream=None):
+    """lrkv_append_scaled: project rows X and quantise them into the cache, addressed as by write_scaled."""
+    dev = _device_of(X, "X")
+    desc, H, d_h, r, G = _scaled_arg(cache, dev)
+    B, max_pages = _row_args(cu_rows, start_pos, page_table, dev)
+    n, d = _projection_args(X, W_S_K, W_S_V, U_K, U_V, H, d_h, r, G, dev)
+    L = _abi.lib()
+    need = L.lrkv_append_scaled_workspace_bytes(desc, n) if ws is None else 0
+    addr, size, ws = _own_workspace(ws, need, dev, X.device, stream)
+    code = L.lrkv_append_scaled(X.data_ptr(), cu_rows.data_ptr(), start_pos.data_ptr(), B, n, d, W_S_K.data_ptr(),
+                                W_S_V.data_ptr(), U_K.data_ptr(), U_V.data_ptr(), desc, page_table.data_ptr(),
+                                max_pages, addr, size, _status(status, dev), _raw_stream(stream, dev))
+    if code:
+        _abi.check("lrkv_append_scaled", code)
+
+
+def decode_scaled_workspace_bytes(cache: ScaledCache, B, max_seq_len) -> int:
+    """lrkv_decode_scaled_workspace_bytes: enough for this call and for every smaller one."""
+    if not (_LEAST <= max_seq_len <= _MOST):
+        _past_32_bits(max_seq_len=max_seq_len)
+    return _abi.lib().lrkv_decode_scaled_workspace_bytes(_scaled_arg(cache, cache.S_K.get_device())[0], B, max_seq_len)
+
+
+def decode_scaled(q, cache: ScaledCache, B_K, B_V, seq_lens, page_table, max_seq_len, out=None, ws=None, status=None,
+                  stream=None):
+    """lrkv_decode_scaled: per-head attention output [B, H, d_h] (bf16) of one decode step over the cache."""
+    dev = _device_of(q, "q")
+    desc, H, d_h, r, G = _scaled_arg(cache, dev)
+    B, max_pages = _dim(q, "q", 3)[0], _dim(page_table, "page_table", 2)[1]
+    if out is None:
+        out = torch.empty_like(q) if stream is None else _own_buffer(q.shape, q.dtype, q.device, stream)
+    shape, base = (B, H, d_h), (H, d_h, r)
+    if not (isinstance(B_K, _Tensor) and isinstance(B_V, _Tensor) and isinstance(seq_lens, _Tensor)
+            and isinstance(out, _Tensor) and q.dtype is _bf16 and B_K.dtype is _bf16 and B_V.dtype is _bf16
+            and out.dtype is _bf16 and seq_lens.dtype is _i32 and page_table.dtype is _i32 and q.shape == shape
+            and out.shape == shape and B_K.shape == base and B_V.shape == base and seq_lens.shape == (B,)
+            and page_table.shape[0] == B and q.get_device() == dev and B_K.get_device() == dev
+            and B_V.get_device() == dev and seq_lens.get_device() == dev and page_table.get_device() == dev
+            and out.get_device() == dev and q.is_contiguous() and B_K.is_contiguous() and B_V.is_contiguous()
+            and seq_lens.is_contiguous() and page_table.is_contiguous() and out.is_contiguous()):
+        _refuse(((q, "q", _bf16, shape), (B_K, "B_K", _bf16, base), (B_V, "B_V", _bf16, base),
+                 (seq_lens, "seq_lens", _i32, (B,)), (page_table, "page_table", _i32, (B, max_pages)),
+                 (out, "out", _bf16, shape)), dev)
+    if not (_LEAST <= max_seq_len <= _MOST):
+        _past_32_bits(max_seq_len=max_seq_len)
+    L = _abi.lib()
+    need = L.lrkv_decode_scaled_workspace_bytes(desc, B, max_seq_len) if ws is None else 0
+    addr, size, ws = _own_workspace(ws, need, dev, q.device, stream)
+    code = L.lrkv_decode_scaled(q.data_ptr(), desc, B_K.data_ptr(), B_V.data_ptr(), seq_lens.data_ptr(),
+                                page_table.data_ptr(), B, max_pages, max_seq_len, out.data_ptr(), addr, size,
+                                _status(status, dev), _raw_stream(stream, dev))
+    if code:
+        _abi.check("lrkv_decode_scaled", code)
+    return out
+
+
+def prefill_scaled_workspace_bytes(cache: ScaledCache, B, n, max_ctx) -> int:
+    """lrkv_prefill_scaled_workspace_bytes of a call of n rows of B requests."""
+    if not (_LEAST <= max_ctx <= _MOST):
+        _past_32_bits(max_ctx=max_ctx)
+    return _abi.lib().lrkv_prefill_scaled_workspace_bytes(_scaled_arg(cache, cache.S_K.get_device())[0], B, n, max_ctx)
+
+
+def prefill_scaled(X, Q, cu_rows, start_pos, max_ctx, W_S_K, W_S_V, U_K, U_V, B_K, B_V, cache: ScaledCache, page_table,
+                   out=None, ws=None, status=None, stream=None):
+    """lrkv_prefill_scaled: append the chunk X, then causal attention of each row's Q over its request's rows."""
+    dev = _device_of(X, "X")
+    desc, H, d_h, r, G = _scaled_arg(cache, dev)
+    B, max_pages = _row_args(cu_rows, start_pos, page_table, dev)
+    n, d = _projection_args(X, W_S_K, W_S_V, U_K, U_V, H, d_h, r, G, dev)
+    shape, base = (n, H, d_h), (H, d_h, r)
+    if out is None:
+        out = _own_buffer(shape, _bf16, X.device, stream)
+    _fits(((Q, "Q", _bf16, shape), (B_K, "B_K", _bf16, base), (B_V, "B_V", _bf16, base), (out, "out", _bf16, shape)), dev)
+    if not (_LEAST <= max_ctx <= _MOST):
+        _past_32_bits(max_ctx=max_ctx)
+    L = _abi.lib()
+    need = L.lrkv_prefill_scaled_workspace_bytes(desc, B, n, max_ctx) if ws is None else 0
+    addr, size, ws = _own_workspace(ws, need, dev, X.device, stream)
+    code = L.lrkv_prefill_scaled(X.data_ptr(), Q.data_ptr(), cu_rows.data_ptr(), start_pos.data_ptr(), B, n, max_ctx, d,
+                                 W_S_K.data_ptr(), W_S_V.data_ptr(), U_K.data_ptr(), U_V.data_ptr(), B_K.data_ptr(),
+                                 B_V.data_ptr(), desc, page_table.data_ptr(), max_pages, out.data_ptr(), addr, size,
+                                 _status(status, dev), _raw_stream(stream, dev))
+    if code:
+        _abi.check("lrkv_prefill_scaled", code)
+    return out
+
+
+# ----------------------------------------------------------------------------
 # Exact rotary position embedding (see include/lrkv.h)
 # ----------------------------------------------------------------------------
 class RopeTable:

@@ -34,6 +34,7 @@ __device__ __forceinline__ int64_t append_dest_row(const int32_t *positions, con
 // lengths or from the caller's arrays.
 template <typename T>
 __device__ __forceinline__ int64_t append_dest_row(const AppendArgsT<T> &a, int i) {
+    if (a.rows32[0]) return i;
     if (a.step_lens) {
         const int32_t L = a.step_lens[i];
         const int32_t b = i, pos = (L < 1 || L > a.step_max_len) ? -1 : L - 1;

@@ -30,6 +30,9 @@ struct AppendArgsT {
     bool fp8 = false;
     uint8_t *q8[4] = {nullptr, nullptr, nullptr, nullptr};  // S_K, S_V, R_K, R_V codes
     float inv_scale[4] = {1.f, 1.f, 1.f, 1.f};
+    // Projection only: row i of the call goes to row i of these dense fp32 arrays
+    // (S_K, S_V, R_K, R_V), whatever positions say; no cache is touched.
+    float *rows32[4] = {nullptr, nullptr, nullptr, nullptr};
 };
 
 // The first request b with cu_rows[b + 1] > row (B when there is none).
@@ -54,7 +57,9 @@ __device__ __forceinline__ void store_projected(const AppendArgsT<T> &a, size_t 
     else if (c < 2 * a.d_h) { k = 1; col = c - a.d_h; width = a.d_h; }
     else if (c < 2 * a.d_h + Hr) { k = 2; col = c - 2 * a.d_h; width = Hr; }
     else { k = 3; col = c - 2 * a.d_h - Hr; width = Hr; }
-    if (a.fp8) {
+    if (a.rows32[0]) {
+        a.rows32[k][row * width + col] = v;
+    } else if (a.fp8) {
         a.q8[k][row * width + col] = (uint8_t)(e4m3x2_from_f32(v * a.inv_scale[k], 0.f) & 0xffu);
     } else {
         T *base = k == 0 ? a.S_K : k == 1 ? a.S_V : k == 2 ? a.R_K : a.R_V;
@@ -79,6 +84,9 @@ cudaError_t launch_append_rows(const AppendArgsT<T> &a);
 // Few-row append on tensor cores (bf16): whether the shape fits, launcher.
 bool rows_mma_append_fits(const AppendArgsT<__nv_bfloat16> &a);
 cudaError_t launch_append_rows_mma(const AppendArgsT<__nv_bfloat16> &a);
+
+// The append of bf16 rows by the kernel that fits them.
+cudaError_t dispatch_append(const AppendArgsT<__nv_bfloat16> &a);
 
 // Tensor-core append (bf16): covered shapes and launcher.
 bool tc_append_supported(int n, int d, int d_h, int H, int r);

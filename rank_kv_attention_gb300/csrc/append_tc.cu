@@ -186,7 +186,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TC_THREADS, 1)
             int64_t dr = -1;
             {
                 const int r = m0 + row;
-                if (r < a.n) {
+                if (r < a.n && a.rows32[0]) {
+                    dr = r;
+                } else if (r < a.n) {
                     int32_t b, pos;
                     if (a.step_lens) {  // decode step: request r at its length - 1
                         const int32_t L = a.step_lens[r];
@@ -230,6 +232,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TC_THREADS, 1)
                     tmem_ld32(tmem + ((uint32_t)(32 * q) << 16) + acc * 2 * TC_BN + k * TC_BN + c * 32, v);
                     const int cc = col0 + c * 32;
                     if (dr < 0 || cc >= width) continue;
+                    if (a.rows32[0]) {  // the sums as they are
+                        float *dst = a.rows32[seg] + dr * rowlen + cc;
+                        if (cc + 32 <= width) {
+                            uint4 *d4 = reinterpret_cast<uint4 *>(dst);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                d4[e] = make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+                        } else {
+                            for (int e = 0; e < width - cc; ++e) dst[e] = __uint_as_float(v[e]);
+                        }
+                        continue;
+                    }
                     if (a.fp8) {  // 8-bit codes of v / scale
                         uint8_t *qd = a.q8[seg] + dr * rowlen + cc;
                         const float is = a.inv_scale[seg];
@@ -342,6 +356,13 @@ bool tc_append_supported(int n, int d, int d_h, int H, int r) {
 bool tc_append_leaves_sms(int n, int d_h, int H, int r) {
     TcBlocks t;
     return tc_blocks(n, d_h, H * r, t) && 2 * t.npairs < device_sm_count();
+}
+
+cudaError_t dispatch_append(const AppendArgsT<__nv_bfloat16> &a) {
+    if (rows_mma_append_fits(a)) return launch_append_rows_mma(a);
+    if (rows_append_fits(a)) return launch_append_rows(a);
+    if (tc_append_supported(a.n, a.d, a.d_h, a.H, a.r)) return launch_append_tc(a);
+    return launch_append_generic(a);
 }
 
 cudaError_t launch_append_tc(const AppendArgsT<__nv_bfloat16> &a) {

@@ -1,0 +1,355 @@
+// Decode over the block-scaled cache (lrkv_decode_scaled) for any supported shape,
+// and the merge of partial states that both of its kernels use.
+//
+//   x_j  = (2^eSK q.S_K[j] + 2^eRK[h] p.R_K[h,j]) / sqrt(d_h),   p = q B_K[h]
+//   o    = sum_j a_j 2^eSV S_V[j] + (sum_j a_j 2^eRV[h] R_V[h,j]) B_V[h]^T,  a = softmax(x)
+// (reading note "Low-Rank Key Value Attention", equations 6 and 7, on codes and
+// scale exponents).  All in fp32.
+//
+// One CTA takes a part of a request's rows for one head.  A warp takes 32 rows at
+// a time: lane j scores row j (q and p from shared memory), the warp updates its
+// running maximum and sum, then every lane adds the rows' values up for four
+// columns of each 128.  The shared rows are read again by every head (out of
+// L2), and the four warps' states meet in shared memory.
+#include <algorithm>
+
+#include "scaled_kernels.cuh"
+
+namespace lrkv {
+
+namespace {
+
+constexpr int kWarps = 4, kThreads = 32 * kWarps;
+
+struct AnyArgs {
+    ScaledDecodeArgs d;
+    ScaledStates st;
+    int splits;
+    float scale_log2;
+};
+
+__device__ __forceinline__ void widen4(uint32_t w, float (&x)[4]) {
+    const uint32_t a = f16x2_from_e4m3x2((uint16_t)w), b = f16x2_from_e4m3x2((uint16_t)(w >> 16));
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&a));
+    const float2 g = __half22float2(*reinterpret_cast<const __half2 *>(&b));
+    x[0] = f.x; x[1] = f.y; x[2] = g.x; x[3] = g.y;
+}
+// sum of eight codes times y
+__device__ __forceinline__ float dot8(const uint2 &w, const float *y, float s) {
+    float x[4];
+    const float4 a = reinterpret_cast<const float4 *>(y)[0], b = reinterpret_cast<const float4 *>(y)[1];
+    widen4(w.x, x);
+    s = fmaf(x[0], a.x, s); s = fmaf(x[1], a.y, s); s = fmaf(x[2], a.z, s); s = fmaf(x[3], a.w, s);
+    widen4(w.y, x);
+    s = fmaf(x[0], b.x, s); s = fmaf(x[1], b.y, s); s = fmaf(x[2], b.z, s); s = fmaf(x[3], b.w, s);
+    return s;
+}
+
+__global__ void __launch_bounds__(kThreads) decode_scaled_any_kernel(const __grid_constant__ AnyArgs P) {
+    __shared__ __align__(16) float qs[256], ps[256];
+    __shared__ float ms[kWarps], ls[kWarps], red[kWarps][512];
+    const ScaledDecodeArgs &a = P.d;
+    const ScaledPools &c = a.c;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int b = blockIdx.x / P.splits, sp = blockIdx.x % P.splits, h = blockIdx.y;
+    const int d_h = c.d_h, r = c.r, H = c.H, g = h / (H / c.G);
+    pdl_wait();
+    pdl_launch_dependents();
+    const int32_t L = a.seq_lens[b];
+    const bool valid = L >= 1 && (int64_t)L <= (int64_t)a.max_pages * c.page_size;
+    // rows of this part: a multiple of a CTA's step, so that parts are even
+    const int part = valid ? ((L + P.splits - 1) / P.splits + kThreads - 1) / kThreads * kThreads : 0;
+    const int64_t first = (int64_t)sp * part;
+    const int begin = (int)min(first, (int64_t)(valid ? L : 0)), end = (int)min(first + part, (int64_t)(valid ? L : 0));
+
+    const int64_t slot = (int64_t)b * P.splits + sp;
+    float *ml = P.st.ml + (slot * H + h) * 2;
+    if (begin >= end) {  // (an empty part: a state without weight)
+        if (tid == 0) {
+            ml[0] = -INFINITY;
+            ml[1] = 0.f;
+        }
+        return;
+    }
+    const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q) + ((size_t)b * H + h) * d_h;
+    for (int d = tid; d < d_h; d += kThreads) qs[d] = __bfloat162float(q[d]);
+    __syncthreads();
+    const __nv_bfloat16 *B = static_cast<const __nv_bfloat16 *>(a.B_K) + (size_t)h * d_h * r;
+    for (int k = tid; k < r; k += kThreads) {
+        float s = 0.f;
+#pragma unroll 8
+        for (int d = 0; d < d_h; ++d) s = fmaf(qs[d], __bfloat162float(B[(size_t)d * r + k]), s);
+        ps[k] = s;
+    }
+    __syncthreads();
+
+    const int32_t *table = a.page_table + (size_t)(a.req_row ? a.req_row[b] : b) * a.max_pages;
+    const int sw = c.G * d_h, rw = H * r;  // bytes of a token's shared and private row
+    float m = -INFINITY, l = 0.f, as[2][4] = {}, ar[2][4] = {};
+    for (int t0 = begin + 32 * warp; t0 < end; t0 += kThreads) {
+        const int j = t0 + lane;
+        int row = -1;
+        float x = -INFINITY, vs = 0.f, vr = 0.f;
+        if (j < end) {
+            const int32_t page = table[j / c.page_size];
+            if (page < 0 || page >= c.num_pages) status_or(a.status, LRKV_STATUS_BAD_PAGE);
+            else row = page * c.page_size + j % c.page_size;
+        }
+        if (row >= 0) {
+            const int64_t eb = row / c.block;
+            const int e0 = c.exp[0][eb * c.G + g], e1 = c.exp[1][eb * c.G + g], e2 = c.exp[2][eb * H + h],
+                      e3 = c.exp[3][eb * H + h];
+            const uint8_t *sk = c.code[0] + (int64_t)row * sw + g * d_h, *rk = c.code[2] + (int64_t)row * rw + h * r;
+            float s = 0.f, t = 0.f;
+            for (int d = 0; d < d_h; d += 8) s = dot8(*reinterpret_cast<const uint2 *>(sk + d), qs + d, s);
+            for (int k = 0; k < r; k += 8) t = dot8(*reinterpret_cast<const uint2 *>(rk + k), ps + k, t);
+            x = (s * exp2i(clamp_exp(e0)) + t * exp2i(clamp_exp(e2))) * P.scale_log2;
+            vs = exp2i(clamp_exp(e1));
+            vr = exp2i(clamp_exp(e3));
+        }
+        float mt = x;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, o));
+        const float mn = fmaxf(m, mt);
+        const float ref = mn == -INFINITY ? 0.f : mn;
+        const float alpha = exp2f(m - ref), w = exp2f(x - ref);
+        m = mn;
+        l = l * alpha + w;
+        vs *= w;
+        vr *= w;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                as[i][e] *= alpha;
+                ar[i][e] *= alpha;
+            }
+        const int rows = min(32, end - t0);
+        for (int t = 0; t < rows; ++t) {
+            const int rt = __shfl_sync(0xffffffffu, row, t);
+            const float ws = __shfl_sync(0xffffffffu, vs, t), wr = __shfl_sync(0xffffffffu, vr, t);
+            if (rt < 0) continue;
+            const uint8_t *sv = c.code[1] + (int64_t)rt * sw + g * d_h, *rv = c.code[3] + (int64_t)rt * rw + h * r;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int col = 4 * lane + 128 * i;
+                float y[4];
+                if (col < d_h) {
+                    widen4(*reinterpret_cast<const uint32_t *>(sv + col), y);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) as[i][e] = fmaf(ws, y[e], as[i][e]);
+                }
+                if (col < r) {
+                    widen4(*reinterpret_cast<const uint32_t *>(rv + col), y);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) ar[i][e] = fmaf(wr, y[e], ar[i][e]);
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    if (lane == 0) {
+        ms[warp] = m;
+        ls[warp] = l;
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int col = 4 * lane + 128 * i;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (col < d_h) red[warp][col + e] = as[i][e];
+            if (col < r) red[warp][256 + col + e] = ar[i][e];
+        }
+    }
+    __syncthreads();
+    float M = ms[0];
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) M = fmaxf(M, ms[w]);
+    const float ref = M == -INFINITY ? 0.f : M;
+    float f[kWarps], lt = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        f[w] = exp2f(ms[w] - ref);
+        lt += ls[w] * f[w];
+    }
+    float *acc = P.st.acc + slot * H * (d_h + r);
+    for (int i = tid; i < d_h + r; i += kThreads) {
+        const int at = i < d_h ? i : 256 + i - d_h;
+        float s = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) s += red[w][at] * f[w];
+        if (i < d_h) acc[(size_t)h * d_h + i] = s;
+        else acc[(size_t)H * d_h + h * r + i - d_h] = s;
+    }
+    if (tid == 0) {
+        ml[0] = M;
+        ml[1] = lt;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Merge: one CTA per (request, head).  o = (sum_s f_s accS_s + (sum_s f_s accR_s)
+// B_V[h]^T) / sum_s f_s l_s with f_s = 2^(m_s - max m).  Groups of threads, one thread
+// a column, take the states in turn.
+// ---------------------------------------------------------------------------
+constexpr int kMergeThreads = 512, kMergeStates = 256;
+
+__global__ void __launch_bounds__(kMergeThreads) scaled_merge_kernel(const __grid_constant__ ScaledMergeArgs P) {
+    __shared__ float fs[kMergeStates], sums[kMergeThreads];
+    __shared__ float red[2][kMergeThreads / 32];
+    const int h = blockIdx.y, b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int H = P.H, d_h = P.d_h, r = P.r, W = d_h + r, cols = (W + 31) & ~31;
+    pdl_wait();
+    pdl_launch_dependents();
+    const int32_t L = P.seq_lens[b];
+    if (P.leave && L == -1) return;
+    int64_t s0 = 0;
+    int ns = 0;
+    if (L < 1 || L > P.max_len) {
+        if (h == 0 && tid == 0) status_or(P.status, LRKV_STATUS_BAD_SEQLEN);
+    } else if (P.off) {
+        // the CTAs whose units [g U / G, (g + 1) U / G) meet the request's
+        const int64_t U = P.off[P.B], G = min((int64_t)P.grid, U), u0 = P.off[b], u1 = P.off[b + 1] - 1;
+        const int64_t g0 = ((u0 + 1) * G - 1) / U, g1 = ((u1 + 1) * G - 1) / U;
+        s0 = b + g0;
+        ns = (int)(g1 - g0) + 1;
+    } else {
+        s0 = (int64_t)b * P.splits;
+        ns = P.splits;
+    }
+    // (at most 256 parts or one state a CTA)
+    float m = -INFINITY, l = 0.f;
+    if (tid < ns) {
+        m = P.st.ml[((s0 + tid) * H + h) * 2];
+        l = P.st.ml[((s0 + tid) * H + h) * 2 + 1];
+    }
+    float M = m;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    if (lane == 0) red[0][warp] = M;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kMergeThreads / 32; ++w) M = fmaxf(M, red[0][w]);
+    const float ref = M == -INFINITY ? 0.f : M;
+    // a part without rows has written no value sums
+    const bool none = m == -INFINITY && l == 0.f;
+    const float f = none ? 0.f : exp2f(m - ref);
+    if (tid < kMergeStates) fs[tid] = none ? -1.f : f;
+    l = none ? 0.f : l * f;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    if (lane == 0) red[1][warp] = l;
+    __syncthreads();
+    l = 0.f;
+#pragma unroll
+    for (int w = 0; w < kMergeThreads / 32; ++w) l += red[1][w];
+    const float inv = l != 0.f ? 1.f / l : 0.f;  // (NaN stays NaN)
+
+    const int groups = kMergeThreads / cols, g = tid / cols, c = tid - g * cols;
+    float x = 0.f;
+    if (g < groups && c < W) {
+        const float *acc = P.st.acc + s0 * H * W + (c < d_h ? (size_t)h * d_h + c : (size_t)H * d_h + h * r + c - d_h);
+#pragma unroll 4
+        for (int s = g; s < ns; s += groups) {
+            const float k = fs[s];
+            if (k >= 0.f || k != k) x += k * acc[(int64_t)s * H * W];
+        }
+    }
+    sums[tid] = x;
+    __syncthreads();
+    if (g == 0 && c < W) {
+        for (int k = 1; k < groups; ++k) x += sums[k * cols + c];
+        sums[c] = x;
+    }
+    __syncthreads();
+    const __nv_bfloat16 *B = static_cast<const __nv_bfloat16 *>(P.B_V) + (size_t)h * d_h * r;
+    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(P.out) + ((size_t)b * H + h) * d_h;
+    for (int d = tid; d < d_h; d += kMergeThreads) {
+        float s = sums[d];
+#pragma unroll 4
+        for (int k = 0; k < r; k += 8) {
+            float y[8];
+            Vec16<__nv_bfloat16>::load(B + (size_t)d * r + k, y);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s = fmaf(sums[d_h + k + e], y[e], s);
+        }
+        out[d] = __float2bfloat16_rn(s * inv);
+    }
+}
+
+__global__ void scaled_row_queries_kernel(const __grid_constant__ ScaledRows rows, int max_len, int32_t *len,
+                                          int32_t *req_row) {
+    pdl_wait();
+    pdl_launch_dependents();
+    const int i = blockIdx.x * blockDim.x + threadIdx.x;
+    if (i >= rows.n) return;
+    int lo = 0, hi = rows.B;  // first request whose rows end past i
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (rows.cu_rows[mid + 1] > i) hi = mid;
+        else lo = mid + 1;
+    }
+    if (lo == rows.B || rows.cu_rows[lo] > i) {
+        len[i] = -1;
+        req_row[i] = 0;
+        return;
+    }
+    const int64_t pos = (int64_t)rows.start_pos[lo] + (i - rows.cu_rows[lo]);
+    len[i] = pos >= 0 && pos < max_len ? (int)pos + 1 : 0;
+    req_row[i] = lo;
+}
+
+// Parts per request: enough CTAs for the device, of at least 128 rows each.
+int any_splits(const ScaledPools &c, int B, int max_seq_len) {
+    const int64_t most = (max_seq_len + kThreads - 1) / kThreads;
+    const int64_t want = (8 * (int64_t)device_sm_count() + (int64_t)B * c.H - 1) / ((int64_t)B * c.H);
+    return (int)std::max<int64_t>(1, std::min<int64_t>({most, want, 256}));
+}
+
+}  // namespace
+
+size_t scaled_any_ws_bytes(const ScaledPools &c, int B, int max_seq_len) {
+    // B * splits is at most 8 SMs / H + B, which grows with B, and at most 256 B
+    const int64_t slots = std::min<int64_t>(8 * (int64_t)device_sm_count() / c.H + 1 + B,
+                                            (int64_t)B * std::min<int64_t>((max_seq_len + kThreads - 1) / kThreads, 256));
+    return scaled_states_bytes(slots, c.H, c.d_h, c.r);
+}
+
+cudaError_t launch_decode_scaled_any(const ScaledDecodeArgs &a, void *ws) {
+    AnyArgs P;
+    P.d = a;
+    P.splits = any_splits(a.c, a.B, a.max_seq_len);
+    P.st = scaled_states(ws, (int64_t)a.B * P.splits, a.c.H);
+    P.scale_log2 = 1.4426950408889634f / sqrtf((float)a.c.d_h);
+    cudaError_t e = launch_pdl(decode_scaled_any_kernel, dim3((unsigned)(a.B * P.splits), a.c.H), dim3(kThreads), 0,
+                               a.stream, P);
+    if (e != cudaSuccess) return e;
+    ScaledMergeArgs m;
+    m.st = P.st;
+    m.off = nullptr;
+    m.splits = P.splits;
+    m.grid = 0;
+    m.seq_lens = a.seq_lens;
+    m.max_len = a.max_pages * a.c.page_size;
+    m.leave = a.req_row != nullptr;
+    m.B_V = a.B_V;
+    m.out = a.out;
+    m.B = a.B;
+    m.H = a.c.H;
+    m.d_h = a.c.d_h;
+    m.r = a.c.r;
+    m.status = a.status;
+    return launch_scaled_merge(m, a.stream);
+}
+
+cudaError_t launch_scaled_row_queries(const ScaledRows &rows, int max_len, int32_t *len, int32_t *req_row,
+                                      cudaStream_t s) {
+    return launch_pdl(scaled_row_queries_kernel, dim3((rows.n + 255) / 256), dim3(256), 0, s, rows, max_len, len, req_row);
+}
+
+cudaError_t launch_scaled_merge(const ScaledMergeArgs &m, cudaStream_t s) {
+    return launch_pdl(scaled_merge_kernel, dim3(m.B, m.H), dim3(kMergeThreads), 0, s, m);
+}
+
+}  // namespace lrkv

@@ -7,6 +7,7 @@
 #include <mutex>
 #include <vector>
 
+#include "api_common.cuh"
 #include "append_kernels.cuh"
 #include "decode_kernels.cuh"
 #include "page_kernels.cuh"
@@ -15,7 +16,7 @@ namespace lrkv {
 
 static thread_local int g_last_cuda_error = 0;
 
-static int cuda_fail(cudaError_t e) {
+int cuda_fail(cudaError_t e) {
     g_last_cuda_error = (int)e;
     return LRKV_E_CUDA;
 }
@@ -31,11 +32,11 @@ struct Profiler {
 static bool g_prof_on = false;
 static Profiler g_prof[3];
 
-static void prof_before(int kind, cudaStream_t s) {
+void prof_before(int kind, cudaStream_t s) {
     Profiler &p = g_prof[kind];
     if (g_prof_on && p.n < Profiler::kCap) cudaEventRecord(p.ev[2 * p.n], s);
 }
-static void prof_after(int kind, cudaStream_t s) {
+void prof_after(int kind, cudaStream_t s) {
     Profiler &p = g_prof[kind];
     if (g_prof_on && p.n < Profiler::kCap) {
         cudaEventRecord(p.ev[2 * p.n + 1], s);
@@ -74,13 +75,11 @@ cudaError_t smem_limit_once(const void *kern, int bytes) {
     return e;
 }
 
-static bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-static bool aligned256(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 255u) == 0; }
 
 // Bytes of one cache element (the pools); activations of an 8-bit cache are bf16.
 static int elem_bytes(int dtype) { return dtype == LRKV_F32 ? 4 : dtype == LRKV_BF16 ? 2 : 1; }
 
-static int check_dims(int H, int d_h, int r, int dtype) {
+int check_dims(int H, int d_h, int r, int dtype) {
     if (dtype != LRKV_F32 && dtype != LRKV_BF16 && dtype != LRKV_FP8_E4M3) return LRKV_E_DTYPE;
     if (H < 1 || H > 128 || d_h < 1 || d_h > 256 || r < 1 || r > 256) return LRKV_E_SHAPE;
     if (dtype == LRKV_FP8_E4M3) {  // 16-byte rows of codes; bf16 activations
@@ -289,10 +288,7 @@ static int run_append(const void *X, const int32_t *positions, const int32_t *se
             a.cu_rows = rows->cu_rows;
             a.start_pos = rows->start_pos;
         }
-        if (rows_mma_append_fits(a)) e = launch_append_rows_mma(a);
-        else if (rows_append_fits(a)) e = launch_append_rows(a);
-        else if (tc_append_supported(n, d, c->d_h, c->H, c->r)) e = launch_append_tc(a);
-        else e = launch_append_generic(a);
+        e = dispatch_append(a);
     } else {
         auto a = make_append_args<float>(X, positions, seq_ids, n, d, W_S_K, W_S_V, U_K, U_V, c,
                                          page_table, B, max_pages, status, s);

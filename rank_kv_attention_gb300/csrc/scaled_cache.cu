@@ -1,0 +1,385 @@
+// Writing, reading back and laying out the block-scaled cache (lrkv_write_scaled,
+// lrkv_read_scaled, and the bf16 layout that lrkv_prefill_scaled attends).
+//
+// value = code * 2^e: codes E4M3, one exponent per (block of tokens, head) of each
+// pool, the least with which the block's largest magnitude a fits, a <= 448 * 2^e.
+// Both directions move bytes and do next to nothing with them: bound by HBM for many
+// rows and by dependent lookups (row -> request -> page -> block) for few.
+#include <algorithm>
+
+#include "scaled_kernels.cuh"
+
+namespace lrkv {
+
+namespace {
+
+// ---------------------------------------------------------------------------
+// Writing.  The unit is the rows of one call in one block: those of request b
+// from its first row to the end of that row's block, then whole blocks.  Unit u
+// is found without a prefix sum: number request b's first unit key(b) =
+// cu_rows[b] / block + 2 b, and the unit that begins at row i after it i / block +
+// 2 b + 1.  These grow strictly (a later unit's row is at least `block` further on, and
+// the next request's key counts two more), so u has one owner: the last b with
+// key(b) <= u.  A few u have none; there are n / block + 2 B of them.
+//
+// One warp takes one head (shared rows: one group) of one pool of a unit: it
+// holds the values in registers where they fit (16 vectors a lane: 64 rows of
+// 64 bf16), takes their maximum, and writes the codes; longer ones are read
+// twice, the second time out of L1 or L2.
+// ---------------------------------------------------------------------------
+constexpr int kWriteWarps = 8, kHeld = 16;
+
+// The last b in [0, B) with cu[b] / block + 2 b <= u, or -1 (whole warp).
+__device__ __forceinline__ int request_of_unit(const int32_t *cu, int B, int block, int64_t u, int lane) {
+    int lo = 0, hi = B;
+    bool any = false;
+    do {
+        const int step = (hi - lo + 31) / 32, i = lo + lane * step;
+        const bool le = i < hi && (int64_t)(cu[i] / block) + 2 * (int64_t)i <= u;
+        const uint32_t no = ~__ballot_sync(0xffffffffu, le);
+        const int k = no ? __ffs(no) - 1 : 32;  // probes that hold
+        if (k == 0) return any ? lo : -1;
+        any = true;
+        lo += (k - 1) * step;
+        hi = min(hi, lo + step);
+    } while (hi - lo > 1);
+    return lo;
+}
+
+template <typename T> struct Bits;
+template <> struct Bits<__nv_bfloat16> {
+    static constexpr int V = 8;  // elements of a 16-byte vector
+    // largest magnitude's bits of the four words' halves, as fp32 bits
+    __device__ static uint32_t top(const uint4 &v) {
+        const uint32_t w[4] = {v.x & 0x7fff7fffu, v.y & 0x7fff7fffu, v.z & 0x7fff7fffu, v.w & 0x7fff7fffu};
+        const uint32_t m = __vmaxu2(__vmaxu2(w[0], w[1]), __vmaxu2(w[2], w[3]));
+        return max(m << 16, m & 0xffff0000u);
+    }
+    __device__ static void get(const uint4 &v, float (&x)[8]) {
+        x[0] = bf16lo(v.x); x[1] = bf16hi(v.x); x[2] = bf16lo(v.y); x[3] = bf16hi(v.y);
+        x[4] = bf16lo(v.z); x[5] = bf16hi(v.z); x[6] = bf16lo(v.w); x[7] = bf16hi(v.w);
+    }
+};
+template <> struct Bits<float> {
+    static constexpr int V = 4;
+    __device__ static uint32_t top(const uint4 &v) {
+        return max(max(v.x & 0x7fffffffu, v.y & 0x7fffffffu), max(v.z & 0x7fffffffu, v.w & 0x7fffffffu));
+    }
+    __device__ static void get(const uint4 &v, float (&x)[4]) {
+        x[0] = __uint_as_float(v.x); x[1] = __uint_as_float(v.y); x[2] = __uint_as_float(v.z); x[3] = __uint_as_float(v.w);
+    }
+};
+
+constexpr uint32_t kInf = 0x7f800000u;
+
+// The same over a vector's finite values (0 where it has none).
+template <typename T>
+__device__ __forceinline__ uint32_t top_finite(const uint4 &v) {
+    float x[Bits<T>::V];
+    Bits<T>::get(v, x);
+    uint32_t m = 0;
+#pragma unroll
+    for (int e = 0; e < Bits<T>::V; ++e) {
+        const uint32_t u = __float_as_uint(x[e]) & 0x7fffffffu;
+        if (u < kInf) m = max(m, u);
+    }
+    return m;
+}
+
+// Codes of one vector of values times `inv`; `odd`: there may be infinities (which
+// the conversion would saturate) among them.
+template <typename T>
+__device__ __forceinline__ void put_codes(uint8_t *dst, const uint4 &v, float inv, bool odd) {
+    constexpr int V = Bits<T>::V;
+    float x[V];
+    Bits<T>::get(v, x);
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+        if (odd && (__float_as_uint(x[e]) & 0x7fffffffu) == kInf) x[e] = __uint_as_float(0x7fffffffu);
+        x[e] *= inv;
+    }
+    uint32_t w[V / 4];
+#pragma unroll
+    for (int e = 0; e < V / 4; ++e)
+        w[e] = (uint32_t)e4m3x2_from_f32(x[4 * e], x[4 * e + 1]) |
+               ((uint32_t)e4m3x2_from_f32(x[4 * e + 2], x[4 * e + 3]) << 16);
+    if constexpr (V == 8) *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
+    else *reinterpret_cast<uint32_t *>(dst) = w[0];
+}
+
+// Four codes times s, rounded to codes again.
+__device__ __forceinline__ uint32_t shrink_codes(uint32_t w, float s) {
+    uint32_t r = 0;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const uint32_t h2 = f16x2_from_e4m3x2((uint16_t)(w >> (16 * k)));
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h2));
+        r |= (uint32_t)e4m3x2_from_f32(f.x * s, f.y * s) << (16 * k);
+    }
+    return r;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(32 * kWriteWarps) write_scaled_kernel(const __grid_constant__ ScaledWriteArgs a) {
+    constexpr int V = Bits<T>::V;
+    const ScaledPools &c = a.c;
+    const int lane = threadIdx.x & 31;
+    const int64_t u = blockIdx.x;
+    int item = blockIdx.y * kWriteWarps + (threadIdx.x >> 5);
+    pdl_wait();
+    pdl_launch_dependents();
+    if (item >= 2 * (c.G + c.H)) return;
+    const bool speaks = item == 0 && lane == 0;  // flags a unit's faults
+    // pool and head
+    int k = 0;
+    while (item >= c.heads(k)) item -= c.heads(k++);
+    const int heads = c.heads(k), width = c.width(k);
+
+    // ---- the unit's rows i0 .. i1 - 1, from position p0 on
+    const int b = request_of_unit(a.rows.cu_rows, a.rows.B, c.block, u, lane);
+    if (b < 0) return;
+    const int r0 = a.rows.cu_rows[b], r1 = min(a.rows.cu_rows[b + 1], a.rows.n);
+    const int start = a.rows.start_pos[b];
+    if (r0 < 0 || r0 >= r1) return;
+    const int64_t max_len = (int64_t)a.rows.max_pages * c.page_size;
+    const int64_t ra = r0 + max((int64_t)0, -(int64_t)start);           // first row at a position >= 0
+    const int64_t rz = min((int64_t)r1, r0 + max_len - (int64_t)start);  // rows past the table start here
+    const int64_t key = u - (r0 / c.block + 2 * (int64_t)b);
+    if (key == 0 && speaks && (ra > r0 || rz < r1)) status_or(a.rows.status, LRKV_STATUS_BAD_ROW);
+    if (ra >= rz) return;
+    const int64_t pa = (int64_t)start + (ra - r0);  // its position
+    const int64_t i2 = ra + c.block - pa % c.block;  // first row of the second unit
+    int64_t i0 = ra, i1 = i2;
+    if (key > 0) {
+        const int64_t m = u - 2 * (int64_t)b - 1 - i2 / c.block;
+        if (m < 0) return;
+        i0 = i2 + m * c.block;
+        i1 = i0 + c.block;
+    }
+    i1 = min(i1, rz);
+    if (i0 >= i1) return;
+    const int p0 = (int)(pa + (i0 - ra));
+
+    // ---- values: vector v of the unit is row v / vpr, vector v % vpr of the head
+    const int vpr = width / V, nv = (int)(i1 - i0) * vpr;
+    const uint32_t magic = 0xffffffffu / (uint32_t)vpr + 1u;  // 2^32 / vpr rounded up; v < 2^17: exact
+    auto row_of = [&](int v) { return vpr == 1 ? v : (int)__umulhi((uint32_t)v, magic); };
+    const int64_t ld = a.ld[k];
+    const T *x = static_cast<const T *>(a.x[k]) + i0 * ld + item * width;
+    auto at = [&](int v) -> const uint4 * {
+        const int row = row_of(v);
+        return reinterpret_cast<const uint4 *>(x + row * ld + (v - row * vpr) * V);
+    };
+    const bool held = nv <= 32 * kHeld;
+    uint4 val[kHeld];
+    uint32_t top = 0;
+    if (held) {
+#pragma unroll
+        for (int j = 0; j < kHeld; ++j)
+            if (lane + 32 * j < nv) val[j] = *at(lane + 32 * j);
+    }
+    // (the lookups of the destination are on their way meanwhile)
+    const int32_t page = a.rows.page_table[(size_t)b * a.rows.max_pages + p0 / c.page_size];
+    if (page < 0 || page >= c.num_pages) {
+        if (speaks) status_or(a.rows.status, LRKV_STATUS_BAD_PAGE);
+        return;
+    }
+    const int slot = p0 % c.page_size, before = slot % c.block;
+    const int nb = c.page_size / c.block;
+    uint8_t *eb = c.exp[k] + ((int64_t)page * nb + slot / c.block) * heads + item;
+    const int old = before ? clamp_exp(*eb) : LRKV_SCALED_MIN_EXP;
+    uint8_t *code = c.code[k] + ((int64_t)page * c.page_size + slot) * heads * width + item * width;
+    const int row_bytes = heads * width;
+
+    if (held) {
+#pragma unroll
+        for (int j = 0; j < kHeld; ++j)
+            if (lane + 32 * j < nv) top = max(top, Bits<T>::top(val[j]));
+    } else {
+        for (int v = lane; v < nv; v += 32) top = max(top, Bits<T>::top(*at(v)));
+    }
+    top = __reduce_max_sync(0xffffffffu, top);
+    const bool odd = top >= kInf;  // infinities or NaN: the finite ones decide
+    if (odd) {
+        top = 0;
+        for (int v = lane; v < nv; v += 32) top = max(top, top_finite<T>(*at(v)));
+        top = __reduce_max_sync(0xffffffffu, top);
+    }
+    const int e = max(old, needed_exp(__uint_as_float(top)));
+    const float inv = exp2i(-e);
+    auto put = [&](int v, const uint4 &w) {
+        const int row = row_of(v);
+        put_codes<T>(code + (int64_t)row * row_bytes + (v - row * vpr) * V, w, inv, odd);
+    };
+    if (held) {
+#pragma unroll
+        for (int j = 0; j < kHeld; ++j)
+            if (lane + 32 * j < nv) put(lane + 32 * j, val[j]);
+    } else {
+        for (int v = lane; v < nv; v += 32) put(v, *at(v));
+    }
+    // ---- rows of the block before the new ones, where the scale grew
+    if (before && e > old) {
+        const float s = exp2i(max(old - e, -126));  // (2^-126 of any code rounds to zero too)
+        const int w8 = width / 8;
+        uint8_t *first = code - (int64_t)before * row_bytes;
+        for (int v = lane; v < before * w8; v += 32) {
+            uint2 *p = reinterpret_cast<uint2 *>(first + (int64_t)(v / w8) * row_bytes + (v % w8) * 8);
+            const uint2 w = *p;
+            *p = make_uint2(shrink_codes(w.x, s), shrink_codes(w.y, s));
+        }
+    }
+    if (lane == 0 && (before == 0 || e > old)) *eb = (uint8_t)(e + 127);
+}
+
+// ---------------------------------------------------------------------------
+// Reading.  A CTA takes 16 rows; a thread takes 8 columns (which lie in one head)
+// of all of them, so a warp reads 256 consecutive bytes of a row.
+// ---------------------------------------------------------------------------
+constexpr int kReadRows = 16, kReadThreads = 256;
+
+// Eight codes times 2^e.
+__device__ __forceinline__ void widen8(const uint2 &w, float s, float (&x)[8]) {
+    const uint32_t u[2] = {w.x, w.y};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const uint32_t h2 = f16x2_from_e4m3x2((uint16_t)(u[k >> 1] >> (16 * (k & 1))));
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h2));
+        x[2 * k] = f.x * s;
+        x[2 * k + 1] = f.y * s;
+    }
+}
+__device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&x)[8]) {
+    *reinterpret_cast<uint4 *>(p) =
+        make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+}
+__device__ __forceinline__ void store8(float *p, const float (&x)[8]) {
+    reinterpret_cast<float4 *>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+    reinterpret_cast<float4 *>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+}
+
+// Rows src[i] of the cache (-1: none) to rows dst[i] of y.
+template <typename T>
+__device__ __forceinline__ void copy_rows(const ScaledPools &c, const int *src, const int *dst, void *const *y,
+                                          const int64_t *ld) {
+    const int chunks = (c.G * c.d_h + c.H * c.r) / 4;  // of 8 columns, in a row of all pools
+    for (int ch = threadIdx.x; ch < chunks; ch += kReadThreads) {
+        int k = 0, col = 8 * ch;
+        while (col >= c.heads(k) * c.width(k)) {
+            col -= c.heads(k) * c.width(k);
+            ++k;
+        }
+        const int heads = c.heads(k), row_bytes = heads * c.width(k), head = col / c.width(k);
+        const uint8_t *code = c.code[k] + col, *exp = c.exp[k] + head;
+        T *out = static_cast<T *>(y[k]) + col;
+        const int64_t ldk = ld[k];
+#pragma unroll
+        for (int i0 = 0; i0 < kReadRows; i0 += 8) {
+            uint2 w[8];
+            int e[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int s = src[i0 + i];
+                if (s >= 0) {
+                    w[i] = *reinterpret_cast<const uint2 *>(code + (int64_t)s * row_bytes);
+                    e[i] = exp[(int64_t)(s / c.block) * heads];
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (src[i0 + i] < 0) continue;
+                float x[8];
+                widen8(w[i], exp2i(clamp_exp(e[i])), x);
+                store8(out + (int64_t)dst[i0 + i] * ldk, x);
+            }
+        }
+    }
+}
+
+// Pool row of position `pos` of request b, or -1.
+__device__ __forceinline__ int pool_row(const ScaledPools &c, const ScaledRows &r, int b, int64_t pos) {
+    if (pos < 0 || pos >= (int64_t)r.max_pages * c.page_size) {
+        status_or(r.status, LRKV_STATUS_BAD_ROW);
+        return -1;
+    }
+    const int32_t page = r.page_table[(size_t)b * r.max_pages + pos / c.page_size];
+    if (page < 0 || page >= c.num_pages) {
+        status_or(r.status, LRKV_STATUS_BAD_PAGE);
+        return -1;
+    }
+    return page * c.page_size + (int)(pos % c.page_size);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kReadThreads) read_scaled_kernel(const __grid_constant__ ScaledReadArgs a) {
+    __shared__ int src[kReadRows], dst[kReadRows];
+    pdl_wait();
+    pdl_launch_dependents();
+    if (threadIdx.x < kReadRows) {
+        const int i = blockIdx.x * kReadRows + threadIdx.x;
+        int s = -1;
+        if (i < a.rows.n) {
+            int lo = 0, hi = a.rows.B;  // first request whose rows end past i
+            while (lo < hi) {
+                const int mid = (lo + hi) >> 1;
+                if (a.rows.cu_rows[mid + 1] > i) hi = mid;
+                else lo = mid + 1;
+            }
+            if (lo < a.rows.B && a.rows.cu_rows[lo] <= i)
+                s = pool_row(a.c, a.rows, lo, (int64_t)a.rows.start_pos[lo] + (i - a.rows.cu_rows[lo]));
+        }
+        src[threadIdx.x] = s;
+        dst[threadIdx.x] = i;
+    }
+    __syncthreads();
+    copy_rows<T>(a.c, src, dst, a.y, a.ld);
+}
+
+__global__ void __launch_bounds__(kReadThreads) expand_scaled_kernel(const __grid_constant__ ScaledExpandArgs a,
+                                                                     int tiles) {
+    __shared__ int src[kReadRows], dst[kReadRows];
+    __shared__ int64_t ld[4];
+    pdl_wait();
+    pdl_launch_dependents();
+    const int b = blockIdx.x / tiles, p0 = (blockIdx.x % tiles) * kReadRows;
+    const int r0 = a.rows.cu_rows[b], r1 = min(a.rows.cu_rows[b + 1], a.rows.n);
+    const int64_t ctx = r0 >= 0 && r0 < r1 ? min((int64_t)a.max_ctx, (int64_t)a.rows.start_pos[b] + (r1 - r0)) : 0;
+    const bool live = p0 < ctx;
+    if (!live && !(a.table && p0 % 64 == 0)) return;
+    if (threadIdx.x < 4) ld[threadIdx.x] = (int64_t)a.c.heads(threadIdx.x) * a.c.width(threadIdx.x);
+    if (threadIdx.x < kReadRows) {
+        const int p = p0 + threadIdx.x;
+        const int s = p < ctx ? pool_row(a.c, a.rows, b, p) : -1;
+        src[threadIdx.x] = s;
+        dst[threadIdx.x] = a.table ? b * a.pages * 64 + p : s;
+        // (a cache page holds whole pages of 64 rows: one is missing where its first row is)
+        if (a.table && threadIdx.x == 0 && p0 % 64 == 0) a.table[(size_t)b * a.pages + p0 / 64] = s >= 0 ? b * a.pages + p0 / 64 : -1;
+    }
+    __syncthreads();
+    if (!live) return;
+    copy_rows<__nv_bfloat16>(a.c, src, dst, a.y, ld);
+}
+
+}  // namespace
+
+cudaError_t launch_write_scaled(const ScaledWriteArgs &a) {
+    const int64_t units = a.rows.n / a.c.block + 2 * (int64_t)a.rows.B;
+    const int items = 2 * (a.c.G + a.c.H);
+    const dim3 grid((unsigned)std::min<int64_t>(units, INT32_MAX), (items + kWriteWarps - 1) / kWriteWarps);
+    return a.f32 ? launch_pdl(write_scaled_kernel<float>, grid, dim3(32 * kWriteWarps), 0, a.stream, a)
+                 : launch_pdl(write_scaled_kernel<__nv_bfloat16>, grid, dim3(32 * kWriteWarps), 0, a.stream, a);
+}
+
+cudaError_t launch_read_scaled(const ScaledReadArgs &a) {
+    const dim3 grid((a.rows.n + kReadRows - 1) / kReadRows);
+    return a.f32 ? launch_pdl(read_scaled_kernel<float>, grid, dim3(kReadThreads), 0, a.stream, a)
+                 : launch_pdl(read_scaled_kernel<__nv_bfloat16>, grid, dim3(kReadThreads), 0, a.stream, a);
+}
+
+cudaError_t launch_expand_scaled(const ScaledExpandArgs &a) {
+    const int tiles = (a.max_ctx + kReadRows - 1) / kReadRows;
+    return launch_pdl(expand_scaled_kernel, dim3((unsigned)(a.rows.B * (int64_t)tiles)), dim3(kReadThreads), 0, a.stream, a,
+                      tiles);
+}
+
+}  // namespace lrkv
