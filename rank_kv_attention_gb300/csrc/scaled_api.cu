@@ -136,13 +136,14 @@ cudaError_t run_append_scaled(const void *X, const ScaledRows &rows, int d, cons
 
 int run_decode_scaled(const ScaledDecodeArgs &a, void *ws) {
     prof_before(LRKV_PROFILE_ATTENTION, a.stream);
-    const cudaError_t e = launch_decode_scaled_any(a, ws);
+    const bool tc = !a.req_row && scaled_tc_covers(a.c);
+    const cudaError_t e = tc ? launch_decode_scaled_tc(a, ws) : launch_decode_scaled_any(a, ws);
     prof_after(LRKV_PROFILE_ATTENTION, a.stream);
     return e == cudaSuccess ? LRKV_OK : cuda_fail(e);
 }
 
 size_t decode_scaled_ws_bytes(const ScaledPools &c, int B, int max_seq_len) {
-    return scaled_any_ws_bytes(c, B, max_seq_len);
+    return scaled_tc_covers(c) ? scaled_tc_ws_bytes(c, B) : scaled_any_ws_bytes(c, B, max_seq_len);
 }
 
 // Prefill workspace: the projected rows; then, tiled, the bf16 pools of the values with
