@@ -35,9 +35,9 @@
 // operands (and the offsets that the merge needs), while the first tiles are on
 // their way.
 //
-// 11 warps: 0-3 scores and weights (thread = token = tensor-memory lane), 4-7 value
-// accumulators (thread = column), 8 copies cache tiles, 9 issues the MMAs, 10 copies
-// operands.  Order of the stream: keys of tile i + 1, then values of tile i, so a
+// 24 warps: 0-15 scores and weights (thread = token = tensor-memory lane, a quarter of
+// the heads each), 16-19 value accumulators (thread = column), one copies cache tiles,
+// one issues the MMAs, one copies operands.  Order of the stream: keys of tile i + 1, then values of tile i, so a
 // tile's softmax runs while the next keys arrive.
 #include <algorithm>
 
@@ -51,7 +51,9 @@ namespace {
 constexpr int kUnit = 64, kTile = 128;
 constexpr int kStageBytes = kTile * 128;
 constexpr int kMaxBoxes = 16, kMaxStages = 12;
-constexpr int kThreads = 352;
+// Warps: 16 of the softmax, 4 accumulating, then copies, operands, MMAs and tensor memory.
+constexpr int kSoftmax = 512, kThreads = kSoftmax + 256;
+constexpr int kWarpCopy = kSoftmax / 32 + 4, kWarpMma = kWarpCopy + 1, kWarpImage = kWarpCopy + 2, kWarpSpare = kWarpCopy + 3;
 constexpr int kSmemMost = 232448;
 
 // Layout of one shape: the R columns in boxes of 128, which heads they hold, and
@@ -116,23 +118,27 @@ struct Offsets {
         img = s.stages * kStageBytes;
         const int one = (s.img_bytes + 1023) / 1024 * 1024;
         weights = img + 2 * one;
-        red = weights + 2 * s.wrows * 128;  // [2][4][H][4 warps]: maxima, sums of the weights
-        fac = red + 2 * 4 * 32 * 4 * 4;     // [2][3][H]: alpha, shared and private factor
-        bars = fac + 2 * 3 * 32 * 4;
-        bytes = bars + 512 + 1024;
+        red = weights + 4 * s.wrows * 128;  // [2][4 quarters of the heads][maxima 3, sum][8][4 warps]
+        fac = red + 2 * 4 * 4 * 8 * 4 * 4;  // [4][3][32]: alpha, shared and private factor
+        bars = fac + 4 * 3 * 32 * 4;
+        bytes = bars + 1152 + 1024;
     }
 };
 
 struct Bars {
     uint64_t full[kMaxStages], empty[kMaxStages];
     uint64_t img_full[2], img_empty[2];
-    uint64_t sc_full, sc_empty, w_full, pv_done, v_empty;
-    uint64_t meet;  // of the 128 softmax threads
+    uint64_t w_full[2], pv_done[2];
+    uint64_t meet[4];  // of the 128 softmax threads of a quarter of the heads
+    uint64_t sc_full, sc_empty, v_empty;
+    // of every box (0: the shared rows): operand's offset, accumulator's column,
+    // instruction descriptor and (keys) contraction steps
+    alignas(16) uint4 kbox[kMaxBoxes + 1], vbox[kMaxBoxes + 1];
     uint32_t tmem;
     int first_b, first_unit, units;
     int warp_sum[kThreads / 32];
 };
-static_assert(sizeof(Bars) <= 512, "barriers");
+static_assert(sizeof(Bars) <= 1152, "barriers");
 
 struct Maps {
     CUtensorMap k[2], v[2];  // S_K, R_K; S_V, R_V: [rows][bytes], box 128 bytes x box_rows
@@ -161,6 +167,16 @@ __device__ __forceinline__ float warp_max(float x) {
     float y;
     asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
     return y;
+}
+
+template <int N> __device__ __forceinline__ void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N> __device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(p));
+    return p != 0;
 }
 
 // D (+)= A B^T, 8-bit E4M3 operands in shared memory, K = 32.
@@ -323,10 +339,58 @@ struct Walk {
     }
 };
 
+// A token's scale exponents for the heads of one softmax thread; `there`: it is a row
+// of the tile on a page of the pool.
+template <int HT>
+struct TokenScales {
+    bool there;
+    int sk, sv;
+    uint32_t rk[HT / 4], rv[HT / 4];
+    __device__ void load(const Args &a, const Walk &w, int token, int h0, int hn) {
+        there = w.live() && token < w.rows();
+        sk = sv = 0;
+#pragma unroll
+        for (int k = 0; k < HT / 4; ++k) rk[k] = rv[k] = 0;
+        if (!there) return;
+        const int pos = w.tok + token;
+        const int32_t page = a.page_table[(size_t)w.b * a.max_pages + pos / a.c.page_size];
+        there = page >= 0 && page < a.c.num_pages;
+        if (!there) return;
+        const int64_t eb = ((int64_t)page * a.c.page_size + pos % a.c.page_size) / a.c.block;
+        const uint8_t *k = a.c.exp[2] + eb * a.c.H + h0, *v = a.c.exp[3] + eb * a.c.H + h0;
+        sk = a.c.exp[0][eb];
+        sv = a.c.exp[1][eb];
+        if (hn % 4 == 0) {
+#pragma unroll
+            for (int j = 0; j < HT / 4; ++j)
+                if (4 * j < hn) {
+                    rk[j] = reinterpret_cast<const uint32_t *>(k)[j];
+                    rv[j] = reinterpret_cast<const uint32_t *>(v)[j];
+                }
+        } else {
+#pragma unroll
+            for (int j = 0; j < HT; ++j)
+                if (j < hn) {
+                    rk[j / 4] |= (uint32_t)k[j] << (8 * (j & 3));
+                    rv[j / 4] |= (uint32_t)v[j] << (8 * (j & 3));
+                }
+        }
+    }
+    __device__ int key(int k) const { return clamp_exp((rk[k / 4] >> (8 * (k & 3))) & 0xff); }
+    __device__ int value(int k) const { return clamp_exp((rv[k / 4] >> (8 * (k & 3))) & 0xff); }
+};
+
+// HM: heads of the shape, rounded up to 16 or 32.
+//
+// Registers: 80 a thread at launch; the warps that copy and issue give 40 of theirs to
+// the accumulating ones (16 * 32 * 80 + 4 * 32 * (120 + 40) = 768 * 80).
+constexpr int kRegs = 80, kRegsFew = 40, kRegsMany = 120;
+static_assert(kRegsFew + kRegsMany == 2 * kRegs, "what one group takes another has given");
 template <int HM>
 __global__ void __launch_bounds__(kThreads, 1)
     decode_scaled_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a,
                          const __grid_constant__ Shape S) {
+    constexpr int HT = HM / 4;  // heads of a softmax thread
     extern __shared__ uint8_t raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     const Offsets off(S);
@@ -347,27 +411,39 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane >= o) inc += v;
         }
         if (lane == 31) bar.warp_sum[warp] = inc;
-        if (tid == 0) {
+        if (tid == kThreads - 1) {
             for (int s = 0; s < stages; ++s) {
                 mbar_init(&bar.full[s], 1);
                 mbar_init(&bar.empty[s], 1);
             }
             for (int k = 0; k < 2; ++k) {
                 mbar_init(&bar.img_full[k], 1);
-                mbar_init(&bar.img_empty[k], 129);
+                mbar_init(&bar.img_empty[k], 1 + kSoftmax);
+                mbar_init(&bar.w_full[k], kSoftmax);
+                mbar_init(&bar.pv_done[k], 1);
             }
-            mbar_init(&bar.meet, 128);
+            for (int k = 0; k < 4; ++k) mbar_init(&bar.meet[k], 128);
             mbar_init(&bar.sc_full, 1);
-            mbar_init(&bar.sc_empty, 128);
-            mbar_init(&bar.w_full, 128);
-            mbar_init(&bar.pv_done, 1);
+            mbar_init(&bar.sc_empty, kSoftmax);
             mbar_init(&bar.v_empty, 128);
             fence_barrier_init();
             bar.first_b = 0;
             bar.first_unit = 0;
         }
+        if (warp == kWarpSpare) tmem_alloc(&bar.tmem, S.tmem_cols);
+        if (warp == kWarpMma && lane <= NB) {
+            const int x = lane;
+            bar.kbox[x] = x ? make_uint4((S.qrows + S.prow[x - 1]) * 128, S.scol[x - 1], idesc_f8(S.n[x - 1], false),
+                                         min(4, (H * S.r - 128 * (x - 1) + 31) / 32))
+                            : make_uint4(0, 0, idesc_f8(S.qrows, false), 4);
+            bar.vbox[x] = x ? make_uint4((S.wrows + 2 * S.ha[x - 1]) * 128, S.vcol[x - 1], idesc_f8(S.nv[x - 1], true), 0)
+                            : make_uint4(0, S.v0, idesc_f8(S.nv0, true), 0);
+        }
+        tc_fence_before();
         __syncthreads();
+        tc_fence_after();
         int64_t total = 0, before = inc - n;
+#pragma unroll
         for (int w = 0; w < kThreads / 32; ++w) {
             if (w < warp) before += bar.warp_sum[w];
             total += bar.warp_sum[w];
@@ -389,317 +465,334 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
     }
-    if (warp == 8) tmem_alloc(&bar.tmem, S.tmem_cols);
-    tc_fence_before();
     __syncthreads();
-    tc_fence_after();
     const uint32_t tmem = bar.tmem;
     pdl_launch_dependents();
     bool ok = true;
-    Walk w(a, bar);
 
-    if (warp == 8) {
-        // ================= cache tiles =================
-        // lane k holds the pool row of the tile's k-th box row group (past every row,
-        // which reads as zeros, where its page is none)
-        const int R = a.box_rows, none = a.c.num_pages * a.c.page_size;
-        auto lookup = [&](const Walk &t) {
-            const int at = t.tok + lane * R;
-            int row = none;
-            if (lane * R < t.rows()) {
-                const int32_t page = a.page_table[(size_t)t.b * a.max_pages + at / a.c.page_size];
-                if (page < 0 || page >= a.c.num_pages) status_or(a.status, LRKV_STATUS_BAD_PAGE);
-                else row = page * a.c.page_size + at % a.c.page_size;
-            }
-            return row;
-        };
-        int it = 0;
-        auto send = [&](const CUtensorMap *m, int rows, int row) {  // the keys or values of one tile
-            const int groups = (rows + R - 1) / R;
-            for (int t = 0; t <= NB; ++t, ++it) {
-                const int s = it % stages;
-                if (it >= stages) ok = __all_sync(0xffffffffu, mbar_wait(&bar.empty[s], ((it / stages) - 1) & 1)) && ok;
-                if (!ok) return;
-                if (lane == 0) mbar_arrive_expect_tx(&bar.full[s], groups * R * 128);
-                __syncwarp();
-                // (each lane issues its own group's copy)
-                if (lane < groups)
-                    tma_load_2d(smem + s * kStageBytes + lane * R * 128, &m[t > 0], t > 0 ? 128 * (t - 1) : 0, row, &bar.full[s]);
-            }
-        };
-        if (w.live()) {
-            int rows = w.rows(), row = lookup(w);
-            send(maps.k, rows, row);
-            while (ok && w.live()) {
-                w.next(a);
-                int nrows = 0, nrow = none;
-                if (w.live()) {
-                    nrows = w.rows();
-                    nrow = lookup(w);
-                    send(maps.k, nrows, nrow);
+    if (warp >= kWarpCopy) {
+        reg_dec<kRegsFew>();
+        if (warp == kWarpCopy) {
+            // ================= cache tiles =================
+            // lane k looks up the pool row of the tile's k-th group of box_rows rows (past every
+            // row, which reads as zeros, where its page is none)
+            Walk w(a, bar);
+            const int R = a.box_rows, none = a.c.num_pages * a.c.page_size;
+            auto lookup = [&](const Walk &t) {
+                const int at = t.tok + lane * R;
+                int row = none;
+                if (lane * R < t.rows()) {
+                    const int32_t page = a.page_table[(size_t)t.b * a.max_pages + at / a.c.page_size];
+                    if (page < 0 || page >= a.c.num_pages) status_or(a.status, LRKV_STATUS_BAD_PAGE);
+                    else row = page * a.c.page_size + at % a.c.page_size;
                 }
-                if (ok) send(maps.v, rows, row);
-                rows = nrows;
-                row = nrow;
-            }
-        }
-        // nothing leaves with copies in flight (the MMA issuer has waited for all unless it gave up)
-        if (!ok && lane == 0)
-            for (int k = max(0, it - stages); k < it; ++k) mbar_wait(&bar.full[k % stages], (k / stages) & 1);
-    } else if (warp == 10) {
-        // ================= operand images =================
-        if (lane == 0) {
-            pdl_wait();
-            int last = -1;
-            for (; ok && w.live(); w.next(a)) {
-                if (w.seg == last) continue;
-                const int s = last = w.seg, k = s & 1;
-                if (s >= 2 && !mbar_wait(&bar.img_empty[k], ((s >> 1) - 1) & 1)) {
-                    ok = false;
-                    break;
-                }
-                mbar_arrive_expect_tx(&bar.img_full[k], S.img_bytes);
-                bulk_load(smem + off.img + k * img_stride, a.img + w.b * a.img_stride, S.img_bytes, &bar.img_full[k]);
-            }
-            for (int s = max(0, last - 1); s <= last; ++s) mbar_wait(&bar.img_full[s & 1], (s >> 1) & 1);
-        }
-    } else if (warp == 9) {
-        // ================= MMA issuer =================
-        const uint32_t base = smem_u32(smem);
-        int it = 0, i = 0;
-        auto stage_wait = [&]() {
-            const bool got = __all_sync(0xffffffffu, mbar_wait(&bar.full[it % stages], (it / stages) & 1));
-            tc_fence_after();
-            return got;
-        };
-        auto keys = [&](const Walk &t, bool first) -> bool {
-            const uint32_t img = base + off.img + (t.seg & 1) * img_stride;
-            if (first && !__all_sync(0xffffffffu, mbar_wait(&bar.img_full[t.seg & 1], (t.seg >> 1) & 1))) return false;
-            if (i > 0 && !__all_sync(0xffffffffu, mbar_wait(&bar.sc_empty, (i - 1) & 1))) return false;
-            tc_fence_after();
-            for (int x = 0; x <= NB; ++x, ++it) {
-                if (!stage_wait()) return false;
-                const uint32_t al = sw128_desc_lo(base + (it % stages) * kStageBytes, 16);
-                const uint32_t bl = sw128_desc_lo(img + (x ? S.qrows + S.prow[x - 1] : 0) * 128, 16);
-                const uint32_t d = tmem + (x ? S.scol[x - 1] : 0), id = idesc_f8(x ? S.n[x - 1] : S.qrows, false);
-                const int steps = x ? min(4, (H * S.r - 128 * (x - 1) + 31) / 32) : 4;
-                if (lane == 0) {
-                    for (int k = 0; k < steps; ++k) tc_mma_f8(d, al + 2 * k, bl + 2 * k, id, k != 0);
-                    tc_commit(&bar.empty[it % stages]);
-                }
-                __syncwarp();
-            }
-            if (lane == 0) {
-                tc_commit(&bar.sc_full);
-                if (t.ends()) tc_commit(&bar.img_empty[t.seg & 1]);
-            }
-            __syncwarp();
-            return true;
-        };
-        auto values = [&](int rows, int n) -> bool {  // of the n-th tile
-            if (!__all_sync(0xffffffffu, mbar_wait(&bar.w_full, n & 1))) return false;
-            if (n > 0 && !__all_sync(0xffffffffu, mbar_wait(&bar.v_empty, (n - 1) & 1))) return false;
-            tc_fence_after();
-            const int steps = (rows + 31) / 32;
-            for (int x = 0; x <= NB; ++x, ++it) {
-                if (!stage_wait()) return false;
-                uint8_t *st = smem + (it % stages) * kStageBytes;
-                if (rows & 31) {
-                    // rows past the end, of whatever bits, in the last group of 32: their
-                    // weights are zero, and zero times a NaN is not
-                    for (int u = rows * 8 + lane; u < steps * 32 * 8; u += 32)
-                        *reinterpret_cast<uint4 *>(st + u * 16) = make_uint4(0, 0, 0, 0);
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                }
-                const uint32_t al = sw128_desc_lo(base + (it % stages) * kStageBytes, 16);
-                const uint32_t bl = sw128_desc_lo(
-                    base + off.weights + (x ? S.wrows + 2 * S.ha[x - 1] : 0) * 128, 16);
-                const uint32_t d = tmem + (x ? S.vcol[x - 1] : S.v0), id = idesc_f8(x ? S.nv[x - 1] : S.nv0, true);
-                if (lane == 0) {
-                    // 32 tokens an instruction: 32 rows of 128 bytes of A, 32 bytes of B's rows
-                    for (int k = 0; k < steps; ++k) tc_mma_f8(d, al + 256 * k, bl + 2 * k, id, k != 0);
-                    tc_commit(&bar.empty[it % stages]);
-                }
-                __syncwarp();
-            }
-            if (lane == 0) tc_commit(&bar.pv_done);
-            __syncwarp();
-            return true;
-        };
-        if (w.live()) {
-            int rows = w.rows(), seg = w.seg;
-            ok = keys(w, true);
-            while (ok && w.live()) {
-                w.next(a);
-                int nrows = 0;
-                ++i;
-                if (w.live()) {
-                    nrows = w.rows();
-                    ok = keys(w, w.seg != seg);
-                    seg = w.seg;
-                }
-                if (ok) ok = values(rows, i - 1);
-                rows = nrows;
-            }
-        }
-        if (!ok && lane == 0) status_or(a.status, LRKV_STATUS_TIMEOUT);
-    } else if (warp < 4) {
-        // ================= scores and weights: thread = token =================
-        const uint32_t lanes = tmem + ((uint32_t)(32 * warp) << 16);
-        float m[HM], l[HM];
-        int last = -1, nb = a.c.page_size / a.c.block;
-        uint32_t met = 0;
-        auto meet = [&]() -> bool {  // all four warps (a wait with a limit, as every wait here)
-            mbar_arrive(&bar.meet);
-            return __all_sync(0xffffffffu, mbar_wait(&bar.meet, met++ & 1));
-        };
-        for (int i = 0; ok && w.live(); ++i, w.next(a)) {
-            // the token's scale exponents
-            const int pos = w.tok + tid;
-            bool there = tid < w.rows();
-            int e_sk = 0, e_sv = 0;
-            uint32_t e_rk[HM / 4] = {}, e_rv[HM / 4] = {};
-            if (there) {
-                const int32_t page = a.page_table[(size_t)w.b * a.max_pages + pos / a.c.page_size];
-                there = page >= 0 && page < a.c.num_pages;
-                if (there) {
-                    const int64_t eb = (int64_t)page * nb + pos % a.c.page_size / a.c.block;
-                    e_sk = a.c.exp[0][eb];
-                    e_sv = a.c.exp[1][eb];
-                    const uint32_t *rk = reinterpret_cast<const uint32_t *>(a.c.exp[2] + eb * H);
-                    const uint32_t *rv = reinterpret_cast<const uint32_t *>(a.c.exp[3] + eb * H);
+                return row;
+            };
+            int s = 0, n = 0;  // stage, times the ring went round
+            auto send = [&](const CUtensorMap *m, int rows, int row) {  // the keys or values of one tile
+                const int groups = (rows + R - 1) / R;
+                int y[8];
 #pragma unroll
-                    for (int k = 0; k < HM / 4; ++k)
-                        if (4 * k < H) {
-                            e_rk[k] = rk[k];
-                            e_rv[k] = rv[k];
-                        }
+                for (int g = 0; g < 8; ++g) y[g] = __shfl_sync(0xffffffffu, row, g);
+                for (int t = 0; t <= NB; ++t) {
+                    if (n > 0) ok = __all_sync(0xffffffffu, mbar_wait(&bar.empty[s], (n - 1) & 1)) && ok;
+                    if (!ok) return;
+                    if (elect_one()) {
+                        const CUtensorMap *map = m + (t > 0);
+                        uint8_t *st = smem + s * kStageBytes;
+                        const int x = t > 0 ? 128 * (t - 1) : 0;
+                        mbar_arrive_expect_tx(&bar.full[s], groups * R * 128);
+#pragma unroll
+                        for (int g = 0; g < 8; ++g)
+                            if (g < groups) tma_load_2d(st + g * R * 128, map, x, y[g], &bar.full[s]);
+                    }
+                    __syncwarp();
+                    if (++s == stages) {
+                        s = 0;
+                        ++n;
+                    }
+                }
+            };
+            if (w.live()) {
+                int rows = w.rows(), row = lookup(w);
+                send(maps.k, rows, row);
+                while (ok && w.live()) {
+                    w.next(a);
+                    int nrows = 0, nrow = none;
+                    if (w.live()) {
+                        nrows = w.rows();
+                        nrow = lookup(w);
+                        send(maps.k, nrows, nrow);
+                    }
+                    if (ok) send(maps.v, rows, row);
+                    rows = nrows;
+                    row = nrow;
                 }
             }
+            // nothing leaves with copies in flight (the MMA issuer has waited for all unless it gave up)
+            if (!ok && lane == 0)
+                for (int k = 0; k < stages; ++k)
+                    if (k < s || n > 0) mbar_wait(&bar.full[k], (k < s ? n : n - 1) & 1);
+        } else if (warp == kWarpImage) {
+            // ================= operand images =================
+            if (lane == 0) {
+                pdl_wait();
+                int last = -1;
+                for (Walk w(a, bar); ok && w.live(); w.next(a)) {
+                    if (w.seg == last) continue;
+                    const int s = last = w.seg, k = s & 1;
+                    if (s >= 2 && !mbar_wait(&bar.img_empty[k], ((s >> 1) - 1) & 1)) {
+                        ok = false;
+                        --last;
+                        break;
+                    }
+                    mbar_arrive_expect_tx(&bar.img_full[k], S.img_bytes);
+                    bulk_load(smem + off.img + k * img_stride, a.img + w.b * a.img_stride, S.img_bytes, &bar.img_full[k]);
+                }
+                for (int s = max(0, last - 1); s <= last; ++s) mbar_wait(&bar.img_full[s & 1], (s >> 1) & 1);
+            }
+        } else if (warp == kWarpMma) {
+            // ================= MMA issuer =================
+            const uint32_t base = smem_u32(smem);
+            int s = 0, n = 0, i = 0;  // stage, times the ring went round; tile
+            auto all_wait = [&](uint64_t *b, uint32_t parity) { return (bool)__all_sync(0xffffffffu, mbar_wait(b, parity)); };
+            auto keys = [&](const Walk &t, bool first) -> bool {
+                const uint32_t img = base + off.img + (t.seg & 1) * img_stride;
+                if (first && !all_wait(&bar.img_full[t.seg & 1], (t.seg >> 1) & 1)) return false;
+                if (i > 0 && !all_wait(&bar.sc_empty, (i - 1) & 1)) return false;
+                const bool ends = t.ends();
+                for (int x = 0; x <= NB; ++x) {
+                    const uint4 box = bar.kbox[x];  // operand, accumulator, instruction, steps
+                    if (!all_wait(&bar.full[s], n & 1)) return false;
+                    tc_fence_after();
+                    if (elect_one()) {
+                        const uint32_t al = sw128_desc_lo(base + s * kStageBytes, 16), bl = sw128_desc_lo(img + box.x, 16);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (k < box.w) tc_mma_f8(tmem + box.y, al + 2 * k, bl + 2 * k, box.z, k != 0);
+                        tc_commit(&bar.empty[s]);
+                        if (x == NB) {
+                            tc_commit(&bar.sc_full);
+                            if (ends) tc_commit(&bar.img_empty[t.seg & 1]);
+                        }
+                    }
+                    __syncwarp();
+                    if (++s == stages) {
+                        s = 0;
+                        ++n;
+                    }
+                }
+                return true;
+            };
+            auto values = [&](int rows, int j) -> bool {  // of the j-th tile
+                if (!all_wait(&bar.w_full[j & 1], (j >> 1) & 1)) return false;
+                if (j > 0 && !all_wait(&bar.v_empty, (j - 1) & 1)) return false;
+                const int steps = (rows + 31) / 32;
+                const uint32_t weights = base + off.weights + (j & 1) * 2 * S.wrows * 128;
+                for (int x = 0; x <= NB; ++x) {
+                    const uint4 box = bar.vbox[x];
+                    if (!all_wait(&bar.full[s], n & 1)) return false;
+                    tc_fence_after();
+                    if (rows & 31) {
+                        // rows past the end, of whatever bits, in the last group of 32: their
+                        // weights are zero, and zero times a NaN is not
+                        uint8_t *st = smem + s * kStageBytes;
+                        for (int u = rows * 8 + lane; u < steps * 32 * 8; u += 32)
+                            *reinterpret_cast<uint4 *>(st + u * 16) = make_uint4(0, 0, 0, 0);
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                    }
+                    if (elect_one()) {
+                        // 32 tokens an instruction: 32 rows of 128 bytes of A, 32 bytes of B's rows
+                        const uint32_t al = sw128_desc_lo(base + s * kStageBytes, 16), bl = sw128_desc_lo(weights + box.x, 16);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (k < steps) tc_mma_f8(tmem + box.y, al + 256 * k, bl + 2 * k, box.z, k != 0);
+                        tc_commit(&bar.empty[s]);
+                        if (x == NB) tc_commit(&bar.pv_done[j & 1]);
+                    }
+                    __syncwarp();
+                    if (++s == stages) {
+                        s = 0;
+                        ++n;
+                    }
+                }
+                return true;
+            };
+            Walk w(a, bar);
+            if (w.live()) {
+                int rows = w.rows(), seg = w.seg;
+                ok = keys(w, true);
+                while (ok && w.live()) {
+                    w.next(a);
+                    int nrows = 0;
+                    ++i;
+                    if (w.live()) {
+                        nrows = w.rows();
+                        ok = keys(w, w.seg != seg);
+                        seg = w.seg;
+                    }
+                    if (ok) ok = values(rows, i - 1);
+                    rows = nrows;
+                }
+            }
+            if (!ok && lane == 0) status_or(a.status, LRKV_STATUS_TIMEOUT);
+        }
+    } else if (warp < kSoftmax / 32) {
+        // ================= scores and weights =================
+        // warp: tokens 32 (warp & 3) + lane of a tile, heads h0 .. h0 + hn - 1 (a quarter)
+        const int hn = H / 4, grp = warp >> 2, h0 = grp * hn, token = 32 * (warp & 3) + lane;
+        const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+        float m[HT], l[HT];
+        uint32_t met = 0;
+        auto meet = [&]() -> bool {  // the four warps of these heads
+            mbar_arrive(&bar.meet[grp]);
+            return __all_sync(0xffffffffu, mbar_wait(&bar.meet[grp], met++ & 1));
+        };
+        Walk w(a, bar);
+        int last = -1;
+        TokenScales<HT> e;
+        e.load(a, w, token, h0, hn);
+        for (int i = 0; ok && w.live(); ++i) {
             const bool first = w.seg != last, ends = w.ends();
-            last = w.seg;
+            const int seg = last = w.seg, b = w.b;
             if (first) {
 #pragma unroll
-                for (int h = 0; h < HM; ++h) {
-                    m[h] = -INFINITY;
-                    l[h] = 0.f;
+                for (int k = 0; k < HT; ++k) {
+                    m[k] = -INFINITY;
+                    l[k] = 0.f;
                 }
-                ok = __all_sync(0xffffffffu, mbar_wait(&bar.img_full[w.seg & 1], (w.seg >> 1) & 1));
+                ok = __all_sync(0xffffffffu, mbar_wait(&bar.img_full[seg & 1], (seg >> 1) & 1));
                 if (!ok) break;
             }
-            const float *f = reinterpret_cast<const float *>(smem + off.img + (w.seg & 1) * img_stride +
-                                                             (S.qrows + S.prows) * 128);
+            const float *f = reinterpret_cast<const float *>(smem + off.img + (seg & 1) * img_stride +
+                                                             (S.qrows + S.prows) * 128) + h0;
             ok = __all_sync(0xffffffffu, mbar_wait(&bar.sc_full, i & 1));
             if (!ok) break;
             tc_fence_after();
-            float x[HM];
-            const float sk = exp2i(clamp_exp(e_sk));
+            float x[HT];
+            const float sk = exp2i(clamp_exp(e.sk));
 #pragma unroll
-            for (int h = 0; h < HM; ++h) {
-                if (h < H) {
-                    const int ta = h * S.r / 128, tb = (h * S.r + S.r - 1) / 128;
-                    uint32_t vs[4], va[4], vb[4];
-                    tmem_ld4(lanes + 4 * h, vs);
-                    tmem_ld4(lanes + S.scol[ta] + 4 * (h - S.h0[ta]), va);
-                    if (tb != ta) tmem_ld4(lanes + S.scol[tb], vb);  // (the first head of that box)
-                    tmem_wait_ld();
-                    const float s = __uint_as_float(vs[0]) + (__uint_as_float(vs[1]) * 0.0625f + __uint_as_float(vs[2]) * 0.001953125f);
-                    float t = __uint_as_float(va[0]) + (__uint_as_float(va[1]) * 0.0625f + __uint_as_float(va[2]) * 0.001953125f);
-                    if (tb != ta)
-                        t += __uint_as_float(vb[0]) + (__uint_as_float(vb[1]) * 0.0625f + __uint_as_float(vb[2]) * 0.001953125f);
-                    const float rk = exp2i(clamp_exp((e_rk[h / 4] >> (8 * (h & 3))) & 0xff));
-                    x[h] = there ? s * (f[h] * sk) + t * (f[H + h] * rk) : -INFINITY;
+            for (int k = 0; k < HT; k += 2) {  // two heads' columns on their way together
+                uint32_t vs[2][4], va[2][4], vb[2][4];
+                bool two[2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int h = h0 + min(k + j, hn - 1), ta = h * S.r / 128, tb = (h * S.r + S.r - 1) / 128;
+                    two[j] = tb != ta;
+                    tmem_ld4(lanes + 4 * h, vs[j]);
+                    tmem_ld4(lanes + S.scol[ta] + 4 * (h - S.h0[ta]), va[j]);
+                    if (two[j]) tmem_ld4(lanes + S.scol[tb], vb[j]);  // (the first head of that box)
+                }
+                tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    auto sum = [](const uint32_t (&v)[4]) {
+                        return __uint_as_float(v[0]) + (__uint_as_float(v[1]) * 0.0625f + __uint_as_float(v[2]) * 0.001953125f);
+                    };
+                    float t = sum(va[j]);
+                    if (two[j]) t += sum(vb[j]);
+                    const int q = min(k + j, hn - 1);
+                    x[k + j] = e.there ? sum(vs[j]) * (f[q] * sk) + t * (f[H + q] * exp2i(e.key(k + j))) : -INFINITY;
                 }
             }
             tc_fence_before();
             mbar_arrive(&bar.sc_empty);
-            if (ends) mbar_arrive(&bar.img_empty[w.seg & 1]);  // (the factors were read)
+            if (ends) mbar_arrive(&bar.img_empty[seg & 1]);  // (the factors were read)
             // (two buffers in turn: a warp writes the one after next only when all have met again)
-            float *red = reinterpret_cast<float *>(smem + off.red) + (i & 1) * 4 * 32 * 4;
-            const float es = (float)clamp_exp(e_sv);
+            float *red = reinterpret_cast<float *>(smem + off.red) + ((i & 1) * 4 + grp) * HT * 16;
+            const float es = (float)clamp_exp(e.sv);
             float mine[3] = {0.f, 0.f, 0.f};
 #pragma unroll
-            for (int h = 0; h < HM; ++h)
-                if (h < H) {
-                    const float er = (float)clamp_exp((e_rv[h / 4] >> (8 * (h & 3))) & 0xff);
-                    const float m0 = warp_max(x[h]), m1 = warp_max(x[h] + es), m2 = warp_max(x[h] + er);
-                    if (lane == (h & 31)) {
+            for (int k = 0; k < HT; ++k)
+                if (k < hn) {
+                    const float m0 = warp_max(x[k]), m1 = warp_max(x[k] + es), m2 = warp_max(x[k] + (float)e.value(k));
+                    if (lane == k) {
                         mine[0] = m0;
                         mine[1] = m1;
                         mine[2] = m2;
                     }
                 }
-            if (lane < H)
+            if (lane < hn)
 #pragma unroll
-                for (int k = 0; k < 3; ++k) red[(k * 32 + lane) * 4 + warp] = mine[k];
+                for (int k = 0; k < 3; ++k) red[(k * HT + lane) * 4 + (warp & 3)] = mine[k];
+            w.next(a);  // (the next tile's scales are on their way during the rest of this one)
+            TokenScales<HT> en;
+            en.load(a, w, token, h0, hn);
             ok = meet();
-            // the operand of the tile before has been read
-            if (ok && i > 0) ok = __all_sync(0xffffffffu, mbar_wait(&bar.pv_done, (i - 1) & 1));
+            // the operand of the tile before the last has been read
+            if (ok && i > 1) ok = __all_sync(0xffffffffu, mbar_wait(&bar.pv_done[i & 1], ((i >> 1) - 1) & 1));
             if (!ok) break;
-            float *fac = reinterpret_cast<float *>(smem + off.fac) + (i & 1) * 3 * 32;
-            uint8_t *ws = smem + off.weights, *wr = ws + S.wrows * 128;
+            float *fac = reinterpret_cast<float *>(smem + off.fac) + (i & 3) * 3 * 32;
+            uint8_t *ws = smem + off.weights + (i & 1) * 2 * S.wrows * 128, *wr = ws + S.wrows * 128;
 #pragma unroll
-            for (int h = 0; h < HM; ++h)
-                if (h < H) {
-                    const float er = (float)clamp_exp((e_rv[h / 4] >> (8 * (h & 3))) & 0xff);
+            for (int k = 0; k < HT; ++k)
+                if (k < hn) {
+                    const int h = h0 + k;
                     float M[3];
 #pragma unroll
-                    for (int k = 0; k < 3; ++k) {
-                        const float4 v = *reinterpret_cast<const float4 *>(&red[(k * 32 + h) * 4]);
-                        M[k] = fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w));
+                    for (int j = 0; j < 3; ++j) {
+                        const float4 v = *reinterpret_cast<const float4 *>(&red[(j * HT + k) * 4]);
+                        M[j] = fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w));
                     }
-                    const float mn = fmaxf(m[h], M[0]), ref = mn == -INFINITY ? 0.f : mn;
+                    const float mn = fmaxf(m[k], M[0]), ref = mn == -INFINITY ? 0.f : mn;
                     const float ms = M[1] == -INFINITY ? 0.f : M[1], mr = M[2] == -INFINITY ? 0.f : M[2];
-                    const float alpha = ex2f(m[h] - ref);
-                    m[h] = mn;
-                    l[h] = l[h] * alpha + ex2f(x[h] - ref);
-                    if (tid == h) {
+                    const float alpha = ex2f(m[k] - ref);
+                    m[k] = mn;
+                    l[k] = l[k] * alpha + ex2f(x[k] - ref);
+                    if (token == k) {
                         fac[h] = alpha;
                         fac[32 + h] = ex2f(ms - ref - 8.f);
                         fac[64 + h] = ex2f(mr - ref - 8.f);
                     }
-                    float y = ex2f(x[h] + es - ms + 8.f), z = ex2f(x[h] + er - mr + 8.f);
-                    ws[op_byte(2 * h, tid)] = take_code(y);
-                    wr[op_byte(2 * h, tid)] = take_code(z);
-                    y *= 16.f;
-                    z *= 16.f;
-                    ws[op_byte(2 * h + 1, tid)] = take_code(y);
-                    wr[op_byte(2 * h + 1, tid)] = take_code(z);
+                    // both operands' terms, a pair at a time
+                    const float y = ex2f(x[k] + es - ms + 8.f), z = ex2f(x[k] + (float)e.value(k) - mr + 8.f);
+                    const uint16_t t1 = e4m3x2_from_f32(y, z);
+                    const uint32_t h2 = f16x2_from_e4m3x2(t1);
+                    const float2 g = __half22float2(*reinterpret_cast<const __half2 *>(&h2));
+                    const uint16_t t2 = e4m3x2_from_f32((y - g.x) * 16.f, (z - g.y) * 16.f);
+                    const uint32_t o1 = op_byte(2 * h, token), o2 = op_byte(2 * h + 1, token);
+                    ws[o1] = (uint8_t)t1;
+                    wr[o1] = (uint8_t)(t1 >> 8);
+                    ws[o2] = (uint8_t)t2;
+                    wr[o2] = (uint8_t)(t2 >> 8);
                 }
             fence_proxy_async_smem();
-            mbar_arrive(&bar.w_full);
+            mbar_arrive(&bar.w_full[i & 1]);
             if (ends) {
                 // the sums of all tokens: over the warp, then over the four warps
                 float sum = 0.f;
 #pragma unroll
-                for (int h = 0; h < HM; ++h)
-                    if (h < H) {
-                        float v = l[h];
+                for (int k = 0; k < HT; ++k)
+                    if (k < hn) {
+                        float v = l[k];
 #pragma unroll
                         for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-                        if (lane == (h & 31)) sum = v;
+                        if (lane == k) sum = v;
                     }
-                if (lane < H) red[(3 * 32 + lane) * 4 + warp] = sum;
-                float *ml = a.st.ml + ((int64_t)w.b + blockIdx.x) * H * 2;
+                if (lane < hn) red[(3 * HT + lane) * 4 + (warp & 3)] = sum;
                 if (!(ok = meet())) break;
+                float *ml = a.st.ml + ((int64_t)b + blockIdx.x) * H * 2;
 #pragma unroll
-                for (int h = 0; h < HM; ++h)
-                    if (h < H && tid == h) {
-                        const float4 v = *reinterpret_cast<const float4 *>(&red[(3 * 32 + h) * 4]);
-                        ml[2 * h] = m[h];
-                        ml[2 * h + 1] = (v.x + v.y) + (v.z + v.w);
+                for (int k = 0; k < HT; ++k)
+                    if (k < hn && token == k) {
+                        const float4 v = *reinterpret_cast<const float4 *>(&red[(3 * HT + k) * 4]);
+                        ml[2 * (h0 + k)] = m[k];
+                        ml[2 * (h0 + k) + 1] = (v.x + v.y) + (v.z + v.w);
                     }
             }
+            e = en;
         }
         if (!ok && lane == 0) status_or(a.status, LRKV_STATUS_TIMEOUT);
     } else {
         // ================= value accumulators: thread = column =================
-        const int col = tid - 128;
+        reg_inc<kRegsMany>();
+        const int col = tid - kSoftmax;
         const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+        const uint32_t magic = 0xffffffffu / (uint32_t)S.r + 1u;  // 2^32 / r rounded up
         float as[HM], ar[kMaxBoxes];
-        int last = -1;
-        for (int i = 0; ok && w.live(); ++i, w.next(a)) {
+        int last = -1, i = 0;
+        for (Walk w(a, bar); ok && w.live(); ++i, w.next(a)) {
             if (w.seg != last) {
 #pragma unroll
                 for (int h = 0; h < HM; ++h) as[h] = 0.f;
@@ -707,27 +800,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int t = 0; t < kMaxBoxes; ++t) ar[t] = 0.f;
                 last = w.seg;
             }
-            ok = __all_sync(0xffffffffu, mbar_wait(&bar.w_full, i & 1) && mbar_wait(&bar.pv_done, i & 1));
+            ok = __all_sync(0xffffffffu, mbar_wait(&bar.w_full[i & 1], (i >> 1) & 1) &&
+                                             mbar_wait(&bar.pv_done[i & 1], (i >> 1) & 1));
             if (!ok) break;
             tc_fence_after();
-            const float *fac = reinterpret_cast<const float *>(smem + off.fac) + (i & 1) * 3 * 32;
+            const float *fac = reinterpret_cast<const float *>(smem + off.fac) + (i & 3) * 3 * 32;
 #pragma unroll
-            for (int g = 0; g < HM / 8; ++g)
-                if (8 * g < H) {
-                    uint32_t v[16];
-                    tmem_ld16(lanes + S.v0 + 16 * g, v);
+            for (int g = 0; g < HM / 16; ++g)
+                if (16 * g < H) {
+                    uint32_t v[32];
+                    tmem_ld32(lanes + S.v0 + 32 * g, v);
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const int h = 8 * g + k;
-                        if (h < H)
-                            as[h] = as[h] * fac[h] +
-                                    (__uint_as_float(v[2 * k]) + __uint_as_float(v[2 * k + 1]) * 0.0625f) * fac[32 + h];
+                    for (int k = 0; k < 16; ++k) {
+                        const int h = 16 * g + k;
+                        as[h] = as[h] * fac[h] +
+                                (__uint_as_float(v[2 * k]) + __uint_as_float(v[2 * k + 1]) * 0.0625f) * fac[32 + h];
                     }
                 }
 #pragma unroll
             for (int t = 0; t < kMaxBoxes; ++t)
                 if (t < NB) {
-                    const int h = min((128 * t + col) / S.r, H - 1), k = h - S.ha[t];
+                    const int h = min((int)__umulhi((uint32_t)(128 * t + col), magic), H - 1), k = h - S.ha[t];
                     float y = 0.f;
 #pragma unroll
                     for (int g = 0; g < 2; ++g)
@@ -757,7 +850,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if (warp == 8) {
+    if (warp == kWarpSpare) {
         tc_fence_after();
         tmem_dealloc(tmem, S.tmem_cols);
     }
@@ -773,6 +866,12 @@ bool map_codes(CUtensorMap *m, const void *base, int64_t rows, int bytes, int bo
     return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, es,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename K>
+int launch_registers(K *kernel) {
+    cudaFuncAttributes f;
+    return cudaFuncGetAttributes(&f, kernel) == cudaSuccess ? f.numRegs : 0;
 }
 
 // Workspace: unit offsets, operand images, states of up to B + CTAs pieces.
@@ -835,6 +934,11 @@ cudaError_t launch_decode_scaled_tc(const ScaledDecodeArgs &d, void *ws) {
     const int sm = device_sm_count();
     const int64_t most = (int64_t)d.B * ((d.max_seq_len + kUnit - 1) / kUnit);
     const int ctas = (int)std::max<int64_t>(1, std::min<int64_t>(sm, most));
+    const auto kernel = c.H <= 16 ? decode_scaled_kernel<16> : decode_scaled_kernel<32>;
+    // (taking registers that the launch does not have would wait forever)
+    static const bool enough = launch_registers(decode_scaled_kernel<16>) == kRegs &&
+                               launch_registers(decode_scaled_kernel<32>) == kRegs;
+    if (!enough) return cudaErrorLaunchOutOfResources;
     const Ws w = layout(ws, s, d.B, sm, c.d_h);
     const int max_len = d.max_pages * c.page_size;
     PrepArgs p;
@@ -860,13 +964,8 @@ cudaError_t launch_decode_scaled_tc(const ScaledDecodeArgs &d, void *ws) {
     a.max_pages = d.max_pages;
     a.max_len = max_len;
     const int bytes = Offsets(s).bytes;
-    if (c.H <= 16) {
-        if ((e = smem_limit_once(decode_scaled_kernel<16>, kSmemMost)) != cudaSuccess) return e;
-        e = launch_pdl(decode_scaled_kernel<16>, dim3(ctas), dim3(kThreads), bytes, d.stream, maps, a, s);
-    } else {
-        if ((e = smem_limit_once(decode_scaled_kernel<32>, kSmemMost)) != cudaSuccess) return e;
-        e = launch_pdl(decode_scaled_kernel<32>, dim3(ctas), dim3(kThreads), bytes, d.stream, maps, a, s);
-    }
+    if ((e = smem_limit_once(kernel, kSmemMost)) != cudaSuccess) return e;
+    e = launch_pdl(kernel, dim3(ctas), dim3(kThreads), bytes, d.stream, maps, a, s);
     if (e != cudaSuccess) return e;
     ScaledMergeArgs m;
     m.st = a.st;
