@@ -507,6 +507,7 @@ LRKV_API int lrkv_prefill_window(const void *X, const void *Q, const int32_t *cu
  * the request.  What pages hold past a request's length never matters.
  * Workspace: lrkv_decode_scaled_workspace_bytes bytes; that never falls as B or
  * max_seq_len grows.  A length may exceed max_seq_len up to the page table's end.
+ * B times the table's length in units of 64 rows is at most 2^24 (LRKV_E_SHAPE).
  *
  * lrkv_prefill_scaled is lrkv_append_scaled, then causal attention of every new
  * row over its request's cache rows (what the cache holds, the new rows

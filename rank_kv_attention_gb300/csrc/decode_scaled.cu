@@ -107,20 +107,23 @@ inline bool make_shape(int H, int r, Shape &s) {
     s.tmem_cols = 32;
     while (s.tmem_cols < col) s.tmem_cols *= 2;
     s.img_bytes = (s.qrows + s.prows) * 128 + 8 * H;
-    s.wrows = 2 * H + 32;  // (a box's window may reach past the last head)
+    s.wrows = 2 * H;  // (a box's window may reach past the last head)
+    for (int t = 0; t < s.boxes; ++t) s.wrows = std::max(s.wrows, 2 * s.ha[t] + s.nv[t]);
+    s.wrows = std::max(s.wrows, (int)s.nv0 + 7) / 8 * 8;
     return true;
 }
 
 // Shared memory after the ring of stages.
 struct Offsets {
-    int img, weights, red, fac, bars, bytes;
+    int img, weights, red, fac, ar, bars, bytes;
     __host__ __device__ explicit Offsets(const Shape &s) {
         img = s.stages * kStageBytes;
         const int one = (s.img_bytes + 1023) / 1024 * 1024;
         weights = img + 2 * one;
         red = weights + 4 * s.wrows * 128;  // [2][4 quarters of the heads][maxima 3, sum][8][4 warps]
         fac = red + 2 * 4 * 4 * 8 * 4 * 4;  // [4][3][32]: alpha, shared and private factor
-        bars = fac + 4 * 3 * 32 * 4;
+        ar = fac + 4 * 3 * 32 * 4;          // [box][128]: the private accumulators
+        bars = ar + s.boxes * 512;
         bytes = bars + 1152 + 1024;
     }
 };
@@ -196,6 +199,9 @@ __device__ __forceinline__ void tmem_ld4(uint32_t taddr, uint32_t (&v)[4]) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
                  : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld2(uint32_t taddr, uint32_t (&v)[2]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0, %1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "r"(taddr));
 }
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
@@ -431,6 +437,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             bar.first_unit = 0;
         }
         if (warp == kWarpSpare) tmem_alloc(&bar.tmem, S.tmem_cols);
+        if (warp == kWarpCopy && elect_one()) {
+            for (int k = 0; k < 2; ++k) {
+                prefetch_tensormap(&maps.k[k]);
+                prefetch_tensormap(&maps.v[k]);
+            }
+        }
         if (warp == kWarpMma && lane <= NB) {
             const int x = lane;
             bar.kbox[x] = x ? make_uint4((S.qrows + S.prow[x - 1]) * 128, S.scol[x - 1], idesc_f8(S.n[x - 1], false),
@@ -442,20 +454,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncthreads();
         tc_fence_after();
-        int64_t total = 0, before = inc - n;
+        uint32_t total = 0, before = inc - n;
 #pragma unroll
         for (int w = 0; w < kThreads / 32; ++w) {
             if (w < warp) before += bar.warp_sum[w];
             total += bar.warp_sum[w];
         }
-        // (CTAs past the last unit have none, so that no request's CTAs have a gap)
-        const int64_t ctas = max((int64_t)1, min((int64_t)gridDim.x, total)), g = min((int64_t)blockIdx.x, ctas);
-        const int64_t u0 = total * g / ctas, u1 = min(total, total * (g + 1) / ctas);
+        // (at most 2^24 units; CTAs past the last unit have none, so that no request's CTAs
+        // have a gap)
+        const uint32_t ctas = max(1u, min(gridDim.x, total)), g = min(blockIdx.x, ctas);
+        const uint32_t u0 = total * g / ctas, u1 = min(total, total * (g + 1) / ctas);
         if (tid == 0) bar.units = (int)(u1 - u0);
         if (n && u0 >= before && u0 < before + n) {
-            int64_t at = before;
+            uint32_t at = before;
             for (int b = b0; b < b1; ++b) {
-                const int k = units_of(a.seq_lens[b], a.max_len);
+                const uint32_t k = units_of(a.seq_lens[b], a.max_len);
                 if (u0 < at + k) {
                     bar.first_b = b;
                     bar.first_unit = (int)(u0 - at);
@@ -787,18 +800,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
         // ================= value accumulators: thread = column =================
         reg_inc<kRegsMany>();
-        const int col = tid - kSoftmax;
-        const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+        const int col = tid - kSoftmax, quad = warp & 3;
+        const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16);
         const uint32_t magic = 0xffffffffu / (uint32_t)S.r + 1u;  // 2^32 / r rounded up
-        float as[HM], ar[kMaxBoxes];
+        auto head_of = [&](int c) { return min((int)__umulhi((uint32_t)c, magic), H - 1); };
+        float as[HM];
+        float *ar = reinterpret_cast<float *>(smem + off.ar) + col;
         int last = -1, i = 0;
         for (Walk w(a, bar); ok && w.live(); ++i, w.next(a)) {
-            if (w.seg != last) {
+            const bool first = w.seg != last;
+            last = w.seg;
+            if (first) {
 #pragma unroll
                 for (int h = 0; h < HM; ++h) as[h] = 0.f;
-#pragma unroll
-                for (int t = 0; t < kMaxBoxes; ++t) ar[t] = 0.f;
-                last = w.seg;
             }
             ok = __all_sync(0xffffffffu, mbar_wait(&bar.w_full[i & 1], (i >> 1) & 1) &&
                                              mbar_wait(&bar.pv_done[i & 1], (i >> 1) & 1));
@@ -811,28 +825,51 @@ __global__ void __launch_bounds__(kThreads, 1)
                     uint32_t v[32];
                     tmem_ld32(lanes + S.v0 + 32 * g, v);
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        const int h = 16 * g + k;
-                        as[h] = as[h] * fac[h] +
-                                (__uint_as_float(v[2 * k]) + __uint_as_float(v[2 * k + 1]) * 0.0625f) * fac[32 + h];
+                    for (int k = 0; k < 16; k += 4) {
+                        const float4 al = *reinterpret_cast<const float4 *>(&fac[16 * g + k]);
+                        const float4 fs = *reinterpret_cast<const float4 *>(&fac[32 + 16 * g + k]);
+                        auto add = [&](int j, float x, float y) {
+                            as[16 * g + k + j] = as[16 * g + k + j] * x +
+                                                 (__uint_as_float(v[2 * (k + j)]) + __uint_as_float(v[2 * (k + j) + 1]) * 0.0625f) * y;
+                        };
+                        add(0, al.x, fs.x);
+                        add(1, al.y, fs.y);
+                        add(2, al.z, fs.z);
+                        add(3, al.w, fs.w);
                     }
                 }
+            // a warp's 32 columns of a box belong to few heads (one or two from r = 32 on):
+            // those heads' columns of D, four boxes on their way together
+#pragma unroll 1
+            for (int t0 = 0; t0 < NB; t0 += 4) {
+                uint32_t v[4][2], u[4][2];
 #pragma unroll
-            for (int t = 0; t < kMaxBoxes; ++t)
-                if (t < NB) {
-                    const int h = min((int)__umulhi((uint32_t)(128 * t + col), magic), H - 1), k = h - S.ha[t];
-                    float y = 0.f;
+                for (int j = 0; j < 4; ++j)
+                    if (t0 + j < NB) {
+                        const int t = t0 + j, ha = S.ha[t], hA = head_of(128 * t + 32 * quad), hB = head_of(128 * t + 32 * quad + 31);
+                        tmem_ld2(lanes + S.vcol[t] + 2 * (hA - ha), v[j]);
+                        tmem_ld2(lanes + S.vcol[t] + 2 * (hB - ha), u[j]);
+                    }
+                tmem_wait_ld();
 #pragma unroll
-                    for (int g = 0; g < 2; ++g)
-                        if (16 * g < S.nv[t]) {
-                            uint32_t v[16];
-                            tmem_ld16(lanes + S.vcol[t] + 16 * g, v);
-#pragma unroll
-                            for (int j = 0; j < 8; ++j)
-                                if (k == 8 * g + j) y = __uint_as_float(v[2 * j]) + __uint_as_float(v[2 * j + 1]) * 0.0625f;
+                for (int j = 0; j < 4; ++j)
+                    if (t0 + j < NB) {
+                        const int t = t0 + j, ha = S.ha[t], hA = head_of(128 * t + 32 * quad), hB = head_of(128 * t + 32 * quad + 31);
+                        const int h = head_of(128 * t + col);
+                        for (int k = hA + 1; k < hB; ++k) {
+                            uint32_t x[2];
+                            tmem_ld2(lanes + S.vcol[t] + 2 * (k - ha), x);
+                            tmem_wait_ld();
+                            if (h == k) {
+                                v[j][0] = x[0];
+                                v[j][1] = x[1];
+                            }
                         }
-                    ar[t] = ar[t] * fac[h] + y * fac[64 + h];
-                }
+                        const bool up = h == hB;
+                        const float y = __uint_as_float(up ? u[j][0] : v[j][0]) + __uint_as_float(up ? u[j][1] : v[j][1]) * 0.0625f;
+                        ar[128 * t] = first ? y * fac[64 + h] : ar[128 * t] * fac[h] + y * fac[64 + h];
+                    }
+            }
             tc_fence_before();
             mbar_arrive(&bar.v_empty);
             if (w.ends()) {
@@ -840,9 +877,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int h = 0; h < HM; ++h)
                     if (h < H) acc[h * 128 + col] = as[h];
-#pragma unroll
-                for (int t = 0; t < kMaxBoxes; ++t)
-                    if (t < NB && 128 * t + col < H * S.r) acc[H * 128 + 128 * t + col] = ar[t];
+                for (int t = 0; t < NB; ++t)
+                    if (128 * t + col < H * S.r) acc[H * 128 + 128 * t + col] = ar[128 * t];
             }
         }
         if (!ok && lane == 0) status_or(a.status, LRKV_STATUS_TIMEOUT);

@@ -191,15 +191,25 @@ __global__ void __launch_bounds__(kThreads) decode_scaled_any_kernel(const __gri
 // ---------------------------------------------------------------------------
 // Merge: one CTA per (request, head).  o = (sum_s f_s accS_s + (sum_s f_s accR_s)
 // B_V[h]^T) / sum_s f_s l_s with f_s = 2^(m_s - max m).  Groups of threads, one thread
-// a column, take the states in turn.
+// a column, take the states in turn.  All of it is latency: B_V[h] is on its way
+// before the states are there, and value sums are read together with the maxima that
+// weigh them.
 // ---------------------------------------------------------------------------
-constexpr int kMergeThreads = 512, kMergeStates = 256;
+constexpr int kMergeThreads = 512, kMergeStates = 256, kMergeHeld = 8, kMergeRows = 2;
 
 __global__ void __launch_bounds__(kMergeThreads) scaled_merge_kernel(const __grid_constant__ ScaledMergeArgs P) {
     __shared__ float fs[kMergeStates], sums[kMergeThreads];
     __shared__ float red[2][kMergeThreads / 32];
     const int h = blockIdx.y, b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int H = P.H, d_h = P.d_h, r = P.r, W = d_h + r, cols = (W + 31) & ~31;
+    // ---- B_V[h] in tasks of eight columns of a row: the first ones of every thread.  (The
+    // kernel before this one started after all that is in front of the call was done.)
+    const int v8 = r / 8, tasks = d_h * v8;
+    const __nv_bfloat16 *B = static_cast<const __nv_bfloat16 *>(P.B_V) + (size_t)h * d_h * r;
+    uint4 bv[kMergeRows];
+#pragma unroll
+    for (int j = 0; j < kMergeRows; ++j)
+        if (tid + j * kMergeThreads < tasks) bv[j] = reinterpret_cast<const uint4 *>(B)[tid + j * kMergeThreads];
     pdl_wait();
     pdl_launch_dependents();
     const int32_t L = P.seq_lens[b];
@@ -210,8 +220,8 @@ __global__ void __launch_bounds__(kMergeThreads) scaled_merge_kernel(const __gri
         if (h == 0 && tid == 0) status_or(P.status, LRKV_STATUS_BAD_SEQLEN);
     } else if (P.off) {
         // the CTAs whose units [g U / G, (g + 1) U / G) meet the request's
-        const int64_t U = P.off[P.B], G = min((int64_t)P.grid, U), u0 = P.off[b], u1 = P.off[b + 1] - 1;
-        const int64_t g0 = ((u0 + 1) * G - 1) / U, g1 = ((u1 + 1) * G - 1) / U;
+        const uint32_t U = P.off[P.B], G = min((uint32_t)P.grid, U), u0 = P.off[b], u1 = P.off[b + 1] - 1;
+        const uint32_t g0 = ((u0 + 1) * G - 1) / U, g1 = ((u1 + 1) * G - 1) / U;
         s0 = b + g0;
         ns = (int)(g1 - g0) + 1;
     } else {
@@ -223,6 +233,15 @@ __global__ void __launch_bounds__(kMergeThreads) scaled_merge_kernel(const __gri
     if (tid < ns) {
         m = P.st.ml[((s0 + tid) * H + h) * 2];
         l = P.st.ml[((s0 + tid) * H + h) * 2 + 1];
+    }
+    const int groups = kMergeThreads / cols, g = tid / cols, c = tid - g * cols;
+    const bool mine = g < groups && c < W;
+    const float *acc = P.st.acc + s0 * H * W + (c < d_h ? (size_t)h * d_h + c : (size_t)H * d_h + h * r + c - d_h);
+    float held[kMergeHeld];
+#pragma unroll
+    for (int j = 0; j < kMergeHeld; ++j) {
+        const int s = g + j * groups;
+        held[j] = mine && s < ns ? acc[(int64_t)s * H * W] : 0.f;
     }
     float M = m;
 #pragma unroll
@@ -246,15 +265,17 @@ __global__ void __launch_bounds__(kMergeThreads) scaled_merge_kernel(const __gri
     for (int w = 0; w < kMergeThreads / 32; ++w) l += red[1][w];
     const float inv = l != 0.f ? 1.f / l : 0.f;  // (NaN stays NaN)
 
-    const int groups = kMergeThreads / cols, g = tid / cols, c = tid - g * cols;
     float x = 0.f;
-    if (g < groups && c < W) {
-        const float *acc = P.st.acc + s0 * H * W + (c < d_h ? (size_t)h * d_h + c : (size_t)H * d_h + h * r + c - d_h);
-#pragma unroll 4
-        for (int s = g; s < ns; s += groups) {
+    if (mine) {
+        auto add = [&](int s, float v) {
             const float k = fs[s];
-            if (k >= 0.f || k != k) x += k * acc[(int64_t)s * H * W];
-        }
+            if (k >= 0.f || k != k) x += k * v;
+        };
+#pragma unroll
+        for (int j = 0; j < kMergeHeld; ++j)
+            if (g + j * groups < ns) add(g + j * groups, held[j]);
+#pragma unroll 8
+        for (int s = g + kMergeHeld * groups; s < ns; s += groups) add(s, acc[(int64_t)s * H * W]);
     }
     sums[tid] = x;
     __syncthreads();
@@ -263,18 +284,32 @@ __global__ void __launch_bounds__(kMergeThreads) scaled_merge_kernel(const __gri
         sums[c] = x;
     }
     __syncthreads();
-    const __nv_bfloat16 *B = static_cast<const __nv_bfloat16 *>(P.B_V) + (size_t)h * d_h * r;
+    // ---- expand: a row's tasks add up in order (one thread a row where tasks are few)
+    __shared__ float part[kMergeRows * kMergeThreads];
     __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(P.out) + ((size_t)b * H + h) * d_h;
-    for (int d = tid; d < d_h; d += kMergeThreads) {
-        float s = sums[d];
-#pragma unroll 4
-        for (int k = 0; k < r; k += 8) {
-            float y[8];
-            Vec16<__nv_bfloat16>::load(B + (size_t)d * r + k, y);
+    auto dot = [&](int task, const uint4 &w) {
+        const float *o = sums + d_h + task % v8 * 8;
+        float s = o[0] * bf16lo(w.x);
+        s = fmaf(o[1], bf16hi(w.x), s); s = fmaf(o[2], bf16lo(w.y), s); s = fmaf(o[3], bf16hi(w.y), s);
+        s = fmaf(o[4], bf16lo(w.z), s); s = fmaf(o[5], bf16hi(w.z), s); s = fmaf(o[6], bf16lo(w.w), s);
+        return fmaf(o[7], bf16hi(w.w), s);
+    };
+    if (tasks <= kMergeRows * kMergeThreads) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) s = fmaf(sums[d_h + k + e], y[e], s);
+        for (int j = 0; j < kMergeRows; ++j)
+            if (tid + j * kMergeThreads < tasks) part[tid + j * kMergeThreads] = dot(tid + j * kMergeThreads, bv[j]);
+        __syncthreads();
+        for (int d = tid; d < d_h; d += kMergeThreads) {
+            float s = sums[d];
+            for (int k = 0; k < v8; ++k) s += part[d * v8 + k];
+            out[d] = __float2bfloat16_rn(s * inv);
         }
-        out[d] = __float2bfloat16_rn(s * inv);
+    } else {
+        for (int d = tid; d < d_h; d += kMergeThreads) {
+            float s = sums[d];
+            for (int k = 0; k < v8; ++k) s += dot(k, reinterpret_cast<const uint4 *>(B)[d * v8 + k]);
+            out[d] = __float2bfloat16_rn(s * inv);
+        }
     }
 }
 

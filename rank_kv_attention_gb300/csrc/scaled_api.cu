@@ -289,8 +289,9 @@ int lrkv_decode_scaled(const void *q, const lrkv_scaled_t *cache, const void *B_
     if (B < 1 || max_pages < 1 || max_seq_len < 1) return LRKV_E_SHAPE;
     if ((int64_t)max_pages * cache->page_size > kMost) return LRKV_E_SHAPE;
     if ((int64_t)max_seq_len > (int64_t)max_pages * cache->page_size) return LRKV_E_BOUNDS;
-    // lengths count up to the page table's end, whatever max_seq_len says, in 32 bits
-    if ((int64_t)B * max_pages * cache->page_size > kMost) return LRKV_E_SHAPE;
+    // lengths count up to the page table's end, whatever max_seq_len says: 2^24 units of 64
+    // rows, whose products with a grid's size stay within 32 bits
+    if ((int64_t)B * (((int64_t)max_pages * cache->page_size + 63) / 64) > (1 << 24)) return LRKV_E_SHAPE;
     const void *p[] = {q, B_K, B_V, out};
     for (const void *x : p)
         if (!x || !aligned16(x)) return LRKV_E_INVALID_ARG;
