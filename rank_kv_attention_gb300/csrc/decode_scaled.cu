@@ -50,6 +50,9 @@ namespace {
 
 constexpr int kUnit = 64, kTile = 128;
 constexpr int kStageBytes = kTile * 128;
+// Scales of 16 tokens, which lie in one block: 2^eS_K (NaN: on no page), eS_V, then
+// 2^eR_K and eR_V of every head.
+constexpr int kScaleRow = 2 + 2 * 32 + 2;
 constexpr int kMaxBoxes = 16, kMaxStages = 12;
 // Warps: 16 of the softmax, 4 accumulating, then copies, operands, MMAs and tensor memory.
 constexpr int kSoftmax = 512, kThreads = kSoftmax + 256;
@@ -113,21 +116,6 @@ inline bool make_shape(int H, int r, Shape &s) {
     return true;
 }
 
-// Shared memory after the ring of stages.
-struct Offsets {
-    int img, weights, red, fac, ar, bars, bytes;
-    __host__ __device__ explicit Offsets(const Shape &s) {
-        img = s.stages * kStageBytes;
-        const int one = (s.img_bytes + 1023) / 1024 * 1024;
-        weights = img + 2 * one;
-        red = weights + 4 * s.wrows * 128;  // [2][4 quarters of the heads][maxima 3, sum][8][4 warps]
-        fac = red + 2 * 4 * 4 * 8 * 4 * 4;  // [4][3][32]: alpha, shared and private factor
-        ar = fac + 4 * 3 * 32 * 4;          // [box][128]: the private accumulators
-        bars = ar + s.boxes * 512;
-        bytes = bars + 1152 + 1024;
-    }
-};
-
 struct Bars {
     uint64_t full[kMaxStages], empty[kMaxStages];
     uint64_t img_full[2], img_empty[2];
@@ -137,11 +125,26 @@ struct Bars {
     // of every box (0: the shared rows): operand's offset, accumulator's column,
     // instruction descriptor and (keys) contraction steps
     alignas(16) uint4 kbox[kMaxBoxes + 1], vbox[kMaxBoxes + 1];
+    uint64_t e_full[2], tmem_ready;
     uint32_t tmem;
-    int first_b, first_unit, units;
-    int warp_sum[kThreads / 32];
+    int upto[kThreads];  // units of a thread's requests and of those before it in its warp
 };
-static_assert(sizeof(Bars) <= 1152, "barriers");
+
+// Shared memory after the ring of stages.
+struct Offsets {
+    int img, weights, red, fac, scales, ar, bars, bytes;
+    __host__ __device__ explicit Offsets(const Shape &s) {
+        img = s.stages * kStageBytes;
+        const int one = (s.img_bytes + 1023) / 1024 * 1024;
+        weights = img + 2 * one;
+        red = weights + 4 * s.wrows * 128;  // [2][4 quarters of the heads][maxima 3, sum][8][4 warps]
+        fac = red + 2 * 4 * 4 * 8 * 4 * 4;  // [4][3][32]: alpha, shared and private factor
+        scales = fac + 4 * 3 * 32 * 4;      // [2][8 groups of 16 tokens][kScaleRow]
+        ar = scales + 2 * 8 * kScaleRow * 4;  // [box][128]: the private accumulators
+        bars = ar + s.boxes * 512;
+        bytes = bars + (int)sizeof(Bars) + 1024;
+    }
+};
 
 struct Maps {
     CUtensorMap k[2], v[2];  // S_K, R_K; S_V, R_V: [rows][bytes], box 128 bytes x box_rows
@@ -257,19 +260,31 @@ __global__ void __launch_bounds__(128) scaled_prep_kernel(const __grid_constant_
     }
     const int b = blockIdx.x, h = blockIdx.y, r = S.r;
     const __nv_bfloat16 *B = P.B_K + (size_t)h * 128 * r;
+    // p: groups of r / 8 threads take every `parts`-th channel, eight at most; all
+    // loads are on their way together
+    const int v8 = r / 8, parts = 128 / v8, pt = tid / v8, vc = tid % v8;
+    uint4 w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (pt < parts && pt + i * parts < 128)
+            w[i] = *reinterpret_cast<const uint4 *>(B + (size_t)(pt + i * parts) * r + 8 * vc);
     qs[tid] = __bfloat162float(P.q[((size_t)b * S.H + h) * 128 + tid]);
     __syncthreads();
-    // p: groups of r / 8 threads take every `parts`-th channel
-    const int v8 = r / 8, parts = 128 / v8, pt = tid / v8, vc = tid % v8;
     if (pt < parts) {
         float acc[8] = {};
-#pragma unroll 4
-        for (int d = pt; d < 128; d += parts) {
-            float y[8];
-            Vec16<__nv_bfloat16>::load(B + (size_t)d * r + 8 * vc, y);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) acc[e] = fmaf(qs[d], y[e], acc[e]);
-        }
+        for (int i = 0; i < 8; ++i)
+            if (pt + i * parts < 128) {
+                const float q = qs[pt + i * parts];
+                acc[0] = fmaf(q, bf16lo(w[i].x), acc[0]);
+                acc[1] = fmaf(q, bf16hi(w[i].x), acc[1]);
+                acc[2] = fmaf(q, bf16lo(w[i].y), acc[2]);
+                acc[3] = fmaf(q, bf16hi(w[i].y), acc[3]);
+                acc[4] = fmaf(q, bf16lo(w[i].z), acc[4]);
+                acc[5] = fmaf(q, bf16hi(w[i].z), acc[5]);
+                acc[6] = fmaf(q, bf16lo(w[i].w), acc[6]);
+                acc[7] = fmaf(q, bf16hi(w[i].w), acc[7]);
+            }
 #pragma unroll
         for (int e = 0; e < 8; ++e) part[(pt * v8 + vc) * 8 + e] = acc[e];
     }
@@ -323,13 +338,7 @@ __global__ void __launch_bounds__(128) scaled_prep_kernel(const __grid_constant_
 // ---------------------------------------------------------------------------
 struct Walk {
     int b, L, tok, left, seg;  // left: units of the CTA from this tile on
-    __device__ Walk(const Args &a, const Bars &bar) {
-        b = bar.first_b;
-        left = bar.units;
-        seg = 0;
-        L = left ? a.seq_lens[b] : 0;
-        tok = bar.first_unit * kUnit;
-    }
+    __device__ Walk() : b(0), L(0), tok(0), left(0), seg(0) {}
     __device__ bool live() const { return left > 0; }
     __device__ int rows() const { return min(min(kTile, L - tok), left * kUnit); }
     __device__ bool ends() const { return tok + kTile >= L || left * kUnit <= kTile; }  // of its request here
@@ -345,52 +354,11 @@ struct Walk {
     }
 };
 
-// A token's scale exponents for the heads of one softmax thread; `there`: it is a row
-// of the tile on a page of the pool.
-template <int HT>
-struct TokenScales {
-    bool there;
-    int sk, sv;
-    uint32_t rk[HT / 4], rv[HT / 4];
-    __device__ void load(const Args &a, const Walk &w, int token, int h0, int hn) {
-        there = w.live() && token < w.rows();
-        sk = sv = 0;
-#pragma unroll
-        for (int k = 0; k < HT / 4; ++k) rk[k] = rv[k] = 0;
-        if (!there) return;
-        const int pos = w.tok + token;
-        const int32_t page = a.page_table[(size_t)w.b * a.max_pages + pos / a.c.page_size];
-        there = page >= 0 && page < a.c.num_pages;
-        if (!there) return;
-        const int64_t eb = ((int64_t)page * a.c.page_size + pos % a.c.page_size) / a.c.block;
-        const uint8_t *k = a.c.exp[2] + eb * a.c.H + h0, *v = a.c.exp[3] + eb * a.c.H + h0;
-        sk = a.c.exp[0][eb];
-        sv = a.c.exp[1][eb];
-        if (hn % 4 == 0) {
-#pragma unroll
-            for (int j = 0; j < HT / 4; ++j)
-                if (4 * j < hn) {
-                    rk[j] = reinterpret_cast<const uint32_t *>(k)[j];
-                    rv[j] = reinterpret_cast<const uint32_t *>(v)[j];
-                }
-        } else {
-#pragma unroll
-            for (int j = 0; j < HT; ++j)
-                if (j < hn) {
-                    rk[j / 4] |= (uint32_t)k[j] << (8 * (j & 3));
-                    rv[j / 4] |= (uint32_t)v[j] << (8 * (j & 3));
-                }
-        }
-    }
-    __device__ int key(int k) const { return clamp_exp((rk[k / 4] >> (8 * (k & 3))) & 0xff); }
-    __device__ int value(int k) const { return clamp_exp((rv[k / 4] >> (8 * (k & 3))) & 0xff); }
-};
-
 // HM: heads of the shape, rounded up to 16 or 32.
 //
-// Registers: 80 a thread at launch; the warps that copy and issue give 40 of theirs to
-// the accumulating ones (16 * 32 * 80 + 4 * 32 * (120 + 40) = 768 * 80).
-constexpr int kRegs = 80, kRegsFew = 40, kRegsMany = 120;
+// Registers: 80 a thread at launch; the warps that copy and issue give 24 of theirs to
+// the accumulating ones (16 * 32 * 80 + 4 * 32 * (104 + 56) = 768 * 80).
+constexpr int kRegs = 80, kRegsFew = 56, kRegsMany = 104;
 static_assert(kRegsFew + kRegsMany == 2 * kRegs, "what one group takes another has given");
 template <int HM>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -405,18 +373,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int H = S.H, stages = S.stages, NB = S.boxes;
     const int img_stride = (S.img_bytes + 1023) / 1024 * 1024;
 
-    // ---- this CTA's share
+    // ---- this CTA's share: threads hold consecutive requests; units before each of them
+    const int per = (a.B + kThreads - 1) / kThreads;
     {
-        const int per = (a.B + kThreads - 1) / kThreads, b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
+        const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
         int n = 0;
         for (int b = b0; b < b1; ++b) n += units_of(a.seq_lens[b], a.max_len);
-        int inc = n;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, inc, o);
-            if (lane >= o) inc += v;
-        }
-        if (lane == 31) bar.warp_sum[warp] = inc;
         if (tid == kThreads - 1) {
             for (int s = 0; s < stages; ++s) {
                 mbar_init(&bar.full[s], 1);
@@ -427,22 +389,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_init(&bar.img_empty[k], 1 + kSoftmax);
                 mbar_init(&bar.w_full[k], kSoftmax);
                 mbar_init(&bar.pv_done[k], 1);
+                mbar_init(&bar.e_full[k], 32);
             }
             for (int k = 0; k < 4; ++k) mbar_init(&bar.meet[k], 128);
             mbar_init(&bar.sc_full, 1);
             mbar_init(&bar.sc_empty, kSoftmax);
             mbar_init(&bar.v_empty, 128);
+            mbar_init(&bar.tmem_ready, 1);
             fence_barrier_init();
-            bar.first_b = 0;
-            bar.first_unit = 0;
         }
-        if (warp == kWarpSpare) tmem_alloc(&bar.tmem, S.tmem_cols);
-        if (warp == kWarpCopy && elect_one()) {
-            for (int k = 0; k < 2; ++k) {
-                prefetch_tensormap(&maps.k[k]);
-                prefetch_tensormap(&maps.v[k]);
-            }
+        int inc = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += v;
         }
+        bar.upto[tid] = inc;
         if (warp == kWarpMma && lane <= NB) {
             const int x = lane;
             bar.kbox[x] = x ? make_uint4((S.qrows + S.prow[x - 1]) * 128, S.scol[x - 1], idesc_f8(S.n[x - 1], false),
@@ -451,36 +413,46 @@ __global__ void __launch_bounds__(kThreads, 1)
             bar.vbox[x] = x ? make_uint4((S.wrows + 2 * S.ha[x - 1]) * 128, S.vcol[x - 1], idesc_f8(S.nv[x - 1], true), 0)
                             : make_uint4(0, S.v0, idesc_f8(S.nv0, true), 0);
         }
-        tc_fence_before();
-        __syncthreads();
-        tc_fence_after();
-        uint32_t total = 0, before = inc - n;
-#pragma unroll
-        for (int w = 0; w < kThreads / 32; ++w) {
-            if (w < warp) before += bar.warp_sum[w];
-            total += bar.warp_sum[w];
-        }
-        // (at most 2^24 units; CTAs past the last unit have none, so that no request's CTAs
-        // have a gap)
-        const uint32_t ctas = max(1u, min(gridDim.x, total)), g = min(blockIdx.x, ctas);
-        const uint32_t u0 = total * g / ctas, u1 = min(total, total * (g + 1) / ctas);
-        if (tid == 0) bar.units = (int)(u1 - u0);
-        if (n && u0 >= before && u0 < before + n) {
-            uint32_t at = before;
-            for (int b = b0; b < b1; ++b) {
-                const uint32_t k = units_of(a.seq_lens[b], a.max_len);
-                if (u0 < at + k) {
-                    bar.first_b = b;
-                    bar.first_unit = (int)(u0 - at);
-                    break;
-                }
-                at += k;
+        if (warp == kWarpCopy && elect_one()) {
+            for (int k = 0; k < 2; ++k) {
+                prefetch_tensormap(&maps.k[k]);
+                prefetch_tensormap(&maps.v[k]);
             }
         }
     }
     __syncthreads();
-    const uint32_t tmem = bar.tmem;
     pdl_launch_dependents();
+    Walk w;
+    {
+        // warps' sums, then the thread whose requests hold the first unit (whole warp)
+        constexpr int kWarps = kThreads / 32;
+        int sum = lane < kWarps ? bar.upto[32 * lane + 31] : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += v;
+        }
+        // (at most 2^24 units; CTAs past the last unit have none, so that no request's CTAs
+        // have a gap)
+        const uint32_t total = __shfl_sync(0xffffffffu, sum, 31);
+        const uint32_t ctas = max(1u, min(gridDim.x, total)), g = min(blockIdx.x, ctas);
+        const uint32_t u0 = total * g / ctas, u1 = min(total, total * (g + 1) / ctas);
+        w.left = (int)(u1 - u0);
+        if (w.left > 0) {
+            const int wp = __popc(__ballot_sync(0xffffffffu, (uint32_t)sum <= u0));  // warps that end before it
+            const uint32_t base = __shfl_sync(0xffffffffu, sum, max(wp - 1, 0)) * (wp > 0);
+            const int th = __popc(__ballot_sync(0xffffffffu, base + bar.upto[32 * wp + lane] <= u0));
+            uint32_t at = base + (th > 0 ? bar.upto[32 * wp + th - 1] : 0);
+            w.b = (32 * wp + th) * per;
+            for (;; ++w.b) {
+                w.L = a.seq_lens[w.b];
+                const uint32_t k = units_of(w.L, a.max_len);
+                if (u0 < at + k) break;
+                at += k;
+            }
+            w.tok = (int)(u0 - at) * kUnit;
+        }
+    }
     bool ok = true;
 
     if (warp >= kWarpCopy) {
@@ -489,7 +461,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             // ================= cache tiles =================
             // lane k looks up the pool row of the tile's k-th group of box_rows rows (past every
             // row, which reads as zeros, where its page is none)
-            Walk w(a, bar);
             const int R = a.box_rows, none = a.c.num_pages * a.c.page_size;
             auto lookup = [&](const Walk &t) {
                 const int at = t.tok + lane * R;
@@ -551,7 +522,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) {
                 pdl_wait();
                 int last = -1;
-                for (Walk w(a, bar); ok && w.live(); w.next(a)) {
+                for (; ok && w.live(); w.next(a)) {
                     if (w.seg == last) continue;
                     const int s = last = w.seg, k = s & 1;
                     if (s >= 2 && !mbar_wait(&bar.img_empty[k], ((s >> 1) - 1) & 1)) {
@@ -567,6 +538,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else if (warp == kWarpMma) {
             // ================= MMA issuer =================
             const uint32_t base = smem_u32(smem);
+            ok = __all_sync(0xffffffffu, mbar_wait(&bar.tmem_ready, 0));
+            const uint32_t tmem = bar.tmem;
             int s = 0, n = 0, i = 0;  // stage, times the ring went round; tile
             auto all_wait = [&](uint64_t *b, uint32_t parity) { return (bool)__all_sync(0xffffffffu, mbar_wait(b, parity)); };
             auto keys = [&](const Walk &t, bool first) -> bool {
@@ -632,8 +605,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 return true;
             };
-            Walk w(a, bar);
-            if (w.live()) {
+            if (ok && w.live()) {
                 int rows = w.rows(), seg = w.seg;
                 ok = keys(w, true);
                 while (ok && w.live()) {
@@ -650,25 +622,69 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             if (!ok && lane == 0) status_or(a.status, LRKV_STATUS_TIMEOUT);
+        } else {
+            // ================= tensor memory, scales of the tiles =================
+            tmem_alloc(&bar.tmem, S.tmem_cols);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.tmem_ready);
+            // lane: 16 tokens, a quarter of the heads
+            const int grp = lane >> 2, quarter = lane & 3, hn = H / 4, h0 = quarter * hn;
+            for (int i = 0; ok && w.live(); ++i, w.next(a)) {
+                const int pos = w.tok + 16 * grp;
+                float sk = __uint_as_float(0x7fffffffu), sv = 0.f, rk[8], rv[8];
+                int64_t eb = -1;
+                if (16 * grp < w.rows()) {
+                    const int32_t page = a.page_table[(size_t)w.b * a.max_pages + pos / a.c.page_size];
+                    if (page >= 0 && page < a.c.num_pages)
+                        eb = ((int64_t)page * a.c.page_size + pos % a.c.page_size) / a.c.block;
+                }
+                if (eb >= 0) {
+                    sk = exp2i(clamp_exp(a.c.exp[0][eb]));
+                    sv = (float)clamp_exp(a.c.exp[1][eb]);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (j < hn) {
+                            rk[j] = exp2i(clamp_exp(a.c.exp[2][eb * H + h0 + j]));
+                            rv[j] = (float)clamp_exp(a.c.exp[3][eb * H + h0 + j]);
+                        }
+                }
+                // the tile before the last is done with this buffer
+                if (i > 1) ok = __all_sync(0xffffffffu, mbar_wait(&bar.w_full[i & 1], ((i >> 1) - 1) & 1));
+                if (!ok) break;
+                float *row = reinterpret_cast<float *>(smem + off.scales) + ((i & 1) * 8 + grp) * kScaleRow;
+                if (quarter == 0) {
+                    row[0] = sk;
+                    row[1] = sv;
+                }
+                if (eb >= 0) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (j < hn) {
+                            row[2 + h0 + j] = rk[j];
+                            row[34 + h0 + j] = rv[j];
+                        }
+                }
+                mbar_arrive(&bar.e_full[i & 1]);
+            }
+            if (!ok && lane == 0) status_or(a.status, LRKV_STATUS_TIMEOUT);
         }
     } else if (warp < kSoftmax / 32) {
         // ================= scores and weights =================
         // warp: tokens 32 (warp & 3) + lane of a tile, heads h0 .. h0 + hn - 1 (a quarter)
         const int hn = H / 4, grp = warp >> 2, h0 = grp * hn, token = 32 * (warp & 3) + lane;
-        const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
         float m[HT], l[HT];
         uint32_t met = 0;
         auto meet = [&]() -> bool {  // the four warps of these heads
             mbar_arrive(&bar.meet[grp]);
             return __all_sync(0xffffffffu, mbar_wait(&bar.meet[grp], met++ & 1));
         };
-        Walk w(a, bar);
+        ok = __all_sync(0xffffffffu, mbar_wait(&bar.tmem_ready, 0));
+        const uint32_t lanes = bar.tmem + ((uint32_t)(32 * (warp & 3)) << 16);
         int last = -1;
-        TokenScales<HT> e;
-        e.load(a, w, token, h0, hn);
-        for (int i = 0; ok && w.live(); ++i) {
+        for (int i = 0; ok && w.live(); ++i, w.next(a)) {
             const bool first = w.seg != last, ends = w.ends();
-            const int seg = last = w.seg, b = w.b;
+            const int seg = last = w.seg;
             if (first) {
 #pragma unroll
                 for (int k = 0; k < HT; ++k) {
@@ -680,11 +696,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             const float *f = reinterpret_cast<const float *>(smem + off.img + (seg & 1) * img_stride +
                                                              (S.qrows + S.prows) * 128) + h0;
-            ok = __all_sync(0xffffffffu, mbar_wait(&bar.sc_full, i & 1));
+            const float *scale = reinterpret_cast<const float *>(smem + off.scales) + ((i & 1) * 8 + token / 16) * kScaleRow;
+            ok = __all_sync(0xffffffffu, mbar_wait(&bar.e_full[i & 1], (i >> 1) & 1) && mbar_wait(&bar.sc_full, i & 1));
             if (!ok) break;
             tc_fence_after();
             float x[HT];
-            const float sk = exp2i(clamp_exp(e.sk));
+            const float sk = scale[0];
+            const bool there = token < w.rows() && sk == sk;
 #pragma unroll
             for (int k = 0; k < HT; k += 2) {  // two heads' columns on their way together
                 uint32_t vs[2][4], va[2][4], vb[2][4];
@@ -706,7 +724,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     float t = sum(va[j]);
                     if (two[j]) t += sum(vb[j]);
                     const int q = min(k + j, hn - 1);
-                    x[k + j] = e.there ? sum(vs[j]) * (f[q] * sk) + t * (f[H + q] * exp2i(e.key(k + j))) : -INFINITY;
+                    x[k + j] = there ? sum(vs[j]) * (f[q] * sk) + t * (f[H + q] * scale[2 + h0 + q]) : -INFINITY;
                 }
             }
             tc_fence_before();
@@ -714,12 +732,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (ends) mbar_arrive(&bar.img_empty[seg & 1]);  // (the factors were read)
             // (two buffers in turn: a warp writes the one after next only when all have met again)
             float *red = reinterpret_cast<float *>(smem + off.red) + ((i & 1) * 4 + grp) * HT * 16;
-            const float es = (float)clamp_exp(e.sv);
+            const float es = scale[1];
+            float er[HT];
             float mine[3] = {0.f, 0.f, 0.f};
 #pragma unroll
             for (int k = 0; k < HT; ++k)
                 if (k < hn) {
-                    const float m0 = warp_max(x[k]), m1 = warp_max(x[k] + es), m2 = warp_max(x[k] + (float)e.value(k));
+                    er[k] = there ? scale[34 + h0 + k] : 0.f;
+                    const float m0 = warp_max(x[k]), m1 = warp_max(x[k] + es), m2 = warp_max(x[k] + er[k]);
                     if (lane == k) {
                         mine[0] = m0;
                         mine[1] = m1;
@@ -729,9 +749,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane < hn)
 #pragma unroll
                 for (int k = 0; k < 3; ++k) red[(k * HT + lane) * 4 + (warp & 3)] = mine[k];
-            w.next(a);  // (the next tile's scales are on their way during the rest of this one)
-            TokenScales<HT> en;
-            en.load(a, w, token, h0, hn);
             ok = meet();
             // the operand of the tile before the last has been read
             if (ok && i > 1) ok = __all_sync(0xffffffffu, mbar_wait(&bar.pv_done[i & 1], ((i >> 1) - 1) & 1));
@@ -759,7 +776,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         fac[64 + h] = ex2f(mr - ref - 8.f);
                     }
                     // both operands' terms, a pair at a time
-                    const float y = ex2f(x[k] + es - ms + 8.f), z = ex2f(x[k] + (float)e.value(k) - mr + 8.f);
+                    const float y = ex2f(x[k] + es - ms + 8.f), z = ex2f(x[k] + er[k] - mr + 8.f);
                     const uint16_t t1 = e4m3x2_from_f32(y, z);
                     const uint32_t h2 = f16x2_from_e4m3x2(t1);
                     const float2 g = __half22float2(*reinterpret_cast<const __half2 *>(&h2));
@@ -785,7 +802,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 if (lane < hn) red[(3 * HT + lane) * 4 + (warp & 3)] = sum;
                 if (!(ok = meet())) break;
-                float *ml = a.st.ml + ((int64_t)b + blockIdx.x) * H * 2;
+                float *ml = a.st.ml + ((int64_t)w.b + blockIdx.x) * H * 2;
 #pragma unroll
                 for (int k = 0; k < HT; ++k)
                     if (k < hn && token == k) {
@@ -794,20 +811,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ml[2 * (h0 + k) + 1] = (v.x + v.y) + (v.z + v.w);
                     }
             }
-            e = en;
         }
         if (!ok && lane == 0) status_or(a.status, LRKV_STATUS_TIMEOUT);
     } else {
         // ================= value accumulators: thread = column =================
         reg_inc<kRegsMany>();
         const int col = tid - kSoftmax, quad = warp & 3;
-        const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16);
+        ok = __all_sync(0xffffffffu, mbar_wait(&bar.tmem_ready, 0));
+        const uint32_t lanes = bar.tmem + ((uint32_t)(32 * quad) << 16);
         const uint32_t magic = 0xffffffffu / (uint32_t)S.r + 1u;  // 2^32 / r rounded up
         auto head_of = [&](int c) { return min((int)__umulhi((uint32_t)c, magic), H - 1); };
         float as[HM];
         float *ar = reinterpret_cast<float *>(smem + off.ar) + col;
         int last = -1, i = 0;
-        for (Walk w(a, bar); ok && w.live(); ++i, w.next(a)) {
+        for (; ok && w.live(); ++i, w.next(a)) {
             const bool first = w.seg != last;
             last = w.seg;
             if (first) {
@@ -888,7 +905,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     if (warp == kWarpSpare) {
         tc_fence_after();
-        tmem_dealloc(tmem, S.tmem_cols);
+        tmem_dealloc(bar.tmem, S.tmem_cols);
     }
 }
 

@@ -195,13 +195,13 @@ __global__ void __launch_bounds__(kThreads) decode_scaled_any_kernel(const __gri
 // before the states are there, and value sums are read together with the maxima that
 // weigh them.
 // ---------------------------------------------------------------------------
-constexpr int kMergeThreads = 512, kMergeStates = 256, kMergeHeld = 8, kMergeRows = 2;
+constexpr int kMergeThreads = 512, kMergeStates = 256, kMergeHeld = 4, kMergeRows = 3;
 
-__global__ void __launch_bounds__(kMergeThreads) scaled_merge_kernel(const __grid_constant__ ScaledMergeArgs P) {
+__global__ void __launch_bounds__(kMergeThreads, 3) scaled_merge_kernel(const __grid_constant__ ScaledMergeArgs P) {
     __shared__ float fs[kMergeStates], sums[kMergeThreads];
     __shared__ float red[2][kMergeThreads / 32];
     const int h = blockIdx.y, b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int H = P.H, d_h = P.d_h, r = P.r, W = d_h + r, cols = (W + 31) & ~31;
+    const int H = P.H, d_h = P.d_h, r = P.r, W = d_h + r, cols = (W + 31) & ~31, threads = blockDim.x;
     // ---- B_V[h] in tasks of eight columns of a row: the first ones of every thread.  (The
     // kernel before this one started after all that is in front of the call was done.)
     const int v8 = r / 8, tasks = d_h * v8;
@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(kMergeThreads) scaled_merge_kernel(const __gri
     uint4 bv[kMergeRows];
 #pragma unroll
     for (int j = 0; j < kMergeRows; ++j)
-        if (tid + j * kMergeThreads < tasks) bv[j] = reinterpret_cast<const uint4 *>(B)[tid + j * kMergeThreads];
+        if (tid + j * threads < tasks) bv[j] = reinterpret_cast<const uint4 *>(B)[tid + j * threads];
     pdl_wait();
     pdl_launch_dependents();
     const int32_t L = P.seq_lens[b];
@@ -228,13 +228,13 @@ __global__ void __launch_bounds__(kMergeThreads) scaled_merge_kernel(const __gri
         s0 = (int64_t)b * P.splits;
         ns = P.splits;
     }
-    // (at most 256 parts or one state a CTA)
+    // (at most 256 parts, or a state of every CTA)
     float m = -INFINITY, l = 0.f;
     if (tid < ns) {
         m = P.st.ml[((s0 + tid) * H + h) * 2];
         l = P.st.ml[((s0 + tid) * H + h) * 2 + 1];
     }
-    const int groups = kMergeThreads / cols, g = tid / cols, c = tid - g * cols;
+    const int groups = threads / cols, g = tid / cols, c = tid - g * cols;
     const bool mine = g < groups && c < W;
     const float *acc = P.st.acc + s0 * H * W + (c < d_h ? (size_t)h * d_h + c : (size_t)H * d_h + h * r + c - d_h);
     float held[kMergeHeld];
@@ -248,8 +248,7 @@ __global__ void __launch_bounds__(kMergeThreads) scaled_merge_kernel(const __gri
     for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
     if (lane == 0) red[0][warp] = M;
     __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kMergeThreads / 32; ++w) M = fmaxf(M, red[0][w]);
+    for (int w = 0; w < threads / 32; ++w) M = fmaxf(M, red[0][w]);
     const float ref = M == -INFINITY ? 0.f : M;
     // a part without rows has written no value sums
     const bool none = m == -INFINITY && l == 0.f;
@@ -261,8 +260,7 @@ __global__ void __launch_bounds__(kMergeThreads) scaled_merge_kernel(const __gri
     if (lane == 0) red[1][warp] = l;
     __syncthreads();
     l = 0.f;
-#pragma unroll
-    for (int w = 0; w < kMergeThreads / 32; ++w) l += red[1][w];
+    for (int w = 0; w < threads / 32; ++w) l += red[1][w];
     const float inv = l != 0.f ? 1.f / l : 0.f;  // (NaN stays NaN)
 
     float x = 0.f;
@@ -294,18 +292,18 @@ __global__ void __launch_bounds__(kMergeThreads) scaled_merge_kernel(const __gri
         s = fmaf(o[4], bf16lo(w.z), s); s = fmaf(o[5], bf16hi(w.z), s); s = fmaf(o[6], bf16lo(w.w), s);
         return fmaf(o[7], bf16hi(w.w), s);
     };
-    if (tasks <= kMergeRows * kMergeThreads) {
+    if (tasks <= kMergeRows * threads) {
 #pragma unroll
         for (int j = 0; j < kMergeRows; ++j)
-            if (tid + j * kMergeThreads < tasks) part[tid + j * kMergeThreads] = dot(tid + j * kMergeThreads, bv[j]);
+            if (tid + j * threads < tasks) part[tid + j * threads] = dot(tid + j * threads, bv[j]);
         __syncthreads();
-        for (int d = tid; d < d_h; d += kMergeThreads) {
+        for (int d = tid; d < d_h; d += threads) {
             float s = sums[d];
             for (int k = 0; k < v8; ++k) s += part[d * v8 + k];
             out[d] = __float2bfloat16_rn(s * inv);
         }
     } else {
-        for (int d = tid; d < d_h; d += kMergeThreads) {
+        for (int d = tid; d < d_h; d += threads) {
             float s = sums[d];
             for (int k = 0; k < v8; ++k) s += dot(k, reinterpret_cast<const uint4 *>(B)[d * v8 + k]);
             out[d] = __float2bfloat16_rn(s * inv);
@@ -384,7 +382,10 @@ cudaError_t launch_scaled_row_queries(const ScaledRows &rows, int max_len, int32
 }
 
 cudaError_t launch_scaled_merge(const ScaledMergeArgs &m, cudaStream_t s) {
-    return launch_pdl(scaled_merge_kernel, dim3(m.B, m.H), dim3(kMergeThreads), 0, s, m);
+    // 256 threads where CTAs are many (each merges few states then; 64 requests of 16 heads:
+    // 12 us with 512), and the columns fit
+    const bool few = (int64_t)m.B * m.H < 2 * device_sm_count() || m.d_h + m.r > 256;
+    return launch_pdl(scaled_merge_kernel, dim3(m.B, m.H), dim3(few ? kMergeThreads : 256), 0, s, m);
 }
 
 }  // namespace lrkv
