@@ -75,6 +75,7 @@ struct Shape {
     uint16_t nv[kMaxBoxes];    // value columns: (head - ha) * 2 + term
     uint16_t vcol[kMaxBoxes];
     uint16_t v0, nv0;          // the shared rows' value columns
+    uint16_t vbufs, vcols;     // value accumulators (tiles in turn), columns of one
 };
 
 inline bool make_shape(int H, int r, Shape &s) {
@@ -107,6 +108,9 @@ inline bool make_shape(int H, int r, Shape &s) {
         if (s.n[t] > 256 || s.nv[t] > 32) return false;
     }
     if (col > 512) return false;
+    s.vcols = (uint16_t)(col - s.v0);
+    s.vbufs = col + s.vcols <= 512 ? 2 : 1;
+    col += (s.vbufs - 1) * s.vcols;
     s.tmem_cols = 32;
     while (s.tmem_cols < col) s.tmem_cols *= 2;
     s.img_bytes = (s.qrows + s.prows) * 128 + 8 * H;
@@ -119,9 +123,9 @@ inline bool make_shape(int H, int r, Shape &s) {
 struct Bars {
     uint64_t full[kMaxStages], empty[kMaxStages];
     uint64_t img_full[2], img_empty[2];
-    uint64_t w_full[2], pv_done[2];
+    uint64_t w_full[4], pv_done[2], v_empty[2];
     uint64_t meet[4];  // of the 128 softmax threads of a quarter of the heads
-    uint64_t sc_full, sc_empty, v_empty;
+    uint64_t sc_full, sc_empty;
     // of every box (0: the shared rows): operand's offset, accumulator's column,
     // instruction descriptor and (keys) contraction steps
     alignas(16) uint4 kbox[kMaxBoxes + 1], vbox[kMaxBoxes + 1];
@@ -388,13 +392,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_init(&bar.img_full[k], 1);
                 mbar_init(&bar.img_empty[k], 1 + kSoftmax);
                 mbar_init(&bar.w_full[k], kSoftmax);
+                mbar_init(&bar.w_full[k + 2], kSoftmax);
+                mbar_init(&bar.v_empty[k], 128);
                 mbar_init(&bar.pv_done[k], 1);
                 mbar_init(&bar.e_full[k], 32);
             }
             for (int k = 0; k < 4; ++k) mbar_init(&bar.meet[k], 128);
             mbar_init(&bar.sc_full, 1);
             mbar_init(&bar.sc_empty, kSoftmax);
-            mbar_init(&bar.v_empty, 128);
             mbar_init(&bar.tmem_ready, 1);
             fence_barrier_init();
         }
@@ -472,6 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 return row;
             };
+            const uint64_t stream = l2_evict_first_policy();
             int s = 0, n = 0;  // stage, times the ring went round
             auto send = [&](const CUtensorMap *m, int rows, int row) {  // the keys or values of one tile
                 const int groups = (rows + R - 1) / R;
@@ -488,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         mbar_arrive_expect_tx(&bar.full[s], groups * R * 128);
 #pragma unroll
                         for (int g = 0; g < 8; ++g)
-                            if (g < groups) tma_load_2d(st + g * R * 128, map, x, y[g], &bar.full[s]);
+                            if (g < groups) tma_load_2d_hint(st + g * R * 128, map, x, y[g], &bar.full[s], stream);
                     }
                     __syncwarp();
                     if (++s == stages) {
@@ -571,8 +577,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 return true;
             };
             auto values = [&](int rows, int j) -> bool {  // of the j-th tile
-                if (!all_wait(&bar.w_full[j & 1], (j >> 1) & 1)) return false;
-                if (j > 0 && !all_wait(&bar.v_empty, (j - 1) & 1)) return false;
+                if (!all_wait(&bar.w_full[j & 3], (j >> 2) & 1)) return false;
+                const int vb = S.vbufs == 2 ? j & 1 : 0, round = S.vbufs == 2 ? j >> 1 : j;
+                if (round > 0 && !all_wait(&bar.v_empty[vb], (round - 1) & 1)) return false;
                 const int steps = (rows + 31) / 32;
                 const uint32_t weights = base + off.weights + (j & 1) * 2 * S.wrows * 128;
                 for (int x = 0; x <= NB; ++x) {
@@ -593,7 +600,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const uint32_t al = sw128_desc_lo(base + s * kStageBytes, 16), bl = sw128_desc_lo(weights + box.x, 16);
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            if (k < steps) tc_mma_f8(tmem + box.y, al + 256 * k, bl + 2 * k, box.z, k != 0);
+                            if (k < steps) tc_mma_f8(tmem + vb * S.vcols + box.y, al + 256 * k, bl + 2 * k, box.z, k != 0);
                         tc_commit(&bar.empty[s]);
                         if (x == NB) tc_commit(&bar.pv_done[j & 1]);
                     }
@@ -632,38 +639,46 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int grp = lane >> 2, quarter = lane & 3, hn = H / 4, h0 = quarter * hn;
             for (int i = 0; ok && w.live(); ++i, w.next(a)) {
                 const int pos = w.tok + 16 * grp;
-                float sk = __uint_as_float(0x7fffffffu), sv = 0.f, rk[8], rv[8];
                 int64_t eb = -1;
                 if (16 * grp < w.rows()) {
                     const int32_t page = a.page_table[(size_t)w.b * a.max_pages + pos / a.c.page_size];
                     if (page >= 0 && page < a.c.num_pages)
                         eb = ((int64_t)page * a.c.page_size + pos % a.c.page_size) / a.c.block;
                 }
+                uint32_t sk = 0, sv = 0, k4[2] = {0, 0}, v4[2] = {0, 0};
                 if (eb >= 0) {
-                    sk = exp2i(clamp_exp(a.c.exp[0][eb]));
-                    sv = (float)clamp_exp(a.c.exp[1][eb]);
+                    const uint8_t *ek = a.c.exp[2] + eb * H + h0, *ev = a.c.exp[3] + eb * H + h0;
+                    sk = a.c.exp[0][eb];
+                    sv = a.c.exp[1][eb];
+                    if (hn % 4 == 0) {  // (then these are aligned words)
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        if (j < hn) {
-                            rk[j] = exp2i(clamp_exp(a.c.exp[2][eb * H + h0 + j]));
-                            rv[j] = (float)clamp_exp(a.c.exp[3][eb * H + h0 + j]);
+                        for (int j = 0; j < 2; ++j)
+                            if (4 * j < hn) {
+                                k4[j] = reinterpret_cast<const uint32_t *>(ek)[j];
+                                v4[j] = reinterpret_cast<const uint32_t *>(ev)[j];
+                            }
+                    } else {
+#pragma unroll 1
+                        for (int j = hn - 1; j >= 0; --j) {
+                            k4[1] = k4[1] << 8 | k4[0] >> 24;
+                            v4[1] = v4[1] << 8 | v4[0] >> 24;
+                            k4[0] = k4[0] << 8 | ek[j];
+                            v4[0] = v4[0] << 8 | ev[j];
                         }
+                    }
                 }
                 // the tile before the last is done with this buffer
-                if (i > 1) ok = __all_sync(0xffffffffu, mbar_wait(&bar.w_full[i & 1], ((i >> 1) - 1) & 1));
+                if (i > 1) ok = __all_sync(0xffffffffu, mbar_wait(&bar.w_full[(i - 2) & 3], ((i - 2) >> 2) & 1));
                 if (!ok) break;
                 float *row = reinterpret_cast<float *>(smem + off.scales) + ((i & 1) * 8 + grp) * kScaleRow;
                 if (quarter == 0) {
-                    row[0] = sk;
-                    row[1] = sv;
+                    row[0] = eb >= 0 ? exp2i(clamp_exp(sk)) : __uint_as_float(0x7fffffffu);
+                    row[1] = (float)clamp_exp(sv);
                 }
-                if (eb >= 0) {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        if (j < hn) {
-                            row[2 + h0 + j] = rk[j];
-                            row[34 + h0 + j] = rv[j];
-                        }
+#pragma unroll 1
+                for (int j = 0; j < hn; ++j) {
+                    row[2 + h0 + j] = exp2i(clamp_exp((j < 4 ? k4[0] : k4[1]) >> (8 * (j & 3)) & 0xff));
+                    row[34 + h0 + j] = (float)clamp_exp((j < 4 ? v4[0] : v4[1]) >> (8 * (j & 3)) & 0xff);
                 }
                 mbar_arrive(&bar.e_full[i & 1]);
             }
@@ -788,7 +803,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     wr[o2] = (uint8_t)(t2 >> 8);
                 }
             fence_proxy_async_smem();
-            mbar_arrive(&bar.w_full[i & 1]);
+            mbar_arrive(&bar.w_full[i & 3]);
             if (ends) {
                 // the sums of all tokens: over the warp, then over the four warps
                 float sum = 0.f;
@@ -831,16 +846,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int h = 0; h < HM; ++h) as[h] = 0.f;
             }
-            ok = __all_sync(0xffffffffu, mbar_wait(&bar.w_full[i & 1], (i >> 1) & 1) &&
+            ok = __all_sync(0xffffffffu, mbar_wait(&bar.w_full[i & 3], (i >> 2) & 1) &&
                                              mbar_wait(&bar.pv_done[i & 1], (i >> 1) & 1));
             if (!ok) break;
             tc_fence_after();
+            const int vb = S.vbufs == 2 ? i & 1 : 0;
+            const uint32_t from = lanes + vb * S.vcols;
             const float *fac = reinterpret_cast<const float *>(smem + off.fac) + (i & 3) * 3 * 32;
 #pragma unroll
             for (int g = 0; g < HM / 16; ++g)
                 if (16 * g < H) {
                     uint32_t v[32];
-                    tmem_ld32(lanes + S.v0 + 32 * g, v);
+                    tmem_ld32(from + S.v0 + 32 * g, v);
 #pragma unroll
                     for (int k = 0; k < 16; k += 4) {
                         const float4 al = *reinterpret_cast<const float4 *>(&fac[16 * g + k]);
@@ -864,8 +881,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int j = 0; j < 4; ++j)
                     if (t0 + j < NB) {
                         const int t = t0 + j, ha = S.ha[t], hA = head_of(128 * t + 32 * quad), hB = head_of(128 * t + 32 * quad + 31);
-                        tmem_ld2(lanes + S.vcol[t] + 2 * (hA - ha), v[j]);
-                        tmem_ld2(lanes + S.vcol[t] + 2 * (hB - ha), u[j]);
+                        tmem_ld2(from + S.vcol[t] + 2 * (hA - ha), v[j]);
+                        tmem_ld2(from + S.vcol[t] + 2 * (hB - ha), u[j]);
                     }
                 tmem_wait_ld();
 #pragma unroll
@@ -875,7 +892,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const int h = head_of(128 * t + col);
                         for (int k = hA + 1; k < hB; ++k) {
                             uint32_t x[2];
-                            tmem_ld2(lanes + S.vcol[t] + 2 * (k - ha), x);
+                            tmem_ld2(from + S.vcol[t] + 2 * (k - ha), x);
                             tmem_wait_ld();
                             if (h == k) {
                                 v[j][0] = x[0];
@@ -888,7 +905,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
             }
             tc_fence_before();
-            mbar_arrive(&bar.v_empty);
+            mbar_arrive(&bar.v_empty[vb]);
             if (w.ends()) {
                 float *acc = a.st.acc + ((int64_t)w.b + blockIdx.x) * H * (128 + S.r);
 #pragma unroll
