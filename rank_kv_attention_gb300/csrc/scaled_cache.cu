@@ -22,12 +22,19 @@ namespace {
 // the next request's key counts two more), so u has one owner: the last b with
 // key(b) <= u.  A few u have none; there are n / block + 2 B of them.
 //
-// One warp takes one head (shared rows: one group) of one pool of a unit: it
-// holds the values in registers where they fit (16 vectors a lane: 64 rows of
-// 64 bf16), takes their maximum, and writes the codes; longer ones are read
-// twice, the second time out of L1 or L2.
+// A CTA takes a slab of neighbouring heads of one pool of a unit.  A thread stays with
+// one 16-byte column of it and takes every rows_par-th row, so rows are read and codes
+// written whole; it holds its values in registers (16 vectors: 64 rows of a slab of
+// 1 KB), the heads' maxima meet in shared memory, and the codes go out.  Longer blocks
+// are read twice, the second time out of L2.  (One warp per head, with rows of 96
+// bytes, took 41 us for 16,384 bf16 rows, 13 at the copy bandwidth.)
 // ---------------------------------------------------------------------------
-constexpr int kWriteWarps = 8, kHeld = 16;
+constexpr int kWriteThreads = 256, kHeld = 16, kSlabVecs = 64;
+
+// Slabs of a pool: heads of one, and how many.
+struct Slabs {
+    int heads[4], count[4];
+};
 
 // The last b in [0, B) with cu[b] / block + 2 b <= u, or -1 (whole warp).
 __device__ __forceinline__ int request_of_unit(const int32_t *cu, int B, int block, int64_t u, int lane) {
@@ -120,20 +127,22 @@ __device__ __forceinline__ uint32_t shrink_codes(uint32_t w, float s) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(32 * kWriteWarps) write_scaled_kernel(const __grid_constant__ ScaledWriteArgs a) {
+__global__ void __launch_bounds__(kWriteThreads) write_scaled_kernel(const __grid_constant__ ScaledWriteArgs a,
+                                                                     const __grid_constant__ Slabs slabs) {
     constexpr int V = Bits<T>::V;
+    __shared__ uint32_t tops[2][kWriteThreads];
     const ScaledPools &c = a.c;
-    const int lane = threadIdx.x & 31;
+    const int tid = threadIdx.x, lane = tid & 31;
     const int64_t u = blockIdx.x;
-    int item = blockIdx.y * kWriteWarps + (threadIdx.x >> 5);
+    tops[0][tid] = tops[1][tid] = 0;
+    __syncthreads();
     pdl_wait();
     pdl_launch_dependents();
-    if (item >= 2 * (c.G + c.H)) return;
-    const bool speaks = item == 0 && lane == 0;  // flags a unit's faults
-    // pool and head
-    int k = 0;
-    while (item >= c.heads(k)) item -= c.heads(k++);
-    const int heads = c.heads(k), width = c.width(k);
+    const bool speaks = blockIdx.y == 0 && tid == 0;  // flags a unit's faults
+    // pool, heads h0 .. h0 + nh - 1
+    int k = 0, slab = blockIdx.y;
+    while (slab >= slabs.count[k]) slab -= slabs.count[k++];
+    const int heads = c.heads(k), width = c.width(k), h0 = slab * slabs.heads[k], nh = min(slabs.heads[k], heads - h0);
 
     // ---- the unit's rows i0 .. i1 - 1, from position p0 on
     const int b = request_of_unit(a.rows.cu_rows, a.rows.B, c.block, u, lane);
@@ -158,26 +167,19 @@ __global__ void __launch_bounds__(32 * kWriteWarps) write_scaled_kernel(const __
     }
     i1 = min(i1, rz);
     if (i0 >= i1) return;
-    const int p0 = (int)(pa + (i0 - ra));
+    const int p0 = (int)(pa + (i0 - ra)), rows = (int)(i1 - i0);
 
-    // ---- values: vector v of the unit is row v / vpr, vector v % vpr of the head
-    const int vpr = width / V, nv = (int)(i1 - i0) * vpr;
-    const uint32_t magic = 0xffffffffu / (uint32_t)vpr + 1u;  // 2^32 / vpr rounded up; v < 2^17: exact
-    auto row_of = [&](int v) { return vpr == 1 ? v : (int)__umulhi((uint32_t)v, magic); };
-    const int64_t ld = a.ld[k];
-    const T *x = static_cast<const T *>(a.x[k]) + i0 * ld + item * width;
-    auto at = [&](int v) -> const uint4 * {
-        const int row = row_of(v);
-        return reinterpret_cast<const uint4 *>(x + row * ld + (v - row * vpr) * V);
-    };
-    const bool held = nv <= 32 * kHeld;
+    // ---- this thread's column and rows
+    const int vpr = nh * width / V, rows_par = kWriteThreads / vpr;
+    const int row0 = tid / vpr, cv = tid - row0 * vpr, hl = cv * V / width;  // head in the slab
+    const bool active = row0 < rows_par;
+    const int mine = active && row0 < rows ? (rows - row0 + rows_par - 1) / rows_par : 0;
+    const int64_t ld = a.ld[k], step = ld * rows_par;
+    const T *x = static_cast<const T *>(a.x[k]) + (i0 + row0) * ld + h0 * width + cv * V;
     uint4 val[kHeld];
-    uint32_t top = 0;
-    if (held) {
 #pragma unroll
-        for (int j = 0; j < kHeld; ++j)
-            if (lane + 32 * j < nv) val[j] = *at(lane + 32 * j);
-    }
+    for (int j = 0; j < kHeld; ++j)
+        if (j < mine) val[j] = *reinterpret_cast<const uint4 *>(x + j * step);
     // (the lookups of the destination are on their way meanwhile)
     const int32_t page = a.rows.page_table[(size_t)b * a.rows.max_pages + p0 / c.page_size];
     if (page < 0 || page >= c.num_pages) {
@@ -185,58 +187,56 @@ __global__ void __launch_bounds__(32 * kWriteWarps) write_scaled_kernel(const __
         return;
     }
     const int slot = p0 % c.page_size, before = slot % c.block;
-    const int nb = c.page_size / c.block;
-    uint8_t *eb = c.exp[k] + ((int64_t)page * nb + slot / c.block) * heads + item;
-    const int old = before ? clamp_exp(*eb) : LRKV_SCALED_MIN_EXP;
-    uint8_t *code = c.code[k] + ((int64_t)page * c.page_size + slot) * heads * width + item * width;
+    uint8_t *eb = c.exp[k] + ((int64_t)page * c.page_size + slot) / c.block * heads + h0 + hl;
+    const int old = before && active ? clamp_exp(*eb) : LRKV_SCALED_MIN_EXP;
     const int row_bytes = heads * width;
+    uint8_t *code = c.code[k] + ((int64_t)page * c.page_size + slot + row0) * row_bytes + h0 * width + cv * V;
 
-    if (held) {
+    uint32_t top = 0;
 #pragma unroll
-        for (int j = 0; j < kHeld; ++j)
-            if (lane + 32 * j < nv) top = max(top, Bits<T>::top(val[j]));
-    } else {
-        for (int v = lane; v < nv; v += 32) top = max(top, Bits<T>::top(*at(v)));
-    }
-    top = __reduce_max_sync(0xffffffffu, top);
-    const bool odd = top >= kInf;  // infinities or NaN: the finite ones decide
+    for (int j = 0; j < kHeld; ++j)
+        if (j < mine) top = max(top, Bits<T>::top(val[j]));
+    for (int j = kHeld; j < mine; ++j) top = max(top, Bits<T>::top(*reinterpret_cast<const uint4 *>(x + j * step)));
+    if (mine) atomicMax(&tops[0][hl], top);
+    // infinities or NaN in the slab: the finite values decide
+    const bool odd = __syncthreads_or(top >= kInf);
     if (odd) {
         top = 0;
-        for (int v = lane; v < nv; v += 32) top = max(top, top_finite<T>(*at(v)));
-        top = __reduce_max_sync(0xffffffffu, top);
+        for (int j = 0; j < mine; ++j) top = max(top, top_finite<T>(*reinterpret_cast<const uint4 *>(x + j * step)));
+        if (mine) atomicMax(&tops[1][hl], top);
+        __syncthreads();
     }
-    const int e = max(old, needed_exp(__uint_as_float(top)));
+    if (!active) return;
+    const int e = max(old, needed_exp(__uint_as_float(tops[odd][hl])));
     const float inv = exp2i(-e);
-    auto put = [&](int v, const uint4 &w) {
-        const int row = row_of(v);
-        put_codes<T>(code + (int64_t)row * row_bytes + (v - row * vpr) * V, w, inv, odd);
-    };
-    if (held) {
+    const int64_t cstep = (int64_t)row_bytes * rows_par;
 #pragma unroll
-        for (int j = 0; j < kHeld; ++j)
-            if (lane + 32 * j < nv) put(lane + 32 * j, val[j]);
-    } else {
-        for (int v = lane; v < nv; v += 32) put(v, *at(v));
-    }
+    for (int j = 0; j < kHeld; ++j)
+        if (j < mine) put_codes<T>(code + j * cstep, val[j], inv, odd);
+    for (int j = kHeld; j < mine; ++j) put_codes<T>(code + j * cstep, *reinterpret_cast<const uint4 *>(x + j * step), inv, odd);
     // ---- rows of the block before the new ones, where the scale grew
     if (before && e > old) {
         const float s = exp2i(max(old - e, -126));  // (2^-126 of any code rounds to zero too)
-        const int w8 = width / 8;
         uint8_t *first = code - (int64_t)before * row_bytes;
-        for (int v = lane; v < before * w8; v += 32) {
-            uint2 *p = reinterpret_cast<uint2 *>(first + (int64_t)(v / w8) * row_bytes + (v % w8) * 8);
-            const uint2 w = *p;
-            *p = make_uint2(shrink_codes(w.x, s), shrink_codes(w.y, s));
+        for (int r = row0; r < before; r += rows_par, first += cstep) {
+            if constexpr (V == 8) {
+                uint2 *p = reinterpret_cast<uint2 *>(first);
+                const uint2 w = *p;
+                *p = make_uint2(shrink_codes(w.x, s), shrink_codes(w.y, s));
+            } else {
+                uint32_t *p = reinterpret_cast<uint32_t *>(first);
+                *p = shrink_codes(*p, s);
+            }
         }
     }
-    if (lane == 0 && (before == 0 || e > old)) *eb = (uint8_t)(e + 127);
+    if (row0 == 0 && cv * V == hl * width && (before == 0 || e > old)) *eb = (uint8_t)(e + 127);
 }
 
 // ---------------------------------------------------------------------------
-// Reading.  A CTA takes 16 rows; a thread takes 8 columns (which lie in one head)
+// Reading.  A CTA takes 16 rows (or 4); a thread takes 8 columns (which lie in one head)
 // of all of them, so a warp reads 256 consecutive bytes of a row.
 // ---------------------------------------------------------------------------
-constexpr int kReadRows = 16, kReadThreads = 256;
+constexpr int kReadThreads = 256;
 
 // Eight codes times 2^e.
 __device__ __forceinline__ void widen8(const uint2 &w, float s, float (&x)[8]) {
@@ -258,9 +258,15 @@ __device__ __forceinline__ void store8(float *p, const float (&x)[8]) {
     reinterpret_cast<float4 *>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
 }
 
-// Rows src[i] of the cache (-1: none) to rows dst[i] of y.
-template <typename T>
-__device__ __forceinline__ void copy_rows(const ScaledPools &c, const int *src, const int *dst, void *const *y,
+// Of the rows of a CTA: row of the cache (-1: none), its block, row of the output;
+// whether all of them lie in one block.
+template <int ROWS>
+struct RowSet {
+    int src[ROWS], block[ROWS], dst[ROWS];
+};
+
+template <typename T, int ROWS>
+__device__ __forceinline__ void copy_rows(const ScaledPools &c, const RowSet<ROWS> &set, bool one_block, void *const *y,
                                           const int64_t *ld) {
     const int chunks = (c.G * c.d_h + c.H * c.r) / 4;  // of 8 columns, in a row of all pools
     for (int ch = threadIdx.x; ch < chunks; ch += kReadThreads) {
@@ -273,25 +279,26 @@ __device__ __forceinline__ void copy_rows(const ScaledPools &c, const int *src, 
         const uint8_t *code = c.code[k] + col, *exp = c.exp[k] + head;
         T *out = static_cast<T *>(y[k]) + col;
         const int64_t ldk = ld[k];
+        uint2 w[ROWS];
+        int e[ROWS];
 #pragma unroll
-        for (int i0 = 0; i0 < kReadRows; i0 += 8) {
-            uint2 w[8];
-            int e[8];
+        for (int i = 0; i < ROWS; ++i)
+            if (set.src[i] >= 0) w[i] = *reinterpret_cast<const uint2 *>(code + (int64_t)set.src[i] * row_bytes);
+        if (one_block) {
+            e[0] = exp[(int64_t)set.block[0] * heads];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int s = src[i0 + i];
-                if (s >= 0) {
-                    w[i] = *reinterpret_cast<const uint2 *>(code + (int64_t)s * row_bytes);
-                    e[i] = exp[(int64_t)(s / c.block) * heads];
-                }
-            }
+            for (int i = 1; i < ROWS; ++i) e[i] = e[0];
+        } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                if (src[i0 + i] < 0) continue;
-                float x[8];
-                widen8(w[i], exp2i(clamp_exp(e[i])), x);
-                store8(out + (int64_t)dst[i0 + i] * ldk, x);
-            }
+            for (int i = 0; i < ROWS; ++i)
+                if (set.src[i] >= 0) e[i] = exp[(int64_t)set.block[i] * heads];
+        }
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) {
+            if (set.src[i] < 0) continue;
+            float x[8];
+            widen8(w[i], exp2i(clamp_exp(e[i])), x);
+            store8(out + (int64_t)set.dst[i] * ldk, x);
         }
     }
 }
@@ -310,13 +317,13 @@ __device__ __forceinline__ int pool_row(const ScaledPools &c, const ScaledRows &
     return page * c.page_size + (int)(pos % c.page_size);
 }
 
-template <typename T>
+template <typename T, int ROWS>
 __global__ void __launch_bounds__(kReadThreads) read_scaled_kernel(const __grid_constant__ ScaledReadArgs a) {
-    __shared__ int src[kReadRows], dst[kReadRows];
+    __shared__ RowSet<ROWS> set;
     pdl_wait();
     pdl_launch_dependents();
-    if (threadIdx.x < kReadRows) {
-        const int i = blockIdx.x * kReadRows + threadIdx.x;
+    if (threadIdx.x < ROWS) {
+        const int i = blockIdx.x * ROWS + threadIdx.x;
         int s = -1;
         if (i < a.rows.n) {
             int lo = 0, hi = a.rows.B;  // first request whose rows end past i
@@ -328,58 +335,89 @@ __global__ void __launch_bounds__(kReadThreads) read_scaled_kernel(const __grid_
             if (lo < a.rows.B && a.rows.cu_rows[lo] <= i)
                 s = pool_row(a.c, a.rows, lo, (int64_t)a.rows.start_pos[lo] + (i - a.rows.cu_rows[lo]));
         }
-        src[threadIdx.x] = s;
-        dst[threadIdx.x] = i;
+        set.src[threadIdx.x] = s;
+        set.block[threadIdx.x] = s >= 0 ? s / a.c.block : -1;
+        set.dst[threadIdx.x] = i;
     }
     __syncthreads();
-    copy_rows<T>(a.c, src, dst, a.y, a.ld);
+    const int mine = threadIdx.x < ROWS ? set.block[threadIdx.x] : set.block[0];
+    const bool one = !__syncthreads_or(mine != set.block[0]) && mine >= 0;
+    copy_rows<T, ROWS>(a.c, set, one, a.y, a.ld);
 }
 
+template <int ROWS>
 __global__ void __launch_bounds__(kReadThreads) expand_scaled_kernel(const __grid_constant__ ScaledExpandArgs a,
                                                                      int tiles) {
-    __shared__ int src[kReadRows], dst[kReadRows];
+    __shared__ RowSet<ROWS> set;
     __shared__ int64_t ld[4];
     pdl_wait();
     pdl_launch_dependents();
-    const int b = blockIdx.x / tiles, p0 = (blockIdx.x % tiles) * kReadRows;
+    const int b = blockIdx.x / tiles, p0 = (blockIdx.x % tiles) * ROWS;
     const int r0 = a.rows.cu_rows[b], r1 = min(a.rows.cu_rows[b + 1], a.rows.n);
     const int64_t ctx = r0 >= 0 && r0 < r1 ? min((int64_t)a.max_ctx, (int64_t)a.rows.start_pos[b] + (r1 - r0)) : 0;
     const bool live = p0 < ctx;
     if (!live && !(a.table && p0 % 64 == 0)) return;
     if (threadIdx.x < 4) ld[threadIdx.x] = (int64_t)a.c.heads(threadIdx.x) * a.c.width(threadIdx.x);
-    if (threadIdx.x < kReadRows) {
+    if (threadIdx.x < ROWS) {
         const int p = p0 + threadIdx.x;
         const int s = p < ctx ? pool_row(a.c, a.rows, b, p) : -1;
-        src[threadIdx.x] = s;
-        dst[threadIdx.x] = a.table ? b * a.pages * 64 + p : s;
+        set.src[threadIdx.x] = s;
+        set.block[threadIdx.x] = s >= 0 ? s / a.c.block : -1;
+        set.dst[threadIdx.x] = a.table ? b * a.pages * 64 + p : s;
         // (a cache page holds whole pages of 64 rows: one is missing where its first row is)
         if (a.table && threadIdx.x == 0 && p0 % 64 == 0) a.table[(size_t)b * a.pages + p0 / 64] = s >= 0 ? b * a.pages + p0 / 64 : -1;
     }
     __syncthreads();
+    const int mine = threadIdx.x < ROWS ? set.block[threadIdx.x] : set.block[0];
+    const bool one = !__syncthreads_or(mine != set.block[0]) && mine >= 0;
     if (!live) return;
-    copy_rows<__nv_bfloat16>(a.c, src, dst, a.y, ld);
+    copy_rows<__nv_bfloat16, ROWS>(a.c, set, one, a.y, ld);
 }
 
 }  // namespace
 
 cudaError_t launch_write_scaled(const ScaledWriteArgs &a) {
     const int64_t units = a.rows.n / a.c.block + 2 * (int64_t)a.rows.B;
-    const int items = 2 * (a.c.G + a.c.H);
-    const dim3 grid((unsigned)std::min<int64_t>(units, INT32_MAX), (items + kWriteWarps - 1) / kWriteWarps);
-    return a.f32 ? launch_pdl(write_scaled_kernel<float>, grid, dim3(32 * kWriteWarps), 0, a.stream, a)
-                 : launch_pdl(write_scaled_kernel<__nv_bfloat16>, grid, dim3(32 * kWriteWarps), 0, a.stream, a);
+    const int V = a.f32 ? 4 : 8;
+    // columns of a slab: 64 vectors, fewer where a block is longer than the values that
+    // threads hold then (and one head at least)
+    const int vecs = std::max(1, std::min(kSlabVecs, kWriteThreads * kHeld / a.c.block));
+    Slabs slabs;
+    int total = 0;
+    for (int k = 0; k < 4; ++k) {
+        const int heads = a.c.heads(k), each = std::max(1, vecs / (a.c.width(k) / V));
+        const int parts = (heads + each - 1) / each;
+        slabs.heads[k] = (heads + parts - 1) / parts;
+        slabs.count[k] = (heads + slabs.heads[k] - 1) / slabs.heads[k];
+        total += slabs.count[k];
+    }
+    const dim3 grid((unsigned)units, total);
+    return a.f32 ? launch_pdl(write_scaled_kernel<float>, grid, dim3(kWriteThreads), 0, a.stream, a, slabs)
+                 : launch_pdl(write_scaled_kernel<__nv_bfloat16>, grid, dim3(kWriteThreads), 0, a.stream, a, slabs);
+}
+
+// Rows of a CTA: 16, or 4 where 16 would leave SMs idle.
+static bool few_rows(int64_t rows) { return rows < 32 * (int64_t)device_sm_count(); }
+
+template <typename T, int ROWS>
+static cudaError_t launch_read(const ScaledReadArgs &a) {
+    return launch_pdl(read_scaled_kernel<T, ROWS>, dim3((a.rows.n + ROWS - 1) / ROWS), dim3(kReadThreads), 0, a.stream, a);
 }
 
 cudaError_t launch_read_scaled(const ScaledReadArgs &a) {
-    const dim3 grid((a.rows.n + kReadRows - 1) / kReadRows);
-    return a.f32 ? launch_pdl(read_scaled_kernel<float>, grid, dim3(kReadThreads), 0, a.stream, a)
-                 : launch_pdl(read_scaled_kernel<__nv_bfloat16>, grid, dim3(kReadThreads), 0, a.stream, a);
+    if (few_rows(a.rows.n)) return a.f32 ? launch_read<float, 4>(a) : launch_read<__nv_bfloat16, 4>(a);
+    return a.f32 ? launch_read<float, 16>(a) : launch_read<__nv_bfloat16, 16>(a);
+}
+
+template <int ROWS>
+static cudaError_t launch_expand(const ScaledExpandArgs &a) {
+    const int tiles = (a.max_ctx + ROWS - 1) / ROWS;
+    return launch_pdl(expand_scaled_kernel<ROWS>, dim3((unsigned)(a.rows.B * (int64_t)tiles)), dim3(kReadThreads), 0,
+                      a.stream, a, tiles);
 }
 
 cudaError_t launch_expand_scaled(const ScaledExpandArgs &a) {
-    const int tiles = (a.max_ctx + kReadRows - 1) / kReadRows;
-    return launch_pdl(expand_scaled_kernel, dim3((unsigned)(a.rows.B * (int64_t)tiles)), dim3(kReadThreads), 0, a.stream, a,
-                      tiles);
+    return few_rows((int64_t)a.rows.B * a.max_ctx) ? launch_expand<4>(a) : launch_expand<16>(a);
 }
 
 }  // namespace lrkv
