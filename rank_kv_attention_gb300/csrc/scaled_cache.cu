@@ -24,33 +24,46 @@ namespace {
 //
 // A CTA takes a slab of neighbouring heads of one pool of a unit.  A thread stays with
 // one 16-byte column of it and takes every rows_par-th row, so rows are read and codes
-// written whole; it holds its values in registers (16 vectors: 64 rows of a slab of
-// 1 KB), the heads' maxima meet in shared memory, and the codes go out.  Longer blocks
+// written whole; it holds its values in registers (8 vectors: 64 rows of a slab of
+// 256 bytes), the heads' maxima meet in shared memory, and the codes go out.  Longer blocks
 // are read twice, the second time out of L2.  (One warp per head, with rows of 96
 // bytes, took 41 us for 16,384 bf16 rows, 13 at the copy bandwidth.)
 // ---------------------------------------------------------------------------
-constexpr int kWriteThreads = 256, kHeld = 16, kSlabVecs = 64;
+constexpr int kWriteThreads = 128, kHeld = 8, kSlabVecs = 64;
 
 // Slabs of a pool: heads of one, and how many.
 struct Slabs {
     int heads[4], count[4];
 };
 
-// The last b in [0, B) with cu[b] / block + 2 b <= u, or -1 (whole warp).
-__device__ __forceinline__ int request_of_unit(const int32_t *cu, int B, int block, int64_t u, int lane) {
+// The request of a unit, its rows [r0, r1) and its first position; b = -1: none.
+struct UnitOwner {
+    int b, r0, r1, start;
+};
+
+// The last b in [0, B) with cu[b] / block + 2 b <= u (whole warp).  The last probes are of
+// neighbouring requests, so that their rows come with them.
+__device__ __forceinline__ UnitOwner owner_of_unit(const int32_t *cu, const int32_t *start, int B, int block, int u,
+                                                   int lane) {
     int lo = 0, hi = B;
-    bool any = false;
-    do {
+    for (;;) {
         const int step = (hi - lo + 31) / 32, i = lo + lane * step;
-        const bool le = i < hi && (int64_t)(cu[i] / block) + 2 * (int64_t)i <= u;
-        const uint32_t no = ~__ballot_sync(0xffffffffu, le);
+        const bool in = i < hi;
+        const int c0 = in ? cu[i] : 0;
+        int c1 = 0, s = 0;
+        if (in && step == 1) {
+            c1 = cu[i + 1];
+            s = start[i];
+        }
+        const uint32_t no = ~__ballot_sync(0xffffffffu, in && (int64_t)(c0 / block) + 2 * (int64_t)i <= u);
         const int k = no ? __ffs(no) - 1 : 32;  // probes that hold
-        if (k == 0) return any ? lo : -1;
-        any = true;
+        if (k == 0) return {-1, 0, 0, 0};       // (only in the first round)
+        if (step == 1)
+            return {lo + k - 1, __shfl_sync(0xffffffffu, c0, k - 1), __shfl_sync(0xffffffffu, c1, k - 1),
+                    __shfl_sync(0xffffffffu, s, k - 1)};
         lo += (k - 1) * step;
         hi = min(hi, lo + step);
-    } while (hi - lo > 1);
-    return lo;
+    }
 }
 
 template <typename T> struct Bits;
@@ -127,47 +140,44 @@ __device__ __forceinline__ uint32_t shrink_codes(uint32_t w, float s) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kWriteThreads) write_scaled_kernel(const __grid_constant__ ScaledWriteArgs a,
-                                                                     const __grid_constant__ Slabs slabs) {
+__global__ void __launch_bounds__(kWriteThreads, 7) write_scaled_kernel(const __grid_constant__ ScaledWriteArgs a,
+                                                                        const __grid_constant__ Slabs slabs) {
     constexpr int V = Bits<T>::V;
     __shared__ uint32_t tops[2][kWriteThreads];
     const ScaledPools &c = a.c;
-    const int tid = threadIdx.x, lane = tid & 31;
-    const int64_t u = blockIdx.x;
+    const int tid = threadIdx.x, lane = tid & 31, u = blockIdx.x;
     tops[0][tid] = tops[1][tid] = 0;
     __syncthreads();
-    pdl_wait();
-    pdl_launch_dependents();
     const bool speaks = blockIdx.y == 0 && tid == 0;  // flags a unit's faults
     // pool, heads h0 .. h0 + nh - 1
     int k = 0, slab = blockIdx.y;
     while (slab >= slabs.count[k]) slab -= slabs.count[k++];
     const int heads = c.heads(k), width = c.width(k), h0 = slab * slabs.heads[k], nh = min(slabs.heads[k], heads - h0);
+    pdl_wait();
+    pdl_launch_dependents();
 
     // ---- the unit's rows i0 .. i1 - 1, from position p0 on
-    const int b = request_of_unit(a.rows.cu_rows, a.rows.B, c.block, u, lane);
-    if (b < 0) return;
-    const int r0 = a.rows.cu_rows[b], r1 = min(a.rows.cu_rows[b + 1], a.rows.n);
-    const int start = a.rows.start_pos[b];
-    if (r0 < 0 || r0 >= r1) return;
+    const UnitOwner own = owner_of_unit(a.rows.cu_rows, a.rows.start_pos, a.rows.B, c.block, u, lane);
+    const int b = own.b, r0 = own.r0, r1 = min(own.r1, a.rows.n), start = own.start;
+    if (b < 0 || r0 < 0 || r0 >= r1) return;
     const int64_t max_len = (int64_t)a.rows.max_pages * c.page_size;
-    const int64_t ra = r0 + max((int64_t)0, -(int64_t)start);           // first row at a position >= 0
-    const int64_t rz = min((int64_t)r1, r0 + max_len - (int64_t)start);  // rows past the table start here
-    const int64_t key = u - (r0 / c.block + 2 * (int64_t)b);
-    if (key == 0 && speaks && (ra > r0 || rz < r1)) status_or(a.rows.status, LRKV_STATUS_BAD_ROW);
-    if (ra >= rz) return;
-    const int64_t pa = (int64_t)start + (ra - r0);  // its position
-    const int64_t i2 = ra + c.block - pa % c.block;  // first row of the second unit
-    int64_t i0 = ra, i1 = i2;
+    const int64_t ra64 = r0 + max((int64_t)0, -(int64_t)start);            // first row at a position >= 0
+    const int64_t rz64 = min((int64_t)r1, r0 + max_len - (int64_t)start);  // rows past the table start here
+    const int key = u - (r0 / c.block + 2 * b);
+    if (key == 0 && speaks && (ra64 > r0 || rz64 < r1)) status_or(a.rows.status, LRKV_STATUS_BAD_ROW);
+    if (ra64 >= rz64) return;
+    const int ra = (int)ra64, rz = (int)rz64, pa = start + (ra - r0);  // (all below 2^30 from here on)
+    const int i2 = ra + c.block - pa % c.block;                       // first row of the second unit
+    int i0 = ra, i1 = i2;
     if (key > 0) {
-        const int64_t m = u - 2 * (int64_t)b - 1 - i2 / c.block;
+        const int m = u - 2 * b - 1 - i2 / c.block;
         if (m < 0) return;
         i0 = i2 + m * c.block;
         i1 = i0 + c.block;
     }
     i1 = min(i1, rz);
     if (i0 >= i1) return;
-    const int p0 = (int)(pa + (i0 - ra)), rows = (int)(i1 - i0);
+    const int p0 = pa + (i0 - ra), rows = i1 - i0;
 
     // ---- this thread's column and rows
     const int vpr = nh * width / V, rows_par = kWriteThreads / vpr;
@@ -175,7 +185,7 @@ __global__ void __launch_bounds__(kWriteThreads) write_scaled_kernel(const __gri
     const bool active = row0 < rows_par;
     const int mine = active && row0 < rows ? (rows - row0 + rows_par - 1) / rows_par : 0;
     const int64_t ld = a.ld[k], step = ld * rows_par;
-    const T *x = static_cast<const T *>(a.x[k]) + (i0 + row0) * ld + h0 * width + cv * V;
+    const T *x = static_cast<const T *>(a.x[k]) + (int64_t)(i0 + row0) * ld + h0 * width + cv * V;
     uint4 val[kHeld];
 #pragma unroll
     for (int j = 0; j < kHeld; ++j)
