@@ -673,51 +673,88 @@ def _scaled_arg(cache, dev):
     """(lrkv_scaled_t as bytes, H, d_h, r, groups) with all tensors' shapes and devices checked."""
     S_K, S_V, R_K, R_V = cache.S_K, cache.S_V, cache.R_K, cache.R_V
     E_S_K, E_S_V, E_R_K, E_R_V = cache.E_S_K, cache.E_S_V, cache.E_R_K, cache.E_R_V
-    if not (isinstance(S_K, _Tensor) and isinstance(R_K, _Tensor) and isinstance(E_R_K, _Tensor)) \
-            or S_K.dim() not in (3, 4) or R_K.dim() != 4 or E_R_K.dim() != 3:
-        raise ValueError("S_K must be [num_pages, page_size, (G,) d_h], R_K [num_pages, page_size, H, r] and E_R_K "
-                         "[num_pages, page_size / block, H]")
-    ss, rs = S_K.shape, R_K.shape
-    n, ps, H, r = rs
-    d_h, G, nb = ss[-1], ss[2] if len(ss) == 4 else 1, E_R_K.shape[1]
-    es, er = (n, nb, G), (n, nb, H)
-    if ss[0] != n or ss[1] != ps:
-        raise ValueError(f"S_K {list(ss)} and R_K {list(rs)} must have the same pages")
-    if nb < 1 or ps % nb:
-        raise ValueError(f"E_R_K {list(E_R_K.shape)} does not divide pages of {ps} tokens into blocks")
-    if not (isinstance(S_V, _Tensor) and isinstance(R_V, _Tensor) and isinstance(E_S_K, _Tensor)
-            and isinstance(E_S_V, _Tensor) and isinstance(E_R_V, _Tensor) and S_K.dtype is _f8 and S_V.dtype is _f8
-            and R_K.dtype is _f8 and R_V.dtype is _f8 and E_S_K.dtype is _u8 and E_S_V.dtype is _u8
-            and E_R_K.dtype is _u8 and E_R_V.dtype is _u8 and S_V.shape == ss and R_V.shape == rs
-            and E_S_K.shape == es and E_S_V.shape == es and E_R_K.shape == er and E_R_V.shape == er
-            and S_K.get_device() == dev and S_V.get_device() == dev and R_K.get_device() == dev
-            and R_V.get_device() == dev and E_S_K.get_device() == dev and E_S_V.get_device() == dev
-            and E_R_K.get_device() == dev and E_R_V.get_device() == dev and S_K.is_contiguous()
-            and S_V.is_contiguous() and R_K.is_contiguous() and R_V.is_contiguous() and E_S_K.is_contiguous()
-            and E_S_V.is_contiguous() and E_R_K.is_contiguous() and E_R_V.is_contiguous()):
-        _refuse(((S_K, "S_K", _f8, ss), (S_V, "S_V", _f8, ss), (R_K, "R_K", _f8, rs), (R_V, "R_V", _f8, rs),
-                 (E_S_K, "E_S_K", _u8, es), (E_S_V, "E_S_V", _u8, es), (E_R_K, "E_R_K", _u8, er),
-                 (E_R_V, "E_R_V", _u8, er)), dev)
+    try:
+        ss, rs, er = S_K.shape, R_K.shape, E_R_K.shape
+        n, ps, H, r = rs
+        _, nb, _ = er
+        d_h, G = ss[-1], ss[2] if len(ss) == 4 else 1
+        es = E_S_K.shape
+        good = (len(ss) in (3, 4) and ss[0] == n and ss[1] == ps and nb > 0 and ps % nb == 0 and er[0] == n
+                and er[2] == H and es[0] == n and es[1] == nb and es[2] == G and S_V.shape == ss and R_V.shape == rs
+                and E_S_V.shape == es and E_R_V.shape == er and len(es) == 3
+                and S_K.dtype is _f8 and S_V.dtype is _f8 and R_K.dtype is _f8 and R_V.dtype is _f8
+                and E_S_K.dtype is _u8 and E_S_V.dtype is _u8 and E_R_K.dtype is _u8 and E_R_V.dtype is _u8
+                and S_K.get_device() == dev and S_V.get_device() == dev and R_K.get_device() == dev
+                and R_V.get_device() == dev and E_S_K.get_device() == dev and E_S_V.get_device() == dev
+                and E_R_K.get_device() == dev and E_R_V.get_device() == dev and S_K.is_contiguous()
+                and S_V.is_contiguous() and R_K.is_contiguous() and R_V.is_contiguous() and E_S_K.is_contiguous()
+                and E_S_V.is_contiguous() and E_R_K.is_contiguous() and E_R_V.is_contiguous())
+    except (AttributeError, IndexError, TypeError, ValueError):  # (no tensors, or of other dimensions)
+        good = False
+    if not good:
+        _refuse_scaled(cache, dev)
     return _abi.pack_scaled(S_K.data_ptr(), S_V.data_ptr(), R_K.data_ptr(), R_V.data_ptr(), E_S_K.data_ptr(),
                             E_S_V.data_ptr(), E_R_K.data_ptr(), E_R_V.data_ptr(), n, ps, H, d_h, r, G, ps // nb,
                             0), H, d_h, r, G
 
 
+def _refuse_scaled(cache, dev):
+    """Say what is wrong with a ScaledCache."""
+    S_K, R_K, E_R_K = cache.S_K, cache.R_K, cache.E_R_K
+    if not (isinstance(S_K, _Tensor) and isinstance(R_K, _Tensor) and isinstance(E_R_K, _Tensor)) \
+            or S_K.dim() not in (3, 4) or R_K.dim() != 4 or E_R_K.dim() != 3:
+        raise ValueError("S_K must be [num_pages, page_size, (G,) d_h], R_K [num_pages, page_size, H, r] and E_R_K "
+                         "[num_pages, page_size / block, H]")
+    ss, rs, nb = S_K.shape, R_K.shape, E_R_K.shape[1]
+    n, ps, H, _ = rs
+    if ss[0] != n or ss[1] != ps:
+        raise ValueError(f"S_K {list(ss)} and R_K {list(rs)} must have the same pages")
+    if nb < 1 or ps % nb:
+        raise ValueError(f"E_R_K {list(E_R_K.shape)} does not divide pages of {ps} tokens into blocks")
+    es, er = (n, nb, ss[2] if len(ss) == 4 else 1), (n, nb, H)
+    _refuse(((S_K, "S_K", _f8, ss), (cache.S_V, "S_V", _f8, ss), (R_K, "R_K", _f8, rs), (cache.R_V, "R_V", _f8, rs),
+             (cache.E_S_K, "E_S_K", _u8, es), (cache.E_S_V, "E_S_V", _u8, es), (E_R_K, "E_R_K", _u8, er),
+             (cache.E_R_V, "E_R_V", _u8, er)), dev)
+    raise ValueError("the cache's tensors do not fit together")
+
+
 def _row_args(cu_rows, start_pos, page_table, dev):
     """(B, max_pages) of the requests' rows of a call."""
-    (B,), max_pages = _dim(start_pos, "start_pos", 1), _dim(page_table, "page_table", 2)[1]
-    if not (isinstance(cu_rows, _Tensor) and cu_rows.dtype is _i32 and start_pos.dtype is _i32
-            and page_table.dtype is _i32 and cu_rows.shape == (B + 1,) and page_table.shape[0] == B
-            and cu_rows.get_device() == dev and start_pos.get_device() == dev and page_table.get_device() == dev
-            and cu_rows.is_contiguous() and start_pos.is_contiguous() and page_table.is_contiguous()):
+    try:
+        (B,), (rows, max_pages) = start_pos.shape, page_table.shape
+        good = (cu_rows.dtype is _i32 and start_pos.dtype is _i32 and page_table.dtype is _i32 and rows == B
+                and cu_rows.shape == (B + 1,) and cu_rows.get_device() == dev and start_pos.get_device() == dev
+                and page_table.get_device() == dev and cu_rows.is_contiguous() and start_pos.is_contiguous()
+                and page_table.is_contiguous())
+    except (AttributeError, TypeError, ValueError):
+        good = False
+    if not good:
+        (B,), max_pages = _dim(start_pos, "start_pos", 1), _dim(page_table, "page_table", 2)[1]
         _refuse(((cu_rows, "cu_rows", _i32, (B + 1,)), (start_pos, "start_pos", _i32, (B,)),
                  (page_table, "page_table", _i32, (B, max_pages))), dev)
+        raise ValueError("cu_rows, start_pos and page_table do not fit together")
     return B, max_pages
 
 
 def _strided_rows(rows, n, H, d_h, r, G, dev):
-    """[address, row stride] of the four pools' rows one after the other, and their dtype.  A row is dense; rows may
+    """Address and row stride of the four pools' rows one after the other, and their dtype.  A row is dense; rows may
     lie apart (slices of one projection's output)."""
+    a, b, c, e = rows
+    try:
+        dt, sa, sb, sc, se = a.dtype, a.stride(), b.stride(), c.stride(), e.stride()
+        shared, private = G * d_h, H * r
+        # rows of a matrix, or of heads that lie next to each other
+        flat = lambda t, st, heads, width: (  # noqa: E731
+            t.shape == (n, heads * width) and st[1] == 1 or
+            t.shape == (n, heads, width) and st[2] == 1 and (st[1] == width or heads == 1))
+        good = (n > 1 and (dt is _bf16 or dt is _f32) and b.dtype is dt and c.dtype is dt and e.dtype is dt
+                and a.get_device() == dev and b.get_device() == dev and c.get_device() == dev
+                and e.get_device() == dev and flat(a, sa, G, d_h) and flat(b, sb, G, d_h) and flat(c, sc, H, r)
+                and flat(e, se, H, r))
+    except (AttributeError, IndexError, TypeError):
+        good = False
+    if good:
+        return (a.data_ptr(), sa[0], b.data_ptr(), sb[0], c.data_ptr(), sc[0], e.data_ptr(), se[0]), dt
     out, dt = [], None
     for name, t in zip(_POOLS, rows):
         if not isinstance(t, _Tensor):
@@ -751,7 +788,8 @@ def write_scaled(S_K, S_V, R_K, R_V, cu_rows, start_pos, cache: ScaledCache, pag
     n = S_K.shape[0] if S_K.dim() else 0
     rows, dt = _strided_rows((S_K, S_V, R_K, R_V), n, H, d_h, r, G, dev)
     code = _abi.lib().lrkv_write_scaled(*rows, _DT[dt], cu_rows.data_ptr(), start_pos.data_ptr(), B, n, desc,
-                                        page_table.data_ptr(), max_pages, _status(status, dev),
+                                        page_table.data_ptr(), max_pages,
+                                        None if status is None else _status(status, dev),
                                         _raw_stream(stream, dev))
     if code:
         _abi.check("lrkv_write_scaled", code)
@@ -772,35 +810,46 @@ def read_scaled(cu_rows, start_pos, n, cache: ScaledCache, page_table, dtype=tor
         shared = (n, d_h) if cache.S_K.dim() == 3 else (n, G, d_h)
         if dtype is not _bf16 and dtype is not _f32:
             raise TypeError(f"dtype must be torch.bfloat16 or torch.float32, got {dtype}")
-        out = ScaledRows(*[_own_buffer(s, dtype, cu_rows.device, stream) for s in (shared, shared, (n, H, r), (n, H, r))])
-    rows, dt = _strided_rows(out, n, H, d_h, r, G, dev)
+        at, private = cu_rows.device, (n, H, r)
+        a, b, c, e = out = ScaledRows(*[_own_buffer(s, dtype, at, stream) for s in (shared, shared, private, private)])
+        rows, dt = (a.data_ptr(), G * d_h, b.data_ptr(), G * d_h, c.data_ptr(), H * r, e.data_ptr(), H * r), dtype
+    else:
+        rows, dt = _strided_rows(out, n, H, d_h, r, G, dev)
+        out = ScaledRows(*out)
     code = _abi.lib().lrkv_read_scaled(desc, cu_rows.data_ptr(), start_pos.data_ptr(), B, n, page_table.data_ptr(),
-                                       max_pages, _DT[dt], *rows, _status(status, dev), _raw_stream(stream, dev))
+                                       max_pages, _DT[dt], *rows, None if status is None else _status(status, dev),
+                                       _raw_stream(stream, dev))
     if code:
         _abi.check("lrkv_read_scaled", code)
-    return ScaledRows(*out)
+    return out
 
 
 def _projection_args(X, W_S_K, W_S_V, U_K, U_V, H, d_h, r, G, dev):
     """(n, d) with the projection's tensors checked."""
-    n, d = _dim(X, "X", 2)
-    shared, private = (G * d_h, d), (H, r, d)
-    if not (isinstance(W_S_K, _Tensor) and isinstance(W_S_V, _Tensor) and isinstance(U_K, _Tensor)
-            and isinstance(U_V, _Tensor) and X.dtype is _bf16 and W_S_K.dtype is _bf16 and W_S_V.dtype is _bf16
-            and U_K.dtype is _bf16 and U_V.dtype is _bf16 and W_S_K.shape == shared and W_S_V.shape == shared
-            and U_K.shape == private and U_V.shape == private and X.get_device() == dev
-            and W_S_K.get_device() == dev and W_S_V.get_device() == dev and U_K.get_device() == dev
-            and U_V.get_device() == dev and X.is_contiguous() and W_S_K.is_contiguous() and W_S_V.is_contiguous()
-            and U_K.is_contiguous() and U_V.is_contiguous()):
+    try:
+        n, d = X.shape
+        shared, private = (G * d_h, d), (H, r, d)
+        good = (X.dtype is _bf16 and W_S_K.dtype is _bf16 and W_S_V.dtype is _bf16
+                and U_K.dtype is _bf16 and U_V.dtype is _bf16 and W_S_K.shape == shared and W_S_V.shape == shared
+                and U_K.shape == private and U_V.shape == private and X.get_device() == dev
+                and W_S_K.get_device() == dev and W_S_V.get_device() == dev and U_K.get_device() == dev
+                and U_V.get_device() == dev and X.is_contiguous() and W_S_K.is_contiguous() and W_S_V.is_contiguous()
+                and U_K.is_contiguous() and U_V.is_contiguous())
+    except (AttributeError, TypeError, ValueError):
+        good = False
+    if not good:
+        n, d = _dim(X, "X", 2)
+        shared, private = (G * d_h, d), (H, r, d)
         _refuse(((X, "X", _bf16, (n, d)), (W_S_K, "W_S_K", _bf16, shared), (W_S_V, "W_S_V", _bf16, shared),
                  (U_K, "U_K", _bf16, private), (U_V, "U_V", _bf16, private)), dev)
+        raise ValueError("X and the weights do not fit together")
     return n, d
 
 
 def _own_workspace(ws, need, dev, device, stream):
     """(address, bytes) of the caller's workspace, or of one made for the call; the tensor, to keep it until then."""
     if ws is None:
-        ws = torch.empty(max(need, 1), dtype=_u8, device=device) if stream is None else _scratch(need, device, stream)
+        ws = torch.empty(need or 1, dtype=_u8, device=device) if stream is None else _scratch(need, device, stream)
         return ws.data_ptr(), need, ws
     return *_workspace(ws, dev), ws
 
@@ -822,7 +871,7 @@ def append_scaled(X, cu_rows, start_pos, W_S_K, W_S_V, U_K, U_V, cache: ScaledCa
     addr, size, ws = _own_workspace(ws, need, dev, X.device, stream)
     code = L.lrkv_append_scaled(X.data_ptr(), cu_rows.data_ptr(), start_pos.data_ptr(), B, n, d, W_S_K.data_ptr(),
                                 W_S_V.data_ptr(), U_K.data_ptr(), U_V.data_ptr(), desc, page_table.data_ptr(),
-                                max_pages, addr, size, _status(status, dev), _raw_stream(stream, dev))
+                                max_pages, addr, size, None if status is None else _status(status, dev), _raw_stream(stream, dev))
     if code:
         _abi.check("lrkv_append_scaled", code)
 
@@ -843,14 +892,17 @@ def decode_scaled(q, cache: ScaledCache, B_K, B_V, seq_lens, page_table, max_seq
     if out is None:
         out = torch.empty_like(q) if stream is None else _own_buffer(q.shape, q.dtype, q.device, stream)
     shape, base = (B, H, d_h), (H, d_h, r)
-    if not (isinstance(B_K, _Tensor) and isinstance(B_V, _Tensor) and isinstance(seq_lens, _Tensor)
-            and isinstance(out, _Tensor) and q.dtype is _bf16 and B_K.dtype is _bf16 and B_V.dtype is _bf16
-            and out.dtype is _bf16 and seq_lens.dtype is _i32 and page_table.dtype is _i32 and q.shape == shape
-            and out.shape == shape and B_K.shape == base and B_V.shape == base and seq_lens.shape == (B,)
-            and page_table.shape[0] == B and q.get_device() == dev and B_K.get_device() == dev
-            and B_V.get_device() == dev and seq_lens.get_device() == dev and page_table.get_device() == dev
-            and out.get_device() == dev and q.is_contiguous() and B_K.is_contiguous() and B_V.is_contiguous()
-            and seq_lens.is_contiguous() and page_table.is_contiguous() and out.is_contiguous()):
+    try:
+        good = (q.dtype is _bf16 and B_K.dtype is _bf16 and B_V.dtype is _bf16
+                and out.dtype is _bf16 and seq_lens.dtype is _i32 and page_table.dtype is _i32 and q.shape == shape
+                and out.shape == shape and B_K.shape == base and B_V.shape == base and seq_lens.shape == (B,)
+                and page_table.shape[0] == B and q.get_device() == dev and B_K.get_device() == dev
+                and B_V.get_device() == dev and seq_lens.get_device() == dev and page_table.get_device() == dev
+                and out.get_device() == dev and q.is_contiguous() and B_K.is_contiguous() and B_V.is_contiguous()
+                and seq_lens.is_contiguous() and page_table.is_contiguous() and out.is_contiguous())
+    except AttributeError:
+        good = False
+    if not good:
         _refuse(((q, "q", _bf16, shape), (B_K, "B_K", _bf16, base), (B_V, "B_V", _bf16, base),
                  (seq_lens, "seq_lens", _i32, (B,)), (page_table, "page_table", _i32, (B, max_pages)),
                  (out, "out", _bf16, shape)), dev)
@@ -861,7 +913,7 @@ def decode_scaled(q, cache: ScaledCache, B_K, B_V, seq_lens, page_table, max_seq
     addr, size, ws = _own_workspace(ws, need, dev, q.device, stream)
     code = L.lrkv_decode_scaled(q.data_ptr(), desc, B_K.data_ptr(), B_V.data_ptr(), seq_lens.data_ptr(),
                                 page_table.data_ptr(), B, max_pages, max_seq_len, out.data_ptr(), addr, size,
-                                _status(status, dev), _raw_stream(stream, dev))
+                                None if status is None else _status(status, dev), _raw_stream(stream, dev))
     if code:
         _abi.check("lrkv_decode_scaled", code)
     return out

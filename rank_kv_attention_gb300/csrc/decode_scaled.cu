@@ -982,10 +982,15 @@ bool scaled_tc_covers(const ScaledPools &c) {
     return fits(c, s);
 }
 
-size_t scaled_tc_ws_bytes(const ScaledPools &c, int B) {
+// CTAs of a call: one per SM; fewer where the requests cannot have as many units.
+static int ctas_of(int B, int max_seq_len) {
+    return (int)std::max<int64_t>(1, std::min<int64_t>(device_sm_count(), (int64_t)B * ((max_seq_len + kUnit - 1) / kUnit)));
+}
+
+size_t scaled_tc_ws_bytes(const ScaledPools &c, int B, int max_seq_len) {
     Shape s;
     if (!fits(c, s)) return 0;
-    return layout(nullptr, s, B, device_sm_count(), c.d_h).bytes;
+    return layout(nullptr, s, B, ctas_of(B, max_seq_len), c.d_h).bytes;
 }
 
 cudaError_t launch_decode_scaled_tc(const ScaledDecodeArgs &d, void *ws) {
@@ -1000,16 +1005,13 @@ cudaError_t launch_decode_scaled_tc(const ScaledDecodeArgs &d, void *ws) {
         !map_codes(&maps.k[1], c.code[2], rows, c.H * c.r, a.box_rows) ||
         !map_codes(&maps.v[1], c.code[3], rows, c.H * c.r, a.box_rows))
         return cudaErrorInvalidValue;
-    // (one CTA per SM; fewer where the requests cannot have as many units)
-    const int sm = device_sm_count();
-    const int64_t most = (int64_t)d.B * ((d.max_seq_len + kUnit - 1) / kUnit);
-    const int ctas = (int)std::max<int64_t>(1, std::min<int64_t>(sm, most));
+    const int ctas = ctas_of(d.B, d.max_seq_len);
     const auto kernel = c.H <= 16 ? decode_scaled_kernel<16> : decode_scaled_kernel<32>;
     // (taking registers that the launch does not have would wait forever)
     static const bool enough = launch_registers(decode_scaled_kernel<16>) == kRegs &&
                                launch_registers(decode_scaled_kernel<32>) == kRegs;
     if (!enough) return cudaErrorLaunchOutOfResources;
-    const Ws w = layout(ws, s, d.B, sm, c.d_h);
+    const Ws w = layout(ws, s, d.B, ctas, c.d_h);
     const int max_len = d.max_pages * c.page_size;
     PrepArgs p;
     p.q = static_cast<const __nv_bfloat16 *>(d.q);
@@ -1028,7 +1030,7 @@ cudaError_t launch_decode_scaled_tc(const ScaledDecodeArgs &d, void *ws) {
     a.page_table = d.page_table;
     a.img = w.img;
     a.img_stride = w.img_stride;
-    a.st = scaled_states(w.states, (int64_t)d.B + sm, c.H);
+    a.st = scaled_states(w.states, (int64_t)d.B + ctas, c.H);
     a.status = d.status;
     a.B = d.B;
     a.max_pages = d.max_pages;

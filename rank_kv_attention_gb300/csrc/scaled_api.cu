@@ -143,7 +143,7 @@ int run_decode_scaled(const ScaledDecodeArgs &a, void *ws) {
 }
 
 size_t decode_scaled_ws_bytes(const ScaledPools &c, int B, int max_seq_len) {
-    return scaled_tc_covers(c) ? scaled_tc_ws_bytes(c, B) : scaled_any_ws_bytes(c, B, max_seq_len);
+    return scaled_tc_covers(c) ? scaled_tc_ws_bytes(c, B, max_seq_len) : scaled_any_ws_bytes(c, B, max_seq_len);
 }
 
 // Prefill workspace: the projected rows; then, tiled, the bf16 pools of the values with

@@ -98,7 +98,7 @@ cudaError_t launch_decode_scaled_any(const ScaledDecodeArgs &a, void *ws);
 // On tensor cores: covered shapes (d_h = 128, one shared basis, H a multiple of 4 up
 // to 32, r up to 64, operands that fit), workspace bytes and launcher (req_row NULL).
 bool scaled_tc_covers(const ScaledPools &c);
-size_t scaled_tc_ws_bytes(const ScaledPools &c, int B);
+size_t scaled_tc_ws_bytes(const ScaledPools &c, int B, int max_seq_len);
 cudaError_t launch_decode_scaled_tc(const ScaledDecodeArgs &a, void *ws);
 
 // Merges the states of request b, slots first(b) .. first(b) + count(b) - 1, into out.
