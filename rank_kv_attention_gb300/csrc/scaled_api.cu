@@ -101,7 +101,15 @@ int check_projection(const void *X, int n, int d, const void *W_S_K, const void 
 
 cudaError_t run_append_scaled(const void *X, const ScaledRows &rows, int d, const void *W_S_K, const void *W_S_V,
                               const void *U_K, const void *U_V, const ScaledPools &c, const StagedRows &st,
-                              cudaStream_t s) {
+                              cudaStream_t s, void *const *y = nullptr, int ypages = 0) {
+    if (append_scaled_tc_fits(c, rows.n, rows.B, d)) {
+        ScaledAppendArgs p = {c, rows, X, W_S_K, W_S_V, U_K, U_V, d, {nullptr, nullptr, nullptr, nullptr}, ypages, s};
+        for (int k = 0; y && k < 4; ++k) p.y[k] = y[k];
+        prof_before(LRKV_PROFILE_PROJECTION, s);
+        const cudaError_t e = launch_append_scaled_tc(p);
+        prof_after(LRKV_PROFILE_PROJECTION, s);
+        return e;
+    }
     AppendArgsT<__nv_bfloat16> a = {};
     a.X = static_cast<const __nv_bfloat16 *>(X);
     a.n = rows.n;
@@ -358,16 +366,17 @@ int lrkv_prefill_scaled(const void *X, const void *Q, const int32_t *cu_rows, co
         p.stream = s;
         if (!prefill_tc_fits(p)) return LRKV_E_SHAPE;  // (more than 65535 heads, requests or query tiles)
     }
-    cudaError_t e = run_append_scaled(X, rows, d, W_S_K, W_S_V, U_K, U_V, c, w.rows, s);
+    // (the append in one kernel lays its own rows' values out)
+    void *const y[4] = {w.cache.S_K, w.cache.S_V, w.cache.R_K, w.cache.R_V};
+    cudaError_t e = run_append_scaled(X, rows, d, W_S_K, W_S_V, U_K, U_V, c, w.rows, s, w.tiled ? y : nullptr,
+                                      w.own_pages ? w.pages : 0);
     if (e != cudaSuccess) return cuda_fail(e);
     if (w.tiled) {
         ScaledExpandArgs x;
         x.c = c;
         x.rows = rows;
-        x.y[0] = w.cache.S_K;
-        x.y[1] = w.cache.S_V;
-        x.y[2] = w.cache.R_K;
-        x.y[3] = w.cache.R_V;
+        for (int k = 0; k < 4; ++k) x.y[k] = y[k];
+        x.history = append_scaled_tc_fits(c, n, B, d);
         x.table = w.table;
         x.pages = w.pages;
         x.max_ctx = max_ctx;

@@ -127,18 +127,6 @@ __device__ __forceinline__ void put_codes(uint8_t *dst, const uint4 &v, float in
     else *reinterpret_cast<uint32_t *>(dst) = w[0];
 }
 
-// Four codes times s, rounded to codes again.
-__device__ __forceinline__ uint32_t shrink_codes(uint32_t w, float s) {
-    uint32_t r = 0;
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        const uint32_t h2 = f16x2_from_e4m3x2((uint16_t)(w >> (16 * k)));
-        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h2));
-        r |= (uint32_t)e4m3x2_from_f32(f.x * s, f.y * s) << (16 * k);
-    }
-    return r;
-}
-
 template <typename T>
 __global__ void __launch_bounds__(kWriteThreads, 7) write_scaled_kernel(const __grid_constant__ ScaledWriteArgs a,
                                                                         const __grid_constant__ Slabs slabs) {
@@ -364,15 +352,16 @@ __global__ void __launch_bounds__(kReadThreads) expand_scaled_kernel(const __gri
     pdl_launch_dependents();
     const int b = blockIdx.x / tiles, p0 = (blockIdx.x % tiles) * ROWS;
     const int r0 = a.rows.cu_rows[b], r1 = min(a.rows.cu_rows[b + 1], a.rows.n);
-    const int64_t ctx = r0 >= 0 && r0 < r1 ? min((int64_t)a.max_ctx, (int64_t)a.rows.start_pos[b] + (r1 - r0)) : 0;
-    const bool live = p0 < ctx;
-    if (!live && !(a.table && p0 % 64 == 0)) return;
+    const int64_t start = a.rows.start_pos[b];
+    const int64_t ctx = r0 >= 0 && r0 < r1 ? min((int64_t)a.max_ctx, start + (r1 - r0)) : 0;
+    const int64_t copied = a.history ? min(ctx, start) : ctx;
+    if (p0 >= copied && !(a.table && p0 % 64 == 0)) return;
     if (threadIdx.x < 4) ld[threadIdx.x] = (int64_t)a.c.heads(threadIdx.x) * a.c.width(threadIdx.x);
     if (threadIdx.x < ROWS) {
         const int p = p0 + threadIdx.x;
         const int s = p < ctx ? pool_row(a.c, a.rows, b, p) : -1;
-        set.src[threadIdx.x] = s;
-        set.block[threadIdx.x] = s >= 0 ? s / a.c.block : -1;
+        set.src[threadIdx.x] = p < copied ? s : -1;
+        set.block[threadIdx.x] = p < copied && s >= 0 ? s / a.c.block : -1;
         set.dst[threadIdx.x] = a.table ? b * a.pages * 64 + p : s;
         // (a cache page holds whole pages of 64 rows: one is missing where its first row is)
         if (a.table && threadIdx.x == 0 && p0 % 64 == 0) a.table[(size_t)b * a.pages + p0 / 64] = s >= 0 ? b * a.pages + p0 / 64 : -1;
@@ -380,7 +369,7 @@ __global__ void __launch_bounds__(kReadThreads) expand_scaled_kernel(const __gri
     __syncthreads();
     const int mine = threadIdx.x < ROWS ? set.block[threadIdx.x] : set.block[0];
     const bool one = !__syncthreads_or(mine != set.block[0]) && mine >= 0;
-    if (!live) return;
+    if (p0 >= copied) return;
     copy_rows<__nv_bfloat16, ROWS>(a.c, set, one, a.y, ld);
 }
 

@@ -55,6 +55,7 @@ struct ScaledExpandArgs {
     int32_t *table;
     int pages;    // of 64 rows, a request
     int max_ctx;  // rows of a request that can be asked for
+    bool history;  // only rows 0 .. start_pos[b] - 1 (the others are there)
     cudaStream_t stream;
 };
 cudaError_t launch_expand_scaled(const ScaledExpandArgs &a);
@@ -119,6 +120,21 @@ cudaError_t launch_scaled_merge(const ScaledMergeArgs &m, cudaStream_t s);
 
 int device_sm_count();  // SMs of the current device (lrkv_api.cu)
 
+// Projection and write in one kernel, on tensor cores: covered shapes and launcher.  y:
+// bf16 pools that get the values too (NULL: none), at row b * ypages * 64 + position, or
+// (ypages 0) at the cache's row.
+struct ScaledAppendArgs {
+    ScaledPools c;
+    ScaledRows rows;
+    const void *X, *W_S_K, *W_S_V, *U_K, *U_V;
+    int d;
+    void *y[4];
+    int ypages;
+    cudaStream_t stream;
+};
+bool append_scaled_tc_fits(const ScaledPools &c, int n, int B, int d);
+cudaError_t launch_append_scaled_tc(const ScaledAppendArgs &p);
+
 // Scale exponents.
 __device__ __forceinline__ int clamp_exp(int byte) {
     return min(max(byte - 127, LRKV_SCALED_MIN_EXP), LRKV_SCALED_MAX_EXP);
@@ -128,6 +144,18 @@ __device__ __forceinline__ int needed_exp(float x) {
     const uint32_t u = __float_as_uint(x);
     const int e = (int)(u >> 23) - 135 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
     return min(max(e, LRKV_SCALED_MIN_EXP), LRKV_SCALED_MAX_EXP);
+}
+
+// Four codes times s, rounded to codes again.
+__device__ __forceinline__ uint32_t shrink_codes(uint32_t w, float s) {
+    uint32_t r = 0;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const uint32_t h2 = f16x2_from_e4m3x2((uint16_t)(w >> (16 * k)));
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h2));
+        r |= (uint32_t)e4m3x2_from_f32(f.x * s, f.y * s) << (16 * k);
+    }
+    return r;
 }
 
 }  // namespace lrkv
