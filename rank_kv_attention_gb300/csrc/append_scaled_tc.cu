@@ -61,7 +61,7 @@ struct Args {
     ScaledRows rows;
     int d, clusters;
     int hb, bw, rblocks;  // heads and columns of a private block, blocks of a pool
-    int coltiles;         // G of shared rows, then rblocks of private ones
+    int per, coltiles;    // blocks of a column tile (2 or 1); tiles: of shared rows, then of private ones
     // bf16 values beside the codes (y[0] NULL: none): row b * ypages * 64 + position,
     // or (ypages 0) the cache's row
     __nv_bfloat16 *y[4];
@@ -131,6 +131,11 @@ struct ColTile {
     int pool[2], head[2], heads, bw, width;
 };
 __device__ __forceinline__ ColTile col_tile(const Args &a, int ct) {
+    if (a.per == 1) {  // (one block: the first entries)
+        if (ct < 2 * a.c.G) return {{ct & 1, 0}, {ct >> 1, 0}, 1, 128, 128};
+        const int k = ct - 2 * a.c.G;
+        return {{2 + k / a.rblocks, 0}, {k % a.rblocks * a.hb, 0}, a.hb, a.bw, a.c.r};
+    }
     if (ct < a.c.G) return {{0, 1}, {ct, ct}, 1, 128, 128};
     const int k0 = 2 * (ct - a.c.G), k1 = k0 + 1;
     return {{2 + k0 / a.rblocks, 2 + k1 / a.rblocks}, {k0 % a.rblocks * a.hb, k1 % a.rblocks * a.hb}, a.hb, a.bw, a.c.r};
@@ -191,11 +196,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 rp = r;
             }
             const ColTile ct = col_tile(a, (int)(item % a.coltiles));
-            // this CTA's half of B: its block
-            const int wrow = (rank ? ct.head[1] : ct.head[0]) * ct.width;
-            const CUtensorMap *wm = &maps.w[rank ? ct.pool[1] : ct.pool[0]];
+            // this CTA's half of B: its block, or its half of the one block
+            const int k = a.per == 2 ? rank : 0, brows = a.per == 2 ? ct.bw : ct.bw / 2;
+            const int wrow = (k ? ct.head[1] : ct.head[0]) * ct.width + (a.per == 2 ? 0 : rank * brows);
+            const CUtensorMap *wm = &maps.w[k ? ct.pool[1] : ct.pool[0]];
             const int x0 = rt.b < 0 ? a.rows.n : rt.x0;  // (no such tile: zeros)
-            const uint32_t bytes = 2 * (kABytes + ct.bw * 128);
+            const uint32_t bytes = 2 * (kABytes + brows * 128);
             for (int kt = 0; kt < nk; ++kt) {
                 if (n > 0) ok = __all_sync(0xffffffffu, mbar_wait(&bar.empty[s], (n - 1) & 1));
                 if (!ok) break;
@@ -219,7 +225,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         int s = 0, n = 0, i = 0;
         for (int64_t item = it0; item < it1 && ok; ++item, ++i) {
             const ColTile ct = col_tile(a, (int)(item % a.coltiles));
-            const uint32_t idesc = tc_idesc_bf16(2 * kBM, 2 * ct.bw);
+            const uint32_t idesc = tc_idesc_bf16(2 * kBM, a.per * ct.bw);
             const int acc = i & 1;
             // the epilogue has drained this accumulator's previous tile
             if (i >= 2 && !mbar_wait(&bar.acc_empty[acc], ((i >> 1) - 1) & 1)) {
@@ -279,7 +285,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 was_block = at >= 0 ? at / block : -1;
             }
             const ColTile ct = col_tile(a, (int)(item % a.coltiles));
-            const int width = ct.width, nheads = 2 * ct.heads;
+            const int width = ct.width, nheads = a.per * ct.heads;
             if (was_block >= 0 && row < nheads) {
                 const int k = row / ct.heads, head = (k ? ct.head[1] : ct.head[0]) + row % ct.heads;
                 const int pool = k ? ct.pool[1] : ct.pool[0], heads = a.c.heads(pool);
@@ -295,15 +301,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (int h = 0; h < nheads; ++h) {
                 if (h == ct.heads) col = ct.bw;
                 uint32_t m = 0;
-#pragma unroll 1
-                for (int c = 0; c < width; c += 8, col += 8) {
-                    uint32_t v[8];
-                    tmem_ld8(lanes + col, v);
+                auto largest = [&](const uint32_t *v, int n) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
+                    for (int e = 0; e < n; ++e) {
                         const uint32_t u = v[e] & 0x7fffffffu;
                         m = max(m, u < kInfBits ? u : 0u);
                     }
+                };
+                int c = 0;
+#pragma unroll 1
+                for (; c + 16 <= width; c += 16, col += 16) {
+                    uint32_t v[16];
+                    tmem_ld16(lanes + col, v);
+                    largest(v, 16);
+                }
+                if (c < width) {
+                    uint32_t v[8];
+                    tmem_ld8(lanes + col, v);
+                    largest(v, 8);
+                    col += 8;
                 }
                 if (!fresh) m = 0;
 #pragma unroll
@@ -329,31 +345,55 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const bool put = live && fresh;
                 uint8_t *code = a.c.code[pool] + (dr * heads + head) * width;
                 __nv_bfloat16 *y = a.y[0] && put && yr >= 0 ? a.y[pool] + (yr * heads + head) * width : nullptr;
-#pragma unroll 1
-                for (int c = 0; c < width; c += 8, col += 8) {
-                    uint32_t v[8];
-                    tmem_ld8(lanes + col, v);
-                    if (put) {
-                        float x[8];
+                // eight values: their codes, and (y) what those are worth in bf16
+                auto codes = [&](const uint32_t *v, uint32_t *w, uint32_t *p) {
+                    float x[8];
 #pragma unroll
-                        for (int j = 0; j < 8; ++j)  // (the conversion would saturate an infinity)
-                            x[j] = (v[j] & 0x7fffffffu) == kInfBits ? __uint_as_float(0x7fffffffu) : __uint_as_float(v[j]) * inv;
-                        uint32_t w[2];
+                    for (int j = 0; j < 8; ++j)  // (the conversion would saturate an infinity)
+                        x[j] = (v[j] & 0x7fffffffu) == kInfBits ? __uint_as_float(0x7fffffffu) : __uint_as_float(v[j]) * inv;
 #pragma unroll
-                        for (int j = 0; j < 2; ++j)
-                            w[j] = (uint32_t)e4m3x2_from_f32(x[4 * j], x[4 * j + 1]) |
-                                   ((uint32_t)e4m3x2_from_f32(x[4 * j + 2], x[4 * j + 3]) << 16);
-                        *reinterpret_cast<uint2 *>(code + c) = make_uint2(w[0], w[1]);
-                        if (y) {
-                            uint32_t p[4];
+                    for (int j = 0; j < 2; ++j)
+                        w[j] = (uint32_t)e4m3x2_from_f32(x[4 * j], x[4 * j + 1]) |
+                               ((uint32_t)e4m3x2_from_f32(x[4 * j + 2], x[4 * j + 3]) << 16);
+                    if (y) {
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                const uint32_t h2 = f16x2_from_e4m3x2((uint16_t)(w[j >> 1] >> (16 * (j & 1))));
-                                const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h2));
-                                p[j] = pack_bf16(f.x * back, f.y * back);
-                            }
-                            *reinterpret_cast<uint4 *>(y + c) = make_uint4(p[0], p[1], p[2], p[3]);
+                        for (int j = 0; j < 4; ++j) {
+                            const uint32_t h2 = f16x2_from_e4m3x2((uint16_t)(w[j >> 1] >> (16 * (j & 1))));
+                            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h2));
+                            p[j] = pack_bf16(f.x * back, f.y * back);
                         }
+                    }
+                };
+                const bool wide = width % 16 == 0;  // (then a head's codes lie at multiples of 16 bytes)
+                int c = 0;
+#pragma unroll 1
+                for (; c + 16 <= width; c += 16, col += 16) {
+                    uint32_t v[16], w[4], p[8];
+                    tmem_ld16(lanes + col, v);
+                    if (put) {
+                        codes(v, w, p);
+                        codes(v + 8, w + 2, p + 4);
+                        if (wide) {
+                            *reinterpret_cast<uint4 *>(code + c) = make_uint4(w[0], w[1], w[2], w[3]);
+                        } else {
+                            *reinterpret_cast<uint2 *>(code + c) = make_uint2(w[0], w[1]);
+                            *reinterpret_cast<uint2 *>(code + c + 8) = make_uint2(w[2], w[3]);
+                        }
+                        if (y) {
+                            reinterpret_cast<uint4 *>(y + c)[0] = make_uint4(p[0], p[1], p[2], p[3]);
+                            reinterpret_cast<uint4 *>(y + c)[1] = make_uint4(p[4], p[5], p[6], p[7]);
+                        }
+                    }
+                    __syncwarp();
+                }
+                if (c < width) {
+                    uint32_t v[8], w[2], p[4];
+                    tmem_ld8(lanes + col, v);
+                    col += 8;
+                    if (put) {
+                        codes(v, w, p);
+                        *reinterpret_cast<uint2 *>(code + c) = make_uint2(w[0], w[1]);
+                        if (y) *reinterpret_cast<uint4 *>(y + c) = make_uint4(p[0], p[1], p[2], p[3]);
                     }
                     __syncwarp();
                 }
@@ -420,20 +460,24 @@ cudaError_t launch_append_scaled_tc(const ScaledAppendArgs &p) {
     a.hb = block_heads(c.r);
     a.bw = a.hb * c.r;
     a.rblocks = (c.H + a.hb - 1) / a.hb;
-    a.coltiles = c.G + a.rblocks;
+    // One block a tile while all of them run at once: each of twice as many SMs then does half
+    // of the products and of the epilogue.  Otherwise two, which need half the copies of X
+    // per product.  (N = one block's columns: a multiple of 32 for a pair of CTAs.)
+    const int64_t pairs = (p.rows.n / kBM + 2 * (int64_t)p.rows.B + 1) / 2;
+    a.per = a.bw % 32 == 0 && 2 * pairs * 2 * (c.G + a.rblocks) <= device_sm_count() ? 1 : 2;
+    a.coltiles = (2 / a.per) * (c.G + a.rblocks);
+    const int share = a.per == 2 ? 1 : 2;  // CTAs that share a block's rows
     a.ypages = p.ypages;
     for (int k = 0; k < 4; ++k) a.y[k] = static_cast<__nv_bfloat16 *>(p.y[k]);
     Maps maps;
-    if (!map_rows(&maps.x, p.X, p.rows.n, p.d, kBM) || !map_rows(&maps.w[0], p.W_S_K, (int64_t)c.G * 128, p.d, 128) ||
-        !map_rows(&maps.w[1], p.W_S_V, (int64_t)c.G * 128, p.d, 128) ||
-        !map_rows(&maps.w[2], p.U_K, (int64_t)c.H * c.r, p.d, a.bw) ||
-        !map_rows(&maps.w[3], p.U_V, (int64_t)c.H * c.r, p.d, a.bw))
+    if (!map_rows(&maps.x, p.X, p.rows.n, p.d, kBM) || !map_rows(&maps.w[0], p.W_S_K, (int64_t)c.G * 128, p.d, 128 / share) ||
+        !map_rows(&maps.w[1], p.W_S_V, (int64_t)c.G * 128, p.d, 128 / share) ||
+        !map_rows(&maps.w[2], p.U_K, (int64_t)c.H * c.r, p.d, a.bw / share) ||
+        !map_rows(&maps.w[3], p.U_V, (int64_t)c.H * c.r, p.d, a.bw / share))
         return cudaErrorInvalidValue;
     cudaError_t e = smem_limit_once(append_scaled_tc_kernel, kSmem);
     if (e != cudaSuccess) return e;
-    // row tiles that n rows of B requests can make
-    const int64_t most = ((p.rows.n / kBM + 2 * (int64_t)p.rows.B + 1) / 2) * a.coltiles;
-    a.clusters = (int)std::max<int64_t>(1, std::min<int64_t>(most, device_sm_count() / 2));
+    a.clusters = (int)std::max<int64_t>(1, std::min<int64_t>(pairs * a.coltiles, device_sm_count() / 2));
     return launch_pdl(append_scaled_tc_kernel, dim3(2 * a.clusters), dim3(kThreads), kSmem, p.stream, maps, a);
 }
 
