@@ -32,7 +32,7 @@
 // over one CTA per SM; a CTA walks its tiles (two units of one request, or one).
 // Each piece of a request in a CTA leaves a state in the workspace, and a second
 // kernel merges and expands them by B_V[h].  A first, small kernel makes the q and p
-// operands (and the offsets that the merge needs), while the first tiles are on
+// operands (and the places of each request's states), while the first tiles are on
 // their way.
 //
 // 24 warps: 0-15 scores and weights (thread = token = tensor-memory lane, a quarter of
@@ -226,15 +226,16 @@ __device__ __forceinline__ uint32_t op_byte(int n, int k) {
 
 // ---------------------------------------------------------------------------
 // Operands: block (h, b) makes the terms of q[b, h] and p = q B_K[h] and the factors
-// that bring a tile's sums to log2 units; one more block the unit offsets.
+// that bring a tile's sums to log2 units; one more block the places of the states.
 // ---------------------------------------------------------------------------
 struct PrepArgs {
     const __nv_bfloat16 *q, *B_K;
     const int32_t *seq_lens;
     uint8_t *img;
     int64_t img_stride;
-    int32_t *off;
-    int B, max_len;
+    int2 *places;  // of request b's states: first slot and count
+    int32_t *status;
+    int B, max_len, grid;
     float scale_log2;
 };
 
@@ -246,20 +247,32 @@ __global__ void __launch_bounds__(128) scaled_prep_kernel(const __grid_constant_
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     pdl_wait();
     pdl_launch_dependents();
-    if (blockIdx.x == (unsigned)P.B) {  // offsets, by the blocks' one column that exists for them
+    if (blockIdx.x == (unsigned)P.B) {
         if (blockIdx.y) return;
-        const int per = (P.B + 127) / 128, b0 = tid * per, b1 = min(P.B, b0 + per);
+        const int per = (P.B + 127) / 128, b0 = min(P.B, tid * per), b1 = min(P.B, b0 + per);
         int n = 0;
         for (int b = b0; b < b1; ++b) n += units_of(P.seq_lens[b], P.max_len);
         sums[tid] = n;
         __syncthreads();
-        int at = 0;
-        for (int i = 0; i < tid; ++i) at += sums[i];
-        for (int b = b0; b < b1; ++b) {
-            P.off[b] = at;
-            at += units_of(P.seq_lens[b], P.max_len);
+        uint32_t at = 0, U = 0;
+        for (int i = 0; i < 128; ++i) {
+            if (i == tid) at = U;
+            U += sums[i];
         }
-        if (b1 == P.B && b0 < b1) P.off[P.B] = at;
+        // the CTAs whose units [g U / G, (g + 1) U / G) meet the request's
+        const uint32_t G = min((uint32_t)P.grid, U);
+        for (int b = b0; b < b1; ++b) {
+            const uint32_t k = units_of(P.seq_lens[b], P.max_len);
+            int2 place = make_int2(0, 0);
+            if (k) {
+                const uint32_t g0 = ((at + 1) * G - 1) / U, g1 = ((at + k) * G - 1) / U;
+                place = make_int2(b + (int)g0, (int)(g1 - g0) + 1);
+            } else {
+                status_or(P.status, LRKV_STATUS_BAD_SEQLEN);
+            }
+            P.places[b] = place;
+            at += k;
+        }
         return;
     }
     const int b = blockIdx.x, h = blockIdx.y, r = S.r;
@@ -426,7 +439,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     }
     __syncthreads();
-    pdl_launch_dependents();
     Walk w;
     {
         // warps' sums, then the thread whose requests hold the first unit (whole warp)
@@ -527,6 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // ================= operand images =================
             if (lane == 0) {
                 pdl_wait();
+                pdl_launch_dependents();  // (the merge reads the places before its own wait)
                 int last = -1;
                 for (; ok && w.live(); w.next(a)) {
                     if (w.seg == last) continue;
@@ -944,9 +957,9 @@ int launch_registers(K *kernel) {
     return cudaFuncGetAttributes(&f, kernel) == cudaSuccess ? f.numRegs : 0;
 }
 
-// Workspace: unit offsets, operand images, states of up to B + CTAs pieces.
+// Workspace: places of the states, operand images, states of up to B + CTAs pieces.
 struct Ws {
-    int32_t *off;
+    int2 *places;
     uint8_t *img;
     int64_t img_stride;
     void *states;
@@ -956,8 +969,8 @@ Ws layout(void *base, const Shape &s, int B, int ctas, int d_h) {
     Ws w;
     char *p = static_cast<char *>(base);
     size_t o = 0;
-    w.off = reinterpret_cast<int32_t *>(p);
-    o += align256(sizeof(int32_t) * ((size_t)B + 1));
+    w.places = reinterpret_cast<int2 *>(p);
+    o += align256(sizeof(int2) * (size_t)B);
     w.img = reinterpret_cast<uint8_t *>(p + o);
     w.img_stride = (int64_t)align256(s.img_bytes);
     o += (size_t)B * w.img_stride;
@@ -1019,7 +1032,9 @@ cudaError_t launch_decode_scaled_tc(const ScaledDecodeArgs &d, void *ws) {
     p.seq_lens = d.seq_lens;
     p.img = w.img;
     p.img_stride = w.img_stride;
-    p.off = w.off;
+    p.places = w.places;
+    p.status = d.status;
+    p.grid = ctas;
     p.B = d.B;
     p.max_len = max_len;
     p.scale_log2 = 1.4426950408889634f / sqrtf(128.f);
@@ -1041,9 +1056,8 @@ cudaError_t launch_decode_scaled_tc(const ScaledDecodeArgs &d, void *ws) {
     if (e != cudaSuccess) return e;
     ScaledMergeArgs m;
     m.st = a.st;
-    m.off = w.off;
+    m.places = w.places;
     m.splits = 0;
-    m.grid = ctas;
     m.seq_lens = d.seq_lens;
     m.max_len = max_len;
     m.leave = false;

@@ -191,99 +191,102 @@ __global__ void __launch_bounds__(kThreads) decode_scaled_any_kernel(const __gri
 // ---------------------------------------------------------------------------
 // Merge: one CTA per (request, head).  o = (sum_s f_s accS_s + (sum_s f_s accR_s)
 // B_V[h]^T) / sum_s f_s l_s with f_s = 2^(m_s - max m).  Groups of threads, one thread
-// a column, take the states in turn.  All of it is latency: B_V[h] is on its way
-// before the states are there, and value sums are read together with the maxima that
-// weigh them.
+// a column, take the states in turn.
+//
+// All of it is latency (about a microsecond for a round trip to memory that other
+// SMs have just written): before the wait it reads what is there already, B_V[h] and the
+// places of the request's states; after it everything else at once, value sums
+// together with the maxima that weigh them.  HELD: value sums a thread has on the way.
 // ---------------------------------------------------------------------------
-constexpr int kMergeThreads = 512, kMergeStates = 256, kMergeHeld = 4, kMergeRows = 3;
+constexpr int kMergeStates = 256, kMergeB = 3;
 
-__global__ void __launch_bounds__(kMergeThreads, 3) scaled_merge_kernel(const __grid_constant__ ScaledMergeArgs P) {
-    __shared__ float fs[kMergeStates], sums[kMergeThreads];
-    __shared__ float red[2][kMergeThreads / 32];
+template <int THREADS, int HELD>
+__global__ void __launch_bounds__(THREADS, HELD == 4 ? 6 : 2) scaled_merge_kernel(const __grid_constant__ ScaledMergeArgs P) {
+    __shared__ float fs[kMergeStates], sums[512], part[kMergeB * THREADS];
+    __shared__ float red[2][THREADS / 32];
     const int h = blockIdx.y, b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int H = P.H, d_h = P.d_h, r = P.r, W = d_h + r, cols = (W + 31) & ~31, threads = blockDim.x;
+    const int H = P.H, d_h = P.d_h, r = P.r, W = d_h + r, cols = (W + 31) & ~31;
     // ---- B_V[h] in tasks of eight columns of a row: the first ones of every thread.  (The
     // kernel before this one started after all that is in front of the call was done.)
     const int v8 = r / 8, tasks = d_h * v8;
-    const __nv_bfloat16 *B = static_cast<const __nv_bfloat16 *>(P.B_V) + (size_t)h * d_h * r;
-    uint4 bv[kMergeRows];
+    const uint4 *B = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(P.B_V) + (size_t)h * d_h * r);
+    uint4 bv[kMergeB];
 #pragma unroll
-    for (int j = 0; j < kMergeRows; ++j)
-        if (tid + j * threads < tasks) bv[j] = reinterpret_cast<const uint4 *>(B)[tid + j * threads];
+    for (int j = 0; j < kMergeB; ++j)
+        if (tid + j * THREADS < tasks) bv[j] = B[tid + j * THREADS];
+    int2 place = P.places ? P.places[b] : make_int2(b * P.splits, P.splits);
     pdl_wait();
     pdl_launch_dependents();
-    const int32_t L = P.seq_lens[b];
-    if (P.leave && L == -1) return;
-    int64_t s0 = 0;
-    int ns = 0;
-    if (L < 1 || L > P.max_len) {
-        if (h == 0 && tid == 0) status_or(P.status, LRKV_STATUS_BAD_SEQLEN);
-    } else if (P.off) {
-        // the CTAs whose units [g U / G, (g + 1) U / G) meet the request's
-        const uint32_t U = P.off[P.B], G = min((uint32_t)P.grid, U), u0 = P.off[b], u1 = P.off[b + 1] - 1;
-        const uint32_t g0 = ((u0 + 1) * G - 1) / U, g1 = ((u1 + 1) * G - 1) / U;
-        s0 = b + g0;
-        ns = (int)(g1 - g0) + 1;
-    } else {
-        s0 = (int64_t)b * P.splits;
-        ns = P.splits;
+    if (!P.places) {
+        const int32_t L = P.seq_lens[b];
+        if (L == -1 && P.leave) return;
+        if (L < 1 || L > P.max_len) {
+            if (h == 0 && tid == 0) status_or(P.status, LRKV_STATUS_BAD_SEQLEN);
+            place.y = 0;
+        }
     }
-    // (at most 256 parts, or a state of every CTA)
-    float m = -INFINITY, l = 0.f;
-    if (tid < ns) {
-        m = P.st.ml[((s0 + tid) * H + h) * 2];
-        l = P.st.ml[((s0 + tid) * H + h) * 2 + 1];
-    }
-    const int groups = threads / cols, g = tid / cols, c = tid - g * cols;
-    const bool mine = g < groups && c < W;
-    const float *acc = P.st.acc + s0 * H * W + (c < d_h ? (size_t)h * d_h + c : (size_t)H * d_h + h * r + c - d_h);
-    float held[kMergeHeld];
+    const int ns = place.y;  // at most 256 parts, or a state of every CTA
+    const int64_t s0 = place.x;
+    float2 ml = make_float2(-INFINITY, 0.f);
+    if (tid < ns) ml = reinterpret_cast<const float2 *>(P.st.ml)[(s0 + tid) * H + h];
+    const int groups = max(1, THREADS / cols), g = tid / cols, c0 = tid - g * cols;
+    const bool mine = g < groups && c0 < W;
+    auto column = [&](int c) { return P.st.acc + s0 * H * W + (c < d_h ? h * d_h + c : H * d_h + h * r + c - d_h); };
+    const float *acc = column(c0);
+    float held[HELD];
 #pragma unroll
-    for (int j = 0; j < kMergeHeld; ++j) {
+    for (int j = 0; j < HELD; ++j) {
         const int s = g + j * groups;
         held[j] = mine && s < ns ? acc[(int64_t)s * H * W] : 0.f;
     }
-    float M = m;
+    float M = ml.x;
 #pragma unroll
     for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
     if (lane == 0) red[0][warp] = M;
     __syncthreads();
-    for (int w = 0; w < threads / 32; ++w) M = fmaxf(M, red[0][w]);
-    const float ref = M == -INFINITY ? 0.f : M;
-    // a part without rows has written no value sums
-    const bool none = m == -INFINITY && l == 0.f;
-    const float f = none ? 0.f : exp2f(m - ref);
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) M = fmaxf(M, red[0][w]);
+    // a part without rows (m = -inf, l = 0) has written no value sums
+    const bool none = ml.x == -INFINITY && ml.y == 0.f;
+    const float f = none ? 0.f : exp2f(ml.x - (M == -INFINITY ? 0.f : M));
     if (tid < kMergeStates) fs[tid] = none ? -1.f : f;
-    l = none ? 0.f : l * f;
+    float l = none ? 0.f : ml.y * f;
 #pragma unroll
     for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
     if (lane == 0) red[1][warp] = l;
     __syncthreads();
     l = 0.f;
-    for (int w = 0; w < threads / 32; ++w) l += red[1][w];
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) l += red[1][w];
     const float inv = l != 0.f ? 1.f / l : 0.f;  // (NaN stays NaN)
-
+    auto weigh = [&](int s, float v) {
+        const float k = fs[s];
+        return k >= 0.f || k != k ? k * v : 0.f;
+    };
     float x = 0.f;
     if (mine) {
-        auto add = [&](int s, float v) {
-            const float k = fs[s];
-            if (k >= 0.f || k != k) x += k * v;
-        };
 #pragma unroll
-        for (int j = 0; j < kMergeHeld; ++j)
-            if (g + j * groups < ns) add(g + j * groups, held[j]);
+        for (int j = 0; j < HELD; ++j)
+            if (g + j * groups < ns) x += weigh(g + j * groups, held[j]);
 #pragma unroll 8
-        for (int s = g + kMergeHeld * groups; s < ns; s += groups) add(s, acc[(int64_t)s * H * W]);
+        for (int s = g + HELD * groups; s < ns; s += groups) x += weigh(s, acc[(int64_t)s * H * W]);
     }
-    sums[tid] = x;
-    __syncthreads();
-    if (g == 0 && c < W) {
-        for (int k = 1; k < groups; ++k) x += sums[k * cols + c];
+    if (groups > 1) {
+        sums[tid] = x;
+        __syncthreads();
+        if (g == 0 && c0 < W)
+            for (int k = 1; k < groups; ++k) x += sums[k * cols + c0];
+        __syncthreads();
+    }
+    if (g == 0 && c0 < W) sums[c0] = x;
+    for (int c = tid + THREADS; c < W; c += THREADS) {  // (wider than the block)
+        const float *a = column(c);
+        x = 0.f;
+        for (int s = 0; s < ns; ++s) x += weigh(s, a[(int64_t)s * H * W]);
         sums[c] = x;
     }
     __syncthreads();
-    // ---- expand: a row's tasks add up in order (one thread a row where tasks are few)
-    __shared__ float part[kMergeRows * kMergeThreads];
+    // ---- expand
     __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(P.out) + ((size_t)b * H + h) * d_h;
     auto dot = [&](int task, const uint4 &w) {
         const float *o = sums + d_h + task % v8 * 8;
@@ -292,22 +295,17 @@ __global__ void __launch_bounds__(kMergeThreads, 3) scaled_merge_kernel(const __
         s = fmaf(o[4], bf16lo(w.z), s); s = fmaf(o[5], bf16hi(w.z), s); s = fmaf(o[6], bf16lo(w.w), s);
         return fmaf(o[7], bf16hi(w.w), s);
     };
-    if (tasks <= kMergeRows * threads) {
+    const bool fit = tasks <= kMergeB * THREADS;
+    if (fit) {
 #pragma unroll
-        for (int j = 0; j < kMergeRows; ++j)
-            if (tid + j * threads < tasks) part[tid + j * threads] = dot(tid + j * threads, bv[j]);
+        for (int j = 0; j < kMergeB; ++j)
+            if (tid + j * THREADS < tasks) part[tid + j * THREADS] = dot(tid + j * THREADS, bv[j]);
         __syncthreads();
-        for (int d = tid; d < d_h; d += threads) {
-            float s = sums[d];
-            for (int k = 0; k < v8; ++k) s += part[d * v8 + k];
-            out[d] = __float2bfloat16_rn(s * inv);
-        }
-    } else {
-        for (int d = tid; d < d_h; d += threads) {
-            float s = sums[d];
-            for (int k = 0; k < v8; ++k) s += dot(k, reinterpret_cast<const uint4 *>(B)[d * v8 + k]);
-            out[d] = __float2bfloat16_rn(s * inv);
-        }
+    }
+    for (int d = tid; d < d_h; d += THREADS) {
+        float s = sums[d];
+        for (int k = 0; k < v8; ++k) s += fit ? part[d * v8 + k] : dot(k, B[d * v8 + k]);
+        out[d] = __float2bfloat16_rn(s * inv);
     }
 }
 
@@ -360,9 +358,8 @@ cudaError_t launch_decode_scaled_any(const ScaledDecodeArgs &a, void *ws) {
     if (e != cudaSuccess) return e;
     ScaledMergeArgs m;
     m.st = P.st;
-    m.off = nullptr;
+    m.places = nullptr;
     m.splits = P.splits;
-    m.grid = 0;
     m.seq_lens = a.seq_lens;
     m.max_len = a.max_pages * a.c.page_size;
     m.leave = a.req_row != nullptr;
@@ -382,10 +379,11 @@ cudaError_t launch_scaled_row_queries(const ScaledRows &rows, int max_len, int32
 }
 
 cudaError_t launch_scaled_merge(const ScaledMergeArgs &m, cudaStream_t s) {
-    // 256 threads where CTAs are many (each merges few states then; 64 requests of 16 heads:
-    // 12 us with 512), and the columns fit
-    const bool few = (int64_t)m.B * m.H < 2 * device_sm_count() || m.d_h + m.r > 256;
-    return launch_pdl(scaled_merge_kernel, dim3(m.B, m.H), dim3(few ? kMergeThreads : 256), 0, s, m);
+    // 512 threads with 16 value sums each on the way where CTAs are few, and states of a
+    // request many; else six CTAs of 256 threads an SM (64 requests of 16 heads: 12 us with 512)
+    const bool few = (int64_t)m.B * m.H < 2 * device_sm_count();
+    return few ? launch_pdl(scaled_merge_kernel<512, 16>, dim3(m.B, m.H), dim3(512), 0, s, m)
+               : launch_pdl(scaled_merge_kernel<256, 4>, dim3(m.B, m.H), dim3(256), 0, s, m);
 }
 
 }  // namespace lrkv

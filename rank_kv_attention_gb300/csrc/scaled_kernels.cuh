@@ -102,12 +102,13 @@ bool scaled_tc_covers(const ScaledPools &c);
 size_t scaled_tc_ws_bytes(const ScaledPools &c, int B, int max_seq_len);
 cudaError_t launch_decode_scaled_tc(const ScaledDecodeArgs &a, void *ws);
 
-// Merges the states of request b, slots first(b) .. first(b) + count(b) - 1, into out.
+// Merges the states of every request and head into out.
 struct ScaledMergeArgs {
     ScaledStates st;
-    const int32_t *off;  // tensor-core kernel: units of 64 rows before request b [B + 1], or NULL
-    int splits;          // off NULL: slots b * splits ..
-    int grid;            // off: CTAs that share the units
+    // first slot and count of request b's states, written before the kernel in front of
+    // the merge lets it start, or NULL:
+    const int2 *places;
+    int splits;  // slots b * splits .. of every request whose length is valid
     const int32_t *seq_lens;
     int max_len;
     bool leave;  // outputs of length -1 are left alone
