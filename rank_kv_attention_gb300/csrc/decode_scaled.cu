@@ -390,53 +390,52 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int H = S.H, stages = S.stages, NB = S.boxes;
     const int img_stride = (S.img_bytes + 1023) / 1024 * 1024;
 
+    // ---- set up while the kernels before this one end
+    if (warp == kWarpImage) {  // (a lane initialises one to three barriers)
+        if (lane < stages) {
+            mbar_init(&bar.full[lane], 1);
+            mbar_init(&bar.empty[lane], 1);
+        } else if (lane >= 16 && lane < 18) {
+            mbar_init(&bar.img_full[lane - 16], 1);
+            mbar_init(&bar.img_empty[lane - 16], 1 + kSoftmax);
+            mbar_init(&bar.e_full[lane - 16], 32);
+        } else if (lane >= 18 && lane < 22) {
+            mbar_init(&bar.w_full[lane - 18], kSoftmax);
+            mbar_init(&bar.meet[lane - 18], 128);
+        } else if (lane >= 22 && lane < 24) {
+            mbar_init(&bar.pv_done[lane - 22], 1);
+            mbar_init(&bar.v_empty[lane - 22], 128);
+        } else if (lane == 24) {
+            mbar_init(&bar.sc_full, 1);
+            mbar_init(&bar.sc_empty, kSoftmax);
+            mbar_init(&bar.tmem_ready, 1);
+        }
+        fence_barrier_init();
+    } else if (warp == kWarpMma && lane <= NB) {
+        const int x = lane;
+        bar.kbox[x] = x ? make_uint4((S.qrows + S.prow[x - 1]) * 128, S.scol[x - 1], idesc_f8(S.n[x - 1], false),
+                                     min(4, (H * S.r - 128 * (x - 1) + 31) / 32))
+                        : make_uint4(0, 0, idesc_f8(S.qrows, false), 4);
+        bar.vbox[x] = x ? make_uint4((S.wrows + 2 * S.ha[x - 1]) * 128, S.vcol[x - 1], idesc_f8(S.nv[x - 1], true), 0)
+                        : make_uint4(0, S.v0, idesc_f8(S.nv0, true), 0);
+    } else if (warp == kWarpCopy && elect_one()) {
+        for (int k = 0; k < 2; ++k) {
+            prefetch_tensormap(&maps.k[k]);
+            prefetch_tensormap(&maps.v[k]);
+        }
+    }
     // ---- this CTA's share: threads hold consecutive requests; units before each of them
     const int per = (a.B + kThreads - 1) / kThreads;
     {
         const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
-        int n = 0;
-        for (int b = b0; b < b1; ++b) n += units_of(a.seq_lens[b], a.max_len);
-        if (tid == kThreads - 1) {
-            for (int s = 0; s < stages; ++s) {
-                mbar_init(&bar.full[s], 1);
-                mbar_init(&bar.empty[s], 1);
-            }
-            for (int k = 0; k < 2; ++k) {
-                mbar_init(&bar.img_full[k], 1);
-                mbar_init(&bar.img_empty[k], 1 + kSoftmax);
-                mbar_init(&bar.w_full[k], kSoftmax);
-                mbar_init(&bar.w_full[k + 2], kSoftmax);
-                mbar_init(&bar.v_empty[k], 128);
-                mbar_init(&bar.pv_done[k], 1);
-                mbar_init(&bar.e_full[k], 32);
-            }
-            for (int k = 0; k < 4; ++k) mbar_init(&bar.meet[k], 128);
-            mbar_init(&bar.sc_full, 1);
-            mbar_init(&bar.sc_empty, kSoftmax);
-            mbar_init(&bar.tmem_ready, 1);
-            fence_barrier_init();
-        }
-        int inc = n;
+        int inc = 0;
+        for (int b = b0; b < b1; ++b) inc += units_of(a.seq_lens[b], a.max_len);
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int v = __shfl_up_sync(0xffffffffu, inc, o);
             if (lane >= o) inc += v;
         }
         bar.upto[tid] = inc;
-        if (warp == kWarpMma && lane <= NB) {
-            const int x = lane;
-            bar.kbox[x] = x ? make_uint4((S.qrows + S.prow[x - 1]) * 128, S.scol[x - 1], idesc_f8(S.n[x - 1], false),
-                                         min(4, (H * S.r - 128 * (x - 1) + 31) / 32))
-                            : make_uint4(0, 0, idesc_f8(S.qrows, false), 4);
-            bar.vbox[x] = x ? make_uint4((S.wrows + 2 * S.ha[x - 1]) * 128, S.vcol[x - 1], idesc_f8(S.nv[x - 1], true), 0)
-                            : make_uint4(0, S.v0, idesc_f8(S.nv0, true), 0);
-        }
-        if (warp == kWarpCopy && elect_one()) {
-            for (int k = 0; k < 2; ++k) {
-                prefetch_tensormap(&maps.k[k]);
-                prefetch_tensormap(&maps.v[k]);
-            }
-        }
     }
     __syncthreads();
     Walk w;
@@ -701,7 +700,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ================= scores and weights =================
         // warp: tokens 32 (warp & 3) + lane of a tile, heads h0 .. h0 + hn - 1 (a quarter)
         const int hn = H / 4, grp = warp >> 2, h0 = grp * hn, token = 32 * (warp & 3) + lane;
-        float m[HT], l[HT];
+        float l[HT], m = -INFINITY;  // m: of lane k's head h0 + k, the same in all four warps
         uint32_t met = 0;
         auto meet = [&]() -> bool {  // the four warps of these heads
             mbar_arrive(&bar.meet[grp]);
@@ -714,11 +713,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool first = w.seg != last, ends = w.ends();
             const int seg = last = w.seg;
             if (first) {
+                m = -INFINITY;
 #pragma unroll
-                for (int k = 0; k < HT; ++k) {
-                    m[k] = -INFINITY;
-                    l[k] = 0.f;
-                }
+                for (int k = 0; k < HT; ++k) l[k] = 0.f;
                 ok = __all_sync(0xffffffffu, mbar_wait(&bar.img_full[seg & 1], (seg >> 1) & 1));
                 if (!ok) break;
             }
@@ -781,30 +778,42 @@ __global__ void __launch_bounds__(kThreads, 1)
             // the operand of the tile before the last has been read
             if (ok && i > 1) ok = __all_sync(0xffffffffu, mbar_wait(&bar.pv_done[i & 1], ((i >> 1) - 1) & 1));
             if (!ok) break;
-            float *fac = reinterpret_cast<float *>(smem + off.fac) + (i & 3) * 3 * 32;
+            // lane k: what head h0 + k needs.  Weights are relative to the running maximum (one
+            // that underflows counts as zero); the operands' to the tile's largest
+            float alpha = 0.f, ref = 0.f, fs = 0.f, fr = 0.f;
+            if (lane < hn) {
+                float M[3];
+#pragma unroll
+                for (int j = 0; j < 3; ++j) {
+                    const float4 v = *reinterpret_cast<const float4 *>(&red[(j * HT + lane) * 4]);
+                    M[j] = fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w));
+                }
+                const float mn = fmaxf(m, M[0]);
+                ref = mn == -INFINITY ? 0.f : mn;
+                const float ms = M[1] == -INFINITY ? ref : M[1] - 8.f, mr = M[2] == -INFINITY ? ref : M[2] - 8.f;
+                alpha = ex2f(m - ref);
+                m = mn;
+                // (bounded: where it is larger than that every weight has underflown)
+                fs = ex2f(fminf(ref - ms, 125.f));
+                fr = ex2f(fminf(ref - mr, 125.f));
+                if ((warp & 3) == 0) {
+                    float *fac = reinterpret_cast<float *>(smem + off.fac) + (i & 3) * 3 * 32 + h0 + lane;
+                    fac[0] = alpha;
+                    fac[32] = ex2f(ms - ref);
+                    fac[64] = ex2f(mr - ref);
+                }
+            }
             uint8_t *ws = smem + off.weights + (i & 1) * 2 * S.wrows * 128, *wr = ws + S.wrows * 128;
+            const float vs = exp2i((int)es);
 #pragma unroll
             for (int k = 0; k < HT; ++k)
                 if (k < hn) {
                     const int h = h0 + k;
-                    float M[3];
-#pragma unroll
-                    for (int j = 0; j < 3; ++j) {
-                        const float4 v = *reinterpret_cast<const float4 *>(&red[(j * HT + k) * 4]);
-                        M[j] = fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w));
-                    }
-                    const float mn = fmaxf(m[k], M[0]), ref = mn == -INFINITY ? 0.f : mn;
-                    const float ms = M[1] == -INFINITY ? 0.f : M[1], mr = M[2] == -INFINITY ? 0.f : M[2];
-                    const float alpha = ex2f(m[k] - ref);
-                    m[k] = mn;
-                    l[k] = l[k] * alpha + ex2f(x[k] - ref);
-                    if (token == k) {
-                        fac[h] = alpha;
-                        fac[32 + h] = ex2f(ms - ref - 8.f);
-                        fac[64 + h] = ex2f(mr - ref - 8.f);
-                    }
+                    const float w = ex2f(x[k] - __shfl_sync(0xffffffffu, ref, k));
+                    l[k] = l[k] * __shfl_sync(0xffffffffu, alpha, k) + w;
                     // both operands' terms, a pair at a time
-                    const float y = ex2f(x[k] + es - ms + 8.f), z = ex2f(x[k] + er[k] - mr + 8.f);
+                    const float y = w * vs * __shfl_sync(0xffffffffu, fs, k);
+                    const float z = w * exp2i((int)er[k]) * __shfl_sync(0xffffffffu, fr, k);
                     const uint16_t t1 = e4m3x2_from_f32(y, z);
                     const uint32_t h2 = f16x2_from_e4m3x2(t1);
                     const float2 g = __half22float2(*reinterpret_cast<const __half2 *>(&h2));
@@ -830,14 +839,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 if (lane < hn) red[(3 * HT + lane) * 4 + (warp & 3)] = sum;
                 if (!(ok = meet())) break;
-                float *ml = a.st.ml + ((int64_t)w.b + blockIdx.x) * H * 2;
-#pragma unroll
-                for (int k = 0; k < HT; ++k)
-                    if (k < hn && token == k) {
-                        const float4 v = *reinterpret_cast<const float4 *>(&red[(3 * HT + k) * 4]);
-                        ml[2 * (h0 + k)] = m[k];
-                        ml[2 * (h0 + k) + 1] = (v.x + v.y) + (v.z + v.w);
-                    }
+                if ((warp & 3) == 0 && lane < hn) {
+                    float2 *ml = reinterpret_cast<float2 *>(a.st.ml) + ((int64_t)w.b + blockIdx.x) * H + h0;
+                    const float4 v = *reinterpret_cast<const float4 *>(&red[(3 * HT + lane) * 4]);
+                    ml[lane] = make_float2(m, (v.x + v.y) + (v.z + v.w));
+                }
             }
         }
         if (!ok && lane == 0) status_or(a.status, LRKV_STATUS_TIMEOUT);
