@@ -32,8 +32,7 @@
 // over one CTA per SM; a CTA walks its tiles (two units of one request, or one).
 // Each piece of a request in a CTA leaves a state in the workspace, and a second
 // kernel merges and expands them by B_V[h].  A first, small kernel makes the q and p
-// operands (and the places of each request's states), while the first tiles are on
-// their way.
+// operands, each CTA's start and the places of each request's states.
 //
 // 24 warps: 0-15 scores and weights (thread = token = tensor-memory lane, a quarter of
 // the heads each), 16-19 value accumulators (thread = column), one copies cache tiles,
@@ -131,7 +130,6 @@ struct Bars {
     alignas(16) uint4 kbox[kMaxBoxes + 1], vbox[kMaxBoxes + 1];
     uint64_t e_full[2], tmem_ready;
     uint32_t tmem;
-    int upto[kThreads];  // units of a thread's requests and of those before it in its warp
 };
 
 // Shared memory after the ring of stages.
@@ -157,6 +155,7 @@ struct Maps {
 struct Args {
     ScaledPools c;
     const int32_t *seq_lens, *page_table;
+    const int4 *starts;  // request, its length, first row, units of every CTA
     const uint8_t *img;  // operand images [B][img_bytes rounded up to 256]
     int64_t img_stride;
     ScaledStates st;
@@ -234,6 +233,7 @@ struct PrepArgs {
     uint8_t *img;
     int64_t img_stride;
     int2 *places;  // of request b's states: first slot and count
+    int4 *starts;  // where the tensor-core kernel's CTAs begin
     int32_t *status;
     int B, max_len, grid;
     float scale_log2;
@@ -243,23 +243,34 @@ __global__ void __launch_bounds__(128) scaled_prep_kernel(const __grid_constant_
                                                           const __grid_constant__ Shape S) {
     __shared__ float qs[128], ps[64], part[128 * 8];
     __shared__ float red[8];
-    __shared__ int sums[128];
+    __shared__ int sums[4];
+    __shared__ uint32_t upto[128];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     pdl_wait();
     pdl_launch_dependents();
     if (blockIdx.x == (unsigned)P.B) {
         if (blockIdx.y) return;
+        // units of 64 rows, threads hold consecutive requests
         const int per = (P.B + 127) / 128, b0 = min(P.B, tid * per), b1 = min(P.B, b0 + per);
-        int n = 0;
+        uint32_t n = 0;
         for (int b = b0; b < b1; ++b) n += units_of(P.seq_lens[b], P.max_len);
-        sums[tid] = n;
-        __syncthreads();
-        uint32_t at = 0, U = 0;
-        for (int i = 0; i < 128; ++i) {
-            if (i == tid) at = U;
-            U += sums[i];
+        uint32_t inc = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t v = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += v;
         }
-        // the CTAs whose units [g U / G, (g + 1) U / G) meet the request's
+        if (lane == 31) sums[warp] = (int)inc;
+        __syncthreads();
+        uint32_t U = 0, at = inc - n;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            if (w < warp) at += sums[w];
+            U += sums[w];
+        }
+        upto[tid] = at + n;
+        // CTA g takes the units [g U / G, (g + 1) U / G) (products below 2^32: at most 2^24
+        // units); CTAs past the last unit have none, so that no request's CTAs have a gap
         const uint32_t G = min((uint32_t)P.grid, U);
         for (int b = b0; b < b1; ++b) {
             const uint32_t k = units_of(P.seq_lens[b], P.max_len);
@@ -272,6 +283,29 @@ __global__ void __launch_bounds__(128) scaled_prep_kernel(const __grid_constant_
             }
             P.places[b] = place;
             at += k;
+        }
+        __syncthreads();
+        for (int g = tid; g < P.grid; g += 128) {
+            int4 start = make_int4(0, 0, 0, 0);  // request, its length, first row, units
+            if (g < (int)G) {
+                const uint32_t u0 = U * g / G, u1 = U * (g + 1) / G;
+                int lo = 0, hi = 127;  // the thread whose requests hold unit u0
+                while (lo < hi) {
+                    const int mid = (lo + hi) >> 1;
+                    if ((uint32_t)upto[mid] > u0) hi = mid;
+                    else lo = mid + 1;
+                }
+                uint32_t from = lo ? upto[lo - 1] : 0;
+                int b = lo * per, L;
+                for (;; ++b) {
+                    L = P.seq_lens[b];
+                    const uint32_t k = units_of(L, P.max_len);
+                    if (u0 < from + k) break;
+                    from += k;
+                }
+                start = make_int4(b, L, (int)(u0 - from) * kUnit, (int)(u1 - u0));
+            }
+            P.starts[g] = start;
         }
         return;
     }
@@ -424,51 +458,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             prefetch_tensormap(&maps.v[k]);
         }
     }
-    // ---- this CTA's share: threads hold consecutive requests; units before each of them
-    const int per = (a.B + kThreads - 1) / kThreads;
-    {
-        const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
-        int inc = 0;
-        for (int b = b0; b < b1; ++b) inc += units_of(a.seq_lens[b], a.max_len);
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, inc, o);
-            if (lane >= o) inc += v;
-        }
-        bar.upto[tid] = inc;
-    }
-    __syncthreads();
+    pdl_wait();  // (the operands' kernel is short: it is done by now)
     Walk w;
     {
-        // warps' sums, then the thread whose requests hold the first unit (whole warp)
-        constexpr int kWarps = kThreads / 32;
-        int sum = lane < kWarps ? bar.upto[32 * lane + 31] : 0;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, sum, o);
-            if (lane >= o) sum += v;
-        }
-        // (at most 2^24 units; CTAs past the last unit have none, so that no request's CTAs
-        // have a gap)
-        const uint32_t total = __shfl_sync(0xffffffffu, sum, 31);
-        const uint32_t ctas = max(1u, min(gridDim.x, total)), g = min(blockIdx.x, ctas);
-        const uint32_t u0 = total * g / ctas, u1 = min(total, total * (g + 1) / ctas);
-        w.left = (int)(u1 - u0);
-        if (w.left > 0) {
-            const int wp = __popc(__ballot_sync(0xffffffffu, (uint32_t)sum <= u0));  // warps that end before it
-            const uint32_t base = __shfl_sync(0xffffffffu, sum, max(wp - 1, 0)) * (wp > 0);
-            const int th = __popc(__ballot_sync(0xffffffffu, base + bar.upto[32 * wp + lane] <= u0));
-            uint32_t at = base + (th > 0 ? bar.upto[32 * wp + th - 1] : 0);
-            w.b = (32 * wp + th) * per;
-            for (;; ++w.b) {
-                w.L = a.seq_lens[w.b];
-                const uint32_t k = units_of(w.L, a.max_len);
-                if (u0 < at + k) break;
-                at += k;
-            }
-            w.tok = (int)(u0 - at) * kUnit;
-        }
+        const int4 start = a.starts[blockIdx.x];
+        w.b = start.x;
+        w.L = start.y;
+        w.tok = start.z;
+        w.left = start.w;
     }
+    __syncthreads();
     bool ok = true;
 
     if (warp >= kWarpCopy) {
@@ -537,7 +536,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else if (warp == kWarpImage) {
             // ================= operand images =================
             if (lane == 0) {
-                pdl_wait();
                 pdl_launch_dependents();  // (the merge reads the places before its own wait)
                 int last = -1;
                 for (; ok && w.live(); w.next(a)) {
@@ -966,6 +964,7 @@ int launch_registers(K *kernel) {
 // Workspace: places of the states, operand images, states of up to B + CTAs pieces.
 struct Ws {
     int2 *places;
+    int4 *starts;
     uint8_t *img;
     int64_t img_stride;
     void *states;
@@ -977,6 +976,8 @@ Ws layout(void *base, const Shape &s, int B, int ctas, int d_h) {
     size_t o = 0;
     w.places = reinterpret_cast<int2 *>(p);
     o += align256(sizeof(int2) * (size_t)B);
+    w.starts = reinterpret_cast<int4 *>(p + o);
+    o += align256(sizeof(int4) * (size_t)ctas);
     w.img = reinterpret_cast<uint8_t *>(p + o);
     w.img_stride = (int64_t)align256(s.img_bytes);
     o += (size_t)B * w.img_stride;
@@ -1039,6 +1040,7 @@ cudaError_t launch_decode_scaled_tc(const ScaledDecodeArgs &d, void *ws) {
     p.img = w.img;
     p.img_stride = w.img_stride;
     p.places = w.places;
+    p.starts = w.starts;
     p.status = d.status;
     p.grid = ctas;
     p.B = d.B;
@@ -1049,6 +1051,7 @@ cudaError_t launch_decode_scaled_tc(const ScaledDecodeArgs &d, void *ws) {
     a.c = c;
     a.seq_lens = d.seq_lens;
     a.page_table = d.page_table;
+    a.starts = w.starts;
     a.img = w.img;
     a.img_stride = w.img_stride;
     a.st = scaled_states(w.states, (int64_t)d.B + ctas, c.H);
