@@ -502,7 +502,8 @@ LRKV_API int lrkv_prefill_window(const void *X, const void *Q, const int32_t *cu
  * bf16.  On tensor cores (d_h = 128, G = 1, H a multiple of 4 up to 32, r up to 64,
  * and what of it fits in tensor memory) the codes are multiplied as
  * they are: q, q B_K[h] and the weights enter as sums of two or three E4M3 terms
- * (at least bf16's precision), and the scales are applied to the sums.  Rows
+ * (at least bf16's precision; a weight below 2^-126 of the largest counts as
+ * zero), and the scales are applied to the sums.  Rows
  * that a query sees must hold no NaN code there: a NaN reaches other heads of
  * the request.  What pages hold past a request's length never matters.
  * Workspace: lrkv_decode_scaled_workspace_bytes bytes; that never falls as B or
@@ -514,7 +515,9 @@ LRKV_API int lrkv_prefill_window(const void *X, const void *Q, const int32_t *cu
  * quantised), as lrkv_prefill.  max_ctx: host upper bound of start_pos[b] + rows of b.
  * Where lrkv_prefill runs its tiled kernel on a bf16 cache of these sizes, the
  * values are laid out in bf16 in the workspace and that kernel runs; other
- * sizes run one decode a row.
+ * sizes run one decode a row.  A row without a place is flagged as by the append,
+ * its output zero; rows past max_ctx are written, not attended (of the tiled
+ * kernel: query tiles past it), and flagged LRKV_STATUS_BAD_SEQLEN.
  *
  * Workspaces are 256-byte aligned device memory, scratch, without
  * initialisation; one per call in flight.

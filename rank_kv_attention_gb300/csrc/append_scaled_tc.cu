@@ -101,11 +101,13 @@ struct Tiles {
         per = (a.rows.B + 31) / 32;
         const int b0 = min(a.rows.B, lane * per), b1 = min(a.rows.B, b0 + per);
         upto = 0;
-        for (int b = b0; b < b1; ++b) upto += span_of(a, b, speaks).tiles();
+        // (requests that do not overlap have far fewer than 2^29 tiles; others stop there)
+        constexpr int kMost = 1 << 29;
+        for (int b = b0; b < b1; ++b) upto = min(upto + span_of(a, b, speaks).tiles(), kMost);
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int v = __shfl_up_sync(0xffffffffu, upto, o);
-            if (lane >= o) upto += v;
+            if (lane >= o) upto = min(upto + v, kMost);
         }
         total = __shfl_sync(0xffffffffu, upto, 31);
     }

@@ -356,8 +356,8 @@ __global__ void __launch_bounds__(128) scaled_prep_kernel(const __grid_constant_
         red[4 + warp] = mp;
     }
     const bool bad = __syncthreads_or(odd);
-    const int eq = bad ? 0 : needed_exp(fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])));
-    const int ep = bad ? 0 : needed_exp(fmaxf(fmaxf(red[4], red[5]), fmaxf(red[6], red[7])));
+    const int eq = bad ? 0 : needed_exp(fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])), 120);
+    const int ep = bad ? 0 : needed_exp(fmaxf(fmaxf(red[4], red[5]), fmaxf(red[6], red[7])), 120);
     uint8_t *img = P.img + b * P.img_stride;
     {
         float x = bad ? 0.f : qs[tid] * exp2i(-eq);

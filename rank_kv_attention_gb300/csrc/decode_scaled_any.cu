@@ -221,7 +221,8 @@ __global__ void __launch_bounds__(THREADS, HELD == 4 ? 6 : 2) scaled_merge_kerne
         const int32_t L = P.seq_lens[b];
         if (L == -1 && P.leave) return;
         if (L < 1 || L > P.max_len) {
-            if (h == 0 && tid == 0) status_or(P.status, LRKV_STATUS_BAD_SEQLEN);
+            // (of a prefill's rows the append and scaled_row_queries_kernel have said it)
+            if (h == 0 && tid == 0 && !P.leave) status_or(P.status, LRKV_STATUS_BAD_SEQLEN);
             place.y = 0;
         }
     }
@@ -309,8 +310,8 @@ __global__ void __launch_bounds__(THREADS, HELD == 4 ? 6 : 2) scaled_merge_kerne
     }
 }
 
-__global__ void scaled_row_queries_kernel(const __grid_constant__ ScaledRows rows, int max_len, int32_t *len,
-                                          int32_t *req_row) {
+__global__ void scaled_row_queries_kernel(const __grid_constant__ ScaledRows rows, int page_size, int max_len,
+                                          int32_t *len, int32_t *req_row) {
     pdl_wait();
     pdl_launch_dependents();
     const int i = blockIdx.x * blockDim.x + threadIdx.x;
@@ -327,6 +328,8 @@ __global__ void scaled_row_queries_kernel(const __grid_constant__ ScaledRows row
         return;
     }
     const int64_t pos = (int64_t)rows.start_pos[lo] + (i - rows.cu_rows[lo]);
+    // (a row that has no place in the table was flagged as it was not written)
+    if (pos >= max_len && pos < (int64_t)rows.max_pages * page_size) status_or(rows.status, LRKV_STATUS_BAD_SEQLEN);
     len[i] = pos >= 0 && pos < max_len ? (int)pos + 1 : 0;
     req_row[i] = lo;
 }
@@ -373,9 +376,10 @@ cudaError_t launch_decode_scaled_any(const ScaledDecodeArgs &a, void *ws) {
     return launch_scaled_merge(m, a.stream);
 }
 
-cudaError_t launch_scaled_row_queries(const ScaledRows &rows, int max_len, int32_t *len, int32_t *req_row,
-                                      cudaStream_t s) {
-    return launch_pdl(scaled_row_queries_kernel, dim3((rows.n + 255) / 256), dim3(256), 0, s, rows, max_len, len, req_row);
+cudaError_t launch_scaled_row_queries(const ScaledRows &rows, int page_size, int max_len, int32_t *len,
+                                      int32_t *req_row, cudaStream_t s) {
+    return launch_pdl(scaled_row_queries_kernel, dim3((rows.n + 255) / 256), dim3(256), 0, s, rows, page_size, max_len, len,
+                      req_row);
 }
 
 cudaError_t launch_scaled_merge(const ScaledMergeArgs &m, cudaStream_t s) {

@@ -387,7 +387,7 @@ int lrkv_prefill_scaled(const void *X, const void *Q, const int32_t *cu_rows, co
         prof_after(LRKV_PROFILE_ATTENTION, s);
         return rc == 0 ? LRKV_OK : cuda_fail(rc < 0 ? (cudaError_t)(-rc) : cudaErrorInvalidValue);
     }
-    e = launch_scaled_row_queries(rows, max_ctx, w.len, w.req_row, s);
+    e = launch_scaled_row_queries(rows, c.page_size, max_ctx, w.len, w.req_row, s);
     if (e != cudaSuccess) return cuda_fail(e);
     ScaledDecodeArgs a;
     a.c = c;

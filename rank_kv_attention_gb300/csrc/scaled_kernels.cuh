@@ -62,8 +62,8 @@ cudaError_t launch_expand_scaled(const ScaledExpandArgs &a);
 
 // What a one-query decode of every row of a call needs: its length (0: no valid position; -1: no request owns the row) and
 // page-table row.
-cudaError_t launch_scaled_row_queries(const ScaledRows &rows, int max_len, int32_t *len, int32_t *req_row,
-                                      cudaStream_t s);
+cudaError_t launch_scaled_row_queries(const ScaledRows &rows, int page_size, int max_len, int32_t *len,
+                                      int32_t *req_row, cudaStream_t s);
 
 struct ScaledDecodeArgs {
     ScaledPools c;
@@ -140,11 +140,12 @@ cudaError_t launch_append_scaled_tc(const ScaledAppendArgs &p);
 __device__ __forceinline__ int clamp_exp(int byte) {
     return min(max(byte - 127, LRKV_SCALED_MIN_EXP), LRKV_SCALED_MAX_EXP);
 }
-// Least exponent e with |x| <= 448 * 2^e (448 = 1.75 * 2^8), in range; x >= 0 finite.
-__device__ __forceinline__ int needed_exp(float x) {
+// Least exponent e with |x| <= 448 * 2^e (448 = 1.75 * 2^8), in [LRKV_SCALED_MIN_EXP, most];
+// x >= 0 finite (of the largest x it is 120).
+__device__ __forceinline__ int needed_exp(float x, int most = LRKV_SCALED_MAX_EXP) {
     const uint32_t u = __float_as_uint(x);
     const int e = (int)(u >> 23) - 135 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
-    return min(max(e, LRKV_SCALED_MIN_EXP), LRKV_SCALED_MAX_EXP);
+    return min(max(e, LRKV_SCALED_MIN_EXP), most);
 }
 
 // Four codes times s, rounded to codes again.

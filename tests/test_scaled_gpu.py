@@ -686,3 +686,238 @@ def test_written_rows_attend_like_a_bf16_cache_of_their_values():
     for b in range(2):
         _, bound = reference(q[1][b], cache, B_K[1], B_V[1], table[b], int(lens[b]))
         assert np.all(np.abs(host(out, "bf16")[b] - want[b]) <= 2 * bound)
+
+
+# ---------------------------------------------------------------------------
+# Ends of the ranges
+# ---------------------------------------------------------------------------
+MORE = [(8, 128, 64, 4, 128, 64, 128), (16, 128, 8, 1, 64, 64, 64), (4, 128, 40, 2, 128, 128, 64), (6, 128, 128, 1, 64, 16, 64),
+        (4, 128, 16, 1, 256, 256, 64), (8, 128, 24, 1, 64, 32, 72)]
+
+
+@pytest.mark.parametrize("rows_of", [[1, 0, 2], [70, 1, 200]])
+@pytest.mark.parametrize("H,d_h,r,G,ps,block,d", MORE)
+def test_append_and_prefill_of_more_shapes(H, d_h, r, G, ps, block, d, rows_of):
+    """Groups of wide heads, narrow and wide private rows, blocks of a page, widths that the projection on tensor cores
+    does not take."""
+    test_append(H, d_h, r, G, ps, block, d, rows_of)
+    test_prefill(H, d_h, r, G, ps, block, d, rows_of, [ps - 3, 0, block + 3])
+
+
+@pytest.mark.parametrize("H,d_h,r,ps", [(16, 128, 48, 64), (4, 32, 8, 32)])
+def test_append_and_prefill_of_rows_that_have_no_place(H, d_h, r, ps):
+    """Negative positions, rows past the table, pages outside the pool: skipped and flagged; the other rows are written and
+    attended as ever."""
+    import rank_kv_attention_gb300 as L
+    rng = np.random.default_rng(40)
+    d, B, width = 64, 4, 4
+    cache = random_cache(rng, 14, ps, H, d_h, r, 16, loud=1)
+    table = np.array([[0, 1, 2, -1], [3, 4, 5, 6], [7, 14, 8, 9], [10, 11, -5, 12]], np.int32)
+    cu, start = np.array([2, 72, 152, 222, 292]), np.array([-9, width * ps - 30, 20, 30])
+    n = 300
+    w, x, q = weights(rng, d, H, d_h, r, 1), bf16(rng, (n, d)), bf16(rng, (n, H, d_h))
+    B_K, B_V = bf16(rng, (H, d_h, r), r ** -0.5), bf16(rng, (H, d_h, r), r ** -0.5)
+    args = (dev(cu, "i32"), dev(start, "i32"))
+    before = cache.copy()
+    for prefill in (False, True):
+        dc, st = to_device(before), status()
+        if prefill:
+            out = L.prefill_scaled(dev(x[0], "bf16"), dev(q[0], "bf16"), *args, width * ps, *[dev(w[m][0], "bf16") for m in w],
+                                   dev(B_K[0], "bf16"), dev(B_V[0], "bf16"), dc, dev(table, "i32"), status=st)
+        else:
+            L.append_scaled(dev(x[0], "bf16"), *args, *[dev(w[m][0], "bf16") for m in w], dc, dev(table, "i32"), status=st)
+        assert int(st) == BAD_ROW | BAD_PAGE
+        want = before.copy()
+        S.write(want, projected(x[1], w), cu, start, table)
+        held = to_host(dc, cache)
+        close_caches(held, want, None, cu, start, table, d)
+    got = host(out, "bf16")
+    for b, i in ((0, 9), (0, 69), (1, 0), (1, 29), (2, 69), (3, 69)):
+        ref, bound = reference(q[1][cu[b] + i], held, B_K[1], B_V[1], table[b], int(start[b]) + i + 1, d_h == 128)
+        check(got[cu[b] + i], ref, bound, f"request {b} row {i}")
+
+
+@pytest.mark.parametrize("H,d_h,r,ps", [(16, 128, 48, 64), (4, 32, 8, 32)])
+def test_a_prefill_past_max_ctx_is_flagged(H, d_h, r, ps):
+    """Rows from max_ctx on (of the tiled kernel: query tiles) are written, not attended, and flagged."""
+    import rank_kv_attention_gb300 as L
+    rng = np.random.default_rng(48)
+    d, n = 64, 300
+    cache = random_cache(rng, 12, ps, H, d_h, r, 16, loud=1)
+    dc, table, st = to_device(cache), np.arange(12, dtype=np.int32)[None], status()
+    w, x, q = weights(rng, d, H, d_h, r, 1), bf16(rng, (n, d)), bf16(rng, (n, H, d_h))
+    B = dev(bf16(rng, (H, d_h, r), r ** -0.5)[0], "bf16")
+    L.prefill_scaled(dev(x[0], "bf16"), dev(q[0], "bf16"), dev(np.array([0, n]), "i32"), dev(np.zeros(1), "i32"), 128,
+                     *[dev(w[m][0], "bf16") for m in w], B, B, dc, dev(table, "i32"), status=st)
+    assert int(st) & BAD_SEQLEN
+    S.write(cache, projected(x[1], w), [0, n], [0], table)
+    close_caches(to_host(dc, cache), cache, None, [0, n], [0], table, d)
+
+
+@pytest.mark.parametrize("H,d_h,r,ps", [(16, 128, 48, 64), (4, 32, 8, 32)])
+def test_append_and_prefill_without_order_do_no_harm(H, d_h, r, ps):
+    """cu_rows that fall or run past n: no row is read or written outside the call's, and the next call is right."""
+    import rank_kv_attention_gb300 as L
+    rng = np.random.default_rng(41)
+    d, n = 64, 150
+    cache = random_cache(rng, 16, ps, H, d_h, r, 16, loud=1)
+    dc, table = to_device(cache), np.arange(16, dtype=np.int32).reshape(4, 4)
+    w, x, q = weights(rng, d, H, d_h, r, 1), bf16(rng, (n, d)), bf16(rng, (n, H, d_h))
+    dw, B = [dev(w[m][0], "bf16") for m in w], dev(bf16(rng, (H, d_h, r), r ** -0.5)[0], "bf16")
+    dx, dq, dt, zero = dev(x[0], "bf16"), dev(q[0], "bf16"), dev(table, "i32"), dev(np.zeros(4), "i32")
+    for cu in ([0, 90, 40, 100, 900], [-50, 4, 3, 2, 1], [400, 500, 600, 700, 800], [2 ** 31 - 1, -2 ** 31, 7, 80, 2 ** 31 - 1],
+               [0, 0, 0, 0, 0]):
+        dcu = dev(np.array(cu), "i32")
+        L.append_scaled(dx, dcu, zero, *dw, dc, dt)
+        L.prefill_scaled(dx, dq, dcu, zero, 4 * ps, *dw, B, B, dc, dt)
+        L.prefill_scaled(dx, dq, dcu, zero, 20, *dw, B, B, dc, dt)          # (rows past max_ctx)
+    torch.cuda.synchronize()
+    cache, cu = to_host(dc, cache), [0, 40, 90, 100, 150]
+    L.append_scaled(dx, dev(np.array(cu), "i32"), zero, *dw, dc, dt)
+    S.write(cache, projected(x[1], w), cu, [0] * 4, table)
+    close_caches(to_host(dc, cache), cache, None, cu, [0] * 4, table, d)
+
+
+@pytest.mark.parametrize("d,rows", [(64, 100), (72, 20)])
+def test_append_of_values_that_are_not_finite(d, rows):
+    """A row of X with an infinity or a NaN: NaN or infinite sums become NaN codes, the block's other rows decide its scale."""
+    import rank_kv_attention_gb300 as L
+    rng = np.random.default_rng(42)
+    H, d_h, r, ps = 16, 128, 48, 64
+    cache = random_cache(rng, 3, ps, H, d_h, r, 32)
+    dc, table = to_device(cache), np.array([[1, 0, 2]], np.int32)
+    w, (bits, x) = weights(rng, d, H, d_h, r, 1), bf16(rng, (rows, d))
+    for i, v, b in ((3, np.nan, I.BF16_NAN_BITS), (7, np.inf, 0x7f80), (rows - 1, -np.inf, 0xff80)):
+        x[i, i % d], bits[i, i % d] = v, b
+    L.append_scaled(dev(bits, "bf16"), dev(np.array([0, rows]), "i32"), dev(np.array([5]), "i32"),
+                    *[dev(w[m][0], "bf16") for m in w], dc, dev(table, "i32"))
+    with np.errstate(invalid="ignore"):
+        y = projected(x, w)
+    for k in POOLS:
+        assert not np.isfinite(y[k][[3, 7, rows - 1]]).any()
+    S.write(cache, y, [0, rows], [5], table)
+    held = to_host(dc, cache)
+    for c in (held, cache):      # (NaN codes in the same places, then compared as zeros)
+        for k in POOLS:
+            nan = (c.codes[k] & 0x7f) == 0x7f
+            for i in (3, 7, rows - 1):
+                assert nan[table[0, (5 + i) // ps], (5 + i) % ps].all()
+            assert nan.sum() == 3 * nan[0, 0].size
+            c.codes[k] = np.where(nan, 0, c.codes[k])
+    close_caches(held, cache, None, [0, rows], [5], table, d)
+
+
+@pytest.mark.parametrize("H,d_h,r", [(16, 128, 48), (4, 32, 8)])
+def test_decode_of_the_largest_queries(H, d_h, r):
+    """Elements at the end of bf16's range against the smallest keys: scores of ordinary size."""
+    rng = np.random.default_rng(43)
+    lens = [200, 64]
+    cache, table, q, B_K, B_V = decode_case(rng, lens, H, d_h, r, 64, 32)
+    for k in ("S_K", "R_K"):
+        cache.codes[k] = (rng.integers(0, 8, cache.codes[k].shape) | (rng.integers(0, 2, cache.codes[k].shape) << 7)).astype(np.uint8)
+        cache.exps[k][:] = 10
+    x = np.zeros((2, H, d_h), np.float32)
+    x[:, :, 5], x[:, :, 9] = 3.38e38, -3e38
+    bits = I.f32_to_bf16_bits(x)
+    bk = B_K[1].copy()
+    bk[:, [5, 9]] = np.clip(bk[:, [5, 9]], -0.45, 0.45)    # (p stays finite)
+    bkb = I.f32_to_bf16_bits(bk.astype(np.float32))
+    q, B_K = (bits, I.bf16_bits_to_f64(bits)), (bkb, I.bf16_bits_to_f64(bkb))
+    check_decode(run_decode(cache, table, q, B_K, B_V, lens), cache, table, q, B_K, B_V, lens)
+
+
+def test_decode_reads_a_page_twice_and_shares_pages():
+    """A table that names a page twice, and requests on the same pages: read as often as named."""
+    rng = np.random.default_rng(44)
+    lens = [250, 128, 70]
+    cache, table, q, B_K, B_V = decode_case(rng, lens, 16, 128, 48, 64, 16)
+    table[0, 2], table[1], table[2, 0] = table[0, 0], table[0], table[0, 3]
+    check_decode(run_decode(cache, table, q, B_K, B_V, lens), cache, table, q, B_K, B_V, lens)
+
+
+@pytest.mark.parametrize("H,r", [(16, 48), (32, 16)])
+def test_decode_of_thousands_of_requests(H, r):
+    """More requests than a launch's threads, of one row or none."""
+    rng = np.random.default_rng(45)
+    B, cache = 5000, random_cache(rng, 8, 64, H, 128, r, 64)
+    lens = rng.choice([0, 1, 1, 2, 64], B)
+    lens[:300], lens[-1] = 0, 64
+    table = rng.integers(0, 8, (B, 1)).astype(np.int32)
+    q, B_K, B_V = bf16(rng, (B, H, 128)), bf16(rng, (H, 128, r), r ** -0.5), bf16(rng, (H, 128, r), r ** -0.5)
+    st = status()
+    out = run_decode(cache, table, q, B_K, B_V, lens, status=st)
+    assert int(st) == BAD_SEQLEN
+    assert not host(out, "bf16")[lens == 0].any()
+    which = [b for b in list(range(300, B, 211)) + [B - 1] if lens[b]]
+    check_decode(out, cache, table, q, B_K, B_V, lens, which=which)
+
+
+def test_a_prefill_captured_in_a_graph_and_on_a_stream():
+    """One graph of a prefill, replayed for other rows, counts and positions, with rows to spare; the same calls on a
+    stream of their own give the same."""
+    import rank_kv_attention_gb300 as L
+    rng = np.random.default_rng(46)
+    s = Server(rng, pages=40, max_pages=8)
+    table = np.array([rng.permutation(40)[:24].reshape(3, 8)], np.int32)[0]
+    dt, n = dev(table, "i32"), 160
+    x, q = (torch.zeros(n, k, dtype=torch.bfloat16, device="cuda") for k in (s.d, 16 * 128))
+    q = q.view(n, 16, 128)
+    cu, at = dev(np.array([0, 0, 0, 0]), "i32"), dev(np.zeros(3), "i32")
+    ws = L.api.workspace(L.prefill_scaled_workspace_bytes(s.cache, 3, n, 512))
+    out, side = torch.empty(n, 16, 128, dtype=torch.bfloat16, device="cuda"), torch.cuda.Stream()
+
+    def call(cache, **kw):
+        return L.prefill_scaled(x, q, cu, at, 512, *s.dw, *s.dB, cache, dt, **kw)
+    with torch.cuda.stream(side):
+        call(s.cache, out=out, ws=ws)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call(s.cache, out=out, ws=ws)
+    for counts, start in (([100, 1, 30], [0, 63, 200]), ([0, 160, 0], [9, 300, 9]), ([50, 50, 50], [100, 0, 230])):
+        xb, qb = bf16(rng, (n, s.d)), bf16(rng, (n, 16, 128))
+        x.copy_(dev(xb[0], "bf16"))
+        q.copy_(dev(qb[0], "bf16"))
+        cu.copy_(dev(np.concatenate([[0], np.cumsum(counts)]), "i32"))
+        at.copy_(dev(np.array(start), "i32"))
+        other = to_device(to_host(s.cache, s.oracle))
+        torch.cuda.synchronize()
+        g.replay()
+        alone = call(other, stream=side)
+        torch.cuda.synchronize()
+        rows = sum(counts)
+        assert torch.equal(out[:rows], alone[:rows])
+        held = to_host(s.cache, s.oracle)
+        assert_same(to_host(other, s.oracle), held)
+        got, c = host(out, "bf16"), np.concatenate([[0], np.cumsum(counts)])
+        for b in range(3):
+            for i in {0, counts[b] - 1} if counts[b] else ():
+                ref, bound = reference(qb[1][c[b] + i], held, s.B_K[1], s.B_V[1], table[b], start[b] + i + 1, True)
+                check(got[c[b] + i], ref, bound)
+
+
+def test_writes_and_reads_on_other_streams():
+    """Rows written on one stream and read on another after it, beside an append into a second cache."""
+    import rank_kv_attention_gb300 as L
+    rng = np.random.default_rng(47)
+    H, d_h, r, ps, d, n = 16, 128, 48, 64, 64, 300
+    caches = [random_cache(rng, 6, ps, H, d_h, r, 32) for _ in range(2)]
+    dcs, table, w = [to_device(c) for c in caches], np.arange(6, dtype=np.int32)[None], weights(rng, d, H, d_h, r, 1)
+    rows, x = values(rng, n, H, d_h, r, 1, "bf16"), bf16(rng, (n, d))
+    dw, cu, at, dt, dx = [dev(w[m][0], "bf16") for m in w], dev(np.array([0, n]), "i32"), dev(np.zeros(1), "i32"), dev(table, "i32"), \
+        dev(x[0], "bf16")
+    a, b, c = (torch.cuda.Stream() for _ in range(3))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        L.append_scaled(dx, cu, at, *dw, dcs[1], dt, stream=b)
+        L.write_scaled(*[rows[k][0].reshape(n, -1) for k in POOLS], cu, at, dcs[0], dt, stream=a)
+    c.wait_stream(a)
+    got = L.read_scaled(cu, at, n, dcs[0], dt, dtype=torch.float32, stream=c)
+    torch.cuda.synchronize()
+    S.write(caches[0], {k: rows[k][1] for k in POOLS}, [0, n], [0], table)
+    S.write(caches[1], projected(x[1], w), [0, n], [0], table)
+    assert_same(to_host(dcs[0], caches[0]), caches[0])
+    close_caches(to_host(dcs[1], caches[1]), caches[1], None, [0, n], [0], table, d)
+    for k, t in zip(POOLS, got):
+        want = S.read(caches[0], k, [0, n], [0], table, np.zeros((n,) + shape_of(k, H, d_h, r, 1)))
+        assert np.array_equal(host(t, "f32").reshape(want.shape), want)
