@@ -517,7 +517,8 @@ LRKV_API int lrkv_prefill_window(const void *X, const void *Q, const int32_t *cu
  * values are laid out in bf16 in the workspace and that kernel runs; other
  * sizes run one decode a row.  A row without a place is flagged as by the append,
  * its output zero; rows past max_ctx are written, not attended (of the tiled
- * kernel: query tiles past it), and flagged LRKV_STATUS_BAD_SEQLEN.
+ * kernel: tiles of 128 rows from the request's first on, past its max_ctx-th row),
+ * and flagged LRKV_STATUS_BAD_SEQLEN (their outputs stay, or become zero).
  *
  * Workspaces are 256-byte aligned device memory, scratch, without
  * initialisation; one per call in flight.

@@ -127,6 +127,9 @@ struct PrefillTcArgs {
     // kernel launch after passing its own wait and finishes within a few
     // milliseconds: only the copies of tiles that may hold new rows wait for it.
     bool early = false;
+    // Query tiles that leave half of the SMs idle may have two CTAs each (no window); the
+    // sums are then added up in another order.
+    bool split = false;
 };
 int launch_prefill_tc(const PrefillTcArgs &p);
 // Whether it covers this call.

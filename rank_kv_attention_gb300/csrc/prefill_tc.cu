@@ -63,10 +63,17 @@
 // Of several requests one may see a history that another's new rows make (a prefix
 // that they share), so every copy of keys and values waits; what goes before (the
 // queries, p) still overlaps.
+//
+// SPLIT (block-scaled prefill whose query tiles leave half of the SMs idle): a cluster of
+// two CTAs takes a query tile, the second the first half of its key tiles.  It hands its
+// sums (O, running maximum and sum, fp32) over through the first one's shared memory,
+// the value stages that are free by then, and the first goes on as one that had seen
+// all keys.  512 rows behind 3001, 16 heads, r = 48 (64 query tiles; the call with its
+// append): 50.1 us, 58.9 with one CTA a tile.
 #include <algorithm>
 
 #include "append_kernels.cuh"
-#include "tc_common.cuh"
+#include "tc_pair.cuh"
 
 namespace lrkv {
 
@@ -96,6 +103,7 @@ struct PfBars {
     uint64_t k_full[2], v_full[2];
     uint64_t s_full[2], p_full[2], pv_done[2];
     uint64_t pair[4];  // per lane quadrant: both softmax warps posted their half (64 arrivals)
+    uint64_t peer, handed;  // SPLIT: the first CTA's stages are free; the second's sums are in them
     uint64_t out_ready;  // all 256 softmax threads staged their output row halves
     uint32_t tmem;
 };
@@ -119,12 +127,15 @@ struct PfArgs {
     bool early;
 };
 
+// SPLIT: a query tile of fewer key tiles is one CTA's
+constexpr int kPfSplitTiles = 4;
+
 // Key tiles that the rows of one CTA visit, in order: tiles 0 .. ns-1 hold the
 // sinks, tiles kt0 .. the rows from `lo` (the first row of the window of the
 // CTA's first query) on.  ns <= kt0; without a window everything from tile 0.
 template <bool WIN>
 struct KeyTiles {
-    int lo, ns, kt0, count;
+    int lo, ns, kt0, count, from = 0;  // from: the CTA's first (no window)
     __device__ __forceinline__ KeyTiles(const PfArgs &a, int min_p, int max_p) {
         lo = WIN ? max(0, min_p - a.window + 1) : 0;
         kt0 = lo / PF_BN;
@@ -133,7 +144,7 @@ struct KeyTiles {
     }
     // position of the first key of the kt-th visited tile
     __device__ __forceinline__ int base(int kt) const {
-        return (!WIN ? kt : kt < ns ? kt : kt - ns + kt0) * PF_BN;
+        return (!WIN ? kt + from : kt < ns ? kt : kt - ns + kt0) * PF_BN;
     }
     // whether no row of the CTA sees any of keys key0 .. key0 + 63 (lower end)
     __device__ __forceinline__ bool dead(const PfArgs &a, int key0) const {
@@ -192,13 +203,42 @@ __device__ __forceinline__ bool elect_one() {
     return p != 0;
 }
 
+// Arrive on an mbarrier of another CTA of the cluster, this thread's writes to its shared
+// memory before.
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cl_addr) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cl_addr) : "memory");
+}
+// Wait on this CTA's mbarrier for such arrivals (2 s bound as mbar_wait).
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t parity) {
+    const uint32_t a = smem_u32(bar);
+    const uint64_t t0 = globaltimer_ns();
+    for (uint32_t it = 0;; ++it) {
+        uint32_t ok;
+        asm volatile(
+            "{ .reg .pred p; mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+            : "=r"(ok)
+            : "r"(a), "r"(parity)
+            : "memory");
+        if (ok) return true;
+        if ((it & 255u) == 255u && globaltimer_ns() - t0 > 2000000000ull) return false;
+    }
+}
+// Four (two) words into another CTA's shared memory (aligned shared::cluster address).
+__device__ __forceinline__ void st_cluster4(uint32_t cl_addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+    asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(cl_addr), "r"(x), "r"(y), "r"(z), "r"(w)
+                 : "memory");
+}
+__device__ __forceinline__ void st_cluster2(uint32_t cl_addr, uint32_t x, uint32_t y) {
+    asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(cl_addr), "r"(x), "r"(y) : "memory");
+}
+
 // x -> (hi, lo) with hi = bf16(x), lo = bf16(x - hi), packed in pairs.
 __device__ __forceinline__ void split_pack(float x0, float x1, uint32_t &hi, uint32_t &lo) {
     hi = pack_bf16(x0, x1);
     lo = pack_bf16(x0 - bf16lo(hi), x1 - bf16hi(hi));
 }
 
-template <int R16, bool WIN>
+template <int R16, bool WIN, bool SPLIT>
 __global__ void __launch_bounds__(PF_THREADS, 1)
     prefill_tc_kernel(const __grid_constant__ PfMaps maps, const PfArgs a) {
     constexpr int NPV = 128 + 16 * R16;  // value columns [S_V | R_V[h] (padded)]
@@ -208,7 +248,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
     PfBars &bar = *reinterpret_cast<PfBars *>(smem + PF_OFF_BAR);
     uint16_t *red = reinterpret_cast<uint16_t *>(smem + PF_OFF_RED);  // [slot][half][row]
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int h = blockIdx.x, b = blockIdx.y, tq = a.n_qtiles - 1 - (int)blockIdx.z;
+    const int h = SPLIT ? blockIdx.x >> 1 : blockIdx.x, b = blockIdx.y, tq = a.n_qtiles - 1 - (int)blockIdx.z;
 
     if (tid == 256) {
         // (initialised by the thread that issues the first copies)
@@ -229,6 +269,10 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
         mbar_init(&bar.ex_ready, 2 * PF_BM);
         for (int k = 0; k < 4; ++k) mbar_init(&bar.pair[k], 64);
         mbar_init(&bar.out_ready, 2 * PF_BM);
+        if (SPLIT) {
+            mbar_init(&bar.peer, 2 * PF_BM);
+            mbar_init(&bar.handed, 2 * PF_BM);
+        }
         fence_barrier_init();
         prefetch_tensormap(&maps.q);
         prefetch_tensormap(&maps.sk);
@@ -265,7 +309,17 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
         return;
     }
     const int max_p = p0 + t_hi - 1;  // last key position any row sees
-    const KeyTiles<WIN> keys(a, p0 + t_lo, max_p);
+    KeyTiles<WIN> keys(a, p0 + t_lo, max_p);
+    // the same in both CTAs of a cluster: whether they share the tiles, and this one's
+    const bool shared = SPLIT && keys.count >= kPfSplitTiles, second = SPLIT && (blockIdx.x & 1);
+    if (SPLIT) {
+        if (second && !shared) return;
+        if (shared) {
+            const int cut = keys.count / 2;
+            keys.from = second ? 0 : cut;
+            keys.count = second ? cut : keys.count - cut;
+        }
+    }
     const int nkt = keys.count;
 
     const int32_t *pt_row = a.page_table + (size_t)b * a.max_pages;
@@ -316,7 +370,8 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
         tmem_alloc(&bar.tmem, PF_TMEM_COLS);
     }
     tc_fence_before();
-    __syncthreads();
+    if (shared) cluster_sync_all();  // (both CTAs' barriers are there before either arrives at the other's)
+    else __syncthreads();
     tc_fence_after();
     const uint32_t tmem = bar.tmem;
 
@@ -359,7 +414,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
             }
             // B_V[h] (K-major for the expansion) into the key stage tile nkt would use
             bool bv_issued = false;
-            if (kprod && ok) {
+            if (kprod && ok && !second) {
                 const int st = nkt & 1;
                 if (nkt >= 2 && !mbar_wait(&bar.s_full[st], ((nkt >> 1) - 1) & 1)) {
                     ok = false;
@@ -470,8 +525,8 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
                 tc_commit(&bar.pv_done[st]);
             }
             // E = (O_R / l)_hi B_V[h]^T + (O_R / l)_lo B_V[h]^T into score buffer 0
-            if (ok) ok = mbar_wait(&bar.ex_ready, 0) && mbar_wait(&bar.bv_full, 0);
-            if (ok) {
+            if (ok && !second) ok = mbar_wait(&bar.ex_ready, 0) && mbar_wait(&bar.bv_full, 0);
+            if (ok && !second) {
                 tc_fence_after();
                 const uint32_t bv = sw128_desc_lo(base + PF_OFF_K + (nkt & 1) * PF_STAGE, 16);
 #pragma unroll
@@ -655,9 +710,58 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
         if (ok) ok = pair_exchange();
         if (ok)
             ok = __all_sync(0xffffffffu, mbar_wait(&bar.pv_done[(nkt - 1) & 1], ((nkt - 1) >> 1) & 1));
-        const float lt = l + lsum[(hf ^ 1) * PF_BM + t];
+        float lt = l + lsum[(hf ^ 1) * PF_BM + t];
+        if (shared) {
+            // thread: 96 columns of its row of O, in vectors of four, 256 threads side by side
+            float2 *ml = reinterpret_cast<float2 *>(red);  // (no longer read, like the value stages)
+            if (second) {
+                if (ok) ok = __all_sync(0xffffffffu, mbar_wait_cluster(&bar.peer, 0));
+                if (ok) {
+                    tc_fence_after();
+                    const uint32_t to = mapa_addr(smem_u32(smem + PF_OFF_V), 0) + tid * 16;
+#pragma unroll 1
+                    for (int c = 0; c < 3; ++c) {
+                        uint32_t v[32];
+                        tmem_ld32(lane_base + 96 * hf + 32 * c, v);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            st_cluster4(to + (8 * c + k) * 2 * PF_BM * 16, v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+                    }
+                    if (hf == 0) st_cluster2(mapa_addr(smem_u32(ml + t), 0), __float_as_uint(m), __float_as_uint(lt));
+                    mbar_arrive_cluster(mapa_rank(&bar.handed, 0));
+                }
+            } else {
+                if (ok) {
+                    mbar_arrive_cluster(mapa_rank(&bar.peer, 1));
+                    ok = __all_sync(0xffffffffu, mbar_wait_cluster(&bar.handed, 0));
+                }
+                if (ok) {
+                    tc_fence_after();
+                    const float2 other = ml[t];
+                    const float mx = fmaxf(m, other.x), ref = mx == -INFINITY ? 0.f : mx;
+                    const float f0 = ex2_approx(m - ref), f1 = ex2_approx(other.x - ref);
+                    lt = lt * f0 + other.y * f1;
+                    const float4 *in = reinterpret_cast<const float4 *>(smem + PF_OFF_V) + tid;
+#pragma unroll 1
+                    for (int c = 0; c < 3; ++c) {
+                        uint32_t v[32];
+                        tmem_ld32(lane_base + 96 * hf + 32 * c, v);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const float4 x = in[(8 * c + k) * 2 * PF_BM];
+                            const float y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                v[4 * k + e] = __float_as_uint(__uint_as_float(v[4 * k + e]) * f0 + y[e] * f1);
+                        }
+                        tmem_st32(lane_base + 96 * hf + 32 * c, v);
+                    }
+                    ok = pair_exchange();  // (the row's other half is read below)
+                }
+            }
+        }
         const float inv_l = lt > 0.f || (WIN && lt != 0.f) ? 1.f / lt : 0.f;  // (NaN stays NaN)
-        if (ok) {
+        if (ok && !second) {
             // (O_R / l) in bf16 halves over p's columns: half 0 the high part, half 1 the low part
             tc_fence_after();
             uint32_t v[32], pk[32];
@@ -679,7 +783,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
             mbar_arrive(&bar.ex_ready);
             ok = __all_sync(0xffffffffu, mbar_wait(&bar.ex_done, 0));
         }
-        if (ok) {
+        if (ok && !second) {
             tc_fence_after();
             // a full tile is staged in the q buffer (TMA swizzle layout, half hf
             // holds output columns 64 hf .. 64 hf + 63) and written by two TMA
@@ -726,13 +830,14 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
                     }
                 }
             }
-        } else if (lane == 0) {
+        } else if (!ok && lane == 0) {
             status_or(a.status, LRKV_STATUS_TIMEOUT);
         }
     }
 
     tc_fence_before();
     __syncthreads();
+    if (shared) cluster_sync_all();  // neither CTA leaves while the other may still write to it
     if (warp == 8) {
         tc_fence_after();
         tmem_dealloc(tmem, PF_TMEM_COLS);
@@ -741,12 +846,20 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
 
 template <int R16, bool WIN>
 cudaError_t launch_win(const PfMaps &maps, const PfArgs &a, dim3 grid, cudaStream_t s) {
-    cudaError_t e = smem_limit_once(prefill_tc_kernel<R16, WIN>, PF_SMEM);
+    cudaError_t e = smem_limit_once(prefill_tc_kernel<R16, WIN, false>, PF_SMEM);
     if (e != cudaSuccess) return e;
-    return launch_pdl(prefill_tc_kernel<R16, WIN>, grid, dim3(PF_THREADS), PF_SMEM, s, maps, a);
+    return launch_pdl(prefill_tc_kernel<R16, WIN, false>, grid, dim3(PF_THREADS), PF_SMEM, s, maps, a);
 }
 template <int R16>
-cudaError_t launch_r16(const PfMaps &maps, const PfArgs &a, dim3 grid, cudaStream_t s) {
+cudaError_t launch_split(const PfMaps &maps, const PfArgs &a, dim3 grid, cudaStream_t s) {
+    cudaError_t e = smem_limit_once(prefill_tc_kernel<R16, false, true>, PF_SMEM);
+    if (e != cudaSuccess) return e;
+    grid.x *= 2;
+    return launch_pdl_clusters(prefill_tc_kernel<R16, false, true>, 2, grid, dim3(PF_THREADS), PF_SMEM, s, maps, a);
+}
+template <int R16>
+cudaError_t launch_r16(const PfMaps &maps, const PfArgs &a, dim3 grid, bool split, cudaStream_t s) {
+    if (split) return launch_split<R16>(maps, a, grid, s);
     return a.window ? launch_win<R16, true>(maps, a, grid, s) : launch_win<R16, false>(maps, a, grid, s);
 }
 
@@ -830,12 +943,13 @@ int launch_prefill_tc(const PrefillTcArgs &p) {
     // rows come first and leave at once (in `early` after the append): 64 requests, one
     // of 8192 rows and 63 of one, take 519 us where the 8192 rows alone take 163
     const dim3 grid(c.H, p.B, n_qtiles);
+    const bool split = p.split && !a.window && 2 * (int64_t)c.H * p.B * n_qtiles <= device_sm_count();
     cudaError_t e;
     switch ((c.r + 15) / 16) {
-        case 1: e = launch_r16<1>(maps, a, grid, p.stream); break;
-        case 2: e = launch_r16<2>(maps, a, grid, p.stream); break;
-        case 3: e = launch_r16<3>(maps, a, grid, p.stream); break;
-        default: e = launch_r16<4>(maps, a, grid, p.stream); break;
+        case 1: e = launch_r16<1>(maps, a, grid, split, p.stream); break;
+        case 2: e = launch_r16<2>(maps, a, grid, split, p.stream); break;
+        case 3: e = launch_r16<3>(maps, a, grid, split, p.stream); break;
+        default: e = launch_r16<4>(maps, a, grid, split, p.stream); break;
     }
     return e == cudaSuccess ? 0 : -(int)e;
 }

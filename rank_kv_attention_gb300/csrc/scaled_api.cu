@@ -364,6 +364,7 @@ int lrkv_prefill_scaled(const void *X, const void *Q, const int32_t *cu_rows, co
         p.out = out;
         p.status = dev_status;
         p.stream = s;
+        p.split = true;
         if (!prefill_tc_fits(p)) return LRKV_E_SHAPE;  // (more than 65535 heads, requests or query tiles)
     }
     // (the append in one kernel lays its own rows' values out)

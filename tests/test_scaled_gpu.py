@@ -549,6 +549,47 @@ def test_prefill_on_bad_pages(H, d_h, r, ps):
         check(got[cu[b] + i], ref, bound)
 
 
+SPLIT = [(16, 48, 64, 32, [700], [300]), (16, 48, 64, 64, [511], [1]), (16, 64, 128, 64, [300, 512], [128, 100]),
+         (32, 32, 64, 64, [1400], [256]), (4, 16, 64, 16, [-40], [900]), (4, 56, 64, 64, [384, 385, 1000], [1, 130, 257]),
+         (8, 8, 192, 48, [900], [127]), (16, 40, 64, 64, [3001], [512])]
+
+
+@pytest.mark.parametrize("bad", [False, True])
+@pytest.mark.parametrize("H,r,ps,block,start,rows_of", SPLIT)
+def test_prefill_of_few_query_tiles(H, r, ps, block, start, rows_of, bad):
+    """Chunks behind long histories, whose query tiles leave SMs idle: two CTAs share a tile's keys.  bad: pages missing in
+    the first and in the second one's part."""
+    import rank_kv_attention_gb300 as L
+    rng = np.random.default_rng(H * r + sum(rows_of) + bad)
+    B, d = len(start), 64
+    lens = np.add(start, rows_of)
+    pages = int(sum(-(-n // ps) for n in lens)) + 1
+    cache, table = random_cache(rng, pages, ps, H, 128, r, block, loud=1), table_of(rng, lens, ps, pages)
+    poison_past_the_end(cache, table, start)
+    for b in range(B) if bad else ():
+        table[b, 1], table[b, (lens[b] - 1) // ps - 1] = -1, pages
+    cu, n = np.concatenate([[0], np.cumsum(rows_of)]), int(sum(rows_of))
+    w, x, q = weights(rng, d, H, 128, r, 1), bf16(rng, (n, d)), bf16(rng, (n, H, 128))
+    B_K, B_V = bf16(rng, (H, 128, r), r ** -0.5), bf16(rng, (H, 128, r), r ** -0.5)
+    dc, st = to_device(cache), status()
+    args = [dev(x[0], "bf16"), dev(q[0], "bf16"), dev(cu, "i32"), dev(np.array(start), "i32"), int(lens.max()),
+            *[dev(w[m][0], "bf16") for m in w], dev(B_K[0], "bf16"), dev(B_V[0], "bf16")]
+    out, again = torch.zeros(2, n, H, 128, dtype=torch.bfloat16, device="cuda")
+    L.prefill_scaled(*args, dc, dev(table, "i32"), out=out, status=st)
+    # (rows that are counted from a negative position may be more than max_ctx)
+    tiled = -(-int(lens.max()) // 128) * 128
+    assert int(st) == (BAD_PAGE if bad else 0) | (BAD_ROW if min(start) < 0 else 0) | (BAD_SEQLEN if max(rows_of) > tiled else 0)
+    L.prefill_scaled(*args, to_device(cache), dev(table, "i32"), out=again)
+    same = torch.equal(again, out)
+    assert same
+    held, got = to_host(dc, cache), host(out, "bf16")
+    for b in range(B):
+        for i in sorted({max(0, -start[b]), rows_of[b] // 2, max(0, rows_of[b] - 129), min(tiled, rows_of[b]) - 1}):
+            ref, bound = reference(q[1][cu[b] + i], held, B_K[1], B_V[1], table[b], start[b] + i + 1, True)
+            check(got[cu[b] + i], ref, bound, f"request {b} row {i}")
+        assert not got[cu[b]:cu[b] + max(0, -start[b])].any()
+
+
 # ---------------------------------------------------------------------------
 # Used together
 # ---------------------------------------------------------------------------
