@@ -473,7 +473,8 @@ LRKV_API int lrkv_prefill_window(const void *X, const void *Q, const int32_t *cu
  * lengths before the step).  Rows of no request are left alone.  A row past the
  * page table or at a negative position is skipped (LRKV_STATUS_BAD_ROW), so are
  * rows on a page outside the pool (LRKV_STATUS_BAD_PAGE).  Two requests of a
- * writing call must not write to the same block.
+ * writing call must not write to the same block, and no table may name a page that
+ * the request writes to twice.
  *
  * lrkv_write_scaled quantises rows into the cache.  For a block that the call
  * writes to, with a the largest finite magnitude of a head's new values there,

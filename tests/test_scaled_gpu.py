@@ -527,6 +527,33 @@ def test_prefill_in_a_pool_smaller_than_its_requests():
             check(got[20 * b + i], ref, bound)
 
 
+@pytest.mark.parametrize("start,rows", [(0, 100), (100, 70), (130, 300), (255, 66)])
+@pytest.mark.parametrize("wide", [False, True])
+def test_prefill_of_one_request(start, rows, wide):
+    """wide: a table beyond the pool, whose pages the values then follow.  The loud new rows make the block that they share
+    with the history grow."""
+    import rank_kv_attention_gb300 as L
+    rng = np.random.default_rng(start + rows)
+    H, r, ps, d, block = 8, 24, 64, 64, 64
+    pages = -(-(start + rows) // ps)
+    cache = random_cache(rng, pages, ps, H, 128, r, block, loud=1)
+    table = np.full((1, 3 * pages if wide else pages), -1, np.int32)
+    table[0, :pages] = rng.permutation(pages)
+    w, x, q = weights(rng, d, H, 128, r, 1), bf16(rng, (rows, d), 8.0), bf16(rng, (rows, H, 128))
+    B_K, B_V = bf16(rng, (H, 128, r), r ** -0.5), bf16(rng, (H, 128, r), r ** -0.5)
+    dc, st = to_device(cache), status()
+    out = L.prefill_scaled(dev(x[0], "bf16"), dev(q[0], "bf16"), dev(np.array([0, rows]), "i32"), dev(np.array([start]), "i32"),
+                           table.shape[1] * ps, *[dev(w[m][0], "bf16") for m in w], dev(B_K[0], "bf16"), dev(B_V[0], "bf16"), dc,
+                           dev(table, "i32"), status=st)
+    assert int(st) == 0
+    held, got = to_host(dc, cache), host(out, "bf16")
+    S.write(cache, projected(x[1], w), [0, rows], [start], table)
+    close_caches(held, cache, None, [0, rows], [start], table, d)
+    for i in sorted({0, 1, rows // 2, rows - 1}):
+        ref, bound = reference(q[1][i], held, B_K[1], B_V[1], table[0], start + i + 1, True)
+        check(got[i], ref, bound, f"row {i}")
+
+
 @pytest.mark.parametrize("H,d_h,r,ps", [(8, 128, 16, 64), (4, 32, 8, 16)])
 def test_prefill_on_bad_pages(H, d_h, r, ps):
     import rank_kv_attention_gb300 as L
