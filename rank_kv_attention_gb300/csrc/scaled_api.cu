@@ -341,8 +341,8 @@ int lrkv_prefill_scaled(const void *X, const void *Q, const int32_t *cu_rows, co
     const void *ptrs[] = {Q, B_K, B_V, out};
     for (const void *x : ptrs)
         if (!x || !aligned16(x)) return LRKV_E_INVALID_ARG;
-    // (a launch that lays out 16 rows a block)
-    if ((int64_t)B * ((max_ctx + 15) / 16) > kMost) return LRKV_E_SHAPE;
+    // (a launch that lays out 8 rows a block)
+    if ((int64_t)B * ((max_ctx + 7) / 8) > INT32_MAX) return LRKV_E_SHAPE;
     const PrefillScaledWs w = prefill_scaled_ws(workspace, *cache, B, n, max_ctx);
     if (!workspace || !aligned256(workspace) || workspace_bytes < w.bytes) return LRKV_E_WORKSPACE;
     cudaStream_t s = (cudaStream_t)stream;

@@ -26,14 +26,27 @@ namespace {
 // one 16-byte column of it and takes every rows_par-th row, so rows are read and codes
 // written whole; it holds its values in registers (8 vectors: 64 rows of a slab of
 // 256 bytes), the heads' maxima meet in shared memory, and the codes go out.  Longer blocks
-// are read twice, the second time out of L2.  (One warp per head, with rows of 96
-// bytes, took 41 us for 16,384 bf16 rows, 13 at the copy bandwidth.)
+// are read twice, the second time out of L2.  16,384 bf16 rows of 16 heads, r = 48 take
+// 18.6 us, 13.0 at the copy bandwidth: half of the time instructions issue (conversions, and what
+// a CTA does for its few vectors).  One warp per head, with rows of 96 bytes, took 41; four
+// vectors a thread 30.  A row of 16 requests each: 3.0.
 // ---------------------------------------------------------------------------
 constexpr int kWriteThreads = 128, kHeld = 8, kSlabVecs = 64;
 
-// Slabs of a pool: heads of one, and how many.
+// n / d by a multiplication: `mul` is 2^32 / d rounded up (0: d = 1), n d below 2^32.  (A
+// division by a variable is 20 to 100 instructions; with nine of them a warp took 1020 for
+// its six vectors a thread.)
+inline uint32_t div_mul(uint32_t d) { return d > 1 ? (uint32_t)(((uint64_t(1) << 32) + d - 1) / d) : 0; }
+__device__ __forceinline__ int div_by(int n, uint32_t mul) { return mul ? (int)__umulhi((uint32_t)n, mul) : n; }
+// The same by a multiple of 16 up to 1024 (tokens of a block, of a page): n below 2^30 + 2^10
+inline uint32_t div16_mul(int d) { return div_mul((uint32_t)d / 16); }
+__device__ __forceinline__ int div16_by(int n, uint32_t mul) { return div_by(n >> 4, mul); }
+
+// Slabs of a pool: heads of one, and how many; 16-byte vectors of a row of it, rows that the
+// threads take at a time; divisors of those and of a head's columns; of block and page.
 struct Slabs {
-    int heads[4], count[4];
+    int heads[4], count[4], vpr[4], rows_par[4];
+    uint32_t by_vpr[4], by_rows[4], by_width[4], by_block, by_page;
 };
 
 // The request of a unit, its rows [r0, r1) and its first position; b = -1: none.
@@ -43,7 +56,7 @@ struct UnitOwner {
 
 // The last b in [0, B) with cu[b] / block + 2 b <= u (whole warp).  The last probes are of
 // neighbouring requests, so that their rows come with them.
-__device__ __forceinline__ UnitOwner owner_of_unit(const int32_t *cu, const int32_t *start, int B, int block, int u,
+__device__ __forceinline__ UnitOwner owner_of_unit(const int32_t *cu, const int32_t *start, int B, uint32_t by_block, int u,
                                                    int lane) {
     int lo = 0, hi = B;
     for (;;) {
@@ -55,7 +68,7 @@ __device__ __forceinline__ UnitOwner owner_of_unit(const int32_t *cu, const int3
             c1 = cu[i + 1];
             s = start[i];
         }
-        const uint32_t no = ~__ballot_sync(0xffffffffu, in && (int64_t)(c0 / block) + 2 * (int64_t)i <= u);
+        const uint32_t no = ~__ballot_sync(0xffffffffu, in && (int64_t)div16_by(max(c0, 0), by_block) + 2 * (int64_t)i <= u);
         const int k = no ? __ffs(no) - 1 : 32;  // probes that hold
         if (k == 0) return {-1, 0, 0, 0};       // (only in the first round)
         if (step == 1)
@@ -106,23 +119,33 @@ __device__ __forceinline__ uint32_t top_finite(const uint4 &v) {
     return m;
 }
 
-// Codes of one vector of values times `inv`; `odd`: there may be infinities (which
-// the conversion would saturate) among them.
-template <typename T>
-__device__ __forceinline__ void put_codes(uint8_t *dst, const uint4 &v, float inv, bool odd) {
+__device__ __forceinline__ uint64_t f2_mul(float lo, float hi, uint64_t s) {
+    uint64_t r;
+    asm("{ .reg .b64 t; mov.b64 t, {%1, %2}; mul.rn.f32x2 %0, t, %3; }" : "=l"(r) : "f"(lo), "f"(hi), "l"(s));
+    return r;
+}
+
+// Codes of one vector of values times `inv`; ODD: there may be infinities (which the
+// conversion would saturate) among them.
+template <typename T, bool ODD>
+__device__ __forceinline__ void put_codes(uint8_t *dst, const uint4 &v, float inv) {
     constexpr int V = Bits<T>::V;
     float x[V];
     Bits<T>::get(v, x);
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-        if (odd && (__float_as_uint(x[e]) & 0x7fffffffu) == kInf) x[e] = __uint_as_float(0x7fffffffu);
-        x[e] *= inv;
-    }
+    uint64_t s2;
+    asm("mov.b64 %0, {%1, %1};" : "=l"(s2) : "f"(inv));
     uint32_t w[V / 4];
 #pragma unroll
-    for (int e = 0; e < V / 4; ++e)
-        w[e] = (uint32_t)e4m3x2_from_f32(x[4 * e], x[4 * e + 1]) |
-               ((uint32_t)e4m3x2_from_f32(x[4 * e + 2], x[4 * e + 3]) << 16);
+    for (int e = 0; e < V; e += 2) {
+        if (ODD)
+#pragma unroll
+            for (int k = e; k < e + 2; ++k)
+                if ((__float_as_uint(x[k]) & 0x7fffffffu) == kInf) x[k] = __uint_as_float(0x7fffffffu);
+        float lo, hi;
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(f2_mul(x[e], x[e + 1], s2)));
+        const uint32_t c = e4m3x2_from_f32(lo, hi);
+        w[e / 4] = e % 4 ? w[e / 4] | c << 16 : c;
+    }
     if constexpr (V == 8) *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
     else *reinterpret_cast<uint32_t *>(dst) = w[0];
 }
@@ -145,21 +168,21 @@ __global__ void __launch_bounds__(kWriteThreads, 7) write_scaled_kernel(const __
     pdl_launch_dependents();
 
     // ---- the unit's rows i0 .. i1 - 1, from position p0 on
-    const UnitOwner own = owner_of_unit(a.rows.cu_rows, a.rows.start_pos, a.rows.B, c.block, u, lane);
+    const UnitOwner own = owner_of_unit(a.rows.cu_rows, a.rows.start_pos, a.rows.B, slabs.by_block, u, lane);
     const int b = own.b, r0 = own.r0, r1 = min(own.r1, a.rows.n), start = own.start;
     if (b < 0 || r0 < 0 || r0 >= r1) return;
     const int64_t max_len = (int64_t)a.rows.max_pages * c.page_size;
     const int64_t ra64 = r0 + max((int64_t)0, -(int64_t)start);            // first row at a position >= 0
     const int64_t rz64 = min((int64_t)r1, r0 + max_len - (int64_t)start);  // rows past the table start here
-    const int key = u - (r0 / c.block + 2 * b);
+    const int key = u - (div16_by(r0, slabs.by_block) + 2 * b);
     if (key == 0 && speaks && (ra64 > r0 || rz64 < r1)) status_or(a.rows.status, LRKV_STATUS_BAD_ROW);
     if (ra64 >= rz64) return;
     const int ra = (int)ra64, rz = (int)rz64, pa = start + (ra - r0);  // (all below 2^30 from here on)
-    const int i2 = ra + c.block - pa % c.block;                       // first row of the second unit
+    const int i2 = ra + (div16_by(pa, slabs.by_block) + 1) * c.block - pa;  // first row of the second unit
     int i0 = ra, i1 = i2;
     if (key > 0) {
-        const int m = u - 2 * b - 1 - i2 / c.block;
-        if (m < 0) return;
+        const int m = u - 2 * b - 1 - div16_by(i2, slabs.by_block);
+        if (m < 0 || (int64_t)m * c.block >= rz - i2) return;
         i0 = i2 + m * c.block;
         i1 = i0 + c.block;
     }
@@ -168,10 +191,11 @@ __global__ void __launch_bounds__(kWriteThreads, 7) write_scaled_kernel(const __
     const int p0 = pa + (i0 - ra), rows = i1 - i0;
 
     // ---- this thread's column and rows
-    const int vpr = nh * width / V, rows_par = kWriteThreads / vpr;
-    const int row0 = tid / vpr, cv = tid - row0 * vpr, hl = cv * V / width;  // head in the slab
-    const bool active = row0 < rows_par;
-    const int mine = active && row0 < rows ? (rows - row0 + rows_par - 1) / rows_par : 0;
+    const int rows_par = slabs.rows_par[k];
+    const int row0 = div_by(tid, slabs.by_vpr[k]), cv = tid - row0 * slabs.vpr[k];
+    const int hl = div_by(cv * V, slabs.by_width[k]);  // head in the slab (the last slab may have fewer)
+    const bool active = row0 < rows_par && hl < nh;
+    const int mine = active && row0 < rows ? div_by(rows - row0 + rows_par - 1, slabs.by_rows[k]) : 0;
     const int64_t ld = a.ld[k], step = ld * rows_par;
     const T *x = static_cast<const T *>(a.x[k]) + (int64_t)(i0 + row0) * ld + h0 * width + cv * V;
     uint4 val[kHeld];
@@ -179,16 +203,18 @@ __global__ void __launch_bounds__(kWriteThreads, 7) write_scaled_kernel(const __
     for (int j = 0; j < kHeld; ++j)
         if (j < mine) val[j] = *reinterpret_cast<const uint4 *>(x + j * step);
     // (the lookups of the destination are on their way meanwhile)
-    const int32_t page = a.rows.page_table[(size_t)b * a.rows.max_pages + p0 / c.page_size];
+    const int pi = div16_by(p0, slabs.by_page);
+    const int32_t page = a.rows.page_table[(size_t)b * a.rows.max_pages + pi];
     if (page < 0 || page >= c.num_pages) {
         if (speaks) status_or(a.rows.status, LRKV_STATUS_BAD_PAGE);
         return;
     }
-    const int slot = p0 % c.page_size, before = slot % c.block;
-    uint8_t *eb = c.exp[k] + ((int64_t)page * c.page_size + slot) / c.block * heads + h0 + hl;
+    const int slot = p0 - pi * c.page_size, row = page * c.page_size + slot, blk = div16_by(row, slabs.by_block);
+    const int before = row - blk * c.block;  // (a block's first row is a multiple of it in the pool)
+    uint8_t *eb = c.exp[k] + (int64_t)blk * heads + h0 + hl;
     const int old = before && active ? clamp_exp(*eb) : LRKV_SCALED_MIN_EXP;
     const int row_bytes = heads * width;
-    uint8_t *code = c.code[k] + ((int64_t)page * c.page_size + slot + row0) * row_bytes + h0 * width + cv * V;
+    uint8_t *code = c.code[k] + (int64_t)(row + row0) * row_bytes + h0 * width + cv * V;
 
     uint32_t top = 0;
 #pragma unroll
@@ -208,10 +234,13 @@ __global__ void __launch_bounds__(kWriteThreads, 7) write_scaled_kernel(const __
     const int e = max(old, needed_exp(__uint_as_float(tops[odd][hl])));
     const float inv = exp2i(-e);
     const int64_t cstep = (int64_t)row_bytes * rows_par;
+    if (!odd) {
 #pragma unroll
-    for (int j = 0; j < kHeld; ++j)
-        if (j < mine) put_codes<T>(code + j * cstep, val[j], inv, odd);
-    for (int j = kHeld; j < mine; ++j) put_codes<T>(code + j * cstep, *reinterpret_cast<const uint4 *>(x + j * step), inv, odd);
+        for (int j = 0; j < kHeld; ++j)
+            if (j < mine) put_codes<T, false>(code + j * cstep, val[j], inv);
+    }
+    for (int j = odd ? 0 : kHeld; j < mine; ++j)
+        put_codes<T, true>(code + j * cstep, *reinterpret_cast<const uint4 *>(x + j * step), inv);
     // ---- rows of the block before the new ones, where the scale grew
     if (before && e > old) {
         const float s = exp2i(max(old - e, -126));  // (2^-126 of any code rounds to zero too)
@@ -231,10 +260,17 @@ __global__ void __launch_bounds__(kWriteThreads, 7) write_scaled_kernel(const __
 }
 
 // ---------------------------------------------------------------------------
-// Reading.  A CTA takes 16 rows (or 4); a thread takes 8 columns (which lie in one head)
-// of all of them, so a warp reads 256 consecutive bytes of a row.
+// Reading.  A CTA takes a few rows; a thread takes 8 columns (which lie in one head) of all
+// of them, so a warp reads 256 consecutive bytes of a row.  Bound by how many rows are on
+// their way: a CTA looks its rows up (request, page, three dependent loads), meets, loads
+// and stores, and others have to fill the gaps.  40,000 rows of 16 heads, r = 48 in bf16 take
+// 36.2 us with 8 rows a CTA and five CTAs an SM (31.8 at the copy bandwidth), 42.4 with 16
+// and two, 36.4 with 4 and eight; one request of 777 rows in fp32 3.8 with 8, 4.1 with 4.
+// The layout for a prefill's attention takes 4 rows a CTA where it is short and waited for (512
+// rows behind 3001: 49.3 us, 51.2 with 8), and 8 where its CTAs are many, of which those past a
+// request's history only leave (8 prompts of 2048 rows: 305.1 us, 306.9 with 4).
 // ---------------------------------------------------------------------------
-constexpr int kReadThreads = 256;
+constexpr int kReadThreads = 256, kReadRows = 8;
 
 // Eight codes times 2^e.
 __device__ __forceinline__ void widen8(const uint2 &w, float s, float (&x)[8]) {
@@ -307,16 +343,18 @@ __device__ __forceinline__ int pool_row(const ScaledPools &c, const ScaledRows &
         status_or(r.status, LRKV_STATUS_BAD_ROW);
         return -1;
     }
-    const int32_t page = r.page_table[(size_t)b * r.max_pages + pos / c.page_size];
+    const int p = (int)pos, pi = p / c.page_size;
+    const int32_t page = r.page_table[(size_t)b * r.max_pages + pi];
     if (page < 0 || page >= c.num_pages) {
         status_or(r.status, LRKV_STATUS_BAD_PAGE);
         return -1;
     }
-    return page * c.page_size + (int)(pos % c.page_size);
+    return page * c.page_size + (p - pi * c.page_size);
 }
 
-template <typename T, int ROWS>
-__global__ void __launch_bounds__(kReadThreads) read_scaled_kernel(const __grid_constant__ ScaledReadArgs a) {
+template <typename T>
+__global__ void __launch_bounds__(kReadThreads, 5) read_scaled_kernel(const __grid_constant__ ScaledReadArgs a) {
+    constexpr int ROWS = kReadRows;
     __shared__ RowSet<ROWS> set;
     pdl_wait();
     pdl_launch_dependents();
@@ -344,8 +382,8 @@ __global__ void __launch_bounds__(kReadThreads) read_scaled_kernel(const __grid_
 }
 
 template <int ROWS>
-__global__ void __launch_bounds__(kReadThreads) expand_scaled_kernel(const __grid_constant__ ScaledExpandArgs a,
-                                                                     int tiles) {
+__global__ void __launch_bounds__(kReadThreads, 5) expand_scaled_kernel(const __grid_constant__ ScaledExpandArgs a,
+                                                                        int tiles) {
     __shared__ RowSet<ROWS> set;
     __shared__ int64_t ld[4];
     pdl_wait();
@@ -388,24 +426,27 @@ cudaError_t launch_write_scaled(const ScaledWriteArgs &a) {
         const int parts = (heads + each - 1) / each;
         slabs.heads[k] = (heads + parts - 1) / parts;
         slabs.count[k] = (heads + slabs.heads[k] - 1) / slabs.heads[k];
+        slabs.vpr[k] = slabs.heads[k] * a.c.width(k) / V;
+        slabs.rows_par[k] = kWriteThreads / slabs.vpr[k];
+        slabs.by_vpr[k] = div_mul(slabs.vpr[k]);
+        slabs.by_rows[k] = div_mul(slabs.rows_par[k]);
+        slabs.by_width[k] = div_mul(a.c.width(k));
         total += slabs.count[k];
     }
+    slabs.by_block = div16_mul(a.c.block);
+    slabs.by_page = div16_mul(a.c.page_size);
     const dim3 grid((unsigned)units, total);
     return a.f32 ? launch_pdl(write_scaled_kernel<float>, grid, dim3(kWriteThreads), 0, a.stream, a, slabs)
                  : launch_pdl(write_scaled_kernel<__nv_bfloat16>, grid, dim3(kWriteThreads), 0, a.stream, a, slabs);
 }
 
-// Rows of a CTA: 16, or 4 where 16 would leave SMs idle.
-static bool few_rows(int64_t rows) { return rows < 32 * (int64_t)device_sm_count(); }
-
-template <typename T, int ROWS>
+template <typename T>
 static cudaError_t launch_read(const ScaledReadArgs &a) {
-    return launch_pdl(read_scaled_kernel<T, ROWS>, dim3((a.rows.n + ROWS - 1) / ROWS), dim3(kReadThreads), 0, a.stream, a);
+    return launch_pdl(read_scaled_kernel<T>, dim3((a.rows.n + kReadRows - 1) / kReadRows), dim3(kReadThreads), 0, a.stream, a);
 }
 
 cudaError_t launch_read_scaled(const ScaledReadArgs &a) {
-    if (few_rows(a.rows.n)) return a.f32 ? launch_read<float, 4>(a) : launch_read<__nv_bfloat16, 4>(a);
-    return a.f32 ? launch_read<float, 16>(a) : launch_read<__nv_bfloat16, 16>(a);
+    return a.f32 ? launch_read<float>(a) : launch_read<__nv_bfloat16>(a);
 }
 
 template <int ROWS>
@@ -416,7 +457,8 @@ static cudaError_t launch_expand(const ScaledExpandArgs &a) {
 }
 
 cudaError_t launch_expand_scaled(const ScaledExpandArgs &a) {
-    return few_rows((int64_t)a.rows.B * a.max_ctx) ? launch_expand<4>(a) : launch_expand<16>(a);
+    // (eight CTAs of 4 rows on every SM)
+    return (int64_t)a.rows.B * a.max_ctx < 32 * (int64_t)device_sm_count() ? launch_expand<4>(a) : launch_expand<8>(a);
 }
 
 }  // namespace lrkv
