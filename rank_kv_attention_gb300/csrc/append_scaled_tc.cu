@@ -14,8 +14,8 @@
 // A pair of CTAs (cta_group::2) takes two row tiles by one column tile, M = 256, N = twice
 // the block's width; the ring, the two accumulators and the warps' parts are append_tc.cu's.
 //
-// Epilogue, thread = row, four warps: the largest magnitude of every head over 16
-// rows each (from tensor memory), those of a block's rows through shared memory; then
+// Epilogue, thread = row, four warps: the exponent that the largest magnitude of
+// every head over 16 rows needs (from tensor memory), those of a block's rows through shared memory; then
 // the values are read again, scaled, rounded and stored: r bytes a head and row.  Rows of
 // the block that were there before are threads of the tile too: they shrink their own
 // codes where the scale grows.  Where the caller wants the values in bf16 (prefill),
@@ -33,7 +33,7 @@ namespace lrkv {
 
 namespace {
 
-constexpr int kBM = 128, kBK = 64, kStages = 6;
+constexpr int kBM = 128, kBK = 64, kStages = 7;
 constexpr int kABytes = kBM * kBK * 2, kBBytes = 128 * kBK * 2, kStage = kABytes + kBBytes;
 constexpr int kMaxHeads = 32;  // heads of a column tile (two blocks of 128 columns, r = 8)
 constexpr int kThreads = 192;  // producer, MMA, 4 epilogue warps
@@ -42,10 +42,10 @@ constexpr int kTmemCols = 512;
 struct Bars {
     uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], meet;
     uint32_t tmem;
-    // of two tiles in turn: largest magnitudes of 16 rows; old exponents of the block that
-    // has rows from before (a tile has one at most)
-    uint32_t top[2][kMaxHeads][8];
-    int was[2][kMaxHeads];
+    // of two tiles in turn: exponents that 16 rows need; old exponents of the block that has
+    // rows from before (a tile has one at most)
+    int8_t top[2][kMaxHeads][8];
+    int8_t was[2][kMaxHeads];
 };
 constexpr int kOffBars = kStages * kStage;
 constexpr int kSmem = kOffBars + (int)sizeof(Bars) + 1024;
@@ -291,12 +291,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (was_block >= 0 && row < nheads) {
                 const int k = row / ct.heads, head = (k ? ct.head[1] : ct.head[0]) + row % ct.heads;
                 const int pool = k ? ct.pool[1] : ct.pool[0], heads = a.c.heads(pool);
-                bar.was[i & 1][row] = head < heads ? clamp_exp(a.c.exp[pool][was_block * heads + head]) : 0;
+                bar.was[i & 1][row] = head < heads ? (int8_t)clamp_exp(a.c.exp[pool][was_block * heads + head]) : 0;
             }
             if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bar.acc_full[acc], (i >> 1) & 1)))) break;
             tc_fence_after();
             const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16) + acc * 256;
-            uint32_t (*top)[8] = bar.top[i & 1];
+            int8_t (*top)[8] = bar.top[i & 1];
             // ---- largest finite magnitudes of 16 rows, head by head
             uint32_t col = 0;  // (heads lie next to each other, the second block's behind the first's columns)
 #pragma unroll 1
@@ -326,7 +326,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (!fresh) m = 0;
 #pragma unroll
                 for (int o = 8; o; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-                if ((lane & 15) == 0) top[h][row >> 4] = m;
+                if ((lane & 15) == 0) top[h][row >> 4] = (int8_t)needed_exp(__uint_as_float(m));
             }
             mbar_arrive(&bar.meet);
             if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bar.meet, met++ & 1)))) break;
@@ -339,9 +339,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const int pool = second ? ct.pool[1] : ct.pool[0];
                 const int head = second ? ct.head[1] + h - ct.heads : ct.head[0] + h, heads = a.c.heads(pool);
                 const bool live = head < heads;  // (the last block may have fewer heads)
-                uint32_t m = 0;
-                for (int g = 0; g < block / 16; ++g) m = max(m, top[h][((bpos & (kBM - 1)) >> 4) + g]);
-                const int was = kept ? bar.was[i & 1][h] : LRKV_SCALED_MIN_EXP, e = max(needed_exp(__uint_as_float(m)), was);
+                const int was = kept ? bar.was[i & 1][h] : LRKV_SCALED_MIN_EXP;
+                int e = was;
+                for (int g = 0; g < block / 16; ++g) e = max(e, (int)top[h][((bpos & (kBM - 1)) >> 4) + g]);
                 if (live && first && (!kept || e > was)) a.c.exp[pool][dr / block * heads + head] = (uint8_t)(e + 127);
                 const float inv = exp2i(-e), back = exp2i(e);
                 const bool put = live && fresh;
