@@ -21,8 +21,12 @@
 // codes where the scale grows.  Where the caller wants the values in bf16 (prefill),
 // they are stored beside the codes.
 //
-// Staged in fp32 instead (the projection's rows written, read again and quantised), 16,384
-// rows of d = 2048, 16 heads, r = 48 take 129 us.
+// 16,384 rows of 8 prompts, d = 2048, 16 heads, r = 48: 94 us, 63.3 at the measured bf16 peak, 129
+// staged in fp32 (the projection's rows written, read again and quantised).  The issuing thread
+// waits 22,000 of its 160,000 cycles for copies and 1000 for the epilogue; the rest is the
+// tensor cores': 535 cycles a step of 256 x 192 x 64, whose products alone are 384, while
+// shared memory serves operands and 28 KB of copies a step.  Two epilogues side by side
+// (eight warps) or a seventh stage changed it by 0.3%.
 #include <algorithm>
 
 #include "append_kernels.cuh"
@@ -448,8 +452,12 @@ int block_heads(int r) {
 }  // namespace
 
 bool append_scaled_tc_fits(const ScaledPools &c, int n, int B, int d) {
-    // (few rows: the row kernel and a staged write; many requests: every warp scans them)
-    return n > 64 && B <= 4096 && d % kBK == 0 && c.d_h == 128 && c.r <= 128 && block_heads(c.r) > 0 && c.block <= 128 &&
+    // Here or staged (the projection's rows in fp32, then a write).  Tiles are 128 positions of one
+    // request, so requests of few rows leave most of theirs empty: 64 of 2 rows take 47.4 us
+    // here and 26.1 staged, 24 of 100 rows 38.7 and 33.1, 32 of 256 rows 69.7 and 67.7, 16 of
+    // 20 rows 19.0 and 21.1, 4 of 512 rows 29.1 and 30.1, 8 prompts of 16,384 rows 94 and 129.
+    // One of 66 rows 15.7 and 17.4, but of 64, where the row kernel runs, 15.4 and 12.4.
+    return n > 64 && B <= 16 + n / 512 && d % kBK == 0 && c.d_h == 128 && c.r <= 128 && block_heads(c.r) > 0 && c.block <= 128 &&
            128 % c.block == 0 && tc_encode() != nullptr;
 }
 
@@ -463,8 +471,9 @@ cudaError_t launch_append_scaled_tc(const ScaledAppendArgs &p) {
     a.bw = a.hb * c.r;
     a.rblocks = (c.H + a.hb - 1) / a.hb;
     // One block a tile while all of them run at once: each of twice as many SMs then does half
-    // of the products and of the epilogue.  Otherwise two, which need half the copies of X
-    // per product.  (N = one block's columns: a multiple of 32 for a pair of CTAs.)
+    // of the products and of the epilogue (512 rows: 16.0 us, 18.2 with two).  Otherwise two,
+    // which need half the copies of X per product.  (N = one block's columns: a multiple of 32
+    // for a pair of CTAs.)
     const int64_t pairs = (p.rows.n / kBM + 2 * (int64_t)p.rows.B + 1) / 2;
     a.per = a.bw % 32 == 0 && 2 * pairs * 2 * (c.G + a.rblocks) <= device_sm_count() ? 1 : 2;
     a.coltiles = (2 / a.per) * (c.G + a.rblocks);

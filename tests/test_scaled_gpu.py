@@ -472,6 +472,37 @@ def test_append(H, d_h, r, G, ps, block, d, rows_of):
     close_caches(to_host(dc, cache), cache, None, cu, start, table, d)
 
 
+@pytest.mark.parametrize("H,d_h,r,G,ps,block,d", [PROJ[0], PROJ[4], PROJ[1], (8, 128, 64, 4, 128, 64, 128)])
+def test_append_and_prefill_of_many_short_requests(H, d_h, r, G, ps, block, d):
+    """More requests than row tiles pay for: none, one and a few rows each."""
+    import rank_kv_attention_gb300 as L
+    rng = np.random.default_rng(H + r)
+    B = 70
+    rows_of, start = rng.integers(0, 5, B), rng.integers(0, 100, B)
+    lens = rows_of + start
+    pages = int(sum(-(-n // ps) for n in lens)) + 1
+    table = table_of(rng, lens, ps, pages, width=-(-104 // ps))
+    cu, n = np.concatenate([[0], np.cumsum(rows_of)]), int(rows_of.sum())
+    before = random_cache(rng, pages, ps, H, d_h, r, block, G, loud=1)
+    w, x, q = weights(rng, d, H, d_h, r, G), bf16(rng, (n, d)), bf16(rng, (n, H, d_h))
+    B_K, B_V = bf16(rng, (H, d_h, r), r ** -0.5), bf16(rng, (H, d_h, r), r ** -0.5)
+    dc, other, st = to_device(before), to_device(before), status()
+    args = [dev(cu, "i32"), dev(start, "i32")]
+    L.append_scaled(dev(x[0], "bf16"), *args, *[dev(w[m][0], "bf16") for m in w], dc, dev(table, "i32"), status=st)
+    out = L.prefill_scaled(dev(x[0], "bf16"), dev(q[0], "bf16"), *args, 104, *[dev(w[m][0], "bf16") for m in w],
+                           dev(B_K[0], "bf16"), dev(B_V[0], "bf16"), other, dev(table, "i32"), status=st)
+    assert int(st) == 0
+    held, want = to_host(dc, before), before.copy()
+    S.write(want, projected(x[1], w), cu, start, table)
+    close_caches(held, want, None, cu, start, table, d)
+    assert_same(to_host(other, before), held)
+    got = host(out, "bf16")
+    for b in range(0, B, 7):
+        for i in {cu[b], cu[b + 1] - 1} if rows_of[b] else ():
+            ref, bound = reference(q[1][i], held, B_K[1], B_V[1], table[b], int(start[b] + i - cu[b] + 1), G == 1)
+            check(got[i], ref, bound, f"request {b}")
+
+
 @pytest.mark.parametrize("rows_of,start", [([1, 1, 1], [5, 0, 200]), ([130, 0, 200], [0, 9, 77]), ([3, 300, 64], [190, 0, 64])])
 @pytest.mark.parametrize("H,d_h,r,G,ps,block,d", PROJ)
 def test_prefill(H, d_h, r, G, ps, block, d, rows_of, start):
