@@ -21,7 +21,7 @@
 // codes where the scale grows.  Where the caller wants the values in bf16 (prefill),
 // they are stored beside the codes.
 //
-// 16,384 rows of 8 prompts, d = 2048, 16 heads, r = 48: 94 us, 63.3 at the measured bf16 peak, 129
+// 16,384 rows of 8 prompts, d = 2048, 16 heads, r = 48: 94 us, 63.3 at the measured bf16 peak, 123
 // staged in fp32 (the projection's rows written, read again and quantised).  The issuing thread
 // waits 22,000 of its 160,000 cycles for copies and 1000 for the epilogue; the rest is the
 // tensor cores': 535 cycles a step of 256 x 192 x 64, whose products alone are 384, while
@@ -454,9 +454,9 @@ int block_heads(int r) {
 bool append_scaled_tc_fits(const ScaledPools &c, int n, int B, int d) {
     // Here or staged (the projection's rows in fp32, then a write).  Tiles are 128 positions of one
     // request, so requests of few rows leave most of theirs empty: 64 of 2 rows take 47.4 us
-    // here and 26.1 staged, 24 of 100 rows 38.7 and 33.1, 32 of 256 rows 69.7 and 67.7, 16 of
-    // 20 rows 19.0 and 21.1, 4 of 512 rows 29.1 and 30.1, 8 prompts of 16,384 rows 94 and 129.
-    // One of 66 rows 15.7 and 17.4, but of 64, where the row kernel runs, 15.4 and 12.4.
+    // here and 20 staged, 24 of 100 rows 38.7 and 33.0, 32 of 256 rows 70.4 and 68.6, 16 of
+    // 20 rows 19.1 and 20.3, 4 of 512 rows 28.9 and 30.1, 8 prompts of 16,384 rows 94 and 123.
+    // Two of 33 rows 15.7 and 17.3, but one of 64, where the row kernel runs, 15.4 and 12.4.
     return n > 64 && B <= 16 + n / 512 && d % kBK == 0 && c.d_h == 128 && c.r <= 128 && block_heads(c.r) > 0 && c.block <= 128 &&
            128 % c.block == 0 && tc_encode() != nullptr;
 }

@@ -29,9 +29,10 @@ namespace {
 // are read twice, the second time out of L2.  16,384 bf16 rows of 16 heads, r = 48 take
 // 18.6 us, 13.0 at the copy bandwidth: half of the time instructions issue (conversions, and what
 // a CTA does for its few vectors).  One warp per head, with rows of 96 bytes, took 41; four
-// vectors a thread 30.  A row of 16 requests each: 3.0.
+// vectors a thread 30.  A row each of 16 requests: 2.4, of 512: 8.9 (33 with slabs of heads for
+// whole blocks).
 // ---------------------------------------------------------------------------
-constexpr int kWriteThreads = 128, kHeld = 8, kSlabVecs = 64;
+constexpr int kWriteThreads = 128, kHeld = 8;
 
 // n / d by a multiplication: `mul` is 2^32 / d rounded up (0: d = 1), n d below 2^32.  (A
 // division by a variable is 20 to 100 instructions; with nine of them a warp took 1020 for
@@ -416,9 +417,10 @@ __global__ void __launch_bounds__(kReadThreads, 5) expand_scaled_kernel(const __
 cudaError_t launch_write_scaled(const ScaledWriteArgs &a) {
     const int64_t units = a.rows.n / a.c.block + 2 * (int64_t)a.rows.B;
     const int V = a.f32 ? 4 : 8;
-    // columns of a slab: 64 vectors, fewer where a block is longer than the values that
-    // threads hold then (and one head at least)
-    const int vecs = std::max(1, std::min(kSlabVecs, kWriteThreads * kHeld / a.c.block));
+    // columns of a slab: a vector a thread, fewer where a unit (of a block, or of twice a request's rows
+    // on average) is longer than the values that threads hold then (and one head at least)
+    const int rows = (int)std::min<int64_t>(a.c.block, 2 * ((a.rows.n + (int64_t)a.rows.B - 1) / a.rows.B));
+    const int vecs = std::max(1, std::min(kWriteThreads, kWriteThreads * kHeld / rows));
     Slabs slabs;
     int total = 0;
     for (int k = 0; k < 4; ++k) {
