@@ -11,6 +11,10 @@
 // running maximum and sum, then every lane adds the rows' values up for four
 // columns of each 128.  The shared rows are read again by every head (out of
 // L2), and the four warps' states meet in shared memory.
+//
+// Bound by the lanes' own loads of rows r or d_h bytes apart and by the conversions of every
+// code, once a head.  16 requests of 4096 rows in a graph: d_h = 64, r = 16, 8 heads 86 us (3.7 at
+// the copy bandwidth); d_h = 128, r = 72, 12 heads 240 (19.2); d_h = 128, r = 16, 40 heads 606 (14.9).
 #include <algorithm>
 
 #include "scaled_kernels.cuh"
@@ -384,7 +388,9 @@ cudaError_t launch_scaled_row_queries(const ScaledRows &rows, int page_size, int
 
 cudaError_t launch_scaled_merge(const ScaledMergeArgs &m, cudaStream_t s) {
     // 512 threads with 16 value sums each on the way where CTAs are few, and states of a
-    // request many; else six CTAs of 256 threads an SM (64 requests of 16 heads: 12 us with 512)
+    // request many (a decode of 4 requests of 32768 rows 65.6 us, 69.4 with 256 threads; of 1500
+    // rows 16.3 and 17.2); else six CTAs of 256 threads an SM (of 64 ragged requests this kernel
+    // took 12 us with 512, 9.5 so)
     const bool few = (int64_t)m.B * m.H < 2 * device_sm_count();
     return few ? launch_pdl(scaled_merge_kernel<512, 16>, dim3(m.B, m.H), dim3(512), 0, s, m)
                : launch_pdl(scaled_merge_kernel<256, 4>, dim3(m.B, m.H), dim3(256), 0, s, m);
