@@ -125,7 +125,8 @@ struct PrefillTcArgs {
     int window = 0, sinks = 0;  // lrkv_prefill_window; window 0: the whole history
     // The predecessor in the stream is the same call's append, which let this
     // kernel launch after passing its own wait and finishes within a few
-    // milliseconds: only the copies of tiles that may hold new rows wait for it.
+    // milliseconds: only the copies of tiles that may hold new rows wait for it.  (split: the
+    // predecessor writes the page table and the history, and all copies wait.)
     bool early = false;
     // Query tiles that leave half of the SMs idle may have two CTAs each (no window); the
     // sums are then added up in another order.

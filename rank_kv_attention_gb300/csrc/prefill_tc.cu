@@ -69,7 +69,8 @@
 // sums (O, running maximum and sum, fp32) over through the first one's shared memory,
 // the value stages that are free by then, and the first goes on as one that had seen
 // all keys.  512 rows behind 3001, 16 heads, r = 48 (64 query tiles; the call with its
-// append): 50.1 us, 58.9 with one CTA a tile.
+// append): 50.1 us, 58.9 with one CTA a tile.  `early` there: the queries and p come before the
+// wait for the layout of the history.
 #include <algorithm>
 
 #include "append_kernels.cuh"
@@ -282,7 +283,8 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
     }
     // early: every thread that leaves, writes the output or reads new rows waits
     // for the append itself
-    if (!(WIN && a.early)) {
+    const bool early = (WIN || SPLIT) && a.early;
+    if (!early) {
         pdl_wait();
         pdl_launch_dependents();
     }
@@ -291,7 +293,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
     const int r0 = a.cu_rows[b], r1 = min(a.cu_rows[b + 1], a.n), start = a.start_pos[b];
     const int i0 = r0 + tq * PF_BM;
     if (r0 < 0 || i0 >= r1) {
-        if (WIN && a.early) pdl_wait();
+        if (early) pdl_wait();
         return;
     }
     if (tq == a.n_qtiles - 1 && r1 > i0 + PF_BM) {  // rows beyond max_ctx: not covered
@@ -301,7 +303,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
     const int p0 = start + (i0 - r0);                       // position of tile row 0
     const int t_lo = max(0, -p0), t_hi = min(nrows, a.max_len - p0);  // rows with a valid position
     if (t_lo >= t_hi) {  // no row of this tile has a valid position: zero its outputs
-        if (WIN && a.early) pdl_wait();
+        if (early) pdl_wait();
         if (tid < nrows) {
             uint4 *dst = reinterpret_cast<uint4 *>(a.out + ((size_t)(i0 + tid) * a.H + h) * 128);
             for (int k = 0; k < 16; ++k) dst[k] = make_uint4(0, 0, 0, 0);
@@ -313,7 +315,10 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
     // the same in both CTAs of a cluster: whether they share the tiles, and this one's
     const bool shared = SPLIT && keys.count >= kPfSplitTiles, second = SPLIT && (blockIdx.x & 1);
     if (SPLIT) {
-        if (second && !shared) return;
+        if (second && !shared) {
+            if (early) pdl_wait();
+            return;
+        }
         if (shared) {
             const int cut = keys.count / 2;
             keys.from = second ? 0 : cut;
@@ -349,7 +354,8 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
     // requests, any (a history may be another's new rows)
     const int first_new = a.B > 1 ? 0 : p0 - tq * PF_BM;
     // whether the append has to be waited for before tile kt is copied
-    auto needs_append = [&](int kt) { return WIN && a.early && keys.base(kt) + PF_BN > first_new; };
+    // (SPLIT: the page table and the whole history are the kernel's in front)
+    auto needs_append = [&](int kt) { return early && (SPLIT || keys.base(kt) + PF_BN > first_new); };
     int n_iss = 0;  // copy threads: tiles issued
 
     if (warp == 8) {
@@ -386,11 +392,16 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
             uint64_t *empty = kprod ? bar.s_full : bar.pv_done;
             uint8_t *ring = smem + (kprod ? PF_OFF_K : PF_OFF_V);
             int ya = 0, yb = 0;
+            bool waited = false;
+            if (SPLIT && early) {
+                pdl_wait();
+                pdl_launch_dependents();
+                waited = true;
+            }
             if (n_iss < nkt) {
                 ya = slice_row(n_iss, 0);
                 yb = slice_row(n_iss, 1);
             }
-            bool waited = false;
             for (int kt = n_iss; kt < nkt; ++kt) {
                 const int st = kt & 1, y0 = ya, y1 = yb;
                 if (!waited && needs_append(kt)) {  // (positions grow from tile to tile)
@@ -585,6 +596,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
             tc_fence_before();
             mbar_arrive(&bar.qa_ready);
         }
+        if (SPLIT && early) pdl_wait();
         int32_t page_next = pt_row[min((keys.base(0) + hf * PF_HALF) / a.page_size, a.max_pages - 1)];
         for (int kt = 0; kt < nkt && ok; ++kt) {
             const int st = kt & 1, key0 = keys.base(kt) + hf * PF_HALF;
@@ -702,7 +714,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
             tc_fence_before();
             mbar_arrive(&bar.p_full[st]);
         }
-        if (WIN && a.early) pdl_wait();  // (long past: the last tiles hold new rows)
+        if (WIN && early) pdl_wait();  // (long past: the last tiles hold new rows)
         // row sum of both halves, exchanged through the q tile (no longer read:
         // the last scores completed before this softmax began)
         float *lsum = reinterpret_cast<float *>(smem + PF_OFF_Q);

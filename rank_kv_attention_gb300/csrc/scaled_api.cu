@@ -364,7 +364,7 @@ int lrkv_prefill_scaled(const void *X, const void *Q, const int32_t *cu_rows, co
         p.out = out;
         p.status = dev_status;
         p.stream = s;
-        p.split = true;
+        p.split = p.early = true;  // (behind launch_expand_scaled, which lets it start after its own wait)
         if (!prefill_tc_fits(p)) return LRKV_E_SHAPE;  // (more than 65535 heads, requests or query tiles)
     }
     // (the append in one kernel lays its own rows' values out)
