@@ -128,8 +128,8 @@ struct PrefillTcArgs {
     // milliseconds: only the copies of tiles that may hold new rows wait for it.  (split: the
     // predecessor writes the page table and the history, and all copies wait.)
     bool early = false;
-    // Query tiles that leave half of the SMs idle may have two CTAs each (no window); the
-    // sums are then added up in another order.
+    // Query tiles that leave SMs idle may have two or four CTAs each (no window); the sums are
+    // then added up in another order.
     bool split = false;
 };
 int launch_prefill_tc(const PrefillTcArgs &p);

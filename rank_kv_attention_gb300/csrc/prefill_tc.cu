@@ -64,13 +64,14 @@
 // that they share), so every copy of keys and values waits; what goes before (the
 // queries, p) still overlaps.
 //
-// SPLIT (block-scaled prefill whose query tiles leave half of the SMs idle): a cluster of
-// two CTAs takes a query tile, the second the first half of its key tiles.  It hands its
-// sums (O, running maximum and sum, fp32) over through the first one's shared memory,
-// the value stages that are free by then, and the first goes on as one that had seen
-// all keys.  512 rows behind 3001, 16 heads, r = 48 (64 query tiles; the call with its
-// append): 50.1 us, 58.9 with one CTA a tile.  `early` there: the queries and p come before the
-// wait for the layout of the history.
+// SPLIT (block-scaled prefill whose query tiles leave SMs idle): a cluster of two or four
+// CTAs takes a query tile, each an equal part of its key tiles.  In pairs, then pairs of
+// pairs, one hands its sums (O, running maximum and sum, fp32) over through the other's
+// shared memory, the value stages that are free by then, and the last goes on as one that
+// had seen all keys.  16 heads, r = 48, behind 3001 rows, the call with its append: 512 rows
+// (64 query tiles) 50.1 us with two, 58.9 with one CTA a tile; 128 rows 43.6 with four, 45.8
+// with two; one row 31.8 and 34.7.  `early` there: the queries and p come before the wait for the
+// layout of the history (512 rows 49.5).
 #include <algorithm>
 
 #include "append_kernels.cuh"
@@ -104,7 +105,7 @@ struct PfBars {
     uint64_t k_full[2], v_full[2];
     uint64_t s_full[2], p_full[2], pv_done[2];
     uint64_t pair[4];  // per lane quadrant: both softmax warps posted their half (64 arrivals)
-    uint64_t peer, handed;  // SPLIT: the first CTA's stages are free; the second's sums are in them
+    uint64_t peer, handed;  // SPLIT: the taker's stages are free; the giver's sums are in them
     uint64_t out_ready;  // all 256 softmax threads staged their output row halves
     uint32_t tmem;
 };
@@ -126,10 +127,8 @@ struct PfArgs {
     float scale_log2;  // log2(e) / sqrt(d_h)
     int window, sinks;  // WIN only; both at most max_len
     bool early;
+    int split;  // SPLIT only: CTAs of a cluster, 2 or 4
 };
-
-// SPLIT: a query tile of fewer key tiles is one CTA's
-constexpr int kPfSplitTiles = 4;
 
 // Key tiles that the rows of one CTA visit, in order: tiles 0 .. ns-1 hold the
 // sinks, tiles kt0 .. the rows from `lo` (the first row of the window of the
@@ -249,7 +248,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
     PfBars &bar = *reinterpret_cast<PfBars *>(smem + PF_OFF_BAR);
     uint16_t *red = reinterpret_cast<uint16_t *>(smem + PF_OFF_RED);  // [slot][half][row]
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int h = SPLIT ? blockIdx.x >> 1 : blockIdx.x, b = blockIdx.y, tq = a.n_qtiles - 1 - (int)blockIdx.z;
+    const int h = SPLIT ? blockIdx.x / a.split : blockIdx.x, b = blockIdx.y, tq = a.n_qtiles - 1 - (int)blockIdx.z;
 
     if (tid == 256) {
         // (initialised by the thread that issues the first copies)
@@ -312,19 +311,23 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
     }
     const int max_p = p0 + t_hi - 1;  // last key position any row sees
     KeyTiles<WIN> keys(a, p0 + t_lo, max_p);
-    // the same in both CTAs of a cluster: whether they share the tiles, and this one's
-    const bool shared = SPLIT && keys.count >= kPfSplitTiles, second = SPLIT && (blockIdx.x & 1);
+    // the same in all CTAs of a cluster: how many share the tiles (two or more each), and this
+    // one's part; the first has the last tiles
+    int parts = 1;
+    const int rank = SPLIT ? (int)cluster_ctarank() : 0;
     if (SPLIT) {
-        if (second && !shared) {
+        parts = a.split;
+        while (parts > 1 && keys.count < 2 * parts) parts >>= 1;
+        if (rank >= parts) {
             if (early) pdl_wait();
+            for (int k = 0; parts > 1 && k < 2; ++k) cluster_sync_all();  // (as the others do)
             return;
         }
-        if (shared) {
-            const int cut = keys.count / 2;
-            keys.from = second ? 0 : cut;
-            keys.count = second ? cut : keys.count - cut;
-        }
+        const int k = parts - 1 - rank, from = keys.count * k / parts;
+        keys.count = keys.count * (k + 1) / parts - from;
+        keys.from = from;
     }
+    const bool shared = SPLIT && parts > 1, gives = SPLIT && rank > 0;
     const int nkt = keys.count;
 
     const int32_t *pt_row = a.page_table + (size_t)b * a.max_pages;
@@ -376,7 +379,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
         tmem_alloc(&bar.tmem, PF_TMEM_COLS);
     }
     tc_fence_before();
-    if (shared) cluster_sync_all();  // (both CTAs' barriers are there before either arrives at the other's)
+    if (shared) cluster_sync_all();  // (all barriers are there before a CTA arrives at another's)
     else __syncthreads();
     tc_fence_after();
     const uint32_t tmem = bar.tmem;
@@ -425,7 +428,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
             }
             // B_V[h] (K-major for the expansion) into the key stage tile nkt would use
             bool bv_issued = false;
-            if (kprod && ok && !second) {
+            if (kprod && ok && !gives) {
                 const int st = nkt & 1;
                 if (nkt >= 2 && !mbar_wait(&bar.s_full[st], ((nkt >> 1) - 1) & 1)) {
                     ok = false;
@@ -536,8 +539,8 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
                 tc_commit(&bar.pv_done[st]);
             }
             // E = (O_R / l)_hi B_V[h]^T + (O_R / l)_lo B_V[h]^T into score buffer 0
-            if (ok && !second) ok = mbar_wait(&bar.ex_ready, 0) && mbar_wait(&bar.bv_full, 0);
-            if (ok && !second) {
+            if (ok && !gives) ok = mbar_wait(&bar.ex_ready, 0) && mbar_wait(&bar.bv_full, 0);
+            if (ok && !gives) {
                 tc_fence_after();
                 const uint32_t bv = sw128_desc_lo(base + PF_OFF_K + (nkt & 1) * PF_STAGE, 16);
 #pragma unroll
@@ -726,54 +729,58 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
         if (shared) {
             // thread: 96 columns of its row of O, in vectors of four, 256 threads side by side
             float2 *ml = reinterpret_cast<float2 *>(red);  // (no longer read, like the value stages)
-            if (second) {
-                if (ok) ok = __all_sync(0xffffffffu, mbar_wait_cluster(&bar.peer, 0));
-                if (ok) {
-                    tc_fence_after();
-                    const uint32_t to = mapa_addr(smem_u32(smem + PF_OFF_V), 0) + tid * 16;
+            int level = 0;
+            for (int d = 1; d < parts; d <<= 1, ++level) {
+                if (rank & d) {  // to the CTA d before
+                    const uint32_t other = rank - d;
+                    if (ok) ok = __all_sync(0xffffffffu, mbar_wait_cluster(&bar.peer, 0));
+                    if (ok) {
+                        tc_fence_after();
+                        const uint32_t to = mapa_addr(smem_u32(smem + PF_OFF_V), other) + tid * 16;
 #pragma unroll 1
-                    for (int c = 0; c < 3; ++c) {
-                        uint32_t v[32];
-                        tmem_ld32(lane_base + 96 * hf + 32 * c, v);
+                        for (int c = 0; c < 3; ++c) {
+                            uint32_t v[32];
+                            tmem_ld32(lane_base + 96 * hf + 32 * c, v);
 #pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            st_cluster4(to + (8 * c + k) * 2 * PF_BM * 16, v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-                    }
-                    if (hf == 0) st_cluster2(mapa_addr(smem_u32(ml + t), 0), __float_as_uint(m), __float_as_uint(lt));
-                    mbar_arrive_cluster(mapa_rank(&bar.handed, 0));
-                }
-            } else {
-                if (ok) {
-                    mbar_arrive_cluster(mapa_rank(&bar.peer, 1));
-                    ok = __all_sync(0xffffffffu, mbar_wait_cluster(&bar.handed, 0));
-                }
-                if (ok) {
-                    tc_fence_after();
-                    const float2 other = ml[t];
-                    const float mx = fmaxf(m, other.x), ref = mx == -INFINITY ? 0.f : mx;
-                    const float f0 = ex2_approx(m - ref), f1 = ex2_approx(other.x - ref);
-                    lt = lt * f0 + other.y * f1;
-                    const float4 *in = reinterpret_cast<const float4 *>(smem + PF_OFF_V) + tid;
-#pragma unroll 1
-                    for (int c = 0; c < 3; ++c) {
-                        uint32_t v[32];
-                        tmem_ld32(lane_base + 96 * hf + 32 * c, v);
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const float4 x = in[(8 * c + k) * 2 * PF_BM];
-                            const float y[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                v[4 * k + e] = __float_as_uint(__uint_as_float(v[4 * k + e]) * f0 + y[e] * f1);
+                            for (int k = 0; k < 8; ++k)
+                                st_cluster4(to + (8 * c + k) * 2 * PF_BM * 16, v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
                         }
-                        tmem_st32(lane_base + 96 * hf + 32 * c, v);
+                        if (hf == 0) st_cluster2(mapa_addr(smem_u32(ml + t), other), __float_as_uint(m), __float_as_uint(lt));
+                        mbar_arrive_cluster(mapa_rank(&bar.handed, other));
                     }
-                    ok = pair_exchange();  // (the row's other half is read below)
+                    break;
+                }
+                if (ok) {
+                    mbar_arrive_cluster(mapa_rank(&bar.peer, rank + d));
+                    ok = __all_sync(0xffffffffu, mbar_wait_cluster(&bar.handed, level & 1));
+                }
+                if (!ok) break;
+                tc_fence_after();
+                const float2 other = ml[t];
+                const float mx = fmaxf(m, other.x), ref = mx == -INFINITY ? 0.f : mx;
+                const float f0 = ex2_approx(m - ref), f1 = ex2_approx(other.x - ref);
+                lt = lt * f0 + other.y * f1;
+                m = mx;
+                const float4 *in = reinterpret_cast<const float4 *>(smem + PF_OFF_V) + tid;
+#pragma unroll 1
+                for (int c = 0; c < 3; ++c) {
+                    uint32_t v[32];
+                    tmem_ld32(lane_base + 96 * hf + 32 * c, v);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const float4 x = in[(8 * c + k) * 2 * PF_BM];
+                        const float y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            v[4 * k + e] = __float_as_uint(__uint_as_float(v[4 * k + e]) * f0 + y[e] * f1);
+                    }
+                    tmem_st32(lane_base + 96 * hf + 32 * c, v);
                 }
             }
+            if (ok && !gives) ok = pair_exchange();  // (the row's other half is read below)
         }
         const float inv_l = lt > 0.f || (WIN && lt != 0.f) ? 1.f / lt : 0.f;  // (NaN stays NaN)
-        if (ok && !second) {
+        if (ok && !gives) {
             // (O_R / l) in bf16 halves over p's columns: half 0 the high part, half 1 the low part
             tc_fence_after();
             uint32_t v[32], pk[32];
@@ -795,7 +802,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
             mbar_arrive(&bar.ex_ready);
             ok = __all_sync(0xffffffffu, mbar_wait(&bar.ex_done, 0));
         }
-        if (ok && !second) {
+        if (ok && !gives) {
             tc_fence_after();
             // a full tile is staged in the q buffer (TMA swizzle layout, half hf
             // holds output columns 64 hf .. 64 hf + 63) and written by two TMA
@@ -849,7 +856,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
 
     tc_fence_before();
     __syncthreads();
-    if (shared) cluster_sync_all();  // neither CTA leaves while the other may still write to it
+    if (shared) cluster_sync_all();  // no CTA leaves while another may still write to it
     if (warp == 8) {
         tc_fence_after();
         tmem_dealloc(tmem, PF_TMEM_COLS);
@@ -866,12 +873,12 @@ template <int R16>
 cudaError_t launch_split(const PfMaps &maps, const PfArgs &a, dim3 grid, cudaStream_t s) {
     cudaError_t e = smem_limit_once(prefill_tc_kernel<R16, false, true>, PF_SMEM);
     if (e != cudaSuccess) return e;
-    grid.x *= 2;
-    return launch_pdl_clusters(prefill_tc_kernel<R16, false, true>, 2, grid, dim3(PF_THREADS), PF_SMEM, s, maps, a);
+    grid.x *= a.split;
+    return launch_pdl_clusters(prefill_tc_kernel<R16, false, true>, a.split, grid, dim3(PF_THREADS), PF_SMEM, s, maps, a);
 }
 template <int R16>
-cudaError_t launch_r16(const PfMaps &maps, const PfArgs &a, dim3 grid, bool split, cudaStream_t s) {
-    if (split) return launch_split<R16>(maps, a, grid, s);
+cudaError_t launch_r16(const PfMaps &maps, const PfArgs &a, dim3 grid, cudaStream_t s) {
+    if (a.split > 1) return launch_split<R16>(maps, a, grid, s);
     return a.window ? launch_win<R16, true>(maps, a, grid, s) : launch_win<R16, false>(maps, a, grid, s);
 }
 
@@ -955,13 +962,15 @@ int launch_prefill_tc(const PrefillTcArgs &p) {
     // rows come first and leave at once (in `early` after the append): 64 requests, one
     // of 8192 rows and 63 of one, take 519 us where the 8192 rows alone take 163
     const dim3 grid(c.H, p.B, n_qtiles);
-    const bool split = p.split && !a.window && 2 * (int64_t)c.H * p.B * n_qtiles <= device_sm_count();
+    // (clusters of four CTAs, one per SM, leave some SMs of a die's groups over: 36 of 38 fit)
+    const int64_t tiles = (int64_t)c.H * p.B * n_qtiles, sms = device_sm_count();
+    a.split = !p.split || a.window || 2 * tiles > sms ? 1 : 4 * tiles > sms - 8 ? 2 : 4;
     cudaError_t e;
     switch ((c.r + 15) / 16) {
-        case 1: e = launch_r16<1>(maps, a, grid, split, p.stream); break;
-        case 2: e = launch_r16<2>(maps, a, grid, split, p.stream); break;
-        case 3: e = launch_r16<3>(maps, a, grid, split, p.stream); break;
-        default: e = launch_r16<4>(maps, a, grid, split, p.stream); break;
+        case 1: e = launch_r16<1>(maps, a, grid, p.stream); break;
+        case 2: e = launch_r16<2>(maps, a, grid, p.stream); break;
+        case 3: e = launch_r16<3>(maps, a, grid, p.stream); break;
+        default: e = launch_r16<4>(maps, a, grid, p.stream); break;
     }
     return e == cudaSuccess ? 0 : -(int)e;
 }

@@ -609,14 +609,15 @@ def test_prefill_on_bad_pages(H, d_h, r, ps):
 
 SPLIT = [(16, 48, 64, 32, [700], [300]), (16, 48, 64, 64, [511], [1]), (16, 64, 128, 64, [300, 512], [128, 100]),
          (32, 32, 64, 64, [1400], [256]), (4, 16, 64, 16, [-40], [900]), (4, 56, 64, 64, [384, 385, 1000], [1, 130, 257]),
-         (8, 8, 192, 48, [900], [127]), (16, 40, 64, 64, [3001], [512])]
+         (8, 8, 192, 48, [900], [127]), (16, 40, 64, 64, [3001], [512]), (16, 48, 64, 64, [3001], [100]),
+         (4, 48, 64, 64, [100, 513, 1300, 900], [20, 3, 128, 129]), (32, 16, 64, 32, [1000], [5])]
 
 
 @pytest.mark.parametrize("bad", [False, True])
 @pytest.mark.parametrize("H,r,ps,block,start,rows_of", SPLIT)
 def test_prefill_of_few_query_tiles(H, r, ps, block, start, rows_of, bad):
-    """Chunks behind long histories, whose query tiles leave SMs idle: two CTAs share a tile's keys.  bad: pages missing in
-    the first and in the second one's part."""
+    """Chunks behind long histories, whose query tiles leave SMs idle: CTAs share a tile's keys.  bad: pages missing near both
+    ends."""
     import rank_kv_attention_gb300 as L
     rng = np.random.default_rng(H * r + sum(rows_of) + bad)
     B, d = len(start), 64
