@@ -49,7 +49,11 @@ __device__ __forceinline__ float dot8(const uint2 &w, const float *y, float s) {
     return s;
 }
 
+// NI: groups of 128 value columns.  HALF (64 columns at most): a half-warp adds a row's values up, so
+// a warp takes two rows at a time.
+template <int NI, bool HALF>
 __global__ void __launch_bounds__(kThreads) decode_scaled_any_kernel(const __grid_constant__ AnyArgs P) {
+    constexpr int kRows = 8, kStep = HALF ? 2 : 1;  // loads on their way, rows of one
     __shared__ __align__(16) float qs[256], ps[256];
     __shared__ float ms[kWarps], ls[kWarps], red[kWarps][512];
     const ScaledDecodeArgs &a = P.d;
@@ -89,7 +93,8 @@ __global__ void __launch_bounds__(kThreads) decode_scaled_any_kernel(const __gri
 
     const int32_t *table = a.page_table + (size_t)(a.req_row ? a.req_row[b] : b) * a.max_pages;
     const int sw = c.G * d_h, rw = H * r;  // bytes of a token's shared and private row
-    float m = -INFINITY, l = 0.f, as[2][4] = {}, ar[2][4] = {};
+    float m = -INFINITY, l = 0.f, as[NI][4] = {}, ar[NI][4] = {};
+    const int col0 = HALF ? 4 * (lane & 15) : 4 * lane, half = HALF ? lane >> 4 : 0;
     for (int t0 = begin + 32 * warp; t0 < end; t0 += kThreads) {
         const int j = t0 + lane;
         int row = -1;
@@ -105,7 +110,13 @@ __global__ void __launch_bounds__(kThreads) decode_scaled_any_kernel(const __gri
                       e3 = c.exp[3][eb * H + h];
             const uint8_t *sk = c.code[0] + (int64_t)row * sw + g * d_h, *rk = c.code[2] + (int64_t)row * rw + h * r;
             float s = 0.f, t = 0.f;
-            for (int d = 0; d < d_h; d += 8) s = dot8(*reinterpret_cast<const uint2 *>(sk + d), qs + d, s);
+#pragma unroll 4
+            for (int d = 0; d < d_h; d += 16) {
+                const uint4 w = *reinterpret_cast<const uint4 *>(sk + d);
+                s = dot8(make_uint2(w.x, w.y), qs + d, s);
+                s = dot8(make_uint2(w.z, w.w), qs + d + 8, s);
+            }
+#pragma unroll 4
             for (int k = 0; k < r; k += 8) t = dot8(*reinterpret_cast<const uint2 *>(rk + k), ps + k, t);
             x = (s * exp2i(clamp_exp(e0)) + t * exp2i(clamp_exp(e2))) * P.scale_log2;
             vs = exp2i(clamp_exp(e1));
@@ -122,35 +133,50 @@ __global__ void __launch_bounds__(kThreads) decode_scaled_any_kernel(const __gri
         vs *= w;
         vr *= w;
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < NI; ++i)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 as[i][e] *= alpha;
                 ar[i][e] *= alpha;
             }
-        const int rows = min(32, end - t0);
-        for (int t = 0; t < rows; ++t) {
-            const int rt = __shfl_sync(0xffffffffu, row, t);
-            const float ws = __shfl_sync(0xffffffffu, vs, t), wr = __shfl_sync(0xffffffffu, vr, t);
-            if (rt < 0) continue;
-            const uint8_t *sv = c.code[1] + (int64_t)rt * sw + g * d_h, *rv = c.code[3] + (int64_t)rt * rw + h * r;
+        // (rows past the part, or on no page, are zeros of weight zero)
+#pragma unroll 1
+        for (int t = 0; t < min(32, end - t0); t += kRows * kStep) {
+            uint32_t cs[NI][kRows], cr[NI][kRows];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int col = 4 * lane + 128 * i;
-                float y[4];
-                if (col < d_h) {
-                    widen4(*reinterpret_cast<const uint32_t *>(sv + col), y);
+            for (int u = 0; u < kRows; ++u) {
+                const int rt = __shfl_sync(0xffffffffu, row, t + u * kStep + half);
+                const uint8_t *sv = c.code[1] + (int64_t)rt * sw + g * d_h, *rv = c.code[3] + (int64_t)rt * rw + h * r;
+#pragma unroll
+                for (int i = 0; i < NI; ++i) {
+                    const int col = col0 + 128 * i;
+                    cs[i][u] = rt >= 0 && col < d_h ? *reinterpret_cast<const uint32_t *>(sv + col) : 0;
+                    cr[i][u] = rt >= 0 && col < r ? *reinterpret_cast<const uint32_t *>(rv + col) : 0;
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < kRows; ++u) {
+                const float ws = __shfl_sync(0xffffffffu, vs, t + u * kStep + half);
+                const float wr = __shfl_sync(0xffffffffu, vr, t + u * kStep + half);
+#pragma unroll
+                for (int i = 0; i < NI; ++i) {
+                    float y[4];
+                    widen4(cs[i][u], y);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) as[i][e] = fmaf(ws, y[e], as[i][e]);
-                }
-                if (col < r) {
-                    widen4(*reinterpret_cast<const uint32_t *>(rv + col), y);
+                    widen4(cr[i][u], y);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) ar[i][e] = fmaf(wr, y[e], ar[i][e]);
                 }
             }
         }
     }
+    if (HALF)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            as[0][e] += __shfl_xor_sync(0xffffffffu, as[0][e], 16);
+            ar[0][e] += __shfl_xor_sync(0xffffffffu, ar[0][e], 16);
+        }
 #pragma unroll
     for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
     if (lane == 0) {
@@ -158,8 +184,8 @@ __global__ void __launch_bounds__(kThreads) decode_scaled_any_kernel(const __gri
         ls[warp] = l;
     }
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int col = 4 * lane + 128 * i;
+    for (int i = 0; i < NI; ++i) {
+        const int col = col0 + 128 * i;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             if (col < d_h) red[warp][col + e] = as[i][e];
@@ -360,8 +386,11 @@ cudaError_t launch_decode_scaled_any(const ScaledDecodeArgs &a, void *ws) {
     P.splits = any_splits(a.c, a.B, a.max_seq_len);
     P.st = scaled_states(ws, (int64_t)a.B * P.splits, a.c.H);
     P.scale_log2 = 1.4426950408889634f / sqrtf((float)a.c.d_h);
-    cudaError_t e = launch_pdl(decode_scaled_any_kernel, dim3((unsigned)(a.B * P.splits), a.c.H), dim3(kThreads), 0,
-                               a.stream, P);
+    const int cols = std::max(a.c.d_h, a.c.r);
+    const auto kernel = cols <= 64    ? decode_scaled_any_kernel<1, true>
+                        : cols <= 128 ? decode_scaled_any_kernel<1, false>
+                                      : decode_scaled_any_kernel<2, false>;
+    cudaError_t e = launch_pdl(kernel, dim3((unsigned)(a.B * P.splits), a.c.H), dim3(kThreads), 0, a.stream, P);
     if (e != cudaSuccess) return e;
     ScaledMergeArgs m;
     m.st = P.st;
