@@ -8,13 +8,15 @@
 //
 // One CTA takes a part of a request's rows for one head.  A warp takes 32 rows at
 // a time: lane j scores row j (q and p from shared memory), the warp updates its
-// running maximum and sum, then every lane adds the rows' values up for four
-// columns of each 128.  The shared rows are read again by every head (out of
-// L2), and the four warps' states meet in shared memory.
+// running maximum and sum, then its lanes add the rows' values up, four columns each,
+// eight loads of a pool on their way at once.  The shared rows are read again by every head
+// (out of L2), and the four warps' states meet in shared memory.
 //
-// Bound by the lanes' own loads of rows r or d_h bytes apart and by the conversions of every
-// code, once a head.  16 requests of 4096 rows in a graph: d_h = 64, r = 16, 8 heads 86 us (3.7 at
-// the copy bandwidth); d_h = 128, r = 72, 12 heads 240 (19.2); d_h = 128, r = 16, 40 heads 606 (14.9).
+// Bound by the lanes' loads of rows r or d_h bytes apart, their latency, and the conversions of
+// every code, once a head.  In a graph, 16 requests of 4096 rows: d_h = 64, r = 16, 8 heads
+// 37 us (3.7 at the copy bandwidth); d_h = 32, r = 40, 6 heads 31; d_h = 128, r = 72, 12 heads 140
+// (19.2); d_h = 128, r = 16, 40 heads 315 (14.9).  One load of a row's values at a time took 86, 63,
+// 240 and 605.
 #include <algorithm>
 
 #include "scaled_kernels.cuh"
@@ -50,9 +52,11 @@ __device__ __forceinline__ float dot8(const uint2 &w, const float *y, float s) {
 }
 
 // NI: groups of 128 value columns.  HALF (64 columns at most): a half-warp adds a row's values up, so
-// a warp takes two rows at a time.
+// a warp takes two rows at a time, and the next rows' pages are looked up ahead in 72
+// registers (37 us of the first case above, 42 in 96, 47 without the look ahead; with 128
+// columns it costs registers that the loads need: 140 us of the third, 168 with it).
 template <int NI, bool HALF>
-__global__ void __launch_bounds__(kThreads) decode_scaled_any_kernel(const __grid_constant__ AnyArgs P) {
+__global__ void __launch_bounds__(kThreads, HALF ? 7 : 5) decode_scaled_any_kernel(const __grid_constant__ AnyArgs P) {
     constexpr int kRows = 8, kStep = HALF ? 2 : 1;  // loads on their way, rows of one
     __shared__ __align__(16) float qs[256], ps[256];
     __shared__ float ms[kWarps], ls[kWarps], red[kWarps][512];
@@ -95,15 +99,20 @@ __global__ void __launch_bounds__(kThreads) decode_scaled_any_kernel(const __gri
     const int sw = c.G * d_h, rw = H * r;  // bytes of a token's shared and private row
     float m = -INFINITY, l = 0.f, as[NI][4] = {}, ar[NI][4] = {};
     const int col0 = HALF ? 4 * (lane & 15) : 4 * lane, half = HALF ? lane >> 4 : 0;
-    for (int t0 = begin + 32 * warp; t0 < end; t0 += kThreads) {
-        const int j = t0 + lane;
+    auto lookup = [&](int j) {
         int row = -1;
-        float x = -INFINITY, vs = 0.f, vr = 0.f;
         if (j < end) {
             const int32_t page = table[j / c.page_size];
             if (page < 0 || page >= c.num_pages) status_or(a.status, LRKV_STATUS_BAD_PAGE);
             else row = page * c.page_size + j % c.page_size;
         }
+        return row;
+    };
+    int next = HALF ? lookup(begin + 32 * warp + lane) : 0;
+    for (int t0 = begin + 32 * warp; t0 < end; t0 += kThreads) {
+        const int row = HALF ? next : lookup(t0 + lane);
+        if (HALF) next = lookup(t0 + kThreads + lane);  // (on its way meanwhile)
+        float x = -INFINITY, vs = 0.f, vr = 0.f;
         if (row >= 0) {
             const int64_t eb = row / c.block;
             const int e0 = c.exp[0][eb * c.G + g], e1 = c.exp[1][eb * c.G + g], e2 = c.exp[2][eb * H + h],
