@@ -503,8 +503,10 @@ LRKV_API int lrkv_prefill_window(const void *X, const void *Q, const int32_t *cu
  * bf16.  On tensor cores (d_h = 128, G = 1, H a multiple of 4 up to 32, r up to 64,
  * and what of it fits in tensor memory) the codes are multiplied as
  * they are: q, q B_K[h] and the weights enter as sums of two or three E4M3 terms
- * (at least bf16's precision; a weight below 2^-126 of the largest counts as
- * zero), and the scales are applied to the sums.  Rows
+ * (q and q B_K[h] off by at most 2^-14 of an element or 2^-26 of the largest; a row's
+ * weight times the scale of its values by 2^-9, or 2^-22 of the largest of its tile of
+ * 128 rows), and the scales are applied to the sums.  Scales may lie anywhere in their range,
+ * next to each other: sums are kept relative to their own largest term.  Rows
  * that a query sees must hold no NaN code there: a NaN reaches other heads of
  * the request.  What pages hold past a request's length never matters.
  * Workspace: lrkv_decode_scaled_workspace_bytes bytes; that never falls as B or

@@ -26,7 +26,10 @@
 // Scales: a token's exponent enters its score, x + e, before the exponential: the
 // value products take 2^(x + eS - MS) and 2^(x + eR - MR), each relative to the tile's
 // largest per head, so tokens of loud and quiet blocks keep their precision next
-// to each other.  Sums, maxima and the accumulators over tiles are fp32 in registers.
+// to each other.  The accumulators over tiles are relative to the largest x + eS and x + eR so
+// far, not to the largest x: values lie between 2^-126 and 2^128, and neither a sum of loud
+// ones nor a weight of a quiet one would fit in fp32 beside the value's own scale.  Sums,
+// maxima and the accumulators are fp32 in registers.
 //
 // Work: the requests' rows in units of 64 tokens, laid end to end and cut evenly
 // over one CTA per SM; a CTA walks its tiles (two units of one request, or one).
@@ -146,14 +149,15 @@ struct Bars {
 
 // Shared memory after the ring of stages.
 struct Offsets {
-    int img, weights, red, fac, scales, ar, bars, bytes;
+    int img, weights, red, fac, tops, scales, ar, bars, bytes;
     __host__ __device__ explicit Offsets(const Shape &s) {
         img = s.stages * kStageBytes;
         const int one = (s.img_bytes + 1023) / 1024 * 1024;
         weights = img + 2 * one;
         red = weights + 4 * s.wrows * 128;  // [2][4 quarters of the heads][maxima 3, sum][8][4 warps]
-        fac = red + 2 * 4 * 4 * 8 * 4 * 4;  // [4][3][32]: alpha, shared and private factor
-        scales = fac + 4 * 3 * 32 * 4;      // [2][8 groups of 16 tokens][kScaleRow]
+        fac = red + 2 * 4 * 4 * 8 * 4 * 4;  // [4][4][32]: what the shared sums and this tile's are multiplied by; the private
+        tops = fac + 4 * 4 * 32 * 4;        // [2][32]: largest x + eS and x + eR of the request so far
+        scales = tops + 2 * 32 * 4;         // [2][8 groups of 16 tokens][kScaleRow]
         ar = scales + 2 * 8 * kScaleRow * 4;  // [box][128]: the private accumulators
         bars = ar + s.boxes * 512;
         bytes = bars + (int)sizeof(Bars) + 1024;
@@ -177,17 +181,6 @@ struct Args {
 
 __device__ __forceinline__ int units_of(int L, int max_len) {
     return L >= 1 && L <= max_len ? (L + kUnit - 1) / kUnit : 0;
-}
-
-__device__ __forceinline__ float ex2f(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ float warp_max(float x) {
-    float y;
-    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
-    return y;
 }
 
 template <int N> __device__ __forceinline__ void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
@@ -711,6 +704,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // warp: tokens 32 (warp & 3) + lane of a tile, heads h0 .. h0 + hn - 1 (a quarter)
         const int hn = H / 4, grp = warp >> 2, h0 = grp * hn, token = 32 * (warp & 3) + lane;
         float l[HT], m = -INFINITY;  // m: of lane k's head h0 + k, the same in all four warps
+        // (largest x + eS and x + eR: written and read by lane k of the first warp)
+        float *tops = reinterpret_cast<float *>(smem + off.tops) + h0 + lane;
         uint32_t met = 0;
         auto meet = [&]() -> bool {  // the four warps of these heads
             mbar_arrive(&bar.meet[grp]);
@@ -724,6 +719,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int seg = last = w.seg;
             if (first) {
                 m = -INFINITY;
+                if ((warp & 3) == 0 && lane < hn) tops[0] = tops[32] = -INFINITY;
 #pragma unroll
                 for (int k = 0; k < HT; ++k) l[k] = 0.f;
                 ok = __all_sync(0xffffffffu, mbar_wait(&bar.img_full[seg & 1], (seg >> 1) & 1));
@@ -788,9 +784,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             // the operand of the tile before the last has been read
             if (ok && i > 1) ok = __all_sync(0xffffffffu, mbar_wait(&bar.pv_done[i & 1], ((i >> 1) - 1) & 1));
             if (!ok) break;
-            // lane k: what head h0 + k needs.  Weights are relative to the running maximum (one
-            // that underflows counts as zero); the operands' to the tile's largest
-            float alpha = 0.f, ref = 0.f, fs = 0.f, fr = 0.f;
+            // lane k: what head h0 + k needs.  Of the weights' sum, weights relative to the running
+            // maximum; of the operands, weights times scales relative to the tile's largest, which
+            // becomes 2^8, and the value sums are relative to their own running maxima
+            float alpha = 0.f, ref = 0.f, ms = 0.f, mr = 0.f;
             if (lane < hn) {
                 float M[3];
 #pragma unroll
@@ -799,22 +796,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                     M[j] = fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w));
                 }
                 const float mn = fmaxf(m, M[0]);
-                ref = mn == -INFINITY ? 0.f : mn;
-                const float ms = M[1] == -INFINITY ? ref : M[1] - 8.f, mr = M[2] == -INFINITY ? ref : M[2] - 8.f;
+                ref = ref_of(mn);
+                ms = ref_of(M[1]) - 8.f;
+                mr = ref_of(M[2]) - 8.f;
                 alpha = ex2f(m - ref);
                 m = mn;
-                // (bounded: where it is larger than that every weight has underflown)
-                fs = ex2f(fminf(ref - ms, 125.f));
-                fr = ex2f(fminf(ref - mr, 125.f));
                 if ((warp & 3) == 0) {
-                    float *fac = reinterpret_cast<float *>(smem + off.fac) + (i & 3) * 3 * 32 + h0 + lane;
-                    fac[0] = alpha;
-                    fac[32] = ex2f(ms - ref);
-                    fac[64] = ex2f(mr - ref);
+                    float *fac = reinterpret_cast<float *>(smem + off.fac) + (i & 3) * 4 * 32 + h0 + lane;
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const float was = tops[32 * j], now = fmaxf(was, M[1 + j]);
+                        fac[64 * j] = ex2f(was - ref_of(now));
+                        fac[64 * j + 32] = ex2f(M[1 + j] - 8.f - ref_of(now));
+                        tops[32 * j] = now;
+                    }
                 }
             }
             uint8_t *ws = smem + off.weights + (i & 1) * 2 * S.wrows * 128, *wr = ws + S.wrows * 128;
-            const float vs = exp2i((int)es);
 #pragma unroll
             for (int k = 0; k < HT; ++k)
                 if (k < hn) {
@@ -822,8 +820,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float w = ex2f(x[k] - __shfl_sync(0xffffffffu, ref, k));
                     l[k] = l[k] * __shfl_sync(0xffffffffu, alpha, k) + w;
                     // both operands' terms, a pair at a time
-                    const float y = w * vs * __shfl_sync(0xffffffffu, fs, k);
-                    const float z = w * exp2i((int)er[k]) * __shfl_sync(0xffffffffu, fr, k);
+                    const float y = ex2f(x[k] + es - __shfl_sync(0xffffffffu, ms, k));
+                    const float z = ex2f(x[k] + er[k] - __shfl_sync(0xffffffffu, mr, k));
                     const uint16_t t1 = e4m3x2_from_f32(y, z);
                     const uint32_t h2 = f16x2_from_e4m3x2(t1);
                     const float2 g = __half22float2(*reinterpret_cast<const __half2 *>(&h2));
@@ -850,9 +848,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane < hn) red[(3 * HT + lane) * 4 + (warp & 3)] = sum;
                 if (!(ok = meet())) break;
                 if ((warp & 3) == 0 && lane < hn) {
-                    float2 *ml = reinterpret_cast<float2 *>(a.st.ml) + ((int64_t)w.b + blockIdx.x) * H + h0;
                     const float4 v = *reinterpret_cast<const float4 *>(&red[(3 * HT + lane) * 4]);
-                    ml[lane] = make_float2(m, (v.x + v.y) + (v.z + v.w));
+                    a.st.head[((int64_t)w.b + blockIdx.x) * H + h0 + lane] = make_float4(m, (v.x + v.y) + (v.z + v.w), tops[0], tops[32]);
                 }
             }
         }
@@ -881,7 +878,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             const int vb = S.vbufs == 2 ? i & 1 : 0;
             const uint32_t from = lanes + vb * S.vcols;
-            const float *fac = reinterpret_cast<const float *>(smem + off.fac) + (i & 3) * 3 * 32;
+            const float *fac = reinterpret_cast<const float *>(smem + off.fac) + (i & 3) * 4 * 32;
 #pragma unroll
             for (int g = 0; g < HM / 16; ++g)
                 if (16 * g < H) {
@@ -930,7 +927,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         const bool up = h == hB;
                         const float y = __uint_as_float(up ? u[j][0] : v[j][0]) + __uint_as_float(up ? u[j][1] : v[j][1]) * 0.0625f;
-                        ar[128 * t] = first ? y * fac[64 + h] : ar[128 * t] * fac[h] + y * fac[64 + h];
+                        ar[128 * t] = first ? y * fac[96 + h] : ar[128 * t] * fac[64 + h] + y * fac[96 + h];
                     }
             }
             tc_fence_before();

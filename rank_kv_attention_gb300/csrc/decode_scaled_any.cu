@@ -59,7 +59,7 @@ template <int NI, bool HALF>
 __global__ void __launch_bounds__(kThreads, HALF ? 7 : 5) decode_scaled_any_kernel(const __grid_constant__ AnyArgs P) {
     constexpr int kRows = 8, kStep = HALF ? 2 : 1;  // loads on their way, rows of one
     __shared__ __align__(16) float qs[256], ps[256];
-    __shared__ float ms[kWarps], ls[kWarps], red[kWarps][512];
+    __shared__ float ls[kWarps], tops[3][kWarps], red[kWarps][512];  // tops: m, ks, kr
     const ScaledDecodeArgs &a = P.d;
     const ScaledPools &c = a.c;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -75,12 +75,9 @@ __global__ void __launch_bounds__(kThreads, HALF ? 7 : 5) decode_scaled_any_kern
     const int begin = (int)min(first, (int64_t)(valid ? L : 0)), end = (int)min(first + part, (int64_t)(valid ? L : 0));
 
     const int64_t slot = (int64_t)b * P.splits + sp;
-    float *ml = P.st.ml + (slot * H + h) * 2;
+    float4 *head = P.st.head + slot * H + h;
     if (begin >= end) {  // (an empty part: a state without weight)
-        if (tid == 0) {
-            ml[0] = -INFINITY;
-            ml[1] = 0.f;
-        }
+        if (tid == 0) *head = make_float4(-INFINITY, 0.f, -INFINITY, -INFINITY);
         return;
     }
     const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q) + ((size_t)b * H + h) * d_h;
@@ -97,7 +94,8 @@ __global__ void __launch_bounds__(kThreads, HALF ? 7 : 5) decode_scaled_any_kern
 
     const int32_t *table = a.page_table + (size_t)(a.req_row ? a.req_row[b] : b) * a.max_pages;
     const int sw = c.G * d_h, rw = H * r;  // bytes of a token's shared and private row
-    float m = -INFINITY, l = 0.f, as[NI][4] = {}, ar[NI][4] = {};
+    // largest x, x + eS and x + eR so far, what the sums are relative to
+    float m = -INFINITY, ks = -INFINITY, kr = -INFINITY, l = 0.f, as[NI][4] = {}, ar[NI][4] = {};
     const int col0 = HALF ? 4 * (lane & 15) : 4 * lane, half = HALF ? lane >> 4 : 0;
     auto lookup = [&](int j) {
         int row = -1;
@@ -128,25 +126,25 @@ __global__ void __launch_bounds__(kThreads, HALF ? 7 : 5) decode_scaled_any_kern
 #pragma unroll 4
             for (int k = 0; k < r; k += 8) t = dot8(*reinterpret_cast<const uint2 *>(rk + k), ps + k, t);
             x = (s * exp2i(clamp_exp(e0)) + t * exp2i(clamp_exp(e2))) * P.scale_log2;
-            vs = exp2i(clamp_exp(e1));
-            vr = exp2i(clamp_exp(e3));
+            vs = (float)clamp_exp(e1);
+            vr = (float)clamp_exp(e3);
         }
-        float mt = x;
-#pragma unroll
-        for (int o = 16; o; o >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, o));
-        const float mn = fmaxf(m, mt);
-        const float ref = mn == -INFINITY ? 0.f : mn;
-        const float alpha = exp2f(m - ref), w = exp2f(x - ref);
+        vs += x;
+        vr += x;
+        const float mn = fmaxf(m, warp_max(x)), sn = fmaxf(ks, warp_max(vs)), rn = fmaxf(kr, warp_max(vr));
+        l = l * exp2f(m - ref_of(mn)) + exp2f(x - ref_of(mn));
+        const float alpha = exp2f(ks - ref_of(sn)), beta = exp2f(kr - ref_of(rn));
+        vs = exp2f(vs - ref_of(sn));
+        vr = exp2f(vr - ref_of(rn));
         m = mn;
-        l = l * alpha + w;
-        vs *= w;
-        vr *= w;
+        ks = sn;
+        kr = rn;
 #pragma unroll
         for (int i = 0; i < NI; ++i)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 as[i][e] *= alpha;
-                ar[i][e] *= alpha;
+                ar[i][e] *= beta;
             }
         // (rows past the part, or on no page, are zeros of weight zero)
 #pragma unroll 1
@@ -189,8 +187,10 @@ __global__ void __launch_bounds__(kThreads, HALF ? 7 : 5) decode_scaled_any_kern
 #pragma unroll
     for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
     if (lane == 0) {
-        ms[warp] = m;
         ls[warp] = l;
+        tops[0][warp] = m;
+        tops[1][warp] = ks;
+        tops[2][warp] = kr;
     }
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
@@ -202,35 +202,35 @@ __global__ void __launch_bounds__(kThreads, HALF ? 7 : 5) decode_scaled_any_kern
         }
     }
     __syncthreads();
-    float M = ms[0];
+    float M[3], f[3][kWarps], lt = 0.f;
 #pragma unroll
-    for (int w = 1; w < kWarps; ++w) M = fmaxf(M, ms[w]);
-    const float ref = M == -INFINITY ? 0.f : M;
-    float f[kWarps], lt = 0.f;
+    for (int k = 0; k < 3; ++k) {
+        M[k] = tops[k][0];
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-        f[w] = exp2f(ms[w] - ref);
-        lt += ls[w] * f[w];
+        for (int w = 1; w < kWarps; ++w) M[k] = fmaxf(M[k], tops[k][w]);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) f[k][w] = exp2f(tops[k][w] - ref_of(M[k]));
     }
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) lt += ls[w] * f[0][w];
     float *acc = P.st.acc + slot * H * (d_h + r);
     for (int i = tid; i < d_h + r; i += kThreads) {
         const int at = i < d_h ? i : 256 + i - d_h;
         float s = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) s += red[w][at] * f[w];
+        for (int w = 0; w < kWarps; ++w) s += red[w][at] * (i < d_h ? f[1][w] : f[2][w]);
         if (i < d_h) acc[(size_t)h * d_h + i] = s;
         else acc[(size_t)H * d_h + h * r + i - d_h] = s;
     }
-    if (tid == 0) {
-        ml[0] = M;
-        ml[1] = lt;
-    }
+    if (tid == 0) *head = make_float4(M[0], lt, M[1], M[2]);
 }
 
 // ---------------------------------------------------------------------------
-// Merge: one CTA per (request, head).  o = (sum_s f_s accS_s + (sum_s f_s accR_s)
-// B_V[h]^T) / sum_s f_s l_s with f_s = 2^(m_s - max m).  Groups of threads, one thread
-// a column, take the states in turn.
+// Merge: one CTA per (request, head).  With f_s = 2^(m_s - M), gS_s = 2^(kS_s - KS) and gR_s
+// = 2^(kR_s - KR) relative to the largest of all states, l = sum_s f_s l_s, the means are
+// S = 2^(KS - M) (sum_s gS_s accS_s) / l and R alike, and o = S + R B_V[h]^T.  (KS - M and KR -
+// M lie in the exponents' range.)  Groups of threads, one thread a column, take the states in
+// turn.
 //
 // All of it is latency (about a microsecond for a round trip to memory that other
 // SMs have just written): before the wait it reads what is there already, B_V[h] and the
@@ -241,8 +241,8 @@ constexpr int kMergeStates = 256, kMergeB = 3;
 
 template <int THREADS, int HELD>
 __global__ void __launch_bounds__(THREADS, HELD == 4 ? 6 : 2) scaled_merge_kernel(const __grid_constant__ ScaledMergeArgs P) {
-    __shared__ float fs[kMergeStates], sums[512], part[kMergeB * THREADS];
-    __shared__ float red[2][THREADS / 32];
+    __shared__ float gs[2][kMergeStates], sums[512], part[kMergeB * THREADS];
+    __shared__ float red[4][THREADS / 32], up[2];
     const int h = blockIdx.y, b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int H = P.H, d_h = P.d_h, r = P.r, W = d_h + r, cols = (W + 31) & ~31;
     // ---- B_V[h] in tasks of eight columns of a row: the first ones of every thread.  (The
@@ -267,8 +267,9 @@ __global__ void __launch_bounds__(THREADS, HELD == 4 ? 6 : 2) scaled_merge_kerne
     }
     const int ns = place.y;  // at most 256 parts, or a state of every CTA
     const int64_t s0 = place.x;
-    float2 ml = make_float2(-INFINITY, 0.f);
-    if (tid < ns) ml = reinterpret_cast<const float2 *>(P.st.ml)[(s0 + tid) * H + h];
+    float4 st = make_float4(-INFINITY, 0.f, -INFINITY, -INFINITY);
+    const float4 *heads = P.st.head + (s0 * H + h);
+    if (tid < ns) st = heads[tid * H];
     const int groups = max(1, THREADS / cols), g = tid / cols, c0 = tid - g * cols;
     const bool mine = g < groups && c0 < W;
     auto column = [&](int c) { return P.st.acc + s0 * H * W + (c < d_h ? h * d_h + c : H * d_h + h * r + c - d_h); };
@@ -279,18 +280,28 @@ __global__ void __launch_bounds__(THREADS, HELD == 4 ? 6 : 2) scaled_merge_kerne
         const int s = g + j * groups;
         held[j] = mine && s < ns ? acc[(int64_t)s * H * W] : 0.f;
     }
-    float M = ml.x;
-#pragma unroll
-    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    if (lane == 0) red[0][warp] = M;
+    float M = warp_max(st.x), KS = warp_max(st.z), KR = warp_max(st.w);
+    if (lane == 0) {
+        red[0][warp] = M;
+        red[2][warp] = KS;
+        red[3][warp] = KR;
+    }
     __syncthreads();
-#pragma unroll
-    for (int w = 0; w < THREADS / 32; ++w) M = fmaxf(M, red[0][w]);
+    const int w = lane % (THREADS / 32);
+    M = warp_max(red[0][w]);
+    KS = warp_max(red[2][w]);
+    KR = warp_max(red[3][w]);
     // a part without rows (m = -inf, l = 0) has written no value sums
-    const bool none = ml.x == -INFINITY && ml.y == 0.f;
-    const float f = none ? 0.f : exp2f(ml.x - (M == -INFINITY ? 0.f : M));
-    if (tid < kMergeStates) fs[tid] = none ? -1.f : f;
-    float l = none ? 0.f : ml.y * f;
+    const bool none = st.x == -INFINITY && st.y == 0.f;
+    if (tid == 0) {
+        up[0] = ex2f(KS - ref_of(M));
+        up[1] = ex2f(KR - ref_of(M));
+    }
+    if (tid < kMergeStates) {
+        gs[0][tid] = none ? -1.f : ex2f(st.z - ref_of(KS));
+        gs[1][tid] = none ? -1.f : ex2f(st.w - ref_of(KR));
+    }
+    float l = none ? 0.f : st.y * ex2f(st.x - ref_of(M));
 #pragma unroll
     for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
     if (lane == 0) red[1][warp] = l;
@@ -299,17 +310,18 @@ __global__ void __launch_bounds__(THREADS, HELD == 4 ? 6 : 2) scaled_merge_kerne
 #pragma unroll
     for (int w = 0; w < THREADS / 32; ++w) l += red[1][w];
     const float inv = l != 0.f ? 1.f / l : 0.f;  // (NaN stays NaN)
-    auto weigh = [&](int s, float v) {
-        const float k = fs[s];
+    auto weigh = [&](int s, bool priv, float v) {
+        const float k = gs[priv][s];
         return k >= 0.f || k != k ? k * v : 0.f;
     };
+    const bool priv = c0 >= d_h;
     float x = 0.f;
     if (mine) {
 #pragma unroll
         for (int j = 0; j < HELD; ++j)
-            if (g + j * groups < ns) x += weigh(g + j * groups, held[j]);
+            if (g + j * groups < ns) x += weigh(g + j * groups, priv, held[j]);
 #pragma unroll 8
-        for (int s = g + HELD * groups; s < ns; s += groups) x += weigh(s, acc[(int64_t)s * H * W]);
+        for (int s = g + HELD * groups; s < ns; s += groups) x += weigh(s, priv, acc[(int64_t)s * H * W]);
     }
     if (groups > 1) {
         sums[tid] = x;
@@ -318,12 +330,13 @@ __global__ void __launch_bounds__(THREADS, HELD == 4 ? 6 : 2) scaled_merge_kerne
             for (int k = 1; k < groups; ++k) x += sums[k * cols + c0];
         __syncthreads();
     }
-    if (g == 0 && c0 < W) sums[c0] = x;
+    // (by l first: a sum of many rows fits next to its own scale, not in the value's)
+    if (g == 0 && c0 < W) sums[c0] = x * inv * up[priv];
     for (int c = tid + THREADS; c < W; c += THREADS) {  // (wider than the block)
         const float *a = column(c);
         x = 0.f;
-        for (int s = 0; s < ns; ++s) x += weigh(s, a[(int64_t)s * H * W]);
-        sums[c] = x;
+        for (int s = 0; s < ns; ++s) x += weigh(s, c >= d_h, a[(int64_t)s * H * W]);
+        sums[c] = x * inv * up[c >= d_h];
     }
     __syncthreads();
     // ---- expand
@@ -345,7 +358,7 @@ __global__ void __launch_bounds__(THREADS, HELD == 4 ? 6 : 2) scaled_merge_kerne
     for (int d = tid; d < d_h; d += THREADS) {
         float s = sums[d];
         for (int k = 0; k < v8; ++k) s += fit ? part[d * v8 + k] : dot(k, B[d * v8 + k]);
-        out[d] = __float2bfloat16_rn(s * inv);
+        out[d] = __float2bfloat16_rn(s);
     }
 }
 

@@ -76,19 +76,21 @@ struct ScaledDecodeArgs {
     cudaStream_t stream;
 };
 
-// Partial softmax states of decode_scaled: slot s holds, for every head, the
-// running maximum (log2 units) and sum, and the value sums [d_h + r] relative
-// to that maximum.
+// Partial softmax states of decode_scaled (log2 units): slot s holds, for every head, the
+// running maximum m of the scores x and the sum of 2^(x - m), and the sums of 2^(x + e - k)
+// code over shared and private rows, each relative to its own maximum k of x + e.  A value
+// may be 2^128 or 2^-126 as it lies in the cache, and a sum of many such, or one that shares a
+// factor with a weight below one, would leave fp32; these neither overflow nor vanish.
 struct ScaledStates {
-    float *ml;   // [slots][H][2]
-    float *acc;  // [slots][H d_h | H r]
+    float4 *head;  // [slots][H]: m, sum, k of the shared rows, k of the private rows
+    float *acc;    // [slots][H d_h | H r]
 };
 __host__ __device__ inline size_t scaled_states_bytes(int64_t slots, int H, int d_h, int r) {
-    return align256(sizeof(float) * (size_t)slots * H * 2) + sizeof(float) * (size_t)slots * H * (d_h + r);
+    return align256(sizeof(float4) * (size_t)slots * H) + sizeof(float) * (size_t)slots * H * (d_h + r);
 }
 inline ScaledStates scaled_states(void *base, int64_t slots, int H) {
-    return {static_cast<float *>(base),
-            reinterpret_cast<float *>(static_cast<char *>(base) + align256(sizeof(float) * (size_t)slots * H * 2))};
+    return {static_cast<float4 *>(base),
+            reinterpret_cast<float *>(static_cast<char *>(base) + align256(sizeof(float4) * (size_t)slots * H))};
 }
 
 // Any shape: one CTA per (request, split, head).  Workspace bytes of a call and
@@ -135,6 +137,21 @@ struct ScaledAppendArgs {
 };
 bool append_scaled_tc_fits(const ScaledPools &c, int n, int B, int d);
 cudaError_t launch_append_scaled_tc(const ScaledAppendArgs &p);
+
+// 2^x, flushing.  (Of -infinity 0.)
+__device__ __forceinline__ float ex2f(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// Largest of a warp's values; NaN does not count.
+__device__ __forceinline__ float warp_max(float x) {
+    float y;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+    return y;
+}
+// A maximum as the point that exponents are relative to: none of -infinity.
+__device__ __forceinline__ float ref_of(float m) { return m == -INFINITY ? 0.f : m; }
 
 // Scale exponents.
 __device__ __forceinline__ int clamp_exp(int byte) {

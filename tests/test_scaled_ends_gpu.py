@@ -1,0 +1,90 @@
+"""The block-scaled cache on the GPU at the ends of what its calls allow."""
+import numpy as np
+import pytest
+
+import lrkv_inputs as I
+import oracle.scaled as S
+from scaled_util import bf16
+from test_scaled_gpu import check_decode, decode_case, poison_past_the_end, run_decode
+
+pytestmark = pytest.mark.gpu
+
+
+# ---------------------------------------------------------------------------
+# Decode: scales of the values at the ends of their range
+# ---------------------------------------------------------------------------
+LOW, HIGH = (10, 28), (237, 247)   # stored bytes: 2^-117 .. 2^-100, 2^110 .. 2^119
+ENDS = [(16, 128, 48, 64, 64, 1), (32, 128, 32, 64, 16, 1), (4, 128, 64, 32, 32, 1), (24, 128, 56, 64, 64, 1),
+        (8, 64, 16, 32, 16, 1), (12, 128, 72, 64, 64, 1), (16, 128, 32, 64, 64, 2), (2, 256, 256, 16, 16, 1)]
+
+
+def set_ends(rng, cache, which):
+    """Scales of the values; codes small enough that sums of a row's parts stay finite."""
+    for k in ("S_V", "R_V"):
+        codes, exps = cache.codes[k], cache.exps[k]
+        codes[...] = S.e4m3_encode(np.clip(rng.standard_normal(codes.shape) * 16, -48, 48))
+        low, high = rng.integers(*LOW, exps.shape), rng.integers(*HIGH, exps.shape)
+        if which == "lowest":
+            exps[...] = LOW[0]
+        elif which == "highest":
+            exps[...] = HIGH[1] - 1
+        elif which == "low":
+            exps[...] = low
+        elif which == "high":
+            exps[...] = high
+        elif which == "heads":                     # loud and quiet heads next to each other
+            exps[...] = np.where(rng.random((1, 1, exps.shape[2])) < 0.5, low, high)
+        else:                                      # loud and quiet blocks of one head
+            exps[...] = np.where(rng.random(exps.shape) < 0.5, low, high)
+    for k in ("S_K", "R_K"):                       # tiles whose largest scores differ by some octaves
+        cache.exps[k][:] = (127 - 7 + rng.integers(-3, 3, cache.exps[k].shape)).astype(np.uint8)
+
+
+@pytest.mark.parametrize("which", ["lowest", "highest", "low", "high", "heads", "blocks"])
+@pytest.mark.parametrize("H,d_h,r,ps,block,G", ENDS)
+def test_decode_of_values_at_the_ends_of_the_range(H, d_h, r, ps, block, G, which):
+    """Values of 2^-117 to 2^127: what a weight is worth does not depend on how loud its value is.  (Requests on shared
+    pages, rows enough that a part of one has several tiles.)"""
+    rng = np.random.default_rng(H + r)
+    lens, many = [1500, 129, 64, 1, 700], 17
+    cache, table, q, B_K, B_V = decode_case(rng, lens, H, d_h, r, ps, block, G)
+    set_ends(rng, cache, which)
+    poison_past_the_end(cache, table, lens)
+    q, lens = bf16(rng, (len(lens) * many, H, d_h)), lens * many
+    case = cache, np.tile(table, (many, 1)), q, B_K, B_V
+    check_decode(run_decode(*case, lens), *case, lens, which=[0, 1, 2, 3, 4, 30, 44, 84], norm=None)
+
+
+@pytest.mark.parametrize("H,d_h,r", [(16, 128, 48), (8, 64, 16)])
+def test_decode_of_a_quiet_tile_behind_a_louder_score(H, d_h, r):
+    """Two tiles of the least scale, equal scores in each, half an octave to two apart: both count.  (Requests on shared
+    pages, enough that a part has both of its tiles.)"""
+    rng = np.random.default_rng(60)
+    B, n, many = 8, 256, 40
+    cache, table, q, B_K, B_V = decode_case(rng, [n] * B, H, d_h, r, 64, 64)
+    set_ends(rng, cache, "lowest")
+    for k in ("S_K", "R_K"):
+        cache.codes[k][:] = 0
+    one = S.e4m3_encode(np.array(1.0))
+    x = np.zeros((B, H, d_h), np.float32)
+    for b in range(B):                             # scores in octaves: 2 and 2^e
+        x[b, :, 0] = 2 * np.sqrt(d_h) * np.log(2.0)
+        for j in range(n):
+            page, slot = table[b, j // 64], j % 64
+            cache.codes["S_K"][page, slot, 0, 0] = one
+            cache.exps["S_K"][page, 0] = 127 + (0 if j < 128 else (-1, -2, -3, 0, -20, 1, -1, -1)[b])
+    bits = I.f32_to_bf16_bits(x)
+    q = np.tile(bits, (many, 1, 1)), np.tile(I.bf16_bits_to_f64(bits), (many, 1, 1))
+    case, lens = (cache, np.tile(table, (many, 1)), q, B_K, B_V), [n] * (B * many)
+    check_decode(run_decode(*case, lens), *case, lens, which=[*range(B), *range(100, 100 + B), B * many - 1], norm=None)
+
+
+@pytest.mark.parametrize("H,d_h,r", [(16, 128, 48), (8, 64, 16)])
+def test_decode_of_the_loudest_rows_that_agree(H, d_h, r):
+    """Many rows of the same largest value: their mean is that value, however many they are."""
+    rng = np.random.default_rng(61)
+    lens = [4096, 1000]
+    cache, table, q, B_K, B_V = decode_case(rng, lens, H, d_h, r, 64, 64)
+    cache.codes["S_V"][:], cache.exps["S_V"][:] = 0x7e, 246        # 448 * 2^119
+    cache.codes["R_V"][:], cache.exps["R_V"][:] = 0, 10
+    check_decode(run_decode(cache, table, q, B_K, B_V, lens), cache, table, q, B_K, B_V, lens)
