@@ -394,6 +394,10 @@ __global__ void __launch_bounds__(kReadThreads, 5) expand_scaled_kernel(const __
     const int64_t start = a.rows.start_pos[b];
     const int64_t ctx = r0 >= 0 && r0 < r1 ? min((int64_t)a.max_ctx, start + (r1 - r0)) : 0;
     const int64_t copied = a.history ? min(ctx, start) : ctx;
+    // rows from max_ctx on that have a place: written, not attended
+    if (p0 == 0 && threadIdx.x == 0 && r0 >= 0 && r0 < r1 &&
+        max(start, (int64_t)a.max_ctx) < min(start + (r1 - r0), (int64_t)a.rows.max_pages * a.c.page_size))
+        status_or(a.rows.status, LRKV_STATUS_BAD_SEQLEN);
     if (p0 >= copied && !(a.table && p0 % 64 == 0)) return;
     if (threadIdx.x < 4) ld[threadIdx.x] = (int64_t)a.c.heads(threadIdx.x) * a.c.width(threadIdx.x);
     if (threadIdx.x < ROWS) {

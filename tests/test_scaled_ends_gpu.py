@@ -1,11 +1,14 @@
 """The block-scaled cache on the GPU at the ends of what its calls allow."""
 import numpy as np
 import pytest
+import torch
 
 import lrkv_inputs as I
 import oracle.scaled as S
-from scaled_util import bf16
-from test_scaled_gpu import check_decode, decode_case, poison_past_the_end, run_decode
+from gpu_util import dev, host
+from scaled_util import bf16, check, random_cache, reference, table_of, to_device, to_host
+from test_scaled_gpu import (BAD_ROW, BAD_SEQLEN, check_decode, close_caches, decode_case, poison_past_the_end, projected,
+                             run_decode, status, weights)
 
 pytestmark = pytest.mark.gpu
 
@@ -88,3 +91,63 @@ def test_decode_of_the_loudest_rows_that_agree(H, d_h, r):
     cache.codes["S_V"][:], cache.exps["S_V"][:] = 0x7e, 246        # 448 * 2^119
     cache.codes["R_V"][:], cache.exps["R_V"][:] = 0, 10
     check_decode(run_decode(cache, table, q, B_K, B_V, lens), cache, table, q, B_K, B_V, lens)
+
+
+# ---------------------------------------------------------------------------
+# Prefill: rows past max_ctx
+# ---------------------------------------------------------------------------
+def prefill(rng, H, d_h, r, ps, start, rows_of, max_ctx, table=None, pages=None, d=64, x=None, q=None, change=None):
+    """A call on an output of threes and a workspace of NaN: (output, the cache after it, status, cu_rows, (q, B_K, B_V), table,
+    (the cache before it, weights, x))."""
+    import rank_kv_attention_gb300 as L
+    B, lens = len(start), np.add(start, rows_of)
+    cu, n = np.concatenate([[0], np.cumsum(rows_of)]), int(sum(rows_of))
+    if table is None:
+        pages = int(sum(-(-v // ps) for v in lens)) + 1
+        table = table_of(rng, lens, ps, pages)
+    cache = random_cache(rng, pages, ps, H, d_h, r, 16, loud=1)
+    if change:
+        change(cache, table)
+    w, x, q = weights(rng, d, H, d_h, r, 1), x or bf16(rng, (n, d)), q or bf16(rng, (n, H, d_h))
+    B_K, B_V = bf16(rng, (H, d_h, r), r ** -0.5), bf16(rng, (H, d_h, r), r ** -0.5)
+    dc, st = to_device(cache), status()
+    out = torch.full((n, H, d_h), 3.0, dtype=torch.bfloat16, device="cuda")
+    ws = torch.full((L.prefill_scaled_workspace_bytes(dc, B, n, max_ctx),), 0xff, dtype=torch.uint8, device="cuda")
+    L.prefill_scaled(dev(x[0], "bf16"), dev(q[0], "bf16"), dev(cu, "i32"), dev(np.asarray(start), "i32"), max_ctx,
+                     *[dev(w[m][0], "bf16") for m in w], dev(B_K[0], "bf16"), dev(B_V[0], "bf16"), dc, dev(table, "i32"), out=out,
+                     ws=ws, status=st)
+    held = to_host(dc, cache)
+    return host(out, "bf16"), held, int(st), cu, (q[1], B_K[1], B_V[1]), table, (cache, w, x)
+
+
+PAST = [([0], [60], 50), ([0], [64], 64), ([0], [300], 200), ([64], [128], 64), ([64], [128], 100), ([64], [128], 192),
+        ([130], [40], 150), ([130], [40], 130), ([700], [20], 705), ([700], [300], 960), ([0, 64, 300], [30, 90, 20], 140),
+        ([0, 200, 10], [10, 20, 30], 215)]
+
+
+PAST_SHAPES = [(16, 128, 48, 64, 64), (16, 128, 48, 64, 72), (8, 128, 16, 128, 64), (4, 32, 8, 32, 64)]
+
+
+@pytest.mark.parametrize("start,rows_of,max_ctx", PAST)
+@pytest.mark.parametrize("H,d_h,r,ps,d", PAST_SHAPES)
+def test_prefill_flags_rows_past_max_ctx(H, d_h, r, ps, d, start, rows_of, max_ctx):
+    """Rows from max_ctx on are written and flagged, behind a history or not; rows before it alone are not.  (d = 72: the
+    append that stages its rows, whatever their number.)"""
+    rng = np.random.default_rng(sum(start) + max_ctx)
+    _, held, st, cu, _, table, (cache, w, x) = prefill(rng, H, d_h, r, ps, start, rows_of, max_ctx, d=d)
+    assert st == (BAD_SEQLEN if max(np.add(start, rows_of)) > max_ctx else 0)
+    S.write(cache, projected(x[1], w), cu, start, table)
+    close_caches(held, cache, None, cu, start, table, d)
+
+
+@pytest.mark.parametrize("H,d_h,r,ps", [(16, 128, 48, 64), (4, 32, 8, 32)])
+def test_prefill_at_the_end_of_the_table(H, d_h, r, ps):
+    """max_ctx is the table's end: rows past it have no place, which is another flag."""
+    rng = np.random.default_rng(62)
+    table = np.arange(4, dtype=np.int32)[None]
+    got, held, st, cu, (q, B_K, B_V), _, _ = prefill(rng, H, d_h, r, ps, [4 * ps - 30], [70], 4 * ps, table, pages=4)
+    assert st == BAD_ROW
+    for i in (0, 29):
+        ref, bound = reference(q[i], held, B_K, B_V, table[0], 4 * ps - 30 + i + 1, d_h == 128)
+        check(got[i], ref, bound, f"row {i}")
+    assert not got[30:].any()
