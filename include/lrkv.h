@@ -519,9 +519,10 @@ LRKV_API int lrkv_prefill_window(const void *X, const void *Q, const int32_t *cu
  * Where lrkv_prefill runs its tiled kernel on a bf16 cache of these sizes, the
  * values are laid out in bf16 in the workspace and that kernel runs; other
  * sizes run one decode a row.  A row without a place is flagged as by the append,
- * its output zero; rows past max_ctx are written, not attended (of the tiled
- * kernel: tiles of 128 rows from the request's first on, past its max_ctx-th row),
- * and flagged LRKV_STATUS_BAD_SEQLEN (their outputs stay, or become zero).
+ * its output zero; rows from position max_ctx on are written, not attended, and
+ * flagged LRKV_STATUS_BAD_SEQLEN (their outputs stay, or become zero; in the tiled
+ * kernel so do those of a request that begins at a negative position, past its
+ * max_ctx-th row rounded up to 128).
  *
  * Workspaces are 256-byte aligned device memory, scratch, without
  * initialisation; one per call in flight.

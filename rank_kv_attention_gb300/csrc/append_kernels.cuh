@@ -131,6 +131,9 @@ struct PrefillTcArgs {
     // Query tiles that leave SMs idle may have two or four CTAs each (no window); the sums are
     // then added up in another order.
     bool split = false;
+    // Rows at this position and past it are not attended and see no key: zero outputs (0: the
+    // end of the page table).
+    int max_len = 0;
 };
 int launch_prefill_tc(const PrefillTcArgs &p);
 // Whether it covers this call.

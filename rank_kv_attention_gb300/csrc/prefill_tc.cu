@@ -952,6 +952,7 @@ int launch_prefill_tc(const PrefillTcArgs &p) {
     a.max_pages = p.max_pages;
     a.num_pages = c.num_pages;
     a.max_len = p.max_pages * c.page_size;
+    if (p.max_len) a.max_len = std::min(a.max_len, p.max_len);
     a.n_qtiles = n_qtiles;
     a.scale_log2 = 1.4426950408889634f / sqrtf(128.f);
     a.window = std::min(p.window, a.max_len);

@@ -356,6 +356,7 @@ int lrkv_prefill_scaled(const void *X, const void *Q, const int32_t *cu_rows, co
         p.B = B;
         p.n = n;
         p.max_ctx = max_ctx;
+        p.max_len = max_ctx;  // (values are laid out up to there)
         p.B_K = B_K;
         p.B_V = B_V;
         p.cache = w.cache;

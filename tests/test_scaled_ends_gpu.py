@@ -140,6 +140,38 @@ def test_prefill_flags_rows_past_max_ctx(H, d_h, r, ps, d, start, rows_of, max_c
     close_caches(held, cache, None, cu, start, table, d)
 
 
+@pytest.mark.parametrize("start,rows_of,max_ctx", PAST)
+@pytest.mark.parametrize("H,d_h,r,ps,d", PAST_SHAPES)
+def test_prefill_past_max_ctx(H, d_h, r, ps, d, start, rows_of, max_ctx):
+    """Rows up to max_ctx are attended as ever, whatever the workspace held; the outputs of those from it on are zero or as
+    they were."""
+    rng = np.random.default_rng(sum(start) + max_ctx)
+    got, held, _, cu, (q, B_K, B_V), table, _ = prefill(rng, H, d_h, r, ps, start, rows_of, max_ctx, d=d)
+    for b in range(len(start)):
+        fit = min(max(0, max_ctx - start[b]), rows_of[b])
+        for i in sorted({0, fit // 2, fit - 1} & set(range(fit))):
+            ref, bound = reference(q[cu[b] + i], held, B_K, B_V, table[b], start[b] + i + 1, d_h == 128)
+            check(got[cu[b] + i], ref, bound, f"request {b} row {i}")
+        rest = got[cu[b] + fit:cu[b + 1]]
+        assert ((rest == 0) | (rest == 3)).all()
+
+
+@pytest.mark.parametrize("rows,d", [(20, 64), (40, 64), (20, 72)])
+def test_prefill_past_max_ctx_in_a_pool_smaller_than_its_requests(rows, d):
+    """Requests behind one shared page, values laid out once a page of the pool."""
+    rng = np.random.default_rng(rows + d)
+    H, r, ps, B, start, max_ctx = 8, 16, 64, 3, [64] * 3, 70
+    table = np.array([[0, 1 + b] for b in range(B)], np.int32)
+    got, held, st, cu, (q, B_K, B_V), _, _ = prefill(rng, H, 128, r, ps, start, [rows] * B, max_ctx, table, pages=4, d=d)
+    assert st == BAD_SEQLEN
+    for b in range(B):
+        for i in (0, max_ctx - 65):
+            ref, bound = reference(q[cu[b] + i], held, B_K, B_V, table[b], 65 + i, True)
+            check(got[cu[b] + i], ref, bound, f"request {b} row {i}")
+        rest = got[cu[b] + max_ctx - 64:cu[b + 1]]
+        assert ((rest == 0) | (rest == 3)).all()
+
+
 @pytest.mark.parametrize("H,d_h,r,ps", [(16, 128, 48, 64), (4, 32, 8, 32)])
 def test_prefill_at_the_end_of_the_table(H, d_h, r, ps):
     """max_ctx is the table's end: rows past it have no place, which is another flag."""
