@@ -518,7 +518,10 @@ LRKV_API int lrkv_prefill_window(const void *X, const void *Q, const int32_t *cu
  * quantised), as lrkv_prefill.  max_ctx: host upper bound of start_pos[b] + rows of b.
  * Where lrkv_prefill runs its tiled kernel on a bf16 cache of these sizes, the
  * values are laid out in bf16 in the workspace and that kernel runs; other
- * sizes run one decode a row.  A row without a place is flagged as by the append,
+ * sizes run one decode a row.  A query that is not finite gives NaN in its row and head.
+ * Rows that some new row of a request sees must hold finite values: the tiled kernel gives
+ * a row that another row of its tile does not see the weight 0, and 0 times a NaN is NaN.
+ * A row without a place is flagged as by the append,
  * its output zero; rows from position max_ctx on are written, not attended, and
  * flagged LRKV_STATUS_BAD_SEQLEN (their outputs stay, or become zero; in the tiled
  * kernel so do those of a request that begins at a negative position, past its

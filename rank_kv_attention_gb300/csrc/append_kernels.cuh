@@ -129,7 +129,8 @@ struct PrefillTcArgs {
     // predecessor writes the page table and the history, and all copies wait.)
     bool early = false;
     // Query tiles that leave SMs idle may have two or four CTAs each (no window); the sums are
-    // then added up in another order.
+    // then added up in another order.  And a query that is not finite, or that sees a key that is
+    // not, gives NaN, where it gives zero else.
     bool split = false;
     // Rows at this position and past it are not attended and see no key: zero outputs (0: the
     // end of the page table).

@@ -183,3 +183,43 @@ def test_prefill_at_the_end_of_the_table(H, d_h, r, ps):
         ref, bound = reference(q[i], held, B_K, B_V, table[0], 4 * ps - 30 + i + 1, d_h == 128)
         check(got[i], ref, bound, f"row {i}")
     assert not got[30:].any()
+
+
+# ---------------------------------------------------------------------------
+# Prefill: what is not finite; many requests; the least values
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("H,d_h,r,ps", [(16, 128, 48, 64), (32, 128, 16, 64), (4, 32, 8, 32)])
+@pytest.mark.parametrize("start,rows", [(0, 40), (10, 150), (900, 100), (0, 900)])
+@pytest.mark.parametrize("value", [np.nan, np.inf])
+def test_prefill_of_a_query_that_is_not_finite(H, d_h, r, ps, start, rows, value):
+    """It gives NaN in its row and head, as a decode does; the other rows and heads are right."""
+    rng = np.random.default_rng(63 + rows)
+    bits, q = bf16(rng, (rows, H, d_h))
+    for i, h in ((0, 1), (rows // 2, 2), (rows - 1, 0)):
+        bits[i, h, 7], q[i, h, 7] = (I.BF16_NAN_BITS if np.isnan(value) else 0x7f80), value
+    got, held, st, _, (_, B_K, B_V), table, _ = prefill(rng, H, d_h, r, ps, [start], [rows], start + rows, q=(bits, q))
+    assert st == 0
+    for i, h in ((0, 1), (rows // 2, 2), (rows - 1, 0)):
+        assert np.isnan(got[i, h]).all(), (i, h)
+        got[i, h] = q[i, h] = 0
+    assert np.isfinite(got).all()
+    for i, h in ((0, 1), (rows // 2, 2), (rows - 1, 0), (rows // 3, 0)):
+        ref, bound = reference(q[i], held, B_K, B_V, table[0], start + i + 1, d_h == 128)
+        if i != rows // 3:
+            ref[h] = 0                             # (the row put to zero above)
+        check(got[i], ref, bound, f"row {i}", norm=None)
+
+
+@pytest.mark.parametrize("H,d_h,r,ps", [(16, 128, 48, 64), (4, 32, 8, 32)])
+@pytest.mark.parametrize("pool", ["S_K", "S_V"])
+def test_prefill_behind_a_row_that_is_not_finite(H, d_h, r, ps, pool):
+    """A NaN code of a row that all queries see makes their outputs NaN, and no other request's."""
+    rng = np.random.default_rng(64)
+
+    def change(cache, table):
+        cache.codes[pool][table[0, 1], 3, 0, :] = 0x7f
+    got, held, st, cu, (q, B_K, B_V), table, _ = prefill(rng, H, d_h, r, ps, [100, 40], [30, 50], 130, change=change)
+    assert st == 0 and np.isnan(got[:30]).all()
+    for i in (30, 79):
+        ref, bound = reference(q[i], held, B_K, B_V, table[1], 40 + i - 30 + 1, d_h == 128)
+        check(got[i], ref, bound, f"row {i}")
