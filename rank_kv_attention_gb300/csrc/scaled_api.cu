@@ -166,8 +166,10 @@ struct PrefillScaledWs {
     void *dec;
     size_t bytes;
 };
-bool prefill_scaled_tiles(const lrkv_scaled_t &c) {
-    return c.d_h == 128 && c.G <= 1 && c.r <= 64 && c.page_size % 64 == 0;
+bool prefill_scaled_tiles(const lrkv_scaled_t &c, int B, int n, int max_ctx) {
+    // (requests and query tiles are a grid's y and z; the layout's CTAs of 4 or 8 rows its x)
+    return c.d_h == 128 && c.G <= 1 && c.r <= 64 && c.page_size % 64 == 0 && B <= 65535 &&
+           (std::min(n, max_ctx) + 127) / 128 <= 65535 && (int64_t)B * ((max_ctx + 7) / 8) <= INT32_MAX;
 }
 PrefillScaledWs prefill_scaled_ws(void *base, const lrkv_scaled_t &sc, int B, int n, int max_ctx) {
     const ScaledPools c = pools_of(sc);
@@ -184,7 +186,7 @@ PrefillScaledWs prefill_scaled_ws(void *base, const lrkv_scaled_t &sc, int B, in
     const int64_t own = (int64_t)B * w.pages * 64, all = (int64_t)c.num_pages * c.page_size;
     w.own_pages = own <= all;
     const int64_t rows = std::min(own, all);
-    w.tiled = prefill_scaled_tiles(sc) && rows + 64 < INT32_MAX / 2;
+    w.tiled = prefill_scaled_tiles(sc, B, n, max_ctx) && rows + 64 < INT32_MAX / 2;
     if (w.tiled) {
         w.cache = lrkv_cache_t{};
         w.cache.S_K = take(2 * (size_t)rows * c.d_h);
@@ -341,8 +343,6 @@ int lrkv_prefill_scaled(const void *X, const void *Q, const int32_t *cu_rows, co
     const void *ptrs[] = {Q, B_K, B_V, out};
     for (const void *x : ptrs)
         if (!x || !aligned16(x)) return LRKV_E_INVALID_ARG;
-    // (a launch that lays out 8 rows a block)
-    if ((int64_t)B * ((max_ctx + 7) / 8) > INT32_MAX) return LRKV_E_SHAPE;
     const PrefillScaledWs w = prefill_scaled_ws(workspace, *cache, B, n, max_ctx);
     if (!workspace || !aligned256(workspace) || workspace_bytes < w.bytes) return LRKV_E_WORKSPACE;
     cudaStream_t s = (cudaStream_t)stream;
@@ -366,7 +366,7 @@ int lrkv_prefill_scaled(const void *X, const void *Q, const int32_t *cu_rows, co
         p.status = dev_status;
         p.stream = s;
         p.split = p.early = true;  // (behind launch_expand_scaled, which lets it start after its own wait)
-        if (!prefill_tc_fits(p)) return LRKV_E_SHAPE;  // (more than 65535 heads, requests or query tiles)
+        if (!prefill_tc_fits(p)) return LRKV_E_SHAPE;  // (no tensor maps: their encoder is not there)
     }
     // (the append in one kernel lays its own rows' values out)
     void *const y[4] = {w.cache.S_K, w.cache.S_V, w.cache.R_K, w.cache.R_V};

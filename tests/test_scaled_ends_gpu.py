@@ -223,3 +223,21 @@ def test_prefill_behind_a_row_that_is_not_finite(H, d_h, r, ps, pool):
     for i in (30, 79):
         ref, bound = reference(q[i], held, B_K, B_V, table[1], 40 + i - 30 + 1, d_h == 128)
         check(got[i], ref, bound, f"row {i}")
+
+
+def test_prefill_of_more_requests_than_a_grid_holds():
+    """70,000 requests, most without rows."""
+    rng = np.random.default_rng(65)
+    H, r, ps, B = 4, 16, 64, 70000
+    live = np.sort(rng.choice(B, 30, replace=False))
+    live[-1] = B - 1
+    rows_of, start = np.zeros(B, int), np.zeros(B, int)
+    rows_of[live], start[live] = rng.integers(1, 70, 30), rng.integers(0, 60, 30)
+    table = np.full((B, 2), -1, np.int32)
+    table[live] = rng.permutation(61)[:60].reshape(30, 2)
+    got, held, st, cu, (q, B_K, B_V), _, _ = prefill(rng, H, 128, r, ps, list(start), list(rows_of), 128, table, pages=61)
+    assert st == 0
+    for b in live:
+        for i in {0, rows_of[b] - 1}:
+            ref, bound = reference(q[cu[b] + i], held, B_K, B_V, table[b], int(start[b] + i) + 1, True)
+            check(got[cu[b] + i], ref, bound, f"request {b} row {i}")
