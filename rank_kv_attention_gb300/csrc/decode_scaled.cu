@@ -1013,7 +1013,7 @@ bool scaled_tc_covers(const ScaledPools &c) {
 
 // CTAs of a call: one per SM; fewer where the requests cannot have as many units.
 static int ctas_of(int B, int max_seq_len) {
-    return (int)std::max<int64_t>(1, std::min<int64_t>(device_sm_count(), (int64_t)B * ((max_seq_len + kUnit - 1) / kUnit)));
+    return (int)std::max<int64_t>(1, std::min<int64_t>(device_sm_count(), B * (((int64_t)max_seq_len + kUnit - 1) / kUnit)));
 }
 
 size_t scaled_tc_ws_bytes(const ScaledPools &c, int B, int max_seq_len) {

@@ -388,7 +388,7 @@ __global__ void scaled_row_queries_kernel(const __grid_constant__ ScaledRows row
 
 // Parts per request: enough CTAs for the device, of at least 128 rows each.
 int any_splits(const ScaledPools &c, int B, int max_seq_len) {
-    const int64_t most = (max_seq_len + kThreads - 1) / kThreads;
+    const int64_t most = ((int64_t)max_seq_len + kThreads - 1) / kThreads;
     const int64_t want = (8 * (int64_t)device_sm_count() + (int64_t)B * c.H - 1) / ((int64_t)B * c.H);
     return (int)std::max<int64_t>(1, std::min<int64_t>({most, want, 256}));
 }
@@ -398,7 +398,7 @@ int any_splits(const ScaledPools &c, int B, int max_seq_len) {
 size_t scaled_any_ws_bytes(const ScaledPools &c, int B, int max_seq_len) {
     // B * splits is at most 8 SMs / H + B, which grows with B, and at most 256 B
     const int64_t slots = std::min<int64_t>(8 * (int64_t)device_sm_count() / c.H + 1 + B,
-                                            (int64_t)B * std::min<int64_t>((max_seq_len + kThreads - 1) / kThreads, 256));
+                                            B * std::min<int64_t>(((int64_t)max_seq_len + kThreads - 1) / kThreads, 256));
     return scaled_states_bytes(slots, c.H, c.d_h, c.r);
 }
 

@@ -169,7 +169,7 @@ struct PrefillScaledWs {
 bool prefill_scaled_tiles(const lrkv_scaled_t &c, int B, int n, int max_ctx) {
     // (requests and query tiles are a grid's y and z; the layout's CTAs of 4 or 8 rows its x)
     return c.d_h == 128 && c.G <= 1 && c.r <= 64 && c.page_size % 64 == 0 && B <= 65535 &&
-           (std::min(n, max_ctx) + 127) / 128 <= 65535 && (int64_t)B * ((max_ctx + 7) / 8) <= INT32_MAX;
+           std::min(n, max_ctx) <= 65535 * 128 && B * (((int64_t)max_ctx + 7) / 8) <= INT32_MAX;
 }
 PrefillScaledWs prefill_scaled_ws(void *base, const lrkv_scaled_t &sc, int B, int n, int max_ctx) {
     const ScaledPools c = pools_of(sc);
@@ -181,7 +181,7 @@ PrefillScaledWs prefill_scaled_ws(void *base, const lrkv_scaled_t &sc, int B, in
         o += align256(bytes);
         return p;
     };
-    w.pages = (max_ctx + 63) / 64;
+    w.pages = (int)(((int64_t)max_ctx + 63) / 64);
     // pages of the requests' own, or, where the whole pool is smaller, its pages
     const int64_t own = (int64_t)B * w.pages * 64, all = (int64_t)c.num_pages * c.page_size;
     w.own_pages = own <= all;

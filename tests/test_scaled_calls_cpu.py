@@ -293,3 +293,12 @@ def test_workspaces_grow_with_the_call(real):
             assert row == sorted(row) and row[0] > 0 and row[-1] >= last
             last = row[-1]
     assert real.lrkv_append_scaled_workspace_bytes(desc(), 100) >= 100 * 4 * 1792
+
+
+def test_workspaces_of_the_largest_sizes(real):
+    """The queries take any int32: the bytes of few requests neither fall nor run away where a length comes near 2^31."""
+    for d in (desc(), desc(H=6, r=40, d_h=32), desc(G=2), desc(r=72)):
+        for call in (lambda n: real.lrkv_decode_scaled_workspace_bytes(d, 3, n),
+                     lambda n: real.lrkv_prefill_scaled_workspace_bytes(d, 3, 50, n)):
+            sizes = [call(n) for n in (2 ** 20, 2 ** 30, 2 ** 31 - 200, 2 ** 31 - 1)]
+            assert sizes == sorted(sizes) and 0 < sizes[0] and sizes[-1] < 2 ** 40, sizes
