@@ -774,7 +774,7 @@ def _strided_rows(rows, n, H, d_h, r, G, dev):
         if n and not (ld[-1] == 1 and (len(shape) == 2 or ld[1] == shape[2] or shape[1] == 1)):
             raise ValueError(f"{name}: the values of a row must be contiguous")
         # (one row has no distance to a next one)
-        out += [t.data_ptr(), max(ld[0], flat[1]) if n <= 1 else ld[0]]
+        out += [t.data_ptr(), flat[1] if n <= 1 else ld[0]]
     return out, dt
 
 

@@ -158,6 +158,17 @@ def test_a_single_row_needs_no_stride(lib):
     assert lib.calls[0][1][1] == D_H and lib.calls[0][1][5] == H * R
 
 
+@pytest.mark.parametrize("dt,stride", [(BF, D_H + 1), (BF, 3 * D_H + 4), (torch.float32, D_H + 2), (BF, 1 << 40)])
+def test_a_single_row_of_any_stride(lib, dt, stride):
+    """The distance to a next row that is not there need not be one that the library takes."""
+    x = [torch.as_strided(z(2, D_H, dt=dt), (1, D_H), (stride, 1)), torch.as_strided(z(2, D_H, dt=dt), (1, 1, D_H), (stride, 7, 1)),
+         torch.as_strided(z(1, H * R, dt=dt), (1, H, R), (stride, R, 1)), z(1, H, R, dt=dt)]
+    write(x=x)
+    read(n=1, out=x)
+    for (_, a), first in zip(lib.calls, (0, 8)):
+        assert [a[first + 1 + 2 * k] for k in range(4)] == [D_H, D_H, H * R, H * R]
+
+
 @pytest.mark.parametrize("call,names", [(decode, ("longest",)), (prefill, ("longest",)), (read, ("n",))])
 def test_sizes_past_32_bits_are_refused(lib, call, names):
     for name in names:
