@@ -996,11 +996,19 @@ Ws layout(void *base, const Shape &s, int B, int ctas, int d_h) {
     return w;
 }
 
+// Whether the compiler gave the kernels the registers that their warps hand on: taking more than
+// the launch has would wait forever.
+bool registers_fit() {
+    static const bool fit = launch_registers(decode_scaled_kernel<16>) == kRegs &&
+                            launch_registers(decode_scaled_kernel<32>) == kRegs;
+    return fit;
+}
+
 bool fits(const ScaledPools &c, Shape &s) {
     if (c.d_h != 128 || c.G != 1 || !make_shape(c.H, c.r, s)) return false;
     if ((int64_t)c.num_pages * c.page_size + kTile >= INT32_MAX) return false;
     for (s.stages = kMaxStages; s.stages >= 6; --s.stages)
-        if (Offsets(s).bytes <= kSmemMost) return tc_encode() != nullptr;
+        if (Offsets(s).bytes <= kSmemMost) return tc_encode() != nullptr && registers_fit();
     return false;
 }
 
@@ -1036,10 +1044,6 @@ cudaError_t launch_decode_scaled_tc(const ScaledDecodeArgs &d, void *ws) {
         return cudaErrorInvalidValue;
     const int ctas = ctas_of(d.B, d.max_seq_len);
     const auto kernel = c.H <= 16 ? decode_scaled_kernel<16> : decode_scaled_kernel<32>;
-    // (taking registers that the launch does not have would wait forever)
-    static const bool enough = launch_registers(decode_scaled_kernel<16>) == kRegs &&
-                               launch_registers(decode_scaled_kernel<32>) == kRegs;
-    if (!enough) return cudaErrorLaunchOutOfResources;
     const Ws w = layout(ws, s, d.B, ctas, c.d_h);
     const int max_len = d.max_pages * c.page_size;
     PrepArgs p;

@@ -94,6 +94,40 @@ def test_decode_of_the_loudest_rows_that_agree(H, d_h, r):
 
 
 # ---------------------------------------------------------------------------
+# Decode: which kernel a shape takes
+# ---------------------------------------------------------------------------
+def on_tensor_cores(H, d_h, r, G=1, ps=64):
+    """Whether a shape's decode keeps an operand image, of 4 rows of 128 bytes a head at least, for every request."""
+    import rank_kv_attention_gb300 as L
+    c = L.ScaledCache.empty(1, ps, H, d_h, r, block=16, groups=G)
+    each = (L.decode_scaled_workspace_bytes(c, 40000, 4096) - L.decode_scaled_workspace_bytes(c, 30000, 4096)) / 10000
+    return each >= 4 * H * (d_h + r + 2) + 512 * H
+
+
+def test_shapes_that_decode_on_tensor_cores():
+    """d_h = 128, one shared basis, 4 heads up to 32 in steps of 4, r up to 64: all of them but those whose operands do not
+    fit, 24 heads of r = 64, 28 of r from 48 on and 32 of r from 48 on."""
+    for H in range(4, 33, 4):
+        for r in range(8, 65, 8):
+            assert on_tensor_cores(H, 128, r) == (r <= {24: 56, 28: 40, 32: 40}.get(H, 64)), (H, r)
+    for other in ((18, 128, 56), (36, 128, 8), (16, 128, 72), (16, 64, 48), (16, 128, 48, 2), (2, 128, 8)):
+        assert not on_tensor_cores(*other), other
+
+
+@pytest.mark.parametrize("H,r,ps,block", [(24, 56, 64, 64), (24, 48, 32, 16), (24, 64, 64, 64), (28, 40, 64, 32), (28, 8, 16, 16),
+                                          (32, 40, 64, 64), (32, 48, 64, 64), (20, 64, 64, 16), (18, 56, 64, 64)])
+def test_decode_of_many_heads(H, r, ps, block):
+    """Shapes on both sides of what fits."""
+    rng = np.random.default_rng(H * 100 + r)
+    lens = [1, 17, 64, 129, 300, 1000, 2300]
+    case = decode_case(rng, lens, H, 128, r, ps, block)
+    poison_past_the_end(case[0], case[1], lens)
+    st = status()
+    check_decode(run_decode(*case, lens, status=st), *case, lens)
+    assert int(st) == 0
+
+
+# ---------------------------------------------------------------------------
 # Prefill: rows past max_ctx
 # ---------------------------------------------------------------------------
 def prefill(rng, H, d_h, r, ps, start, rows_of, max_ctx, table=None, pages=None, d=64, x=None, q=None, change=None):
@@ -241,3 +275,16 @@ def test_prefill_of_more_requests_than_a_grid_holds():
         for i in {0, rows_of[b] - 1}:
             ref, bound = reference(q[cu[b] + i], held, B_K, B_V, table[b], int(start[b] + i) + 1, True)
             check(got[cu[b] + i], ref, bound, f"request {b} row {i}")
+
+
+@pytest.mark.parametrize("H,d_h,r,ps", [(16, 128, 48, 64), (4, 32, 8, 32)])
+@pytest.mark.parametrize("which", ["lowest", "low"])
+def test_prefill_behind_the_smallest_values(H, d_h, r, ps, which):
+    """One new row of zeros behind a history of the least scales."""
+    rng = np.random.default_rng(66)
+    x = np.zeros((1, 64), np.uint16), np.zeros((1, 64))
+    got, held, st, _, (q, B_K, B_V), table, _ = prefill(rng, H, d_h, r, ps, [400], [1], 401, x=x,
+                                                        change=lambda c, t: set_ends(rng, c, which))
+    ref, bound = reference(q[0], held, B_K, B_V, table[0], 401, d_h == 128)
+    check(got[0], ref, bound, norm=None)
+    assert st == 0 and ref.any()
