@@ -154,8 +154,9 @@ size_t decode_scaled_ws_bytes(const ScaledPools &c, int B, int max_seq_len) {
     return scaled_tc_covers(c) ? scaled_tc_ws_bytes(c, B, max_seq_len) : scaled_any_ws_bytes(c, B, max_seq_len);
 }
 
-// Prefill workspace: the projected rows; then, tiled, the bf16 pools of the values with
-// their page table, or, a decode a row, the rows' places and the decode's workspace.
+// Prefill workspace: the projected rows, and over them, when those have been written, tiled, the
+// bf16 pools of the values with their page table, or, a decode a row, the rows' places and the
+// decode's workspace.  (The append in one kernel has no projected rows, and lays values out.)
 struct PrefillScaledWs {
     StagedRows rows;
     bool tiled, own_pages;
@@ -175,7 +176,7 @@ PrefillScaledWs prefill_scaled_ws(void *base, const lrkv_scaled_t &sc, int B, in
     const ScaledPools c = pools_of(sc);
     PrefillScaledWs w = {};
     w.rows = staged_rows(base, c, n);
-    size_t o = w.rows.bytes;
+    size_t o = 0;
     auto take = [&](size_t bytes) {
         void *p = static_cast<char *>(base) + o;
         o += align256(bytes);
@@ -207,7 +208,7 @@ PrefillScaledWs prefill_scaled_ws(void *base, const lrkv_scaled_t &sc, int B, in
         w.req_row = static_cast<int32_t *>(take(arr));
         w.dec = take(scaled_any_ws_bytes(c, n, max_ctx));
     }
-    w.bytes = o;
+    w.bytes = std::max(o, w.rows.bytes);
     return w;
 }
 

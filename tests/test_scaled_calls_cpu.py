@@ -313,3 +313,16 @@ def test_workspaces_of_the_largest_sizes(real):
                      lambda n: real.lrkv_prefill_scaled_workspace_bytes(d, 3, 50, n)):
             sizes = [call(n) for n in (2 ** 20, 2 ** 30, 2 ** 31 - 200, 2 ** 31 - 1)]
             assert sizes == sorted(sizes) and 0 < sizes[0] and sizes[-1] < 2 ** 40, sizes
+
+
+@pytest.mark.parametrize("B,n,max_ctx", [(8, 16384, 2048), (1, 512, 40000), (4, 100, 700), (3, 5, 9000)])
+def test_prefill_workspace_holds_one_part_at_a_time(real, B, n, max_ctx):
+    """The projected rows are done with when the values are laid out (or the rows' decode begins): one part over the other."""
+    for kw in (dict(), dict(page_size=32), dict(r=72)):
+        d, width = desc(num_pages=2 ** 14, **kw), 2 * (128 + 16 * kw.get("r", 48))
+        tiled = not kw
+        rows = min(B * -(-max_ctx // 64) * 64, 2 ** 14 * 64)
+        staged = n * width * 4 + 4 * 256
+        later = rows * width * 2 + 4 * B * -(-max_ctx // 64) + 5 * 256 if tiled else \
+            real.lrkv_decode_scaled_workspace_bytes(d, n, max_ctx) + 8 * n + 2 * 256
+        assert real.lrkv_prefill_scaled_workspace_bytes(d, B, n, max_ctx) <= max(staged, later)
