@@ -288,3 +288,49 @@ def test_prefill_behind_the_smallest_values(H, d_h, r, ps, which):
     ref, bound = reference(q[0], held, B_K, B_V, table[0], 401, d_h == 128)
     check(got[0], ref, bound, norm=None)
     assert st == 0 and ref.any()
+
+
+# ---------------------------------------------------------------------------
+# Calls one after another
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("H,d_h,r,ps", [(16, 128, 48, 64), (4, 32, 8, 32)])
+def test_calls_in_a_row_share_a_workspace(H, d_h, r, ps):
+    """Prefills with either append, appends and decodes on one stream and one workspace, none waited for: the same to the
+    bit as each with its own, waited for."""
+    import rank_kv_attention_gb300 as L
+    rng = np.random.default_rng(67)
+    d, B, width = 64, 3, 2048 // ps
+    cache, table = random_cache(rng, B * width, ps, H, d_h, r, 16, loud=1), rng.permutation(B * width).astype(np.int32)
+    dt = dev(table.reshape(B, width), "i32")
+    w = [dev(a, "bf16") for a, _ in weights(rng, d, H, d_h, r, 1).values()]
+    Bs = [dev(bf16(rng, (H, d_h, r), r ** -0.5)[0], "bf16") for _ in range(2)]
+    steps, at = [], np.zeros(B, int)
+    for rows_of in ([300, 1, 200], [10, 20, 9], [1, 1, 1], [0, 700, 40], [1, 1, 1], [30, 0, 0], [1, 1, 1], [600, 500, 400]):
+        n = sum(rows_of)
+        steps.append((dev(bf16(rng, (n, d))[0], "bf16"), dev(bf16(rng, (n, H, d_h))[0], "bf16"),
+                      dev(np.concatenate([[0], np.cumsum(rows_of)]), "i32"), dev(at, "i32"), dev(at + rows_of, "i32"),
+                      max(rows_of) == 1))
+        at = at + rows_of
+    size = max(L.prefill_scaled_workspace_bytes(to_device(cache), B, s[0].shape[0], 2048) for s in steps)
+    size = max(size, L.decode_scaled_workspace_bytes(to_device(cache), B, 2048))
+
+    def run(ws_of, after):
+        dc, outs = to_device(cache), []
+        torch.cuda.synchronize()
+        for x, q, cu, start, lens, single in steps:
+            if single:
+                L.append_scaled(x, cu, start, *w, dc, dt, ws=ws_of())
+                after()
+                outs.append(L.decode_scaled(q, dc, *Bs, lens, dt, 2048, ws=ws_of()))
+            else:
+                outs.append(L.prefill_scaled(x, q, cu, start, 2048, *w, *Bs, dc, dt, ws=ws_of()))
+            after()
+        torch.cuda.synchronize()
+        return dc, outs
+    one = torch.full((size,), 0xff, dtype=torch.uint8, device="cuda")
+    a, outs = run(lambda: one, lambda: None)
+    b, alone = run(lambda: torch.full((size,), 0x7f, dtype=torch.uint8, device="cuda"), torch.cuda.synchronize)
+    for x, y in zip(outs, alone):
+        assert torch.isfinite(x).all() and torch.equal(x, y)
+    for k in ("S_K", "S_V", "R_K", "R_V", "E_S_K", "E_S_V", "E_R_K", "E_R_V"):
+        assert torch.equal(getattr(a, k).view(torch.uint8), getattr(b, k).view(torch.uint8)), k
