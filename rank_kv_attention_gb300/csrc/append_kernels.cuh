@@ -35,17 +35,6 @@ struct AppendArgsT {
     float *rows32[4] = {nullptr, nullptr, nullptr, nullptr};
 };
 
-// The first request b with cu_rows[b + 1] > row (B when there is none).
-__device__ __forceinline__ int request_of_row(const int32_t *cu_rows, int B, int row) {
-    int lo = 0, hi = B;
-    while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (cu_rows[mid + 1] > row) hi = mid;
-        else lo = mid + 1;
-    }
-    return lo;
-}
-
 // Store value v of packed output column c (0 .. 2 d_h + 2 H r) for pool row
 // `row`: the four pools in order S_K, S_V, R_K, R_V.
 template <typename T>

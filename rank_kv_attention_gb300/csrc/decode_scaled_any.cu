@@ -368,22 +368,17 @@ __global__ void scaled_row_queries_kernel(const __grid_constant__ ScaledRows row
     pdl_launch_dependents();
     const int i = blockIdx.x * blockDim.x + threadIdx.x;
     if (i >= rows.n) return;
-    int lo = 0, hi = rows.B;  // first request whose rows end past i
-    while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (rows.cu_rows[mid + 1] > i) hi = mid;
-        else lo = mid + 1;
-    }
-    if (lo == rows.B || rows.cu_rows[lo] > i) {
+    const int b = request_of_row(rows.cu_rows, rows.B, i);
+    if (b == rows.B || rows.cu_rows[b] > i) {
         len[i] = -1;
         req_row[i] = 0;
         return;
     }
-    const int64_t pos = (int64_t)rows.start_pos[lo] + (i - rows.cu_rows[lo]);
+    const int64_t pos = (int64_t)rows.start_pos[b] + (i - rows.cu_rows[b]);
     // (a row that has no place in the table was flagged as it was not written)
     if (pos >= max_len && pos < (int64_t)rows.max_pages * page_size) status_or(rows.status, LRKV_STATUS_BAD_SEQLEN);
     len[i] = pos >= 0 && pos < max_len ? (int)pos + 1 : 0;
-    req_row[i] = lo;
+    req_row[i] = b;
 }
 
 // Parts per request: enough CTAs for the device, of at least 128 rows each.

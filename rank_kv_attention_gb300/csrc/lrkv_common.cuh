@@ -504,6 +504,24 @@ inline cudaError_t smem_limit_once(void (*kern)(KArgs...), int bytes) {
     return smem_limit_once(reinterpret_cast<const void *>(kern), bytes);
 }
 
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(p));
+    return p != 0;
+}
+
+// The first request b with cu_rows[b + 1] > row (B when there is none).
+__device__ __forceinline__ int request_of_row(const int32_t *cu_rows, int B, int row) {
+    int lo = 0, hi = B;
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (cu_rows[mid + 1] > row) hi = mid;
+        else lo = mid + 1;
+    }
+    return lo;
+}
+
 // Launch with programmatic dependent launch allowed: the kernel may be
 // scheduled while its predecessor in the stream drains; every kernel of this
 // library starts with pdl_wait(), so stream order is kept for its reads.

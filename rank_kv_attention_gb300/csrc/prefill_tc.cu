@@ -196,13 +196,6 @@ __device__ __forceinline__ float max3f(float a, float b, float c) {
     return r;
 }
 
-// One lane of a converged warp.
-__device__ __forceinline__ bool elect_one() {
-    uint32_t p;
-    asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(p));
-    return p != 0;
-}
-
 // Arrive on an mbarrier of another CTA of the cluster, this thread's writes to its shared
 // memory before.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cl_addr) {

@@ -363,14 +363,9 @@ __global__ void __launch_bounds__(kReadThreads, 5) read_scaled_kernel(const __gr
         const int i = blockIdx.x * ROWS + threadIdx.x;
         int s = -1;
         if (i < a.rows.n) {
-            int lo = 0, hi = a.rows.B;  // first request whose rows end past i
-            while (lo < hi) {
-                const int mid = (lo + hi) >> 1;
-                if (a.rows.cu_rows[mid + 1] > i) hi = mid;
-                else lo = mid + 1;
-            }
-            if (lo < a.rows.B && a.rows.cu_rows[lo] <= i)
-                s = pool_row(a.c, a.rows, lo, (int64_t)a.rows.start_pos[lo] + (i - a.rows.cu_rows[lo]));
+            const int b = request_of_row(a.rows.cu_rows, a.rows.B, i);
+            if (b < a.rows.B && a.rows.cu_rows[b] <= i)
+                s = pool_row(a.c, a.rows, b, (int64_t)a.rows.start_pos[b] + (i - a.rows.cu_rows[b]));
         }
         set.src[threadIdx.x] = s;
         set.block[threadIdx.x] = s >= 0 ? s / a.c.block : -1;
