@@ -8,15 +8,16 @@
 //
 // One CTA takes a part of a request's rows for one head.  A warp takes 32 rows at
 // a time: lane j scores row j (q and p from shared memory), the warp updates its
-// running maximum and sum, then its lanes add the rows' values up, four columns each,
-// eight loads of a pool on their way at once.  The shared rows are read again by every head
-// (out of L2), and the four warps' states meet in shared memory.
+// running maxima and sum, then its lanes add the rows' values up, four columns each,
+// eight loads of a pool on their way at once.  A row's place and weights go to those lanes through
+// shared memory: by shuffles the registers that hold them are missing for the loads.  The shared rows
+// are read again by every head (out of L2), and the four warps' states meet in shared memory.
 //
 // Bound by the lanes' loads of rows r or d_h bytes apart, their latency, and the conversions of
 // every code, once a head.  In a graph, 16 requests of 4096 rows: d_h = 64, r = 16, 8 heads
-// 37 us (3.7 at the copy bandwidth); d_h = 32, r = 40, 6 heads 31; d_h = 128, r = 72, 12 heads 140
-// (19.2); d_h = 128, r = 16, 40 heads 315 (14.9).  One load of a row's values at a time took 86, 63,
-// 240 and 605.
+// 33 us (3.7 at the copy bandwidth); d_h = 32, r = 40, 6 heads 26; d_h = 128, r = 72, 12 heads 111
+// (19.2); d_h = 128, r = 16, 40 heads 234 (14.9).  With places and weights by shuffles 38, 30, 140 and
+// 310, and one load of a row's values at a time 86, 63, 240 and 605.
 #include <algorithm>
 
 #include "scaled_kernels.cuh"
@@ -53,13 +54,17 @@ __device__ __forceinline__ float dot8(const uint2 &w, const float *y, float s) {
 
 // NI: groups of 128 value columns.  HALF (64 columns at most): a half-warp adds a row's values up, so
 // a warp takes two rows at a time, and the next rows' pages are looked up ahead in 72
-// registers (37 us of the first case above, 42 in 96, 47 without the look ahead; with 128
-// columns it costs registers that the loads need: 140 us of the third, 168 with it).
+// registers (with shuffles, 37 us of the first case above, 42 in 96, 47 without the look ahead; with
+// 128 columns it cost registers that the loads need: 140 us of the third, 168 with it).
 template <int NI, bool HALF>
 __global__ void __launch_bounds__(kThreads, HALF ? 7 : 5) decode_scaled_any_kernel(const __grid_constant__ AnyArgs P) {
     constexpr int kRows = 8, kStep = HALF ? 2 : 1;  // loads on their way, rows of one
     __shared__ __align__(16) float qs[256], ps[256];
-    __shared__ float ls[kWarps], tops[3][kWarps], red[kWarps][512];  // tops: m, ks, kr
+    __shared__ __align__(16) float tops[3][kWarps];  // m, ks, kr
+    __shared__ float ls[kWarps], red[kWarps][512];
+    // of the rows that a warp adds up: row of the pool, weights of the shared and the private value
+    __shared__ int at[kWarps][32];
+    __shared__ float2 weight[kWarps][32];
     const ScaledDecodeArgs &a = P.d;
     const ScaledPools &c = a.c;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -132,10 +137,11 @@ __global__ void __launch_bounds__(kThreads, HALF ? 7 : 5) decode_scaled_any_kern
         vs += x;
         vr += x;
         const float mn = fmaxf(m, warp_max(x)), sn = fmaxf(ks, warp_max(vs)), rn = fmaxf(kr, warp_max(vr));
-        l = l * exp2f(m - ref_of(mn)) + exp2f(x - ref_of(mn));
-        const float alpha = exp2f(ks - ref_of(sn)), beta = exp2f(kr - ref_of(rn));
-        vs = exp2f(vs - ref_of(sn));
-        vr = exp2f(vr - ref_of(rn));
+        l = l * ex2f(m - ref_of(mn)) + ex2f(x - ref_of(mn));
+        const float alpha = ex2f(ks - ref_of(sn)), beta = ex2f(kr - ref_of(rn));
+        weight[warp][lane] = make_float2(ex2f(vs - ref_of(sn)), ex2f(vr - ref_of(rn)));
+        at[warp][lane] = row;
+        __syncwarp();
         m = mn;
         ks = sn;
         kr = rn;
@@ -152,7 +158,7 @@ __global__ void __launch_bounds__(kThreads, HALF ? 7 : 5) decode_scaled_any_kern
             uint32_t cs[NI][kRows], cr[NI][kRows];
 #pragma unroll
             for (int u = 0; u < kRows; ++u) {
-                const int rt = __shfl_sync(0xffffffffu, row, t + u * kStep + half);
+                const int rt = at[warp][t + u * kStep + half];
                 const uint8_t *sv = c.code[1] + (int64_t)rt * sw + g * d_h, *rv = c.code[3] + (int64_t)rt * rw + h * r;
 #pragma unroll
                 for (int i = 0; i < NI; ++i) {
@@ -163,20 +169,20 @@ __global__ void __launch_bounds__(kThreads, HALF ? 7 : 5) decode_scaled_any_kern
             }
 #pragma unroll
             for (int u = 0; u < kRows; ++u) {
-                const float ws = __shfl_sync(0xffffffffu, vs, t + u * kStep + half);
-                const float wr = __shfl_sync(0xffffffffu, vr, t + u * kStep + half);
+                const float2 w = weight[warp][t + u * kStep + half];
 #pragma unroll
                 for (int i = 0; i < NI; ++i) {
                     float y[4];
                     widen4(cs[i][u], y);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) as[i][e] = fmaf(ws, y[e], as[i][e]);
+                    for (int e = 0; e < 4; ++e) as[i][e] = fmaf(w.x, y[e], as[i][e]);
                     widen4(cr[i][u], y);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) ar[i][e] = fmaf(wr, y[e], ar[i][e]);
+                    for (int e = 0; e < 4; ++e) ar[i][e] = fmaf(w.y, y[e], ar[i][e]);
                 }
             }
         }
+        __syncwarp();
     }
     if (HALF)
 #pragma unroll
@@ -202,27 +208,24 @@ __global__ void __launch_bounds__(kThreads, HALF ? 7 : 5) decode_scaled_any_kern
         }
     }
     __syncthreads();
-    float M[3], f[3][kWarps], lt = 0.f;
-#pragma unroll
-    for (int k = 0; k < 3; ++k) {
-        M[k] = tops[k][0];
-#pragma unroll
-        for (int w = 1; w < kWarps; ++w) M[k] = fmaxf(M[k], tops[k][w]);
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) f[k][w] = exp2f(tops[k][w] - ref_of(M[k]));
-    }
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) lt += ls[w] * f[0][w];
+    // the four warps' sums: v of warp w, relative to tops[k][w], relative to the largest of those
+    auto join = [&](int k, const float *v, int step) {
+        const float4 t = *reinterpret_cast<const float4 *>(tops[k]);
+        const float ref = ref_of(fmaxf(fmaxf(t.x, t.y), fmaxf(t.z, t.w)));
+        return (v[0] * ex2f(t.x - ref) + v[step] * ex2f(t.y - ref)) +
+               (v[2 * step] * ex2f(t.z - ref) + v[3 * step] * ex2f(t.w - ref));
+    };
     float *acc = P.st.acc + slot * H * (d_h + r);
+#pragma unroll 1
     for (int i = tid; i < d_h + r; i += kThreads) {
-        const int at = i < d_h ? i : 256 + i - d_h;
-        float s = 0.f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) s += red[w][at] * (i < d_h ? f[1][w] : f[2][w]);
-        if (i < d_h) acc[(size_t)h * d_h + i] = s;
-        else acc[(size_t)H * d_h + h * r + i - d_h] = s;
+        const bool priv = i >= d_h;
+        const float s = join(priv ? 2 : 1, &red[0][priv ? 256 + i - d_h : i], 512);
+        acc[priv ? (size_t)H * d_h + h * r + i - d_h : (size_t)h * d_h + i] = s;
     }
-    if (tid == 0) *head = make_float4(M[0], lt, M[1], M[2]);
+    if (tid == 0) {
+        auto most = [&](int k) { return fmaxf(fmaxf(tops[k][0], tops[k][1]), fmaxf(tops[k][2], tops[k][3])); };
+        *head = make_float4(most(0), join(0, ls, 1), most(1), most(2));
+    }
 }
 
 // ---------------------------------------------------------------------------
