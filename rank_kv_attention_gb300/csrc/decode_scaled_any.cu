@@ -244,6 +244,7 @@ constexpr int kMergeStates = 256, kMergeB = 3;
 
 template <int THREADS, int HELD>
 __global__ void __launch_bounds__(THREADS, HELD == 4 ? 6 : 2) scaled_merge_kernel(const __grid_constant__ ScaledMergeArgs P) {
+    constexpr int kAhead = HELD == 4 ? 4 : 8;  // (four held: eight more would spill B_V)
     __shared__ float gs[2][kMergeStates], sums[512], part[kMergeB * THREADS];
     __shared__ float red[4][THREADS / 32], up[2];
     const int h = blockIdx.y, b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -283,35 +284,46 @@ __global__ void __launch_bounds__(THREADS, HELD == 4 ? 6 : 2) scaled_merge_kerne
         const int s = g + j * groups;
         held[j] = mine && s < ns ? acc[(int64_t)s * H * W] : 0.f;
     }
-    float M = warp_max(st.x), KS = warp_max(st.z), KR = warp_max(st.w);
-    if (lane == 0) {
-        red[0][warp] = M;
-        red[2][warp] = KS;
-        red[3][warp] = KR;
+    // (the warps that hold states, most often one: then they need not meet before)
+    const int nw = max(1, (ns + 31) / 32);
+    float M = -INFINITY, KS = -INFINITY, KR = -INFINITY;
+    if (warp < nw) {
+        M = warp_max(st.x);
+        KS = warp_max(st.z);
+        KR = warp_max(st.w);
+        if (lane == 0) {
+            red[0][warp] = M;
+            red[2][warp] = KS;
+            red[3][warp] = KR;
+        }
     }
-    __syncthreads();
-    const int w = lane % (THREADS / 32);
-    M = warp_max(red[0][w]);
-    KS = warp_max(red[2][w]);
-    KR = warp_max(red[3][w]);
-    // a part without rows (m = -inf, l = 0) has written no value sums
-    const bool none = st.x == -INFINITY && st.y == 0.f;
-    if (tid == 0) {
-        up[0] = ex2f(KS - ref_of(M));
-        up[1] = ex2f(KR - ref_of(M));
+    if (nw > 1) {
+        __syncthreads();
+        if (warp < nw) {
+            const int w = lane < nw ? lane : 0;
+            M = warp_max(red[0][w]);
+            KS = warp_max(red[2][w]);
+            KR = warp_max(red[3][w]);
+        }
     }
-    if (tid < kMergeStates) {
+    if (warp < nw) {
+        if (tid == 0) {
+            up[0] = ex2f(KS - ref_of(M));
+            up[1] = ex2f(KR - ref_of(M));
+        }
+        // a part without rows (m = -inf, l = 0) has written no value sums
+        const bool none = st.x == -INFINITY && st.y == 0.f;
         gs[0][tid] = none ? -1.f : ex2f(st.z - ref_of(KS));
         gs[1][tid] = none ? -1.f : ex2f(st.w - ref_of(KR));
+        float l = none ? 0.f : st.y * ex2f(st.x - ref_of(M));
+#pragma unroll
+        for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+        if (lane == 0) red[1][warp] = l;
     }
-    float l = none ? 0.f : st.y * ex2f(st.x - ref_of(M));
-#pragma unroll
-    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    if (lane == 0) red[1][warp] = l;
     __syncthreads();
-    l = 0.f;
-#pragma unroll
-    for (int w = 0; w < THREADS / 32; ++w) l += red[1][w];
+    float l = red[1][0];
+#pragma unroll 1
+    for (int w = 1; w < nw; ++w) l += red[1][w];
     const float inv = l != 0.f ? 1.f / l : 0.f;  // (NaN stays NaN)
     auto weigh = [&](int s, bool priv, float v) {
         const float k = gs[priv][s];
@@ -323,7 +335,7 @@ __global__ void __launch_bounds__(THREADS, HELD == 4 ? 6 : 2) scaled_merge_kerne
 #pragma unroll
         for (int j = 0; j < HELD; ++j)
             if (g + j * groups < ns) x += weigh(g + j * groups, priv, held[j]);
-#pragma unroll 8
+#pragma unroll kAhead
         for (int s = g + HELD * groups; s < ns; s += groups) x += weigh(s, priv, acc[(int64_t)s * H * W]);
     }
     if (groups > 1) {
