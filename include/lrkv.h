@@ -497,11 +497,13 @@ LRKV_API int lrkv_prefill_window(const void *X, const void *Q, const int32_t *cu
  *
  * lrkv_append_scaled projects X as lrkv_append does (fp32 sums) and writes the
  * fp32 rows as lrkv_write_scaled does; they are rounded once.  Workspace:
- * lrkv_append_scaled_workspace_bytes bytes.
+ * lrkv_append_scaled_workspace_bytes bytes, the fp32 rows (8 n (G d_h + H r) bytes), which
+ * a call whose epilogue stores codes leaves unused.
  *
  * lrkv_decode_scaled is lrkv_decode on such a cache, with q, B_K, B_V and out in
- * bf16.  On tensor cores (d_h = 128, G = 1, H a multiple of 4 up to 32, r up to 64,
- * and what of it fits in tensor memory) the codes are multiplied as
+ * bf16.  On tensor cores (d_h = 128, G = 1, H a multiple of 4 up to 20 with r up to 64,
+ * 24 heads with r up to 56, 28 and 32 with r up to 40; other shapes take several
+ * times as long for their bytes) the codes are multiplied as
  * they are: q, q B_K[h] and the weights enter as sums of two or three E4M3 terms
  * (q and q B_K[h] off by at most 2^-14 of an element or 2^-26 of the largest; a row's
  * weight times the scale of its values by 2^-9, or 2^-22 of the largest of its tile of
@@ -518,7 +520,11 @@ LRKV_API int lrkv_prefill_window(const void *X, const void *Q, const int32_t *cu
  * quantised), as lrkv_prefill.  max_ctx: host upper bound of start_pos[b] + rows of b.
  * Where lrkv_prefill runs its tiled kernel on a bf16 cache of these sizes, the
  * values are laid out in bf16 in the workspace and that kernel runs; other
- * sizes run one decode a row.  A query that is not finite gives NaN in its row and head.
+ * sizes run one decode a row.  Workspace: lrkv_prefill_scaled_workspace_bytes bytes, the larger of
+ * the append's and of what comes after it: 4 (d_h + H r) bytes for each of B max_ctx rows (of the
+ * pool's rows, where those are fewer), or, a decode a row, about 4 n H (d_h + r) bytes.
+ * A query that is not finite gives NaN in its row and head.  The tiled kernel's sums of weighted
+ * values are not normalised: they are finite where max_ctx times the largest value is below 2^100.
  * Rows that some new row of a request sees must hold finite values: the tiled kernel gives
  * a row that another row of its tile does not see the weight 0, and 0 times a NaN is NaN.
  * A row without a place is flagged as by the append,

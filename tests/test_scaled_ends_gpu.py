@@ -290,6 +290,23 @@ def test_prefill_behind_the_smallest_values(H, d_h, r, ps, which):
     assert st == 0 and ref.any()
 
 
+@pytest.mark.parametrize("H,d_h,r,ps", [(16, 128, 48, 64), (4, 32, 8, 32)])
+@pytest.mark.parametrize("byte", [10, 207])
+def test_prefill_behind_rows_that_agree(H, d_h, r, ps, byte):
+    """A history of the same largest values, as quiet as the cache holds them, or 448 * 2^80: with 1500 rows below the 2^100
+    to which the tiled kernel's sums are finite.  Their mean is that value."""
+    rng = np.random.default_rng(68)
+
+    def change(cache, table):
+        cache.codes["S_V"][:], cache.exps["S_V"][:] = 0x7e, byte
+        cache.codes["R_V"][:], cache.exps["R_V"][:] = 0, 10
+    x = np.zeros((1, 64), np.uint16), np.zeros((1, 64))
+    got, held, st, _, (q, B_K, B_V), table, _ = prefill(rng, H, d_h, r, ps, [1500], [1], 1501, x=x, change=change)
+    ref, bound = reference(q[0], held, B_K, B_V, table[0], 1501, d_h == 128)
+    check(got[0], ref, bound)
+    assert st == 0
+
+
 # ---------------------------------------------------------------------------
 # Calls one after another
 # ---------------------------------------------------------------------------
