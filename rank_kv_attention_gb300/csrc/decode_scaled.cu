@@ -23,13 +23,13 @@
 // N = 16 to 64 columns of M = 128, bound by reading A: 32 cycles per 4 KB, where HBM
 // delivers 4 KB per SM in 170.
 //
-// Scales: a token's exponent enters its score, x + e, before the exponential: the
-// value products take 2^(x + eS - MS) and 2^(x + eR - MR), each relative to the tile's
-// largest per head, so tokens of loud and quiet blocks keep their precision next
-// to each other.  The accumulators over tiles are relative to the largest x + eS and x + eR so
-// far, not to the largest x: values lie between 2^-126 and 2^128, and neither a sum of loud
-// ones nor a weight of a quiet one would fit in fp32 beside the value's own scale.  Sums,
-// maxima and the accumulators are fp32 in registers.
+// Scales: a token's exponent enters its score, d + e with d = x less the largest x so far,
+// before the exponential: the value products take 2^(d + eS - MS) and 2^(d + eR - MR), each
+// relative to the tile's largest per head, so tokens of loud and quiet blocks keep their
+// precision next to each other.  The accumulators over tiles are relative to the largest d + eS
+// and d + eR so far, not to the largest x: values lie between 2^-126 and 2^128, and neither a
+// sum of loud ones nor a weight of a quiet one would fit in fp32 beside the value's own scale.
+// Sums, maxima and the accumulators are fp32 in registers.
 //
 // Work: the requests' rows in units of 64 tokens, laid end to end and cut evenly
 // over one CTA per SM; a CTA walks its tiles (two units of one request, or one).
@@ -156,7 +156,7 @@ struct Offsets {
         weights = img + 2 * one;
         red = weights + 4 * s.wrows * 128;  // [2][4 quarters of the heads][maxima 3, sum][8][4 warps]
         fac = red + 2 * 4 * 4 * 8 * 4 * 4;  // [4][4][32]: what the shared sums and this tile's are multiplied by; the private
-        tops = fac + 4 * 4 * 32 * 4;        // [2][32]: largest x + eS and x + eR of the request so far
+        tops = fac + 4 * 4 * 32 * 4;        // [2][32]: largest x - m + eS and x - m + eR of the request so far
         scales = tops + 2 * 32 * 4;         // [2][8 groups of 16 tokens][kScaleRow]
         ar = scales + 2 * 8 * kScaleRow * 4;  // [box][128]: the private accumulators
         bars = ar + s.boxes * 512;
@@ -697,7 +697,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // warp: tokens 32 (warp & 3) + lane of a tile, heads h0 .. h0 + hn - 1 (a quarter)
         const int hn = H / 4, grp = warp >> 2, h0 = grp * hn, token = 32 * (warp & 3) + lane;
         float l[HT], m = -INFINITY;  // m: of lane k's head h0 + k, the same in all four warps
-        // (largest x + eS and x + eR: written and read by lane k of the first warp)
+        // (largest x - m + eS and x - m + eR: written and read by lane k of the first warp)
         float *tops = reinterpret_cast<float *>(smem + off.tops) + h0 + lane;
         uint32_t met = 0;
         auto meet = [&]() -> bool {  // the four warps of these heads
@@ -763,7 +763,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int k = 0; k < HT; ++k)
                 if (k < hn) {
                     er[k] = there ? scale[34 + h0 + k] : 0.f;
-                    const float m0 = warp_max(x[k]), m1 = warp_max(x[k] + es), m2 = warp_max(x[k] + er[k]);
+                    const float m0 = warp_max(x[k]), d = x[k] - ref_of(m0), m1 = warp_max(d + es), m2 = warp_max(d + er[k]);
                     if (lane == k) {
                         mine[0] = m0;
                         mine[1] = m1;
@@ -782,25 +782,27 @@ __global__ void __launch_bounds__(kThreads, 1)
             // becomes 2^8, and the value sums are relative to their own running maxima
             float alpha = 0.f, ref = 0.f, ms = 0.f, mr = 0.f;
             if (lane < hn) {
-                float M[3];
-#pragma unroll
-                for (int j = 0; j < 3; ++j) {
-                    const float4 v = *reinterpret_cast<const float4 *>(&red[(j * HT + lane) * 4]);
-                    M[j] = fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w));
-                }
-                const float mn = fmaxf(m, M[0]);
+                const float4 v = *reinterpret_cast<const float4 *>(&red[lane * 4]);
+                const float mn = fmaxf(fmaxf(m, fmaxf(v.x, v.y)), fmaxf(v.z, v.w));
                 ref = ref_of(mn);
-                ms = ref_of(M[1]) - 8.f;
-                mr = ref_of(M[2]) - 8.f;
-                alpha = ex2f(m - ref);
+                float M[2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {  // the warps' maxima are relative to their own largest scores
+                    const float4 u = *reinterpret_cast<const float4 *>(&red[((1 + j) * HT + lane) * 4]);
+                    M[j] = fmaxf(fmaxf(u.x + (v.x - ref), u.y + (v.y - ref)), fmaxf(u.z + (v.z - ref), u.w + (v.w - ref)));
+                }
+                ms = ref_of(M[0]) - 8.f;
+                mr = ref_of(M[1]) - 8.f;
+                const float down = m - ref;  // (-infinity: no row yet)
+                alpha = ex2f(down);
                 m = mn;
                 if ((warp & 3) == 0) {
                     float *fac = reinterpret_cast<float *>(smem + off.fac) + (i & 3) * 4 * 32 + h0 + lane;
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        const float was = tops[32 * j], now = fmaxf(was, M[1 + j]);
+                        const float was = tops[32 * j] + down, now = fmaxf(was, M[j]);
                         fac[64 * j] = ex2f(was - ref_of(now));
-                        fac[64 * j + 32] = ex2f(M[1 + j] - 8.f - ref_of(now));
+                        fac[64 * j + 32] = ex2f(M[j] - 8.f - ref_of(now));
                         tops[32 * j] = now;
                     }
                 }
@@ -810,11 +812,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int k = 0; k < HT; ++k)
                 if (k < hn) {
                     const int h = h0 + k;
-                    const float w = ex2f(x[k] - __shfl_sync(0xffffffffu, ref, k));
+                    const float d = x[k] - __shfl_sync(0xffffffffu, ref, k), w = ex2f(d);
                     l[k] = l[k] * __shfl_sync(0xffffffffu, alpha, k) + w;
                     // both operands' terms, a pair at a time
-                    const float y = ex2f(x[k] + es - __shfl_sync(0xffffffffu, ms, k));
-                    const float z = ex2f(x[k] + er[k] - __shfl_sync(0xffffffffu, mr, k));
+                    const float y = ex2f(d + es - __shfl_sync(0xffffffffu, ms, k));
+                    const float z = ex2f(d + er[k] - __shfl_sync(0xffffffffu, mr, k));
                     const uint16_t t1 = e4m3x2_from_f32(y, z);
                     const uint32_t h2 = f16x2_from_e4m3x2(t1);
                     const float2 g = __half22float2(*reinterpret_cast<const __half2 *>(&h2));

@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(kThreads, HALF ? 7 : 5) decode_scaled_any_kern
 
     const int32_t *table = a.page_table + (size_t)(a.req_row ? a.req_row[b] : b) * a.max_pages;
     const int sw = c.G * d_h, rw = H * r;  // bytes of a token's shared and private row
-    // largest x, x + eS and x + eR so far, what the sums are relative to
+    // largest x, x - m + eS and x - m + eR so far, what the sums are relative to
     float m = -INFINITY, ks = -INFINITY, kr = -INFINITY, l = 0.f, as[NI][4] = {}, ar[NI][4] = {};
     const int col0 = HALF ? 4 * (lane & 15) : 4 * lane, half = HALF ? lane >> 4 : 0;
     auto lookup = [&](int j) {
@@ -134,10 +134,14 @@ __global__ void __launch_bounds__(kThreads, HALF ? 7 : 5) decode_scaled_any_kern
             vs = (float)clamp_exp(e1);
             vr = (float)clamp_exp(e3);
         }
+        const float mn = fmaxf(m, warp_max(x)), down = m - ref_of(mn);
+        x -= ref_of(mn);
         vs += x;
         vr += x;
-        const float mn = fmaxf(m, warp_max(x)), sn = fmaxf(ks, warp_max(vs)), rn = fmaxf(kr, warp_max(vr));
-        l = l * ex2f(m - ref_of(mn)) + ex2f(x - ref_of(mn));
+        ks += down;
+        kr += down;
+        const float sn = fmaxf(ks, warp_max(vs)), rn = fmaxf(kr, warp_max(vr));
+        l = l * ex2f(down) + ex2f(x);
         const float alpha = ex2f(ks - ref_of(sn)), beta = ex2f(kr - ref_of(rn));
         weight[warp][lane] = make_float2(ex2f(vs - ref_of(sn)), ex2f(vr - ref_of(rn)));
         at[warp][lane] = row;
@@ -208,10 +212,18 @@ __global__ void __launch_bounds__(kThreads, HALF ? 7 : 5) decode_scaled_any_kern
         }
     }
     __syncthreads();
-    // the four warps' sums: v of warp w, relative to tops[k][w], relative to the largest of those
+    // the four warps' sums: v of warp w, relative to its k-th maximum, relative to the largest of those
+    auto most = [](const float4 &t) { return fmaxf(fmaxf(t.x, t.y), fmaxf(t.z, t.w)); };
+    auto maxima = [&](int k) {
+        const float4 t = *reinterpret_cast<const float4 *>(tops[0]);
+        if (!k) return t;
+        const float4 u = *reinterpret_cast<const float4 *>(tops[k]);
+        const float m = ref_of(most(t));
+        return make_float4(u.x + (t.x - m), u.y + (t.y - m), u.z + (t.z - m), u.w + (t.w - m));
+    };
     auto join = [&](int k, const float *v, int step) {
-        const float4 t = *reinterpret_cast<const float4 *>(tops[k]);
-        const float ref = ref_of(fmaxf(fmaxf(t.x, t.y), fmaxf(t.z, t.w)));
+        const float4 t = maxima(k);
+        const float ref = ref_of(most(t));
         return (v[0] * ex2f(t.x - ref) + v[step] * ex2f(t.y - ref)) +
                (v[2 * step] * ex2f(t.z - ref) + v[3 * step] * ex2f(t.w - ref));
     };
@@ -222,17 +234,14 @@ __global__ void __launch_bounds__(kThreads, HALF ? 7 : 5) decode_scaled_any_kern
         const float s = join(priv ? 2 : 1, &red[0][priv ? 256 + i - d_h : i], 512);
         acc[priv ? (size_t)H * d_h + h * r + i - d_h : (size_t)h * d_h + i] = s;
     }
-    if (tid == 0) {
-        auto most = [&](int k) { return fmaxf(fmaxf(tops[k][0], tops[k][1]), fmaxf(tops[k][2], tops[k][3])); };
-        *head = make_float4(most(0), join(0, ls, 1), most(1), most(2));
-    }
+    if (tid == 0) *head = make_float4(most(maxima(0)), join(0, ls, 1), most(maxima(1)), most(maxima(2)));
 }
 
 // ---------------------------------------------------------------------------
-// Merge: one CTA per (request, head).  With f_s = 2^(m_s - M), gS_s = 2^(kS_s - KS) and gR_s
-// = 2^(kR_s - KR) relative to the largest of all states, l = sum_s f_s l_s, the means are
-// S = 2^(KS - M) (sum_s gS_s accS_s) / l and R alike, and o = S + R B_V[h]^T.  (KS - M and KR -
-// M lie in the exponents' range.)  Groups of threads, one thread a column, take the states in
+// Merge: one CTA per (request, head).  With M the largest m_s, KS the largest m_s - M + kS_s (of all
+// states), f_s = 2^(m_s - M), gS_s = 2^(m_s - M + kS_s - KS) and l = sum_s f_s l_s, the mean
+// is S = 2^KS (sum_s gS_s accS_s) / l, that of the private rows R alike, and o = S + R B_V[h]^T.
+// (KS and KR lie in the exponents' range.)  Groups of threads, one thread a column, take the states in
 // turn.
 //
 // All of it is latency (about a microsecond for a round trip to memory that other
@@ -286,9 +295,11 @@ __global__ void __launch_bounds__(THREADS, HELD == 4 ? 6 : 2) scaled_merge_kerne
     }
     // (the warps that hold states, most often one: then they need not meet before)
     const int nw = max(1, (ns + 31) / 32);
-    float M = -INFINITY, KS = -INFINITY, KR = -INFINITY;
+    float M = -INFINITY, KS = -INFINITY, KR = -INFINITY;  // (KS, KR: less M)
     if (warp < nw) {
         M = warp_max(st.x);
+        st.z += st.x - ref_of(M);
+        st.w += st.x - ref_of(M);
         KS = warp_max(st.z);
         KR = warp_max(st.w);
         if (lane == 0) {
@@ -301,15 +312,18 @@ __global__ void __launch_bounds__(THREADS, HELD == 4 ? 6 : 2) scaled_merge_kerne
         __syncthreads();
         if (warp < nw) {
             const int w = lane < nw ? lane : 0;
+            const float was = ref_of(M);
             M = warp_max(red[0][w]);
-            KS = warp_max(red[2][w]);
-            KR = warp_max(red[3][w]);
+            KS = warp_max(red[2][w] + (red[0][w] - ref_of(M)));
+            KR = warp_max(red[3][w] + (red[0][w] - ref_of(M)));
+            st.z += was - ref_of(M);
+            st.w += was - ref_of(M);
         }
     }
     if (warp < nw) {
         if (tid == 0) {
-            up[0] = ex2f(KS - ref_of(M));
-            up[1] = ex2f(KR - ref_of(M));
+            up[0] = ex2f(KS);
+            up[1] = ex2f(KR);
         }
         // a part without rows (m = -inf, l = 0) has written no value sums
         const bool none = st.x == -INFINITY && st.y == 0.f;

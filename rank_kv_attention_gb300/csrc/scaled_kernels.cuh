@@ -77,10 +77,12 @@ struct ScaledDecodeArgs {
 };
 
 // Partial softmax states of decode_scaled (log2 units): slot s holds, for every head, the
-// running maximum m of the scores x and the sum of 2^(x - m), and the sums of 2^(x + e - k)
-// code over shared and private rows, each relative to its own maximum k of x + e.  A value
+// running maximum m of the scores x and the sum of 2^(x - m), and the sums of 2^(x - m + e - k)
+// code over shared and private rows, each relative to its own maximum k of x - m + e.  A value
 // may be 2^128 or 2^-126 as it lies in the cache, and a sum of many such, or one that shares a
-// factor with a weight below one, would leave fp32; these neither overflow nor vanish.
+// factor with a weight below one, would leave fp32; these neither overflow nor vanish.  (The
+// exponent is added to a score's distance from the largest: next to a large score it would
+// lose its digits.)
 struct ScaledStates {
     float4 *head;  // [slots][H]: m, sum, k of the shared rows, k of the private rows
     float *acc;    // [slots][H d_h | H r]

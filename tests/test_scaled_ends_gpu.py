@@ -93,6 +93,44 @@ def test_decode_of_the_loudest_rows_that_agree(H, d_h, r):
     check_decode(run_decode(cache, table, q, B_K, B_V, lens), cache, table, q, B_K, B_V, lens)
 
 
+@pytest.mark.parametrize("which", ["one", "two"])
+@pytest.mark.parametrize("H,d_h,r,G", [(16, 128, 48, 1), (32, 128, 32, 1), (8, 64, 16, 1), (12, 128, 72, 1), (16, 128, 32, 2)])
+def test_decode_of_scores_larger_than_any_scale(H, d_h, r, G, which):
+    """One row of each request (or two that agree) scores 2^12 to 2^100, all others nothing: the output is its value (their
+    mean), whose scale must not drown in the score.  The weights are exactly 0 and 1 (or 1/2), so what is left of the bound
+    is their rounding, the sums' and the output's."""
+    rng = np.random.default_rng(69)
+    powers, n, many = [12, 17, 22, 24, 26, 30, 60, 100], 300, 30
+    B = len(powers)
+    cache, table, q, B_K, B_V = decode_case(rng, [n] * B, H, d_h, r, 64, 16, G)
+    set_ends(rng, cache, "blocks")
+    cache.exps["R_V"][:] = rng.integers(120, 135, cache.exps["R_V"].shape)
+    cache.exps["S_V"][:] = rng.integers(115, 140, cache.exps["S_V"].shape)
+    for k in ("S_K", "R_K"):
+        cache.codes[k][:] = 0
+    x = np.zeros((B, H, d_h), np.float32)
+    x[:, :, 0] = 1.5                               # (no power of two: the score has digits below its first)
+    rows = [rng.choice(n, 2, replace=False) for _ in range(B)]
+    want, size = np.zeros((B, H, d_h)), np.zeros((B, H, d_h))
+    for b in range(B):
+        picked = rows[b][:1] if which == "one" else rows[b]
+        for j in picked:
+            page, slot = table[b, j // 64], j % 64
+            cache.codes["S_K"][page, slot, :, 0] = S.e4m3_encode(np.array(1.125))
+            cache.exps["S_K"][page, slot // 16] = 127 + powers[b]
+        for j in picked:
+            page, slot = table[b, j // 64], j % 64
+            for h in range(H):
+                sv, rv = cache.row("S_V", page, slot)[h * G // H], cache.row("R_V", page, slot)[h]
+                want[b, h] += (sv + B_V[1][h] @ rv) / len(picked)
+                size[b, h] += (np.abs(sv) + np.abs(B_V[1][h]) @ np.abs(rv)) / len(picked)
+    bits = I.f32_to_bf16_bits(x)
+    q = np.tile(bits, (many, 1, 1)), np.tile(I.bf16_bits_to_f64(bits), (many, 1, 1))
+    out = host(run_decode(cache, np.tile(table, (many, 1)), q, B_K, B_V, [n] * (B * many)), "bf16").reshape(many, B, H, d_h)
+    for got in (out[0], out[many // 2], out[-1]):
+        check(got, want, 2.0 ** -8 * np.abs(want) + (2.0 ** -9 + 2.0 ** -21 + (r + 32) * 2.0 ** -23) * size)
+
+
 # ---------------------------------------------------------------------------
 # Decode: which kernel a shape takes
 # ---------------------------------------------------------------------------
