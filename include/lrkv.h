@@ -524,7 +524,8 @@ LRKV_API int lrkv_prefill_window(const void *X, const void *Q, const int32_t *cu
  * the append's and of what comes after it: 4 (d_h + H r) bytes for each of B max_ctx rows (of the
  * pool's rows, where those are fewer), or, a decode a row, about 4 n H (d_h + r) bytes.
  * A query that is not finite gives NaN in its row and head.  The tiled kernel's sums of weighted
- * values are not normalised: they are finite where max_ctx times the largest value is below 2^100.
+ * values are not normalised: they are finite where max_ctx times the largest value is below 2^100
+ * and scores are below 2^13.
  * Rows that some new row of a request sees must hold finite values: the tiled kernel gives
  * a row that another row of its tile does not see the weight 0, and 0 times a NaN is NaN.
  * A row without a place is flagged as by the append,
